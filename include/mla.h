@@ -293,6 +293,123 @@ mla_status mla_decode_paged_combine_fp8(const mla_config* cfg, const void* q_abs
                                         void* stream);
 
 /*
+ * The page-scaled 8-bit latent cache, and eviction from it. The pages name
+ * neither; both serve long contexts in less cache memory. A row of cache8
+ * [num_blocks, block_size, 640] bytes is the FP8 row above (512 e4m3 codes,
+ * then k_rot as 64 bf16), but the codes of page p are c_hat / page_scales[p]:
+ * page_scales [num_blocks] float32 holds one power of two per page, set by
+ * the write from the values themselves, so nothing is calibrated and nothing
+ * saturates. A page of scale 0 is empty: zero page_scales once when the cache
+ * is allocated, and the entry of a page that is handed to another sequence (a
+ * stale scale costs precision only, never correctness). bf16 only.
+ *
+ * mla_page8_cache_write -- mla_cache_write into such pages. With amax_p the
+ * largest |c_hat| of the call's tokens in page p,
+ *   page_scales[p] = max(page_scales[p], 2^e),
+ *   e = the least integer in [-64, 64] with amax_p <= 448 * 2^e;
+ * rows already in a page whose scale grows keep their values in the new scale
+ * (code' = e4m3(code * old / new), round to nearest even: exact but for codes
+ * that become subnormal). NaN stays NaN and does not enter amax. Tokens may
+ * come in any order; when a slot is named twice, the later token of the call
+ * is written. Negative slots are skipped, slots past the cache set
+ * MLA_DEV_BAD_SLOT. mass (may be NULL), [num_blocks, block_size] float32, is
+ * set to 0 at the written slots.
+ *   workspace: mla_page8_write_workspace_size() bytes, 256-byte aligned; it
+ *   needs no initialisation. Calls that share it must not overlap.
+ */
+size_t mla_page8_write_workspace_size(const mla_config* cfg, int64_t num_tokens,
+                                      int64_t num_blocks);
+mla_status mla_page8_cache_write(const mla_config* cfg, const void* c_kv, const void* k_pe,
+                                 const int32_t* positions, const int64_t* slot_mapping,
+                                 int64_t num_tokens, const void* rms_weight, void* cache8,
+                                 float* page_scales, int64_t num_blocks, float* mass,
+                                 void* workspace, size_t ws_bytes, uint32_t* dev_status,
+                                 void* stream);
+
+/*
+ * mla_page8_decode -- attention of absorbed queries over page-scaled pages,
+ * projected to v_head_dim: mla_decode_paged_combine_fp8 and mla_out_proj for
+ * every supported head count and for prefill chunks (conventions, checks and
+ * device status bits of mla_decode_paged; num_q <= 48 * 1024).
+ *   s_t = softmax_scale * (S_t q_abs[n,h,0:512] . code_t + q_abs[n,h,512:576] . k_t)
+ *   out[n,h] = (sum_t softmax(s)_t S_t code_t) W_uv[h],   S_t = page_scales of t's page
+ *   q_abs [num_q, H, 576] bf16; W_uv [H, 512, 128] bf16; out [num_q, H, 128]
+ *   bf16, zeros for a row that sees no token. A page may appear in several
+ *   sequences. Scales below 2^-64 read as 2^-64.
+ *   workspace: mla_page8_decode_workspace_size(cfg, num_q, batch,
+ *   max_blocks_per_seq, with_mass) bytes, 256-byte aligned, mla_workspace_init
+ *   once; its first word is the device status. Calls that share it must not
+ *   overlap.
+ *
+ * mla_page8_decode_mass -- the same, and each visible token's attention weight
+ * accumulates at its slot of mass [num_blocks, block_size] float32:
+ *   mass[slot(t)] = decay * mass[slot(t)] + sum_{rows n of the sequence} sum_h p[n,h,t]
+ * for every token t of every sequence with a query row (0 <= decay <= 1; with
+ * decay 0 the old value is not read). The sum over rows and heads is fp32 in a
+ * fixed order. With this call a page belongs to one sequence of the batch
+ * only. Its workspace (with_mass = 1) also holds the scores: num_q * num_heads
+ * * max_blocks_per_seq * block_size floats.
+ */
+size_t mla_page8_decode_workspace_size(const mla_config* cfg, int64_t num_q, int32_t batch,
+                                       int32_t max_blocks_per_seq, int32_t with_mass);
+mla_status mla_page8_decode(const mla_config* cfg, const void* q_abs, const void* cache8,
+                            const float* page_scales, int64_t num_blocks,
+                            const int32_t* block_table, int32_t max_blocks_per_seq,
+                            const int32_t* seq_lens, const int32_t* query_start_loc,
+                            int32_t batch, int64_t num_q, const void* W_uv, void* workspace,
+                            size_t ws_bytes, void* out, void* stream);
+mla_status mla_page8_decode_mass(const mla_config* cfg, const void* q_abs, const void* cache8,
+                                 const float* page_scales, int64_t num_blocks,
+                                 const int32_t* block_table, int32_t max_blocks_per_seq,
+                                 const int32_t* seq_lens, const int32_t* query_start_loc,
+                                 int32_t batch, int64_t num_q, const void* W_uv, float* mass,
+                                 float decay, void* workspace, size_t ws_bytes, void* out,
+                                 void* stream);
+
+/*
+ * mla_evict_select -- which tokens of each sequence stay in a cache of at most
+ * `budget` tokens: all of them when seq_lens[b] <= budget; else the first
+ * `sinks`, the last `recent`, and of the others those of the largest mass
+ * (accumulated attention weight, as mla_page8_decode_mass keeps it), equal
+ * masses by the lower index. A NaN mass counts as the least.
+ *   mass [num_blocks, block_size] float32; block_table, seq_lens as above;
+ *   sinks, recent >= 0, budget >= 1, sinks + recent <= budget;
+ *   keep [batch, budget] int32 (output): the token indices that stay,
+ *   ascending, -1 behind them; new_lens [batch] int32 (output): their number.
+ * A sequence longer than its block table (MLA_DEV_BAD_SEQ) keeps nothing;
+ * tokens of a page out of range (MLA_DEV_BAD_BLOCK) count as NaN. dev_status
+ * may be NULL. No workspace.
+ */
+mla_status mla_evict_select(const mla_config* cfg, const float* mass, int64_t num_blocks,
+                            const int32_t* block_table, int32_t max_blocks_per_seq,
+                            const int32_t* seq_lens, int32_t batch, int32_t sinks, int32_t recent,
+                            int32_t budget, int32_t* keep, int32_t* new_lens,
+                            uint32_t* dev_status, void* stream);
+
+/*
+ * mla_page8_compact -- move the kept tokens of each sequence, in order, into
+ * the pages of dst_block_table [batch, dst_max_blocks]: token i of the new
+ * sequence is token keep[b][i] of the old one, i < new_lens[b]. The scale of a
+ * destination page becomes the largest scale of the pages its tokens come
+ * from; codes from smaller scales are recoded as in mla_page8_cache_write.
+ * mass (may be NULL) moves with the tokens. Keys keep the rotation of their
+ * old positions, so q_positions of later queries go on from the old length
+ * while seq_lens goes on from new_lens. The destination pages must not be
+ * pages of any block_table row (both live in the same cache), and each
+ * belongs to one sequence; the pages in block_table are left as they were and
+ * are the caller's to free afterwards. Destination rows behind new_lens[b]
+ * are left as they were. Entries out of range: keep MLA_DEV_BAD_SLOT (that
+ * row is skipped), pages MLA_DEV_BAD_BLOCK, new_lens beyond budget or the
+ * destination pages MLA_DEV_BAD_SEQ (that sequence is skipped).
+ */
+mla_status mla_page8_compact(const mla_config* cfg, void* cache8, float* page_scales, float* mass,
+                             int64_t num_blocks, const int32_t* block_table,
+                             int32_t max_blocks_per_seq, const int32_t* keep,
+                             const int32_t* new_lens, int32_t batch, int32_t budget,
+                             const int32_t* dst_block_table, int32_t dst_max_blocks,
+                             uint32_t* dev_status, void* stream);
+
+/*
  * mla_combine -- merge the split partials of mla_decode_paged.
  * For each (n, h): M = max_s lse_s, o_lat = sum_s 2^(lse_s - M) o_s /
  * sum_s 2^(lse_s - M) (the split-softmax identity; lse is kept in base 2

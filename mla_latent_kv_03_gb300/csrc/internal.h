@@ -117,6 +117,9 @@ cudaError_t launch_wait_timeout_selftest(uint32_t* status, int64_t timeout_ns,
 // the TMA descriptors (bf16, 128-byte swizzle) of 576-value rows and of a
 // row-major [rows, cols] matrix.
 mla_status validate_config(const mla_config* cfg);
+// The CTA count of a split-KV launch: cfg->num_ctas, or one per SM of the
+// current device (-1 if the device cannot be asked).
+int split_ctas(const mla_config* cfg);
 // Every host-side check mla_decode_paged makes on its arguments other than
 // the workspace (configuration, sizes, row limit, null and misaligned
 // pointers); MLA_OK for num_q == 0 once the sizes are valid.

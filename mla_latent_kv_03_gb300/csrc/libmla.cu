@@ -218,6 +218,7 @@ inline mla_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MLA_OK : 
 
 namespace mla {
 mla_status validate_config(const mla_config* cfg) { return check_cfg(cfg); }
+int split_ctas(const mla_config* cfg) { return resolve_num_ctas(cfg); }
 
 mla_status decode_paged_checks(const mla_config* cfg, const void* q_abs, const void* cache,
                                int64_t num_blocks, const int32_t* block_table,

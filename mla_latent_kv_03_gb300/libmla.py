@@ -32,6 +32,8 @@ EXPORTS = (
     "mla_decode_combine", "mla_decode_paged_combine", "mla_decode_paged_noalloc",
     "mla_combine_out_proj", "mla_cache_write_fp8", "mla_decode_fp8_workspace_size",
     "mla_decode_paged_combine_fp8",
+    "mla_page8_write_workspace_size", "mla_page8_cache_write", "mla_page8_decode_workspace_size",
+    "mla_page8_decode", "mla_page8_decode_mass", "mla_evict_select", "mla_page8_compact",
     "mla_proj_workspace_size", "mla_q_proj", "mla_kv_a_proj", "mla_o_proj",
     "mla_naive_workspace_size", "mla_naive_cache_write",
     "mla_latent_expand", "mla_latent_expand_prepare", "mla_latent_expand_prepared",
@@ -86,6 +88,18 @@ _SIGS = {
                                    _i64, _vp, _vp]),
     "mla_decode_paged_combine_fp8": (_i32, [_cfgp, _vp, _vp, _i64, _vp, _i32, _vp, _vp, _i32,
                                             _i64, ctypes.c_float, _vp, _sz, _vp, _vp]),
+    "mla_page8_write_workspace_size": (_sz, [_cfgp, _i64, _i64]),
+    "mla_page8_cache_write": (_i32, [_cfgp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp,
+                                     _sz, _vp, _vp]),
+    "mla_page8_decode_workspace_size": (_sz, [_cfgp, _i64, _i32, _i32, _i32]),
+    "mla_page8_decode": (_i32, [_cfgp, _vp, _vp, _vp, _i64, _vp, _i32, _vp, _vp, _i32, _i64, _vp,
+                                _vp, _sz, _vp, _vp]),
+    "mla_page8_decode_mass": (_i32, [_cfgp, _vp, _vp, _vp, _i64, _vp, _i32, _vp, _vp, _i32, _i64,
+                                     _vp, _vp, ctypes.c_float, _vp, _sz, _vp, _vp]),
+    "mla_evict_select": (_i32, [_cfgp, _vp, _i64, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _vp,
+                                _vp, _vp]),
+    "mla_page8_compact": (_i32, [_cfgp, _vp, _vp, _vp, _i64, _vp, _i32, _vp, _vp, _i32, _i32, _vp,
+                                 _i32, _vp, _vp]),
     "mla_naive_workspace_size": (_sz, [_cfgp, _i64, _i32, _i64]),
     "mla_naive_cache_write": (_i32, [_cfgp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _i64,
                                      _vp, _sz, _vp]),
@@ -313,6 +327,116 @@ def mla_naive_workspace_size(cfg: MlaConfig, num_q: int, max_blocks_per_seq: int
 
 def _nbytes(t) -> int:
     return t.numel() * t.element_size()
+
+
+def _shape(t, shape, name: str) -> None:
+    """Refuse a tensor whose size is not the one the call reads or writes."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def mla_page8_write_workspace_size(cfg: MlaConfig, num_tokens: int, num_blocks: int) -> int:
+    return int(load().mla_page8_write_workspace_size(ctypes.byref(cfg), num_tokens, num_blocks))
+
+
+def _page8_pages(cfg: MlaConfig, cache8, page_scales, mass):
+    nb = cache8.shape[0]
+    _shape(cache8, (nb, cfg.block_size, 640), "cache8")
+    _shape(page_scales, (nb,), "page_scales")
+    if mass is not None:
+        _shape(mass, (nb, cfg.block_size), "mass")
+    return nb
+
+
+def mla_page8_cache_write(cfg: MlaConfig, c_kv, k_pe, positions, slot_mapping, rms_weight, cache8,
+                          page_scales, workspace, mass=None, dev_status=None, stream=None) -> None:
+    nb, n = _page8_pages(cfg, cache8, page_scales, mass), c_kv.shape[0]
+    _shape(c_kv, (n, 512), "c_kv")
+    _shape(k_pe, (n, 64), "k_pe")
+    _shape(positions, (n,), "positions")
+    _shape(slot_mapping, (n,), "slot_mapping")
+    _shape(rms_weight, (512,), "rms_weight")
+    bf = torch.bfloat16
+    _check(load().mla_page8_cache_write(
+        ctypes.byref(cfg), _ptr(c_kv, bf, "c_kv"), _ptr(k_pe, bf, "k_pe"),
+        _ptr(positions, torch.int32, "positions"), _ptr(slot_mapping, torch.int64, "slot_mapping"),
+        n, _ptr(rms_weight, bf, "rms_weight"), _ptr(cache8, torch.uint8, "cache8"),
+        _ptr(page_scales, torch.float32, "page_scales"), nb, _ptr(mass, torch.float32, "mass"),
+        _ptr(workspace, None, "workspace"), _nbytes(workspace),
+        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)), "mla_page8_cache_write")
+
+
+def mla_page8_decode_workspace_size(cfg: MlaConfig, num_q: int, batch: int, max_blocks_per_seq: int,
+                                    with_mass: bool = False) -> int:
+    return int(load().mla_page8_decode_workspace_size(ctypes.byref(cfg), num_q, batch,
+                                                      max_blocks_per_seq, int(bool(with_mass))))
+
+
+def _page8_decode_args(cfg, q_abs, cache8, page_scales, block_table, seq_lens, query_start_loc,
+                       W_uv, mass, out):
+    nb, n, b, H = _page8_pages(cfg, cache8, page_scales, mass), q_abs.shape[0], seq_lens.shape[0], cfg.num_heads
+    _shape(q_abs, (n, H, 576), "q_abs")
+    _shape(block_table, (b, block_table.shape[1]), "block_table")
+    _shape(query_start_loc, (b + 1,), "query_start_loc")
+    _shape(W_uv, (H, 512, 128), "W_uv")
+    _shape(out, (n, H, 128), "out")
+    bf = torch.bfloat16
+    return [ctypes.byref(cfg), _ptr(q_abs, bf, "q_abs"), _ptr(cache8, torch.uint8, "cache8"),
+            _ptr(page_scales, torch.float32, "page_scales"), nb,
+            _ptr(block_table, torch.int32, "block_table"), block_table.shape[1],
+            _ptr(seq_lens, torch.int32, "seq_lens"),
+            _ptr(query_start_loc, torch.int32, "query_start_loc"), b, n, _ptr(W_uv, bf, "W_uv")]
+
+
+def mla_page8_decode(cfg: MlaConfig, q_abs, cache8, page_scales, block_table, seq_lens,
+                     query_start_loc, W_uv, workspace, out, stream=None) -> None:
+    args = _page8_decode_args(cfg, q_abs, cache8, page_scales, block_table, seq_lens,
+                              query_start_loc, W_uv, None, out)
+    _check(load().mla_page8_decode(
+        *args, _ptr(workspace, None, "workspace"), _nbytes(workspace),
+        _ptr(out, torch.bfloat16, "out"), _stream(stream)), "mla_page8_decode")
+
+
+def mla_page8_decode_mass(cfg: MlaConfig, q_abs, cache8, page_scales, block_table, seq_lens,
+                          query_start_loc, W_uv, mass, decay: float, workspace, out,
+                          stream=None) -> None:
+    args = _page8_decode_args(cfg, q_abs, cache8, page_scales, block_table, seq_lens,
+                              query_start_loc, W_uv, mass, out)
+    _check(load().mla_page8_decode_mass(
+        *args, _ptr(mass, torch.float32, "mass"), float(decay), _ptr(workspace, None, "workspace"),
+        _nbytes(workspace), _ptr(out, torch.bfloat16, "out"), _stream(stream)),
+        "mla_page8_decode_mass")
+
+
+def mla_evict_select(cfg: MlaConfig, mass, block_table, seq_lens, sinks: int, recent: int, keep,
+                     new_lens, dev_status=None, stream=None) -> None:
+    """The budget is keep.shape[1]."""
+    nb, b = mass.shape[0], seq_lens.shape[0]
+    _shape(mass, (nb, cfg.block_size), "mass")
+    _shape(block_table, (b, block_table.shape[1]), "block_table")
+    _shape(keep, (b, keep.shape[1]), "keep")
+    _shape(new_lens, (b,), "new_lens")
+    _check(load().mla_evict_select(
+        ctypes.byref(cfg), _ptr(mass, torch.float32, "mass"), nb,
+        _ptr(block_table, torch.int32, "block_table"), block_table.shape[1],
+        _ptr(seq_lens, torch.int32, "seq_lens"), b, sinks, recent, keep.shape[1],
+        _ptr(keep, torch.int32, "keep"), _ptr(new_lens, torch.int32, "new_lens"),
+        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)), "mla_evict_select")
+
+
+def mla_page8_compact(cfg: MlaConfig, cache8, page_scales, mass, block_table, keep, new_lens,
+                      dst_block_table, dev_status=None, stream=None) -> None:
+    nb, b = _page8_pages(cfg, cache8, page_scales, mass), new_lens.shape[0]
+    _shape(block_table, (b, block_table.shape[1]), "block_table")
+    _shape(keep, (b, keep.shape[1]), "keep")
+    _shape(dst_block_table, (b, dst_block_table.shape[1]), "dst_block_table")
+    _check(load().mla_page8_compact(
+        ctypes.byref(cfg), _ptr(cache8, torch.uint8, "cache8"),
+        _ptr(page_scales, torch.float32, "page_scales"), _ptr(mass, torch.float32, "mass"), nb,
+        _ptr(block_table, torch.int32, "block_table"), block_table.shape[1],
+        _ptr(keep, torch.int32, "keep"), _ptr(new_lens, torch.int32, "new_lens"), b, keep.shape[1],
+        _ptr(dst_block_table, torch.int32, "dst_block_table"), dst_block_table.shape[1],
+        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)), "mla_page8_compact")
 
 
 def mla_naive_cache_write(cfg: MlaConfig, c_kv, k_pe, positions, slot_mapping, rms_weight, W_uk,

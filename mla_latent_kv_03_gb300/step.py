@@ -154,6 +154,62 @@ class MlaDecodeStep:
                                        self.seq_lens, self.query_start_loc, self.kv_scale,
                                        self.workspace, self.o_lat, stream=stream)
 
+    # -- the page-scaled 8-bit cache, and eviction from it --------------------
+    def page8_setup(self, with_mass: bool = False, spare_blocks: int = 0) -> None:
+        """Pages of e4m3 codes, one scale per page, `spare_blocks` free pages
+        behind the workload's, and (with_mass) a weight per cached token."""
+        w, dev = self.w, self.device
+        self.p8_blocks = w.num_blocks + spare_blocks
+        self.p8_cache = torch.empty((self.p8_blocks, w.block_size, 640), dtype=torch.uint8, device=dev)
+        self.p8_scales = torch.zeros(self.p8_blocks, dtype=torch.float32, device=dev)
+        self.p8_mass = (torch.zeros((self.p8_blocks, w.block_size), dtype=torch.float32, device=dev)
+                        if with_mass else None)
+        self.p8_table, self.p8_lens = self.block_table, self.seq_lens
+        need = L.mla_page8_decode_workspace_size(self.cfg, w.num_q, w.batch,
+                                                 self.block_table.shape[1], with_mass)
+        wneed = L.mla_page8_write_workspace_size(self.cfg, int(self.c_kv.shape[0]), self.p8_blocks)
+        if need == 0 or wneed == 0:
+            raise L.MlaError(L.MLA_OK + 2, "mla_page8_decode_workspace_size")
+        self.p8_ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        self.p8_write_ws = torch.empty(wneed, dtype=torch.uint8, device=dev)
+        L.mla_workspace_init(self.p8_ws)
+
+    def page8_populate(self) -> None:
+        L.mla_page8_cache_write(self.cfg, self.c_kv, self.k_pe, self.kv_positions, self.slot_mapping,
+                                self.rms_weight, self.p8_cache, self.p8_scales, self.p8_write_ws,
+                                mass=self.p8_mass, dev_status=self.status)
+
+    def page8_write_new(self, stream=None) -> None:
+        L.mla_page8_cache_write(self.cfg, self.c_kv_new, self.k_pe_new, self.pos_new, self.slot_new,
+                                self.rms_weight, self.p8_cache, self.p8_scales, self.p8_write_ws,
+                                mass=self.p8_mass, dev_status=self.status, stream=stream)
+
+    def page8_decode(self, decay: float = 1.0, stream=None) -> torch.Tensor:
+        """The step's attention and output projection; with a mass, the
+        weights accumulate too."""
+        if self.p8_mass is None:
+            L.mla_page8_decode(self.cfg, self.q_abs, self.p8_cache, self.p8_scales, self.p8_table,
+                               self.p8_lens, self.query_start_loc, self.W_uv, self.p8_ws, self.out,
+                               stream=stream)
+        else:
+            L.mla_page8_decode_mass(self.cfg, self.q_abs, self.p8_cache, self.p8_scales,
+                                    self.p8_table, self.p8_lens, self.query_start_loc, self.W_uv,
+                                    self.p8_mass, decay, self.p8_ws, self.out, stream=stream)
+        return self.out
+
+    def page8_evict(self, budget: int, sinks: int, recent: int, dst_block_table, stream=None):
+        """Cut every sequence to `budget` tokens, moved into the pages of
+        dst_block_table, which becomes the sequences' table. Returns (keep,
+        new lengths)."""
+        keep = torch.empty((self.w.batch, budget), dtype=torch.int32, device=self.device)
+        lens = torch.empty(self.w.batch, dtype=torch.int32, device=self.device)
+        L.mla_evict_select(self.cfg, self.p8_mass, self.p8_table, self.p8_lens, sinks, recent, keep,
+                           lens, dev_status=self.status, stream=stream)
+        L.mla_page8_compact(self.cfg, self.p8_cache, self.p8_scales, self.p8_mass, self.p8_table,
+                            keep, lens, dst_block_table, dev_status=self.status, stream=stream)
+        self.p8_table, self.p8_lens = dst_block_table, lens
+        return keep, lens
+
     # -- the projections either side (the whole attention layer) -----------
     def layer_setup(self, hidden_size: int = 2048, seed: int = 7) -> None:
         """Hidden states of every token and the q_proj / kv_a_proj / o_proj
