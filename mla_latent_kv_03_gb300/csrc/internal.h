@@ -128,6 +128,9 @@ mla_status decode_paged_checks(const mla_config* cfg, const void* q_abs, const v
                                int32_t max_blocks_per_seq, const int32_t* seq_lens,
                                const int32_t* query_start_loc, int32_t batch, int64_t num_q);
 bool encode_row_map(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows);
+// The two views of a 640-byte-row FP8 cache (see make_fp8_maps in libmla.cu).
+bool encode_fp8_maps(CUtensorMap* codes, CUtensorMap* rope, const void* base, uint64_t rows,
+                     uint32_t box_rows);
 bool encode_map_2d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
                    uint32_t box_cols, uint32_t box_rows);
 // 3-D map over (d, head, row) of a [rows, heads, dims] bf16 tensor: box =

@@ -241,6 +241,10 @@ mla_status decode_paged_checks(const mla_config* cfg, const void* q_abs, const v
 bool encode_row_map(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows) {
   return make_row_map(map, base, rows, box_rows);
 }
+bool encode_fp8_maps(CUtensorMap* codes, CUtensorMap* rope, const void* base, uint64_t rows,
+                     uint32_t box_rows) {
+  return make_fp8_maps(codes, rope, base, rows, box_rows);
+}
 bool encode_map_2d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
                    uint32_t box_cols, uint32_t box_rows) {
   return make_map_2d(map, base, cols, rows, box_cols, box_rows);

@@ -6,9 +6,44 @@
 // For query row n, head h and token t of page p with scale S_p:
 //   s_t = softmax_scale * log2(e) * (S_p q_lat . code_t + q_rope . k_t)   (base 2)
 //   o   = sum_t 2^(s_t - lse) S_p code_t,     lse = log2 sum_t 2^(s_t)
-// The work is cut as in the other decodes (plan_kernel: units of one row, 16
-// heads and 64 tokens in equal contiguous shares), the parts are merged by the
-// CTA that finishes a (row, 16 heads) last.
+//
+// The codes go to the 5th-generation tensor cores as they lie in the cache
+// (kind::f8f6f4, fp32 accumulation in TMEM): nothing is dequantised. For that
+// the 128 tokens of a tile are the rows of both products, and the few
+// (row, head) columns are the other operand, split into 8-bit terms that are
+// columns of their own, so a tile is read from shared memory once for all of
+// them:
+//   scores  S[128 tokens, 2 NH] = codes[128, 512] . (q_1 | q_2)^T,
+//           R[128 tokens, NH]   = k[128, 64] . q_rope^T  (bf16)
+//     q_lat 2^a = q_1 + 2^-5 q_2 in e4m3, a per head: both terms together hold
+//     a bf16 exactly down to 2^-15 of the head's largest, and the rest within
+//     2^-23 of that largest;
+//   output  O[512, 3 NH] = codes[128, 512]^T . (p_1 | p_2 | p_3)
+//     p = p_1 + p_2 + p_3 in e5m2: 9 significant bits (error 2^-10), down to
+//     2^-27 of the running reference, so a long tail of small weights behind a
+//     large one is not lost.
+// The page's scale enters a score as a factor of its token (a row), and the
+// output as part of the weight: the columns hold 2^(s_t - ref) S_p, and the
+// softmax sum adds the same number divided by S_p again. The running reference
+// of a head follows s_t + log2 S_p, and O is rescaled in TMEM only when it is
+// outgrown by more than 2^3.
+//
+// NH = 16 or 32 heads of one row make a column group. The work is cut as in
+// the other decodes (units of one row, one group and 64 tokens in equal
+// contiguous shares, one CTA a share). Per CTA (384 threads):
+//   warp 0      copies: 128 tokens a stage (4 slabs of 128 codes, one of rope
+//               values), two stages, SWIZZLE_128B; block ids are checked;
+//   warp 1      issues every MMA from one lane: scores of tile i, then the
+//               output of tile i - 1, so the softmax of a tile has two products
+//               to hide behind; owns the TMEM;
+//   warps 2-3   split the query of the next segment into its terms;
+//   warps 4-11  softmax: thread r of each half owns token r and half of the
+//               heads. Token rows that are not live are zeroed in the stage,
+//               so a weight of 0 never meets a NaN code.
+// Every wait is bounded; on a timeout the roles leave their loops, the issuer
+// waits for its products and the copies' warp for its copies before TMEM is
+// freed.
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "async_copy.cuh"
@@ -16,205 +51,807 @@
 #include "merge.cuh"
 #include "page8.cuh"
 #include "sched.cuh"
+#include "tcgen05.cuh"
 
 namespace mla {
 namespace {
 
-constexpr int kSub = 16;  // tokens per inner step
+constexpr int kTok = 128;                     // tokens per stage
+constexpr int kSlab = kTok * 128;             // 128 rows of 128 bytes
+constexpr int kStageB = 5 * kSlab;            // four slabs of codes, one of rope values
+constexpr int kThreads = 384;
+constexpr int kSoftWarp0 = 4, kSoftThreads = 256;
+constexpr int kSoftBar = 1, kHalfBar = 2;     // named barriers: all softmax warps; one half (2, 3)
+constexpr float kRefLog2 = 11.f;              // a weight equal to the reference is held as 2^11
+constexpr float kGrowLog2 = 3.f;              // the reference follows when outgrown by 2^3
+constexpr uint32_t kTmemCols = 512, kSCol = 0, kOCol = 128;
 
 struct P8Args {
-  const __nv_bfloat16* q_abs;
-  const uint8_t* cache8;
+  const uint16_t* q_abs;
   const float* scales;
   int64_t num_blocks;
   const int32_t* block_table;
   int32_t max_blocks;
   int32_t block_size;
   int32_t num_heads;
-  int32_t groups;
+  int32_t groups;     // column groups of a row: num_heads / NH
   int32_t num_ctas;
   int64_t num_q;
   float scale_log2;
   uint8_t* ws;
-  float* o_lat;       // [num_q, H, 512]
-  float* lse;         // [num_q, H], base 2
-  float* scores;      // [num_q, groups, max tokens, 16], base 2; NULL without mass
+  float* lse_part[2];  // [slots][16] of each 16 heads of a group
+  float* o_part[2];    // [slots][16][512]
+  float* o_lat;        // [num_q, H, 512]
+  float* lse;          // [num_q, H], base 2
+  float* scores;       // [num_q, H / 16, max tokens, 16], base 2; NULL without mass
+  int32_t fused;       // merge the splits here
 };
 
-// The decode workspace: the split plan and partials of ws_layout, then
-// the merged latents, their log-sum-exps and (with mass) the scores.
+// The decode workspace: the split plan and the partials of ws_layout, the
+// partials of a group's second 16 heads, the merged latents, their
+// log-sum-exps and (with mass) the scores.
 struct P8Ws {
-  size_t o_lat, lse, scores, total;
+  size_t lse2, opart2, o_lat, lse, scores, total;
 };
+int group_heads(int H) { return H >= 32 ? 32 : 16; }
 P8Ws p8_ws(int64_t num_q, int H, int num_ctas, int64_t max_tokens, bool mass) {
+  const int NH = group_heads(H);
+  const WsLayout W = ws_layout(num_q, H / NH, num_ctas);
   P8Ws L;
-  L.o_lat = align_up(ws_layout(num_q, H / kHG, num_ctas).total, 256);
+  L.lse2 = align_up(W.total, 256);
+  L.opart2 = NH == 32 ? align_up(L.lse2 + (size_t)W.slots * kHG * 4, 256) : L.lse2;
+  L.o_lat = NH == 32 ? align_up(L.opart2 + (size_t)W.slots * kHG * kDc * 4, 256) : L.lse2;
   L.lse = align_up(L.o_lat + (size_t)num_q * H * kDc * 4, 256);
   L.scores = align_up(L.lse + (size_t)num_q * H * 4, 256);
   L.total = mass ? align_up(L.scores + (size_t)num_q * H * max_tokens * 4, 256) : L.scores;
   return L;
 }
 
-__device__ __forceinline__ float page_scale(float s) {
-  return fmaxf(s, __uint_as_float((uint32_t)(kP8MinExp + 127) << 23));
+// Shared memory of one CTA.
+template <int NH>
+struct Sm {
+  static constexpr int QB = NH == 16 ? 2 : 1;           // query buffers
+  static constexpr int q_slab = 2 * NH * 128;           // 128 codes of every term row
+  static constexpr int q_rope = 4 * q_slab;
+  static constexpr int q_bytes = q_rope + NH * 128;
+  static constexpr int p_bytes = 3 * NH * kTok;         // blocks of 16 columns: [16][8 tokens][16 bytes]
+  static constexpr int stage = 0;
+  static constexpr int q = stage + 2 * kStageB;
+  static constexpr int p = q + QB * q_bytes;
+  static constexpr int coef = p + 2 * p_bytes;          // [QB][NH] score factor of a head
+  static constexpr int red = coef + QB * NH * 4;         // [8 warps][NH / 2]
+  static constexpr int merge = red + 8 * (NH / 2) * 4;  // merge scratch, one per half
+  static constexpr int merge_bytes = (2 * kHG + kMergeChunk * kHG) * 4;
+  static constexpr int info = merge + 2 * merge_bytes;  // [2] live rows of a stage
+  static constexpr int scale = info + 16;               // [2][8] page scales of a stage, -1: no page
+  static constexpr int bars = scale + 64;
+  static constexpr int misc = bars + 24 * 8;            // TMEM base, abort flag, merge flag
+  static constexpr int bytes = misc + 16;
+  static constexpr int alloc = bytes + 1024;
+  static_assert(alloc <= 227 * 1024, "shared memory budget");
+  static_assert(q % 1024 == 0 && q_rope % 1024 == 0 && q_bytes % 1024 == 0 && p % 128 == 0, "swizzle atoms");
+  static_assert(bars % 8 == 0 && merge % 16 == 0, "alignment");
+};
+
+enum {
+  kFull = 0,      // [2] stage landed
+  kEmpty = 2,     // [2] stage's products done
+  kQReady = 4,    // [2] query terms stored (2 arrivals)
+  kQFree = 6,     // [2] the segment's score products done, its factors read (1 + 8 arrivals)
+  kSFull = 8,     // scores in TMEM
+  kSFree = 9,     // scores read (8 arrivals)
+  kPFull = 10,    // [2] weights stored (8 arrivals)
+  kPVDone = 12,   // [2] output products done
+  kODone = 14,    // the segment's output products done
+  kOFree = 15,    // the output read (8 arrivals)
+  kFinal = 16,    // every product done
+  kNumBars = 17
+};
+
+// Instruction descriptor, kind::f8f6f4, fp32 accumulator: A e4m3, B e4m3 (0) or
+// e5m2 (1), each K-major or MN-major.
+__host__ __device__ constexpr uint32_t idesc_f8(int N, int b_type, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((uint32_t)b_type << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kTok >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                       bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
 }
 
-__global__ void __launch_bounds__(256) page8_decode_kernel(P8Args a) {
-  extern __shared__ float smem_f[];
-  float* sQ = smem_f;                         // [16][576]
-  float* sK = sQ + kHG * kRow;                // [16][577], dequantised
-  float* sP = sK + kSub * (kRow + 1);         // [16][16]
-  float* sA = sP + kHG * kSub;                // [16] alpha
-  float* sL = sA + kHG;                       // [16] final l
-  float* sM = sL + kHG;                       // [16] final m
-  float* sMerge = sM + kHG;                   // fused-merge scratch
-  int* sFlag = reinterpret_cast<int*>(sMerge + 2 * kHG + kMergeChunk * kHG);
-  int64_t* sOff = reinterpret_cast<int64_t*>(sFlag + 2);  // [kSub] cache row, -1: none
-  float* sS = reinterpret_cast<float*>(sOff + kSub);      // [kSub] page scales
-  const int tid = threadIdx.x;
-  const int h = tid >> 4, j = tid & 15;       // score role: head h, token j
-  const int d0 = tid * 2;                     // output role: columns d0, d0 + 1 of all heads
-  WsHeader* hdr = reinterpret_cast<WsHeader*>(a.ws);
+// Lane l reads (writes) N consecutive 32-bit columns of TMEM lane (base + l).
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&r)[N]) {
+  static_assert(N == 8 || N == 16, "shapes in use");
+  if constexpr (N == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]),
+                   "=f"(r[6]), "=f"(r[7])
+                 : "r"(taddr));
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+          "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]),
+          "=f"(r[14]), "=f"(r[15])
+        : "r"(taddr));
+  }
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&r)[N]) {
+  if constexpr (N == 8) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+                 "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
+                 : "memory");
+  } else {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]),
+        "f"(r[8]), "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15])
+        : "memory");
+  }
+}
+
+// Bounded wait that also gives up when another role has aborted.
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 15u) == 0) {
+      if (*abort_flag) return false;
+      if (globaltimer_ns() - t0 > kWaitTimeoutNs) return false;
+    }
+  }
+}
+
+__device__ __forceinline__ bool bar_or(int id, int nthreads, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\t"
+      "barrier.red.or.pred po, %2, %3, pi;\n\tselp.u32 %0, 1, 0, po;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id), "r"(nthreads)
+      : "memory");
+  return r != 0;
+}
+
+// The largest of a value over the warp (NaN does not count).
+__device__ __forceinline__ float warp_max(float x) {
+  int i = __float_as_int(isnan(x) ? -INFINITY : x);
+  i ^= (i >> 31) & 0x7fffffff;  // the integer order of the floats
+  i = __reduce_max_sync(0xffffffffu, i);
+  return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+}
+
+// The log-sum-exp of merged parts from their largest and 1 / the weight sum
+// (0 where the sum is not a positive number).
+__device__ __forceinline__ float merged_lse(float m, float inv) {
+  if (m == -INFINITY) return m;
+  return inv > 0.f ? m - log2f(inv) : __int_as_float(0x7fffffff);
+}
+
+// The two e4m3 terms of 16 scaled query values (eight bf16 pairs in u):
+// t1 = e4m3(x), t2 = e4m3((x - t1) 2^5); a value that is not finite is NaN.
+__device__ __forceinline__ void query_terms(const uint32_t* u, float f, uint4& t1, uint4& t2) {
+  uint32_t a[4], b[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    a[k] = b[k] = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t w = u[2 * k + i];
+      // (inf - inf = NaN)
+      float x0 = __uint_as_float(w << 16), x1 = __uint_as_float(w & 0xffff0000u);
+      x0 = isinf(x0) ? __int_as_float(0x7fffffff) : x0 * f;
+      x1 = isinf(x1) ? __int_as_float(0x7fffffff) : x1 * f;
+      const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+      const float2 v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
+      const __nv_fp8x2_storage_t d = __nv_cvt_float2_to_fp8x2(
+          make_float2((x0 - v.x) * 32.f, (x1 - v.y) * 32.f), __NV_SATFINITE, __NV_E4M3);
+      a[k] |= (uint32_t)c << (16 * i);
+      b[k] |= (uint32_t)d << (16 * i);
+    }
+  }
+  t1 = make_uint4(a[0], a[1], a[2], a[3]);
+  t2 = make_uint4(b[0], b[1], b[2], b[3]);
+}
+
+template <int NH>
+__global__ void __launch_bounds__(kThreads, 1)
+    page8_decode_kernel(const __grid_constant__ CUtensorMap codes_map,
+                        const __grid_constant__ CUtensorMap rope_map, const __grid_constant__ P8Args a) {
+  using S = Sm<NH>;
+  constexpr int QB = S::QB, HT = NH / 2;  // heads of a softmax thread
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::bars);
+  int* info = reinterpret_cast<int*>(sm + S::info);
+  float* page_sc = reinterpret_cast<float*>(sm + S::scale);
+  float* coef = reinterpret_cast<float*>(sm + S::coef);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::misc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::misc + 4);
+  int* merge_flag = reinterpret_cast<int*>(sm + S::misc + 8);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const WsLayout L = ws_layout(a.num_q, a.groups, a.num_ctas);
-  float* lse_out = reinterpret_cast<float*>(a.ws + L.lse);
-  float* o_out = reinterpret_cast<float*>(a.ws + L.opart);
-  pdl_wait();
+  uint32_t* status = &reinterpret_cast<WsHeader*>(a.ws)->status;
+  const int bs = a.block_size;
+  const int bs_shift = bs == 16 ? 4 : (bs == 32 ? 5 : 6);
+
+  if (tid == 0) {
+    for (int i = 0; i < kNumBars; ++i) {
+      const int n = (i == kSFree || i == kPFull || i == kPFull + 1 || i == kOFree) ? kSoftThreads / 32
+                    : (i == kQReady || i == kQReady + 1) ? 2
+                    : (i == kQFree || i == kQFree + 1)   ? 1 + kSoftThreads / 32
+                                                         : 1;
+      mbar_init(&bars[i], n);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&codes_map);
+    prefetch_tensormap(&rope_map);
+  }
+  if (warp == 1) tc::alloc(tmem_slot, kTmemCols);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();  // the plan and q_abs come from earlier kernels
   pdl_launch_dependents();
 
   SchedWalker sw;
   const bool has_work = sw.init(a.ws, a.num_q, a.groups, a.num_ctas, blockIdx.x);
-  zero_unvisited_rows(sw.row_info, sw.plan_ok, a.num_q, a.num_heads, a.o_lat, tid, 256);
-  if (!has_work) return;
-  Segment seg;
-  while (sw.next(seg)) {
-    const int t = seg.n * a.groups + seg.g;
-    const int64_t slot = (int64_t)blockIdx.x + t;
-    __syncthreads();
-    const __nv_bfloat16* qsrc = a.q_abs + ((size_t)seg.n * a.num_heads + seg.g * kHG) * kRow;
-    for (int i = tid; i < kHG * kRow; i += 256) sQ[i] = __bfloat162float(qsrc[i]);
-    float m = -INFINITY, l = 0.f;
-    float o[kHG][2];
+  if (a.fused && warp >= kSoftWarp0)
+    zero_unvisited_rows(sw.row_info, sw.plan_ok, a.num_q, a.num_heads, a.o_lat,
+                        tid - kSoftWarp0 * 32, kSoftThreads);
+  Segment seg{};
+  // tokens of the segment: [k0 * 64, end), in tiles of 128
+  auto seg_end = [&] { return min(seg.pos + 1, seg.k1 * kTile); };
+  auto seg_tiles = [&] { return (seg_end() - seg.k0 * kTile + kTok - 1) / kTok; };
+  auto warp_wait = [&](int bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_or_abort(&bars[bar], parity, abort_flag));
+  };
+
+  if (has_work && warp == 0) {
+    // -------------------------------------------------------------- copies
+    const uint64_t policy = l2_evict_first_policy();
+    int i = 0;
+    bool ok = true;
+    while (ok && sw.next(seg)) {
+      const int32_t* bt = a.block_table + (size_t)seg.b * a.max_blocks;
+      const int end = seg_end(), n = seg_tiles();
+      // lane l holds block-table entry base + l and its page's scale
+      int base = -(1 << 30), id = -1;
+      float sc = -1.f;
+#pragma unroll 1
+      for (int t = 0; t < n; ++t, ++i) {
+        const int t0 = seg.k0 * kTile + t * kTok, v = min(kTok, end - t0), slot = i & 1;
+        const int b0 = t0 >> bs_shift, pages = (v + bs - 1) >> bs_shift;  // at most 8
+        if (b0 < base || b0 + pages > base + 32) {
+          base = b0;
+          id = base + lane < a.max_blocks ? bt[base + lane] : -1;
+          const bool fine = id >= 0 && id < a.num_blocks;
+          sc = fine ? fmaxf(a.scales[id], __uint_as_float((uint32_t)(kP8MinExp + 127) << 23)) : -1.f;
+          if (!fine) id = -1;
+        }
+        if (i >= 2 && !warp_wait(kEmpty + slot, ((i >> 1) - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        const int src = (b0 - base + lane) & 31;
+        const int my_id = __shfl_sync(0xffffffffu, id, src);
+        const float my_sc = __shfl_sync(0xffffffffu, sc, src);
+        const bool mine = lane < pages && my_id >= 0;
+        if (lane < 8) page_sc[slot * 8 + lane] = mine ? my_sc : -1.f;
+        const uint32_t okmask = __ballot_sync(0xffffffffu, mine);
+        if (lane == 0) {
+          if (__popc(okmask) != pages) set_status(status, MLA_DEV_BAD_BLOCK);
+          info[slot] = v;
+          mbar_arrive_expect_tx(&bars[kFull + slot], (uint32_t)(__popc(okmask) * 5 * bs * 128));
+        }
+        __syncwarp();
+        // lanes 0-4 each copy one slab of every page
+        uint8_t* dst = sm + S::stage + slot * kStageB + (lane < 5 ? lane : 0) * kSlab;
+        for (int p = 0; p < pages; ++p) {
+          const int y = __shfl_sync(0xffffffffu, my_id, p) << bs_shift;
+          if (!((okmask >> p) & 1)) continue;
+          if (lane < 4)
+            tma_load_2d_hint(dst + (p << bs_shift) * 128, &codes_map, 128 * lane, y, &bars[kFull + slot], policy);
+          else if (lane == 4)
+            tma_load_2d_hint(dst + (p << bs_shift) * 128, &rope_map, kDc / 2, y, &bars[kFull + slot], policy);
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) {
+      if (!ok) {
+        set_status(status, MLA_DEV_TIMEOUT);
+        *abort_flag = 1;
+      }
+      // never leave with copies in flight
+      for (int slot = 0; slot < 2; ++slot) {
+        const int fills = i > slot ? (i - 1 - slot) / 2 + 1 : 0;
+        if (fills > 0 && !mbar_wait(&bars[kFull + slot], (fills - 1) & 1))
+          set_status(status, MLA_DEV_TIMEOUT);
+      }
+    }
+    __syncwarp();
+  } else if (has_work && warp == 1) {
+    // ------------------------------------------------------------ products
+    constexpr uint32_t kIdS = idesc_f8(2 * NH, 0, false, false);
+    constexpr uint32_t kIdR = tc::idesc_bf16(kTok, NH, false, false);
+    constexpr uint32_t kIdO = idesc_f8(3 * NH, 1, true, true);
+    const uint64_t kdesc = tc::smem_desc(smem_u32(sm + S::stage), 16, 1024, tc::kSwizzle128);
+    const uint64_t vdesc = tc::smem_desc(smem_u32(sm + S::stage), kSlab, 1024, tc::kSwizzle128);
+    const uint64_t qdesc = tc::smem_desc(smem_u32(sm + S::q), 16, 1024, tc::kSwizzle128);
+    // weights: 16-byte cores of 16 columns, 8 tokens of a core group 128 bytes
+    // (leading), blocks of 16 columns 2,048 bytes apart (stride), no swizzle
+    const uint64_t pdesc = tc::smem_desc(smem_u32(sm + S::p), 128, 2048, 0);
+    const bool leader = tc::elect_one();
+    int i = 0, seg_i = 0, o_segs = 0;
+    bool ok = true;
+    // the tile whose output products are still to be issued
+    int pend = -1, pend_ks = 0;
+    bool pend_first = false, pend_last = false;
+    auto issue_pv = [&] {
+      if (pend < 0) return true;
+      if (!warp_wait(kPFull + (pend & 1), (pend >> 1) & 1)) return false;
+      if (pend_first && o_segs > 0 && !warp_wait(kOFree, (o_segs - 1) & 1)) return false;
+      tc::fence_after_sync();
+      if (leader) {
+        const uint32_t st = (uint32_t)((pend & 1) * kStageB), pb = (uint32_t)((pend & 1) * S::p_bytes);
+#pragma unroll 1
+        for (int ks = 0; ks < pend_ks; ++ks) {
 #pragma unroll
-    for (int r = 0; r < kHG; ++r) o[r][0] = o[r][1] = 0.f;
-    const int end = min(seg.pos + 1, seg.k1 * kTile);
-    for (int tok0 = seg.k0 * kTile; tok0 < end; tok0 += kSub) {
-      __syncthreads();
-      if (tid < kSub) {
-        const int tok = tok0 + tid;
-        int64_t off = -1;
-        float sc = 0.f;
-        if (tok < end) {
-          const int blk = a.block_table[(size_t)seg.b * a.max_blocks + tok / a.block_size];
-          if (blk >= 0 && blk < a.num_blocks) {
-            off = (int64_t)blk * a.block_size + tok % a.block_size;
-            sc = page_scale(a.scales[blk]);
-          } else {
-            set_status(&hdr->status, MLA_DEV_BAD_BLOCK);
+          for (int j = 0; j < 4; ++j)
+            mma_f8(tmem + kOCol + (uint32_t)(j * 3 * NH), vdesc + ((st + j * kSlab + ks * 4096) >> 4),
+                   pdesc + ((pb + ks * 512) >> 4), kIdO, !(pend_first && ks == 0));
+        }
+        tc::commit(&bars[kEmpty + (pend & 1)]);
+        tc::commit(&bars[kPVDone + (pend & 1)]);
+        if (pend_last) tc::commit(&bars[kODone]);
+      }
+      __syncwarp();
+      if (pend_last) ++o_segs;
+      pend = -1;
+      return true;
+    };
+    while (ok && sw.next(seg)) {
+      const int end = seg_end(), n = seg_tiles(), qb = seg_i % QB;
+      // with one query buffer the next query comes late: do not wait for it
+      // with products at hand
+      if (QB == 1 && !issue_pv()) { ok = false; break; }
+      if (!warp_wait(kQReady + qb, (seg_i / QB) & 1)) { ok = false; break; }
+#pragma unroll 1
+      for (int t = 0; t < n; ++t, ++i) {
+        const int v = min(kTok, end - (seg.k0 * kTile + t * kTok)), slot = i & 1;
+        if (!warp_wait(kFull + slot, (i >> 1) & 1) || (i > 0 && !warp_wait(kSFree, (i - 1) & 1))) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        if (leader) {
+          const uint32_t st = (uint32_t)(slot * kStageB), q0 = (uint32_t)(qb * S::q_bytes);
+#pragma unroll
+          for (int kk = 0; kk < 16; ++kk)
+            mma_f8(tmem + kSCol, kdesc + ((st + (kk >> 2) * kSlab + (kk & 3) * 32) >> 4),
+                   qdesc + ((q0 + (kk >> 2) * S::q_slab + (kk & 3) * 32) >> 4), kIdS, kk > 0);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc::mma_bf16(tmem + kSCol + 2 * NH, kdesc + ((st + 4 * kSlab + kk * 32) >> 4),
+                         qdesc + ((q0 + S::q_rope + kk * 32) >> 4), kIdR, kk > 0);
+          tc::commit(&bars[kSFull]);
+          if (t == n - 1) tc::commit(&bars[kQFree + qb]);
+        }
+        __syncwarp();
+        if (!issue_pv()) { ok = false; break; }
+        pend = i;
+        pend_ks = (v + 31) / 32;
+        pend_first = t == 0;
+        pend_last = t == n - 1;
+      }
+      ++seg_i;
+    }
+    if (ok && !issue_pv()) ok = false;
+    if (!ok && leader) {
+      set_status(status, MLA_DEV_TIMEOUT);
+      *abort_flag = 1;
+    }
+    // every product issued so far must finish before TMEM is freed
+    if (leader) tc::commit(&bars[kFinal]);
+    __syncwarp();
+    if (!mbar_wait(&bars[kFinal], 0) && leader) set_status(status, MLA_DEV_TIMEOUT);
+    __syncwarp();
+  } else if (has_work && warp < kSoftWarp0) {
+    // ------------------------------------------------------- query terms
+    // TH threads of a warp share a head: 512 / TH latent columns each, and
+    // 64 / TH rope values
+    constexpr int TH = 64 / NH;
+    const int qt = tid - 64, h = qt / TH, part = qt % TH;
+    int seg_i = 0;
+    bool ok = true;
+    while (ok && sw.next(seg)) {
+      const int qb = seg_i % QB;
+      if (seg_i >= QB && !warp_wait(kQFree + qb, ((seg_i / QB) - 1) & 1)) { ok = false; break; }
+      uint8_t* dst = sm + S::q + qb * S::q_bytes;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          a.q_abs + ((size_t)seg.n * a.num_heads + seg.g * NH + h) * kRow);
+      constexpr int kVec = kDc / TH / 8;   // 16-byte loads of the latent part
+      // in rounds of 16 loads: the largest magnitude first, then the terms
+      // (the second time from L1)
+      float mx = 0.f;
+#pragma unroll
+      for (int r = 0; r < kVec / 16; ++r) {
+        uint4 x[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) x[k] = src[part * kVec + r * 16 + k];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float v0 = fabsf(__uint_as_float(u[e] << 16)), v1 = fabsf(__uint_as_float(u[e] & 0xffff0000u));
+            mx = fmaxf(mx, fmaxf(isinf(v0) ? 0.f : v0, isinf(v1) ? 0.f : v1));
           }
         }
-        sOff[tid] = off;
-        sS[tid] = sc;
       }
-      __syncthreads();
-      // 16 rows of 40 16-byte pieces: 32 of codes, 8 of rope values
-      for (int i = tid; i < kSub * 40; i += 256) {
-        const int r = i / 40, c = i % 40;
-        const int64_t off = sOff[r];
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (off >= 0) v = *reinterpret_cast<const uint4*>(a.cache8 + off * kRow8 + c * 16);
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-        float* d = sK + r * (kRow + 1);
-        if (c < 32) {
-          const float sc = sS[r];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            __nv_fp8_e4m3 code;
-            code.__x = (uint8_t)(u[k >> 2] >> (8 * (k & 3)));
-            d[c * 16 + k] = off >= 0 ? (float)code * sc : 0.f;
+      for (int o = 1; o < TH; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      // 2^e with mx 2^e in [2^7, 2^8); heads below 2^-112 as 2^-112
+      const int e = min(134 - (int)(__float_as_uint(mx) >> 23), 119);
+      const float f = __uint_as_float((uint32_t)(e + 127) << 23);
+#pragma unroll
+      for (int r = 0; r < kVec / 16; ++r) {
+        uint4 x[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) x[k] = src[part * kVec + r * 16 + k];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t u[8] = {x[2 * k].x, x[2 * k].y, x[2 * k].z, x[2 * k].w,
+                                 x[2 * k + 1].x, x[2 * k + 1].y, x[2 * k + 1].z, x[2 * k + 1].w};
+          uint4 t1, t2;
+          query_terms(u, f, t1, t2);
+          const int c16 = part * (kVec / 2) + r * 8 + k;  // 16-code piece of the row
+          uint8_t* slab = dst + (c16 >> 3) * S::q_slab;
+          *reinterpret_cast<uint4*>(slab + sw128(h, c16 & 7)) = t1;
+          *reinterpret_cast<uint4*>(slab + sw128(NH + h, c16 & 7)) = t2;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8 / TH; ++k) {
+        const int c = part * (8 / TH) + k;
+        *reinterpret_cast<uint4*>(dst + S::q_rope + sw128(h, c)) = src[kDc / 8 + c];
+      }
+      if (part == 0)
+        coef[qb * NH + h] = a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kQReady + qb]);
+      ++seg_i;
+    }
+    if (!ok && lane == 0) {
+      set_status(status, MLA_DEV_TIMEOUT);
+      *abort_flag = 1;
+    }
+  } else if (has_work) {
+    // ------------------------------------------------------------- softmax
+    const int st = tid - kSoftWarp0 * 32;               // 0-255
+    const int half = st >> 7, r = st & 127, w4 = (warp & 3);
+    const int h0 = half * HT;                           // first head of this thread
+    const uint32_t trow = tmem + ((uint32_t)(w4 * 32) << 16);
+    const int bar = kHalfBar + half;
+    float* red = reinterpret_cast<float*>(sm + S::red);
+    float* scratch = reinterpret_cast<float*>(sm + S::merge);
+    int* arrive = reinterpret_cast<int*>(a.ws + L.arrive);
+    int i = 0, seg_i = 0;
+    bool aborted = false;
+    while (!aborted && sw.next(seg)) {
+      const int n = seg_tiles(), qb = seg_i % QB;
+      const int64_t tile = (int64_t)seg.n * a.groups + seg.g;
+      float cq[HT], ref[HT], l[HT];
+      const bool okq = warp_wait(kQReady + qb, (seg_i / QB) & 1);
+#pragma unroll
+      for (int k = 0; k < HT; ++k) {
+        cq[k] = okq ? coef[qb * NH + h0 + k] : 0.f;
+        ref[k] = -INFINITY;
+        l[k] = 0.f;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kQFree + qb]);
+#pragma unroll 1
+      for (int t = 0; t < n; ++t, ++i) {
+        const int slot = i & 1;
+        // the scores, the stage's info, and the weights' buffer (tile i - 2)
+        bool fine = okq && wait_or_abort(&bars[kSFull], i & 1, abort_flag) &&
+                    wait_or_abort(&bars[kFull + slot], (i >> 1) & 1, abort_flag) &&
+                    (i < 2 || wait_or_abort(&bars[kPVDone + slot], ((i >> 1) - 1) & 1, abort_flag));
+        fine = __all_sync(0xffffffffu, fine);
+        float x[HT];
+        int v = 0;
+        float sc = 1.f;
+        bool live = false;
+        int ex = 0;
+        if (fine) {
+          tc::fence_after_sync();
+          float d1[HT], d2[HT], dr[HT];
+          tmem_ld(trow + kSCol + h0, d1);
+          tmem_ld(trow + kSCol + NH + h0, d2);
+          tmem_ld(trow + kSCol + 2 * NH + h0, dr);
+          v = info[slot];
+          sc = page_sc[slot * 8 + (r >> bs_shift)];
+          live = r < v && sc > 0.f;
+          if (!live) sc = 1.f;
+          // S = m 2^ex, m in [1, 2)
+          ex = (int)(__float_as_uint(sc) >> 23) - 127;
+          tc::wait_ld();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[kSFree]);
+#pragma unroll
+          for (int k = 0; k < HT; ++k) {
+            const float s = fmaf(fmaf(d2[k], 0.03125f, d1[k]) * sc, cq[k], dr[k] * a.scale_log2);
+            x[k] = live ? s : -INFINITY;
+          }
+          if (a.scores && live) {
+            const int64_t tok = (int64_t)seg.k0 * kTile + t * kTok + r;
+            const int64_t t16 = (int64_t)seg.n * (a.num_heads / kHG) + seg.g * (NH / kHG) + h0 / kHG;
+            float4* o = reinterpret_cast<float4*>(
+                a.scores + (t16 * a.max_blocks * bs + tok) * kHG + h0 % kHG);
+#pragma unroll
+            for (int k = 0; k < HT / 4; ++k)
+              o[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
           }
         } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            d[kDc + (c - 32) * 8 + k] = __uint_as_float((k & 1) ? u[k >> 1] & 0xffff0000u : u[k >> 1] << 16);
+          for (int k = 0; k < HT; ++k) x[k] = -INFINITY;
+        }
+        const float exf = (float)ex;
+        // does any weight outgrow its reference?
+        bool grow = !fine;
+#pragma unroll
+        for (int k = 0; k < HT; ++k) {
+          x[k] += exf;
+          grow |= x[k] > ref[k] + kGrowLog2;
+        }
+        if (bar_or(bar, 128, grow)) {
+#pragma unroll
+          for (int k = 0; k < HT; ++k) {
+            const float m = warp_max(x[k]);
+            if (lane == 0) red[(half * 4 + w4) * HT + k] = m;
+          }
+          // (the output products of tile i - 1 must have landed before O is rescaled)
+          if (t > 0 && fine)
+            fine = warp_wait(kPVDone + (slot ^ 1), ((i - 1) >> 1) & 1);
+          if (bar_or(bar, 128, !fine)) {
+            // (the other half meets this at the end of the segment or here)
+            bar_or(kSoftBar, kSoftThreads, true);
+            aborted = true;
+            break;
+          }
+          float f[HT];
+          bool any = false;
+#pragma unroll
+          for (int k = 0; k < HT; ++k) {
+            float m = ref[k];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) m = fmaxf(m, red[(half * 4 + u) * HT + k]);
+            f[k] = m == ref[k] ? 1.f : fast_exp2(ref[k] - m);   // (from -inf: 0)
+            any |= f[k] != 1.f;
+            ref[k] = m;
+            l[k] *= f[k];
+          }
+          if (t > 0 && any) {   // the same for every thread of the half
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int c = 0; c < 12; ++c) {
+              float o[HT];
+              const uint32_t at = trow + kOCol + (uint32_t)(c * NH + h0);
+              tmem_ld(at, o);
+              tc::wait_ld();
+#pragma unroll
+              for (int k = 0; k < HT; ++k) o[k] *= f[k];
+              tmem_st(at, o);
+            }
+            tc::wait_st();
+          }
+        }
+        // weights 2^(s - ref) S, as three e5m2 terms, and the sum of 2^(s - ref)
+        const float mant = __uint_as_float((__float_as_uint(sc) & 0x7fffffu) | 0x3f800000u);
+        const float inv_s = 1.f / sc;
+        uint32_t hp[HT / 2];
+#pragma unroll
+        for (int k = 0; k < HT; k += 2) {
+          const float b0 = ref[k] == -INFINITY ? 0.f : ref[k], b1 = ref[k + 1] == -INFINITY ? 0.f : ref[k + 1];
+          const float p0 = fast_exp2(x[k] - b0 + kRefLog2) * mant, p1 = fast_exp2(x[k + 1] - b1 + kRefLog2) * mant;
+          l[k] = fmaf(p0, inv_s, l[k]);
+          l[k + 1] = fmaf(p1, inv_s, l[k + 1]);
+          const __half2 hh = __floats2half2_rn(p0, p1);
+          hp[k / 2] = *reinterpret_cast<const uint32_t*>(&hh);
+        }
+        uint32_t tm[3][HT / 4];
+#pragma unroll
+        for (int k = 0; k < HT / 2; k += 2) {
+          // e5m2 is the upper byte of f16: cut the first two terms off, round the last
+          uint32_t a0 = hp[k], a1 = hp[k + 1];
+          tm[0][k / 2] = __byte_perm(a0, a1, 0x7531);
+#pragma unroll
+          for (int s = 1; s < 3; ++s) {
+            const uint32_t c0 = a0 & 0xff00ff00u, c1 = a1 & 0xff00ff00u;
+            const __half2 r0 = __hsub2(*reinterpret_cast<const __half2*>(&a0), *reinterpret_cast<const __half2*>(&c0));
+            const __half2 r1 = __hsub2(*reinterpret_cast<const __half2*>(&a1), *reinterpret_cast<const __half2*>(&c1));
+            a0 = *reinterpret_cast<const uint32_t*>(&r0);
+            a1 = *reinterpret_cast<const uint32_t*>(&r1);
+            if (s == 1) {
+              tm[1][k / 2] = __byte_perm(a0, a1, 0x7531);
+            } else {
+              uint16_t e0, e1;
+              asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(e0) : "r"(a0));
+              asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(e1) : "r"(a1));
+              tm[2][k / 2] = (uint32_t)e0 | ((uint32_t)e1 << 16);
+            }
+          }
+        }
+        uint8_t* pb = sm + S::p + slot * S::p_bytes + (r >> 3) * 128 + (r & 7) * 16;
+#pragma unroll
+        for (int s = 0; s < 3; ++s) {
+          if constexpr (NH == 16)
+            *reinterpret_cast<uint2*>(pb + s * 2048 + h0) = make_uint2(tm[s][0], tm[s][1]);
+          else
+            *reinterpret_cast<uint4*>(pb + (2 * s + half) * 2048) =
+                make_uint4(tm[s][0], tm[s][1], tm[s][2], tm[s][3]);
+        }
+        if (!live && r < ((v + 31) & ~31)) {
+          // a row that is not live may hold anything: zero its codes, so that a
+          // weight of 0 stays 0 (each half two slabs)
+          uint8_t* row = sm + S::stage + slot * kStageB + 2 * half * kSlab + r * 128;
+#pragma unroll 1
+          for (int c = 0; c < 16; ++c)
+            *reinterpret_cast<uint4*>(row + (c >> 3) * kSlab + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kPFull + slot]);
+      }
+      if (aborted) break;
+
+      // ---- the segment's sums, then its output rows
+#pragma unroll
+      for (int k = 0; k < HT; ++k) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], o);
+      }
+      const bool okd = warp_wait(kODone, seg_i & 1);
+      if (bar_or(kSoftBar, kSoftThreads, !okd)) { aborted = true; break; }
+      tc::fence_after_sync();
+#pragma unroll
+      for (int k = 0; k < HT; ++k)
+        if (lane == 0) red[(half * 4 + w4) * HT + k] = l[k];
+      named_bar_sync(bar, 128);
+      const int u_first = seg.ustart + seg.g * seg.tiles;
+      const int c_first = u_first / sw.share, c_last = (u_first + seg.tiles - 1) / sw.share;
+      const bool direct = a.fused && c_first == c_last;
+      const int64_t slot = (int64_t)blockIdx.x + tile;
+      const int s16 = h0 / kHG, hr = h0 % kHG;       // 16-head part of the group, head in it
+      float* o_row = a.o_lat + ((size_t)seg.n * a.num_heads + seg.g * NH) * kDc;
+      float* dst = (direct ? o_row + (size_t)h0 * kDc : a.o_part[s16] + ((size_t)slot * kHG + hr) * kDc) +
+                   w4 * 32 + lane;
+#pragma unroll
+      for (int k = 0; k < HT; ++k) {
+        l[k] = (red[half * 4 * HT + k] + red[(half * 4 + 1) * HT + k]) +
+               (red[(half * 4 + 2) * HT + k] + red[(half * 4 + 3) * HT + k]);
+        if (r == k) {
+          const float lse = l[k] == 0.f ? -INFINITY : ref[k] - kRefLog2 + log2f(l[k]);
+          if (direct)
+            a.lse[(size_t)seg.n * a.num_heads + seg.g * NH + h0 + k] = lse;
+          else
+            a.lse_part[s16][slot * kHG + hr + k] = lse;
+        }
+        l[k] = l[k] == 0.f ? 0.f : 1.f / l[k];       // (a NaN sum stays NaN)
+      }
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j) {
+        float o1[HT], o2[HT], o3[HT];
+        const uint32_t at = trow + kOCol + (uint32_t)(j * 3 * NH + h0);
+        tmem_ld(at, o1);
+        tmem_ld(at + NH, o2);
+        tmem_ld(at + 2 * NH, o3);
+        tc::wait_ld();
+#pragma unroll
+        for (int k = 0; k < HT; ++k) dst[(size_t)k * kDc + j * 128] = ((o1[k] + o2[k]) + o3[k]) * l[k];
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kOFree]);
+      if (a.fused && !direct) {
+        __threadfence();  // publish protocol: see count_arrival
+        named_bar_sync(kSoftBar, kSoftThreads);
+        if (st == 0) *merge_flag = count_arrival(&arrive[tile]) == c_last - c_first;
+        named_bar_sync(kSoftBar, kSoftThreads);
+        if (*merge_flag) {
+          const int parts = c_last - c_first + 1;
+          // merge_qtile leaves the maxima and the inverse weight sums in its scratch
+          if constexpr (NH == 16) {
+            merge_qtile<kSoftThreads>(a.lse_part[0], a.o_part[0], c_first + tile, parts, 1, o_row, st,
+                                      scratch, [] { named_bar_sync(kSoftBar, kSoftThreads); });
+            if (st < kHG) a.lse[tile * kHG + st] = merged_lse(scratch[st], scratch[kHG + st]);
+          } else {
+            float* mine = scratch + half * (S::merge_bytes / 4);
+            merge_qtile<128>(a.lse_part[half], a.o_part[half], c_first + tile, parts, 1,
+                             o_row + half * kHG * kDc, r, mine, [&] { named_bar_sync(bar, 128); });
+            if (r < kHG) a.lse[tile * NH + half * kHG + r] = merged_lse(mine[r], mine[kHG + r]);
+          }
+          if (st == 0) arrive[tile] = 0;  // every part has arrived: ready for the next launch
         }
       }
-      __syncthreads();
-      const int tok = tok0 + j;
-      const bool live = tok < end && sOff[j] >= 0;
-      float s0 = 0.f, s1 = 0.f;
-      for (int c = 0; c < kRow; c += 2) {
-        s0 = fmaf(sQ[h * kRow + c], sK[j * (kRow + 1) + c], s0);
-        s1 = fmaf(sQ[h * kRow + c + 1], sK[j * (kRow + 1) + c + 1], s1);
-      }
-      const float s = live ? (s0 + s1) * a.scale_log2 : -INFINITY;
-      if (a.scores && live)
-        a.scores[((size_t)t * a.max_blocks * a.block_size + tok) * kHG + h] = s;
-      float mx = s;
-#pragma unroll
-      for (int o2 = 8; o2 > 0; o2 >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o2));
-      const float mn = fmaxf(m, mx);
-      const float mu = mn == -INFINITY ? 0.f : mn;
-      const float alpha = fast_exp2(m - mu);
-      const float p = fast_exp2(s - mu);
-      float ps = p;
-#pragma unroll
-      for (int o2 = 8; o2 > 0; o2 >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o2);
-      l = l * alpha + ps;
-      m = mn;
-      sP[h * kSub + j] = p;
-      if (j == 0) sA[h] = alpha;
-      __syncthreads();
-#pragma unroll
-      for (int r = 0; r < kHG; ++r) {
-        const float al = sA[r];
-        float acc0 = o[r][0] * al, acc1 = o[r][1] * al;
-        for (int jj = 0; jj < kSub; ++jj) {
-          const float pj = sP[r * kSub + jj];
-          acc0 = fmaf(pj, sK[jj * (kRow + 1) + d0], acc0);
-          acc1 = fmaf(pj, sK[jj * (kRow + 1) + d0 + 1], acc1);
-        }
-        o[r][0] = acc0;
-        o[r][1] = acc1;
-      }
+      named_bar_sync(kSoftBar, kSoftThreads);  // red and the scratch may be written again
+      ++seg_i;
     }
-    __syncthreads();
-    if (j == 0) { sL[h] = l; sM[h] = m; }
-    __syncthreads();
-    const int u_first = seg.ustart + seg.g * seg.tiles;
-    const int c_first = u_first / sw.share, c_last = (u_first + seg.tiles - 1) / sw.share;
-    const bool direct = c_first == c_last;
-    float* o_tile = a.o_lat + ((size_t)seg.n * a.num_heads + seg.g * kHG) * kDc;
-    float* dst = direct ? o_tile : o_out + (size_t)slot * kHG * kDc;
-#pragma unroll
-    for (int r = 0; r < kHG; ++r) {
-      // (a NaN sum stays NaN)
-      const float lr = sL[r];
-      const float inv = lr == 0.f ? 0.f : 1.f / lr;
-      *reinterpret_cast<float2*>(dst + (size_t)r * kDc + d0) = make_float2(o[r][0] * inv, o[r][1] * inv);
-    }
-    if (tid < kHG) {
-      const float lr = sL[tid], lse = lr == 0.f ? -INFINITY : sM[tid] + log2f(lr);
-      if (direct)
-        a.lse[(size_t)t * kHG + tid] = lse;
-      else
-        lse_out[(size_t)slot * kHG + tid] = lse;
-    }
-    if (!direct) {
-      int* arrive = reinterpret_cast<int*>(a.ws + L.arrive);
-      __threadfence();  // publish protocol: see count_arrival
-      __syncthreads();
-      if (tid == 0) sFlag[0] = count_arrival(&arrive[t]) == c_last - c_first;
-      __syncthreads();
-      if (sFlag[0]) {
-        merge_qtile<256>(lse_out, o_out, (int64_t)c_first + t, c_last - c_first + 1, 1, o_tile, tid,
-                         sMerge, [] { __syncthreads(); });
-        // merge_qtile leaves the maxima and inverse weight sums in its scratch
-        if (tid < kHG) a.lse[(size_t)t * kHG + tid] = sMerge[tid] - log2f(sMerge[kHG + tid]);
-        if (tid == 0) arrive[t] = 0;  // every part has arrived: ready for the next launch
-      }
-      __syncthreads();
+    if (aborted && lane == 0) {
+      set_status(status, MLA_DEV_TIMEOUT);
+      *abort_flag = 1;
     }
   }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 1) tc::dealloc(tmem, kTmemCols);
+}
+
+// The merge of many parts of few (row, 16 heads) tiles, spread over the
+// device: CTA = (tile, 64 of the 512 columns), thread = (head, 4 columns).
+constexpr int kMergeCols = 64;
+__global__ void __launch_bounds__(256) page8_merge_kernel(P8Args a, int NH) {
+  __shared__ float sW[32][kHG];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int H16 = a.num_heads / kHG, sub = NH / kHG;
+  const int n = blockIdx.x / H16, t16 = blockIdx.x % H16, tid = threadIdx.x;
+  const int h = tid >> 4, c = blockIdx.y * kMergeCols + (tid & 15) * 4;
+  const QtileParts qp = locate_qtile(a.ws, a.num_q, a.groups, a.num_ctas, 0, n, t16 / sub);
+  const float* lse = a.lse_part[t16 % sub];
+  const float* part = a.o_part[t16 % sub];
+  // the largest log-sum-exp, then the weights
+  float m = -INFINITY;
+  for (int s = tid & 15; s < qp.count; s += 16) m = fmaxf(m, lse[(qp.first + s) * kHG + h]);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float den = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < qp.count; s0 += 32) {
+    const int ns = min(32, qp.count - s0);
+    __syncthreads();
+    for (int s = tid & 15; s < ns; s += 16) {
+      const float w = m == -INFINITY ? 0.f : fast_exp2(lse[(qp.first + s0 + s) * kHG + h] - m);
+      sW[s][h] = w;
+      den += w;
+    }
+    __syncthreads();
+#pragma unroll 8
+    for (int s = 0; s < ns; ++s) {
+      const float4 v = *reinterpret_cast<const float4*>(part + ((qp.first + s0 + s) * kHG + h) * kDc + c);
+      const float w = sW[s][h];
+      acc.x = fmaf(w, v.x, acc.x);
+      acc.y = fmaf(w, v.y, acc.y);
+      acc.z = fmaf(w, v.z, acc.z);
+      acc.w = fmaf(w, v.w, acc.w);
+    }
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  const size_t row = (size_t)n * a.num_heads + t16 * kHG + h;
+  *reinterpret_cast<float4*>(a.o_lat + row * kDc + c) =
+      make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  if (blockIdx.y == 0 && (tid & 15) == 0) a.lse[row] = den == 0.f ? -INFINITY : m + log2f(den);
 }
 
 // mass[slot(t)] = decay * mass[slot(t)] + sum over the sequence's rows and all
@@ -278,24 +915,51 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
   const size_t need = mla_page8_decode_workspace_size(cfg, num_q, batch, max_blocks, with_mass);
   if (need == 0) return MLA_ERR_UNSUPPORTED;
   if (ws_bytes < need) return MLA_ERR_WORKSPACE_TOO_SMALL;
-  const int C = split_ctas(cfg), H = cfg->num_heads, bs = cfg->block_size;
+  const int C = split_ctas(cfg), H = cfg->num_heads, bs = cfg->block_size, NH = group_heads(H);
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const P8Ws L = p8_ws(num_q, H, C, (int64_t)max_blocks * bs, with_mass);
-  const PlanArgs pa{seq_lens, query_start_loc, batch, (int32_t)num_q, H / kHG, C, bs, max_blocks,
+  const WsLayout W = ws_layout(num_q, H / NH, C);
+  // With num_blocks == 0 every block id is rejected before any copy; the maps
+  // still need an extent.
+  CUtensorMap codes_map, rope_map;
+  if (!encode_fp8_maps(&codes_map, &rope_map, cache8,
+                       (uint64_t)(num_blocks > 0 ? num_blocks : 1) * bs, (uint32_t)bs))
+    return MLA_ERR_CUDA;
+  const PlanArgs pa{seq_lens, query_start_loc, batch, (int32_t)num_q, H / NH, C, bs, max_blocks,
                     workspace};
   cudaError_t e = launch_plan(pa, st);
   if (e != cudaSuccess) return MLA_ERR_CUDA;
-  P8Args a{(const __nv_bfloat16*)q_abs, (const uint8_t*)cache8, page_scales, num_blocks,
-           block_table, max_blocks, bs, H, H / kHG, C, num_q,
-           (float)(cfg->softmax_scale * 1.4426950408889634), ws,
-           reinterpret_cast<float*>(ws + L.o_lat), reinterpret_cast<float*>(ws + L.lse),
-           with_mass ? reinterpret_cast<float*>(ws + L.scores) : nullptr};
-  const size_t smem =
-      (size_t)(kHG * kRow + kSub * (kRow + 1) + kHG * kSub + 3 * kHG + 2 * kHG + kMergeChunk * kHG + 2) * 4 +
-      kSub * 12;
-  e = cudaFuncSetAttribute(page8_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e == cudaSuccess) e = launch_pdl(page8_decode_kernel, dim3(C), dim3(256), smem, st, a);
+  P8Args a{};
+  a.q_abs = (const uint16_t*)q_abs;
+  a.scales = page_scales;
+  a.num_blocks = num_blocks;
+  a.block_table = block_table;
+  a.max_blocks = max_blocks;
+  a.block_size = bs;
+  a.num_heads = H;
+  a.groups = H / NH;
+  a.num_ctas = C;
+  a.num_q = num_q;
+  a.scale_log2 = (float)(cfg->softmax_scale * 1.4426950408889634);
+  a.ws = ws;
+  a.lse_part[0] = reinterpret_cast<float*>(ws + W.lse);
+  a.lse_part[1] = reinterpret_cast<float*>(ws + L.lse2);
+  a.o_part[0] = reinterpret_cast<float*>(ws + W.opart);
+  a.o_part[1] = reinterpret_cast<float*>(ws + L.opart2);
+  a.o_lat = reinterpret_cast<float*>(ws + L.o_lat);
+  a.lse = reinterpret_cast<float*>(ws + L.lse);
+  a.scores = with_mass ? reinterpret_cast<float*>(ws + L.scores) : nullptr;
+  // few tiles for many CTAs: each is cut into many parts, which one CTA would
+  // merge alone at the end; the merge kernel spreads them over the device
+  a.fused = num_q * (H / NH) * 4 >= C;
+  auto launch = [&](auto kernel, int smem) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return e != cudaSuccess ? e : launch_pdl(kernel, dim3(C), dim3(kThreads), smem, st, codes_map, rope_map, a);
+  };
+  e = NH == 16 ? launch(page8_decode_kernel<16>, Sm<16>::alloc) : launch(page8_decode_kernel<32>, Sm<32>::alloc);
+  if (e == cudaSuccess && !a.fused)
+    e = launch_pdl(page8_merge_kernel, dim3((unsigned)(num_q * (H / kHG)), kDc / kMergeCols), dim3(256), 0, st, a, NH);
   if (e != cudaSuccess) return MLA_ERR_CUDA;
   if (with_mass) {
     const MassArgs ma{a.scores, a.lse, seq_lens, query_start_loc, block_table, max_blocks, bs,
