@@ -20,23 +20,25 @@
 //     2^-23 of that largest;
 //   output  O[512, 3 NH] = codes[128, 512]^T . (p_1 | p_2 | p_3)
 //     p = p_1 + p_2 + p_3 in e5m2: 9 significant bits (error 2^-10), down to
-//     2^-27 of the running reference, so a long tail of small weights behind a
+//     2^-24 of the running reference, so a long tail of small weights behind a
 //     large one is not lost.
 // The page's scale enters a score as a factor of its token (a row), and the
 // output as part of the weight: the columns hold 2^(s_t - ref) S_p, and the
 // softmax sum adds the same number divided by S_p again. The running reference
 // of a head follows s_t + log2 S_p, and O is rescaled in TMEM only when it is
-// outgrown by more than 2^3.
+// outgrown by more than 2^6.
 //
 // NH = 16 or 32 heads of one row make a column group. The work is cut as in
 // the other decodes (units of one row, one group and 64 tokens in equal
 // contiguous shares, one CTA a share). Per CTA (384 threads):
 //   warp 0      copies: 128 tokens a stage (4 slabs of 128 codes, one of rope
 //               values), two stages, SWIZZLE_128B; block ids are checked;
-//   warp 1      issues every MMA from one lane: scores of tile i, then the
-//               output of tile i - 1, so the softmax of a tile has two products
-//               to hide behind; owns the TMEM;
-//   warps 2-3   split the query of the next segment into its terms;
+//   warp 1      issues the output products of a tile as soon as its weights are
+//               stored (one lane); owns the TMEM;
+//   warp 2      issues the scores of a tile as soon as it has landed and the
+//               score columns are read;
+//   warp 3      copies the next segment's query terms, which a kernel before
+//               this one has split and laid out as the operand;
 //   warps 4-11  softmax: thread r of each half owns token r and half of the
 //               heads. Token rows that are not live are zeroed in the stage,
 //               so a weight of 0 never meets a NaN code.
@@ -62,8 +64,8 @@ constexpr int kStageB = 5 * kSlab;            // four slabs of codes, one of rop
 constexpr int kThreads = 384;
 constexpr int kSoftWarp0 = 4, kSoftThreads = 256;
 constexpr int kSoftBar = 1, kHalfBar = 2;     // named barriers: all softmax warps; one half (2, 3)
-constexpr float kRefLog2 = 11.f;              // a weight equal to the reference is held as 2^11
-constexpr float kGrowLog2 = 3.f;              // the reference follows when outgrown by 2^3
+constexpr float kRefLog2 = 8.f;               // a weight equal to the reference is held as 2^8
+constexpr float kGrowLog2 = 6.f;              // the reference follows when outgrown by 2^6
 constexpr uint32_t kTmemCols = 512, kSCol = 0, kOCol = 128;
 
 struct P8Args {
@@ -79,6 +81,12 @@ struct P8Args {
   int64_t num_q;
   float scale_log2;
   uint8_t* ws;
+  uint8_t* q8;         // [num_q, groups] query terms as shared memory holds them
+  float* coef;         // [num_q, H] score factors
+  const int32_t* seq_lens;
+  const int32_t* query_start_loc;
+  int32_t batch;
+  int32_t self_plan;   // the kernel derives the split itself
   float* lse_part[2];  // [slots][16] of each 16 heads of a group
   float* o_part[2];    // [slots][16][512]
   float* o_lat;        // [num_q, H, 512]
@@ -88,10 +96,10 @@ struct P8Args {
 };
 
 // The decode workspace: the split plan and the partials of ws_layout, the
-// partials of a group's second 16 heads, the merged latents, their
-// log-sum-exps and (with mass) the scores.
+// partials of a group's second 16 heads, the query terms and score factors,
+// the merged latents, their log-sum-exps and (with mass) the scores.
 struct P8Ws {
-  size_t lse2, opart2, o_lat, lse, scores, total;
+  size_t lse2, opart2, q8, coef, o_lat, lse, scores, total;
 };
 int group_heads(int H) { return H >= 32 ? 32 : 16; }
 P8Ws p8_ws(int64_t num_q, int H, int num_ctas, int64_t max_tokens, bool mass) {
@@ -100,7 +108,9 @@ P8Ws p8_ws(int64_t num_q, int H, int num_ctas, int64_t max_tokens, bool mass) {
   P8Ws L;
   L.lse2 = align_up(W.total, 256);
   L.opart2 = NH == 32 ? align_up(L.lse2 + (size_t)W.slots * kHG * 4, 256) : L.lse2;
-  L.o_lat = NH == 32 ? align_up(L.opart2 + (size_t)W.slots * kHG * kDc * 4, 256) : L.lse2;
+  L.q8 = NH == 32 ? align_up(L.opart2 + (size_t)W.slots * kHG * kDc * 4, 256) : L.lse2;
+  L.coef = align_up(L.q8 + (size_t)num_q * H * (2 * kDc + 2 * kDr), 256);
+  L.o_lat = align_up(L.coef + (size_t)num_q * H * 4, 256);
   L.lse = align_up(L.o_lat + (size_t)num_q * H * kDc * 4, 256);
   L.scores = align_up(L.lse + (size_t)num_q * H * 4, 256);
   L.total = mass ? align_up(L.scores + (size_t)num_q * H * max_tokens * 4, 256) : L.scores;
@@ -124,19 +134,21 @@ struct Sm {
   static constexpr int merge_bytes = (2 * kHG + kMergeChunk * kHG) * 4;
   static constexpr int info = merge + 2 * merge_bytes;  // [2] live rows of a stage
   static constexpr int scale = info + 16;               // [2][8] page scales of a stage, -1: no page
-  static constexpr int bars = scale + 64;
+  static constexpr int self_rows = NH == 16 ? kSelfMaxRows : 128;  // rows of a self-planned launch
+  static constexpr int rows = scale + 64;               // [self_rows] int4
+  static constexpr int bars = rows + self_rows * 16;
   static constexpr int misc = bars + 24 * 8;            // TMEM base, abort flag, merge flag
   static constexpr int bytes = misc + 16;
   static constexpr int alloc = bytes + 1024;
   static_assert(alloc <= 227 * 1024, "shared memory budget");
   static_assert(q % 1024 == 0 && q_rope % 1024 == 0 && q_bytes % 1024 == 0 && p % 128 == 0, "swizzle atoms");
-  static_assert(bars % 8 == 0 && merge % 16 == 0, "alignment");
+  static_assert(bars % 8 == 0 && merge % 16 == 0 && coef % 16 == 0 && rows % 16 == 0, "alignment");
 };
 
 enum {
   kFull = 0,      // [2] stage landed
   kEmpty = 2,     // [2] stage's products done
-  kQReady = 4,    // [2] query terms stored (2 arrivals)
+  kQReady = 4,    // [2] query terms landed
   kQFree = 6,     // [2] the segment's score products done, its factors read (1 + 8 arrivals)
   kSFull = 8,     // scores in TMEM
   kSFree = 9,     // scores read (8 arrivals)
@@ -144,8 +156,9 @@ enum {
   kPVDone = 12,   // [2] output products done
   kODone = 14,    // the segment's output products done
   kOFree = 15,    // the output read (8 arrivals)
-  kFinal = 16,    // every product done
-  kNumBars = 17
+  kFinalS = 16,   // every score product done
+  kFinalO = 17,   // every output product done
+  kNumBars = 18
 };
 
 // Instruction descriptor, kind::f8f6f4, fp32 accumulator: A e4m3, B e4m3 (0) or
@@ -263,6 +276,64 @@ __device__ __forceinline__ void query_terms(const uint32_t* u, float f, uint4& t
   t2 = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
+// The query of one (row, column group) as the decode's operand: for each head
+// its two e4m3 terms (rows h and NH + h of four 128-byte slabs) and its bf16
+// rope values, swizzled as shared memory holds them, and the factor that
+// undoes the head's scale. 8 threads a head, 64 latent columns each.
+template <int NH>
+__global__ void __launch_bounds__(NH * 8) page8_query_kernel(const uint16_t* q_abs, int64_t num_q,
+                                                             int groups, float scale_log2,
+                                                             uint8_t* q8, float* coef) {
+  using S = Sm<NH>;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int h = threadIdx.x >> 3, part = threadIdx.x & 7;
+  const size_t row = (size_t)blockIdx.x * NH + h;   // (row n, head) in order
+  const uint4* src = reinterpret_cast<const uint4*>(q_abs + row * kRow);
+  uint8_t* dst = q8 + (size_t)blockIdx.x * S::q_bytes;
+  uint4 x[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) x[k] = src[part * 8 + k];
+  const uint4 rope = src[kDc / 8 + part];
+  float mx = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float v0 = fabsf(__uint_as_float(u[e] << 16)), v1 = fabsf(__uint_as_float(u[e] & 0xffff0000u));
+      mx = fmaxf(mx, fmaxf(isinf(v0) ? 0.f : v0, isinf(v1) ? 0.f : v1));
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  // 2^e with mx 2^e in [2^7, 2^8); heads below 2^-112 as 2^-112
+  const int e = min(134 - (int)(__float_as_uint(mx) >> 23), 119);
+  const float f = __uint_as_float((uint32_t)(e + 127) << 23);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t u[8] = {x[2 * k].x, x[2 * k].y, x[2 * k].z, x[2 * k].w,
+                           x[2 * k + 1].x, x[2 * k + 1].y, x[2 * k + 1].z, x[2 * k + 1].w};
+    uint4 t1, t2;
+    query_terms(u, f, t1, t2);
+    const int c16 = part * 4 + k;  // 16-code piece of the row
+    uint8_t* slab = dst + (c16 >> 3) * S::q_slab;
+    *reinterpret_cast<uint4*>(slab + sw128(h, c16 & 7)) = t1;
+    *reinterpret_cast<uint4*>(slab + sw128(NH + h, c16 & 7)) = t2;
+  }
+  *reinterpret_cast<uint4*>(dst + S::q_rope + sw128(h, part)) = rope;
+  if (part == 0) coef[row] = scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
+}
+
+// Untiled copy of `bytes` (a multiple of 16) to shared memory.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
 template <int NH>
 __global__ void __launch_bounds__(kThreads, 1)
     page8_decode_kernel(const __grid_constant__ CUtensorMap codes_map,
@@ -289,7 +360,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       const int n = (i == kSFree || i == kPFull || i == kPFull + 1 || i == kOFree) ? kSoftThreads / 32
-                    : (i == kQReady || i == kQReady + 1) ? 2
                     : (i == kQFree || i == kQFree + 1)   ? 1 + kSoftThreads / 32
                                                          : 1;
       mbar_init(&bars[i], n);
@@ -304,14 +374,47 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  pdl_wait();  // the plan and q_abs come from earlier kernels
-  pdl_launch_dependents();
-
+  // The kernel before this one is page8_query_kernel, which starts when
+  // everything before it has finished. So what the caller gave (lengths, pages,
+  // scales) may be read now; the query terms, the workspace and the output
+  // have to wait.
   SchedWalker sw;
-  const bool has_work = sw.init(a.ws, a.num_q, a.groups, a.num_ctas, blockIdx.x);
-  if (a.fused && warp >= kSoftWarp0)
-    zero_unvisited_rows(sw.row_info, sw.plan_ok, a.num_q, a.num_heads, a.o_lat,
-                        tid - kSoftWarp0 * 32, kSoftThreads);
+  bool has_work;
+  int total = 0;
+  if (a.self_plan) {
+    int4* rows = reinterpret_cast<int4*>(sm + S::rows);
+    total = self_plan<kThreads>(a.seq_lens, a.query_start_loc, a.batch, (int)a.num_q, a.groups,
+                                (int64_t)a.max_blocks * bs, rows, reinterpret_cast<int*>(sm + S::red),
+                                status, tid);
+    has_work = sw.init_rows(rows, (int)a.num_q, a.groups, total, a.num_ctas, blockIdx.x);
+  } else {
+    pdl_wait();
+    has_work = sw.init(a.ws, a.num_q, a.groups, a.num_ctas, blockIdx.x);
+  }
+  pdl_launch_dependents();
+  if (warp >= kSoftWarp0) {
+    pdl_wait();
+    const int st = tid - kSoftWarp0 * 32;
+    if (a.self_plan && blockIdx.x == 0) {
+      // the plan, for the merge kernel
+      int4* row_info = reinterpret_cast<int4*>(a.ws + L.row_info);
+      for (int n = st; n < (int)a.num_q; n += kSoftThreads) row_info[n] = sw.row_info[n];
+      if (st == 0) {
+        WsHeader* hdr = reinterpret_cast<WsHeader*>(a.ws);
+        hdr->magic = kMagic;
+        hdr->mode = 0;
+        hdr->qblocks = 0;
+        hdr->total_units = total;
+        hdr->share = sw.share;
+        hdr->num_ctas = a.num_ctas;
+        hdr->groups = a.groups;
+        hdr->num_q = (int32_t)a.num_q;
+        hdr->batch = a.batch;
+      }
+    }
+    if (a.fused)
+      zero_unvisited_rows(sw.row_info, sw.plan_ok, a.num_q, a.num_heads, a.o_lat, st, kSoftThreads);
+  }
   Segment seg{};
   // tokens of the segment: [k0 * 64, end), in tiles of 128
   auto seg_end = [&] { return min(seg.pos + 1, seg.k1 * kTile); };
@@ -385,54 +488,67 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (has_work && warp == 1) {
-    // ------------------------------------------------------------ products
-    constexpr uint32_t kIdS = idesc_f8(2 * NH, 0, false, false);
-    constexpr uint32_t kIdR = tc::idesc_bf16(kTok, NH, false, false);
+    // ----------------------------------------------------- output products
     constexpr uint32_t kIdO = idesc_f8(3 * NH, 1, true, true);
-    const uint64_t kdesc = tc::smem_desc(smem_u32(sm + S::stage), 16, 1024, tc::kSwizzle128);
     const uint64_t vdesc = tc::smem_desc(smem_u32(sm + S::stage), kSlab, 1024, tc::kSwizzle128);
-    const uint64_t qdesc = tc::smem_desc(smem_u32(sm + S::q), 16, 1024, tc::kSwizzle128);
     // weights: 16-byte cores of 16 columns, 8 tokens of a core group 128 bytes
     // (leading), blocks of 16 columns 2,048 bytes apart (stride), no swizzle
     const uint64_t pdesc = tc::smem_desc(smem_u32(sm + S::p), 128, 2048, 0);
     const bool leader = tc::elect_one();
-    int i = 0, seg_i = 0, o_segs = 0;
+    int i = 0, seg_i = 0;
     bool ok = true;
-    // the tile whose output products are still to be issued
-    int pend = -1, pend_ks = 0;
-    bool pend_first = false, pend_last = false;
-    auto issue_pv = [&] {
-      if (pend < 0) return true;
-      if (!warp_wait(kPFull + (pend & 1), (pend >> 1) & 1)) return false;
-      if (pend_first && o_segs > 0 && !warp_wait(kOFree, (o_segs - 1) & 1)) return false;
-      tc::fence_after_sync();
-      if (leader) {
-        const uint32_t st = (uint32_t)((pend & 1) * kStageB), pb = (uint32_t)((pend & 1) * S::p_bytes);
-#pragma unroll 1
-        for (int ks = 0; ks < pend_ks; ++ks) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_f8(tmem + kOCol + (uint32_t)(j * 3 * NH), vdesc + ((st + j * kSlab + ks * 4096) >> 4),
-                   pdesc + ((pb + ks * 512) >> 4), kIdO, !(pend_first && ks == 0));
-        }
-        tc::commit(&bars[kEmpty + (pend & 1)]);
-        tc::commit(&bars[kPVDone + (pend & 1)]);
-        if (pend_last) tc::commit(&bars[kODone]);
-      }
-      __syncwarp();
-      if (pend_last) ++o_segs;
-      pend = -1;
-      return true;
-    };
     while (ok && sw.next(seg)) {
-      const int end = seg_end(), n = seg_tiles(), qb = seg_i % QB;
-      // with one query buffer the next query comes late: do not wait for it
-      // with products at hand
-      if (QB == 1 && !issue_pv()) { ok = false; break; }
+      const int end = seg_end(), n = seg_tiles();
+#pragma unroll 1
+      for (int t = 0; t < n; ++t, ++i) {
+        const int nks = (min(kTok, end - (seg.k0 * kTile + t * kTok)) + 31) / 32, slot = i & 1;
+        if (!warp_wait(kPFull + slot, (i >> 1) & 1) ||
+            (t == 0 && seg_i > 0 && !warp_wait(kOFree, (seg_i - 1) & 1))) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        if (leader) {
+          const uint32_t st = (uint32_t)(slot * kStageB), pb = (uint32_t)(slot * S::p_bytes);
+#pragma unroll 1
+          for (int ks = 0; ks < nks; ++ks) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma_f8(tmem + kOCol + (uint32_t)(j * 3 * NH), vdesc + ((st + j * kSlab + ks * 4096) >> 4),
+                     pdesc + ((pb + ks * 512) >> 4), kIdO, t > 0 || ks > 0);
+          }
+          tc::commit(&bars[kEmpty + slot]);
+          tc::commit(&bars[kPVDone + slot]);
+          if (t == n - 1) tc::commit(&bars[kODone]);
+        }
+        __syncwarp();
+      }
+      ++seg_i;
+    }
+    if (!ok && leader) {
+      set_status(status, MLA_DEV_TIMEOUT);
+      *abort_flag = 1;
+    }
+    // every product issued so far must finish before TMEM is freed
+    if (leader) tc::commit(&bars[kFinalO]);
+    __syncwarp();
+    if (!mbar_wait(&bars[kFinalO], 0) && leader) set_status(status, MLA_DEV_TIMEOUT);
+    __syncwarp();
+  } else if (has_work && warp == 2) {
+    // -------------------------------------------------------------- scores
+    constexpr uint32_t kIdS = idesc_f8(2 * NH, 0, false, false);
+    constexpr uint32_t kIdR = tc::idesc_bf16(kTok, NH, false, false);
+    const uint64_t kdesc = tc::smem_desc(smem_u32(sm + S::stage), 16, 1024, tc::kSwizzle128);
+    const uint64_t qdesc = tc::smem_desc(smem_u32(sm + S::q), 16, 1024, tc::kSwizzle128);
+    const bool leader = tc::elect_one();
+    int i = 0, seg_i = 0;
+    bool ok = true;
+    while (ok && sw.next(seg)) {
+      const int n = seg_tiles(), qb = seg_i % QB;
       if (!warp_wait(kQReady + qb, (seg_i / QB) & 1)) { ok = false; break; }
 #pragma unroll 1
       for (int t = 0; t < n; ++t, ++i) {
-        const int v = min(kTok, end - (seg.k0 * kTile + t * kTok)), slot = i & 1;
+        const int slot = i & 1;
         if (!warp_wait(kFull + slot, (i >> 1) & 1) || (i > 0 && !warp_wait(kSFree, (i - 1) & 1))) {
           ok = false;
           break;
@@ -452,95 +568,47 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (t == n - 1) tc::commit(&bars[kQFree + qb]);
         }
         __syncwarp();
-        if (!issue_pv()) { ok = false; break; }
-        pend = i;
-        pend_ks = (v + 31) / 32;
-        pend_first = t == 0;
-        pend_last = t == n - 1;
       }
       ++seg_i;
     }
-    if (ok && !issue_pv()) ok = false;
     if (!ok && leader) {
       set_status(status, MLA_DEV_TIMEOUT);
       *abort_flag = 1;
     }
-    // every product issued so far must finish before TMEM is freed
-    if (leader) tc::commit(&bars[kFinal]);
+    if (leader) tc::commit(&bars[kFinalS]);
     __syncwarp();
-    if (!mbar_wait(&bars[kFinal], 0) && leader) set_status(status, MLA_DEV_TIMEOUT);
+    if (!mbar_wait(&bars[kFinalS], 0) && leader) set_status(status, MLA_DEV_TIMEOUT);
     __syncwarp();
-  } else if (has_work && warp < kSoftWarp0) {
-    // ------------------------------------------------------- query terms
-    // TH threads of a warp share a head: 512 / TH latent columns each, and
-    // 64 / TH rope values
-    constexpr int TH = 64 / NH;
-    const int qt = tid - 64, h = qt / TH, part = qt % TH;
+  } else if (has_work && warp == 3) {
+    // --------------------------------------------------------- query copies
+    pdl_wait();
     int seg_i = 0;
     bool ok = true;
     while (ok && sw.next(seg)) {
       const int qb = seg_i % QB;
       if (seg_i >= QB && !warp_wait(kQFree + qb, ((seg_i / QB) - 1) & 1)) { ok = false; break; }
-      uint8_t* dst = sm + S::q + qb * S::q_bytes;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          a.q_abs + ((size_t)seg.n * a.num_heads + seg.g * NH + h) * kRow);
-      constexpr int kVec = kDc / TH / 8;   // 16-byte loads of the latent part
-      // in rounds of 16 loads: the largest magnitude first, then the terms
-      // (the second time from L1)
-      float mx = 0.f;
-#pragma unroll
-      for (int r = 0; r < kVec / 16; ++r) {
-        uint4 x[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) x[k] = src[part * kVec + r * 16 + k];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float v0 = fabsf(__uint_as_float(u[e] << 16)), v1 = fabsf(__uint_as_float(u[e] & 0xffff0000u));
-            mx = fmaxf(mx, fmaxf(isinf(v0) ? 0.f : v0, isinf(v1) ? 0.f : v1));
-          }
-        }
+      if (lane == 0) {
+        const int64_t tile = (int64_t)seg.n * a.groups + seg.g;
+        mbar_arrive_expect_tx(&bars[kQReady + qb], S::q_bytes + NH * 4);
+        bulk_load(sm + S::q + qb * S::q_bytes, a.q8 + tile * S::q_bytes, S::q_bytes, &bars[kQReady + qb]);
+        bulk_load(coef + qb * NH, a.coef + tile * NH, NH * 4, &bars[kQReady + qb]);
       }
-#pragma unroll
-      for (int o = 1; o < TH; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      // 2^e with mx 2^e in [2^7, 2^8); heads below 2^-112 as 2^-112
-      const int e = min(134 - (int)(__float_as_uint(mx) >> 23), 119);
-      const float f = __uint_as_float((uint32_t)(e + 127) << 23);
-#pragma unroll
-      for (int r = 0; r < kVec / 16; ++r) {
-        uint4 x[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) x[k] = src[part * kVec + r * 16 + k];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t u[8] = {x[2 * k].x, x[2 * k].y, x[2 * k].z, x[2 * k].w,
-                                 x[2 * k + 1].x, x[2 * k + 1].y, x[2 * k + 1].z, x[2 * k + 1].w};
-          uint4 t1, t2;
-          query_terms(u, f, t1, t2);
-          const int c16 = part * (kVec / 2) + r * 8 + k;  // 16-code piece of the row
-          uint8_t* slab = dst + (c16 >> 3) * S::q_slab;
-          *reinterpret_cast<uint4*>(slab + sw128(h, c16 & 7)) = t1;
-          *reinterpret_cast<uint4*>(slab + sw128(NH + h, c16 & 7)) = t2;
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 8 / TH; ++k) {
-        const int c = part * (8 / TH) + k;
-        *reinterpret_cast<uint4*>(dst + S::q_rope + sw128(h, c)) = src[kDc / 8 + c];
-      }
-      if (part == 0)
-        coef[qb * NH + h] = a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
-      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kQReady + qb]);
       ++seg_i;
     }
-    if (!ok && lane == 0) {
-      set_status(status, MLA_DEV_TIMEOUT);
-      *abort_flag = 1;
+    if (lane == 0) {
+      if (!ok) {
+        set_status(status, MLA_DEV_TIMEOUT);
+        *abort_flag = 1;
+      }
+      // never leave with copies in flight
+      for (int qb = 0; qb < QB; ++qb) {
+        const int fills = seg_i > qb ? (seg_i - 1 - qb) / QB + 1 : 0;
+        if (fills > 0 && !mbar_wait(&bars[kQReady + qb], (fills - 1) & 1))
+          set_status(status, MLA_DEV_TIMEOUT);
+      }
     }
+    __syncwarp();
   } else if (has_work) {
     // ------------------------------------------------------------- softmax
     const int st = tid - kSoftWarp0 * 32;               // 0-255
@@ -926,10 +994,6 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
   if (!encode_fp8_maps(&codes_map, &rope_map, cache8,
                        (uint64_t)(num_blocks > 0 ? num_blocks : 1) * bs, (uint32_t)bs))
     return MLA_ERR_CUDA;
-  const PlanArgs pa{seq_lens, query_start_loc, batch, (int32_t)num_q, H / NH, C, bs, max_blocks,
-                    workspace};
-  cudaError_t e = launch_plan(pa, st);
-  if (e != cudaSuccess) return MLA_ERR_CUDA;
   P8Args a{};
   a.q_abs = (const uint16_t*)q_abs;
   a.scales = page_scales;
@@ -943,6 +1007,12 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
   a.num_q = num_q;
   a.scale_log2 = (float)(cfg->softmax_scale * 1.4426950408889634);
   a.ws = ws;
+  a.q8 = ws + L.q8;
+  a.coef = reinterpret_cast<float*>(ws + L.coef);
+  a.seq_lens = seq_lens;
+  a.query_start_loc = query_start_loc;
+  a.batch = batch;
+  a.self_plan = num_q <= (NH == 16 ? Sm<16>::self_rows : Sm<32>::self_rows);
   a.lse_part[0] = reinterpret_cast<float*>(ws + W.lse);
   a.lse_part[1] = reinterpret_cast<float*>(ws + L.lse2);
   a.o_part[0] = reinterpret_cast<float*>(ws + W.opart);
@@ -953,9 +1023,22 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
   // few tiles for many CTAs: each is cut into many parts, which one CTA would
   // merge alone at the end; the merge kernel spreads them over the device
   a.fused = num_q * (H / NH) * 4 >= C;
+  cudaError_t e = cudaSuccess;
+  if (!a.self_plan)
+    e = launch_plan(PlanArgs{seq_lens, query_start_loc, batch, (int32_t)num_q, H / NH, C, bs,
+                             max_blocks, workspace},
+                    st);
+  if (e == cudaSuccess) {
+    const dim3 grid((unsigned)(num_q * (H / NH)));
+    e = NH == 16 ? launch_pdl(page8_query_kernel<16>, grid, dim3(128), 0, st, a.q_abs, num_q,
+                              a.groups, a.scale_log2, a.q8, a.coef)
+                 : launch_pdl(page8_query_kernel<32>, grid, dim3(256), 0, st, a.q_abs, num_q,
+                              a.groups, a.scale_log2, a.q8, a.coef);
+  }
+  if (e != cudaSuccess) return MLA_ERR_CUDA;
   auto launch = [&](auto kernel, int smem) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    return e != cudaSuccess ? e : launch_pdl(kernel, dim3(C), dim3(kThreads), smem, st, codes_map, rope_map, a);
+    const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return r != cudaSuccess ? r : launch_pdl(kernel, dim3(C), dim3(kThreads), smem, st, codes_map, rope_map, a);
   };
   e = NH == 16 ? launch(page8_decode_kernel<16>, Sm<16>::alloc) : launch(page8_decode_kernel<32>, Sm<32>::alloc);
   if (e == cudaSuccess && !a.fused)
