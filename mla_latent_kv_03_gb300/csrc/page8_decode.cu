@@ -92,7 +92,7 @@ struct P8Args {
   float* o_lat;        // [num_q, H, 512]
   float* lse;          // [num_q, H], base 2
   float* scores;       // [num_q, H / 16, max tokens, 16], base 2; NULL without mass
-  int32_t fused;       // merge the splits here
+  int32_t fused;       // merge the splits in the decode kernel
 };
 
 // The decode workspace: the split plan and the partials of ws_layout, the
@@ -451,16 +451,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int src = (b0 - base + lane) & 31;
         const int my_id = __shfl_sync(0xffffffffu, id, src);
-        const float my_sc = __shfl_sync(0xffffffffu, sc, src);
         const bool mine = lane < pages && my_id >= 0;
-        if (lane < 8) page_sc[slot * 8 + lane] = mine ? my_sc : -1.f;
         const uint32_t okmask = __ballot_sync(0xffffffffu, mine);
-        if (lane == 0) {
-          if (__popc(okmask) != pages) set_status(status, MLA_DEV_BAD_BLOCK);
-          info[slot] = v;
-          mbar_arrive_expect_tx(&bars[kFull + slot], (uint32_t)(__popc(okmask) * 5 * bs * 128));
-        }
-        __syncwarp();
         // lanes 0-4 each copy one slab of every page
         uint8_t* dst = sm + S::stage + slot * kStageB + (lane < 5 ? lane : 0) * kSlab;
         for (int p = 0; p < pages; ++p) {
@@ -470,6 +462,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_2d_hint(dst + (p << bs_shift) * 128, &codes_map, 128 * lane, y, &bars[kFull + slot], policy);
           else if (lane == 4)
             tma_load_2d_hint(dst + (p << bs_shift) * 128, &rope_map, kDc / 2, y, &bars[kFull + slot], policy);
+        }
+        // the scales, whose loads the copies did not wait for; the barrier's
+        // one arrival comes last
+        const float my_sc = __shfl_sync(0xffffffffu, sc, src);
+        if (lane < 8) page_sc[slot * 8 + lane] = mine ? my_sc : -1.f;
+        __syncwarp();
+        if (lane == 0) {
+          if (__popc(okmask) != pages) set_status(status, MLA_DEV_BAD_BLOCK);
+          info[slot] = v;
+          mbar_arrive_expect_tx(&bars[kFull + slot], (uint32_t)(__popc(okmask) * 5 * bs * 128));
         }
         __syncwarp();
       }
@@ -874,52 +876,187 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tc::dealloc(tmem, kTmemCols);
 }
 
-// The merge of many parts of few (row, 16 heads) tiles, spread over the
-// device: CTA = (tile, 64 of the 512 columns), thread = (head, 4 columns).
-constexpr int kMergeCols = 64;
-__global__ void __launch_bounds__(256) page8_merge_kernel(P8Args a, int NH) {
-  __shared__ float sW[32][kHG];
+// The parts of (row n, head h): 16-row groups first, first + 1, ... of its
+// half's partials.
+struct HeadParts {
+  const float* lse;   // of the head, kHG apart
+  const float* o;     // [512] of the head, kHG * 512 apart
+  int count;
+};
+__device__ __forceinline__ HeadParts head_parts(const P8Args& a, int NH, int n, int h) {
+  const QtileParts qp = locate_qtile(a.ws, a.num_q, a.groups, a.num_ctas, 0, n, h / NH);
+  const int sub = (h % NH) / kHG, hr = h % kHG;
+  return {a.lse_part[sub] + qp.first * kHG + hr, a.o_part[sub] + (qp.first * kHG + hr) * kDc, qp.count};
+}
+// 2^lse sums: the largest log-sum-exp m, and den = sum of 2^(lse - m), by a
+// group of G neighbouring lanes.
+template <int G>
+__device__ __forceinline__ void merge_weights(const HeadParts& hp, int lane_in_group, float& m, float& den) {
+  m = -INFINITY;
+  for (int s = lane_in_group; s < hp.count; s += G) m = fmaxf(m, hp.lse[s * kHG]);
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  den = 0.f;
+  if (m != -INFINITY)
+    for (int s = lane_in_group; s < hp.count; s += G) den += fast_exp2(hp.lse[s * kHG] - m);
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+}
+
+// The merge of many parts of few (row, head)s: one CTA each. Thread (p, c) sums
+// 4 columns over every fourth part, eight loads in flight; the four sums meet
+// in shared memory.
+__global__ void __launch_bounds__(512) page8_merge_kernel(P8Args a, int NH) {
+  __shared__ float4 sAcc[3][128];
   pdl_wait();
   pdl_launch_dependents();
-  const int H16 = a.num_heads / kHG, sub = NH / kHG;
-  const int n = blockIdx.x / H16, t16 = blockIdx.x % H16, tid = threadIdx.x;
-  const int h = tid >> 4, c = blockIdx.y * kMergeCols + (tid & 15) * 4;
-  const QtileParts qp = locate_qtile(a.ws, a.num_q, a.groups, a.num_ctas, 0, n, t16 / sub);
-  const float* lse = a.lse_part[t16 % sub];
-  const float* part = a.o_part[t16 % sub];
-  // the largest log-sum-exp, then the weights
-  float m = -INFINITY;
-  for (int s = tid & 15; s < qp.count; s += 16) m = fmaxf(m, lse[(qp.first + s) * kHG + h]);
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float den = 0.f;
+  const int n = blockIdx.x / a.num_heads, h = blockIdx.x % a.num_heads;
+  const int p = threadIdx.x >> 7, c = threadIdx.x & 127;
+  const HeadParts hp = head_parts(a, NH, n, h);
+  float m, den;
+  merge_weights<32>(hp, threadIdx.x & 31, m, den);
+  const float inv = den == 0.f ? 0.f : 1.f / den, b = m == -INFINITY ? 0.f : m;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < qp.count; s0 += 32) {
-    const int ns = min(32, qp.count - s0);
-    __syncthreads();
-    for (int s = tid & 15; s < ns; s += 16) {
-      const float w = m == -INFINITY ? 0.f : fast_exp2(lse[(qp.first + s0 + s) * kHG + h] - m);
-      sW[s][h] = w;
-      den += w;
+#pragma unroll 1
+  for (int s0 = p; s0 < hp.count; s0 += 32) {
+    float4 v[8];
+    float w[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int s = min(s0 + 4 * u, hp.count - 1);
+      v[u] = *reinterpret_cast<const float4*>(hp.o + (size_t)s * kHG * kDc + 4 * c);
+      w[u] = s0 + 4 * u < hp.count ? fast_exp2(hp.lse[s * kHG] - b) * inv : 0.f;
     }
-    __syncthreads();
-#pragma unroll 8
-    for (int s = 0; s < ns; ++s) {
-      const float4 v = *reinterpret_cast<const float4*>(part + ((qp.first + s0 + s) * kHG + h) * kDc + c);
-      const float w = sW[s][h];
-      acc.x = fmaf(w, v.x, acc.x);
-      acc.y = fmaf(w, v.y, acc.y);
-      acc.z = fmaf(w, v.z, acc.z);
-      acc.w = fmaf(w, v.w, acc.w);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (s0 + 4 * u >= hp.count) break;
+      acc.x = fmaf(w[u], v[u].x, acc.x);
+      acc.y = fmaf(w[u], v[u].y, acc.y);
+      acc.z = fmaf(w[u], v[u].z, acc.z);
+      acc.w = fmaf(w[u], v[u].w, acc.w);
+    }
+  }
+  if (p > 0) sAcc[p - 1][c] = acc;
+  __syncthreads();
+  if (p == 0) {
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+      const float4 v = sAcc[u][c];
+      acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+    }
+    const size_t row = (size_t)n * a.num_heads + h;
+    *reinterpret_cast<float4*>(a.o_lat + row * kDc + 4 * c) = acc;
+    if (c == 0) a.lse[row] = den == 0.f ? -INFINITY : m + log2f(den);
+  }
+}
+
+// The merge of a few parts for up to 16 rows and the output projection in one:
+// CTA = (16 rows, 64 output columns, head h). Its slice of W_uv (64 KB) comes
+// by cp.async while 16 threads a row merge the row's 512 latents to bf16 (as
+// the other projections take theirs); then 8 warps, each a quarter of K and 32
+// of the columns (m16n8k16), whose sums meet in shared memory.
+constexpr int kMpStride = kDc * 2 + 16;  // bytes of a merged row, padded against bank conflicts
+constexpr int kMpW = 0, kMpA = kDc * 128, kMpRed = kMpA + 16 * kMpStride, kMpSmem = kMpRed + 4 * 16 * 64 * 4;
+__global__ void __launch_bounds__(256) page8_merge_proj_kernel(P8Args a, int NH, const __nv_bfloat16* W_uv,
+                                                               __nv_bfloat16* out) {
+  extern __shared__ __align__(1024) uint8_t smem_mp[];
+  uint8_t* sW = smem_mp + kMpW;
+  uint8_t* sA = smem_mp + kMpA;
+  float* sRed = reinterpret_cast<float*>(smem_mp + kMpRed);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.z, row0 = blockIdx.x * 16, col0 = blockIdx.y * 64, H = a.num_heads;
+  const __nv_bfloat16* src = W_uv + (size_t)h * kDc * kDv + col0;
+#pragma unroll 4
+  for (int i = tid; i < kDc * 8; i += 256)
+    cp_async16(sW + sw128(i >> 3, i & 7), src + (size_t)(i >> 3) * kDv + (i & 7) * 8);
+  cp_async_commit();
+  // the weights do not depend on earlier kernels; the partials do
+  pdl_wait();
+  pdl_launch_dependents();
+  {
+    const int r = tid >> 4, j = tid & 15, n = row0 + r;
+    HeadParts hp{a.lse_part[0], a.o_part[0], 0};
+    if (n < a.num_q) hp = head_parts(a, NH, n, h);
+    float m, den;
+    merge_weights<16>(hp, j, m, den);
+    const float inv = den == 0.f ? 0.f : 1.f / den, b = m == -INFINITY ? 0.f : m;
+    if (blockIdx.y == 0 && j == 0 && n < a.num_q)
+      a.lse[(size_t)n * H + h] = den == 0.f ? -INFINITY : m + log2f(den);
+    float4 acc[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int s = 0; s < hp.count; s += 2) {
+      const bool two = s + 1 < hp.count;
+      const float* p0 = hp.o + (size_t)s * kHG * kDc + 4 * j;
+      const float* p1 = two ? p0 + kHG * kDc : p0;
+      float4 v0[8], v1[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v0[k] = *reinterpret_cast<const float4*>(p0 + 64 * k);
+        v1[k] = *reinterpret_cast<const float4*>(p1 + 64 * k);
+      }
+      const float w0 = fast_exp2(hp.lse[s * kHG] - b) * inv;
+      const float w1 = two ? fast_exp2(hp.lse[(s + 1) * kHG] - b) * inv : 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        acc[k].x = fmaf(w0, v0[k].x, acc[k].x);
+        acc[k].y = fmaf(w0, v0[k].y, acc[k].y);
+        acc[k].z = fmaf(w0, v0[k].z, acc[k].z);
+        acc[k].w = fmaf(w0, v0[k].w, acc[k].w);
+        if (two) {
+          acc[k].x = fmaf(w1, v1[k].x, acc[k].x);
+          acc[k].y = fmaf(w1, v1[k].y, acc[k].y);
+          acc[k].z = fmaf(w1, v1[k].z, acc[k].z);
+          acc[k].w = fmaf(w1, v1[k].w, acc[k].w);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      *reinterpret_cast<uint2*>(sA + r * kMpStride + (j + 16 * k) * 8) =
+          make_uint2(pack_bf16(acc[k].x, acc[k].y), pack_bf16(acc[k].z, acc[k].w));
+  }
+  cp_async_wait_all();
+  __syncthreads();
+  const int g = lane >> 2, q = lane & 3, kq = warp >> 1, nh = warp & 1;
+  float acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+#pragma unroll
+  for (int ks = 0; ks < 8; ++ks) {
+    const int k = kq * 128 + ks * 16;
+    const uint8_t* lo = sA + g * kMpStride + (k + 2 * q) * 2;
+    const uint8_t* hi = lo + 8 * kMpStride;
+    const uint32_t a0 = *reinterpret_cast<const uint32_t*>(lo), a1 = *reinterpret_cast<const uint32_t*>(hi);
+    const uint32_t a2 = *reinterpret_cast<const uint32_t*>(lo + 16), a3 = *reinterpret_cast<const uint32_t*>(hi + 16);
+    const int kr = k + (lane & 7) + (((lane >> 3) & 1) << 3);
+#pragma unroll
+    for (int np = 0; np < 2; ++np) {
+      uint32_t b0, b1, b2, b3;
+      ldsm_x4_t(smem_u32(sW + sw128(kr, nh * 4 + np * 2 + (lane >> 4))), b0, b1, b2, b3);
+      mma_16816(acc[2 * np], a0, a1, a2, a3, b0, b1);
+      mma_16816(acc[2 * np + 1], a0, a1, a2, a3, b2, b3);
     }
   }
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-  const float inv = den == 0.f ? 0.f : 1.f / den;
-  const size_t row = (size_t)n * a.num_heads + t16 * kHG + h;
-  *reinterpret_cast<float4*>(a.o_lat + row * kDc + c) =
-      make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-  if (blockIdx.y == 0 && (tid & 15) == 0) a.lse[row] = den == 0.f ? -INFINITY : m + log2f(den);
+  for (int nt = 0; nt < 4; ++nt) {
+    float* d = sRed + (kq * 16 + g) * 64 + nh * 32 + nt * 8 + 2 * q;
+    *reinterpret_cast<float2*>(d) = make_float2(acc[nt][0], acc[nt][1]);
+    *reinterpret_cast<float2*>(d + 8 * 64) = make_float2(acc[nt][2], acc[nt][3]);
+  }
+  __syncthreads();
+  const int r = tid >> 4, c = (tid & 15) * 4, row = row0 + r;
+  if (row < a.num_q) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 x = *reinterpret_cast<const float4*>(sRed + (k * 16 + r) * 64 + c);
+      v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+    }
+    *reinterpret_cast<uint2*>(out + ((size_t)row * H + h) * kDv + col0 + c) =
+        make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+  }
 }
 
 // mass[slot(t)] = decay * mass[slot(t)] + sum over the sequence's rows and all
@@ -1020,9 +1157,13 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
   a.o_lat = reinterpret_cast<float*>(ws + L.o_lat);
   a.lse = reinterpret_cast<float*>(ws + L.lse);
   a.scores = with_mass ? reinterpret_cast<float*>(ws + L.scores) : nullptr;
-  // few tiles for many CTAs: each is cut into many parts, which one CTA would
-  // merge alone at the end; the merge kernel spreads them over the device
-  a.fused = num_q * (H / NH) * 4 >= C;
+  // Who merges the splits. From 256 rows on most tiles are whole and the rest
+  // is merged in the decode kernel; the tensor-core projection follows. Below,
+  // the merge goes into the projection, unless there are few tiles, each cut
+  // into so many parts that the merge has to spread over the device first.
+  const bool many_parts = num_q * (H / NH) * 4 < C;
+  a.fused = num_q >= 256 && !many_parts;
+  const bool merge_proj = num_q < 256 && !many_parts;
   cudaError_t e = cudaSuccess;
   if (!a.self_plan)
     e = launch_plan(PlanArgs{seq_lens, query_start_loc, batch, (int32_t)num_q, H / NH, C, bs,
@@ -1041,8 +1182,14 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
     return r != cudaSuccess ? r : launch_pdl(kernel, dim3(C), dim3(kThreads), smem, st, codes_map, rope_map, a);
   };
   e = NH == 16 ? launch(page8_decode_kernel<16>, Sm<16>::alloc) : launch(page8_decode_kernel<32>, Sm<32>::alloc);
-  if (e == cudaSuccess && !a.fused)
-    e = launch_pdl(page8_merge_kernel, dim3((unsigned)(num_q * (H / kHG)), kDc / kMergeCols), dim3(256), 0, st, a, NH);
+  if (e == cudaSuccess && many_parts)
+    e = launch_pdl(page8_merge_kernel, dim3((unsigned)(num_q * H)), dim3(512), 0, st, a, NH);
+  if (e == cudaSuccess && merge_proj) {
+    e = cudaFuncSetAttribute(page8_merge_proj_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMpSmem);
+    if (e == cudaSuccess)
+      e = launch_pdl(page8_merge_proj_kernel, dim3((unsigned)((num_q + 15) / 16), kDv / 64, H), dim3(256),
+                     kMpSmem, st, a, NH, (const __nv_bfloat16*)W_uv, (__nv_bfloat16*)out);
+  }
   if (e != cudaSuccess) return MLA_ERR_CUDA;
   if (with_mass) {
     const MassArgs ma{a.scores, a.lse, seq_lens, query_start_loc, block_table, max_blocks, bs,
@@ -1054,7 +1201,7 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
       if (e != cudaSuccess) return MLA_ERR_CUDA;
     }
   }
-  return mla_out_proj(cfg, a.o_lat, W_uv, out, num_q, stream);
+  return merge_proj ? MLA_OK : mla_out_proj(cfg, a.o_lat, W_uv, out, num_q, stream);
 }
 
 }  // namespace
