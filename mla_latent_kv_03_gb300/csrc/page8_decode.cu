@@ -29,8 +29,10 @@
 // outgrown by more than 2^6.
 //
 // NH = 16 or 32 heads of one row make a column group. The work is cut as in
-// the other decodes (units of one row, one group and 64 tokens in equal
-// contiguous shares, one CTA a share). Per CTA (384 threads):
+// the other decodes (units of one row and 64 tokens in equal contiguous
+// shares), and each share is taken by one CTA per group: the CTAs of a share
+// read the same tokens at the same time, so a token comes from HBM once for
+// all heads. Per CTA (384 threads):
 //   warp 0      copies: 128 tokens a stage (4 slabs of 128 codes, one of rope
 //               values), two stages, SWIZZLE_128B; block ids are checked;
 //   warp 1      issues the output products of a tile as soon as its weights are
@@ -77,7 +79,7 @@ struct P8Args {
   int32_t block_size;
   int32_t num_heads;
   int32_t groups;     // column groups of a row: num_heads / NH
-  int32_t num_ctas;
+  int32_t shares;     // shares of the work; CTAs = shares * groups
   int64_t num_q;
   float scale_log2;
   uint8_t* ws;
@@ -87,30 +89,51 @@ struct P8Args {
   const int32_t* query_start_loc;
   int32_t batch;
   int32_t self_plan;   // the kernel derives the split itself
-  float* lse_part[2];  // [slots][16] of each 16 heads of a group
-  float* o_part[2];    // [slots][16][512]
+  // partials of each 16 heads: [slots][16] and [slots][16][512]; the first
+  // 16 heads' where ws_layout has them, the others' one after another
+  float* lse_first;
+  float* o_first;
+  float* lse_rest;
+  float* o_rest;
+  int64_t slots;
+  int* arrive;         // [num_q, groups] parts merged so far (fused)
   float* o_lat;        // [num_q, H, 512]
   float* lse;          // [num_q, H], base 2
   float* scores;       // [num_q, H / 16, max tokens, 16], base 2; NULL without mass
   int32_t fused;       // merge the splits in the decode kernel
 };
 
-// The decode workspace: the split plan and the partials of ws_layout, the
-// partials of a group's second 16 heads, the query terms and score factors,
-// the merged latents, their log-sum-exps and (with mass) the scores.
+// The partials of heads 16 t16 ... 16 t16 + 15.
+__device__ __forceinline__ float* lse_part(const P8Args& a, int t16) {
+  return t16 == 0 ? a.lse_first : a.lse_rest + (int64_t)(t16 - 1) * a.slots * kHG;
+}
+__device__ __forceinline__ float* o_part(const P8Args& a, int t16) {
+  return t16 == 0 ? a.o_first : a.o_rest + (int64_t)(t16 - 1) * a.slots * kHG * kDc;
+}
+
+// The decode workspace: the split plan and the first 16 heads' partials of
+// ws_layout, the other heads' partials, the query terms and score factors, the
+// merge's counters, the merged latents, their log-sum-exps and (with mass) the
+// scores.
 struct P8Ws {
-  size_t lse2, opart2, q8, coef, o_lat, lse, scores, total;
+  size_t lse_rest, o_rest, q8, coef, arrive, o_lat, lse, scores, total;
 };
 int group_heads(int H) { return H >= 32 ? 32 : 16; }
-P8Ws p8_ws(int64_t num_q, int H, int num_ctas, int64_t max_tokens, bool mass) {
-  const int NH = group_heads(H);
-  const WsLayout W = ws_layout(num_q, H / NH, num_ctas);
+// Shares of the work: with one CTA per group to a share, about num_ctas CTAs.
+int p8_shares(int H, int num_ctas) {
+  const int s = num_ctas / (H / group_heads(H));
+  return s > 0 ? s : 1;
+}
+P8Ws p8_ws(int64_t num_q, int H, int shares, int64_t max_tokens, bool mass) {
+  const WsLayout W = ws_layout(num_q, 1, shares);
+  const size_t rest = (size_t)(H / kHG - 1) * W.slots * kHG;
   P8Ws L;
-  L.lse2 = align_up(W.total, 256);
-  L.opart2 = NH == 32 ? align_up(L.lse2 + (size_t)W.slots * kHG * 4, 256) : L.lse2;
-  L.q8 = NH == 32 ? align_up(L.opart2 + (size_t)W.slots * kHG * kDc * 4, 256) : L.lse2;
+  L.lse_rest = align_up(W.total, 256);
+  L.o_rest = align_up(L.lse_rest + rest * 4, 256);
+  L.q8 = align_up(L.o_rest + rest * kDc * 4, 256);
   L.coef = align_up(L.q8 + (size_t)num_q * H * (2 * kDc + 2 * kDr), 256);
-  L.o_lat = align_up(L.coef + (size_t)num_q * H * 4, 256);
+  L.arrive = align_up(L.coef + (size_t)num_q * H * 4, 256);
+  L.o_lat = align_up(L.arrive + (size_t)num_q * (H / kHG) * 4, 256);
   L.lse = align_up(L.o_lat + (size_t)num_q * H * kDc * 4, 256);
   L.scores = align_up(L.lse + (size_t)num_q * H * 4, 256);
   L.total = mass ? align_up(L.scores + (size_t)num_q * H * max_tokens * 4, 256) : L.scores;
@@ -281,9 +304,9 @@ __device__ __forceinline__ void query_terms(const uint32_t* u, float f, uint4& t
 // rope values, swizzled as shared memory holds them, and the factor that
 // undoes the head's scale. 8 threads a head, 64 latent columns each.
 template <int NH>
-__global__ void __launch_bounds__(NH * 8) page8_query_kernel(const uint16_t* q_abs, int64_t num_q,
-                                                             int groups, float scale_log2,
-                                                             uint8_t* q8, float* coef) {
+__global__ void __launch_bounds__(NH * 8) page8_query_kernel(const uint16_t* q_abs,
+                                                             float scale_log2, uint8_t* q8,
+                                                             float* coef, int* arrive) {
   using S = Sm<NH>;
   pdl_wait();
   pdl_launch_dependents();
@@ -322,6 +345,7 @@ __global__ void __launch_bounds__(NH * 8) page8_query_kernel(const uint16_t* q_a
     *reinterpret_cast<uint4*>(slab + sw128(NH + h, c16 & 7)) = t2;
   }
   *reinterpret_cast<uint4*>(dst + S::q_rope + sw128(h, part)) = rope;
+  if (arrive && threadIdx.x == 0) arrive[blockIdx.x] = 0;
   if (part == 0) coef[row] = scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
 }
 
@@ -352,11 +376,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* merge_flag = reinterpret_cast<int*>(sm + S::misc + 8);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const WsLayout L = ws_layout(a.num_q, a.groups, a.num_ctas);
+  const int share = blockIdx.x / a.groups, grp = blockIdx.x % a.groups;
   uint32_t* status = &reinterpret_cast<WsHeader*>(a.ws)->status;
   const int bs = a.block_size;
   const int bs_shift = bs == 16 ? 4 : (bs == 32 ? 5 : 6);
 
+  // (the split's inputs on their way to L1 during the set-up)
+  if (a.self_plan && tid < a.batch) {
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(a.seq_lens + tid));
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(a.query_start_loc + tid + 1));
+  }
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       const int n = (i == kSFree || i == kPFull || i == kPFull + 1 || i == kOFree) ? kSoftThreads / 32
@@ -383,21 +412,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   int total = 0;
   if (a.self_plan) {
     int4* rows = reinterpret_cast<int4*>(sm + S::rows);
-    total = self_plan<kThreads>(a.seq_lens, a.query_start_loc, a.batch, (int)a.num_q, a.groups,
+    total = self_plan<kThreads>(a.seq_lens, a.query_start_loc, a.batch, (int)a.num_q, 1,
                                 (int64_t)a.max_blocks * bs, rows, reinterpret_cast<int*>(sm + S::red),
                                 status, tid);
-    has_work = sw.init_rows(rows, (int)a.num_q, a.groups, total, a.num_ctas, blockIdx.x);
+    has_work = sw.init_rows(rows, (int)a.num_q, 1, total, a.shares, share);
   } else {
     pdl_wait();
-    has_work = sw.init(a.ws, a.num_q, a.groups, a.num_ctas, blockIdx.x);
+    has_work = sw.init(a.ws, a.num_q, 1, a.shares, share);
   }
   pdl_launch_dependents();
   if (warp >= kSoftWarp0) {
     pdl_wait();
     const int st = tid - kSoftWarp0 * 32;
     if (a.self_plan && blockIdx.x == 0) {
-      // the plan, for the merge kernel
-      int4* row_info = reinterpret_cast<int4*>(a.ws + L.row_info);
+      // the plan, for the merge kernels
+      int4* row_info = reinterpret_cast<int4*>(a.ws + ws_layout(a.num_q, 1, a.shares).row_info);
       for (int n = st; n < (int)a.num_q; n += kSoftThreads) row_info[n] = sw.row_info[n];
       if (st == 0) {
         WsHeader* hdr = reinterpret_cast<WsHeader*>(a.ws);
@@ -406,8 +435,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         hdr->qblocks = 0;
         hdr->total_units = total;
         hdr->share = sw.share;
-        hdr->num_ctas = a.num_ctas;
-        hdr->groups = a.groups;
+        hdr->num_ctas = a.shares;
+        hdr->groups = 1;
         hdr->num_q = (int32_t)a.num_q;
         hdr->batch = a.batch;
       }
@@ -425,7 +454,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (has_work && warp == 0) {
     // -------------------------------------------------------------- copies
-    const uint64_t policy = l2_evict_first_policy();
+    // tokens that only this CTA reads leave L2 first; those that other groups
+    // or rows read as well stay as they are
+    uint64_t policy = l2_evict_first_policy();
+    if (a.groups > 1 || a.num_q > a.batch)
+      asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
     int i = 0;
     bool ok = true;
     while (ok && sw.next(seg)) {
@@ -590,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int qb = seg_i % QB;
       if (seg_i >= QB && !warp_wait(kQFree + qb, ((seg_i / QB) - 1) & 1)) { ok = false; break; }
       if (lane == 0) {
-        const int64_t tile = (int64_t)seg.n * a.groups + seg.g;
+        const int64_t tile = (int64_t)seg.n * a.groups + grp;
         mbar_arrive_expect_tx(&bars[kQReady + qb], S::q_bytes + NH * 4);
         bulk_load(sm + S::q + qb * S::q_bytes, a.q8 + tile * S::q_bytes, S::q_bytes, &bars[kQReady + qb]);
         bulk_load(coef + qb * NH, a.coef + tile * NH, NH * 4, &bars[kQReady + qb]);
@@ -620,12 +653,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int bar = kHalfBar + half;
     float* red = reinterpret_cast<float*>(sm + S::red);
     float* scratch = reinterpret_cast<float*>(sm + S::merge);
-    int* arrive = reinterpret_cast<int*>(a.ws + L.arrive);
     int i = 0, seg_i = 0;
     bool aborted = false;
     while (!aborted && sw.next(seg)) {
       const int n = seg_tiles(), qb = seg_i % QB;
-      const int64_t tile = (int64_t)seg.n * a.groups + seg.g;
+      const int64_t tile = (int64_t)seg.n * a.groups + grp;
       float cq[HT], ref[HT], l[HT];
       const bool okq = warp_wait(kQReady + qb, (seg_i / QB) & 1);
 #pragma unroll
@@ -672,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (a.scores && live) {
             const int64_t tok = (int64_t)seg.k0 * kTile + t * kTok + r;
-            const int64_t t16 = (int64_t)seg.n * (a.num_heads / kHG) + seg.g * (NH / kHG) + h0 / kHG;
+            const int64_t t16 = (int64_t)seg.n * (a.num_heads / kHG) + grp * (NH / kHG) + h0 / kHG;
             float4* o = reinterpret_cast<float4*>(
                 a.scores + (t16 * a.max_blocks * bs + tok) * kHG + h0 % kHG);
 #pragma unroll
@@ -806,37 +838,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < HT; ++k)
         if (lane == 0) red[(half * 4 + w4) * HT + k] = l[k];
       named_bar_sync(bar, 128);
-      const int u_first = seg.ustart + seg.g * seg.tiles;
-      const int c_first = u_first / sw.share, c_last = (u_first + seg.tiles - 1) / sw.share;
+      const int c_first = seg.ustart / sw.share, c_last = (seg.ustart + seg.tiles - 1) / sw.share;
       const bool direct = a.fused && c_first == c_last;
-      const int64_t slot = (int64_t)blockIdx.x + tile;
-      const int s16 = h0 / kHG, hr = h0 % kHG;       // 16-head part of the group, head in it
-      float* o_row = a.o_lat + ((size_t)seg.n * a.num_heads + seg.g * NH) * kDc;
-      float* dst = (direct ? o_row + (size_t)h0 * kDc : a.o_part[s16] + ((size_t)slot * kHG + hr) * kDc) +
+      const int64_t slot = (int64_t)share + seg.n;
+      const int t16 = grp * (NH / kHG) + h0 / kHG, hr = h0 % kHG;  // 16 heads of the row, head in them
+      float* o_row = a.o_lat + ((size_t)seg.n * a.num_heads + grp * NH) * kDc;
+      float* dst = (direct ? o_row + (size_t)h0 * kDc : o_part(a, t16) + (slot * kHG + hr) * kDc) +
                    w4 * 32 + lane;
+      // (all of a row's loads before the first is used)
+      float o1[2][HT], o2[2][HT], o3[2][HT];
+      auto load_o = [&](int j) {
+        const uint32_t at = trow + kOCol + (uint32_t)(j * 3 * NH + h0);
+        tmem_ld(at, o1[j & 1]);
+        tmem_ld(at + NH, o2[j & 1]);
+        tmem_ld(at + 2 * NH, o3[j & 1]);
+      };
+      load_o(0);
+      float mine = 0.f, mref = 0.f;
 #pragma unroll
       for (int k = 0; k < HT; ++k) {
         l[k] = (red[half * 4 * HT + k] + red[(half * 4 + 1) * HT + k]) +
                (red[(half * 4 + 2) * HT + k] + red[(half * 4 + 3) * HT + k]);
-        if (r == k) {
-          const float lse = l[k] == 0.f ? -INFINITY : ref[k] - kRefLog2 + log2f(l[k]);
-          if (direct)
-            a.lse[(size_t)seg.n * a.num_heads + seg.g * NH + h0 + k] = lse;
-          else
-            a.lse_part[s16][slot * kHG + hr + k] = lse;
-        }
-        l[k] = l[k] == 0.f ? 0.f : 1.f / l[k];       // (a NaN sum stays NaN)
+        if (r == k) mine = l[k], mref = ref[k];
+        l[k] = l[k] == 0.f ? 0.f : __fdividef(1.f, l[k]);       // (a NaN sum stays NaN)
       }
-#pragma unroll 1
-      for (int j = 0; j < 4; ++j) {
-        float o1[HT], o2[HT], o3[HT];
-        const uint32_t at = trow + kOCol + (uint32_t)(j * 3 * NH + h0);
-        tmem_ld(at, o1);
-        tmem_ld(at + NH, o2);
-        tmem_ld(at + 2 * NH, o3);
-        tc::wait_ld();
+      if (r < HT) {
+        const float lse = mine == 0.f ? -INFINITY : mref - kRefLog2 + log2f(mine);
+        if (direct)
+          a.lse[(size_t)seg.n * a.num_heads + grp * NH + h0 + r] = lse;
+        else
+          lse_part(a, t16)[slot * kHG + hr + r] = lse;
+      }
 #pragma unroll
-        for (int k = 0; k < HT; ++k) dst[(size_t)k * kDc + j * 128] = ((o1[k] + o2[k]) + o3[k]) * l[k];
+      for (int j = 0; j < 4; ++j) {
+        tc::wait_ld();
+        if (j < 3) load_o(j + 1);
+#pragma unroll
+        for (int k = 0; k < HT; ++k)
+          dst[(size_t)k * kDc + j * 128] = ((o1[j & 1][k] + o2[j & 1][k]) + o3[j & 1][k]) * l[k];
       }
       tc::fence_before_sync();
       __syncwarp();
@@ -844,22 +883,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (a.fused && !direct) {
         __threadfence();  // publish protocol: see count_arrival
         named_bar_sync(kSoftBar, kSoftThreads);
-        if (st == 0) *merge_flag = count_arrival(&arrive[tile]) == c_last - c_first;
+        if (st == 0) *merge_flag = count_arrival(&a.arrive[tile]) == c_last - c_first;
         named_bar_sync(kSoftBar, kSoftThreads);
         if (*merge_flag) {
           const int parts = c_last - c_first + 1;
           // merge_qtile leaves the maxima and the inverse weight sums in its scratch
           if constexpr (NH == 16) {
-            merge_qtile<kSoftThreads>(a.lse_part[0], a.o_part[0], c_first + tile, parts, 1, o_row, st,
+            merge_qtile<kSoftThreads>(a.lse_first, a.o_first, (int64_t)c_first + seg.n, parts, 1, o_row, st,
                                       scratch, [] { named_bar_sync(kSoftBar, kSoftThreads); });
             if (st < kHG) a.lse[tile * kHG + st] = merged_lse(scratch[st], scratch[kHG + st]);
           } else {
             float* mine = scratch + half * (S::merge_bytes / 4);
-            merge_qtile<128>(a.lse_part[half], a.o_part[half], c_first + tile, parts, 1,
+            merge_qtile<128>(lse_part(a, t16), o_part(a, t16), (int64_t)c_first + seg.n, parts, 1,
                              o_row + half * kHG * kDc, r, mine, [&] { named_bar_sync(bar, 128); });
             if (r < kHG) a.lse[tile * NH + half * kHG + r] = merged_lse(mine[r], mine[kHG + r]);
           }
-          if (st == 0) arrive[tile] = 0;  // every part has arrived: ready for the next launch
         }
       }
       named_bar_sync(kSoftBar, kSoftThreads);  // red and the scratch may be written again
@@ -876,17 +914,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tc::dealloc(tmem, kTmemCols);
 }
 
-// The parts of (row n, head h): 16-row groups first, first + 1, ... of its
-// half's partials.
+// The parts of (row n, head h), from the row's entry of the plan: its 16
+// heads' partials, one slot after another.
 struct HeadParts {
   const float* lse;   // of the head, kHG apart
   const float* o;     // [512] of the head, kHG * 512 apart
   int count;
 };
-__device__ __forceinline__ HeadParts head_parts(const P8Args& a, int NH, int n, int h) {
-  const QtileParts qp = locate_qtile(a.ws, a.num_q, a.groups, a.num_ctas, 0, n, h / NH);
-  const int sub = (h % NH) / kHG, hr = h % kHG;
-  return {a.lse_part[sub] + qp.first * kHG + hr, a.o_part[sub] + (qp.first * kHG + hr) * kDc, qp.count};
+__device__ __forceinline__ HeadParts head_parts(const P8Args& a, const int4* rows, int share, int n, int h) {
+  HeadParts r{a.lse_first, a.o_first, 0};
+  const int4 ri = rows[n];
+  if (ri.z <= 0) return r;
+  const int cf = ri.w / share, cl = (ri.w + ri.z - 1) / share;
+  const int64_t slot = ((int64_t)cf + n) * kHG + h % kHG;
+  r.lse = lse_part(a, h / kHG) + slot;
+  r.o = o_part(a, h / kHG) + slot * kDc;
+  r.count = cl - cf + 1;
+  return r;
 }
 // 2^lse sums: the largest log-sum-exp m, and den = sum of 2^(lse - m), by a
 // group of G neighbouring lanes.
@@ -906,13 +950,15 @@ __device__ __forceinline__ void merge_weights(const HeadParts& hp, int lane_in_g
 // The merge of many parts of few (row, head)s: one CTA each. Thread (p, c) sums
 // 4 columns over every fourth part, eight loads in flight; the four sums meet
 // in shared memory.
-__global__ void __launch_bounds__(512) page8_merge_kernel(P8Args a, int NH) {
+__global__ void __launch_bounds__(512) page8_merge_kernel(const __grid_constant__ P8Args a) {
   __shared__ float4 sAcc[3][128];
   pdl_wait();
   pdl_launch_dependents();
   const int n = blockIdx.x / a.num_heads, h = blockIdx.x % a.num_heads;
   const int p = threadIdx.x >> 7, c = threadIdx.x & 127;
-  const HeadParts hp = head_parts(a, NH, n, h);
+  const HeadParts hp = head_parts(
+      a, reinterpret_cast<const int4*>(a.ws + ws_layout(a.num_q, 1, a.shares).row_info),
+      reinterpret_cast<const WsHeader*>(a.ws)->share, n, h);
   float m, den;
   merge_weights<32>(hp, threadIdx.x & 31, m, den);
   const float inv = den == 0.f ? 0.f : 1.f / den, b = m == -INFINITY ? 0.f : m;
@@ -956,8 +1002,9 @@ __global__ void __launch_bounds__(512) page8_merge_kernel(P8Args a, int NH) {
 // the other projections take theirs); then 8 warps, each a quarter of K and 32
 // of the columns (m16n8k16), whose sums meet in shared memory.
 constexpr int kMpStride = kDc * 2 + 16;  // bytes of a merged row, padded against bank conflicts
-constexpr int kMpW = 0, kMpA = kDc * 128, kMpRed = kMpA + 16 * kMpStride, kMpSmem = kMpRed + 4 * 16 * 64 * 4;
-__global__ void __launch_bounds__(256) page8_merge_proj_kernel(P8Args a, int NH, const __nv_bfloat16* W_uv,
+constexpr int kMpW = 0, kMpA = kDc * 128, kMpRed = kMpA + 16 * kMpStride, kMpRows = kMpRed + 4 * 16 * 64 * 4, kMpSmem = kMpRows + kSelfMaxRows * 16;
+__global__ void __launch_bounds__(256) page8_merge_proj_kernel(const __grid_constant__ P8Args a,
+                                                               const __nv_bfloat16* W_uv,
                                                                __nv_bfloat16* out) {
   extern __shared__ __align__(1024) uint8_t smem_mp[];
   uint8_t* sW = smem_mp + kMpW;
@@ -970,13 +1017,28 @@ __global__ void __launch_bounds__(256) page8_merge_proj_kernel(P8Args a, int NH,
   for (int i = tid; i < kDc * 8; i += 256)
     cp_async16(sW + sw128(i >> 3, i & 7), src + (size_t)(i >> 3) * kDv + (i & 7) * 8);
   cp_async_commit();
-  // the weights do not depend on earlier kernels; the partials do
-  pdl_wait();
+  // The weights do not depend on earlier kernels, and where the parts lie is
+  // known from the lengths (the split of the decode, derived again); the parts
+  // themselves have to be waited for.
+  const int4* rows = reinterpret_cast<const int4*>(a.ws + ws_layout(a.num_q, 1, a.shares).row_info);
+  int share = 1;
+  if (a.self_plan) {
+    int4* mine = reinterpret_cast<int4*>(smem_mp + kMpRows);
+    const int total = self_plan<256>(a.seq_lens, a.query_start_loc, a.batch, (int)a.num_q, 1,
+                                     (int64_t)a.max_blocks * a.block_size, mine,
+                                     reinterpret_cast<int*>(sRed), nullptr, tid);
+    share = total > 0 ? (total + a.shares - 1) / a.shares : 1;
+    rows = mine;
+    pdl_wait();
+  } else {
+    pdl_wait();
+    share = reinterpret_cast<const WsHeader*>(a.ws)->share;
+  }
   pdl_launch_dependents();
   {
     const int r = tid >> 4, j = tid & 15, n = row0 + r;
-    HeadParts hp{a.lse_part[0], a.o_part[0], 0};
-    if (n < a.num_q) hp = head_parts(a, NH, n, h);
+    HeadParts hp{a.lse_first, a.o_first, 0};
+    if (n < a.num_q) hp = head_parts(a, rows, share, n, h);
     float m, den;
     merge_weights<16>(hp, j, m, den);
     const float inv = den == 0.f ? 0.f : 1.f / den, b = m == -INFINITY ? 0.f : m;
@@ -1120,11 +1182,12 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
   const size_t need = mla_page8_decode_workspace_size(cfg, num_q, batch, max_blocks, with_mass);
   if (need == 0) return MLA_ERR_UNSUPPORTED;
   if (ws_bytes < need) return MLA_ERR_WORKSPACE_TOO_SMALL;
-  const int C = split_ctas(cfg), H = cfg->num_heads, bs = cfg->block_size, NH = group_heads(H);
+  const int H = cfg->num_heads, bs = cfg->block_size, NH = group_heads(H);
+  const int shares = p8_shares(H, split_ctas(cfg));
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const P8Ws L = p8_ws(num_q, H, C, (int64_t)max_blocks * bs, with_mass);
-  const WsLayout W = ws_layout(num_q, H / NH, C);
+  const P8Ws L = p8_ws(num_q, H, shares, (int64_t)max_blocks * bs, with_mass);
+  const WsLayout W = ws_layout(num_q, 1, shares);
   // With num_blocks == 0 every block id is rejected before any copy; the maps
   // still need an extent.
   CUtensorMap codes_map, rope_map;
@@ -1140,7 +1203,7 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
   a.block_size = bs;
   a.num_heads = H;
   a.groups = H / NH;
-  a.num_ctas = C;
+  a.shares = shares;
   a.num_q = num_q;
   a.scale_log2 = (float)(cfg->softmax_scale * 1.4426950408889634);
   a.ws = ws;
@@ -1150,10 +1213,12 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
   a.query_start_loc = query_start_loc;
   a.batch = batch;
   a.self_plan = num_q <= (NH == 16 ? Sm<16>::self_rows : Sm<32>::self_rows);
-  a.lse_part[0] = reinterpret_cast<float*>(ws + W.lse);
-  a.lse_part[1] = reinterpret_cast<float*>(ws + L.lse2);
-  a.o_part[0] = reinterpret_cast<float*>(ws + W.opart);
-  a.o_part[1] = reinterpret_cast<float*>(ws + L.opart2);
+  a.lse_first = reinterpret_cast<float*>(ws + W.lse);
+  a.o_first = reinterpret_cast<float*>(ws + W.opart);
+  a.lse_rest = reinterpret_cast<float*>(ws + L.lse_rest);
+  a.o_rest = reinterpret_cast<float*>(ws + L.o_rest);
+  a.slots = W.slots;
+  a.arrive = reinterpret_cast<int*>(ws + L.arrive);
   a.o_lat = reinterpret_cast<float*>(ws + L.o_lat);
   a.lse = reinterpret_cast<float*>(ws + L.lse);
   a.scores = with_mass ? reinterpret_cast<float*>(ws + L.scores) : nullptr;
@@ -1161,34 +1226,34 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
   // is merged in the decode kernel; the tensor-core projection follows. Below,
   // the merge goes into the projection, unless there are few tiles, each cut
   // into so many parts that the merge has to spread over the device first.
-  const bool many_parts = num_q * (H / NH) * 4 < C;
+  const bool many_parts = num_q * 4 < shares;
   a.fused = num_q >= 256 && !many_parts;
   const bool merge_proj = num_q < 256 && !many_parts;
   cudaError_t e = cudaSuccess;
   if (!a.self_plan)
-    e = launch_plan(PlanArgs{seq_lens, query_start_loc, batch, (int32_t)num_q, H / NH, C, bs,
+    e = launch_plan(PlanArgs{seq_lens, query_start_loc, batch, (int32_t)num_q, 1, shares, bs,
                              max_blocks, workspace},
                     st);
   if (e == cudaSuccess) {
     const dim3 grid((unsigned)(num_q * (H / NH)));
-    e = NH == 16 ? launch_pdl(page8_query_kernel<16>, grid, dim3(128), 0, st, a.q_abs, num_q,
-                              a.groups, a.scale_log2, a.q8, a.coef)
-                 : launch_pdl(page8_query_kernel<32>, grid, dim3(256), 0, st, a.q_abs, num_q,
-                              a.groups, a.scale_log2, a.q8, a.coef);
+    e = NH == 16 ? launch_pdl(page8_query_kernel<16>, grid, dim3(128), 0, st, a.q_abs,
+                              a.scale_log2, a.q8, a.coef, a.fused ? a.arrive : nullptr)
+                 : launch_pdl(page8_query_kernel<32>, grid, dim3(256), 0, st, a.q_abs,
+                              a.scale_log2, a.q8, a.coef, a.fused ? a.arrive : nullptr);
   }
   if (e != cudaSuccess) return MLA_ERR_CUDA;
   auto launch = [&](auto kernel, int smem) {
     const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    return r != cudaSuccess ? r : launch_pdl(kernel, dim3(C), dim3(kThreads), smem, st, codes_map, rope_map, a);
+    return r != cudaSuccess ? r : launch_pdl(kernel, dim3(shares * a.groups), dim3(kThreads), smem, st, codes_map, rope_map, a);
   };
   e = NH == 16 ? launch(page8_decode_kernel<16>, Sm<16>::alloc) : launch(page8_decode_kernel<32>, Sm<32>::alloc);
   if (e == cudaSuccess && many_parts)
-    e = launch_pdl(page8_merge_kernel, dim3((unsigned)(num_q * H)), dim3(512), 0, st, a, NH);
+    e = launch_pdl(page8_merge_kernel, dim3((unsigned)(num_q * H)), dim3(512), 0, st, a);
   if (e == cudaSuccess && merge_proj) {
     e = cudaFuncSetAttribute(page8_merge_proj_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMpSmem);
     if (e == cudaSuccess)
       e = launch_pdl(page8_merge_proj_kernel, dim3((unsigned)((num_q + 15) / 16), kDv / 64, H), dim3(256),
-                     kMpSmem, st, a, NH, (const __nv_bfloat16*)W_uv, (__nv_bfloat16*)out);
+                     kMpSmem, st, a, (const __nv_bfloat16*)W_uv, (__nv_bfloat16*)out);
   }
   if (e != cudaSuccess) return MLA_ERR_CUDA;
   if (with_mass) {
@@ -1217,9 +1282,9 @@ size_t mla_page8_decode_workspace_size(const mla_config* cfg, int64_t num_q, int
       num_q > 48 * 1024 || batch < 0 || max_blocks_per_seq < 0 ||
       max_blocks_per_seq > ((int64_t)1 << 31) / cfg->block_size)
     return 0;
-  const int C = split_ctas(cfg);
+  const int C = split_ctas(cfg), H = cfg->num_heads;
   if (C <= 0) return 0;
-  return p8_ws(num_q, cfg->num_heads, C, (int64_t)max_blocks_per_seq * cfg->block_size,
+  return p8_ws(num_q, H, p8_shares(H, C), (int64_t)max_blocks_per_seq * cfg->block_size,
                with_mass != 0)
       .total;
 }
