@@ -19,14 +19,14 @@
 //     a bf16 exactly down to 2^-15 of the head's largest, and the rest within
 //     2^-23 of that largest;
 //   output  O[512, 3 NH] = codes[128, 512]^T . (p_1 | p_2 | p_3)
-//     p = p_1 + p_2 + p_3 in e5m2: 9 significant bits (error 2^-10), down to
-//     2^-24 of the running reference, so a long tail of small weights behind a
-//     large one is not lost.
+//     p = p_1 + p_2 + 2^-5 p_3 in e5m2: 9 significant bits (error 2^-10), in
+//     steps of 2^-25 of the running reference at the least, so a long tail of
+//     small weights behind a large one is not lost.
 // The page's scale enters a score as a factor of its token (a row), and the
 // output as part of the weight: the columns hold 2^(s_t - ref) S_p, and the
 // softmax sum adds the same number divided by S_p again. The running reference
 // of a head follows s_t + log2 S_p, and O is rescaled in TMEM only when it is
-// outgrown by more than 2^6.
+// outgrown by more than 2^10.
 //
 // NH = 16 or 32 heads of one row make a column group. The work is cut as in
 // the other decodes (units of one row and 64 tokens in equal contiguous
@@ -66,8 +66,8 @@ constexpr int kStageB = 5 * kSlab;            // four slabs of codes, one of rop
 constexpr int kThreads = 384;
 constexpr int kSoftWarp0 = 4, kSoftThreads = 256;
 constexpr int kSoftBar = 1, kHalfBar = 2;     // named barriers: all softmax warps; one half (2, 3)
-constexpr float kRefLog2 = 8.f;               // a weight equal to the reference is held as 2^8
-constexpr float kGrowLog2 = 6.f;              // the reference follows when outgrown by 2^6
+constexpr float kRefLog2 = 4.f;               // a weight equal to the reference is held as 2^4
+constexpr float kGrowLog2 = 10.f;             // the reference follows when outgrown by 2^10
 constexpr uint32_t kTmemCols = 512, kSCol = 0, kOCol = 128;
 
 struct P8Args {
@@ -781,7 +781,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t tm[3][HT / 4];
 #pragma unroll
         for (int k = 0; k < HT / 2; k += 2) {
-          // e5m2 is the upper byte of f16: cut the first two terms off, round the last
+          // e5m2 is the upper byte of f16: cut the first two terms off, round
+          // the rest, which is below 2^-5 of the weight, times 2^5
           uint32_t a0 = hp[k], a1 = hp[k + 1];
           tm[0][k / 2] = __byte_perm(a0, a1, 0x7531);
 #pragma unroll
@@ -795,6 +796,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               tm[1][k / 2] = __byte_perm(a0, a1, 0x7531);
             } else {
               uint16_t e0, e1;
+              const __half2 f = __floats2half2_rn(32.f, 32.f);
+              const __half2 m0 = __hmul2(r0, f), m1 = __hmul2(r1, f);
+              a0 = *reinterpret_cast<const uint32_t*>(&m0);
+              a1 = *reinterpret_cast<const uint32_t*>(&m1);
               asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(e0) : "r"(a0));
               asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(e1) : "r"(a1));
               tm[2][k / 2] = (uint32_t)e0 | ((uint32_t)e1 << 16);
@@ -875,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j < 3) load_o(j + 1);
 #pragma unroll
         for (int k = 0; k < HT; ++k)
-          dst[(size_t)k * kDc + j * 128] = ((o1[j & 1][k] + o2[j & 1][k]) + o3[j & 1][k]) * l[k];
+          dst[(size_t)k * kDc + j * 128] = fmaf(o3[j & 1][k], 0.03125f, o1[j & 1][k] + o2[j & 1][k]) * l[k];
       }
       tc::fence_before_sync();
       __syncwarp();
