@@ -2,6 +2,7 @@
 // mla_evict_select (which tokens of each sequence stay) and mla_page8_compact
 // (their rows moved, in order, into other pages).
 #include "async_copy.cuh"
+#include "cluster.cuh"
 #include "internal.h"
 #include "page8.cuh"
 
@@ -10,14 +11,26 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // select. The middle tokens (behind the sinks, before the recent ones) are
-// ranked by mass: as an unsigned key that orders like the float (NaN lowest,
-// -0 = +0), a radix select finds the key T of the last token that stays, 8
-// bits at a time from the top, and how many tokens of key T stay; one ordered
-// pass then writes every token above T and the first ones of key T.
-// One CTA per sequence.
+// ranked by mass, as an unsigned key that orders like the float (NaN lowest,
+// -0 = +0). A radix select finds the key T of the last token that stays, 8 bits
+// at a time from the top, and how many tokens of key T stay; then every token
+// above T and the first ones of key T are written in order.
+//
+// A cluster of 1 to 8 CTAs takes a sequence, each CTA a contiguous piece of it,
+// and each warp a contiguous piece of that, so order is a matter of prefix
+// counts: over a warp's 32-token steps by ballots, over warps and CTAs by their
+// totals. The keys are read once, into shared memory (kKeys a CTA; a piece
+// beyond that is read again from the cache in every pass). The CTAs of a
+// cluster meet once a pass: each adds up all their histograms through
+// distributed shared memory.
+// Bound: latency (one pass over 4 bytes a token, five meetings). More than one
+// CTA pays from about 4,096 tokens a CTA.
 // ---------------------------------------------------------------------------
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kKeys = 40 * 1024;              // keys a CTA holds
+constexpr int kSelSmem = kKeys * 4;
+constexpr int kSelPiece = 2048;               // tokens a CTA takes before another joins
 
 struct SelectArgs {
   const float* mass;
@@ -25,7 +38,7 @@ struct SelectArgs {
   const int32_t* block_table;
   int32_t max_blocks;
   const int32_t* seq_lens;
-  int32_t block_size, sinks, recent, budget;
+  int32_t bs_shift, sinks, recent, budget, cluster;
   int32_t* keep;
   int32_t* new_lens;
   uint32_t* status;
@@ -36,90 +49,188 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
   const uint32_t u = __float_as_uint(m + 0.f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+__device__ __forceinline__ int ld_cluster(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a) {
-  __shared__ int hist[256];
-  __shared__ int sWarp[kSelWarps], sWarp2[kSelWarps];
+  extern __shared__ uint32_t sKey[];
+  __shared__ int hist[3][256];  // (another CTA may still read the last pass's)
+  __shared__ int sTotal[2];                     // tokens above T and of key T in this CTA
+  __shared__ int sAbove[kSelWarps], sTies[kSelWarps];
   __shared__ int sPick, sNeed;
   pdl_wait();
   pdl_launch_dependents();
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int len = a.seq_lens[b], bs = a.block_size;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int CL = a.cluster, b = blockIdx.x / CL, rank = blockIdx.x % CL;
+  const int len = a.seq_lens[b];
   const int32_t* bt = a.block_table + (size_t)b * a.max_blocks;
   int32_t* keep = a.keep + (size_t)b * a.budget;
-  const bool bad = len < 0 || (int64_t)len > (int64_t)a.max_blocks * bs;
+  const bool bad = len < 0 || (int64_t)len > ((int64_t)a.max_blocks << a.bs_shift);
   if (bad && tid == 0) set_status(a.status, MLA_DEV_BAD_SEQ);
-  const int n = bad ? 0 : len;
-  const int kept = min(n, a.budget);
-  if (tid == 0) a.new_lens[b] = kept;
-  for (int i = kept + tid; i < a.budget; i += kSelThreads) keep[i] = -1;
-  if (n <= a.budget) {
-    for (int i = tid; i < n; i += kSelThreads) keep[i] = i;
+  const int n = bad ? 0 : len, kept = min(n, a.budget);
+  if (tid == 0 && rank == 0) a.new_lens[b] = kept;
+  if (n <= a.budget) {  // (the whole cluster)
+    for (int i = rank * kSelThreads + tid; i < a.budget; i += CL * kSelThreads) keep[i] = i < n ? i : -1;
     return;
   }
-  const int m0 = a.sinks, m1 = n - a.recent;  // the middle tokens
-  auto key_of = [&](int t) {
-    const int32_t p = bt[t / bs];
-    if (p < 0 || p >= a.num_blocks) return 0u;
-    return mass_key(a.mass[(size_t)p * bs + t % bs]);
+  // this CTA's tokens [c0, c1); warp w's are 32 * steps of them
+  const int steps = (n + CL * kSelThreads - 1) / (CL * kSelThreads);
+  const int c0 = (int)min((int64_t)rank * steps * kSelThreads, (int64_t)n);
+  const int c1 = (int)min((int64_t)c0 + (int64_t)steps * kSelThreads, (int64_t)n);
+  const int m0 = a.sinks, m1 = n - a.recent;    // the middle tokens
+  auto load_key = [&](int t) {
+    const int32_t p = bt[t >> a.bs_shift];
+    if (p < 0 || p >= a.num_blocks) {
+      if ((t & ((1 << a.bs_shift) - 1)) == 0) set_status(a.status, MLA_DEV_BAD_BLOCK);
+      return 0u;
+    }
+    return mass_key(a.mass[((size_t)p << a.bs_shift) + (t & ((1 << a.bs_shift) - 1))]);
   };
-  for (int i = tid; i < (n + bs - 1) / bs; i += kSelThreads)
-    if (bt[i] < 0 || bt[i] >= a.num_blocks) set_status(a.status, MLA_DEV_BAD_BLOCK);
-  int need = a.budget - a.sinks - a.recent;  // middle tokens that stay
+#pragma unroll 8
+  for (int t = c0 + tid; t < c1; t += kSelThreads) {
+    const uint32_t k = load_key(t);
+    if (t - c0 < kKeys) sKey[t - c0] = k;
+  }
+  auto key = [&](int t) { return t - c0 < kKeys ? sKey[t - c0] : load_key(t); };
+  const int want = a.budget - a.sinks - a.recent;  // middle tokens that stay
+  int need = want;
   uint32_t prefix = 0, mask = 0;
-  if (need > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      for (int t = m0 + tid; t < m1; t += kSelThreads) {
-        const uint32_t k = key_of(t);
-        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+  if (tid < 256) hist[0][tid] = 0;
+  __syncthreads();
+  for (int pass = 0; pass < 4 && want > 0; ++pass) {
+    const int shift = 24 - 8 * pass;
+    int* h = hist[pass % 3];
+    const int lo = max(c0, m0), hi = min(c1, m1);
+    for (int t0 = lo; t0 < hi; t0 += kSelThreads) {
+      const int t = t0 + tid;
+      const uint32_t k = t < hi ? key(t) : 0u;
+      const bool in = t < hi && (k & mask) == prefix;
+      const uint32_t d = in ? (k >> shift) & 255u : 256u;
+      int all;
+      __match_all_sync(0xffffffffu, d, &all);
+      if (all) {  // a warp of equal digits counts once: equal keys do not queue up
+        if (in && lane == 0) atomicAdd(&h[d], 32);
+      } else if (in) {
+        atomicAdd(&h[d], 1);
       }
-      __syncthreads();
-      if (tid == 0) {
-        int d = 255, left = need;
-        while (hist[d] < left) left -= hist[d--];
-        sPick = d;
+    }
+    if (tid < 256) hist[(pass + 1) % 3][tid] = 0;
+    cl::sync();
+    // warp 0: the cluster's counts, 8 digits a lane from the top down
+    if (warp == 0) {
+      int c[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int d = 255 - (lane * 8 + i);
+        int v = 0;
+        for (int r = 0; r < CL; ++r) v += ld_cluster(cl::map(smem_u32(&h[d]), r));
+        c[i] = v;
+        sum += v;
+      }
+      int before = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
+      }
+      before -= sum;
+      if (before < need && need <= before + sum) {  // (one lane)
+        int left = need - before, i = 0;
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+          if (i == j && c[j] < left) left -= c[j], ++i;
+        sPick = 255 - (lane * 8 + i);
         sNeed = left;
       }
-      __syncthreads();
-      prefix |= (uint32_t)sPick << shift;
-      mask |= 255u << shift;
-      need = sNeed;
     }
+    __syncthreads();
+    prefix |= (uint32_t)sPick << shift;
+    mask |= 255u << shift;
+    need = sNeed;
+    __syncthreads();
   }
-  // `need` tokens of key `prefix` stay, the first ones
-  int out = 0, ties = 0;
-  for (int t0 = 0; t0 < n; t0 += kSelThreads) {
-    const int t = t0 + tid;
-    bool stay = t < n && (t < m0 || t >= m1), tie = false;
-    if (t < n && !stay && a.budget > a.sinks + a.recent) {
-      const uint32_t k = key_of(t);
-      stay = k > prefix;
+  // how many tokens of each warp stay for sure, and how many have key T
+  const int w0 = c0 + warp * steps * 32;
+  auto classify = [&](int t, bool& above, bool& tie) {
+    above = t < c1 && (t < m0 || t >= m1);
+    tie = false;
+    if (t < c1 && !above && want > 0) {
+      const uint32_t k = key(t);
+      above = k > prefix;
       tie = k == prefix;
     }
-    const uint32_t tb = __ballot_sync(0xffffffffu, tie);
-    if (lane == 0) sWarp[warp] = __popc(tb);
-    __syncthreads();
-    int before = ties, all = 0;
-    for (int k = 0; k < kSelWarps; ++k) {
-      if (k < warp) before += sWarp[k];
-      all += sWarp[k];
-    }
-    if (tie && before + __popc(tb & ((1u << lane) - 1)) < need) stay = true;
-    ties += all;
-    const uint32_t sb = __ballot_sync(0xffffffffu, stay);
-    if (lane == 0) sWarp2[warp] = __popc(sb);
-    __syncthreads();
-    int at = out, total = 0;
-    for (int k = 0; k < kSelWarps; ++k) {
-      if (k < warp) at += sWarp2[k];
-      total += sWarp2[k];
-    }
-    if (stay) keep[at + __popc(sb & ((1u << lane) - 1))] = t;
-    out += total;
-    __syncthreads();
+  };
+  int above_n = 0, ties_n = 0;
+  for (int s = 0; s < steps; ++s) {
+    bool above, tie;
+    classify(w0 + s * 32 + lane, above, tie);
+    above_n += __popc(__ballot_sync(0xffffffffu, above));
+    ties_n += __popc(__ballot_sync(0xffffffffu, tie));
   }
+  if (lane == 0) sAbove[warp] = above_n, sTies[warp] = ties_n;
+  __syncthreads();
+  int above_at = sAbove[lane], ties_at = sTies[lane];  // (kSelWarps is 32)
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, above_at, o), v = __shfl_up_sync(0xffffffffu, ties_at, o);
+    if (lane >= o) above_at += u, ties_at += v;
+  }
+  if (tid == 31) sTotal[0] = above_at, sTotal[1] = ties_at;
+  above_at = __shfl_sync(0xffffffffu, above_at - sAbove[lane], warp);
+  ties_at = __shfl_sync(0xffffffffu, ties_at - sTies[lane], warp);
+  cl::sync();
+  for (int r = 0; r < rank; ++r) {
+    above_at += ld_cluster(cl::map(smem_u32(&sTotal[0]), r));
+    ties_at += ld_cluster(cl::map(smem_u32(&sTotal[1]), r));
+  }
+  for (int s = 0; s < steps; ++s) {
+    const int t = w0 + s * 32 + lane;
+    bool above, tie;
+    classify(t, above, tie);
+    const uint32_t am = __ballot_sync(0xffffffffu, above), tm = __ballot_sync(0xffffffffu, tie);
+    const uint32_t below = (1u << lane) - 1;
+    const int ties_before = ties_at + __popc(tm & below);
+    if (above || (tie && ties_before < need))
+      keep[above_at + __popc(am & below) + min(need, ties_before)] = t;
+    above_at += __popc(am);
+    ties_at += __popc(tm);
+  }
+  cl::sync();  // the others may still read this CTA's totals
+}
+
+// CTAs that share a sequence of up to `tokens`: measured on one GB300 at 64
+// sequences of 4,096 tokens and at 3 of 131,072 (see the table of measurements
+// beside the launch).
+int select_cluster(int64_t tokens) {
+  int c = 1;
+  while (c < 8 && tokens > (int64_t)c * kSelPiece) c *= 2;
+  return c;
+}
+
+cudaError_t launch_select(const SelectArgs& a, int batch, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmem);
+  if (e != cudaSuccess) return e;
+  // a piece of the longest sequence, in shared memory as far as it fits
+  const int64_t tokens = (int64_t)a.max_blocks << a.bs_shift;
+  int64_t piece = (tokens + a.cluster * kSelThreads - 1) / (a.cluster * kSelThreads) * kSelThreads;
+  if (piece > kKeys) piece = kKeys;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)batch * a.cluster);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = (size_t)piece * 4;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -231,10 +342,11 @@ mla_status mla_evict_select(const mla_config* cfg, const float* mass, int64_t nu
   if (!p8_aligned(mass, 4) || !p8_aligned(block_table, 4) || !p8_aligned(seq_lens, 4) ||
       !p8_aligned(keep, 4) || !p8_aligned(new_lens, 4) || !p8_aligned(dev_status, 4))
     return MLA_ERR_INVALID_ARGUMENT;
-  const SelectArgs a{mass, num_blocks, block_table, max_blocks_per_seq, seq_lens, cfg->block_size,
-                     sinks, recent, budget, keep, new_lens, dev_status};
-  const cudaError_t e = launch_pdl(evict_select_kernel, dim3((unsigned)batch), dim3(kSelThreads), 0,
-                                   reinterpret_cast<cudaStream_t>(stream), a);
+  const int shift = cfg->block_size == 16 ? 4 : cfg->block_size == 32 ? 5 : 6;
+  const SelectArgs a{mass, num_blocks, block_table, max_blocks_per_seq, seq_lens, shift, sinks,
+                     recent, budget, select_cluster((int64_t)max_blocks_per_seq << shift), keep,
+                     new_lens, dev_status};
+  const cudaError_t e = launch_select(a, batch, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 

@@ -24,6 +24,7 @@
 #include "async_copy.cuh"
 #include "internal.h"
 #include "page8.cuh"
+#include "pair_math.cuh"
 #include "rope_pairs.cuh"
 
 namespace mla {
@@ -64,62 +65,116 @@ P8WriteWs write_ws(int64_t tokens, int64_t num_blocks, int bs) {
   return L;
 }
 
-__device__ __forceinline__ void unpack2(uint32_t v, float& a, float& b) {
-  a = __uint_as_float(v << 16);
-  b = __uint_as_float(v & 0xffff0000u);
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f32x2_pack(a.x, a.y)), "l"(f32x2_pack(b.x, b.y)));
+  return f32x2_unpack(d);
 }
 
-// One page: sTok[r] is the token of row r, or -1. All threads call it.
+// Shared memory of a page: its tokens' latents and rope keys as given, and what
+// the warps exchange.
+template <int BS>
+struct PageSm {
+  static constexpr int x = 0;                       // [BS][512] bf16
+  static constexpr int k = x + BS * kDc * 2;        // [BS][64] bf16
+  static constexpr int tok = k + BS * kDr * 2;      // [BS] token of a row, or -1
+  static constexpr int mx = tok + BS * 4;           // [8] largest magnitude of a warp
+  static constexpr int bytes = mx + kWarps * 4;
+};
+
+// cos and sin of pos * inv_freq (hi + lo). The angle as in rope_cos_sin, reduced
+// by multiples of pi / 2 to [-pi/4, pi/4] (Cody and Waite, pi / 2 in two
+// floats), then the Taylor series to r^9 and r^8 (remainders below 2e-9 and
+// 3e-8), a third of the instructions of sincosf.
+__device__ __forceinline__ void page_cos_sin(int pos, float hi, float lo, float* c, float* s) {
+  const float p = (float)pos, a = p * hi, tail = fmaf(p, lo, fmaf(p, hi, -a));
+  const float k = rintf(a * 0.636619772367581f);
+  float r = fmaf(-k, 1.57079637050628662f, a);   // pi / 2 rounded to a float
+  r = fmaf(-k, -4.37113900018624283e-08f, r);    // what that rounding took off
+  r += tail;
+  const float z = r * r;
+  const float sp = fmaf(z, fmaf(z, fmaf(z, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f);
+  const float cp = fmaf(z, fmaf(z, fmaf(z, 1.f / 40320.f, -1.f / 720.f), 1.f / 24.f), -0.5f);
+  const float sn = fmaf(r * z, sp, r), cs = fmaf(z, cp, 1.f);
+  const int q = (int)k;
+  const float u = q & 1 ? cs : sn, v = q & 1 ? sn : cs;
+  *s = q & 2 ? -u : u;
+  *c = (q + 1) & 2 ? -v : v;
+}
+
+// One page, all threads: tok[r] (shared) is the token of row r, or -1. Warp w
+// has rows w, w + 8, ...: all their bytes are on their way at once (cp.async),
+// and a row is read from shared memory for the norm and again for the codes, so
+// that few registers hold many rows in flight (three CTAs an SM at 64 rows).
+//   c_hat = (x w) r,  r = 1 / sqrt(mean(x^2) + eps)
+// x w is exact in fp32 (two bf16 factors), so c_hat is one rounding away from
+// r, the largest |c_hat| of a row is r times its largest |x w|, and dividing by
+// the scale is a power of two folded into r. Lane l has elements 8 l ... 8 l + 7
+// and 256 + those.
 template <int BS>
 __device__ __forceinline__ void write_page(const P8WriteArgs& a, const RopeFreq& freq, int64_t page,
-                                           const int* sTok, float* sMax) {
-  constexpr int kRows = BS / kWarps;  // rows of one warp
+                                           uint8_t* sm) {
+  using S = PageSm<BS>;
+  constexpr int kRows = BS / kWarps;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int* sTok = reinterpret_cast<const int*>(sm + S::tok);
+  float* sMax = reinterpret_cast<float*>(sm + S::mx);
   const float old = a.scales[page];
-  int tok[kRows];
-  uint4 x[kRows][2];
+  uint32_t mine = 0;  // bit i: row warp + 8 i has a token
+  int pos[kRows];
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    tok[i] = sTok[warp + kWarps * i];
-    if (tok[i] >= 0) {
-      const uint4* src = reinterpret_cast<const uint4*>(a.c_kv + (size_t)tok[i] * kDc + lane * 16);
-      x[i][0] = __ldg(src);
-      x[i][1] = __ldg(src + 1);
-    } else {
-      x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
-    }
+    const int row = warp + kWarps * i, tok = sTok[row];
+    pos[i] = 0;
+    if (tok < 0) continue;
+    mine |= 1u << i;
+    const __nv_bfloat16* src = a.c_kv + (size_t)tok * kDc + lane * 8;
+    cp_async16(sm + S::x + row * (kDc * 2) + lane * 16, src);
+    cp_async16(sm + S::x + row * (kDc * 2) + 512 + lane * 16, src + kDc / 2);
+    if (lane < 8) cp_async16(sm + S::k + row * (kDr * 2) + lane * 16, a.k_pe + (size_t)tok * kDr + lane * 8);
+    pos[i] = a.positions[tok];
   }
-  float w[16];
-  {
-    const uint4* wp = reinterpret_cast<const uint4*>(a.w + lane * 16);
-    const uint4 w0 = __ldg(wp), w1 = __ldg(wp + 1);
-    const uint32_t u[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-    for (int k = 0; k < 8; ++k) unpack2(u[k], w[2 * k], w[2 * k + 1]);
-  }
-  // c_hat = x r w, fp32; the largest magnitude over the warp's rows
-  float rn[kRows], amax = 0.f;
+  cp_async_commit();
+  const uint4 w0 = *reinterpret_cast<const uint4*>(a.w + lane * 8);
+  const uint4 w1 = *reinterpret_cast<const uint4*>(a.w + kDc / 2 + lane * 8);
+  const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+  const float fhi = freq.hi[lane], flo = freq.lo[lane];
+  const int i1 = rope_i1(a.interleaved, lane), i2 = rope_i2(a.interleaved, lane);
+  auto load_row = [&](int row, uint32_t (&u)[8]) {
+    const uint4 x0 = *reinterpret_cast<const uint4*>(sm + S::x + row * (kDc * 2) + lane * 16);
+    const uint4 x1 = *reinterpret_cast<const uint4*>(sm + S::x + row * (kDc * 2) + 512 + lane * 16);
+    u[0] = x0.x; u[1] = x0.y; u[2] = x0.z; u[3] = x0.w;
+    u[4] = x1.x; u[5] = x1.y; u[6] = x1.z; u[7] = x1.w;
+  };
+  cp_async_wait_all();
+  __syncwarp();
+  float r[kRows], amax = 0.f;
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    const uint32_t u[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w,
-                           x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
-    float ss = 0.f;
+    r[i] = 0.f;
+    if (!((mine >> i) & 1)) continue;  // (the same for the warp)
+    uint32_t u[8];
+    load_row(warp + kWarps * i, u);
+    float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+    float mx = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float v0, v1;
-      unpack2(u[k], v0, v1);
-      ss = fmaf(v0, v0, ss);
-      ss = fmaf(v1, v1, ss);
+    for (int k = 0; k < 8; k += 2) {
+      const float2 v0 = unpack2(u[k]), v1 = unpack2(u[k + 1]);
+      s0 = fma_f32x2(v0, v0, s0);
+      s1 = fma_f32x2(v1, v1, s1);
+      const float2 p0 = mul_f32x2(v0, unpack2(w[k])), p1 = mul_f32x2(v1, unpack2(w[k + 1]));
+      mx = fmaxf(mx, fmaxf(fmaxf(fabsf(p0.x), fabsf(p0.y)), fmaxf(fabsf(p1.x), fabsf(p1.y))));
     }
+    float sum = (s0.x + s1.x) + (s0.y + s1.y);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    rn[i] = 1.0f / sqrtf(ss * (1.0f / kDc) + a.eps);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float v0, v1;
-      unpack2(u[k], v0, v1);
-      amax = fmaxf(amax, fmaxf(fabsf(v0 * rn[i] * w[2 * k]), fabsf(v1 * rn[i] * w[2 * k + 1])));
-    }
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    // one Newton step takes the reciprocal root to about half a rounding
+    const float ms = fmaf(sum, 1.0f / kDc, a.eps), r0 = rsqrtf(ms);
+    r[i] = ms > 0.f && ms < INFINITY ? fmaf(r0 * 0.5f, fmaf(-ms * r0, r0, 1.f), r0) : r0;
+    amax = fmaxf(amax, mx * r[i]);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -133,38 +188,34 @@ __device__ __forceinline__ void write_page(const P8WriteArgs& a, const RopeFreq&
   const float inv = 1.0f / scale;
   const bool grew = old > 0.f && scale > old;
   const float f = grew ? old / scale : 1.f;
-
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    const int64_t slot = page * BS + warp + kWarps * i;
+    const int row = warp + kWarps * i;
+    const int64_t slot = page * BS + row;
     uint8_t* dst = a.cache8 + slot * kRow8;
-    uint4* codes = reinterpret_cast<uint4*>(dst + lane * 16);
-    if (tok[i] < 0) {
-      if (grew) *codes = p8_recode16(*codes, f);
+    if (!((mine >> i) & 1)) {
+      if (grew) {
+        uint4* codes = reinterpret_cast<uint4*>(dst + lane * 16);
+        *codes = p8_recode16(*codes, f);
+      }
       continue;
     }
-    const uint32_t u[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w,
-                           x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
-    uint32_t q[4];
+    uint32_t u[8], q[4];
+    load_row(row, u);
+    const float2 rs = make_float2(r[i] * inv, r[i] * inv);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      float v0, v1, v2, v3;
-      unpack2(u[2 * k], v0, v1);
-      unpack2(u[2 * k + 1], v2, v3);
-      q[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(
-                 make_float2(v0 * rn[i] * w[4 * k] * inv, v1 * rn[i] * w[4 * k + 1] * inv),
-                 __NV_SATFINITE, __NV_E4M3) |
-             ((uint32_t)__nv_cvt_float2_to_fp8x2(
-                  make_float2(v2 * rn[i] * w[4 * k + 2] * inv, v3 * rn[i] * w[4 * k + 3] * inv),
-                  __NV_SATFINITE, __NV_E4M3)
-              << 16);
+      const float2 lo = mul_f32x2(mul_f32x2(unpack2(u[2 * k]), unpack2(w[2 * k])), rs);
+      const float2 hi = mul_f32x2(mul_f32x2(unpack2(u[2 * k + 1]), unpack2(w[2 * k + 1])), rs);
+      q[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3) |
+             ((uint32_t)__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3) << 16);
     }
-    *codes = make_uint4(q[0], q[1], q[2], q[3]);
-    const int i1 = rope_i1(a.interleaved, lane), i2 = rope_i2(a.interleaved, lane);
-    const __nv_bfloat16* kp = a.k_pe + (size_t)tok[i] * kDr;
+    *reinterpret_cast<uint2*>(dst + lane * 8) = make_uint2(q[0], q[1]);
+    *reinterpret_cast<uint2*>(dst + kDc / 2 + lane * 8) = make_uint2(q[2], q[3]);
+    const __nv_bfloat16* kp = reinterpret_cast<const __nv_bfloat16*>(sm + S::k + row * (kDr * 2));
     const float x1 = __bfloat162float(kp[i1]), x2 = __bfloat162float(kp[i2]);
     float cs, sn;
-    rope_cos_sin(a.positions[tok[i]], freq.hi[lane], freq.lo[lane], &cs, &sn);
+    page_cos_sin(pos[i], fhi, flo, &cs, &sn);
     __nv_bfloat16* kr = reinterpret_cast<__nv_bfloat16*>(dst + kDc);
     kr[i1] = __float2bfloat16_rn(x1 * cs - x2 * sn);
     kr[i2] = __float2bfloat16_rn(x2 * cs + x1 * sn);
@@ -173,10 +224,10 @@ __device__ __forceinline__ void write_page(const P8WriteArgs& a, const RopeFreq&
 }
 
 template <int BS>
-__global__ void __launch_bounds__(kThreads) p8_write_scan_kernel(P8WriteArgs a,
-                                                                 const __grid_constant__ RopeFreq freq) {
-  __shared__ int sTok[BS];
-  __shared__ float sMax[kWarps];
+__global__ void __launch_bounds__(kThreads, 3) p8_write_scan_kernel(P8WriteArgs a,
+                                                                    const __grid_constant__ RopeFreq freq) {
+  extern __shared__ __align__(16) uint8_t sm_page[];
+  int* sTok = reinterpret_cast<int*>(sm_page + PageSm<BS>::tok);
   pdl_wait();
   pdl_launch_dependents();
   const int t = blockIdx.x;
@@ -198,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) p8_write_scan_kernel(P8WriteArgs a,
     }
   }
   if (__syncthreads_or(earlier)) return;  // an earlier token's CTA owns the page
-  write_page<BS>(a, freq, page, sTok, sMax);
+  write_page<BS>(a, freq, page, sm_page);
 }
 
 // Numbers the pages that the call's tokens touch: id_of[page] = number + 1.
@@ -238,12 +289,12 @@ __global__ void __launch_bounds__(kThreads) p8_last_token_kernel(P8WriteArgs a, 
 }
 
 template <int BS>
-__global__ void __launch_bounds__(kThreads) p8_write_pages_kernel(P8WriteArgs a,
-                                                                  const __grid_constant__ RopeFreq freq,
-                                                                  const int* count, const int* list,
-                                                                  const int* last) {
-  __shared__ int sTok[BS];
-  __shared__ float sMax[kWarps];
+__global__ void __launch_bounds__(kThreads, 3) p8_write_pages_kernel(P8WriteArgs a,
+                                                                     const __grid_constant__ RopeFreq freq,
+                                                                     const int* count, const int* list,
+                                                                     const int* last) {
+  extern __shared__ __align__(16) uint8_t sm_page[];
+  int* sTok = reinterpret_cast<int*>(sm_page + PageSm<BS>::tok);
   pdl_wait();
   pdl_launch_dependents();
   const int n = *count;
@@ -251,20 +302,25 @@ __global__ void __launch_bounds__(kThreads) p8_write_pages_kernel(P8WriteArgs a,
     __syncthreads();  // the last page's rows and maxima are read
     for (int r = threadIdx.x; r < BS; r += kThreads) sTok[r] = last[(size_t)i * BS + r] - 1;
     __syncthreads();
-    write_page<BS>(a, freq, list[i], sTok, sMax);
+    write_page<BS>(a, freq, list[i], sm_page);
   }
 }
 
 template <int BS>
 cudaError_t write_pages(const P8WriteArgs& a, const RopeFreq& freq, uint8_t* ws, cudaStream_t st) {
+  const int smem = PageSm<BS>::bytes;
+  cudaError_t e = cudaFuncSetAttribute(p8_write_scan_kernel<BS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(p8_write_pages_kernel<BS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
   if (a.num_tokens <= kScanTokens)
-    return launch_pdl(p8_write_scan_kernel<BS>, dim3(a.num_tokens), dim3(kThreads), 0, st, a, freq);
+    return launch_pdl(p8_write_scan_kernel<BS>, dim3(a.num_tokens), dim3(kThreads), smem, st, a, freq);
   const P8WriteWs L = write_ws(a.num_tokens, a.num_blocks, BS);
   int* count = reinterpret_cast<int*>(ws + L.count);
   int* id_of = reinterpret_cast<int*>(ws + L.id_of);
   int* last = reinterpret_cast<int*>(ws + L.last);
   int* list = reinterpret_cast<int*>(ws + L.list);
-  cudaError_t e = cudaMemsetAsync(ws, 0, L.list, st);  // count, id_of and last
+  e = cudaMemsetAsync(ws, 0, L.list, st);  // count, id_of and last
   const dim3 grid((unsigned)((a.num_tokens + kThreads - 1) / kThreads));
   if (e == cudaSuccess)
     e = launch_pdl(p8_number_pages_kernel, grid, dim3(kThreads), 0, st, a, BS, count, id_of, list);
@@ -273,7 +329,7 @@ cudaError_t write_pages(const P8WriteArgs& a, const RopeFreq& freq, uint8_t* ws,
   if (e != cudaSuccess) return e;
   const int64_t pages = a.num_tokens < a.num_blocks ? a.num_tokens : a.num_blocks;
   return launch_pdl(p8_write_pages_kernel<BS>, dim3((unsigned)(pages < 65536 ? pages : 65536)),
-                    dim3(kThreads), 0, st, a, freq, (const int*)count, (const int*)list,
+                    dim3(kThreads), smem, st, a, freq, (const int*)count, (const int*)list,
                     (const int*)last);
 }
 
