@@ -21,6 +21,8 @@
 // neighbours in the page.
 //
 // Bound: HBM, 1,152 bytes read and 640 written per token.
+#include <type_traits>
+
 #include "async_copy.cuh"
 #include "internal.h"
 #include "page8.cuh"
@@ -80,8 +82,8 @@ template <int BS>
 struct PageSm {
   static constexpr int x = 0;                       // [BS][512] bf16
   static constexpr int k = x + BS * kDc * 2;        // [BS][64] bf16
-  static constexpr int tok = k + BS * kDr * 2;      // [BS] token of a row, or -1
-  static constexpr int mx = tok + BS * 4;           // [8] largest magnitude of a warp
+  static constexpr int tok = k + BS * kDr * 2;      // [2][BS] token of a row, or -1
+  static constexpr int mx = tok + 2 * BS * 4;       // [8] largest magnitude of a warp
   static constexpr int bytes = mx + kWarps * 4;
 };
 
@@ -105,123 +107,170 @@ __device__ __forceinline__ void page_cos_sin(int pos, float hi, float lo, float*
   *c = (q + 1) & 2 ? -v : v;
 }
 
-// One page, all threads: tok[r] (shared) is the token of row r, or -1. Warp w
-// has rows w, w + 8, ...: all their bytes are on their way at once (cp.async),
-// and a row is read from shared memory for the norm and again for the codes, so
-// that few registers hold many rows in flight (three CTAs an SM at 64 rows).
+// The pages of one CTA, one after another, all threads. Warp w has rows w,
+// w + 8, ... of a page: all their bytes are on their way at once (cp.async); a
+// row is read from shared memory for the norm and again for the codes, so that
+// few registers hold many rows in flight (three CTAs an SM at 64 rows), and as
+// soon as a row's codes are made its place takes the same row of the next page.
 //   c_hat = (x w) r,  r = 1 / sqrt(mean(x^2) + eps)
 // x w is exact in fp32 (two bf16 factors), so c_hat is one rounding away from
 // r, the largest |c_hat| of a row is r times its largest |x w|, and dividing by
 // the scale is a power of two folded into r. Lane l has elements 8 l ... 8 l + 7
 // and 256 + those.
 template <int BS>
-__device__ __forceinline__ void write_page(const P8WriteArgs& a, const RopeFreq& freq, int64_t page,
-                                           uint8_t* sm) {
+struct PageWriter {
   using S = PageSm<BS>;
-  constexpr int kRows = BS / kWarps;
+  static constexpr int kRows = BS / kWarps;
+  const P8WriteArgs& a;
+  uint8_t* sm;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int* sTok = reinterpret_cast<const int*>(sm + S::tok);
-  float* sMax = reinterpret_cast<float*>(sm + S::mx);
-  const float old = a.scales[page];
-  uint32_t mine = 0;  // bit i: row warp + 8 i has a token
+  uint32_t mine = 0;  // bit i: row warp + 8 i of the page in shared memory has a token
   int pos[kRows];
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
+
+  // Row i of a page from its token list.
+  __device__ __forceinline__ bool fetch(int i, const int* sTok, int& p) {
     const int row = warp + kWarps * i, tok = sTok[row];
-    pos[i] = 0;
-    if (tok < 0) continue;
-    mine |= 1u << i;
+    if (tok < 0) return false;
     const __nv_bfloat16* src = a.c_kv + (size_t)tok * kDc + lane * 8;
     cp_async16(sm + S::x + row * (kDc * 2) + lane * 16, src);
     cp_async16(sm + S::x + row * (kDc * 2) + 512 + lane * 16, src + kDc / 2);
     if (lane < 8) cp_async16(sm + S::k + row * (kDr * 2) + lane * 16, a.k_pe + (size_t)tok * kDr + lane * 8);
-    pos[i] = a.positions[tok];
+    p = a.positions[tok];
+    return true;
   }
-  cp_async_commit();
-  const uint4 w0 = *reinterpret_cast<const uint4*>(a.w + lane * 8);
-  const uint4 w1 = *reinterpret_cast<const uint4*>(a.w + kDc / 2 + lane * 8);
-  const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-  const float fhi = freq.hi[lane], flo = freq.lo[lane];
-  const int i1 = rope_i1(a.interleaved, lane), i2 = rope_i2(a.interleaved, lane);
-  auto load_row = [&](int row, uint32_t (&u)[8]) {
+  __device__ __forceinline__ void fetch_page(const int* sTok) {
+    mine = 0;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) mine |= (uint32_t)fetch(i, sTok, pos[i]) << i;
+    cp_async_commit();
+  }
+  __device__ __forceinline__ void load_row(int row, uint32_t (&u)[8]) const {
     const uint4 x0 = *reinterpret_cast<const uint4*>(sm + S::x + row * (kDc * 2) + lane * 16);
     const uint4 x1 = *reinterpret_cast<const uint4*>(sm + S::x + row * (kDc * 2) + 512 + lane * 16);
     u[0] = x0.x; u[1] = x0.y; u[2] = x0.z; u[3] = x0.w;
     u[4] = x1.x; u[5] = x1.y; u[6] = x1.z; u[7] = x1.w;
-  };
-  cp_async_wait_all();
-  __syncwarp();
-  float r[kRows], amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    r[i] = 0.f;
-    if (!((mine >> i) & 1)) continue;  // (the same for the warp)
-    uint32_t u[8];
-    load_row(warp + kWarps * i, u);
-    float2 s0 = make_float2(0.f, 0.f), s1 = s0;
-    float mx = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; k += 2) {
-      const float2 v0 = unpack2(u[k]), v1 = unpack2(u[k + 1]);
-      s0 = fma_f32x2(v0, v0, s0);
-      s1 = fma_f32x2(v1, v1, s1);
-      const float2 p0 = mul_f32x2(v0, unpack2(w[k])), p1 = mul_f32x2(v1, unpack2(w[k + 1]));
-      mx = fmaxf(mx, fmaxf(fmaxf(fabsf(p0.x), fabsf(p0.y)), fmaxf(fabsf(p1.x), fabsf(p1.y))));
-    }
-    float sum = (s0.x + s1.x) + (s0.y + s1.y);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    // one Newton step takes the reciprocal root to about half a rounding
-    const float ms = fmaf(sum, 1.0f / kDc, a.eps), r0 = rsqrtf(ms);
-    r[i] = ms > 0.f && ms < INFINITY ? fmaf(r0 * 0.5f, fmaf(-ms * r0, r0, 1.f), r0) : r0;
-    amax = fmaxf(amax, mx * r[i]);
   }
+
+  // Writes `page`, whose rows were fetched. nextTok: the token list of the page
+  // to fetch meanwhile, complete at the barrier inside (after publish(), which
+  // every thread calls before it), or NULL.
+  template <typename F>
+  __device__ __forceinline__ void write(const RopeFreq& freq, int64_t page, const int* nextTok, F publish) {
+    float* sMax = reinterpret_cast<float*>(sm + S::mx);
+    const float old = a.scales[page];
+    const uint4 w0 = __ldg(reinterpret_cast<const uint4*>(a.w + lane * 8));
+    const uint4 w1 = __ldg(reinterpret_cast<const uint4*>(a.w + kDc / 2 + lane * 8));
+    const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+    cp_async_wait_all();
+    __syncwarp();
+    // (a row without a token reads what is there, and its results are dropped:
+    // without branches the rows' latencies overlap)
+    float r[kRows], mx[kRows], amax = 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if (lane == 0) sMax[warp] = amax;
-  __syncthreads();
-  amax = sMax[0];
+    for (int i = 0; i < kRows; ++i) {
+      uint32_t u[8];
+      load_row(warp + kWarps * i, u);
+      float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+      float m = 0.f;
 #pragma unroll
-  for (int k = 1; k < kWarps; ++k) amax = fmaxf(amax, sMax[k]);
-  const float scale = fmaxf(old, p8_scale_for(amax));
-  if (threadIdx.x == 0 && scale != old) a.scales[page] = scale;
-  const float inv = 1.0f / scale;
-  const bool grew = old > 0.f && scale > old;
-  const float f = grew ? old / scale : 1.f;
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int row = warp + kWarps * i;
-    const int64_t slot = page * BS + row;
-    uint8_t* dst = a.cache8 + slot * kRow8;
-    if (!((mine >> i) & 1)) {
-      if (grew) {
-        uint4* codes = reinterpret_cast<uint4*>(dst + lane * 16);
-        *codes = p8_recode16(*codes, f);
+      for (int k = 0; k < 8; k += 2) {
+        const float2 v0 = unpack2(u[k]), v1 = unpack2(u[k + 1]);
+        s0 = fma_f32x2(v0, v0, s0);
+        s1 = fma_f32x2(v1, v1, s1);
+        const float2 p0 = mul_f32x2(v0, unpack2(w[k])), p1 = mul_f32x2(v1, unpack2(w[k + 1]));
+        m = fmaxf(m, fmaxf(fmaxf(fabsf(p0.x), fabsf(p0.y)), fmaxf(fabsf(p1.x), fabsf(p1.y))));
       }
-      continue;
+      mx[i] = m;
+      r[i] = (s0.x + s1.x) + (s0.y + s1.y);
     }
-    uint32_t u[8], q[4];
-    load_row(row, u);
-    const float2 rs = make_float2(r[i] * inv, r[i] * inv);
+    // the rows' sums over the warp: every exchange halves the rows a lane holds,
+    // so the lanes of (bits 4, 3, 2 of the lane) end with one row's sum each
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 lo = mul_f32x2(mul_f32x2(unpack2(u[2 * k]), unpack2(w[2 * k])), rs);
-      const float2 hi = mul_f32x2(mul_f32x2(unpack2(u[2 * k + 1]), unpack2(w[2 * k + 1])), rs);
-      q[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3) |
-             ((uint32_t)__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3) << 16);
+    for (int h = kRows / 2, o = 16; h > 0; h >>= 1, o >>= 1) {
+      const bool up = lane & o;
+#pragma unroll
+      for (int j = 0; j < h; ++j) {
+        const float send = up ? r[j] : r[j + h], keep = up ? r[j + h] : r[j];
+        r[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+      }
     }
-    *reinterpret_cast<uint2*>(dst + lane * 8) = make_uint2(q[0], q[1]);
-    *reinterpret_cast<uint2*>(dst + kDc / 2 + lane * 8) = make_uint2(q[2], q[3]);
-    const __nv_bfloat16* kp = reinterpret_cast<const __nv_bfloat16*>(sm + S::k + row * (kDr * 2));
-    const float x1 = __bfloat162float(kp[i1]), x2 = __bfloat162float(kp[i2]);
-    float cs, sn;
-    page_cos_sin(pos[i], fhi, flo, &cs, &sn);
-    __nv_bfloat16* kr = reinterpret_cast<__nv_bfloat16*>(dst + kDc);
-    kr[i1] = __float2bfloat16_rn(x1 * cs - x2 * sn);
-    kr[i2] = __float2bfloat16_rn(x2 * cs + x1 * sn);
-    if (a.mass && lane == 0) a.mass[slot] = 0.f;
+#pragma unroll
+    for (int o = 16 / kRows; o > 0; o >>= 1) r[0] += __shfl_xor_sync(0xffffffffu, r[0], o);
+    // one Newton step takes the reciprocal root to about half a rounding
+    const float ms = fmaf(r[0], 1.0f / kDc, a.eps), r0 = rsqrtf(ms);
+    const float root = ms > 0.f && ms < INFINITY ? fmaf(r0 * 0.5f, fmaf(-ms * r0, r0, 1.f), r0) : r0;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      r[i] = __shfl_sync(0xffffffffu, root, i * (32 / kRows));
+      amax = fmaxf(amax, (mine >> i) & 1 ? mx[i] * r[i] : 0.f);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if (lane == 0) sMax[warp] = amax;
+    publish();
+    __syncthreads();
+    amax = sMax[0];
+#pragma unroll
+    for (int k = 1; k < kWarps; ++k) amax = fmaxf(amax, sMax[k]);
+    const float scale = fmaxf(old, p8_scale_for(amax));
+    if (threadIdx.x == 0 && scale != old) a.scales[page] = scale;
+    const float inv = 1.0f / scale;
+    const bool grew = old > 0.f && scale > old;
+    const float f = grew ? old / scale : 1.f;
+    const float fhi = freq.hi[lane], flo = freq.lo[lane];
+    const int i1 = rope_i1(a.interleaved, lane), i2 = rope_i2(a.interleaved, lane);
+    uint32_t next = 0;
+    // (the page whose every row is written has no branches but the copies')
+    auto rows = [&](auto all) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int row = warp + kWarps * i;
+        const int64_t slot = page * BS + row;
+        uint8_t* dst = a.cache8 + slot * kRow8;
+        const bool has = decltype(all)::value || ((mine >> i) & 1);
+        uint32_t u[8];
+        load_row(row, u);
+        const __nv_bfloat16* kp = reinterpret_cast<const __nv_bfloat16*>(sm + S::k + row * (kDr * 2));
+        const float x1 = __bfloat162float(kp[i1]), x2 = __bfloat162float(kp[i2]);
+        const int p = pos[i];
+        if (nextTok) {
+          __syncwarp();  // every lane has the row in registers
+          next |= (uint32_t)fetch(i, nextTok, pos[i]) << i;
+        }
+        if (!has) {
+          if (grew) {
+            uint4* codes = reinterpret_cast<uint4*>(dst + lane * 16);
+            *codes = p8_recode16(*codes, f);
+          }
+          continue;
+        }
+        const float2 rs = make_float2(r[i] * inv, r[i] * inv);
+        uint32_t q[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 lo = mul_f32x2(mul_f32x2(unpack2(u[2 * k]), unpack2(w[2 * k])), rs);
+          const float2 hi = mul_f32x2(mul_f32x2(unpack2(u[2 * k + 1]), unpack2(w[2 * k + 1])), rs);
+          q[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3) |
+                 ((uint32_t)__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3) << 16);
+        }
+        *reinterpret_cast<uint2*>(dst + lane * 8) = make_uint2(q[0], q[1]);
+        *reinterpret_cast<uint2*>(dst + kDc / 2 + lane * 8) = make_uint2(q[2], q[3]);
+        float cs, sn;
+        page_cos_sin(p, fhi, flo, &cs, &sn);
+        __nv_bfloat16* kr = reinterpret_cast<__nv_bfloat16*>(dst + kDc);
+        kr[i1] = __float2bfloat16_rn(x1 * cs - x2 * sn);
+        kr[i2] = __float2bfloat16_rn(x2 * cs + x1 * sn);
+        if (a.mass && lane == 0) a.mass[slot] = 0.f;
+      }
+    };
+    if (mine == (1u << kRows) - 1)
+      rows(std::true_type{});
+    else
+      rows(std::false_type{});
+    cp_async_commit();
+    mine = next;
   }
-}
+};
 
 template <int BS>
 __global__ void __launch_bounds__(kThreads, 3) p8_write_scan_kernel(P8WriteArgs a,
@@ -249,7 +298,9 @@ __global__ void __launch_bounds__(kThreads, 3) p8_write_scan_kernel(P8WriteArgs 
     }
   }
   if (__syncthreads_or(earlier)) return;  // an earlier token's CTA owns the page
-  write_page<BS>(a, freq, page, sm_page);
+  PageWriter<BS> pw{a, sm_page};
+  pw.fetch_page(sTok);
+  pw.write(freq, page, nullptr, [] {});
 }
 
 // Numbers the pages that the call's tokens touch: id_of[page] = number + 1.
@@ -297,13 +348,36 @@ __global__ void __launch_bounds__(kThreads, 3) p8_write_pages_kernel(P8WriteArgs
   int* sTok = reinterpret_cast<int*>(sm_page + PageSm<BS>::tok);
   pdl_wait();
   pdl_launch_dependents();
-  const int n = *count;
-  for (int i = blockIdx.x; i < n; i += gridDim.x) {
-    __syncthreads();  // the last page's rows and maxima are read
-    for (int r = threadIdx.x; r < BS; r += kThreads) sTok[r] = last[(size_t)i * BS + r] - 1;
-    __syncthreads();
-    write_page<BS>(a, freq, list[i], sm_page);
+  const int n = *count, r = threadIdx.x;
+  int i = blockIdx.x;
+  if (i >= n) return;
+  // token lists are fetched two pages ahead, rows one page ahead
+  int page = list[i];
+  if (r < BS) sTok[r] = last[(size_t)i * BS + r] - 1;
+  __syncthreads();
+  PageWriter<BS> pw{a, sm_page};
+  pw.fetch_page(sTok);
+  for (int buf = 1; i < n; i += gridDim.x, buf ^= 1) {
+    const int next = i + gridDim.x;
+    int next_page = 0, next_tok = 0;
+    if (next < n) {
+      next_page = list[next];
+      if (r < BS) next_tok = last[(size_t)next * BS + r] - 1;
+    }
+    pw.write(freq, page, next < n ? sTok + buf * BS : nullptr, [&] {
+      if (next < n && r < BS) sTok[buf * BS + r] = next_tok;
+    });
+    __syncthreads();  // the maxima are read
+    page = next_page;
   }
+}
+
+int device_sms() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+    return 1;
+  return sms;
 }
 
 template <int BS>
@@ -328,7 +402,8 @@ cudaError_t write_pages(const P8WriteArgs& a, const RopeFreq& freq, uint8_t* ws,
     e = launch_pdl(p8_last_token_kernel, grid, dim3(kThreads), 0, st, a, BS, (const int*)id_of, last);
   if (e != cudaSuccess) return e;
   const int64_t pages = a.num_tokens < a.num_blocks ? a.num_tokens : a.num_blocks;
-  return launch_pdl(p8_write_pages_kernel<BS>, dim3((unsigned)(pages < 65536 ? pages : 65536)),
+  const int64_t most = (int64_t)device_sms() * 3;  // as many CTAs as run at once
+  return launch_pdl(p8_write_pages_kernel<BS>, dim3((unsigned)(pages < most ? pages : most)),
                     dim3(kThreads), smem, st, a, freq, (const int*)count, (const int*)list,
                     (const int*)last);
 }
