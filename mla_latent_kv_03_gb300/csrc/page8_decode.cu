@@ -161,7 +161,7 @@ struct Sm {
   static constexpr int rows = scale + 64;               // [self_rows] int4
   static constexpr int bars = rows + self_rows * 16;
   static constexpr int misc = bars + 24 * 8;            // TMEM base, abort flag, merge flag
-  static constexpr int bytes = misc + 16;
+  static constexpr int bytes = misc + 16;               // ... and the plan's units
   static constexpr int alloc = bytes + 1024;
   static_assert(alloc <= 227 * 1024, "shared memory budget");
   static_assert(q % 1024 == 0 && q_rope % 1024 == 0 && q_bytes % 1024 == 0 && p % 128 == 0, "swizzle atoms");
@@ -358,6 +358,68 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
+// The split plan of plan_kernel for at most S::self_rows rows, derived in shared
+// memory by every CTA. rows[] must be zero; between that and the call, and
+// around it, all threads pass a barrier. Sequences that are not valid own no
+// tiles (CTA 0 reports them). Returns the number of units.
+__device__ __forceinline__ void plan_rows(const P8Args& a, int4* rows, uint32_t* status, int tid, int nthreads) {
+  const int64_t max_len = (int64_t)a.max_blocks * a.block_size;
+  for (int b = tid; b < a.batch; b += nthreads) {
+    const int len = a.seq_lens[b];
+    const int q0 = a.query_start_loc[b], q1 = a.query_start_loc[b + 1];
+    const int ql = q1 - q0;
+    if (q0 < 0 || q1 > a.num_q || ql < 0) {
+      if (blockIdx.x == 0) set_status(status, MLA_DEV_BAD_SEQ);
+      continue;
+    }
+    const bool bad = ql > len || len < 0 || (int64_t)len > max_len;
+    if (bad && ql > 0 && blockIdx.x == 0) set_status(status, MLA_DEV_BAD_SEQ);
+    for (int j = 0; j < ql; ++j) {
+      const int pos = len - ql + j;
+      rows[q0 + j] = make_int4(b, pos, bad ? 0 : (pos + kTile) / kTile, 0);
+    }
+  }
+}
+// The rows' first units, by one warp.
+__device__ __forceinline__ void scan_rows(int4* rows, int num_q, int lane, int* total) {
+  int run = 0;
+  for (int c = 0; c < num_q; c += 32) {
+    const int v = c + lane < num_q ? rows[c + lane].z : 0;
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    if (c + lane < num_q) rows[c + lane].w = run + incl - v;
+    run += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (lane == 0) *total = run;
+}
+// Where share `c` begins: a walker over the rows (each warp for itself).
+__device__ __forceinline__ bool start_share(SchedWalker& sw, const int4* rows, int num_q, int total,
+                                            int shares, int c, int lane) {
+  sw.row_info = rows;
+  sw.plan_ok = true;
+  sw.G = 1;
+  sw.g = 0;
+  sw.share = total > 0 ? (total + shares - 1) / shares : 1;
+  sw.u = c * sw.share;
+  sw.u_end = min(sw.u + sw.share, total);
+  if (sw.u >= sw.u_end) return false;
+  for (int r = 0; r < num_q; r += 32) {
+    const int4 ri = r + lane < num_q ? rows[r + lane] : make_int4(0, 0, 0, 0);
+    const uint32_t hit = __ballot_sync(0xffffffffu, ri.z > 0 && ri.w <= sw.u && sw.u < ri.w + ri.z);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      sw.n = r + l;
+      sw.k = sw.u - __shfl_sync(0xffffffffu, ri.w, l);
+      return true;
+    }
+  }
+  return false;
+}
+
 template <int NH>
 __global__ void __launch_bounds__(kThreads, 1)
     page8_decode_kernel(const __grid_constant__ CUtensorMap codes_map,
@@ -381,11 +443,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int bs = a.block_size;
   const int bs_shift = bs == 16 ? 4 : (bs == 32 ? 5 : 6);
 
-  // (the split's inputs on their way to L1 during the set-up)
-  if (a.self_plan && tid < a.batch) {
-    asm volatile("prefetch.global.L1 [%0];" ::"l"(a.seq_lens + tid));
-    asm volatile("prefetch.global.L1 [%0];" ::"l"(a.query_start_loc + tid + 1));
-  }
+  int4* plan = reinterpret_cast<int4*>(sm + S::rows);
+  int* plan_total = reinterpret_cast<int*>(sm + S::misc + 12);
+  if (a.self_plan)
+    for (int n = tid; n < (int)a.num_q; n += kThreads) plan[n] = make_int4(-1, -1, 0, 0);
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       const int n = (i == kSFree || i == kPFull || i == kPFull + 1 || i == kOFree) ? kSoftThreads / 32
@@ -409,13 +470,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // have to wait.
   SchedWalker sw;
   bool has_work;
-  int total = 0;
   if (a.self_plan) {
-    int4* rows = reinterpret_cast<int4*>(sm + S::rows);
-    total = self_plan<kThreads>(a.seq_lens, a.query_start_loc, a.batch, (int)a.num_q, 1,
-                                (int64_t)a.max_blocks * bs, rows, reinterpret_cast<int*>(sm + S::red),
-                                status, tid);
-    has_work = sw.init_rows(rows, (int)a.num_q, 1, total, a.shares, share);
+    plan_rows(a, plan, status, tid, kThreads);
+    __syncthreads();
+    if (warp == 0) scan_rows(plan, (int)a.num_q, lane, plan_total);
+    __syncthreads();
+    has_work = start_share(sw, plan, (int)a.num_q, *plan_total, a.shares, share, lane);
   } else {
     pdl_wait();
     has_work = sw.init(a.ws, a.num_q, 1, a.shares, share);
@@ -433,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         hdr->magic = kMagic;
         hdr->mode = 0;
         hdr->qblocks = 0;
-        hdr->total_units = total;
+        hdr->total_units = *plan_total;
         hdr->share = sw.share;
         hdr->num_ctas = a.shares;
         hdr->groups = 1;
@@ -753,14 +813,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (t > 0 && any) {   // the same for every thread of the half
             tc::fence_after_sync();
 #pragma unroll 1
-            for (int c = 0; c < 12; ++c) {
-              float o[HT];
-              const uint32_t at = trow + kOCol + (uint32_t)(c * NH + h0);
-              tmem_ld(at, o);
+            for (int j = 0; j < 4; ++j) {
+              float o[3][HT];
+              const uint32_t at = trow + kOCol + (uint32_t)(j * 3 * NH + h0);
+#pragma unroll
+              for (int c = 0; c < 3; ++c) tmem_ld(at + c * NH, o[c]);
               tc::wait_ld();
 #pragma unroll
-              for (int k = 0; k < HT; ++k) o[k] *= f[k];
-              tmem_st(at, o);
+              for (int c = 0; c < 3; ++c) {
+#pragma unroll
+                for (int k = 0; k < HT; ++k) o[c][k] *= f[k];
+                tmem_st(at + c * NH, o[c]);
+              }
             }
             tc::wait_st();
           }
@@ -1001,26 +1065,42 @@ __global__ void __launch_bounds__(512) page8_merge_kernel(const __grid_constant_
   }
 }
 
-// The merge of a few parts for up to 16 rows and the output projection in one:
-// CTA = (16 rows, 64 output columns, head h). Its slice of W_uv (64 KB) comes
-// by cp.async while 16 threads a row merge the row's 512 latents to bf16 (as
-// the other projections take theirs); then 8 warps, each a quarter of K and 32
-// of the columns (m16n8k16), whose sums meet in shared memory.
-constexpr int kMpStride = kDc * 2 + 16;  // bytes of a merged row, padded against bank conflicts
-constexpr int kMpW = 0, kMpA = kDc * 128, kMpRed = kMpA + 16 * kMpStride, kMpRows = kMpRed + 4 * 16 * 64 * 4, kMpSmem = kMpRows + kSelfMaxRows * 16;
+// The merge of a few parts and the output projection in one: CTA = (ROWS rows,
+// head h). W_uv[h] (128 KB) comes by cp.async while 256 / ROWS threads a row
+// merge its 512 latents to bf16 (as the other projections take theirs); then 8
+// warps, each a quarter of K and half of the columns (m16n8k16), whose sums meet
+// in shared memory. Every part is read once. ROWS = 8 (half of the mma's rows
+// idle) where that still leaves at most one CTA an SM: the merge, at latency, is
+// what takes the time.
+template <int ROWS>
+struct Mp {
+  static constexpr int stride = kDc * 2 + 16;     // bytes of a merged row, padded against bank conflicts
+  static constexpr int w = 0;                     // two halves of 64 columns, 128-byte rows
+  static constexpr int a = w + kDc * 256;
+  static constexpr int red = a + ROWS * stride;   // [4][ROWS][128]
+  static constexpr int rows = red + 4 * ROWS * kDv * 4;
+  static constexpr int bytes = rows + kSelfMaxRows * 16 + 16;
+};
+template <int ROWS>
 __global__ void __launch_bounds__(256) page8_merge_proj_kernel(const __grid_constant__ P8Args a,
                                                                const __nv_bfloat16* W_uv,
                                                                __nv_bfloat16* out) {
+  using M = Mp<ROWS>;
+  constexpr int kTr = 256 / ROWS, kVec = kDc / 4 / kTr, kBatch = 16 / kVec;  // threads, float4s, parts at a time
   extern __shared__ __align__(1024) uint8_t smem_mp[];
-  uint8_t* sW = smem_mp + kMpW;
-  uint8_t* sA = smem_mp + kMpA;
-  float* sRed = reinterpret_cast<float*>(smem_mp + kMpRed);
+  float* sRed = reinterpret_cast<float*>(smem_mp + M::red);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.z, row0 = blockIdx.x * 16, col0 = blockIdx.y * 64, H = a.num_heads;
-  const __nv_bfloat16* src = W_uv + (size_t)h * kDc * kDv + col0;
+  const int h = blockIdx.y, row0 = blockIdx.x * ROWS, H = a.num_heads;
+  int4* plan = reinterpret_cast<int4*>(smem_mp + M::rows);
+  int* plan_total = reinterpret_cast<int*>(smem_mp + M::rows + kSelfMaxRows * 16);
+  if (a.self_plan)
+    for (int n = tid; n < (int)a.num_q; n += 256) plan[n] = make_int4(-1, -1, 0, 0);
+  const __nv_bfloat16* src = W_uv + (size_t)h * kDc * kDv;
 #pragma unroll 4
-  for (int i = tid; i < kDc * 8; i += 256)
-    cp_async16(sW + sw128(i >> 3, i & 7), src + (size_t)(i >> 3) * kDv + (i & 7) * 8);
+  for (int i = tid; i < kDc * 16; i += 256) {
+    const int k = i >> 4, c = i & 15;
+    cp_async16(smem_mp + M::w + (c >> 3) * (kDc * 128) + sw128(k, c & 7), src + (size_t)k * kDv + c * 8);
+  }
   cp_async_commit();
   // The weights do not depend on earlier kernels, and where the parts lie is
   // known from the lengths (the split of the decode, derived again); the parts
@@ -1028,12 +1108,13 @@ __global__ void __launch_bounds__(256) page8_merge_proj_kernel(const __grid_cons
   const int4* rows = reinterpret_cast<const int4*>(a.ws + ws_layout(a.num_q, 1, a.shares).row_info);
   int share = 1;
   if (a.self_plan) {
-    int4* mine = reinterpret_cast<int4*>(smem_mp + kMpRows);
-    const int total = self_plan<256>(a.seq_lens, a.query_start_loc, a.batch, (int)a.num_q, 1,
-                                     (int64_t)a.max_blocks * a.block_size, mine,
-                                     reinterpret_cast<int*>(sRed), nullptr, tid);
-    share = total > 0 ? (total + a.shares - 1) / a.shares : 1;
-    rows = mine;
+    __syncthreads();
+    plan_rows(a, plan, nullptr, tid, 256);
+    __syncthreads();
+    if (warp == 0) scan_rows(plan, (int)a.num_q, lane, plan_total);
+    __syncthreads();
+    share = *plan_total > 0 ? (*plan_total + a.shares - 1) / a.shares : 1;
+    rows = plan;
     pdl_wait();
   } else {
     pdl_wait();
@@ -1041,87 +1122,89 @@ __global__ void __launch_bounds__(256) page8_merge_proj_kernel(const __grid_cons
   }
   pdl_launch_dependents();
   {
-    const int r = tid >> 4, j = tid & 15, n = row0 + r;
+    const int r = tid / kTr, j = tid % kTr, n = row0 + r;
     HeadParts hp{a.lse_first, a.o_first, 0};
     if (n < a.num_q) hp = head_parts(a, rows, share, n, h);
-    float m, den;
-    merge_weights<16>(hp, j, m, den);
-    const float inv = den == 0.f ? 0.f : 1.f / den, b = m == -INFINITY ? 0.f : m;
-    if (blockIdx.y == 0 && j == 0 && n < a.num_q)
-      a.lse[(size_t)n * H + h] = den == 0.f ? -INFINITY : m + log2f(den);
-    float4 acc[8];
+    float4 v[kBatch][kVec];
+    auto load = [&](int s0) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-    for (int s = 0; s < hp.count; s += 2) {
-      const bool two = s + 1 < hp.count;
-      const float* p0 = hp.o + (size_t)s * kHG * kDc + 4 * j;
-      const float* p1 = two ? p0 + kHG * kDc : p0;
-      float4 v0[8], v1[8];
+      for (int u = 0; u < kBatch; ++u)
+        if (s0 + u < hp.count) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        v0[k] = *reinterpret_cast<const float4*>(p0 + 64 * k);
-        v1[k] = *reinterpret_cast<const float4*>(p1 + 64 * k);
-      }
-      const float w0 = fast_exp2(hp.lse[s * kHG] - b) * inv;
-      const float w1 = two ? fast_exp2(hp.lse[(s + 1) * kHG] - b) * inv : 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        acc[k].x = fmaf(w0, v0[k].x, acc[k].x);
-        acc[k].y = fmaf(w0, v0[k].y, acc[k].y);
-        acc[k].z = fmaf(w0, v0[k].z, acc[k].z);
-        acc[k].w = fmaf(w0, v0[k].w, acc[k].w);
-        if (two) {
-          acc[k].x = fmaf(w1, v1[k].x, acc[k].x);
-          acc[k].y = fmaf(w1, v1[k].y, acc[k].y);
-          acc[k].z = fmaf(w1, v1[k].z, acc[k].z);
-          acc[k].w = fmaf(w1, v1[k].w, acc[k].w);
+          for (int k = 0; k < kVec; ++k)
+            v[u][k] = *reinterpret_cast<const float4*>(hp.o + (size_t)(s0 + u) * kHG * kDc + 4 * (j + kTr * k));
         }
-      }
+    };
+    load(0);  // on their way while the weights are found
+    float m, den;
+    merge_weights<kTr>(hp, j, m, den);
+    const float inv = den == 0.f ? 0.f : 1.f / den, b = m == -INFINITY ? 0.f : m;
+    if (j == 0 && n < a.num_q) a.lse[(size_t)n * H + h] = den == 0.f ? -INFINITY : m + log2f(den);
+    float4 acc[kVec];
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int s0 = 0; s0 < hp.count; s0 += kBatch) {
+      if (s0 > 0) load(s0);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (s0 + u < hp.count) {
+          const float w = fast_exp2(hp.lse[(s0 + u) * kHG] - b) * inv;
+#pragma unroll
+          for (int k = 0; k < kVec; ++k) {
+            acc[k].x = fmaf(w, v[u][k].x, acc[k].x);
+            acc[k].y = fmaf(w, v[u][k].y, acc[k].y);
+            acc[k].z = fmaf(w, v[u][k].z, acc[k].z);
+            acc[k].w = fmaf(w, v[u][k].w, acc[k].w);
+          }
+        }
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      *reinterpret_cast<uint2*>(sA + r * kMpStride + (j + 16 * k) * 8) =
+    for (int k = 0; k < kVec; ++k)
+      *reinterpret_cast<uint2*>(smem_mp + M::a + r * M::stride + (j + kTr * k) * 8) =
           make_uint2(pack_bf16(acc[k].x, acc[k].y), pack_bf16(acc[k].z, acc[k].w));
   }
   cp_async_wait_all();
   __syncthreads();
   const int g = lane >> 2, q = lane & 3, kq = warp >> 1, nh = warp & 1;
-  float acc[4][4];
+  const uint8_t* sW = smem_mp + M::w + nh * (kDc * 128);
+  float acc[8][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+  for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 #pragma unroll
   for (int ks = 0; ks < 8; ++ks) {
     const int k = kq * 128 + ks * 16;
-    const uint8_t* lo = sA + g * kMpStride + (k + 2 * q) * 2;
-    const uint8_t* hi = lo + 8 * kMpStride;
-    const uint32_t a0 = *reinterpret_cast<const uint32_t*>(lo), a1 = *reinterpret_cast<const uint32_t*>(hi);
-    const uint32_t a2 = *reinterpret_cast<const uint32_t*>(lo + 16), a3 = *reinterpret_cast<const uint32_t*>(hi + 16);
+    const uint8_t* lo = smem_mp + M::a + g * M::stride + (k + 2 * q) * 2;
+    const uint32_t a0 = *reinterpret_cast<const uint32_t*>(lo), a2 = *reinterpret_cast<const uint32_t*>(lo + 16);
+    const uint32_t a1 = ROWS == 16 ? *reinterpret_cast<const uint32_t*>(lo + 8 * M::stride) : 0u;
+    const uint32_t a3 = ROWS == 16 ? *reinterpret_cast<const uint32_t*>(lo + 8 * M::stride + 16) : 0u;
     const int kr = k + (lane & 7) + (((lane >> 3) & 1) << 3);
 #pragma unroll
-    for (int np = 0; np < 2; ++np) {
+    for (int np = 0; np < 4; ++np) {
       uint32_t b0, b1, b2, b3;
-      ldsm_x4_t(smem_u32(sW + sw128(kr, nh * 4 + np * 2 + (lane >> 4))), b0, b1, b2, b3);
+      ldsm_x4_t(smem_u32(sW + sw128(kr, np * 2 + (lane >> 4))), b0, b1, b2, b3);
       mma_16816(acc[2 * np], a0, a1, a2, a3, b0, b1);
       mma_16816(acc[2 * np + 1], a0, a1, a2, a3, b2, b3);
     }
   }
 #pragma unroll
-  for (int nt = 0; nt < 4; ++nt) {
-    float* d = sRed + (kq * 16 + g) * 64 + nh * 32 + nt * 8 + 2 * q;
+  for (int nt = 0; nt < 8; ++nt) {
+    float* d = sRed + (kq * ROWS + g) * kDv + nh * 64 + nt * 8 + 2 * q;
     *reinterpret_cast<float2*>(d) = make_float2(acc[nt][0], acc[nt][1]);
-    *reinterpret_cast<float2*>(d + 8 * 64) = make_float2(acc[nt][2], acc[nt][3]);
+    if (ROWS == 16) *reinterpret_cast<float2*>(d + 8 * kDv) = make_float2(acc[nt][2], acc[nt][3]);
   }
   __syncthreads();
-  const int r = tid >> 4, c = (tid & 15) * 4, row = row0 + r;
-  if (row < a.num_q) {
+#pragma unroll
+  for (int i = tid; i < ROWS * kDv / 4; i += 256) {
+    const int r = i / (kDv / 4), c = (i % (kDv / 4)) * 4, row = row0 + r;
+    if (row >= a.num_q) continue;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float4 x = *reinterpret_cast<const float4*>(sRed + (k * 16 + r) * 64 + c);
+      const float4 x = *reinterpret_cast<const float4*>(sRed + (k * ROWS + r) * kDv + c);
       v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
     }
-    *reinterpret_cast<uint2*>(out + ((size_t)row * H + h) * kDv + col0 + c) =
+    *reinterpret_cast<uint2*>(out + ((size_t)row * H + h) * kDv + c) =
         make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
   }
 }
@@ -1255,10 +1338,15 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
   if (e == cudaSuccess && many_parts)
     e = launch_pdl(page8_merge_kernel, dim3((unsigned)(num_q * H)), dim3(512), 0, st, a);
   if (e == cudaSuccess && merge_proj) {
-    e = cudaFuncSetAttribute(page8_merge_proj_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMpSmem);
-    if (e == cudaSuccess)
-      e = launch_pdl(page8_merge_proj_kernel, dim3((unsigned)((num_q + 15) / 16), kDv / 64, H), dim3(256),
-                     kMpSmem, st, a, (const __nv_bfloat16*)W_uv, (__nv_bfloat16*)out);
+    auto project = [&](auto kernel, int rows, int smem) {
+      const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      return r != cudaSuccess ? r
+                              : launch_pdl(kernel, dim3((unsigned)((num_q + rows - 1) / rows), H), dim3(256), smem,
+                                           st, a, (const __nv_bfloat16*)W_uv, (__nv_bfloat16*)out);
+    };
+    e = (num_q + 7) / 8 * H <= (int64_t)shares * a.groups
+            ? project(page8_merge_proj_kernel<8>, 8, Mp<8>::bytes)
+            : project(page8_merge_proj_kernel<16>, 16, Mp<16>::bytes);
   }
   if (e != cudaSuccess) return MLA_ERR_CUDA;
   if (with_mass) {
