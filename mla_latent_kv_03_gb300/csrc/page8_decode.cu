@@ -155,7 +155,8 @@ struct Sm {
   static constexpr int red = coef + QB * NH * 4;         // [8 warps][NH / 2]
   static constexpr int merge = red + 8 * (NH / 2) * 4;  // merge scratch, one per half
   static constexpr int merge_bytes = (2 * kHG + kMergeChunk * kHG) * 4;
-  static constexpr int info = merge + 2 * merge_bytes;  // [2] live rows of a stage
+  static constexpr int votes = merge + 2 * merge_bytes; // [2 tiles][2 halves][4 warps] heads that outgrow
+  static constexpr int info = votes + 64;               // [2] live rows of a stage
   static constexpr int scale = info + 16;               // [2][8] page scales of a stage, -1: no page
   static constexpr int self_rows = NH == 16 ? kSelfMaxRows : 128;  // rows of a self-planned launch
   static constexpr int rows = scale + 64;               // [self_rows] int4
@@ -199,7 +200,7 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, 
       : "memory");
 }
 
-// Lane l reads (writes) N consecutive 32-bit columns of TMEM lane (base + l).
+// Lane l reads N consecutive 32-bit columns of TMEM lane (base + l).
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&r)[N]) {
   static_assert(N == 8 || N == 16, "shapes in use");
@@ -218,20 +219,11 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&r)[N]) {
         : "r"(taddr));
   }
 }
-template <int N>
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&r)[N]) {
-  if constexpr (N == 8) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
-                 "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
-                 : "memory");
-  } else {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]),
-        "f"(r[8]), "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15])
-        : "memory");
-  }
+__device__ __forceinline__ void tmem_ld1(uint32_t taddr, float& r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=f"(r) : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, float r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "f"(r) : "memory");
 }
 
 // Bounded wait that also gives up when another role has aborted.
@@ -302,25 +294,26 @@ __device__ __forceinline__ void query_terms(const uint32_t* u, float f, uint4& t
 // The query of one (row, column group) as the decode's operand: for each head
 // its two e4m3 terms (rows h and NH + h of four 128-byte slabs) and its bf16
 // rope values, swizzled as shared memory holds them, and the factor that
-// undoes the head's scale. 8 threads a head, 64 latent columns each.
+// undoes the head's scale. 16 threads a head, 32 latent columns each.
 template <int NH>
-__global__ void __launch_bounds__(NH * 8) page8_query_kernel(const uint16_t* q_abs,
+__global__ void __launch_bounds__(NH * 16) page8_query_kernel(const uint16_t* q_abs,
                                                              float scale_log2, uint8_t* q8,
                                                              float* coef, int* arrive) {
   using S = Sm<NH>;
   pdl_wait();
   pdl_launch_dependents();
-  const int h = threadIdx.x >> 3, part = threadIdx.x & 7;
+  const int h = threadIdx.x >> 4, part = threadIdx.x & 15;
   const size_t row = (size_t)blockIdx.x * NH + h;   // (row n, head) in order
   const uint4* src = reinterpret_cast<const uint4*>(q_abs + row * kRow);
   uint8_t* dst = q8 + (size_t)blockIdx.x * S::q_bytes;
-  uint4 x[8];
+  uint4 x[4];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) x[k] = src[part * 8 + k];
-  const uint4 rope = src[kDc / 8 + part];
+  for (int k = 0; k < 4; ++k) x[k] = src[part * 4 + k];
+  uint4 rope = make_uint4(0, 0, 0, 0);
+  if (part < 8) rope = src[kDc / 8 + part];
   float mx = 0.f;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < 4; ++k) {
     const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -329,22 +322,22 @@ __global__ void __launch_bounds__(NH * 8) page8_query_kernel(const uint16_t* q_a
     }
   }
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   // 2^e with mx 2^e in [2^7, 2^8); heads below 2^-112 as 2^-112
   const int e = min(134 - (int)(__float_as_uint(mx) >> 23), 119);
   const float f = __uint_as_float((uint32_t)(e + 127) << 23);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < 2; ++k) {
     const uint32_t u[8] = {x[2 * k].x, x[2 * k].y, x[2 * k].z, x[2 * k].w,
                            x[2 * k + 1].x, x[2 * k + 1].y, x[2 * k + 1].z, x[2 * k + 1].w};
     uint4 t1, t2;
     query_terms(u, f, t1, t2);
-    const int c16 = part * 4 + k;  // 16-code piece of the row
+    const int c16 = part * 2 + k;  // 16-code piece of the row
     uint8_t* slab = dst + (c16 >> 3) * S::q_slab;
     *reinterpret_cast<uint4*>(slab + sw128(h, c16 & 7)) = t1;
     *reinterpret_cast<uint4*>(slab + sw128(NH + h, c16 & 7)) = t2;
   }
-  *reinterpret_cast<uint4*>(dst + S::q_rope + sw128(h, part)) = rope;
+  if (part < 8) *reinterpret_cast<uint4*>(dst + S::q_rope + sw128(h, part)) = rope;
   if (arrive && threadIdx.x == 0) arrive[blockIdx.x] = 0;
   if (part == 0) coef[row] = scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
 }
@@ -420,8 +413,11 @@ __device__ __forceinline__ bool start_share(SchedWalker& sw, const int4* rows, i
   return false;
 }
 
+// (Registers: 168 a thread are free, and 32 heads use them. 16 heads get by with
+// 128, which leaves room on the SM for a CTA of the query kernel, so that a
+// decode CTA starts before that one has ended.)
 template <int NH>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
     page8_decode_kernel(const __grid_constant__ CUtensorMap codes_map,
                         const __grid_constant__ CUtensorMap rope_map, const __grid_constant__ P8Args a) {
   using S = Sm<NH>;
@@ -776,55 +772,62 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < HT; ++k) x[k] = -INFINITY;
         }
         const float exf = (float)ex;
-        // does any weight outgrow its reference?
-        bool grow = !fine;
+        // which heads' weights outgrow their reference, over the half's tokens
+        // (bit 31: a wait failed)
+        uint32_t grown = fine ? 0u : 1u << 31;
 #pragma unroll
         for (int k = 0; k < HT; ++k) {
           x[k] += exf;
-          grow |= x[k] > ref[k] + kGrowLog2;
+          grown |= x[k] > ref[k] + kGrowLog2 ? 1u << k : 0u;
         }
-        if (bar_or(bar, 128, grow)) {
+        grown = __reduce_or_sync(0xffffffffu, grown);
+        uint32_t* votes = reinterpret_cast<uint32_t*>(sm + S::votes) + (slot * 2 + half) * 4;
+        if (lane == 0) votes[w4] = grown;
+        named_bar_sync(bar, 128);
+        {
+          const uint4 v4 = *reinterpret_cast<const uint4*>(votes);
+          grown = v4.x | v4.y | v4.z | v4.w;
+        }
+        if (grown) {
+          // their largest weights over the warps
 #pragma unroll
-          for (int k = 0; k < HT; ++k) {
-            const float m = warp_max(x[k]);
-            if (lane == 0) red[(half * 4 + w4) * HT + k] = m;
-          }
+          for (int k = 0; k < HT; ++k)
+            if ((grown >> k) & 1) {
+              const float m = warp_max(x[k]);
+              if (lane == 0) red[(half * 4 + w4) * HT + k] = m;
+            }
           // (the output products of tile i - 1 must have landed before O is rescaled)
-          if (t > 0 && fine)
-            fine = warp_wait(kPVDone + (slot ^ 1), ((i - 1) >> 1) & 1);
+          if (t > 0 && fine) fine = warp_wait(kPVDone + (slot ^ 1), ((i - 1) >> 1) & 1);
           if (bar_or(bar, 128, !fine)) {
             // (the other half meets this at the end of the segment or here)
             bar_or(kSoftBar, kSoftThreads, true);
             aborted = true;
             break;
           }
-          float f[HT];
-          bool any = false;
+          float fl = 1.f;   // lane k: the factor of head k
 #pragma unroll
-          for (int k = 0; k < HT; ++k) {
-            float m = ref[k];
+          for (int k = 0; k < HT; ++k)
+            if ((grown >> k) & 1) {
+              float m = ref[k];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) m = fmaxf(m, red[(half * 4 + u) * HT + k]);
-            f[k] = m == ref[k] ? 1.f : fast_exp2(ref[k] - m);   // (from -inf: 0)
-            any |= f[k] != 1.f;
-            ref[k] = m;
-            l[k] *= f[k];
-          }
-          if (t > 0 && any) {   // the same for every thread of the half
+              for (int u = 0; u < 4; ++u) m = fmaxf(m, red[(half * 4 + u) * HT + k]);
+              const float f = fast_exp2(ref[k] - m);   // (from -inf: 0)
+              if (lane == k) fl = f;
+              ref[k] = m;
+              l[k] *= f;
+            }
+          if (t > 0) {
             tc::fence_after_sync();
-#pragma unroll 1
-            for (int j = 0; j < 4; ++j) {
-              float o[3][HT];
-              const uint32_t at = trow + kOCol + (uint32_t)(j * 3 * NH + h0);
+            for (uint32_t g = grown; g; g &= g - 1) {
+              const int k = __ffs(g) - 1;
+              const float f = __shfl_sync(0xffffffffu, fl, k);
+              const uint32_t at = trow + kOCol + (uint32_t)(h0 + k);
+              float o[12];
 #pragma unroll
-              for (int c = 0; c < 3; ++c) tmem_ld(at + c * NH, o[c]);
+              for (int c = 0; c < 12; ++c) tmem_ld1(at + c * NH, o[c]);
               tc::wait_ld();
 #pragma unroll
-              for (int c = 0; c < 3; ++c) {
-#pragma unroll
-                for (int k = 0; k < HT; ++k) o[c][k] *= f[k];
-                tmem_st(at + c * NH, o[c]);
-              }
+              for (int c = 0; c < 12; ++c) tmem_st1(at + c * NH, o[c] * f);
             }
             tc::wait_st();
           }
@@ -1324,9 +1327,9 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
                     st);
   if (e == cudaSuccess) {
     const dim3 grid((unsigned)(num_q * (H / NH)));
-    e = NH == 16 ? launch_pdl(page8_query_kernel<16>, grid, dim3(128), 0, st, a.q_abs,
+    e = NH == 16 ? launch_pdl(page8_query_kernel<16>, grid, dim3(256), 0, st, a.q_abs,
                               a.scale_log2, a.q8, a.coef, a.fused ? a.arrive : nullptr)
-                 : launch_pdl(page8_query_kernel<32>, grid, dim3(256), 0, st, a.q_abs,
+                 : launch_pdl(page8_query_kernel<32>, grid, dim3(512), 0, st, a.q_abs,
                               a.scale_log2, a.q8, a.coef, a.fused ? a.arrive : nullptr);
   }
   if (e != cudaSuccess) return MLA_ERR_CUDA;
