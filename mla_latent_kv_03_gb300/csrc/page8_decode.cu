@@ -28,8 +28,10 @@
 // of a head follows s_t + log2 S_p, and O is rescaled in TMEM only when it is
 // outgrown by more than 2^10.
 //
-// NH = 16 or 32 heads of one row make a column group. The work is cut as in
-// the other decodes (units of one row and 64 tokens in equal contiguous
+// NH = 16 or 32 heads of one row make a column group; with 16 heads and several
+// rows a sequence (R = 2), two rows that follow one another do, each with its
+// own last token, so that a tile of tokens serves both. The work is cut as in
+// the other decodes (units of one row or pair and 64 tokens in equal contiguous
 // shares), and each share is taken by one CTA per group: the CTAs of a share
 // read the same tokens at the same time, so a token comes from HBM once for
 // all heads. Per CTA (384 threads):
@@ -89,6 +91,7 @@ struct P8Args {
   const int32_t* query_start_loc;
   int32_t batch;
   int32_t self_plan;   // the kernel derives the split itself
+  int32_t pair;        // rows go in pairs (R = 2)
   // partials of each 16 heads: [slots][16] and [slots][16][512]; the first
   // 16 heads' where ws_layout has them, the others' one after another
   float* lse_first;
@@ -103,7 +106,7 @@ struct P8Args {
   int32_t fused;       // merge the splits in the decode kernel
 };
 
-// The partials of heads 16 t16 ... 16 t16 + 15.
+// The partials of heads 16 t16 ... 16 t16 + 15 (of row t16 of a pair).
 __device__ __forceinline__ float* lse_part(const P8Args& a, int t16) {
   return t16 == 0 ? a.lse_first : a.lse_rest + (int64_t)(t16 - 1) * a.slots * kHG;
 }
@@ -119,14 +122,18 @@ struct P8Ws {
   size_t lse_rest, o_rest, q8, coef, arrive, o_lat, lse, scores, total;
 };
 int group_heads(int H) { return H >= 32 ? 32 : 16; }
+// Rows go in pairs where the 16 heads of one leave half of the columns empty
+// and at least every other sequence has a second row. (Rows of their own take
+// the narrower kernel, which is quicker by itself.)
+bool use_pairs(int H, int64_t num_q, int32_t batch) { return H == 16 && 2 * num_q >= 3 * (int64_t)batch; }
 // Shares of the work: with one CTA per group to a share, about num_ctas CTAs.
 int p8_shares(int H, int num_ctas) {
   const int s = num_ctas / (H / group_heads(H));
   return s > 0 ? s : 1;
 }
-P8Ws p8_ws(int64_t num_q, int H, int shares, int64_t max_tokens, bool mass) {
+P8Ws p8_ws(int64_t num_q, int H, bool pair, int shares, int64_t max_tokens, bool mass) {
   const WsLayout W = ws_layout(num_q, 1, shares);
-  const size_t rest = (size_t)(H / kHG - 1) * W.slots * kHG;
+  const size_t rest = (size_t)((pair ? 2 : H / kHG) - 1) * W.slots * kHG;
   P8Ws L;
   L.lse_rest = align_up(W.total, 256);
   L.o_rest = align_up(L.lse_rest + rest * 4, 256);
@@ -351,25 +358,30 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-// The split plan of plan_kernel for at most S::self_rows rows, derived in shared
-// memory by every CTA. rows[] must be zero; between that and the call, and
-// around it, all threads pass a barrier. Sequences that are not valid own no
-// tiles (CTA 0 reports them). Returns the number of units.
-__device__ __forceinline__ void plan_rows(const P8Args& a, int4* rows, uint32_t* status, int tid, int nthreads) {
+// The split plan: rows[n] = {sequence, position of the (pair's last) row, tiles,
+// first unit}; tiles is -1 for the second row of a pair and 0 where nothing is
+// to be done. fill_rows writes all but the first units, of the sequences
+// first, first + step, ... and their rows (of a pair, the first) lane,
+// lane + lanes, .... Sequences that are not valid own no tiles.
+__device__ __forceinline__ void fill_rows(const P8Args& a, int4* rows, uint32_t* status, int first,
+                                          int step, int lane, int lanes) {
   const int64_t max_len = (int64_t)a.max_blocks * a.block_size;
-  for (int b = tid; b < a.batch; b += nthreads) {
+  const int R = a.pair ? 2 : 1;
+  for (int b = first; b < a.batch; b += step) {
     const int len = a.seq_lens[b];
     const int q0 = a.query_start_loc[b], q1 = a.query_start_loc[b + 1];
     const int ql = q1 - q0;
     if (q0 < 0 || q1 > a.num_q || ql < 0) {
-      if (blockIdx.x == 0) set_status(status, MLA_DEV_BAD_SEQ);
+      set_status(status, MLA_DEV_BAD_SEQ);
       continue;
     }
     const bool bad = ql > len || len < 0 || (int64_t)len > max_len;
-    if (bad && ql > 0 && blockIdx.x == 0) set_status(status, MLA_DEV_BAD_SEQ);
-    for (int j = 0; j < ql; ++j) {
-      const int pos = len - ql + j;
+    if (bad && ql > 0) set_status(status, MLA_DEV_BAD_SEQ);
+    for (int j = lane * R; j < ql; j += lanes * R) {
+      const bool two = R == 2 && j + 1 < ql;
+      const int pos = len - ql + j + (two ? 1 : 0);
       rows[q0 + j] = make_int4(b, pos, bad ? 0 : (pos + kTile) / kTile, 0);
+      if (two) rows[q0 + j + 1] = make_int4(b, pos, bad ? 0 : -1, 0);
     }
   }
 }
@@ -377,7 +389,7 @@ __device__ __forceinline__ void plan_rows(const P8Args& a, int4* rows, uint32_t*
 __device__ __forceinline__ void scan_rows(int4* rows, int num_q, int lane, int* total) {
   int run = 0;
   for (int c = 0; c < num_q; c += 32) {
-    const int v = c + lane < num_q ? rows[c + lane].z : 0;
+    const int v = c + lane < num_q ? max(rows[c + lane].z, 0) : 0;
     int incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -413,15 +425,87 @@ __device__ __forceinline__ bool start_share(SchedWalker& sw, const int4* rows, i
   return false;
 }
 
+// The plan of more rows than that: one CTA, a warp per sequence, into the
+// workspace.
+constexpr int kPlanThreads = 1024;
+__global__ void __launch_bounds__(kPlanThreads) page8_plan_kernel(const __grid_constant__ P8Args a) {
+  extern __shared__ int s_first[];  // [num_q] units, then first units
+  __shared__ int s_warp[32], s_total;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, Nq = (int)a.num_q;
+  const WsLayout L = ws_layout(a.num_q, 1, a.shares);
+  WsHeader* hdr = reinterpret_cast<WsHeader*>(a.ws);
+  int4* rows = reinterpret_cast<int4*>(a.ws + L.row_info);
+  int4* cta_start = reinterpret_cast<int4*>(a.ws + L.cta_start);
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int n = tid; n < Nq; n += kPlanThreads) rows[n] = make_int4(-1, -1, 0, 0);
+  __syncthreads();
+  fill_rows(a, rows, &hdr->status, warp, kPlanThreads / 32, lane, 32);
+  __syncthreads();
+  // exclusive scan of the units, a contiguous piece per thread
+  const int per = (Nq + kPlanThreads - 1) / kPlanThreads;
+  const int beg = min(Nq, tid * per), end = min(Nq, beg + per);
+  int local = 0;
+  for (int n = beg; n < end; ++n) local += max(rows[n].z, 0);
+  int incl = local;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) s_warp[warp] = incl;
+  __syncthreads();
+  int run = incl - local;
+  for (int w = 0; w < warp; ++w) run += s_warp[w];
+  if (tid == kPlanThreads - 1) s_total = run + local;
+  for (int n = beg; n < end; ++n) {
+    s_first[n] = run;
+    rows[n].w = run;
+    run += max(rows[n].z, 0);
+  }
+  __syncthreads();
+  const int total = s_total, share = total > 0 ? (total + a.shares - 1) / a.shares : 1;
+  if (tid == 0) {
+    hdr->magic = kMagic;
+    hdr->mode = 0;
+    hdr->qblocks = 0;
+    hdr->total_units = total;
+    hdr->share = share;
+    hdr->num_ctas = a.shares;
+    hdr->groups = 1;
+    hdr->num_q = Nq;
+    hdr->batch = a.batch;
+  }
+  for (int c = tid; c < a.shares; c += kPlanThreads) {
+    const int u = c * share;
+    int lo = 0, hi = Nq;  // the last row whose first unit is <= u: it owns units
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_first[mid] <= u) lo = mid; else hi = mid;
+    }
+    cta_start[c] = u < total ? make_int4(lo, 0, u - s_first[lo], 0) : make_int4(-1, 0, 0, 0);
+  }
+}
+
+// Zeros for the latents of rows that own no tiles.
+__device__ __forceinline__ void zero_other_rows(const P8Args& a, const int4* rows, int tid, int nthreads) {
+  for (int64_t n = blockIdx.x; n < a.num_q; n += gridDim.x) {
+    if (rows[n].z != 0) continue;
+    float4* row = reinterpret_cast<float4*>(a.o_lat + (size_t)n * a.num_heads * kDc);
+    for (int i = tid; i < a.num_heads * kDc / 4; i += nthreads) row[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+}
+
 // (Registers: 168 a thread are free, and 32 heads use them. 16 heads get by with
 // 128, which leaves room on the SM for a CTA of the query kernel, so that a
 // decode CTA starts before that one has ended.)
-template <int NH>
+template <int NH, int R>
 __global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
     page8_decode_kernel(const __grid_constant__ CUtensorMap codes_map,
                         const __grid_constant__ CUtensorMap rope_map, const __grid_constant__ P8Args a) {
+  static_assert(R == 1 || NH == 32, "a pair is 2 x 16 heads");
   using S = Sm<NH>;
-  constexpr int QB = S::QB, HT = NH / 2;  // heads of a softmax thread
+  constexpr int QB = S::QB, HT = NH / 2;  // heads (columns) of a softmax thread
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
@@ -467,7 +551,7 @@ __global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
   SchedWalker sw;
   bool has_work;
   if (a.self_plan) {
-    plan_rows(a, plan, status, tid, kThreads);
+    fill_rows(a, plan, blockIdx.x == 0 ? status : nullptr, tid, kThreads, 0, 1);
     __syncthreads();
     if (warp == 0) scan_rows(plan, (int)a.num_q, lane, plan_total);
     __syncthreads();
@@ -498,11 +582,13 @@ __global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
       }
     }
     if (a.fused)
-      zero_unvisited_rows(sw.row_info, sw.plan_ok, a.num_q, a.num_heads, a.o_lat, st, kSoftThreads);
+      zero_other_rows(a, sw.row_info, st, kSoftThreads);
   }
   Segment seg{};
   // tokens of the segment: [k0 * 64, end), in tiles of 128
   auto seg_end = [&] { return min(seg.pos + 1, seg.k1 * kTile); };
+  // rows of the segment: 2 if the next row is the second of a pair
+  auto seg_rows = [&] { return R == 2 && seg.n + 1 < a.num_q && sw.row_info[seg.n + 1].z == -1 ? 2 : 1; };
   auto seg_tiles = [&] { return (seg_end() - seg.k0 * kTile + kTok - 1) / kTok; };
   auto warp_wait = [&](int bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait_or_abort(&bars[bar], parity, abort_flag));
@@ -678,11 +764,28 @@ __global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
     while (ok && sw.next(seg)) {
       const int qb = seg_i % QB;
       if (seg_i >= QB && !warp_wait(kQFree + qb, ((seg_i / QB) - 1) & 1)) { ok = false; break; }
-      if (lane == 0) {
+      uint64_t* bar = &bars[kQReady + qb];
+      if (lane == 0) mbar_arrive_expect_tx(bar, S::q_bytes + NH * 4);
+      __syncwarp();
+      uint8_t* dst = sm + S::q + qb * S::q_bytes;
+      if constexpr (R == 1) {
         const int64_t tile = (int64_t)seg.n * a.groups + grp;
-        mbar_arrive_expect_tx(&bars[kQReady + qb], S::q_bytes + NH * 4);
-        bulk_load(sm + S::q + qb * S::q_bytes, a.q8 + tile * S::q_bytes, S::q_bytes, &bars[kQReady + qb]);
-        bulk_load(coef + qb * NH, a.coef + tile * NH, NH * 4, &bars[kQReady + qb]);
+        if (lane == 0) bulk_load(dst, a.q8 + tile * S::q_bytes, S::q_bytes, bar);
+        if (lane == 1) bulk_load(coef + qb * NH, a.coef + tile * NH, NH * 4, bar);
+      } else {
+        // the rows' operands, each of eight (slab, term) pieces of 16 head rows
+        // and one of rope values, interleaved (a single row stands in for its
+        // missing second, whose columns stay masked)
+        using S1 = Sm<16>;
+        const int sub = lane / 9, p = lane % 9, rows = seg_rows();
+        const int64_t row = seg.n + (sub < rows ? sub : 0);
+        constexpr int kPiece = kHG * 128;
+        if (lane < 18)
+          bulk_load(dst + (p < 8 ? (p >> 1) * S::q_slab + (p & 1) * 2 * kPiece : S::q_rope) + sub * kPiece,
+                    a.q8 + row * S1::q_bytes + p * kPiece, kPiece, bar);
+        else if (lane < 20)
+          bulk_load(coef + (lane - 18) * kHG, a.coef + (seg.n + (lane - 18 < rows ? lane - 18 : 0)) * kHG,
+                    kHG * 4, bar);
       }
       __syncwarp();
       ++seg_i;
@@ -714,6 +817,11 @@ __global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
     while (!aborted && sw.next(seg)) {
       const int n = seg_tiles(), qb = seg_i % QB;
       const int64_t tile = (int64_t)seg.n * a.groups + grp;
+      // this half's row, its first head there, and the tokens it sees
+      const int nrows = seg_rows();
+      const int64_t row = seg.n + (R == 2 ? half : 0);
+      const int head0 = R == 2 ? 0 : grp * NH + h0;
+      const int seen = R == 1 ? seg.pos + 1 : half < nrows ? seg.pos + 2 - nrows + half : 0;
       float cq[HT], ref[HT], l[HT];
       const bool okq = warp_wait(kQReady + qb, (seg_i / QB) & 1);
 #pragma unroll
@@ -735,7 +843,7 @@ __global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
         float x[HT];
         int v = 0;
         float sc = 1.f;
-        bool live = false;
+        bool live = false, there = false, odd = false;
         int ex = 0;
         if (fine) {
           tc::fence_after_sync();
@@ -745,7 +853,8 @@ __global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
           tmem_ld(trow + kSCol + 2 * NH + h0, dr);
           v = info[slot];
           sc = page_sc[slot * 8 + (r >> bs_shift)];
-          live = r < v && sc > 0.f;
+          there = r < v && sc > 0.f;
+          live = there && (R == 1 || seg.k0 * kTile + t * kTok + r < seen);
           if (!live) sc = 1.f;
           // S = m 2^ex, m in [1, 2)
           ex = (int)(__float_as_uint(sc) >> 23) - 127;
@@ -753,6 +862,16 @@ __global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[kSFree]);
+          if constexpr (R == 2) {
+            // a token that only the second row sees, with a NaN code: all of
+            // that row is NaN by its scores, and the codes must not reach the
+            // first row's columns (0 times NaN)
+            odd = half == 1 && live && nrows == 2 && seg.k0 * kTile + t * kTok + r == seen - 1;
+            if (odd) {
+#pragma unroll
+              for (int k = 0; k < HT; ++k) odd &= isnan(d1[k]);
+            }
+          }
 #pragma unroll
           for (int k = 0; k < HT; ++k) {
             const float s = fmaf(fmaf(d2[k], 0.03125f, d1[k]) * sc, cq[k], dr[k] * a.scale_log2);
@@ -760,9 +879,9 @@ __global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
           }
           if (a.scores && live) {
             const int64_t tok = (int64_t)seg.k0 * kTile + t * kTok + r;
-            const int64_t t16 = (int64_t)seg.n * (a.num_heads / kHG) + grp * (NH / kHG) + h0 / kHG;
+            const int64_t t16 = row * (a.num_heads / kHG) + head0 / kHG;
             float4* o = reinterpret_cast<float4*>(
-                a.scores + (t16 * a.max_blocks * bs + tok) * kHG + h0 % kHG);
+                a.scores + (t16 * a.max_blocks * bs + tok) * kHG + head0 % kHG);
 #pragma unroll
             for (int k = 0; k < HT / 4; ++k)
               o[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
@@ -882,13 +1001,13 @@ __global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
             *reinterpret_cast<uint4*>(pb + (2 * s + half) * 2048) =
                 make_uint4(tm[s][0], tm[s][1], tm[s][2], tm[s][3]);
         }
-        if (!live && r < ((v + 31) & ~31)) {
-          // a row that is not live may hold anything: zero its codes, so that a
-          // weight of 0 stays 0 (each half two slabs)
-          uint8_t* row = sm + S::stage + slot * kStageB + 2 * half * kSlab + r * 128;
+        if ((!there && r < ((v + 31) & ~31)) || odd) {
+          // a token that is not there may hold anything: zero its codes, so that
+          // a weight of 0 stays 0 (each half two slabs)
+          uint8_t* tok_row = sm + S::stage + slot * kStageB + (odd ? 0 : 2 * half) * kSlab + r * 128;
 #pragma unroll 1
-          for (int c = 0; c < 16; ++c)
-            *reinterpret_cast<uint4*>(row + (c >> 3) * kSlab + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < (odd ? 32 : 16); ++c)
+            *reinterpret_cast<uint4*>(tok_row + (c >> 3) * kSlab + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         tc::fence_before_sync();
@@ -913,10 +1032,11 @@ __global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
       const int c_first = seg.ustart / sw.share, c_last = (seg.ustart + seg.tiles - 1) / sw.share;
       const bool direct = a.fused && c_first == c_last;
       const int64_t slot = (int64_t)share + seg.n;
-      const int t16 = grp * (NH / kHG) + h0 / kHG, hr = h0 % kHG;  // 16 heads of the row, head in them
-      float* o_row = a.o_lat + ((size_t)seg.n * a.num_heads + grp * NH) * kDc;
-      float* dst = (direct ? o_row + (size_t)h0 * kDc : o_part(a, t16) + (slot * kHG + hr) * kDc) +
+      const int t16 = R == 2 ? half : head0 / kHG, hr = head0 % kHG;  // which partials, head in them
+      float* dst = (direct ? a.o_lat + ((size_t)row * a.num_heads + head0) * kDc
+                           : o_part(a, t16) + (slot * kHG + hr) * kDc) +
                    w4 * 32 + lane;
+      const bool mine_too = R == 1 || half < nrows;   // (a pair's missing second row)
       // (all of a row's loads before the first is used)
       float o1[2][HT], o2[2][HT], o3[2][HT];
       auto load_o = [&](int j) {
@@ -934,10 +1054,10 @@ __global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
         if (r == k) mine = l[k], mref = ref[k];
         l[k] = l[k] == 0.f ? 0.f : __fdividef(1.f, l[k]);       // (a NaN sum stays NaN)
       }
-      if (r < HT) {
+      if (r < HT && mine_too) {
         const float lse = mine == 0.f ? -INFINITY : mref - kRefLog2 + log2f(mine);
         if (direct)
-          a.lse[(size_t)seg.n * a.num_heads + grp * NH + h0 + r] = lse;
+          a.lse[(size_t)row * a.num_heads + head0 + r] = lse;
         else
           lse_part(a, t16)[slot * kHG + hr + r] = lse;
       }
@@ -945,6 +1065,7 @@ __global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
       for (int j = 0; j < 4; ++j) {
         tc::wait_ld();
         if (j < 3) load_o(j + 1);
+        if (!mine_too) continue;
 #pragma unroll
         for (int k = 0; k < HT; ++k)
           dst[(size_t)k * kDc + j * 128] = fmaf(o3[j & 1][k], 0.03125f, o1[j & 1][k] + o2[j & 1][k]) * l[k];
@@ -961,14 +1082,16 @@ __global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
           const int parts = c_last - c_first + 1;
           // merge_qtile leaves the maxima and the inverse weight sums in its scratch
           if constexpr (NH == 16) {
-            merge_qtile<kSoftThreads>(a.lse_first, a.o_first, (int64_t)c_first + seg.n, parts, 1, o_row, st,
-                                      scratch, [] { named_bar_sync(kSoftBar, kSoftThreads); });
+            merge_qtile<kSoftThreads>(a.lse_first, a.o_first, (int64_t)c_first + seg.n, parts, 1,
+                                      a.o_lat + (size_t)row * a.num_heads * kDc, st, scratch,
+                                      [] { named_bar_sync(kSoftBar, kSoftThreads); });
             if (st < kHG) a.lse[tile * kHG + st] = merged_lse(scratch[st], scratch[kHG + st]);
-          } else {
-            float* mine = scratch + half * (S::merge_bytes / 4);
+          } else if (mine_too) {
+            float* own = scratch + half * (S::merge_bytes / 4);
             merge_qtile<128>(lse_part(a, t16), o_part(a, t16), (int64_t)c_first + seg.n, parts, 1,
-                             o_row + half * kHG * kDc, r, mine, [&] { named_bar_sync(bar, 128); });
-            if (r < kHG) a.lse[tile * NH + half * kHG + r] = merged_lse(mine[r], mine[kHG + r]);
+                             a.o_lat + ((size_t)row * a.num_heads + head0) * kDc, r, own,
+                             [&] { named_bar_sync(bar, 128); });
+            if (r < kHG) a.lse[(size_t)row * a.num_heads + head0 + r] = merged_lse(own[r], own[kHG + r]);
           }
         }
       }
@@ -995,12 +1118,14 @@ struct HeadParts {
 };
 __device__ __forceinline__ HeadParts head_parts(const P8Args& a, const int4* rows, int share, int n, int h) {
   HeadParts r{a.lse_first, a.o_first, 0};
-  const int4 ri = rows[n];
+  int4 ri = rows[n];
+  int t16 = h / kHG;
+  if (ri.z == -1 && n > 0) ri = rows[--n], t16 = 1;  // the second row of a pair
   if (ri.z <= 0) return r;
   const int cf = ri.w / share, cl = (ri.w + ri.z - 1) / share;
   const int64_t slot = ((int64_t)cf + n) * kHG + h % kHG;
-  r.lse = lse_part(a, h / kHG) + slot;
-  r.o = o_part(a, h / kHG) + slot * kDc;
+  r.lse = lse_part(a, t16) + slot;
+  r.o = o_part(a, t16) + slot * kDc;
   r.count = cl - cf + 1;
   return r;
 }
@@ -1112,7 +1237,7 @@ __global__ void __launch_bounds__(256) page8_merge_proj_kernel(const __grid_cons
   int share = 1;
   if (a.self_plan) {
     __syncthreads();
-    plan_rows(a, plan, nullptr, tid, 256);
+    fill_rows(a, plan, nullptr, tid, 256, 0, 1);
     __syncthreads();
     if (warp == 0) scan_rows(plan, (int)a.num_q, lane, plan_total);
     __syncthreads();
@@ -1273,11 +1398,13 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
   const size_t need = mla_page8_decode_workspace_size(cfg, num_q, batch, max_blocks, with_mass);
   if (need == 0) return MLA_ERR_UNSUPPORTED;
   if (ws_bytes < need) return MLA_ERR_WORKSPACE_TOO_SMALL;
-  const int H = cfg->num_heads, bs = cfg->block_size, NH = group_heads(H);
+  const int H = cfg->num_heads, bs = cfg->block_size;
+  const bool pair = use_pairs(H, num_q, batch);
+  const int NH = pair ? 32 : group_heads(H);
   const int shares = p8_shares(H, split_ctas(cfg));
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const P8Ws L = p8_ws(num_q, H, shares, (int64_t)max_blocks * bs, with_mass);
+  const P8Ws L = p8_ws(num_q, H, pair, shares, (int64_t)max_blocks * bs, with_mass);
   const WsLayout W = ws_layout(num_q, 1, shares);
   // With num_blocks == 0 every block id is rejected before any copy; the maps
   // still need an extent.
@@ -1293,7 +1420,8 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
   a.max_blocks = max_blocks;
   a.block_size = bs;
   a.num_heads = H;
-  a.groups = H / NH;
+  a.groups = pair ? 1 : H / NH;
+  a.pair = pair;
   a.shares = shares;
   a.num_q = num_q;
   a.scale_log2 = (float)(cfg->softmax_scale * 1.4426950408889634);
@@ -1321,23 +1449,26 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
   a.fused = num_q >= 256 && !many_parts;
   const bool merge_proj = num_q < 256 && !many_parts;
   cudaError_t e = cudaSuccess;
-  if (!a.self_plan)
-    e = launch_plan(PlanArgs{seq_lens, query_start_loc, batch, (int32_t)num_q, 1, shares, bs,
-                             max_blocks, workspace},
-                    st);
+  if (!a.self_plan) {
+    e = cudaFuncSetAttribute(page8_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)num_q * 4);
+    if (e == cudaSuccess) e = launch_pdl(page8_plan_kernel, dim3(1), dim3(kPlanThreads), (size_t)num_q * 4, st, a);
+  }
   if (e == cudaSuccess) {
-    const dim3 grid((unsigned)(num_q * (H / NH)));
-    e = NH == 16 ? launch_pdl(page8_query_kernel<16>, grid, dim3(256), 0, st, a.q_abs,
-                              a.scale_log2, a.q8, a.coef, a.fused ? a.arrive : nullptr)
-                 : launch_pdl(page8_query_kernel<32>, grid, dim3(512), 0, st, a.q_abs,
-                              a.scale_log2, a.q8, a.coef, a.fused ? a.arrive : nullptr);
+    // (a row of a pair has its operand as 16 heads by themselves do)
+    int* arrive = a.fused ? a.arrive : nullptr;
+    e = H == 16 ? launch_pdl(page8_query_kernel<16>, dim3((unsigned)num_q), dim3(256), 0, st, a.q_abs,
+                             a.scale_log2, a.q8, a.coef, arrive)
+                : launch_pdl(page8_query_kernel<32>, dim3((unsigned)(num_q * a.groups)), dim3(512), 0, st, a.q_abs,
+                             a.scale_log2, a.q8, a.coef, arrive);
   }
   if (e != cudaSuccess) return MLA_ERR_CUDA;
   auto launch = [&](auto kernel, int smem) {
     const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     return r != cudaSuccess ? r : launch_pdl(kernel, dim3(shares * a.groups), dim3(kThreads), smem, st, codes_map, rope_map, a);
   };
-  e = NH == 16 ? launch(page8_decode_kernel<16>, Sm<16>::alloc) : launch(page8_decode_kernel<32>, Sm<32>::alloc);
+  e = pair       ? launch(page8_decode_kernel<32, 2>, Sm<32>::alloc)
+      : NH == 16 ? launch(page8_decode_kernel<16, 1>, Sm<16>::alloc)
+                 : launch(page8_decode_kernel<32, 1>, Sm<32>::alloc);
   if (e == cudaSuccess && many_parts)
     e = launch_pdl(page8_merge_kernel, dim3((unsigned)(num_q * H)), dim3(512), 0, st, a);
   if (e == cudaSuccess && merge_proj) {
@@ -1380,7 +1511,7 @@ size_t mla_page8_decode_workspace_size(const mla_config* cfg, int64_t num_q, int
     return 0;
   const int C = split_ctas(cfg), H = cfg->num_heads;
   if (C <= 0) return 0;
-  return p8_ws(num_q, H, p8_shares(H, C), (int64_t)max_blocks_per_seq * cfg->block_size,
+  return p8_ws(num_q, H, use_pairs(H, num_q, batch), p8_shares(H, C), (int64_t)max_blocks_per_seq * cfg->block_size,
                with_mass != 0)
       .total;
 }

@@ -192,6 +192,8 @@ CASES = {
     "chunks_h32_bs16": ([90, 17], [33, 17], 32, 16),
     "chunk_h128": ([70], [9], 128, 32),
     "many_rows": ([700, 20], [300, 1], 16, 64),
+    "speculative": ([130, 500, 2, 66], [2, 3, 2, 1], 16, 32),
+    "mixed": ([300, 64, 5, 1, 190], [100, 1, 1, 1, 33], 16, 16),
     "long": ([9000], [1], 16, 64),
 }
 
@@ -348,19 +350,35 @@ def test_a_nan_query_stays_in_its_head_and_a_nan_key_in_its_sequence():
     assert torch.equal(s.out.cpu()[fine], clean.cpu()[fine])
 
 
-def test_a_token_ahead_of_a_row_may_hold_anything():
-    # the chunk's later tokens are NaN: earlier rows do not see them
-    w, s = _step("many_rows")
+@pytest.mark.parametrize("name,far", [("many_rows", 10), ("many_rows", 1), ("many_rows", 7), ("chunks", 3),
+                                      ("chunks_h32_bs16", 5)])
+def test_a_token_ahead_of_a_row_may_hold_anything(name, far):
+    # the chunk's last tokens are NaN: earlier rows do not see them
+    w, s = _step(name)
     s.page8_decode()
     clean = s.out.clone()
-    n, q = 700, 300
-    for t in range(n - 10, n):
-        s.p8_cache[int(w.block_table[0, t // 64]), t % 64] = 0x7F
+    n, q, bs = int(w.seq_lens[0]), int(w.q_lens[0]), w.block_size
+    for t in range(n - far, n):
+        s.p8_cache[int(w.block_table[0, t // bs]), t % bs] = 0x7F
     s.page8_decode()
     torch.cuda.synchronize()
-    assert torch.equal(s.out[:q - 10], clean[:q - 10])
-    assert torch.isnan(s.out[q - 10:q].float()).all()
+    assert torch.equal(s.out[:q - far], clean[:q - far])
+    assert torch.isnan(s.out[q - far:q].float()).all()
     assert torch.equal(s.out[q:], clean[q:])
+
+
+def test_a_nan_query_row_leaves_the_row_beside_it():
+    w, s = _step("chunks")
+    s.page8_decode()
+    clean = s.out.clone()
+    for n in (0, 7, 39, 44):
+        s.q_abs[n] = float("nan")
+    s.page8_decode()
+    torch.cuda.synchronize()
+    fine = torch.ones(w.num_q, dtype=torch.bool)
+    fine[[0, 7, 39, 44]] = False
+    assert torch.isnan(s.out[~fine].float()).all()
+    assert torch.equal(s.out[fine], clean[fine])
 
 
 def test_scales_may_differ_widely_between_pages():
