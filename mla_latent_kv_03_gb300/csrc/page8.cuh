@@ -5,6 +5,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "pair_math.cuh"
 
 namespace mla {
 
@@ -22,6 +23,13 @@ __device__ __forceinline__ float p8_scale_for(float amax) {
   int e = (int)(u >> 23) - 126 - 9 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
   e = min(max(e, kP8MinExp), kP8MaxExp);
   return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// Two packed fp32 products, as the pair_math.cuh ones.
+__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f32x2_pack(a.x, a.y)), "l"(f32x2_pack(b.x, b.y)));
+  return f32x2_unpack(d);
 }
 
 // Four e4m3 codes times f <= 1, rounded to nearest even again (exact for a

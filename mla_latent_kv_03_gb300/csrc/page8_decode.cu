@@ -34,7 +34,7 @@
 // the other decodes (units of one row or pair and 64 tokens in equal contiguous
 // shares), and each share is taken by one CTA per group: the CTAs of a share
 // read the same tokens at the same time, so a token comes from HBM once for
-// all heads. Per CTA (384 threads):
+// all heads. Per CTA (384 or 640 threads):
 //   warp 0      copies: 128 tokens a stage (4 slabs of 128 codes, one of rope
 //               values), two stages, SWIZZLE_128B; block ids are checked;
 //   warp 1      issues the output products of a tile as soon as its weights are
@@ -43,9 +43,9 @@
 //               score columns are read;
 //   warp 3      copies the next segment's query terms, which a kernel before
 //               this one has split and laid out as the operand;
-//   warps 4-11  softmax: thread r of each half owns token r and half of the
-//               heads. Token rows that are not live are zeroed in the stage,
-//               so a weight of 0 never meets a NaN code.
+//   warps 4-    softmax, 4 warps for every 8 heads: thread r of each such group
+//               owns token r. Tokens that are not there are zeroed in the
+//               stage, so a weight of 0 never meets a NaN code.
 // Every wait is bounded; on a timeout the roles leave their loops, the issuer
 // waits for its products and the copies' warp for its copies before TMEM is
 // freed.
@@ -56,6 +56,7 @@
 #include "internal.h"
 #include "merge.cuh"
 #include "page8.cuh"
+#include "pair_math.cuh"
 #include "sched.cuh"
 #include "tcgen05.cuh"
 
@@ -65,10 +66,12 @@ namespace {
 constexpr int kTok = 128;                     // tokens per stage
 constexpr int kSlab = kTok * 128;             // 128 rows of 128 bytes
 constexpr int kStageB = 5 * kSlab;            // four slabs of codes, one of rope values
-constexpr int kThreads = 384;
-constexpr int kSoftWarp0 = 4, kSoftThreads = 256;
-constexpr int kSoftBar = 1, kHalfBar = 2;     // named barriers: all softmax warps; one half (2, 3)
+constexpr int HT = 8;                         // heads (columns) of a softmax thread
+constexpr int kSoftWarp0 = 4;
+// named barriers: all softmax warps; each 16 columns' (2, 3); each 8 columns' (4-7)
+constexpr int kSoftBar = 1, kHeadsBar = 2, kGroupBar = 4;
 constexpr float kRefLog2 = 4.f;               // a weight equal to the reference is held as 2^4
+constexpr float kNoRef = 1e38f;
 constexpr float kGrowLog2 = 10.f;             // the reference follows when outgrown by 2^10
 constexpr uint32_t kTmemCols = 512, kSCol = 0, kOCol = 128;
 
@@ -150,6 +153,9 @@ P8Ws p8_ws(int64_t num_q, int H, bool pair, int shares, int64_t max_tokens, bool
 // Shared memory of one CTA.
 template <int NH>
 struct Sm {
+  static constexpr int groups = NH / HT;                // of softmax warps
+  static constexpr int soft = groups * 128;             // softmax threads
+  static constexpr int threads = kSoftWarp0 * 32 + soft;
   static constexpr int QB = NH == 16 ? 2 : 1;           // query buffers
   static constexpr int q_slab = 2 * NH * 128;           // 128 codes of every term row
   static constexpr int q_rope = 4 * q_slab;
@@ -159,11 +165,10 @@ struct Sm {
   static constexpr int q = stage + 2 * kStageB;
   static constexpr int p = q + QB * q_bytes;
   static constexpr int coef = p + 2 * p_bytes;          // [QB][NH] score factor of a head
-  static constexpr int red = coef + QB * NH * 4;         // [8 warps][NH / 2]
-  static constexpr int merge = red + 8 * (NH / 2) * 4;  // merge scratch, one per half
+  static constexpr int red = coef + QB * NH * 4;        // [softmax warps][HT]
+  static constexpr int merge = red + groups * 4 * HT * 4;  // merge scratch, one per 16 columns
   static constexpr int merge_bytes = (2 * kHG + kMergeChunk * kHG) * 4;
-  static constexpr int votes = merge + 2 * merge_bytes; // [2 tiles][2 halves][4 warps] heads that outgrow
-  static constexpr int info = votes + 64;               // [2] live rows of a stage
+  static constexpr int info = merge + NH / 16 * merge_bytes;  // [2] tokens of a stage
   static constexpr int scale = info + 16;               // [2][8] page scales of a stage, -1: no page
   static constexpr int self_rows = NH == 16 ? kSelfMaxRows : 128;  // rows of a self-planned launch
   static constexpr int rows = scale + 64;               // [self_rows] int4
@@ -496,16 +501,16 @@ __device__ __forceinline__ void zero_other_rows(const P8Args& a, const int4* row
   }
 }
 
-// (Registers: 168 a thread are free, and 32 heads use them. 16 heads get by with
-// 128, which leaves room on the SM for a CTA of the query kernel, so that a
-// decode CTA starts before that one has ended.)
+// (Registers: 16 heads are held to 128 a thread, not the 168 that are free,
+// which leaves room on the SM for a CTA of the query kernel, so that a decode
+// CTA starts before that one has ended.)
 template <int NH, int R>
-__global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
+__global__ void __launch_bounds__(NH == 16 ? 448 : Sm<32>::threads, 1)
     page8_decode_kernel(const __grid_constant__ CUtensorMap codes_map,
                         const __grid_constant__ CUtensorMap rope_map, const __grid_constant__ P8Args a) {
   static_assert(R == 1 || NH == 32, "a pair is 2 x 16 heads");
   using S = Sm<NH>;
-  constexpr int QB = S::QB, HT = NH / 2;  // heads (columns) of a softmax thread
+  constexpr int QB = S::QB, kThreads = S::threads, kSoftThreads = S::soft;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
@@ -806,10 +811,10 @@ __global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
   } else if (has_work) {
     // ------------------------------------------------------------- softmax
     const int st = tid - kSoftWarp0 * 32;               // 0-255
-    const int half = st >> 7, r = st & 127, w4 = (warp & 3);
-    const int h0 = half * HT;                           // first head of this thread
+    const int sg = st >> 7, r = st & 127, w4 = (warp & 3);  // group, token, warp of the group
+    const int h0 = sg * HT, c16 = h0 / kHG;                 // first column of this thread, its 16 columns
     const uint32_t trow = tmem + ((uint32_t)(w4 * 32) << 16);
-    const int bar = kHalfBar + half;
+    const int bar = kGroupBar + sg;
     float* red = reinterpret_cast<float*>(sm + S::red);
     float* scratch = reinterpret_cast<float*>(sm + S::merge);
     int i = 0, seg_i = 0;
@@ -817,18 +822,21 @@ __global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
     while (!aborted && sw.next(seg)) {
       const int n = seg_tiles(), qb = seg_i % QB;
       const int64_t tile = (int64_t)seg.n * a.groups + grp;
-      // this half's row, its first head there, and the tokens it sees
+      // this thread's row, its first head there, and the tokens the row sees
       const int nrows = seg_rows();
-      const int64_t row = seg.n + (R == 2 ? half : 0);
-      const int head0 = R == 2 ? 0 : grp * NH + h0;
-      const int seen = R == 1 ? seg.pos + 1 : half < nrows ? seg.pos + 2 - nrows + half : 0;
-      float cq[HT], ref[HT], l[HT];
+      const int64_t row = seg.n + (R == 2 ? c16 : 0);
+      const int head0 = R == 2 ? h0 % kHG : grp * NH + h0;
+      const int seen = R == 1 ? seg.pos + 1 : c16 < nrows ? seg.pos + 2 - nrows + c16 : 0;
+      // pairs of heads go through the packed fp32 instructions. nref is what is
+      // added to a score to give the exponent of its weight: kRefLog2 less the
+      // head's reference, and before a head has one, enough to exceed any bound
+      float2 cq[HT / 2], nref[HT / 2], l[HT / 2];
       const bool okq = warp_wait(kQReady + qb, (seg_i / QB) & 1);
 #pragma unroll
-      for (int k = 0; k < HT; ++k) {
-        cq[k] = okq ? coef[qb * NH + h0 + k] : 0.f;
-        ref[k] = -INFINITY;
-        l[k] = 0.f;
+      for (int k = 0; k < HT / 2; ++k) {
+        cq[k] = okq ? *reinterpret_cast<const float2*>(coef + qb * NH + h0 + 2 * k) : make_float2(0.f, 0.f);
+        nref[k] = make_float2(kNoRef, kNoRef);
+        l[k] = make_float2(0.f, 0.f);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kQFree + qb]);
@@ -840,11 +848,10 @@ __global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
                     wait_or_abort(&bars[kFull + slot], (i >> 1) & 1, abort_flag) &&
                     (i < 2 || wait_or_abort(&bars[kPVDone + slot], ((i >> 1) - 1) & 1, abort_flag));
         fine = __all_sync(0xffffffffu, fine);
-        float x[HT];
+        float2 x[HT / 2];   // score + log2 S: the base-2 logarithm of a weight as it enters the output
         int v = 0;
-        float sc = 1.f;
-        bool live = false, there = false, odd = false;
-        int ex = 0;
+        bool there = false, odd = false;
+        float inv_s = 1.f;
         if (fine) {
           tc::fence_after_sync();
           float d1[HT], d2[HT], dr[HT];
@@ -852,12 +859,17 @@ __global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
           tmem_ld(trow + kSCol + NH + h0, d2);
           tmem_ld(trow + kSCol + 2 * NH + h0, dr);
           v = info[slot];
-          sc = page_sc[slot * 8 + (r >> bs_shift)];
+          float sc = page_sc[slot * 8 + (r >> bs_shift)];
           there = r < v && sc > 0.f;
-          live = there && (R == 1 || seg.k0 * kTile + t * kTok + r < seen);
+          const int tok = seg.k0 * kTile + t * kTok + r;
+          const bool live = there && (R == 1 || tok < seen);
           if (!live) sc = 1.f;
-          // S = m 2^ex, m in [1, 2)
-          ex = (int)(__float_as_uint(sc) >> 23) - 127;
+          // S = m 2^e, m in [1, 2): its logarithm is exact for a power of two
+          const float m = __uint_as_float((__float_as_uint(sc) & 0x7fffffu) | 0x3f800000u);
+          const float lg = (float)((int)(__float_as_uint(sc) >> 23) - 127) + (m == 1.f ? 0.f : log2f(m));
+          inv_s = 1.f / sc;
+          const float2 c32 = make_float2(0.03125f, 0.03125f), s2 = make_float2(sc, sc);
+          const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), lg2 = make_float2(lg, lg);
           tc::wait_ld();
           tc::fence_before_sync();
           __syncwarp();
@@ -866,147 +878,150 @@ __global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
             // a token that only the second row sees, with a NaN code: all of
             // that row is NaN by its scores, and the codes must not reach the
             // first row's columns (0 times NaN)
-            odd = half == 1 && live && nrows == 2 && seg.k0 * kTile + t * kTok + r == seen - 1;
+            odd = c16 == 1 && live && nrows == 2 && tok == seen - 1;
             if (odd) {
 #pragma unroll
               for (int k = 0; k < HT; ++k) odd &= isnan(d1[k]);
             }
           }
 #pragma unroll
-          for (int k = 0; k < HT; ++k) {
-            const float s = fmaf(fmaf(d2[k], 0.03125f, d1[k]) * sc, cq[k], dr[k] * a.scale_log2);
-            x[k] = live ? s : -INFINITY;
+          for (int k = 0; k < HT / 2; ++k) {
+            const float2 d = fma_f32x2(make_float2(d2[2 * k], d2[2 * k + 1]), c32, make_float2(d1[2 * k], d1[2 * k + 1]));
+            x[k] = fma_f32x2(mul_f32x2(d, s2), cq[k],
+                             fma_f32x2(make_float2(dr[2 * k], dr[2 * k + 1]), scale2, lg2));
           }
           if (a.scores && live) {
-            const int64_t tok = (int64_t)seg.k0 * kTile + t * kTok + r;
             const int64_t t16 = row * (a.num_heads / kHG) + head0 / kHG;
             float4* o = reinterpret_cast<float4*>(
                 a.scores + (t16 * a.max_blocks * bs + tok) * kHG + head0 % kHG);
 #pragma unroll
             for (int k = 0; k < HT / 4; ++k)
-              o[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+              o[k] = make_float4(x[2 * k].x - lg, x[2 * k].y - lg, x[2 * k + 1].x - lg, x[2 * k + 1].y - lg);
+          }
+          if (!__all_sync(0xffffffffu, live)) {
+#pragma unroll
+            for (int k = 0; k < HT / 2; ++k)
+              if (!live) x[k] = make_float2(-INFINITY, -INFINITY);
           }
         } else {
 #pragma unroll
-          for (int k = 0; k < HT; ++k) x[k] = -INFINITY;
+          for (int k = 0; k < HT / 2; ++k) x[k] = make_float2(-INFINITY, -INFINITY);
         }
-        const float exf = (float)ex;
-        // which heads' weights outgrow their reference, over the half's tokens
-        // (bit 31: a wait failed)
-        uint32_t grown = fine ? 0u : 1u << 31;
+        // does any weight outgrow its reference? (NaN does not)
+        float2 y[HT / 2];
 #pragma unroll
-        for (int k = 0; k < HT; ++k) {
-          x[k] += exf;
-          grown |= x[k] > ref[k] + kGrowLog2 ? 1u << k : 0u;
-        }
-        grown = __reduce_or_sync(0xffffffffu, grown);
-        uint32_t* votes = reinterpret_cast<uint32_t*>(sm + S::votes) + (slot * 2 + half) * 4;
-        if (lane == 0) votes[w4] = grown;
-        named_bar_sync(bar, 128);
-        {
-          const uint4 v4 = *reinterpret_cast<const uint4*>(votes);
-          grown = v4.x | v4.y | v4.z | v4.w;
-        }
-        if (grown) {
-          // their largest weights over the warps
+        for (int k = 0; k < HT / 2; ++k) y[k] = add_f32x2(x[k], nref[k]);
+        float top = fmaxf(y[0].x, y[0].y);
 #pragma unroll
-          for (int k = 0; k < HT; ++k)
-            if ((grown >> k) & 1) {
-              const float m = warp_max(x[k]);
-              if (lane == 0) red[(half * 4 + w4) * HT + k] = m;
-            }
+        for (int k = 1; k < HT / 2; ++k) top = fmax3(top, y[k].x, y[k].y);
+        if (bar_or(bar, 128, !fine || top > kRefLog2 + kGrowLog2)) {
+          // every head's largest weight (no branches between them), lane k
+          // holding head k's
+          float mx = -INFINITY, old = 0.f;
+#pragma unroll
+          for (int k = 0; k < HT; ++k) {
+            const float m = warp_max(k & 1 ? x[k / 2].y : x[k / 2].x);
+            if (lane == k) mx = m, old = k & 1 ? nref[k / 2].y : nref[k / 2].x;
+          }
+          if (lane < HT) red[(sg * 4 + w4) * HT + lane] = mx;
           // (the output products of tile i - 1 must have landed before O is rescaled)
           if (t > 0 && fine) fine = warp_wait(kPVDone + (slot ^ 1), ((i - 1) >> 1) & 1);
           if (bar_or(bar, 128, !fine)) {
-            // (the other half meets this at the end of the segment or here)
+            // (the other groups meet this at the end of the segment or here)
             bar_or(kSoftBar, kSoftThreads, true);
             aborted = true;
             break;
           }
-          float fl = 1.f;   // lane k: the factor of head k
+          bool grew = false;
+          float now = old, fl = 1.f;   // lane k: head k's nref and factor
+          if (lane < HT) {
 #pragma unroll
-          for (int k = 0; k < HT; ++k)
-            if ((grown >> k) & 1) {
-              float m = ref[k];
-#pragma unroll
-              for (int u = 0; u < 4; ++u) m = fmaxf(m, red[(half * 4 + u) * HT + k]);
-              const float f = fast_exp2(ref[k] - m);   // (from -inf: 0)
-              if (lane == k) fl = f;
-              ref[k] = m;
-              l[k] *= f;
+            for (int u = 0; u < 4; ++u) mx = fmaxf(mx, red[(sg * 4 + u) * HT + lane]);
+            grew = mx + old > kRefLog2 + kGrowLog2;
+            if (grew) {
+              now = kRefLog2 - mx;
+              fl = fast_exp2(now - old);   // (from kNoRef: 0)
             }
-          if (t > 0) {
-            tc::fence_after_sync();
-            for (uint32_t g = grown; g; g &= g - 1) {
-              const int k = __ffs(g) - 1;
-              const float f = __shfl_sync(0xffffffffu, fl, k);
-              const uint32_t at = trow + kOCol + (uint32_t)(h0 + k);
-              float o[12];
+          }
+          uint32_t grown = __ballot_sync(0xffffffffu, grew);
 #pragma unroll
-              for (int c = 0; c < 12; ++c) tmem_ld1(at + c * NH, o[c]);
+          for (int k = 0; k < HT / 2; ++k) {
+            nref[k].x = __shfl_sync(0xffffffffu, now, 2 * k);
+            nref[k].y = __shfl_sync(0xffffffffu, now, 2 * k + 1);
+            l[k].x *= __shfl_sync(0xffffffffu, fl, 2 * k);
+            l[k].y *= __shfl_sync(0xffffffffu, fl, 2 * k + 1);
+            y[k] = add_f32x2(x[k], nref[k]);
+          }
+          if (t > 0) {
+            // the output columns of the heads that grew, two heads at a time
+            tc::fence_after_sync();
+            while (grown) {
+              const int k0 = __ffs(grown) - 1;
+              grown &= grown - 1;
+              const int k1 = grown ? __ffs(grown) - 1 : k0;
+              grown &= grown - 1;
+              const float f0 = __shfl_sync(0xffffffffu, fl, k0), f1 = __shfl_sync(0xffffffffu, fl, k1);
+              const uint32_t at0 = trow + kOCol + (uint32_t)(h0 + k0), at1 = trow + kOCol + (uint32_t)(h0 + k1);
+              float o0[12], o1[12];
+#pragma unroll
+              for (int c = 0; c < 12; ++c) {
+                tmem_ld1(at0 + c * NH, o0[c]);
+                tmem_ld1(at1 + c * NH, o1[c]);
+              }
               tc::wait_ld();
 #pragma unroll
-              for (int c = 0; c < 12; ++c) tmem_st1(at + c * NH, o[c] * f);
+              for (int c = 0; c < 12; ++c) {
+                tmem_st1(at0 + c * NH, o0[c] * f0);
+                if (k1 != k0) tmem_st1(at1 + c * NH, o1[c] * f1);
+              }
             }
             tc::wait_st();
           }
         }
-        // weights 2^(s - ref) S, as three e5m2 terms, and the sum of 2^(s - ref)
-        const float mant = __uint_as_float((__float_as_uint(sc) & 0x7fffffu) | 0x3f800000u);
-        const float inv_s = 1.f / sc;
+        // weights 2^(s - ref) S, and the sum of 2^(s - ref)
         uint32_t hp[HT / 2];
+        const float2 inv2 = make_float2(inv_s, inv_s);
 #pragma unroll
-        for (int k = 0; k < HT; k += 2) {
-          const float b0 = ref[k] == -INFINITY ? 0.f : ref[k], b1 = ref[k + 1] == -INFINITY ? 0.f : ref[k + 1];
-          const float p0 = fast_exp2(x[k] - b0 + kRefLog2) * mant, p1 = fast_exp2(x[k + 1] - b1 + kRefLog2) * mant;
-          l[k] = fmaf(p0, inv_s, l[k]);
-          l[k + 1] = fmaf(p1, inv_s, l[k + 1]);
-          const __half2 hh = __floats2half2_rn(p0, p1);
-          hp[k / 2] = *reinterpret_cast<const uint32_t*>(&hh);
+        for (int k = 0; k < HT / 2; ++k) {
+          const float2 p = make_float2(fast_exp2(y[k].x), fast_exp2(y[k].y));
+          l[k] = fma_f32x2(p, inv2, l[k]);
+          const __half2 hh = __floats2half2_rn(p.x, p.y);
+          hp[k] = *reinterpret_cast<const uint32_t*>(&hh);
         }
+        // as three e5m2 terms. e5m2 is the upper byte of f16: cut the first two
+        // off, round the rest, which is below 2^-5 of the weight, times 2^5
         uint32_t tm[3][HT / 4];
 #pragma unroll
         for (int k = 0; k < HT / 2; k += 2) {
-          // e5m2 is the upper byte of f16: cut the first two terms off, round
-          // the rest, which is below 2^-5 of the weight, times 2^5
           uint32_t a0 = hp[k], a1 = hp[k + 1];
-          tm[0][k / 2] = __byte_perm(a0, a1, 0x7531);
 #pragma unroll
-          for (int s = 1; s < 3; ++s) {
+          for (int s = 0; s < 2; ++s) {
+            tm[s][k / 2] = __byte_perm(a0, a1, 0x7531);
             const uint32_t c0 = a0 & 0xff00ff00u, c1 = a1 & 0xff00ff00u;
             const __half2 r0 = __hsub2(*reinterpret_cast<const __half2*>(&a0), *reinterpret_cast<const __half2*>(&c0));
             const __half2 r1 = __hsub2(*reinterpret_cast<const __half2*>(&a1), *reinterpret_cast<const __half2*>(&c1));
             a0 = *reinterpret_cast<const uint32_t*>(&r0);
             a1 = *reinterpret_cast<const uint32_t*>(&r1);
-            if (s == 1) {
-              tm[1][k / 2] = __byte_perm(a0, a1, 0x7531);
-            } else {
-              uint16_t e0, e1;
-              const __half2 f = __floats2half2_rn(32.f, 32.f);
-              const __half2 m0 = __hmul2(r0, f), m1 = __hmul2(r1, f);
-              a0 = *reinterpret_cast<const uint32_t*>(&m0);
-              a1 = *reinterpret_cast<const uint32_t*>(&m1);
-              asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(e0) : "r"(a0));
-              asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(e1) : "r"(a1));
-              tm[2][k / 2] = (uint32_t)e0 | ((uint32_t)e1 << 16);
-            }
           }
+          const __half2 f = __floats2half2_rn(32.f, 32.f);
+          const __half2 m0 = __hmul2(*reinterpret_cast<const __half2*>(&a0), f);
+          const __half2 m1 = __hmul2(*reinterpret_cast<const __half2*>(&a1), f);
+          uint16_t e0, e1;
+          asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(e0) : "r"(*reinterpret_cast<const uint32_t*>(&m0)));
+          asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(e1) : "r"(*reinterpret_cast<const uint32_t*>(&m1)));
+          tm[2][k / 2] = (uint32_t)e0 | ((uint32_t)e1 << 16);
         }
         uint8_t* pb = sm + S::p + slot * S::p_bytes + (r >> 3) * 128 + (r & 7) * 16;
 #pragma unroll
-        for (int s = 0; s < 3; ++s) {
-          if constexpr (NH == 16)
-            *reinterpret_cast<uint2*>(pb + s * 2048 + h0) = make_uint2(tm[s][0], tm[s][1]);
-          else
-            *reinterpret_cast<uint4*>(pb + (2 * s + half) * 2048) =
-                make_uint4(tm[s][0], tm[s][1], tm[s][2], tm[s][3]);
-        }
+        for (int s = 0; s < 3; ++s)
+          *reinterpret_cast<uint2*>(pb + (s * (NH / kHG) + c16) * 2048 + h0 % kHG) = make_uint2(tm[s][0], tm[s][1]);
         if ((!there && r < ((v + 31) & ~31)) || odd) {
           // a token that is not there may hold anything: zero its codes, so that
-          // a weight of 0 stays 0 (each half two slabs)
-          uint8_t* tok_row = sm + S::stage + slot * kStageB + (odd ? 0 : 2 * half) * kSlab + r * 128;
+          // a weight of 0 stays 0 (each group its part of the four slabs)
+          constexpr int kSlabs = 4 / S::groups;
+          uint8_t* tok_row = sm + S::stage + slot * kStageB + (odd ? 0 : kSlabs * sg) * kSlab + r * 128;
 #pragma unroll 1
-          for (int c = 0; c < (odd ? 32 : 16); ++c)
+          for (int c = 0; c < (odd ? 32 : 8 * kSlabs); ++c)
             *reinterpret_cast<uint4*>(tok_row + (c >> 3) * kSlab + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
@@ -1018,25 +1033,29 @@ __global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
 
       // ---- the segment's sums, then its output rows
 #pragma unroll
-      for (int k = 0; k < HT; ++k) {
+      for (int o = 16; o > 0; o >>= 1) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], o);
+        for (int k = 0; k < HT / 2; ++k) {
+          l[k].x += __shfl_xor_sync(0xffffffffu, l[k].x, o);
+          l[k].y += __shfl_xor_sync(0xffffffffu, l[k].y, o);
+        }
       }
       const bool okd = warp_wait(kODone, seg_i & 1);
       if (bar_or(kSoftBar, kSoftThreads, !okd)) { aborted = true; break; }
       tc::fence_after_sync();
+      if (lane == 0) {
 #pragma unroll
-      for (int k = 0; k < HT; ++k)
-        if (lane == 0) red[(half * 4 + w4) * HT + k] = l[k];
+        for (int k = 0; k < HT / 2; ++k) *reinterpret_cast<float2*>(red + (sg * 4 + w4) * HT + 2 * k) = l[k];
+      }
       named_bar_sync(bar, 128);
       const int c_first = seg.ustart / sw.share, c_last = (seg.ustart + seg.tiles - 1) / sw.share;
       const bool direct = a.fused && c_first == c_last;
       const int64_t slot = (int64_t)share + seg.n;
-      const int t16 = R == 2 ? half : head0 / kHG, hr = head0 % kHG;  // which partials, head in them
+      const int t16 = R == 2 ? c16 : head0 / kHG, hr = head0 % kHG;  // which partials, head in them
       float* dst = (direct ? a.o_lat + ((size_t)row * a.num_heads + head0) * kDc
                            : o_part(a, t16) + (slot * kHG + hr) * kDc) +
                    w4 * 32 + lane;
-      const bool mine_too = R == 1 || half < nrows;   // (a pair's missing second row)
+      const bool mine_too = R == 1 || c16 < nrows;   // (a pair's missing second row)
       // (all of a row's loads before the first is used)
       float o1[2][HT], o2[2][HT], o3[2][HT];
       auto load_o = [&](int j) {
@@ -1046,16 +1065,16 @@ __global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
         tmem_ld(at + 2 * NH, o3[j & 1]);
       };
       load_o(0);
-      float mine = 0.f, mref = 0.f;
+      float mine = 0.f, mref = 0.f, inv[HT];
 #pragma unroll
       for (int k = 0; k < HT; ++k) {
-        l[k] = (red[half * 4 * HT + k] + red[(half * 4 + 1) * HT + k]) +
-               (red[(half * 4 + 2) * HT + k] + red[(half * 4 + 3) * HT + k]);
-        if (r == k) mine = l[k], mref = ref[k];
-        l[k] = l[k] == 0.f ? 0.f : __fdividef(1.f, l[k]);       // (a NaN sum stays NaN)
+        const float sum = (red[sg * 4 * HT + k] + red[(sg * 4 + 1) * HT + k]) +
+                          (red[(sg * 4 + 2) * HT + k] + red[(sg * 4 + 3) * HT + k]);
+        if (r == k) mine = sum, mref = k & 1 ? nref[k / 2].y : nref[k / 2].x;
+        inv[k] = sum == 0.f ? 0.f : __fdividef(1.f, sum);       // (a NaN sum stays NaN)
       }
       if (r < HT && mine_too) {
-        const float lse = mine == 0.f ? -INFINITY : mref - kRefLog2 + log2f(mine);
+        const float lse = mine == 0.f ? -INFINITY : log2f(mine) - mref;
         if (direct)
           a.lse[(size_t)row * a.num_heads + head0 + r] = lse;
         else
@@ -1068,7 +1087,7 @@ __global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
         if (!mine_too) continue;
 #pragma unroll
         for (int k = 0; k < HT; ++k)
-          dst[(size_t)k * kDc + j * 128] = fmaf(o3[j & 1][k], 0.03125f, o1[j & 1][k] + o2[j & 1][k]) * l[k];
+          dst[(size_t)k * kDc + j * 128] = fmaf(o3[j & 1][k], 0.03125f, o1[j & 1][k] + o2[j & 1][k]) * inv[k];
       }
       tc::fence_before_sync();
       __syncwarp();
@@ -1081,17 +1100,14 @@ __global__ void __launch_bounds__(NH == 16 ? 448 : kThreads, 1)
         if (*merge_flag) {
           const int parts = c_last - c_first + 1;
           // merge_qtile leaves the maxima and the inverse weight sums in its scratch
-          if constexpr (NH == 16) {
-            merge_qtile<kSoftThreads>(a.lse_first, a.o_first, (int64_t)c_first + seg.n, parts, 1,
-                                      a.o_lat + (size_t)row * a.num_heads * kDc, st, scratch,
-                                      [] { named_bar_sync(kSoftBar, kSoftThreads); });
-            if (st < kHG) a.lse[tile * kHG + st] = merged_lse(scratch[st], scratch[kHG + st]);
-          } else if (mine_too) {
-            float* own = scratch + half * (S::merge_bytes / 4);
-            merge_qtile<128>(lse_part(a, t16), o_part(a, t16), (int64_t)c_first + seg.n, parts, 1,
-                             a.o_lat + ((size_t)row * a.num_heads + head0) * kDc, r, own,
-                             [&] { named_bar_sync(bar, 128); });
-            if (r < kHG) a.lse[(size_t)row * a.num_heads + head0 + r] = merged_lse(own[r], own[kHG + r]);
+          // (16 heads by the 256 threads that have them)
+          if (mine_too) {
+            float* own = scratch + c16 * (S::merge_bytes / 4);
+            const int ht = st & 255, hb = head0 - h0 % kHG;
+            merge_qtile<256>(lse_part(a, t16), o_part(a, t16), (int64_t)c_first + seg.n, parts, 1,
+                             a.o_lat + ((size_t)row * a.num_heads + hb) * kDc, ht, own,
+                             [&] { named_bar_sync(kHeadsBar + c16, 256); });
+            if (ht < kHG) a.lse[(size_t)row * a.num_heads + hb + ht] = merged_lse(own[ht], own[kHG + ht]);
           }
         }
       }
@@ -1462,13 +1478,15 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
                              a.scale_log2, a.q8, a.coef, arrive);
   }
   if (e != cudaSuccess) return MLA_ERR_CUDA;
-  auto launch = [&](auto kernel, int smem) {
+  auto launch = [&](auto kernel, int threads, int smem) {
     const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    return r != cudaSuccess ? r : launch_pdl(kernel, dim3(shares * a.groups), dim3(kThreads), smem, st, codes_map, rope_map, a);
+    return r != cudaSuccess
+               ? r
+               : launch_pdl(kernel, dim3(shares * a.groups), dim3(threads), smem, st, codes_map, rope_map, a);
   };
-  e = pair       ? launch(page8_decode_kernel<32, 2>, Sm<32>::alloc)
-      : NH == 16 ? launch(page8_decode_kernel<16, 1>, Sm<16>::alloc)
-                 : launch(page8_decode_kernel<32, 1>, Sm<32>::alloc);
+  e = pair       ? launch(page8_decode_kernel<32, 2>, Sm<32>::threads, Sm<32>::alloc)
+      : NH == 16 ? launch(page8_decode_kernel<16, 1>, Sm<16>::threads, Sm<16>::alloc)
+                 : launch(page8_decode_kernel<32, 1>, Sm<32>::threads, Sm<32>::alloc);
   if (e == cudaSuccess && many_parts)
     e = launch_pdl(page8_merge_kernel, dim3((unsigned)(num_q * H)), dim3(512), 0, st, a);
   if (e == cudaSuccess && merge_proj) {

@@ -26,7 +26,6 @@
 #include "async_copy.cuh"
 #include "internal.h"
 #include "page8.cuh"
-#include "pair_math.cuh"
 #include "rope_pairs.cuh"
 
 namespace mla {
@@ -69,11 +68,6 @@ P8WriteWs write_ws(int64_t tokens, int64_t num_blocks, int bs) {
 
 __device__ __forceinline__ float2 unpack2(uint32_t v) {
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-}
-__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f32x2_pack(a.x, a.y)), "l"(f32x2_pack(b.x, b.y)));
-  return f32x2_unpack(d);
 }
 
 // Shared memory of a page: its tokens' latents and rope keys as given, and what
