@@ -83,17 +83,32 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a)
   const int m0 = a.sinks, m1 = n - a.recent;    // the middle tokens
   auto load_key = [&](int t) {
     const int32_t p = bt[t >> a.bs_shift];
-    if (p < 0 || p >= a.num_blocks) {
-      if ((t & ((1 << a.bs_shift) - 1)) == 0) set_status(a.status, MLA_DEV_BAD_BLOCK);
-      return 0u;
-    }
-    return mass_key(a.mass[((size_t)p << a.bs_shift) + (t & ((1 << a.bs_shift) - 1))]);
+    return p >= 0 && p < a.num_blocks
+               ? mass_key(a.mass[((size_t)p << a.bs_shift) + (t & ((1 << a.bs_shift) - 1))])
+               : 0u;
   };
-#pragma unroll 8
-  for (int t = c0 + tid; t < c1; t += kSelThreads) {
-    const uint32_t k = load_key(t);
-    if (t - c0 < kKeys) sKey[t - c0] = k;
+  // eight tokens of a thread at a time: their pages together, then their masses
+  bool bad_page = false;
+  for (int t0 = c0 + tid; t0 < c1; t0 += 8 * kSelThreads) {
+    int32_t p[8];
+    float m[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) p[u] = t0 + u * kSelThreads < c1 ? bt[(t0 + u * kSelThreads) >> a.bs_shift] : 0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int t = t0 + u * kSelThreads;
+      const bool fine = p[u] >= 0 && p[u] < a.num_blocks;
+      bad_page |= t < c1 && !fine;
+      m[u] = __int_as_float(0x7fffffff);
+      if (t < c1 && fine) m[u] = a.mass[((size_t)p[u] << a.bs_shift) + (t & ((1 << a.bs_shift) - 1))];
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = t0 - c0 + u * kSelThreads;
+      if (t0 + u * kSelThreads < c1 && i < kKeys) sKey[i] = mass_key(m[u]);
+    }
   }
+  if (bad_page) set_status(a.status, MLA_DEV_BAD_BLOCK);
   auto key = [&](int t) { return t - c0 < kKeys ? sKey[t - c0] : load_key(t); };
   const int want = a.budget - a.sinks - a.recent;  // middle tokens that stay
   int need = want;

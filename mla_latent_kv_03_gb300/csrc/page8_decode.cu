@@ -1160,48 +1160,65 @@ __device__ __forceinline__ void merge_weights(const HeadParts& hp, int lane_in_g
   for (int o = G / 2; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
 }
 
-// The merge of many parts of few (row, head)s: one CTA each. Thread (p, c) sums
-// 4 columns over every fourth part, eight loads in flight; the four sums meet
-// in shared memory.
-__global__ void __launch_bounds__(512) page8_merge_kernel(const __grid_constant__ P8Args a) {
-  __shared__ float4 sAcc[3][128];
-  pdl_wait();
+// The merge of many parts of few (row, head)s: two CTAs each, of 256 columns.
+// Thread (p, c) sums 4 columns over every fourth part, eight loads in flight;
+// the four sums meet in shared memory.
+__global__ void __launch_bounds__(256) page8_merge_kernel(const __grid_constant__ P8Args a) {
+  __shared__ float4 sAcc[3][64];
+  __shared__ int4 plan[kSelfMaxRows];
+  __shared__ int plan_total;
+  const int n = blockIdx.x / a.num_heads, h = blockIdx.x % a.num_heads, tid = threadIdx.x;
+  const int p = tid >> 6, c = blockIdx.y * 64 + (tid & 63);
+  const int4* rows = reinterpret_cast<const int4*>(a.ws + ws_layout(a.num_q, 1, a.shares).row_info);
+  int share;
+  if (a.self_plan) {  // (as in the projection below: known before the wait)
+    for (int i = tid; i < (int)a.num_q; i += 256) plan[i] = make_int4(-1, -1, 0, 0);
+    __syncthreads();
+    fill_rows(a, plan, nullptr, tid, 256, 0, 1);
+    __syncthreads();
+    if (tid < 32) scan_rows(plan, (int)a.num_q, tid, &plan_total);
+    __syncthreads();
+    share = plan_total > 0 ? (plan_total + a.shares - 1) / a.shares : 1;
+    rows = plan;
+    pdl_wait();
+  } else {
+    pdl_wait();
+    share = reinterpret_cast<const WsHeader*>(a.ws)->share;
+  }
   pdl_launch_dependents();
-  const int n = blockIdx.x / a.num_heads, h = blockIdx.x % a.num_heads;
-  const int p = threadIdx.x >> 7, c = threadIdx.x & 127;
-  const HeadParts hp = head_parts(
-      a, reinterpret_cast<const int4*>(a.ws + ws_layout(a.num_q, 1, a.shares).row_info),
-      reinterpret_cast<const WsHeader*>(a.ws)->share, n, h);
+  const HeadParts hp = head_parts(a, rows, share, n, h);
+  float4 v[8];
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (s0 + 4 * u < hp.count)
+        v[u] = *reinterpret_cast<const float4*>(hp.o + (size_t)(s0 + 4 * u) * kHG * kDc + 4 * c);
+  };
+  load(p);  // on their way while the weights are found
   float m, den;
-  merge_weights<32>(hp, threadIdx.x & 31, m, den);
+  merge_weights<32>(hp, tid & 31, m, den);
   const float inv = den == 0.f ? 0.f : 1.f / den, b = m == -INFINITY ? 0.f : m;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
   for (int s0 = p; s0 < hp.count; s0 += 32) {
-    float4 v[8];
-    float w[8];
+    if (s0 != p) load(s0);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int s = min(s0 + 4 * u, hp.count - 1);
-      v[u] = *reinterpret_cast<const float4*>(hp.o + (size_t)s * kHG * kDc + 4 * c);
-      w[u] = s0 + 4 * u < hp.count ? fast_exp2(hp.lse[s * kHG] - b) * inv : 0.f;
-    }
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      if (s0 + 4 * u >= hp.count) break;
-      acc.x = fmaf(w[u], v[u].x, acc.x);
-      acc.y = fmaf(w[u], v[u].y, acc.y);
-      acc.z = fmaf(w[u], v[u].z, acc.z);
-      acc.w = fmaf(w[u], v[u].w, acc.w);
-    }
+    for (int u = 0; u < 8; ++u)
+      if (s0 + 4 * u < hp.count) {
+        const float w = fast_exp2(hp.lse[(s0 + 4 * u) * kHG] - b) * inv;
+        acc.x = fmaf(w, v[u].x, acc.x);
+        acc.y = fmaf(w, v[u].y, acc.y);
+        acc.z = fmaf(w, v[u].z, acc.z);
+        acc.w = fmaf(w, v[u].w, acc.w);
+      }
   }
-  if (p > 0) sAcc[p - 1][c] = acc;
+  if (p > 0) sAcc[p - 1][tid & 63] = acc;
   __syncthreads();
   if (p == 0) {
 #pragma unroll
     for (int u = 0; u < 3; ++u) {
-      const float4 v = sAcc[u][c];
-      acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+      const float4 x = sAcc[u][tid];
+      acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
     }
     const size_t row = (size_t)n * a.num_heads + h;
     *reinterpret_cast<float4*>(a.o_lat + row * kDc + 4 * c) = acc;
@@ -1367,16 +1384,26 @@ struct MassArgs {
   float* mass;
 };
 __global__ void __launch_bounds__(256) page8_mass_kernel(MassArgs a) {
-  pdl_wait();
-  pdl_launch_dependents();
+  // (what the caller gave and the old mass are there, see page8_decode_kernel;
+  // the scores and sums have to be waited for)
   const int b = blockIdx.y, t = blockIdx.x * 256 + threadIdx.x;
   const int len = a.seq_lens[b], q0 = a.query_start_loc[b], q1 = a.query_start_loc[b + 1];
   const int ql = q1 - q0;
   const int64_t max_tokens = (int64_t)a.max_blocks * a.block_size;
-  if (q0 < 0 || q1 > a.num_q || ql <= 0 || ql > len || (int64_t)len > max_tokens) return;
-  if (t >= len) return;
-  const int32_t p = a.block_table[(size_t)b * a.max_blocks + t / a.block_size];
-  if (p < 0 || p >= a.num_blocks) return;
+  bool mine = q0 >= 0 && q1 <= a.num_q && ql > 0 && ql <= len && (int64_t)len <= max_tokens && t < len;
+  float* m = a.mass;
+  float old = 0.f;
+  if (mine) {
+    const int32_t p = a.block_table[(size_t)b * a.max_blocks + t / a.block_size];
+    mine = p >= 0 && p < a.num_blocks;
+    if (mine) {
+      m += (size_t)p * a.block_size + t % a.block_size;
+      if (a.decay > 0.f) old = a.decay * *m;
+    }
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  if (!mine) return;
   float sum = 0.f;
   for (int n = max(q0, q0 + t - (len - ql)); n < q1; ++n) {  // rows at or behind token t
     for (int g = 0; g < a.groups; ++g) {
@@ -1386,12 +1413,11 @@ __global__ void __launch_bounds__(256) page8_mass_kernel(MassArgs a) {
 #pragma unroll
       for (int k = 0; k < kHG / 4; ++k) {
         const float4 x = s[k], y = e[k];
-        sum += fast_exp2(x.x - y.x) + fast_exp2(x.y - y.y) + fast_exp2(x.z - y.z) + fast_exp2(x.w - y.w);
+        sum += (fast_exp2(x.x - y.x) + fast_exp2(x.y - y.y)) + (fast_exp2(x.z - y.z) + fast_exp2(x.w - y.w));
       }
     }
   }
-  float* m = a.mass + (size_t)p * a.block_size + t % a.block_size;
-  *m = a.decay > 0.f ? fmaf(a.decay, *m, sum) : sum;
+  *m = old + sum;
 }
 
 mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache8,
@@ -1488,7 +1514,7 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
       : NH == 16 ? launch(page8_decode_kernel<16, 1>, Sm<16>::threads, Sm<16>::alloc)
                  : launch(page8_decode_kernel<32, 1>, Sm<32>::threads, Sm<32>::alloc);
   if (e == cudaSuccess && many_parts)
-    e = launch_pdl(page8_merge_kernel, dim3((unsigned)(num_q * H)), dim3(512), 0, st, a);
+    e = launch_pdl(page8_merge_kernel, dim3((unsigned)(num_q * H), 2), dim3(256), 0, st, a);
   if (e == cudaSuccess && merge_proj) {
     auto project = [&](auto kernel, int rows, int smem) {
       const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
