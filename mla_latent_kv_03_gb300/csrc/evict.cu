@@ -51,7 +51,7 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
 }
 __device__ __forceinline__ int ld_cluster(uint32_t addr) {
   int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
 
@@ -134,31 +134,29 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a)
     }
     if (tid < 256) hist[(pass + 1) % 3][tid] = 0;
     cl::sync();
-    // warp 0: the cluster's counts, 8 digits a lane from the top down
-    if (warp == 0) {
-      int c[8], sum = 0;
+    // the cluster's count of digit 255 - tid, and of the digits above it
+    int count = 0, above = 0;
+    if (tid < 256) {
+      const uint32_t at = smem_u32(&h[255 - tid]);
+      int v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int d = 255 - (lane * 8 + i);
-        int v = 0;
-        for (int r = 0; r < CL; ++r) v += ld_cluster(cl::map(smem_u32(&h[d]), r));
-        c[i] = v;
-        sum += v;
-      }
-      int before = sum;
+      for (int r = 0; r < 8; ++r) v[r] = r < CL ? ld_cluster(cl::map(at, r)) : 0;
+      count = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+      above = count;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += v;
+        const int u = __shfl_up_sync(0xffffffffu, above, o);
+        if (lane >= o) above += u;
       }
-      before -= sum;
-      if (before < need && need <= before + sum) {  // (one lane)
-        int left = need - before, i = 0;
-#pragma unroll
-        for (int j = 0; j < 7; ++j)
-          if (i == j && c[j] < left) left -= c[j], ++i;
-        sPick = 255 - (lane * 8 + i);
-        sNeed = left;
+      if (lane == 31) sAbove[warp] = above;
+      above -= count;
+    }
+    __syncthreads();
+    if (tid < 256) {
+      for (int w = 0; w < warp; ++w) above += sAbove[w];
+      if (above < need && need <= above + count) {  // (one thread)
+        sPick = 255 - tid;
+        sNeed = need - above;
       }
     }
     __syncthreads();
