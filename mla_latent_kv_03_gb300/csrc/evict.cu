@@ -248,10 +248,11 @@ cudaError_t launch_select(const SelectArgs& a, int batch, cudaStream_t stream) {
 
 // ---------------------------------------------------------------------------
 // compact. One CTA per destination page: the largest scale among the pages its
-// rows come from, then one warp per row (16 bytes of codes a lane, the rope
-// part by 8 lanes). Rows whose page has that scale are copied as they are;
-// the others are recoded. Source and destination pages are distinct, so the
-// CTAs share nothing they write.
+// rows come from, then the rows in pieces of 16 bytes (32 of codes, 8 of rope
+// values each), every thread's pieces on their way before the first is stored.
+// Rows whose page has that scale are copied as they are; the others are
+// recoded. Source and destination pages are distinct, so the CTAs share nothing
+// they write.
 // Bound: HBM, each kept row read once and written once.
 // ---------------------------------------------------------------------------
 constexpr int kCmpThreads = 256;
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(kCmpThreads) page8_compact_kernel(CompactArgs 
   __shared__ float sScale[BS];
   pdl_wait();
   pdl_launch_dependents();
-  const int b = blockIdx.y, j = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.y, j = blockIdx.x, tid = threadIdx.x;
   const int n = a.new_lens[b];
   if (n < 0 || n > a.budget || (int64_t)n > (int64_t)a.dst_max * BS) {
     if (tid == 0 && j == 0) set_status(a.status, MLA_DEV_BAD_SEQ);
@@ -315,19 +316,26 @@ __global__ void __launch_bounds__(kCmpThreads) page8_compact_kernel(CompactArgs 
 #pragma unroll
   for (int r = 0; r < BS; ++r) top = fmaxf(top, sScale[r]);
   if (tid == 0) a.scales[dp] = top;
-  for (int r = warp; r < rows; r += kCmpThreads / 32) {
-    const int64_t slot = sSlot[r];
-    if (slot < 0) continue;
-    const uint8_t* src = a.cache8 + slot * kRow8;
-    uint8_t* dst = a.cache8 + ((int64_t)dp * BS + r) * kRow8;
-    uint4 c = *reinterpret_cast<const uint4*>(src + lane * 16);
-    uint4 k = make_uint4(0, 0, 0, 0);
-    if (lane < 8) k = *reinterpret_cast<const uint4*>(src + kDc + lane * 16);
-    if (sScale[r] != top) c = p8_recode16(c, sScale[r] / top);
-    *reinterpret_cast<uint4*>(dst + lane * 16) = c;
-    if (lane < 8) *reinterpret_cast<uint4*>(dst + kDc + lane * 16) = k;
-    if (a.mass && lane == 0) a.mass[(int64_t)dp * BS + r] = a.mass[slot];
+  constexpr int kPieces = kRow8 / 16, kPer = (BS * kPieces + kCmpThreads - 1) / kCmpThreads;  // pieces of a row, of a thread
+  uint4 c[kPer];
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int i = tid + u * kCmpThreads, r = i / kPieces;
+    if (r < rows && sSlot[r] >= 0)
+      c[u] = __ldcs(reinterpret_cast<const uint4*>(a.cache8 + sSlot[r] * kRow8) + i % kPieces);
   }
+  float m = 0.f;
+  const bool with_mass = a.mass && tid < rows && sSlot[tid] >= 0;
+  if (with_mass) m = a.mass[sSlot[tid]];
+  uint4* dst = reinterpret_cast<uint4*>(a.cache8 + (int64_t)dp * BS * kRow8);
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int i = tid + u * kCmpThreads, r = i / kPieces;
+    if (r >= rows || sSlot[r] < 0) continue;
+    if (i % kPieces < kDc / 16 && sScale[r] != top) c[u] = p8_recode16(c[u], sScale[r] / top);
+    dst[i] = c[u];
+  }
+  if (with_mass) a.mass[(int64_t)dp * BS + tid] = m;
 }
 
 }  // namespace
