@@ -273,7 +273,7 @@ struct CompactArgs {
 };
 
 template <int BS>
-__global__ void __launch_bounds__(kCmpThreads) page8_compact_kernel(CompactArgs a) {
+__global__ void __launch_bounds__(kCmpThreads, 4) page8_compact_kernel(CompactArgs a) {
   __shared__ int64_t sSlot[BS];
   __shared__ float sScale[BS];
   pdl_wait();
