@@ -330,7 +330,8 @@ mla_status mla_page8_cache_write(const mla_config* cfg, const void* c_kv, const 
  * mla_page8_decode -- attention of absorbed queries over page-scaled pages,
  * projected to v_head_dim: mla_decode_paged_combine_fp8 and mla_out_proj for
  * every supported head count and for prefill chunks (conventions, checks and
- * device status bits of mla_decode_paged; num_q <= 48 * 1024).
+ * device status bits of mla_decode_paged; num_q <= 48 * 1024, block tables of
+ * at most 2^30 tokens, and num_q times that many tokens at most 2^36).
  *   s_t = softmax_scale * (S_t q_abs[n,h,0:512] . code_t + q_abs[n,h,512:576] . k_t)
  *   out[n,h] = (sum_t softmax(s)_t S_t code_t) W_uv[h],   S_t = page_scales of t's page
  *   q_abs [num_q, H, 576] bf16; W_uv [H, 512, 128] bf16; out [num_q, H, 128]

@@ -356,7 +356,7 @@ mla_status mla_evict_select(const mla_config* cfg, const float* mass, int64_t nu
       budget < 1 || (int64_t)sinks + recent > budget)
     return MLA_ERR_INVALID_ARGUMENT;
   if (num_blocks > ((int64_t)1 << 31) / cfg->block_size ||
-      max_blocks_per_seq > ((int64_t)1 << 30) / cfg->block_size)
+      max_blocks_per_seq > ((int64_t)1 << 30) / cfg->block_size || batch > (1 << 27))
     return MLA_ERR_UNSUPPORTED;
   if (batch == 0) return MLA_OK;
   if (!mass || !block_table || !seq_lens || !keep || !new_lens) return MLA_ERR_INVALID_ARGUMENT;

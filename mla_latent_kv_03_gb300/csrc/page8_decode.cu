@@ -1551,8 +1551,10 @@ size_t mla_page8_decode_workspace_size(const mla_config* cfg, int64_t num_q, int
                                        int32_t max_blocks_per_seq, int32_t with_mass) {
   if (validate_config(cfg) != MLA_OK || cfg->dtype != MLA_BF16 || num_q < 0 ||
       num_q > 48 * 1024 || batch < 0 || max_blocks_per_seq < 0 ||
-      max_blocks_per_seq > ((int64_t)1 << 31) / cfg->block_size)
+      max_blocks_per_seq > ((int64_t)1 << 30) / cfg->block_size)
     return 0;
+  // (the split counts units of 64 tokens and a row in 32 bits)
+  if (num_q * (((int64_t)max_blocks_per_seq * cfg->block_size + kTile - 1) / kTile) > (int64_t)1 << 30) return 0;
   const int C = split_ctas(cfg), H = cfg->num_heads;
   if (C <= 0) return 0;
   return p8_ws(num_q, H, use_pairs(H, num_q, batch), p8_shares(H, C), (int64_t)max_blocks_per_seq * cfg->block_size,

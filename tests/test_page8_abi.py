@@ -86,6 +86,7 @@ def _decode(lib, cfg, with_mass, **kw):
     (dict(ws=ctypes.c_void_p((1 << 20) + 128)), 1), (dict(batch=0), 1), (dict(batch=-1), 1),
     (dict(nq=-1), 1), (dict(nb=-1), 1), (dict(mb=-1), 1), (dict(nq=48 * 1024 + 1), 2),
     (dict(nb=(1 << 31) // 64 + 1), 2), (dict(wsb=4096), 3),
+    (dict(mb=(1 << 30) // 64 + 1), 2), (dict(nq=48 * 1024, mb=(1 << 30) // (48 * 1024) + 1), 2),
 ])
 def test_decode_refuses(lib, with_mass, kw, want):
     assert _decode(lib, _cfg(), with_mass, **kw) == want
@@ -127,7 +128,7 @@ def _select(lib, cfg, **kw):
     (dict(recent=-1), 1), (dict(budget=0), 1), (dict(sinks=5, recent=4), 1),
     (dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1, budget=2 ** 31 - 1), 1), (dict(batch=-1), 1),
     (dict(nb=-1), 1), (dict(mb=-1), 1), (dict(nb=(1 << 31) // 64 + 1), 2),
-    (dict(mb=(1 << 30) // 64 + 1), 2), (dict(batch=0, mass=NONE), 0),
+    (dict(mb=(1 << 30) // 64 + 1), 2), (dict(batch=(1 << 27) + 1), 2), (dict(batch=0, mass=NONE), 0),
 ])
 def test_select_refuses(lib, kw, want):
     assert _select(lib, _cfg(), **kw) == want
