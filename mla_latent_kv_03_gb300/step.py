@@ -201,8 +201,11 @@ class MlaDecodeStep:
         """Cut every sequence to `budget` tokens, moved into the pages of
         dst_block_table, which becomes the sequences' table. Returns (keep,
         new lengths)."""
-        keep = torch.empty((self.w.batch, budget), dtype=torch.int32, device=self.device)
-        lens = torch.empty(self.w.batch, dtype=torch.int32, device=self.device)
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        with torch.cuda.stream(stream):  # memory of the stream that writes it
+            keep = torch.empty((self.w.batch, budget), dtype=torch.int32, device=self.device)
+            lens = torch.empty(self.w.batch, dtype=torch.int32, device=self.device)
         L.mla_evict_select(self.cfg, self.p8_mass, self.p8_table, self.p8_lens, sinks, recent, keep,
                            lens, dev_status=self.status, stream=stream)
         L.mla_page8_compact(self.cfg, self.p8_cache, self.p8_scales, self.p8_mass, self.p8_table,

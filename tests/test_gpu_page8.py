@@ -633,6 +633,23 @@ def test_write_decode_evict_decode():
         assert np.array_equal(new[:, 512:], old[keep.cpu().numpy()[b, :n[b]], 512:])
 
 
+def test_evict_on_a_stream_writes_memory_that_no_other_stream_still_uses():
+    w, s, dst, budget = _together()
+    side = torch.cuda.Stream()
+    s.page8_decode(0.9)
+    torch.cuda.synchronize()
+    old = torch.empty((4, budget), dtype=torch.int32, device=DEV)   # as keep will be
+    torch.cuda._sleep(100_000_000)
+    old.fill_(-7)
+    del old
+    keep, lens = s.page8_evict(budget, 4, 20, dst, stream=side)
+    torch.cuda.synchronize()
+    for b, n in enumerate(lens.tolist()):
+        k = keep[b].tolist()
+        assert n == min(budget, int(w.seq_lens[b])) and -7 not in k
+        assert k[:n] == sorted(set(k[:n])) and k[n:] == [-1] * (budget - n)
+
+
 def test_the_same_run_on_another_stream_and_captured():
     w, s, dst, budget = _together()
     _run_together(s, w, dst, budget)
@@ -673,3 +690,113 @@ def test_the_same_run_on_another_stream_and_captured():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(s3.out, want) and torch.equal(s3.p8_mass, want_mass)
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Different caches and workspaces; every call fills the device, so parts
+    of the two run side by side and behind one another."""
+    wants, runs = [], []
+    for name, seed in (("many_rows", 5), ("h128", 6)):
+        w, s = _step(name, with_mass=True, seed=seed)
+        m0 = s.p8_mass.clone()
+        s.page8_decode(0.5)
+        torch.cuda.synchronize()
+        wants.append((s.out.clone(), s.p8_mass.clone()))
+        s.p8_mass.copy_(m0)
+        s.out.fill_(float("nan"))
+        runs.append((s, m0, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, m0, st in runs:
+            with torch.cuda.stream(st):
+                s.p8_mass.copy_(m0)
+                s.page8_decode(0.5)
+    torch.cuda.synchronize()
+    for (s, _, _), (out, mass) in zip(runs, wants):
+        assert torch.equal(s.out, out) and torch.equal(s.p8_mass, mass)
+
+
+def test_two_captured_graphs_that_share_a_workspace():
+    """Two batches of different size, a workspace that fits either, the graphs
+    replayed in turn on one stream: neither finds what the other left."""
+    ws, wws, steps = None, None, []
+    for name in ("chunks", "speculative"):
+        w, s = _step(name)
+        steps.append(s)
+        if ws is None or s.p8_ws.numel() > ws.numel():
+            ws = s.p8_ws
+        if wws is None or s.p8_write_ws.numel() > wws.numel():
+            wws = s.p8_write_ws
+    wants, graphs = [], []
+    for s in steps:
+        s.p8_ws, s.p8_write_ws = ws, wws
+        state = s.p8_cache.clone()
+        s.page8_write_new()
+        wants.append(s.page8_decode().clone())
+        torch.cuda.synchronize()
+        s.p8_cache.copy_(state)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            s.page8_write_new()
+            s.page8_decode()
+        graphs.append(g)
+    for k in (0, 1, 1, 0, 0, 1):
+        steps[k].out.fill_(float("nan"))
+        graphs[k].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(steps[k].out, wants[k])
+    assert status_bits(ws) == 0
+
+
+def test_sequences_may_share_pages_and_repeat_them():
+    """A common prefix in two block tables, and one page three times in a row."""
+    w, s = _step("tails_bs64")
+    table = w.block_table.copy()
+    table[7, :2] = table[6, :2]
+    table[7, 3:6] = table[7, 2]
+    s.block_table.copy_(dev(table, torch.int32))
+    got = s.page8_decode()
+    torch.cuda.synchronize()
+    assert status_bits(s.p8_ws) == 0
+    check_out(w, s, got, oracle_rows(s), table)
+
+
+def test_rows_behind_the_last_sequence_are_zeros():
+    """A padded batch: more rows than query_start_loc names (as the other
+    decodes: a row that sees no token is zeros), in each split's form."""
+    for name in ("speculative", "h128", "many_rows"):
+        w, s = _step(name)
+        qsl = w.query_start_loc.copy()
+        qsl[-1] = qsl[-2]                       # the last sequence's rows belong to none
+        want = s.page8_decode().clone()
+        s.query_start_loc.copy_(dev(qsl, torch.int32))
+        s.out.fill_(float("nan"))
+        got = s.page8_decode()
+        torch.cuda.synchronize()
+        assert status_bits(s.p8_ws) == 0
+        n = int(qsl[-1])
+        assert torch.all(got[n:] == 0)
+        err = (got[:n].double() - want[:n].double()).abs().max() / want[:n].double().abs().max()
+        assert err <= 2.0 ** -7                 # (another split, another order of sums)
+
+
+def test_a_token_kept_twice_is_moved_twice():
+    w, s = _step("tails_bs64", with_mass=True)
+    b, n = 7, 5
+    keep = dev(np.array([[3, 3, 700, 3, 12]]), torch.int32)
+    lens = dev(np.array([n]), torch.int32)
+    dst = dev(np.array([[w.num_blocks]]), torch.int32)
+    s2 = torch.zeros((1, w.block_size, 640), dtype=torch.uint8, device=DEV)
+    cache = torch.cat([s.p8_cache, s2])
+    scales = torch.cat([s.p8_scales, s.p8_scales.new_zeros(1)])
+    mass = torch.cat([s.p8_mass, s.p8_mass.new_zeros((1, w.block_size))])
+    L.mla_page8_compact(s.cfg, cache, scales, mass, s.block_table[b:b + 1].contiguous(), keep, lens, dst,
+                        dev_status=s.status)
+    torch.cuda.synchronize()
+    assert status_bits(s.status) == 0
+    for row, t in enumerate([3, 3, 700, 3, 12]):
+        p, r = int(w.block_table[b][t // w.block_size]), t % w.block_size
+        assert torch.equal(cache[-1, row, 512:], cache[p, r, 512:])
+        assert float(mass[-1, row]) == float(mass[p, r])
+        if float(scales[p]) == float(scales[-1]):
+            assert torch.equal(cache[-1, row], cache[p, r])
