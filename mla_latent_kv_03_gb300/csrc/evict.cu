@@ -23,14 +23,16 @@ namespace {
 // beyond that is read again from the cache in every pass). The CTAs of a
 // cluster meet once a pass: each adds up all their histograms through
 // distributed shared memory.
-// Bound: latency (one pass over 4 bytes a token, five meetings). More than one
-// CTA pays from about 4,096 tokens a CTA.
+// Bound: latency. One pass over 4 bytes a token, a histogram, a meeting and a
+// scan for each of the four digits, and the two steps at the end: 10.8 us for 64
+// sequences of 4,096 tokens on one GB300 (2 CTAs each), 26.6 us for 3 of 131,072
+// (8 each), of which reading the masses at HBM's rate would be 0.2 us.
 // ---------------------------------------------------------------------------
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kKeys = 40 * 1024;              // keys a CTA holds
 constexpr int kSelSmem = kKeys * 4;
-constexpr int kSelPiece = 2048;               // tokens a CTA takes before another joins
+constexpr int kSelPiece = 1024;               // tokens a CTA takes before another joins
 
 struct SelectArgs {
   const float* mass;
@@ -214,12 +216,22 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a)
   cl::sync();  // the others may still read this CTA's totals
 }
 
-// CTAs that share a sequence of up to `tokens`: measured on one GB300 at 64
-// sequences of 4,096 tokens and at 3 of 131,072 (see the table of measurements
-// beside the launch).
-int select_cluster(int64_t tokens) {
+// CTAs that share a sequence of up to `tokens`: another as long as each has more
+// than kSelPiece tokens and all of them run at once (clusters of 8 place badly
+// beyond 64 CTAs), and wherever the keys would not fit otherwise. Measured on one
+// GB300, us with 1 / 2 / 4 / 8 CTAs (the choice marked):
+//     1 x 3,000     10.8   10.4   *9.6   10.3
+//    64 x 2,048     10.3   *9.6   14.6   27.8
+//    64 x 8,192     15.8  *12.6   18.5   31.8
+//   256 x 4,096    *19.6   30.1   47.2  100.9
+//    16 x 16,384    24.5   16.2  *12.8   17.3
+//     3 x 131,072  309.3  130.9   43.3  *26.6
+//    64 x 131,072  318.5  136.1  *90.5   99.9
+int select_cluster(int64_t tokens, int batch) {
   int c = 1;
-  while (c < 8 && tokens > (int64_t)c * kSelPiece) c *= 2;
+  while (c < 8 && (tokens > (int64_t)c * kKeys ||
+                   (tokens > (int64_t)c * kSelPiece && (int64_t)batch * 2 * c <= (c == 4 ? 64 : 152))))
+    c *= 2;
   return c;
 }
 
@@ -365,7 +377,7 @@ mla_status mla_evict_select(const mla_config* cfg, const float* mass, int64_t nu
     return MLA_ERR_INVALID_ARGUMENT;
   const int shift = cfg->block_size == 16 ? 4 : cfg->block_size == 32 ? 5 : 6;
   const SelectArgs a{mass, num_blocks, block_table, max_blocks_per_seq, seq_lens, shift, sinks,
-                     recent, budget, select_cluster((int64_t)max_blocks_per_seq << shift), keep,
+                     recent, budget, select_cluster((int64_t)max_blocks_per_seq << shift, batch), keep,
                      new_lens, dev_status};
   const cudaError_t e = launch_select(a, batch, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;

@@ -126,9 +126,11 @@ struct P8Ws {
 };
 int group_heads(int H) { return H >= 32 ? 32 : 16; }
 // Rows go in pairs where the 16 heads of one leave half of the columns empty
-// and at least every other sequence has a second row. (Rows of their own take
-// the narrower kernel, which is quicker by itself.)
-bool use_pairs(int H, int64_t num_q, int32_t batch) { return H == 16 && 2 * num_q >= 3 * (int64_t)batch; }
+// and two of three sequences have a second row. (Rows of their own take the
+// narrower kernel, which is quicker by itself.) 32 sequences of 4,096 tokens on
+// one GB300, us by rows / in pairs: 32 rows 34.8 / 39.3, 48 rows 35.5 / 36.2,
+// 56 rows 37.9 / 36.4, 64 rows 41.8 / 36.8; 8 chunks of 128 rows 125 / 99.
+bool use_pairs(int H, int64_t num_q, int32_t batch) { return H == 16 && 3 * num_q >= 5 * (int64_t)batch; }
 // Shares of the work: with one CTA per group to a share, about num_ctas CTAs.
 int p8_shares(int H, int num_ctas) {
   const int s = num_ctas / (H / group_heads(H));
@@ -501,11 +503,8 @@ __device__ __forceinline__ void zero_other_rows(const P8Args& a, const int4* row
   }
 }
 
-// (Registers: 16 heads are held to 128 a thread, not the 168 that are free,
-// which leaves room on the SM for a CTA of the query kernel, so that a decode
-// CTA starts before that one has ended.)
 template <int NH, int R>
-__global__ void __launch_bounds__(NH == 16 ? 448 : Sm<32>::threads, 1)
+__global__ void __launch_bounds__(Sm<NH>::threads, 1)
     page8_decode_kernel(const __grid_constant__ CUtensorMap codes_map,
                         const __grid_constant__ CUtensorMap rope_map, const __grid_constant__ P8Args a) {
   static_assert(R == 1 || NH == 32, "a pair is 2 x 16 heads");
@@ -1483,13 +1482,20 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
   a.o_lat = reinterpret_cast<float*>(ws + L.o_lat);
   a.lse = reinterpret_cast<float*>(ws + L.lse);
   a.scores = with_mass ? reinterpret_cast<float*>(ws + L.scores) : nullptr;
-  // Who merges the splits. From 256 rows on most tiles are whole and the rest
-  // is merged in the decode kernel; the tensor-core projection follows. Below,
-  // the merge goes into the projection, unless there are few tiles, each cut
-  // into so many parts that the merge has to spread over the device first.
-  const bool many_parts = num_q * 4 < shares;
-  a.fused = num_q >= 256 && !many_parts;
-  const bool merge_proj = num_q < 256 && !many_parts;
+  // Who merges the splits. With many outputs (rows x heads) most tiles are
+  // whole and the rest is merged in the decode kernel; the tensor-core
+  // projection follows. Below, the merge goes into the projection, unless there
+  // are so few outputs, each cut into many parts, that the merge has to spread
+  // over the device first. Measured on one GB300, us:
+  //   rows x heads       320 x 16  448 x 16  56 x 128  256 x 32  256 x 128
+  //   in the projection    66.7      82.7      59.4      77.2      223.4
+  //   in the decode        68.1      83.0      56.4      74.5      181.1
+  //   rows x heads (65,536 tokens)  1 x 16  8 x 16  16 x 16  32 x 16  1 x 128  4 x 128
+  //   in the projection              61.1    27.4    24.9     23.2      52.5     45.7
+  //   spread                         26.6    23.6    25.2     28.5      46.8     51.2
+  const bool many_parts = num_q * H < 256;
+  a.fused = num_q * H >= 7168;
+  const bool merge_proj = !a.fused && !many_parts;
   cudaError_t e = cudaSuccess;
   if (!a.self_plan) {
     e = cudaFuncSetAttribute(page8_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)num_q * 4);
@@ -1522,6 +1528,7 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
                               : launch_pdl(kernel, dim3((unsigned)((num_q + rows - 1) / rows), H), dim3(256), smem,
                                            st, a, (const __nv_bfloat16*)W_uv, (__nv_bfloat16*)out);
     };
+    // (40 rows of 16 heads: 24.3 us by 8, 25.9 by 16; 96 rows: 40.3 and 36.4)
     e = (num_q + 7) / 8 * H <= (int64_t)shares * a.groups
             ? project(page8_merge_proj_kernel<8>, 8, Mp<8>::bytes)
             : project(page8_merge_proj_kernel<16>, 16, Mp<16>::bytes);

@@ -126,7 +126,7 @@ class Writer:
 
 
 @pytest.mark.parametrize("bs", [16, 32, 64])
-@pytest.mark.parametrize("n", [1, 2, 63, 64, 65, 1000, 1024, 1025, 2500])
+@pytest.mark.parametrize("n", [1, 2, 63, 64, 65, 1000, 1024, 1025, 2048, 2049, 2500])
 def test_write_fills_pages(bs, n):
     w = Writer(nb=n // bs + 3, bs=bs, seed=n + bs, interleaved=bool(n & 1))
     w.write(np.arange(n) + bs // 2, outliers=0.02)
@@ -195,6 +195,11 @@ CASES = {
     "speculative": ([130, 500, 2, 66], [2, 3, 2, 1], 16, 32),
     "mixed": ([300, 64, 5, 1, 190], [100, 1, 1, 1, 33], 16, 16),
     "long": ([9000], [1], 16, 64),
+    # the splits merged in the decode itself: pairs, single rows, wide groups
+    "merged_pairs": ([700, 20, 9], [450, 1, 9], 16, 64),
+    "merged_rows": ([3 + 7 * i % 150 for i in range(450)], [1] * 450, 16, 16),
+    "merged_h128": ([200, 70, 130], [33, 20, 10], 128, 64),
+    "merged_h32": ([260, 90], [200, 40], 32, 32),
 }
 
 
@@ -266,7 +271,8 @@ def test_decode_vs_oracle(name, num_ctas):
 
 
 @pytest.mark.parametrize("decay", [0.0, 0.75, 1.0])
-@pytest.mark.parametrize("name", ["tails_bs64", "bs16_h32", "h128", "empty_rows", "chunks", "many_rows", "long"])
+@pytest.mark.parametrize("name", ["tails_bs64", "bs16_h32", "h128", "empty_rows", "chunks", "many_rows", "long",
+                                  "merged_pairs", "merged_h128"])
 def test_mass_vs_oracle(name, decay):
     w, s = _step(name, 0 if name != "chunks" else 5, with_mass=True)
     if decay == 0:
