@@ -26,7 +26,7 @@
 // output as part of the weight: the columns hold 2^(s_t - ref) S_p, and the
 // softmax sum adds the same number divided by S_p again. The running reference
 // of a head follows s_t + log2 S_p, and O is rescaled in TMEM only when it is
-// outgrown by more than 2^10.
+// outgrown by more than 2^11.75.
 //
 // NH = 16 or 32 heads of one row make a column group; with 16 heads and several
 // rows a sequence (R = 2), two rows that follow one another do, each with its
@@ -72,7 +72,9 @@ constexpr int kSoftWarp0 = 4;
 constexpr int kSoftBar = 1, kHeadsBar = 2, kGroupBar = 4;
 constexpr float kRefLog2 = 4.f;               // a weight equal to the reference is held as 2^4
 constexpr float kNoRef = 1e38f;
-constexpr float kGrowLog2 = 10.f;             // the reference follows when outgrown by 2^10
+// the reference follows when outgrown by 2^11.75: a weight of 2^15.75 is still
+// below e5m2's largest number, 1.75 * 2^15
+constexpr float kGrowLog2 = 11.75f;
 constexpr uint32_t kTmemCols = 512, kSCol = 0, kOCol = 128;
 
 struct P8Args {
@@ -264,12 +266,11 @@ __device__ __forceinline__ bool bar_or(int id, int nthreads, bool v) {
   return r != 0;
 }
 
-// The largest of a value over the warp (NaN does not count).
+// The largest of a value over the warp (NaN does not count, unless all are).
 __device__ __forceinline__ float warp_max(float x) {
-  int i = __float_as_int(isnan(x) ? -INFINITY : x);
-  i ^= (i >> 31) & 0x7fffffff;  // the integer order of the floats
-  i = __reduce_max_sync(0xffffffffu, i);
-  return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // The log-sum-exp of merged parts from their largest and 1 / the weight sum
@@ -913,69 +914,39 @@ __global__ void __launch_bounds__(Sm<NH>::threads, 1)
         float top = fmaxf(y[0].x, y[0].y);
 #pragma unroll
         for (int k = 1; k < HT / 2; ++k) top = fmax3(top, y[k].x, y[k].y);
+        uint32_t grown = 0;
+        float fl = 1.f;   // lane k: what head k's sums are multiplied by
         if (bar_or(bar, 128, !fine || top > kRefLog2 + kGrowLog2)) {
           // every head's largest weight (no branches between them), lane k
           // holding head k's
-          float mx = -INFINITY, old = 0.f;
+          float mx = -INFINITY;
 #pragma unroll
           for (int k = 0; k < HT; ++k) {
             const float m = warp_max(k & 1 ? x[k / 2].y : x[k / 2].x);
-            if (lane == k) mx = m, old = k & 1 ? nref[k / 2].y : nref[k / 2].x;
+            if (lane == k) mx = m;
           }
           if (lane < HT) red[(sg * 4 + w4) * HT + lane] = mx;
-          // (the output products of tile i - 1 must have landed before O is rescaled)
-          if (t > 0 && fine) fine = warp_wait(kPVDone + (slot ^ 1), ((i - 1) >> 1) & 1);
           if (bar_or(bar, 128, !fine)) {
             // (the other groups meet this at the end of the segment or here)
             bar_or(kSoftBar, kSoftThreads, true);
             aborted = true;
             break;
           }
-          bool grew = false;
-          float now = old, fl = 1.f;   // lane k: head k's nref and factor
-          if (lane < HT) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) mx = fmaxf(mx, red[(sg * 4 + u) * HT + lane]);
-            grew = mx + old > kRefLog2 + kGrowLog2;
-            if (grew) {
-              now = kRefLog2 - mx;
-              fl = fast_exp2(now - old);   // (from kNoRef: 0)
-            }
+          for (int k = 0; k < HT; ++k) {
+            const float* m = red + sg * 4 * HT + k;
+            const float mx = fmaxf(fmaxf(m[0], m[HT]), fmaxf(m[2 * HT], m[3 * HT]));
+            float& ref = k & 1 ? nref[k / 2].y : nref[k / 2].x;
+            const bool grew = mx + ref > kRefLog2 + kGrowLog2;
+            const float now = grew ? kRefLog2 - mx : ref;
+            const float f = grew ? fast_exp2(now - ref) : 1.f;   // (from kNoRef: 0)
+            (k & 1 ? l[k / 2].y : l[k / 2].x) *= f;
+            ref = now;
+            grown |= (uint32_t)grew << k;
+            if (lane == k) fl = f;
           }
-          uint32_t grown = __ballot_sync(0xffffffffu, grew);
 #pragma unroll
-          for (int k = 0; k < HT / 2; ++k) {
-            nref[k].x = __shfl_sync(0xffffffffu, now, 2 * k);
-            nref[k].y = __shfl_sync(0xffffffffu, now, 2 * k + 1);
-            l[k].x *= __shfl_sync(0xffffffffu, fl, 2 * k);
-            l[k].y *= __shfl_sync(0xffffffffu, fl, 2 * k + 1);
-            y[k] = add_f32x2(x[k], nref[k]);
-          }
-          if (t > 0) {
-            // the output columns of the heads that grew, two heads at a time
-            tc::fence_after_sync();
-            while (grown) {
-              const int k0 = __ffs(grown) - 1;
-              grown &= grown - 1;
-              const int k1 = grown ? __ffs(grown) - 1 : k0;
-              grown &= grown - 1;
-              const float f0 = __shfl_sync(0xffffffffu, fl, k0), f1 = __shfl_sync(0xffffffffu, fl, k1);
-              const uint32_t at0 = trow + kOCol + (uint32_t)(h0 + k0), at1 = trow + kOCol + (uint32_t)(h0 + k1);
-              float o0[12], o1[12];
-#pragma unroll
-              for (int c = 0; c < 12; ++c) {
-                tmem_ld1(at0 + c * NH, o0[c]);
-                tmem_ld1(at1 + c * NH, o1[c]);
-              }
-              tc::wait_ld();
-#pragma unroll
-              for (int c = 0; c < 12; ++c) {
-                tmem_st1(at0 + c * NH, o0[c] * f0);
-                if (k1 != k0) tmem_st1(at1 + c * NH, o1[c] * f1);
-              }
-            }
-            tc::wait_st();
-          }
+          for (int k = 0; k < HT / 2; ++k) y[k] = add_f32x2(x[k], nref[k]);
         }
         // weights 2^(s - ref) S, and the sum of 2^(s - ref)
         uint32_t hp[HT / 2];
@@ -1014,6 +985,39 @@ __global__ void __launch_bounds__(Sm<NH>::threads, 1)
 #pragma unroll
         for (int s = 0; s < 3; ++s)
           *reinterpret_cast<uint2*>(pb + (s * (NH / kHG) + c16) * 2048 + h0 % kHG) = make_uint2(tm[s][0], tm[s][1]);
+        if (t > 0 && grown) {
+          // the output columns of the heads that grew, two heads at a time, when
+          // the products of tile i - 1 have landed (which takes as long as the
+          // weights above)
+          if (warp_wait(kPVDone + (slot ^ 1), ((i - 1) >> 1) & 1)) {
+            tc::fence_after_sync();
+            while (grown) {
+              const int k0 = __ffs(grown) - 1;
+              grown &= grown - 1;
+              const int k1 = grown ? __ffs(grown) - 1 : k0;
+              grown &= grown - 1;
+              const float f0 = __shfl_sync(0xffffffffu, fl, k0), f1 = __shfl_sync(0xffffffffu, fl, k1);
+              const uint32_t at0 = trow + kOCol + (uint32_t)(h0 + k0), at1 = trow + kOCol + (uint32_t)(h0 + k1);
+              float o0[12], o1[12];
+#pragma unroll
+              for (int c = 0; c < 12; ++c) {
+                tmem_ld1(at0 + c * NH, o0[c]);
+                tmem_ld1(at1 + c * NH, o1[c]);
+              }
+              tc::wait_ld();
+#pragma unroll
+              for (int c = 0; c < 12; ++c) {
+                tmem_st1(at0 + c * NH, o0[c] * f0);
+                if (k1 != k0) tmem_st1(at1 + c * NH, o1[c] * f1);
+              }
+            }
+            tc::wait_st();
+          } else if (lane == 0) {
+            // (all groups leave at their next wait or at the segment's end)
+            set_status(status, MLA_DEV_TIMEOUT);
+            *abort_flag = 1;
+          }
+        }
         if ((!there && r < ((v + 31) & ~31)) || odd) {
           // a token that is not there may hold anything: zero its codes, so that
           // a weight of 0 stays 0 (each group its part of the four slabs)
