@@ -306,57 +306,6 @@ __device__ __forceinline__ void query_terms(const uint32_t* u, float f, uint4& t
   t2 = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
-// The query of one (row, column group) as the decode's operand: for each head
-// its two e4m3 terms (rows h and NH + h of four 128-byte slabs) and its bf16
-// rope values, swizzled as shared memory holds them, and the factor that
-// undoes the head's scale. 16 threads a head, 32 latent columns each.
-template <int NH>
-__global__ void __launch_bounds__(NH * 16) page8_query_kernel(const uint16_t* q_abs,
-                                                             float scale_log2, uint8_t* q8,
-                                                             float* coef, int* arrive) {
-  using S = Sm<NH>;
-  pdl_wait();
-  pdl_launch_dependents();
-  const int h = threadIdx.x >> 4, part = threadIdx.x & 15;
-  const size_t row = (size_t)blockIdx.x * NH + h;   // (row n, head) in order
-  const uint4* src = reinterpret_cast<const uint4*>(q_abs + row * kRow);
-  uint8_t* dst = q8 + (size_t)blockIdx.x * S::q_bytes;
-  uint4 x[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) x[k] = src[part * 4 + k];
-  uint4 rope = make_uint4(0, 0, 0, 0);
-  if (part < 8) rope = src[kDc / 8 + part];
-  float mx = 0.f;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float v0 = fabsf(__uint_as_float(u[e] << 16)), v1 = fabsf(__uint_as_float(u[e] & 0xffff0000u));
-      mx = fmaxf(mx, fmaxf(isinf(v0) ? 0.f : v0, isinf(v1) ? 0.f : v1));
-    }
-  }
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  // 2^e with mx 2^e in [2^7, 2^8); heads below 2^-112 as 2^-112
-  const int e = min(134 - (int)(__float_as_uint(mx) >> 23), 119);
-  const float f = __uint_as_float((uint32_t)(e + 127) << 23);
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const uint32_t u[8] = {x[2 * k].x, x[2 * k].y, x[2 * k].z, x[2 * k].w,
-                           x[2 * k + 1].x, x[2 * k + 1].y, x[2 * k + 1].z, x[2 * k + 1].w};
-    uint4 t1, t2;
-    query_terms(u, f, t1, t2);
-    const int c16 = part * 2 + k;  // 16-code piece of the row
-    uint8_t* slab = dst + (c16 >> 3) * S::q_slab;
-    *reinterpret_cast<uint4*>(slab + sw128(h, c16 & 7)) = t1;
-    *reinterpret_cast<uint4*>(slab + sw128(NH + h, c16 & 7)) = t2;
-  }
-  if (part < 8) *reinterpret_cast<uint4*>(dst + S::q_rope + sw128(h, part)) = rope;
-  if (arrive && threadIdx.x == 0) arrive[blockIdx.x] = 0;
-  if (part == 0) coef[row] = scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
-}
-
 // Untiled copy of `bytes` (a multiple of 16) to shared memory.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile(
@@ -433,27 +382,25 @@ __device__ __forceinline__ bool start_share(SchedWalker& sw, const int4* rows, i
   return false;
 }
 
-// The plan of more rows than that: one CTA, a warp per sequence, into the
-// workspace.
-constexpr int kPlanThreads = 1024;
-__global__ void __launch_bounds__(kPlanThreads) page8_plan_kernel(const __grid_constant__ P8Args a) {
-  extern __shared__ int s_first[];  // [num_q] units, then first units
-  __shared__ int s_warp[32], s_total;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, Nq = (int)a.num_q;
+// The plan of more rows than a CTA holds: one CTA, a warp per sequence, into the
+// workspace (as SchedWalker::init reads it).
+template <int NT>
+__device__ __forceinline__ void plan_rows(const P8Args& a, int tid) {
+  __shared__ int s_warp[NT / 32];
+  const int lane = tid & 31, warp = tid >> 5, Nq = (int)a.num_q;
   const WsLayout L = ws_layout(a.num_q, 1, a.shares);
   WsHeader* hdr = reinterpret_cast<WsHeader*>(a.ws);
   int4* rows = reinterpret_cast<int4*>(a.ws + L.row_info);
   int4* cta_start = reinterpret_cast<int4*>(a.ws + L.cta_start);
-  pdl_wait();
-  pdl_launch_dependents();
-  for (int n = tid; n < Nq; n += kPlanThreads) rows[n] = make_int4(-1, -1, 0, 0);
+  for (int n = tid; n < Nq; n += NT) rows[n] = make_int4(-1, -1, 0, 0);
   __syncthreads();
-  fill_rows(a, rows, &hdr->status, warp, kPlanThreads / 32, lane, 32);
+  fill_rows(a, rows, &hdr->status, warp, NT / 32, lane, 32);
   __syncthreads();
-  // exclusive scan of the units, a contiguous piece per thread
-  const int per = (Nq + kPlanThreads - 1) / kPlanThreads;
+  // first units: an exclusive scan, a contiguous piece per thread
+  const int per = (Nq + NT - 1) / NT;
   const int beg = min(Nq, tid * per), end = min(Nq, beg + per);
   int local = 0;
+#pragma unroll 8
   for (int n = beg; n < end; ++n) local += max(rows[n].z, 0);
   int incl = local;
 #pragma unroll
@@ -463,16 +410,21 @@ __global__ void __launch_bounds__(kPlanThreads) page8_plan_kernel(const __grid_c
   }
   if (lane == 31) s_warp[warp] = incl;
   __syncthreads();
-  int run = incl - local;
-  for (int w = 0; w < warp; ++w) run += s_warp[w];
-  if (tid == kPlanThreads - 1) s_total = run + local;
-  for (int n = beg; n < end; ++n) {
-    s_first[n] = run;
-    rows[n].w = run;
-    run += max(rows[n].z, 0);
+  int run = incl - local, total = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    run += w < warp ? s_warp[w] : 0;
+    total += s_warp[w];
   }
-  __syncthreads();
-  const int total = s_total, share = total > 0 ? (total + a.shares - 1) / a.shares : 1;
+  const int share = total > 0 ? (total + a.shares - 1) / a.shares : 1;
+#pragma unroll 8
+  for (int n = beg; n < end; ++n) {
+    const int z = max(rows[n].z, 0);
+    rows[n].w = run;
+    // the shares that begin in this row
+    for (int c = (run + share - 1) / share; c * share < run + z; ++c) cta_start[c] = make_int4(n, 0, c * share - run, 0);
+    run += z;
+  }
   if (tid == 0) {
     hdr->magic = kMagic;
     hdr->mode = 0;
@@ -484,15 +436,61 @@ __global__ void __launch_bounds__(kPlanThreads) page8_plan_kernel(const __grid_c
     hdr->num_q = Nq;
     hdr->batch = a.batch;
   }
-  for (int c = tid; c < a.shares; c += kPlanThreads) {
-    const int u = c * share;
-    int lo = 0, hi = Nq;  // the last row whose first unit is <= u: it owns units
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_first[mid] <= u) lo = mid; else hi = mid;
-    }
-    cta_start[c] = u < total ? make_int4(lo, 0, u - s_first[lo], 0) : make_int4(-1, 0, 0, 0);
+}
+
+// The query of one (row, column group) as the decode's operand: for each head
+// its two e4m3 terms (rows h and NH + h of four 128-byte slabs) and its bf16
+// rope values, swizzled as shared memory holds them, and the factor that
+// undoes the head's scale. 16 threads a head, 32 latent columns each. Where the
+// decode does not find its split itself, the first CTA does, beside the others.
+template <int NH>
+__global__ void __launch_bounds__(NH * 16) page8_query_kernel(const __grid_constant__ P8Args a) {
+  using S = Sm<NH>;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (!a.self_plan && blockIdx.x == 0) {
+    plan_rows<NH * 16>(a, threadIdx.x);
+    return;
   }
+  const int block = blockIdx.x - (a.self_plan ? 0 : 1);
+  const int h = threadIdx.x >> 4, part = threadIdx.x & 15;
+  const size_t row = (size_t)block * NH + h;   // (row n, head) in order
+  const uint4* src = reinterpret_cast<const uint4*>(a.q_abs + row * kRow);
+  uint8_t* dst = a.q8 + (size_t)block * S::q_bytes;
+  uint4 x[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] = src[part * 4 + k];
+  uint4 rope = make_uint4(0, 0, 0, 0);
+  if (part < 8) rope = src[kDc / 8 + part];
+  float mx = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float v0 = fabsf(__uint_as_float(u[e] << 16)), v1 = fabsf(__uint_as_float(u[e] & 0xffff0000u));
+      mx = fmaxf(mx, fmaxf(isinf(v0) ? 0.f : v0, isinf(v1) ? 0.f : v1));
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  // 2^e with mx 2^e in [2^7, 2^8); heads below 2^-112 as 2^-112
+  const int e = min(134 - (int)(__float_as_uint(mx) >> 23), 119);
+  const float f = __uint_as_float((uint32_t)(e + 127) << 23);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t u[8] = {x[2 * k].x, x[2 * k].y, x[2 * k].z, x[2 * k].w,
+                           x[2 * k + 1].x, x[2 * k + 1].y, x[2 * k + 1].z, x[2 * k + 1].w};
+    uint4 t1, t2;
+    query_terms(u, f, t1, t2);
+    const int c16 = part * 2 + k;  // 16-code piece of the row
+    uint8_t* slab = dst + (c16 >> 3) * S::q_slab;
+    *reinterpret_cast<uint4*>(slab + sw128(h, c16 & 7)) = t1;
+    *reinterpret_cast<uint4*>(slab + sw128(NH + h, c16 & 7)) = t2;
+  }
+  if (part < 8) *reinterpret_cast<uint4*>(dst + S::q_rope + sw128(h, part)) = rope;
+  if (a.fused && threadIdx.x == 0) a.arrive[block] = 0;
+  if (part == 0) a.coef[row] = a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
 }
 
 // Zeros for the latents of rows that own no tiles.
@@ -1500,19 +1498,11 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
   const bool many_parts = num_q * H < 256;
   a.fused = num_q * H >= 7168;
   const bool merge_proj = !a.fused && !many_parts;
-  cudaError_t e = cudaSuccess;
-  if (!a.self_plan) {
-    e = cudaFuncSetAttribute(page8_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)num_q * 4);
-    if (e == cudaSuccess) e = launch_pdl(page8_plan_kernel, dim3(1), dim3(kPlanThreads), (size_t)num_q * 4, st, a);
-  }
-  if (e == cudaSuccess) {
-    // (a row of a pair has its operand as 16 heads by themselves do)
-    int* arrive = a.fused ? a.arrive : nullptr;
-    e = H == 16 ? launch_pdl(page8_query_kernel<16>, dim3((unsigned)num_q), dim3(256), 0, st, a.q_abs,
-                             a.scale_log2, a.q8, a.coef, arrive)
-                : launch_pdl(page8_query_kernel<32>, dim3((unsigned)(num_q * a.groups)), dim3(512), 0, st, a.q_abs,
-                             a.scale_log2, a.q8, a.coef, arrive);
-  }
+  cudaError_t e;
+  // (a row of a pair has its operand as 16 heads by themselves do)
+  const dim3 query_ctas((unsigned)(num_q * a.groups + !a.self_plan));
+  e = H == 16 ? launch_pdl(page8_query_kernel<16>, query_ctas, dim3(256), 0, st, a)
+              : launch_pdl(page8_query_kernel<32>, query_ctas, dim3(512), 0, st, a);
   if (e != cudaSuccess) return MLA_ERR_CUDA;
   auto launch = [&](auto kernel, int threads, int smem) {
     const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
