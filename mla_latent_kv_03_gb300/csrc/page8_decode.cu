@@ -36,7 +36,9 @@
 // read the same tokens at the same time, so a token comes from HBM once for
 // all heads. Per CTA (384 or 640 threads):
 //   warp 0      copies: 128 tokens a stage (4 slabs of 128 codes, one of rope
-//               values), two stages, SWIZZLE_128B; block ids are checked;
+//               values), two stages, SWIZZLE_128B; block ids are checked. 64
+//               tokens are copied as soon as the output products of those in
+//               their place are done;
 //   warp 1      issues the output products of a tile as soon as its weights are
 //               stored (one lane); owns the TMEM;
 //   warp 2      issues the scores of a tile as soon as it has landed and the
@@ -187,18 +189,18 @@ struct Sm {
 
 enum {
   kFull = 0,      // [2] stage landed
-  kEmpty = 2,     // [2] stage's products done
-  kQReady = 4,    // [2] query terms landed
-  kQFree = 6,     // [2] the segment's score products done, its factors read (1 + 8 arrivals)
-  kSFull = 8,     // scores in TMEM
-  kSFree = 9,     // scores read (8 arrivals)
-  kPFull = 10,    // [2] weights stored (8 arrivals)
-  kPVDone = 12,   // [2] output products done
-  kODone = 14,    // the segment's output products done
-  kOFree = 15,    // the output read (8 arrivals)
-  kFinalS = 16,   // every score product done
-  kFinalO = 17,   // every output product done
-  kNumBars = 18
+  kEmpty = 2,     // [2][2] products of a stage's first and last 64 tokens done
+  kQReady = 6,    // [2] query terms landed
+  kQFree = 8,     // [2] the segment's score products done, its factors read (1 + softmax warps)
+  kSFull = 10,    // scores in TMEM
+  kSFree = 11,    // scores read (softmax warps)
+  kPFull = 12,    // [2] weights stored (softmax warps)
+  kPVDone = 14,   // [2] output products done
+  kODone = 16,    // the segment's output products done
+  kOFree = 17,    // the output read (softmax warps)
+  kFinalS = 18,   // every score product done
+  kFinalO = 19,   // every output product done
+  kNumBars = 20
 };
 
 // Instruction descriptor, kind::f8f6f4, fp32 accumulator: A e4m3, B e4m3 (0) or
@@ -623,35 +625,45 @@ __global__ void __launch_bounds__(Sm<NH>::threads, 1)
           sc = fine ? fmaxf(a.scales[id], __uint_as_float((uint32_t)(kP8MinExp + 127) << 23)) : -1.f;
           if (!fine) id = -1;
         }
-        if (i >= 2 && !warp_wait(kEmpty + slot, ((i >> 1) - 1) & 1)) {
-          ok = false;
-          break;
-        }
         const int src = (b0 - base + lane) & 31;
         const int my_id = __shfl_sync(0xffffffffu, id, src);
+        const float my_sc = __shfl_sync(0xffffffffu, sc, src);
         const bool mine = lane < pages && my_id >= 0;
         const uint32_t okmask = __ballot_sync(0xffffffffu, mine);
         // lanes 0-4 each copy one slab of every page
         uint8_t* dst = sm + S::stage + slot * kStageB + (lane < 5 ? lane : 0) * kSlab;
-        for (int p = 0; p < pages; ++p) {
-          const int y = __shfl_sync(0xffffffffu, my_id, p) << bs_shift;
-          if (!((okmask >> p) & 1)) continue;
-          if (lane < 4)
-            tma_load_2d_hint(dst + (p << bs_shift) * 128, &codes_map, 128 * lane, y, &bars[kFull + slot], policy);
-          else if (lane == 4)
-            tma_load_2d_hint(dst + (p << bs_shift) * 128, &rope_map, kDc / 2, y, &bars[kFull + slot], policy);
+        uint32_t bytes = 0;
+        // 64 tokens as soon as their place is free
+        for (int half = 0; half < 2; ++half) {
+          ok = i < 2 || warp_wait(kEmpty + 2 * slot + half, ((i >> 1) - 1) & 1);
+          if (!ok) break;
+          const int p0 = half * kTile >> bs_shift, p1 = min(pages, (half + 1) * kTile >> bs_shift);
+          for (int p = p0; p < p1; ++p) {
+            const int y = __shfl_sync(0xffffffffu, my_id, p) << bs_shift;
+            if (!((okmask >> p) & 1)) continue;
+            bytes += 5 * bs * 128;
+            if (lane < 4)
+              tma_load_2d_hint(dst + (p << bs_shift) * 128, &codes_map, 128 * lane, y, &bars[kFull + slot], policy);
+            else if (lane == 4)
+              tma_load_2d_hint(dst + (p << bs_shift) * 128, &rope_map, kDc / 2, y, &bars[kFull + slot], policy);
+          }
         }
-        // the scales, whose loads the copies did not wait for; the barrier's
-        // one arrival comes last
-        const float my_sc = __shfl_sync(0xffffffffu, sc, src);
-        if (lane < 8) page_sc[slot * 8 + lane] = mine ? my_sc : -1.f;
+        // (read by the softmax, before whose end nothing of the stage is free;
+        // the copies did not wait for the scales' loads)
+        if (ok && lane < 8) page_sc[slot * 8 + lane] = mine ? my_sc : -1.f;
         __syncwarp();
         if (lane == 0) {
-          if (__popc(okmask) != pages) set_status(status, MLA_DEV_BAD_BLOCK);
-          info[slot] = v;
-          mbar_arrive_expect_tx(&bars[kFull + slot], (uint32_t)(__popc(okmask) * 5 * bs * 128));
+          if (ok && __popc(okmask) != pages) set_status(status, MLA_DEV_BAD_BLOCK);
+          if (ok) info[slot] = v;
+          // (the barrier's one arrival comes after the copies; of a tile that is
+          // given up, too: the copies so far are waited for below)
+          mbar_arrive_expect_tx(&bars[kFull + slot], bytes);
         }
         __syncwarp();
+        if (!ok) {
+          ++i;
+          break;
+        }
       }
     }
     if (lane == 0) {
@@ -696,8 +708,9 @@ __global__ void __launch_bounds__(Sm<NH>::threads, 1)
             for (int j = 0; j < 4; ++j)
               mma_f8(tmem + kOCol + (uint32_t)(j * 3 * NH), vdesc + ((st + j * kSlab + ks * 4096) >> 4),
                      pdesc + ((pb + ks * 512) >> 4), kIdO, t > 0 || ks > 0);
+            if (ks == min(nks, 2) - 1) tc::commit(&bars[kEmpty + 2 * slot]);
           }
-          tc::commit(&bars[kEmpty + slot]);
+          tc::commit(&bars[kEmpty + 2 * slot + 1]);
           tc::commit(&bars[kPVDone + slot]);
           if (t == n - 1) tc::commit(&bars[kODone]);
         }
