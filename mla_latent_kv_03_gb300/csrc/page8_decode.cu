@@ -48,9 +48,26 @@
 //   warps 4-    softmax, 4 warps for every 8 heads: thread r of each such group
 //               owns token r. Tokens that are not there are zeroed in the
 //               stage, so a weight of 0 never meets a NaN code.
-// Every wait is bounded; on a timeout the roles leave their loops, the issuer
-// waits for its products and the copies' warp for its copies before TMEM is
+// Every wait is bounded; on a timeout the roles leave their loops, the issuers
+// wait for their products and the copies' warps for their copies before TMEM is
 // freed.
+//
+// Bound and measurements (one GB300, launches alone with a cold L2):
+//  - 64 sequences of 4,096 tokens, 16 heads: 41 us for 168 MB. 27 us of them are
+//    the main loop, at 6.2 TB/s (0.92 of a copy's rate); the rest is the start
+//    (split, block table, first pages: 5 us), the last products, the partials
+//    and a tail of shares that end apart.
+//  - 32 sequences of up to 32,768 tokens, 128 heads: 275 us; 4 chunks of 512 rows
+//    on 2,560 tokens, 16 heads: 293 us. Neither bytes (0.18 and 0.04 of HBM) nor
+//    products (tensor pipe busy 0.30 and 0.27) bound these, but the time of one
+//    stage from copy to release: copy 1,700 cycles, scores 1,500, softmax 1,900,
+//    output products 1,600, over two stages 3,400 cycles a tile of which the
+//    products need 1,820. Three stages do not fit beside the operands of 32
+//    columns (36 KB of query terms, 24 KB of weights). A tile in which a
+//    reference is outgrown takes some 2,000 cycles more.
+//  Tried and not kept: each slab of a stage with barriers of its own (3 to 8 %
+//  slower), pairs of CTAs that copy each other's tokens by multicast (no
+//  difference: the L2 is not what bounds the copies).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -73,7 +90,7 @@ constexpr int kSoftWarp0 = 4;
 // named barriers: all softmax warps; each 16 columns' (2, 3); each 8 columns' (4-7)
 constexpr int kSoftBar = 1, kHeadsBar = 2, kGroupBar = 4;
 constexpr float kRefLog2 = 4.f;               // a weight equal to the reference is held as 2^4
-constexpr float kNoRef = 1e38f;
+constexpr float kNoRef = 1e38f;               // nref of a head without one: every score outgrows it
 // the reference follows when outgrown by 2^11.75: a weight of 2^15.75 is still
 // below e5m2's largest number, 1.75 * 2^15
 constexpr float kGrowLog2 = 11.75f;
@@ -445,6 +462,9 @@ __device__ __forceinline__ void plan_rows(const P8Args& a, int tid) {
 // rope values, swizzled as shared memory holds them, and the factor that
 // undoes the head's scale. 16 threads a head, 32 latent columns each. Where the
 // decode does not find its split itself, the first CTA does, beside the others.
+// Latency for a decode step (4.0 us for 64 rows of 16 heads, mostly the launch,
+// and hidden behind the decode's start); HBM for chunks: 15 us for 2,048 rows, 75
+// MB read and written.
 template <int NH>
 __global__ void __launch_bounds__(NH * 16) page8_query_kernel(const __grid_constant__ P8Args a) {
   using S = Sm<NH>;
@@ -1176,7 +1196,8 @@ __device__ __forceinline__ void merge_weights(const HeadParts& hp, int lane_in_g
 
 // The merge of many parts of few (row, head)s: two CTAs each, of 256 columns.
 // Thread (p, c) sums 4 columns over every fourth part, eight loads in flight;
-// the four sums meet in shared memory.
+// the four sums meet in shared memory. Bound by latency: 5.6 us for one row of 16
+// heads, 9.6 us for two rows of 32 heads in 76 parts each (10 MB).
 __global__ void __launch_bounds__(256) page8_merge_kernel(const __grid_constant__ P8Args a) {
   __shared__ float4 sAcc[3][64];
   __shared__ int4 plan[kSelfMaxRows];
@@ -1246,7 +1267,8 @@ __global__ void __launch_bounds__(256) page8_merge_kernel(const __grid_constant_
 // warps, each a quarter of K and half of the columns (m16n8k16), whose sums meet
 // in shared memory. Every part is read once. ROWS = 8 (half of the mma's rows
 // idle) where that still leaves at most one CTA an SM: the merge, at latency, is
-// what takes the time.
+// what takes the time. 64 rows of 16 heads: 9.0 us alone, 4 us behind a decode,
+// which hides the weights' copy (2 MB in all); 32 rows of 128 heads: 18 us.
 template <int ROWS>
 struct Mp {
   static constexpr int stride = kDc * 2 + 16;     // bytes of a merged row, padded against bank conflicts
@@ -1385,7 +1407,9 @@ __global__ void __launch_bounds__(256) page8_merge_proj_kernel(const __grid_cons
 }
 
 // mass[slot(t)] = decay * mass[slot(t)] + sum over the sequence's rows and all
-// heads of 2^(score - lse), rows and heads in order: one thread per token.
+// heads of 2^(score - lse), rows and heads in order: one thread per token. Bound
+// by latency and the scores' bytes: 8.7 us for 64 sequences of 4,096 tokens and 16
+// heads (16.8 MB, most of it still in L2).
 struct MassArgs {
   const float* scores;
   const float* lse;
@@ -1487,6 +1511,8 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
   a.seq_lens = seq_lens;
   a.query_start_loc = query_start_loc;
   a.batch = batch;
+  // (64 rows of 16 heads: 21.9 us, 25.3 with the plan in the kernel before; 256
+  // rows: 49.0 and 57.7; 128 rows of 32 heads: 39.4 and 42.0)
   a.self_plan = num_q <= (NH == 16 ? Sm<16>::self_rows : Sm<32>::self_rows);
   a.lse_first = reinterpret_cast<float*>(ws + W.lse);
   a.o_first = reinterpret_cast<float*>(ws + W.opart);
