@@ -201,6 +201,8 @@ class MlaDecodeStep:
         """Cut every sequence to `budget` tokens, moved into the pages of
         dst_block_table, which becomes the sequences' table. Returns (keep,
         new lengths)."""
+        if self.p8_mass is None:
+            raise ValueError("page8_evict needs page8_setup(with_mass=True)")
         if stream is not None and not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream), device=self.device)
         with torch.cuda.stream(stream):  # memory of the stream that writes it

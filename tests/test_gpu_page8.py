@@ -639,6 +639,12 @@ def test_write_decode_evict_decode():
         assert np.array_equal(new[:, 512:], old[keep.cpu().numpy()[b, :n[b]], 512:])
 
 
+def test_evict_needs_weights():
+    _, s = _step("bs16_h32")
+    with pytest.raises(ValueError, match="with_mass"):
+        s.page8_evict(8, 0, 0, s.block_table)
+
+
 def test_evict_on_a_stream_writes_memory_that_no_other_stream_still_uses():
     w, s, dst, budget = _together()
     side = torch.cuda.Stream()

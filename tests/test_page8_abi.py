@@ -100,6 +100,7 @@ def test_decode_configs_mass_and_empty_calls(lib):
     for decay in (-0.1, 1.5, float("nan"), float("inf")):
         assert _decode(lib, _cfg(), True, decay=decay) == 1
     assert _decode(lib, _cfg(), True, mass=NONE) == 1
+    assert _decode(lib, _cfg(), True, batch=65536) == 2
     assert _decode(lib, _cfg(), True, mass=ODD) == 1
     size = lib.mla_page8_decode_workspace_size
     c = _cfg()
