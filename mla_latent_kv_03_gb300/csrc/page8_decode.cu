@@ -1513,15 +1513,19 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
   // Who merges the splits. With many outputs (rows x heads) most tiles are
   // whole and the rest is merged in the decode kernel; the tensor-core
   // projection follows. Below, the merge goes into the projection, unless there
-  // are so few outputs, each cut into many parts, that the merge has to spread
-  // over the device first. Measured on one GB300, us:
+  // are so few outputs, each cut into more than a few parts (one per 64 tokens at
+  // the most), that the merge has to spread over the device first. Measured on
+  // one GB300, us:
   //   rows x heads       320 x 16  448 x 16  56 x 128  256 x 32  256 x 128
   //   in the projection    66.7      82.7      59.4      77.2      223.4
   //   in the decode        68.1      83.0      56.4      74.5      181.1
   //   rows x heads (65,536 tokens)  1 x 16  8 x 16  16 x 16  32 x 16  1 x 128  4 x 128
   //   in the projection              61.1    27.4    24.9     23.2      52.5     45.7
   //   spread                         26.6    23.6    25.2     28.5      46.8     51.2
-  const bool many_parts = num_q * H < 256;
+  //   tokens of 2 x 32       512   1,024  2,048
+  //   in the projection      14.6   16.3   20.3  (one launch less: 2.7 us of the host's time)
+  //   spread                 15.6   15.7   15.4
+  const bool many_parts = num_q * H < 256 && (int64_t)max_blocks * bs > 512;
   a.fused = num_q * H >= 7168;
   const bool merge_proj = !a.fused && !many_parts;
   cudaError_t e;
