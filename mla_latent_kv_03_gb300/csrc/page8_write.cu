@@ -383,12 +383,15 @@ int device_sms() {
 template <int BS>
 cudaError_t write_pages(const P8WriteArgs& a, const RopeFreq& freq, uint8_t* ws, cudaStream_t st) {
   const int smem = PageSm<BS>::bytes;
-  cudaError_t e = cudaFuncSetAttribute(p8_write_scan_kernel<BS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(p8_write_pages_kernel<BS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  if (a.num_tokens <= kScanTokens) {
+    const cudaError_t r = cudaFuncSetAttribute(p8_write_scan_kernel<BS>, attr, smem);
+    return r != cudaSuccess
+               ? r
+               : launch_pdl(p8_write_scan_kernel<BS>, dim3(a.num_tokens), dim3(kThreads), smem, st, a, freq);
+  }
+  cudaError_t e = cudaFuncSetAttribute(p8_write_pages_kernel<BS>, attr, smem);
   if (e != cudaSuccess) return e;
-  if (a.num_tokens <= kScanTokens)
-    return launch_pdl(p8_write_scan_kernel<BS>, dim3(a.num_tokens), dim3(kThreads), smem, st, a, freq);
   const P8WriteWs L = write_ws(a.num_tokens, a.num_blocks, BS);
   int* count = reinterpret_cast<int*>(ws + L.count);
   int* id_of = reinterpret_cast<int*>(ws + L.id_of);

@@ -335,33 +335,41 @@ def _shape(t, shape, name: str) -> None:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _ptrs(*args) -> list:
+    """The addresses of (tensor, dtype, shape, name)s, None for None; sizes are
+    refused before anything else. (One loop without calls: a decode step's
+    checks are a part of its time.)"""
+    out = []
+    for t, dtype, shape, _ in args:
+        if t is None:
+            out.append(None)
+        elif t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
+            break
+    else:
+        return out
+    for t, _, shape, name in args:
+        if t is not None:
+            _shape(t, shape, name)
+    return [_ptr(t, dtype, name) for t, dtype, _, name in args]
+
+
 def mla_page8_write_workspace_size(cfg: MlaConfig, num_tokens: int, num_blocks: int) -> int:
     return int(load().mla_page8_write_workspace_size(ctypes.byref(cfg), num_tokens, num_blocks))
 
 
-def _page8_pages(cfg: MlaConfig, cache8, page_scales, mass):
-    nb = cache8.shape[0]
-    _shape(cache8, (nb, cfg.block_size, 640), "cache8")
-    _shape(page_scales, (nb,), "page_scales")
-    if mass is not None:
-        _shape(mass, (nb, cfg.block_size), "mass")
-    return nb
-
-
 def mla_page8_cache_write(cfg: MlaConfig, c_kv, k_pe, positions, slot_mapping, rms_weight, cache8,
                           page_scales, workspace, mass=None, dev_status=None, stream=None) -> None:
-    nb, n = _page8_pages(cfg, cache8, page_scales, mass), c_kv.shape[0]
-    _shape(c_kv, (n, 512), "c_kv")
-    _shape(k_pe, (n, 64), "k_pe")
-    _shape(positions, (n,), "positions")
-    _shape(slot_mapping, (n,), "slot_mapping")
-    _shape(rms_weight, (512,), "rms_weight")
-    bf = torch.bfloat16
+    nb, n, bs, bf = cache8.shape[0], c_kv.shape[0], cfg.block_size, torch.bfloat16
+    p_cache, p_scales, p_mass, p_kv, p_pe, p_pos, p_slot, p_w = _ptrs(
+        (cache8, torch.uint8, (nb, bs, 640), "cache8"),
+        (page_scales, torch.float32, (nb,), "page_scales"),
+        (mass, torch.float32, (nb, bs), "mass"), (c_kv, bf, (n, 512), "c_kv"),
+        (k_pe, bf, (n, 64), "k_pe"), (positions, torch.int32, (n,), "positions"),
+        (slot_mapping, torch.int64, (n,), "slot_mapping"), (rms_weight, bf, (512,), "rms_weight"))
     _check(load().mla_page8_cache_write(
-        ctypes.byref(cfg), _ptr(c_kv, bf, "c_kv"), _ptr(k_pe, bf, "k_pe"),
-        _ptr(positions, torch.int32, "positions"), _ptr(slot_mapping, torch.int64, "slot_mapping"),
-        n, _ptr(rms_weight, bf, "rms_weight"), _ptr(cache8, torch.uint8, "cache8"),
-        _ptr(page_scales, torch.float32, "page_scales"), nb, _ptr(mass, torch.float32, "mass"),
+        ctypes.byref(cfg), p_kv, p_pe, p_pos, p_slot, n, p_w, p_cache, p_scales, nb, p_mass,
         _ptr(workspace, None, "workspace"), _nbytes(workspace),
         _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)), "mla_page8_cache_write")
 
@@ -374,69 +382,62 @@ def mla_page8_decode_workspace_size(cfg: MlaConfig, num_q: int, batch: int, max_
 
 def _page8_decode_args(cfg, q_abs, cache8, page_scales, block_table, seq_lens, query_start_loc,
                        W_uv, mass, out):
-    nb, n, b, H = _page8_pages(cfg, cache8, page_scales, mass), q_abs.shape[0], seq_lens.shape[0], cfg.num_heads
-    _shape(q_abs, (n, H, 576), "q_abs")
-    _shape(block_table, (b, block_table.shape[1]), "block_table")
-    _shape(query_start_loc, (b + 1,), "query_start_loc")
-    _shape(W_uv, (H, 512, 128), "W_uv")
-    _shape(out, (n, H, 128), "out")
-    bf = torch.bfloat16
-    return [ctypes.byref(cfg), _ptr(q_abs, bf, "q_abs"), _ptr(cache8, torch.uint8, "cache8"),
-            _ptr(page_scales, torch.float32, "page_scales"), nb,
-            _ptr(block_table, torch.int32, "block_table"), block_table.shape[1],
-            _ptr(seq_lens, torch.int32, "seq_lens"),
-            _ptr(query_start_loc, torch.int32, "query_start_loc"), b, n, _ptr(W_uv, bf, "W_uv")]
+    nb, n, b, H = cache8.shape[0], q_abs.shape[0], seq_lens.shape[0], cfg.num_heads
+    mb, bs, bf, i32 = block_table.shape[1], cfg.block_size, torch.bfloat16, torch.int32
+    p_cache, p_scales, p_mass, p_q, p_bt, p_lens, p_qsl, p_w, p_out = _ptrs(
+        (cache8, torch.uint8, (nb, bs, 640), "cache8"),
+        (page_scales, torch.float32, (nb,), "page_scales"),
+        (mass, torch.float32, (nb, bs), "mass"), (q_abs, bf, (n, H, 576), "q_abs"),
+        (block_table, i32, (b, mb), "block_table"), (seq_lens, i32, (b,), "seq_lens"),
+        (query_start_loc, i32, (b + 1,), "query_start_loc"), (W_uv, bf, (H, 512, 128), "W_uv"),
+        (out, bf, (n, H, 128), "out"))
+    return [ctypes.byref(cfg), p_q, p_cache, p_scales, nb, p_bt, mb, p_lens, p_qsl, b, n, p_w], p_mass, p_out
 
 
 def mla_page8_decode(cfg: MlaConfig, q_abs, cache8, page_scales, block_table, seq_lens,
                      query_start_loc, W_uv, workspace, out, stream=None) -> None:
-    args = _page8_decode_args(cfg, q_abs, cache8, page_scales, block_table, seq_lens,
-                              query_start_loc, W_uv, None, out)
-    _check(load().mla_page8_decode(
-        *args, _ptr(workspace, None, "workspace"), _nbytes(workspace),
-        _ptr(out, torch.bfloat16, "out"), _stream(stream)), "mla_page8_decode")
+    args, _, p_out = _page8_decode_args(cfg, q_abs, cache8, page_scales, block_table, seq_lens,
+                                        query_start_loc, W_uv, None, out)
+    _check(load().mla_page8_decode(*args, _ptr(workspace, None, "workspace"), _nbytes(workspace),
+                                   p_out, _stream(stream)), "mla_page8_decode")
 
 
 def mla_page8_decode_mass(cfg: MlaConfig, q_abs, cache8, page_scales, block_table, seq_lens,
                           query_start_loc, W_uv, mass, decay: float, workspace, out,
                           stream=None) -> None:
-    args = _page8_decode_args(cfg, q_abs, cache8, page_scales, block_table, seq_lens,
-                              query_start_loc, W_uv, mass, out)
+    args, p_mass, p_out = _page8_decode_args(cfg, q_abs, cache8, page_scales, block_table, seq_lens,
+                                             query_start_loc, W_uv, mass, out)
     _check(load().mla_page8_decode_mass(
-        *args, _ptr(mass, torch.float32, "mass"), float(decay), _ptr(workspace, None, "workspace"),
-        _nbytes(workspace), _ptr(out, torch.bfloat16, "out"), _stream(stream)),
-        "mla_page8_decode_mass")
+        *args, p_mass, float(decay), _ptr(workspace, None, "workspace"), _nbytes(workspace), p_out,
+        _stream(stream)), "mla_page8_decode_mass")
 
 
 def mla_evict_select(cfg: MlaConfig, mass, block_table, seq_lens, sinks: int, recent: int, keep,
                      new_lens, dev_status=None, stream=None) -> None:
     """The budget is keep.shape[1]."""
-    nb, b = mass.shape[0], seq_lens.shape[0]
-    _shape(mass, (nb, cfg.block_size), "mass")
-    _shape(block_table, (b, block_table.shape[1]), "block_table")
-    _shape(keep, (b, keep.shape[1]), "keep")
-    _shape(new_lens, (b,), "new_lens")
+    nb, b, mb, budget, i32 = mass.shape[0], seq_lens.shape[0], block_table.shape[1], keep.shape[1], torch.int32
+    p_mass, p_bt, p_lens, p_keep, p_new = _ptrs(
+        (mass, torch.float32, (nb, cfg.block_size), "mass"), (block_table, i32, (b, mb), "block_table"),
+        (seq_lens, i32, (b,), "seq_lens"), (keep, i32, (b, budget), "keep"),
+        (new_lens, i32, (b,), "new_lens"))
     _check(load().mla_evict_select(
-        ctypes.byref(cfg), _ptr(mass, torch.float32, "mass"), nb,
-        _ptr(block_table, torch.int32, "block_table"), block_table.shape[1],
-        _ptr(seq_lens, torch.int32, "seq_lens"), b, sinks, recent, keep.shape[1],
-        _ptr(keep, torch.int32, "keep"), _ptr(new_lens, torch.int32, "new_lens"),
+        ctypes.byref(cfg), p_mass, nb, p_bt, mb, p_lens, b, sinks, recent, budget, p_keep, p_new,
         _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)), "mla_evict_select")
 
 
 def mla_page8_compact(cfg: MlaConfig, cache8, page_scales, mass, block_table, keep, new_lens,
                       dst_block_table, dev_status=None, stream=None) -> None:
-    nb, b = _page8_pages(cfg, cache8, page_scales, mass), new_lens.shape[0]
-    _shape(block_table, (b, block_table.shape[1]), "block_table")
-    _shape(keep, (b, keep.shape[1]), "keep")
-    _shape(dst_block_table, (b, dst_block_table.shape[1]), "dst_block_table")
+    nb, b, mb, budget = cache8.shape[0], new_lens.shape[0], block_table.shape[1], keep.shape[1]
+    dmb, bs, i32 = dst_block_table.shape[1], cfg.block_size, torch.int32
+    p_cache, p_scales, p_mass, p_bt, p_keep, p_new, p_dst = _ptrs(
+        (cache8, torch.uint8, (nb, bs, 640), "cache8"),
+        (page_scales, torch.float32, (nb,), "page_scales"),
+        (mass, torch.float32, (nb, bs), "mass"), (block_table, i32, (b, mb), "block_table"),
+        (keep, i32, (b, budget), "keep"), (new_lens, i32, (b,), "new_lens"),
+        (dst_block_table, i32, (b, dmb), "dst_block_table"))
     _check(load().mla_page8_compact(
-        ctypes.byref(cfg), _ptr(cache8, torch.uint8, "cache8"),
-        _ptr(page_scales, torch.float32, "page_scales"), _ptr(mass, torch.float32, "mass"), nb,
-        _ptr(block_table, torch.int32, "block_table"), block_table.shape[1],
-        _ptr(keep, torch.int32, "keep"), _ptr(new_lens, torch.int32, "new_lens"), b, keep.shape[1],
-        _ptr(dst_block_table, torch.int32, "dst_block_table"), dst_block_table.shape[1],
-        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)), "mla_page8_compact")
+        ctypes.byref(cfg), p_cache, p_scales, p_mass, nb, p_bt, mb, p_keep, p_new, b, budget, p_dst,
+        dmb, _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)), "mla_page8_compact")
 
 
 def mla_naive_cache_write(cfg: MlaConfig, c_kv, k_pe, positions, slot_mapping, rms_weight, W_uk,
