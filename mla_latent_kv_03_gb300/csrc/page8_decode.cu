@@ -157,6 +157,11 @@ int p8_shares(int H, int num_ctas) {
   const int s = num_ctas / (H / group_heads(H));
   return s > 0 ? s : 1;
 }
+// (the split counts units of 64 tokens and a row in 32 bits)
+bool p8_sizes_fit(int64_t num_q, int32_t max_blocks, int bs) {
+  const int64_t tokens = (int64_t)max_blocks * bs;
+  return num_q <= 48 * 1024 && tokens <= (int64_t)1 << 30 && num_q * ((tokens + kTile - 1) / kTile) <= (int64_t)1 << 30;
+}
 P8Ws p8_ws(int64_t num_q, int H, bool pair, int shares, int64_t max_tokens, bool mass) {
   const WsLayout W = ws_layout(num_q, 1, shares);
   const size_t rest = (size_t)((pair ? 2 : H / kHG) - 1) * W.slots * kHG;
@@ -1462,16 +1467,15 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
       !p8_aligned(mass, 4))
     return MLA_ERR_INVALID_ARGUMENT;
   if (with_mass && batch > 65535) return MLA_ERR_UNSUPPORTED;
-  const size_t need = mla_page8_decode_workspace_size(cfg, num_q, batch, max_blocks, with_mass);
-  if (need == 0) return MLA_ERR_UNSUPPORTED;
-  if (ws_bytes < need) return MLA_ERR_WORKSPACE_TOO_SMALL;
-  const int H = cfg->num_heads, bs = cfg->block_size;
+  const int H = cfg->num_heads, bs = cfg->block_size, C = split_ctas(cfg);
+  if (!p8_sizes_fit(num_q, max_blocks, bs) || C <= 0) return MLA_ERR_UNSUPPORTED;
   const bool pair = use_pairs(H, num_q, batch);
   const int NH = pair ? 32 : group_heads(H);
-  const int shares = p8_shares(H, split_ctas(cfg));
+  const int shares = p8_shares(H, C);
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const P8Ws L = p8_ws(num_q, H, pair, shares, (int64_t)max_blocks * bs, with_mass);
+  if (ws_bytes < L.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
   const WsLayout W = ws_layout(num_q, 1, shares);
   // With num_blocks == 0 every block id is rejected before any copy; the maps
   // still need an extent.
@@ -1580,12 +1584,9 @@ extern "C" {
 
 size_t mla_page8_decode_workspace_size(const mla_config* cfg, int64_t num_q, int32_t batch,
                                        int32_t max_blocks_per_seq, int32_t with_mass) {
-  if (validate_config(cfg) != MLA_OK || cfg->dtype != MLA_BF16 || num_q < 0 ||
-      num_q > 48 * 1024 || batch < 0 || max_blocks_per_seq < 0 ||
-      max_blocks_per_seq > ((int64_t)1 << 30) / cfg->block_size)
+  if (validate_config(cfg) != MLA_OK || cfg->dtype != MLA_BF16 || num_q < 0 || batch < 0 ||
+      max_blocks_per_seq < 0 || !p8_sizes_fit(num_q, max_blocks_per_seq, cfg->block_size))
     return 0;
-  // (the split counts units of 64 tokens and a row in 32 bits)
-  if (num_q * (((int64_t)max_blocks_per_seq * cfg->block_size + kTile - 1) / kTile) > (int64_t)1 << 30) return 0;
   const int C = split_ctas(cfg), H = cfg->num_heads;
   if (C <= 0) return 0;
   return p8_ws(num_q, H, use_pairs(H, num_q, batch), p8_shares(H, C), (int64_t)max_blocks_per_seq * cfg->block_size,
