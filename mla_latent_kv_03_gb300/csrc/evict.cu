@@ -1,6 +1,8 @@
 // Eviction from a paged cache by accumulated attention weight:
 // mla_evict_select (which tokens of each sequence stay) and mla_page8_compact
 // (their rows moved, in order, into other pages).
+#include <type_traits>
+
 #include "async_copy.cuh"
 #include "cluster.cuh"
 #include "internal.h"
@@ -21,8 +23,9 @@ namespace {
 // counts: over a warp's 32-token steps by ballots, over warps and CTAs by their
 // totals. The keys are read once, into shared memory (kKeys a CTA; a piece
 // beyond that is read again from the cache in every pass). The CTAs of a
-// cluster meet once a pass: each adds up all their histograms through
-// distributed shared memory.
+// cluster meet once a pass: each copies its histogram to all (bulk copies counted
+// on the receiver's mbarrier; a barrier of the cluster would order global memory
+// too, which takes longer than the counting) and adds up what it gets.
 // Bound: latency. One pass over 4 bytes a token, a histogram, a meeting and a
 // scan for each of the four digits, and the two steps at the end: 10.8 us for 64
 // sequences of 4,096 tokens on one GB300 (2 CTAs each), 26.6 us for 3 of 131,072
@@ -31,7 +34,8 @@ namespace {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kKeys = 40 * 1024;              // keys a CTA holds
-constexpr int kSelSmem = kKeys * 4;
+constexpr int kList = 256;                    // keys of the first digit that a warp lists
+constexpr int kSelSmem = (kKeys + kSelWarps * kList) * 4;
 constexpr int kSelPiece = 1024;               // tokens a CTA takes before another joins
 
 struct SelectArgs {
@@ -41,6 +45,7 @@ struct SelectArgs {
   int32_t max_blocks;
   const int32_t* seq_lens;
   int32_t bs_shift, sinks, recent, budget, cluster;
+  int32_t held;   // keys of a CTA in shared memory
   int32_t* keep;
   int32_t* new_lens;
   uint32_t* status;
@@ -51,16 +56,14 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
   const uint32_t u = __float_as_uint(m + 0.f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
-__device__ __forceinline__ int ld_cluster(uint32_t addr) {
-  int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a) {
   extern __shared__ uint32_t sKey[];
-  __shared__ int hist[3][256];  // (another CTA may still read the last pass's)
-  __shared__ int sTotal[2];                     // tokens above T and of key T in this CTA
+  __shared__ __align__(16) int hist[2][256];    // this CTA's digits
+  __shared__ __align__(16) int got[2][8][256];  // every CTA's
+  __shared__ __align__(16) int gotTotal[8][4];
+  __shared__ uint64_t bar[3];                   // of got and of gotTotal
+  __shared__ __align__(16) int sTotal[4];       // tokens above T and of key T in this CTA
   __shared__ int sAbove[kSelWarps], sTies[kSelWarps];
   __shared__ int sPick, sNeed;
   pdl_wait();
@@ -78,6 +81,14 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a)
     for (int i = rank * kSelThreads + tid; i < a.budget; i += CL * kSelThreads) keep[i] = i < n ? i : -1;
     return;
   }
+  // (every CTA's barriers are there before the first counts reach them)
+  if (tid < 256) hist[0][tid] = 0;
+  if (tid == 0) {
+    for (int i = 0; i < 3; ++i) mbar_init(&bar[i], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   // this CTA's tokens [c0, c1); warp w's are 32 * steps of them
   const int steps = (n + CL * kSelThreads - 1) / (CL * kSelThreads);
   const int c0 = (int)min((int64_t)rank * steps * kSelThreads, (int64_t)n);
@@ -89,15 +100,16 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a)
                ? mass_key(a.mass[((size_t)p << a.bs_shift) + (t & ((1 << a.bs_shift) - 1))])
                : 0u;
   };
-  // eight tokens of a thread at a time: their pages together, then their masses
+  // U tokens of a thread at a time: their pages together, then their masses
   bool bad_page = false;
-  for (int t0 = c0 + tid; t0 < c1; t0 += 8 * kSelThreads) {
-    int32_t p[8];
-    float m[8];
+  auto load_keys = [&](int t0, auto batch) {
+    constexpr int U = decltype(batch)::value;
+    int32_t p[U];
+    float m[U];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) p[u] = t0 + u * kSelThreads < c1 ? bt[(t0 + u * kSelThreads) >> a.bs_shift] : 0;
+    for (int u = 0; u < U; ++u) p[u] = t0 + u * kSelThreads < c1 ? bt[(t0 + u * kSelThreads) >> a.bs_shift] : 0;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
+    for (int u = 0; u < U; ++u) {
       const int t = t0 + u * kSelThreads;
       const bool fine = p[u] >= 0 && p[u] < a.num_blocks;
       bad_page |= t < c1 && !fine;
@@ -105,45 +117,88 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a)
       if (t < c1 && fine) m[u] = a.mass[((size_t)p[u] << a.bs_shift) + (t & ((1 << a.bs_shift) - 1))];
     }
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
+    for (int u = 0; u < U; ++u) {
       const int i = t0 - c0 + u * kSelThreads;
-      if (t0 + u * kSelThreads < c1 && i < kKeys) sKey[i] = mass_key(m[u]);
+      if (t0 + u * kSelThreads < c1 && i < a.held) sKey[i] = mass_key(m[u]);
+    }
+  };
+  for (int t0 = c0 + tid; t0 < c1;) {
+    if (c1 - t0 > 2 * kSelThreads) {
+      load_keys(t0, std::integral_constant<int, 16>{});
+      t0 += 16 * kSelThreads;
+    } else {
+      load_keys(t0, std::integral_constant<int, 2>{});
+      t0 += 2 * kSelThreads;
     }
   }
   if (bad_page) set_status(a.status, MLA_DEV_BAD_BLOCK);
-  auto key = [&](int t) { return t - c0 < kKeys ? sKey[t - c0] : load_key(t); };
+  __syncwarp();
+  auto key = [&](int t) { return t - c0 < a.held ? sKey[t - c0] : load_key(t); };
   const int want = a.budget - a.sinks - a.recent;  // middle tokens that stay
   int need = want;
   uint32_t prefix = 0, mask = 0;
-  if (tid < 256) hist[0][tid] = 0;
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   __syncthreads();
+  uint32_t* list = sKey + a.held + warp * kList;
+  int listed = kList + 1;
   for (int pass = 0; pass < 4 && want > 0; ++pass) {
     const int shift = 24 - 8 * pass;
-    int* h = hist[pass % 3];
-    const int lo = max(c0, m0), hi = min(c1, m1);
-    for (int t0 = lo; t0 < hi; t0 += kSelThreads) {
-      const int t = t0 + tid;
-      const uint32_t k = t < hi ? key(t) : 0u;
-      const bool in = t < hi && (k & mask) == prefix;
+    auto count_digit = [&](uint32_t k, bool there) {
+      const bool in = there && (k & mask) == prefix;
       const uint32_t d = in ? (k >> shift) & 255u : 256u;
       int all;
       __match_all_sync(0xffffffffu, d, &all);
       if (all) {  // a warp of equal digits counts once: equal keys do not queue up
-        if (in && lane == 0) atomicAdd(&h[d], 32);
+        if (in && lane == 0) atomicAdd(&hist[pass & 1][d], 32);
       } else if (in) {
-        atomicAdd(&h[d], 1);
+        atomicAdd(&hist[pass & 1][d], 1);
+      }
+      return in;
+    };
+    if (pass > 1 && listed <= kList) {
+      for (int i = 0; i < listed; i += 32) count_digit(list[i + lane], i + lane < listed);
+    } else {
+      // The second pass lists the warp's keys of the first digit, which are few
+      // in most distributions: if they fit, the passes after it need no others.
+      if (pass == 1) listed = 0;
+      const int hi = min(c1, m1);
+      for (int t0 = max(c0, m0); t0 < hi; t0 += kSelThreads) {
+        const int t = t0 + tid;
+        const uint32_t k = t < hi ? key(t) : 0u;
+        const bool in = count_digit(k, t < hi);
+        if (pass == 1) {
+          const uint32_t some = __ballot_sync(0xffffffffu, in);
+          const int at = listed + __popc(some & ((1u << lane) - 1));
+          if (in && at < kList) list[at] = k;
+          listed += __popc(some);
+        }
       }
     }
-    if (tid < 256) hist[(pass + 1) % 3][tid] = 0;
-    cl::sync();
+    if (CL > 1) fence_proxy_async_smem();
+    __syncthreads();
+    if (CL > 1 && warp == 0) {
+      if (lane == 0) mbar_arrive_expect_tx(&bar[pass & 1], CL * (int)sizeof(hist[0]));
+      __syncwarp();
+      if (lane < CL) {
+        cl::bulk_to_peer(cl::map(smem_u32(got[pass & 1][rank]), lane), smem_u32(hist[pass & 1]), sizeof(hist[0]),
+                         cl::map(smem_u32(&bar[pass & 1]), lane));
+        cl::bulk_commit();
+      }
+      __syncwarp();
+    }
     // the cluster's count of digit 255 - tid, and of the digits above it
     int count = 0, above = 0;
     if (tid < 256) {
-      const uint32_t at = smem_u32(&h[255 - tid]);
-      int v[8];
+      if (CL > 1) {
+        if (!mbar_wait(&bar[pass & 1], pass >> 1)) set_status(a.status, MLA_DEV_TIMEOUT);
 #pragma unroll
-      for (int r = 0; r < 8; ++r) v[r] = r < CL ? ld_cluster(cl::map(at, r)) : 0;
-      count = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+        for (int r = 0; r < 8; ++r)
+          if (r < CL) count += got[pass & 1][r][255 - tid];
+      } else {
+        count = hist[pass & 1][255 - tid];
+      }
+      // (its last copies have been read: every CTA has sent the counts that follow them)
+      hist[(pass + 1) & 1][tid] = 0;
       above = count;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -155,7 +210,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a)
     }
     __syncthreads();
     if (tid < 256) {
-      for (int w = 0; w < warp; ++w) above += sAbove[w];
+#pragma unroll
+      for (int w = 0; w < 7; ++w) above += w < warp ? sAbove[w] : 0;
       if (above < need && need <= above + count) {  // (one thread)
         sPick = 255 - tid;
         sNeed = need - above;
@@ -165,7 +221,6 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a)
     prefix |= (uint32_t)sPick << shift;
     mask |= 255u << shift;
     need = sNeed;
-    __syncthreads();
   }
   // how many tokens of each warp stay for sure, and how many have key T
   const int w0 = c0 + warp * steps * 32;
@@ -178,12 +233,17 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a)
       tie = k == prefix;
     }
   };
+  // (as far as the lists' place holds it, it is not found again)
+  uint2* found = reinterpret_cast<uint2*>(list);
+  const int places = kList / 2;
   int above_n = 0, ties_n = 0;
   for (int s = 0; s < steps; ++s) {
     bool above, tie;
     classify(w0 + s * 32 + lane, above, tie);
-    above_n += __popc(__ballot_sync(0xffffffffu, above));
-    ties_n += __popc(__ballot_sync(0xffffffffu, tie));
+    const uint32_t am = __ballot_sync(0xffffffffu, above), tm = __ballot_sync(0xffffffffu, tie);
+    if (lane == 0 && s < places) found[s] = make_uint2(am, tm);
+    above_n += __popc(am);
+    ties_n += __popc(tm);
   }
   if (lane == 0) sAbove[warp] = above_n, sTies[warp] = ties_n;
   __syncthreads();
@@ -193,27 +253,48 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a)
     const int u = __shfl_up_sync(0xffffffffu, above_at, o), v = __shfl_up_sync(0xffffffffu, ties_at, o);
     if (lane >= o) above_at += u, ties_at += v;
   }
-  if (tid == 31) sTotal[0] = above_at, sTotal[1] = ties_at;
+  if (CL > 1 && warp == 0) {
+    if (lane == 31) {
+      sTotal[0] = above_at, sTotal[1] = ties_at;
+      fence_proxy_async_smem();
+      mbar_arrive_expect_tx(&bar[2], CL * (int)sizeof(sTotal));
+    }
+    __syncwarp();
+    if (lane < CL) {
+      cl::bulk_to_peer(cl::map(smem_u32(gotTotal[rank]), lane), smem_u32(sTotal), sizeof(sTotal),
+                       cl::map(smem_u32(&bar[2]), lane));
+      cl::bulk_commit();
+    }
+    __syncwarp();
+  }
   above_at = __shfl_sync(0xffffffffu, above_at - sAbove[lane], warp);
   ties_at = __shfl_sync(0xffffffffu, ties_at - sTies[lane], warp);
-  cl::sync();
-  for (int r = 0; r < rank; ++r) {
-    above_at += ld_cluster(cl::map(smem_u32(&sTotal[0]), r));
-    ties_at += ld_cluster(cl::map(smem_u32(&sTotal[1]), r));
+  if (CL > 1) {
+    if (!mbar_wait(&bar[2], 0)) set_status(a.status, MLA_DEV_TIMEOUT);
+    for (int r = 0; r < rank; ++r) above_at += gotTotal[r][0], ties_at += gotTotal[r][1];
   }
   for (int s = 0; s < steps; ++s) {
     const int t = w0 + s * 32 + lane;
-    bool above, tie;
-    classify(t, above, tie);
-    const uint32_t am = __ballot_sync(0xffffffffu, above), tm = __ballot_sync(0xffffffffu, tie);
+    uint2 f;
+    if (s < places) {
+      f = found[s];
+    } else {
+      bool above, tie;
+      classify(t, above, tie);
+      f.x = __ballot_sync(0xffffffffu, above), f.y = __ballot_sync(0xffffffffu, tie);
+    }
+    const uint32_t am = f.x, tm = f.y;
+    const bool above = am >> lane & 1, tie = tm >> lane & 1;
     const uint32_t below = (1u << lane) - 1;
     const int ties_before = ties_at + __popc(tm & below);
-    if (above || (tie && ties_before < need))
-      keep[above_at + __popc(am & below) + min(need, ties_before)] = t;
+    const int at = above_at + __popc(am & below) + min(need, ties_before);
+    // (at lies in the budget, unless a wait has run out)
+    if ((above || (tie && ties_before < need)) && (uint32_t)at < (uint32_t)a.budget) keep[at] = t;
     above_at += __popc(am);
     ties_at += __popc(tm);
   }
-  cl::sync();  // the others may still read this CTA's totals
+  // What the others send has arrived; what this CTA sends has to be read.
+  if (warp == 0) cl::bulk_wait_read<0>();
 }
 
 // CTAs that share a sequence of up to `tokens`: another as long as each has more
@@ -235,17 +316,18 @@ int select_cluster(int64_t tokens, int batch) {
   return c;
 }
 
-cudaError_t launch_select(const SelectArgs& a, int batch, cudaStream_t stream) {
+cudaError_t launch_select(SelectArgs a, int batch, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmem);
   if (e != cudaSuccess) return e;
   // a piece of the longest sequence, in shared memory as far as it fits
   const int64_t tokens = (int64_t)a.max_blocks << a.bs_shift;
   int64_t piece = (tokens + a.cluster * kSelThreads - 1) / (a.cluster * kSelThreads) * kSelThreads;
   if (piece > kKeys) piece = kKeys;
+  a.held = (int32_t)piece;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)batch * a.cluster);
   cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = (size_t)piece * 4;
+  cfg.dynamicSmemBytes = (size_t)(piece + kSelWarps * kList) * 4;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -380,7 +462,7 @@ mla_status mla_evict_select(const mla_config* cfg, const float* mass, int64_t nu
     return MLA_ERR_INVALID_ARGUMENT;
   const int shift = cfg->block_size == 16 ? 4 : cfg->block_size == 32 ? 5 : 6;
   const SelectArgs a{mass, num_blocks, block_table, max_blocks_per_seq, seq_lens, shift, sinks,
-                     recent, budget, select_cluster((int64_t)max_blocks_per_seq << shift, batch), keep,
+                     recent, budget, select_cluster((int64_t)max_blocks_per_seq << shift, batch), 0, keep,
                      new_lens, dev_status};
   const cudaError_t e = launch_select(a, batch, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
