@@ -26,13 +26,17 @@ namespace {
 // cluster meet once a pass: each copies its histogram to all (bulk copies counted
 // on the receiver's mbarrier; a barrier of the cluster would order global memory
 // too, which takes longer than the counting) and adds up what it gets.
-// Bound: latency. One pass over 4 bytes a token, a histogram, a meeting and a
-// scan for each of the four digits, and the two steps at the end: 10.8 us for 64
-// sequences of 4,096 tokens on one GB300 (2 CTAs each), 26.6 us for 3 of 131,072
-// (8 each), of which reading the masses at HBM's rate would be 0.2 us.
+// The second pass also lists the keys of the first digit, so that the last two
+// need not go through all; and what the count of the classes found is kept for the
+// writing, 2 bits a token.
+// Bound: latency. One pass over 4 bytes a token, a histogram, a meeting and a scan
+// for each of the four digits, and the two steps at the end: 9.0 us for 64
+// sequences of 4,096 tokens on one GB300 (2 CTAs each), 22.6 us for 3 of up to
+// 131,072 (8 each), of which reading the masses at HBM's rate would be 0.2 us.
 // ---------------------------------------------------------------------------
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSms = 152;                     // of the device
 constexpr int kKeys = 40 * 1024;              // keys a CTA holds
 constexpr int kList = 256;                    // keys of the first digit that a warp lists
 constexpr int kSelSmem = (kKeys + kSelWarps * kList) * 4;
@@ -57,7 +61,11 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a) {
+// PER_SM: CTAs that run on an SM. With one, the registers are free for twice as
+// many tokens at a time.
+template <int PER_SM>
+__global__ void __launch_bounds__(kSelThreads, PER_SM) evict_select_kernel(SelectArgs a) {
+  constexpr int kBatch = PER_SM == 1 ? 16 : 8;
   extern __shared__ uint32_t sKey[];
   __shared__ __align__(16) int hist[2][256];    // this CTA's digits
   __shared__ __align__(16) int got[2][8][256];  // every CTA's
@@ -124,8 +132,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a)
   };
   for (int t0 = c0 + tid; t0 < c1;) {
     if (c1 - t0 > 2 * kSelThreads) {
-      load_keys(t0, std::integral_constant<int, 16>{});
-      t0 += 16 * kSelThreads;
+      load_keys(t0, std::integral_constant<int, kBatch>{});
+      t0 += kBatch * kSelThreads;
     } else {
       load_keys(t0, std::integral_constant<int, 2>{});
       t0 += 2 * kSelThreads;
@@ -299,25 +307,29 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a)
 
 // CTAs that share a sequence of up to `tokens`: another as long as each has more
 // than kSelPiece tokens and all of them run at once (clusters of 8 place badly
-// beyond 64 CTAs), and wherever the keys would not fit otherwise. Measured on one
+// beyond 96 CTAs), and wherever the keys would not fit otherwise. Measured on one
 // GB300, us with 1 / 2 / 4 / 8 CTAs (the choice marked):
-//     1 x 3,000     10.8   10.4   *9.6   10.3
-//    64 x 2,048     10.3   *9.6   14.6   27.8
-//    64 x 8,192     15.8  *12.6   18.5   31.8
-//   256 x 4,096    *19.6   30.1   47.2  100.9
-//    16 x 16,384    24.5   16.2  *12.8   17.3
-//     3 x 131,072  309.3  130.9   43.3  *26.6
-//    64 x 131,072  318.5  136.1  *90.5   99.9
+//     1 x 3,000     10.9    8.7   *8.0    8.3
+//     8 x 16,384    24.7   16.5   13.3  *10.0
+//    16 x 16,384    24.8   16.5  *13.3   18.7
+//    64 x 2,048      7.7   *8.1   15.4   38.9
+//    64 x 4,096     11.7   *9.0   16.0   39.6
+//   256 x 4,096    *17.8   25.6   38.6   81.0
+//     3 x 131,072  296.5  127.5   46.4  *27.0
+//    64 x 131,072  315.4  137.9 *104.1  147.0
 int select_cluster(int64_t tokens, int batch) {
   int c = 1;
   while (c < 8 && (tokens > (int64_t)c * kKeys ||
-                   (tokens > (int64_t)c * kSelPiece && (int64_t)batch * 2 * c <= (c == 4 ? 64 : 152))))
+                   (tokens > (int64_t)c * kSelPiece && (int64_t)batch * 2 * c <= (c == 4 ? 96 : kSms))))
     c *= 2;
   return c;
 }
 
 cudaError_t launch_select(SelectArgs a, int batch, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmem);
+  // (more CTAs than SMs: 256 x 4,096 takes 17.8 us by two an SM, 22.9 by one; fewer:
+  // 3 x 131,072 28.9 and 27.0)
+  auto kernel = (int64_t)batch * a.cluster > kSms ? evict_select_kernel<2> : evict_select_kernel<1>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmem);
   if (e != cudaSuccess) return e;
   // a piece of the longest sequence, in shared memory as far as it fits
   const int64_t tokens = (int64_t)a.max_blocks << a.bs_shift;
@@ -337,7 +349,7 @@ cudaError_t launch_select(SelectArgs a, int batch, cudaStream_t stream) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 // ---------------------------------------------------------------------------

@@ -518,6 +518,24 @@ def test_select_long(n, budget, kind):
     assert np.array_equal(keep[0], want)
 
 
+@pytest.mark.parametrize("batch,n", [(1, 900), (3, 3000), (20, 9000), (160, 1500), (300, 700)])
+@pytest.mark.parametrize("kind", ["positive", "equal"])
+def test_select_at_every_split(batch, n, kind):
+    """Every number of CTAs a sequence and of CTAs an SM, ragged lengths (some
+    below the budget), with few keys of the first digit and with all of them."""
+    rng = np.random.default_rng(batch)
+    lens = rng.integers(0, n + 1, batch)
+    lens[0] = n
+    most = (n + 31) // 32
+    table = rng.permutation(batch * most).reshape(batch, most).astype(np.int32)
+    mass = _masses(rng, batch * most, 32, kind)
+    keep, new, bits = _select(mass, table, lens.tolist(), 3, 17, 300, 32)
+    want_keep, want_new = P.select(mass, table, lens, 3, 17, 300)
+    assert bits == 0
+    assert np.array_equal(new, want_new)
+    assert np.array_equal(keep, want_keep)
+
+
 def test_select_flags_bad_tables_and_lengths():
     rng = np.random.default_rng(1)
     mass = _masses(rng, 8, 16, "positive")
