@@ -18,7 +18,7 @@ namespace {
 // at a time from the top, and how many tokens of key T stay; then every token
 // above T and the first ones of key T are written in order.
 //
-// A cluster of 1 to 8 CTAs takes a sequence, each CTA a contiguous piece of it,
+// A cluster of 1 to 16 CTAs takes a sequence, each CTA a contiguous piece of it,
 // and each warp a contiguous piece of that, so order is a matter of prefix
 // counts: over a warp's 32-token steps by ballots, over warps and CTAs by their
 // totals. The keys are read once, into shared memory (kKeys a CTA; a piece
@@ -31,11 +31,12 @@ namespace {
 // writing, 2 bits a token.
 // Bound: latency. One pass over 4 bytes a token, a histogram, a meeting and a scan
 // for each of the four digits, and the two steps at the end: 9.0 us for 64
-// sequences of 4,096 tokens on one GB300 (2 CTAs each), 22.6 us for 3 of up to
-// 131,072 (8 each), of which reading the masses at HBM's rate would be 0.2 us.
+// sequences of 4,096 tokens on one GB300 (2 CTAs each), 18 us for 3 of up to
+// 131,072 (16 each), of which reading the masses at HBM's rate would be 0.2 us.
 // ---------------------------------------------------------------------------
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kMaxCl = 16;                    // CTAs of a cluster
 constexpr int kSms = 152;                     // of the device
 constexpr int kKeys = 40 * 1024;              // keys a CTA holds
 constexpr int kList = 256;                    // keys of the first digit that a warp lists
@@ -68,8 +69,8 @@ __global__ void __launch_bounds__(kSelThreads, PER_SM) evict_select_kernel(Selec
   constexpr int kBatch = PER_SM == 1 ? 16 : 8;
   extern __shared__ uint32_t sKey[];
   __shared__ __align__(16) int hist[2][256];    // this CTA's digits
-  __shared__ __align__(16) int got[2][8][256];  // every CTA's
-  __shared__ __align__(16) int gotTotal[8][4];
+  __shared__ __align__(16) int got[2][kMaxCl][256];  // every CTA's
+  __shared__ __align__(16) int gotTotal[kMaxCl][4];
   __shared__ uint64_t bar[3];                   // of got and of gotTotal
   __shared__ __align__(16) int sTotal[4];       // tokens above T and of key T in this CTA
   __shared__ int sAbove[kSelWarps], sTies[kSelWarps];
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(kSelThreads, PER_SM) evict_select_kernel(Selec
       if (CL > 1) {
         if (!mbar_wait(&bar[pass & 1], pass >> 1)) set_status(a.status, MLA_DEV_TIMEOUT);
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
+        for (int r = 0; r < kMaxCl; ++r)
           if (r < CL) count += got[pass & 1][r][255 - tid];
       } else {
         count = hist[pass & 1][255 - tid];
@@ -306,30 +307,35 @@ __global__ void __launch_bounds__(kSelThreads, PER_SM) evict_select_kernel(Selec
 }
 
 // CTAs that share a sequence of up to `tokens`: another as long as each has more
-// than kSelPiece tokens and all of them run at once (clusters of 8 place badly
-// beyond 96 CTAs), and wherever the keys would not fit otherwise. Measured on one
-// GB300, us with 1 / 2 / 4 / 8 CTAs (the choice marked):
+// than kSelPiece tokens and all of them run at once (clusters of 8 and 16 place
+// badly beyond 96 CTAs, and 16 pay later), and up to 8 wherever the keys would
+// not fit otherwise. Measured on one GB300, us with 1 / 2 / 4 / 8 / 16 CTAs (the
+// choice marked):
 //     1 x 3,000     10.9    8.7   *8.0    8.3
-//     8 x 16,384    24.7   16.5   13.3  *10.0
+//     1 x 16,384    24.6   16.4   13.3   *9.8   10.3
+//     6 x 32,768                  16.9   14.0  *11.6
+//     8 x 65,536   125.4   46.1   26.5  *17.6   29.7
 //    16 x 16,384    24.8   16.5  *13.3   18.7
 //    64 x 2,048      7.7   *8.1   15.4   38.9
 //    64 x 4,096     11.7   *9.0   16.0   39.6
 //   256 x 4,096    *17.8   25.6   38.6   81.0
-//     3 x 131,072  296.5  127.5   46.4  *27.0
+//     3 x 131,072  296.5  127.5   46.4   27.0  *19.0
 //    64 x 131,072  315.4  137.9 *104.1  147.0
-int select_cluster(int64_t tokens, int batch) {
+int select_cluster(int64_t tokens, int64_t batch) {
   int c = 1;
   while (c < 8 && (tokens > (int64_t)c * kKeys ||
-                   (tokens > (int64_t)c * kSelPiece && (int64_t)batch * 2 * c <= (c == 4 ? 96 : kSms))))
+                   (tokens > (int64_t)c * kSelPiece && batch * 2 * c <= (c == 4 ? 96 : kSms))))
     c *= 2;
-  return c;
+  return c == 8 && tokens > 16 * kSelPiece && batch * 16 <= 96 ? 16 : c;
 }
 
 cudaError_t launch_select(SelectArgs a, int batch, cudaStream_t stream) {
   // (more CTAs than SMs: 256 x 4,096 takes 17.8 us by two an SM, 22.9 by one; fewer:
   // 3 x 131,072 28.9 and 27.0)
   auto kernel = (int64_t)batch * a.cluster > kSms ? evict_select_kernel<2> : evict_select_kernel<1>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmem);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmem);
+  if (e == cudaSuccess && a.cluster > 8)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   // a piece of the longest sequence, in shared memory as far as it fits
   const int64_t tokens = (int64_t)a.max_blocks << a.bs_shift;
