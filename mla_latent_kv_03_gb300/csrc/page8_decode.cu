@@ -1255,22 +1255,23 @@ __global__ void __launch_bounds__(256) page8_merge_kernel(const __grid_constant_
 
 // The merge of a few parts and the output projection in one: CTA = (ROWS rows,
 // head h). W_uv[h] (128 KB) comes by cp.async while 256 / ROWS threads a row
-// merge its 512 latents to bf16 (as the other projections take theirs); then 8
-// warps, each a quarter of K and half of the columns (m16n8k16), whose sums meet
-// in shared memory. Every part is read once. ROWS = 8 (half of the mma's rows
-// idle) where that still leaves at most one CTA an SM: the merge, at latency, is
-// what takes the time. 64 rows of 16 heads: 9.0 us alone, 4 us behind a decode,
+// merge its 512 latents to two bf16 terms each (one would add as much error as
+// the rounding of the output); then 8 warps, each a quarter of K and half of the
+// columns (m16n8k16), whose sums meet in shared memory. Every part is read once.
+// MERGED: one part a row, merged before. ROWS = 8 (the second terms are the mma's
+// other rows) where that still leaves at most one CTA an SM: the merge, at
+// latency, is what takes the time. 64 rows of 16 heads: 9.0 us alone, 4 us behind a decode,
 // which hides the weights' copy (2 MB in all); 32 rows of 128 heads: 18 us.
 template <int ROWS>
 struct Mp {
   static constexpr int stride = kDc * 2 + 16;     // bytes of a merged row, padded against bank conflicts
   static constexpr int w = 0;                     // two halves of 64 columns, 128-byte rows
   static constexpr int a = w + kDc * 256;
-  static constexpr int red = a + ROWS * stride;   // [4][ROWS][128]
+  static constexpr int red = a + 2 * ROWS * stride;  // [4][ROWS][128]
   static constexpr int rows = red + 4 * ROWS * kDv * 4;
   static constexpr int bytes = rows + kSelfMaxRows * 16 + 16;
 };
-template <int ROWS>
+template <int ROWS, bool MERGED>
 __global__ void __launch_bounds__(256) page8_merge_proj_kernel(const __grid_constant__ P8Args a,
                                                                const __nv_bfloat16* W_uv,
                                                                __nv_bfloat16* out) {
@@ -1282,7 +1283,7 @@ __global__ void __launch_bounds__(256) page8_merge_proj_kernel(const __grid_cons
   const int h = blockIdx.y, row0 = blockIdx.x * ROWS, H = a.num_heads;
   int4* plan = reinterpret_cast<int4*>(smem_mp + M::rows);
   int* plan_total = reinterpret_cast<int*>(smem_mp + M::rows + kSelfMaxRows * 16);
-  if (a.self_plan)
+  if (a.self_plan && !MERGED)
     for (int n = tid; n < (int)a.num_q; n += 256) plan[n] = make_int4(-1, -1, 0, 0);
   const __nv_bfloat16* src = W_uv + (size_t)h * kDc * kDv;
 #pragma unroll 4
@@ -1296,7 +1297,7 @@ __global__ void __launch_bounds__(256) page8_merge_proj_kernel(const __grid_cons
   // themselves have to be waited for.
   const int4* rows = reinterpret_cast<const int4*>(a.ws + ws_layout(a.num_q, 1, a.shares).row_info);
   int share = 1;
-  if (a.self_plan) {
+  if (a.self_plan && !MERGED) {
     __syncthreads();
     fill_rows(a, plan, nullptr, tid, 256, 0, 1);
     __syncthreads();
@@ -1313,7 +1314,8 @@ __global__ void __launch_bounds__(256) page8_merge_proj_kernel(const __grid_cons
   {
     const int r = tid / kTr, j = tid % kTr, n = row0 + r;
     HeadParts hp{a.lse_first, a.o_first, 0};
-    if (n < a.num_q) hp = head_parts(a, rows, share, n, h);
+    if (n < a.num_q)
+      hp = MERGED ? HeadParts{nullptr, a.o_lat + ((size_t)n * H + h) * kDc, 1} : head_parts(a, rows, share, n, h);
     float4 v[kBatch][kVec];
     auto load = [&](int s0) {
 #pragma unroll
@@ -1325,10 +1327,10 @@ __global__ void __launch_bounds__(256) page8_merge_proj_kernel(const __grid_cons
         }
     };
     load(0);  // on their way while the weights are found
-    float m, den;
-    merge_weights<kTr>(hp, j, m, den);
+    float m = 0.f, den = 1.f;
+    if (!MERGED) merge_weights<kTr>(hp, j, m, den);
     const float inv = den == 0.f ? 0.f : 1.f / den, b = m == -INFINITY ? 0.f : m;
-    if (j == 0 && n < a.num_q) a.lse[(size_t)n * H + h] = den == 0.f ? -INFINITY : m + log2f(den);
+    if (!MERGED && j == 0 && n < a.num_q) a.lse[(size_t)n * H + h] = den == 0.f ? -INFINITY : m + log2f(den);
     float4 acc[kVec];
 #pragma unroll
     for (int k = 0; k < kVec; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1338,7 +1340,7 @@ __global__ void __launch_bounds__(256) page8_merge_proj_kernel(const __grid_cons
 #pragma unroll
       for (int u = 0; u < kBatch; ++u)
         if (s0 + u < hp.count) {
-          const float w = fast_exp2(hp.lse[(s0 + u) * kHG] - b) * inv;
+          const float w = MERGED ? 1.f : fast_exp2(hp.lse[(s0 + u) * kHG] - b) * inv;
 #pragma unroll
           for (int k = 0; k < kVec; ++k) {
             acc[k].x = fmaf(w, v[u][k].x, acc[k].x);
@@ -1349,9 +1351,16 @@ __global__ void __launch_bounds__(256) page8_merge_proj_kernel(const __grid_cons
         }
     }
 #pragma unroll
-    for (int k = 0; k < kVec; ++k)
-      *reinterpret_cast<uint2*>(smem_mp + M::a + r * M::stride + (j + kTr * k) * 8) =
-          make_uint2(pack_bf16(acc[k].x, acc[k].y), pack_bf16(acc[k].z, acc[k].w));
+    for (int k = 0; k < kVec; ++k) {
+      const uint32_t t0 = pack_bf16(acc[k].x, acc[k].y), t1 = pack_bf16(acc[k].z, acc[k].w);
+      auto low = [](uint32_t t) { return __uint_as_float(t << 16); };
+      auto high = [](uint32_t t) { return __uint_as_float(t & 0xffff0000u); };
+      uint8_t* at = smem_mp + M::a + r * M::stride + (j + kTr * k) * 8;
+      *reinterpret_cast<uint2*>(at) = make_uint2(t0, t1);
+      *reinterpret_cast<uint2*>(at + ROWS * M::stride) =
+          make_uint2(pack_bf16(acc[k].x - low(t0), acc[k].y - high(t0)),
+                     pack_bf16(acc[k].z - low(t1), acc[k].w - high(t1)));
+    }
   }
   cp_async_wait_all();
   __syncthreads();
@@ -1363,10 +1372,12 @@ __global__ void __launch_bounds__(256) page8_merge_proj_kernel(const __grid_cons
 #pragma unroll
   for (int ks = 0; ks < 8; ++ks) {
     const int k = kq * 128 + ks * 16;
+    // row g + 8: of the second terms, or a row of its own
     const uint8_t* lo = smem_mp + M::a + g * M::stride + (k + 2 * q) * 2;
-    const uint32_t a0 = *reinterpret_cast<const uint32_t*>(lo), a2 = *reinterpret_cast<const uint32_t*>(lo + 16);
-    const uint32_t a1 = ROWS == 16 ? *reinterpret_cast<const uint32_t*>(lo + 8 * M::stride) : 0u;
-    const uint32_t a3 = ROWS == 16 ? *reinterpret_cast<const uint32_t*>(lo + 8 * M::stride + 16) : 0u;
+    auto frag = [&](int row, int at) { return *reinterpret_cast<const uint32_t*>(lo + row * M::stride + at); };
+    const uint32_t a0 = frag(0, 0), a1 = frag(8, 0), a2 = frag(0, 16), a3 = frag(8, 16);
+    uint32_t c0 = 0, c1 = 0, c2 = 0, c3 = 0;
+    if (ROWS == 16) c0 = frag(16, 0), c1 = frag(24, 0), c2 = frag(16, 16), c3 = frag(24, 16);
     const int kr = k + (lane & 7) + (((lane >> 3) & 1) << 3);
 #pragma unroll
     for (int np = 0; np < 4; ++np) {
@@ -1374,13 +1385,21 @@ __global__ void __launch_bounds__(256) page8_merge_proj_kernel(const __grid_cons
       ldsm_x4_t(smem_u32(sW + sw128(kr, np * 2 + (lane >> 4))), b0, b1, b2, b3);
       mma_16816(acc[2 * np], a0, a1, a2, a3, b0, b1);
       mma_16816(acc[2 * np + 1], a0, a1, a2, a3, b2, b3);
+      if (ROWS == 16) {
+        mma_16816(acc[2 * np], c0, c1, c2, c3, b0, b1);
+        mma_16816(acc[2 * np + 1], c0, c1, c2, c3, b2, b3);
+      }
     }
   }
 #pragma unroll
   for (int nt = 0; nt < 8; ++nt) {
     float* d = sRed + (kq * ROWS + g) * kDv + nh * 64 + nt * 8 + 2 * q;
-    *reinterpret_cast<float2*>(d) = make_float2(acc[nt][0], acc[nt][1]);
-    if (ROWS == 16) *reinterpret_cast<float2*>(d + 8 * kDv) = make_float2(acc[nt][2], acc[nt][3]);
+    if (ROWS == 16) {
+      *reinterpret_cast<float2*>(d) = make_float2(acc[nt][0], acc[nt][1]);
+      *reinterpret_cast<float2*>(d + 8 * kDv) = make_float2(acc[nt][2], acc[nt][3]);
+    } else {
+      *reinterpret_cast<float2*>(d) = make_float2(acc[nt][0] + acc[nt][2], acc[nt][1] + acc[nt][3]);
+    }
   }
   __syncthreads();
 #pragma unroll
@@ -1549,17 +1568,17 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
                  : launch(page8_decode_kernel<32, 1>, Sm<32>::threads, Sm<32>::alloc);
   if (e == cudaSuccess && many_parts)
     e = launch_pdl(page8_merge_kernel, dim3((unsigned)(num_q * H), 2), dim3(256), 0, st, a);
+  auto project = [&](auto kernel, int rows, int smem) {
+    const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return r != cudaSuccess ? r
+                            : launch_pdl(kernel, dim3((unsigned)((num_q + rows - 1) / rows), H), dim3(256), smem,
+                                         st, a, (const __nv_bfloat16*)W_uv, (__nv_bfloat16*)out);
+  };
   if (e == cudaSuccess && merge_proj) {
-    auto project = [&](auto kernel, int rows, int smem) {
-      const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      return r != cudaSuccess ? r
-                              : launch_pdl(kernel, dim3((unsigned)((num_q + rows - 1) / rows), H), dim3(256), smem,
-                                           st, a, (const __nv_bfloat16*)W_uv, (__nv_bfloat16*)out);
-    };
     // (40 rows of 16 heads: 24.3 us by 8, 25.9 by 16; 96 rows: 40.3 and 36.4)
     e = (num_q + 7) / 8 * H <= (int64_t)shares * a.groups
-            ? project(page8_merge_proj_kernel<8>, 8, Mp<8>::bytes)
-            : project(page8_merge_proj_kernel<16>, 16, Mp<16>::bytes);
+            ? project(page8_merge_proj_kernel<8, false>, 8, Mp<8>::bytes)
+            : project(page8_merge_proj_kernel<16, false>, 16, Mp<16>::bytes);
   }
   if (e != cudaSuccess) return MLA_ERR_CUDA;
   if (with_mass) {
@@ -1572,7 +1591,10 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
       if (e != cudaSuccess) return MLA_ERR_CUDA;
     }
   }
-  return merge_proj ? MLA_OK : mla_out_proj(cfg, a.o_lat, W_uv, out, num_q, stream);
+  if (merge_proj) return MLA_OK;
+  if (many_parts)
+    return project(page8_merge_proj_kernel<8, true>, 8, Mp<8>::bytes) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  return mla_out_proj(cfg, a.o_lat, W_uv, out, num_q, stream);
 }
 
 }  // namespace
