@@ -1418,9 +1418,9 @@ __global__ void __launch_bounds__(256) page8_merge_proj_kernel(const __grid_cons
 }
 
 // mass[slot(t)] = decay * mass[slot(t)] + sum over the sequence's rows and all
-// heads of 2^(score - lse), rows and heads in order: one thread per token. Bound
-// by latency and the scores' bytes: 8.7 us for 64 sequences of 4,096 tokens and 16
-// heads (16.8 MB, most of it still in L2).
+// heads of 2^(score - lse), in a fixed order: P neighbouring threads per token, each
+// with every P-th (row, 16 heads). Bound by latency and the scores' bytes: 8.7 us
+// for 64 sequences of 4,096 tokens and 16 heads (16.8 MB, most of it still in L2).
 struct MassArgs {
   const float* scores;
   const float* lse;
@@ -1432,10 +1432,11 @@ struct MassArgs {
   float decay;
   float* mass;
 };
+template <int P>
 __global__ void __launch_bounds__(256) page8_mass_kernel(MassArgs a) {
   // (what the caller gave and the old mass are there, see page8_decode_kernel;
   // the scores and sums have to be waited for)
-  const int b = blockIdx.y, t = blockIdx.x * 256 + threadIdx.x;
+  const int b = blockIdx.y, t = (blockIdx.x * 256 + threadIdx.x) / P, part = threadIdx.x % P;
   const int len = a.seq_lens[b], q0 = a.query_start_loc[b], q1 = a.query_start_loc[b + 1];
   const int ql = q1 - q0;
   const int64_t max_tokens = (int64_t)a.max_blocks * a.block_size;
@@ -1452,13 +1453,14 @@ __global__ void __launch_bounds__(256) page8_mass_kernel(MassArgs a) {
   }
   pdl_wait();
   pdl_launch_dependents();
-  if (!mine) return;
   float sum = 0.f;
-  for (int n = max(q0, q0 + t - (len - ql)); n < q1; ++n) {  // rows at or behind token t
-    for (int g = 0; g < a.groups; ++g) {
-      const size_t tile = (size_t)n * a.groups + g;
+  if (mine) {
+    // rows at or behind token t (of at most 48 * 1,024, of 8 groups each)
+    const int end = q1 * a.groups;
+#pragma unroll 2
+    for (int tile = max(q0, q0 + t - (len - ql)) * a.groups + part; tile < end; tile += P) {
       const float4* s = reinterpret_cast<const float4*>(a.scores + (tile * max_tokens + t) * kHG);
-      const float4* e = reinterpret_cast<const float4*>(a.lse + tile * kHG);
+      const float4* e = reinterpret_cast<const float4*>(a.lse + (size_t)tile * kHG);
 #pragma unroll
       for (int k = 0; k < kHG / 4; ++k) {
         const float4 x = s[k], y = e[k];
@@ -1466,7 +1468,9 @@ __global__ void __launch_bounds__(256) page8_mass_kernel(MassArgs a) {
       }
     }
   }
-  *m = old + sum;
+#pragma unroll
+  for (int o = 1; o < P; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (mine && part == 0) *m = old + sum;
 }
 
 mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache8,
@@ -1586,8 +1590,16 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
                       H / kHG, num_q, num_blocks, decay, mass};
     const int64_t tokens = (int64_t)max_blocks * bs;
     if (tokens > 0) {
-      e = launch_pdl(page8_mass_kernel, dim3((unsigned)((tokens + 255) / 256), (unsigned)batch),
-                     dim3(256), 0, st, ma);
+      auto launch_mass = [&](auto kernel, int per_token) {
+        return launch_pdl(kernel, dim3((unsigned)((tokens * per_token + 255) / 256), (unsigned)batch), dim3(256), 0,
+                          st, ma);
+      };
+      // A warp a token from 8 (row, 16 heads) of a sequence on. By thread / by warp,
+      // us of the whole call: 64 x 4,096, 16 heads, 1 row 47.1 / 108; 16 x 4,096, 64
+      // heads, 1 row 42.9 / 54.3; 8 x 2,048, 128 heads, 1 row 36.0 / 33.6; 8 x 1,000, 16
+      // heads, 16 rows 41.9 / 34.5; 4 x 2,560, 16 heads, 512 rows 3,157 / 659.
+      e = num_q * (H / kHG) >= 8 * (int64_t)batch ? launch_mass(page8_mass_kernel<32>, 32)
+                                                  : launch_mass(page8_mass_kernel<1>, 1);
       if (e != cudaSuccess) return MLA_ERR_CUDA;
     }
   }
