@@ -830,3 +830,48 @@ def test_a_token_kept_twice_is_moved_twice():
         assert float(mass[-1, row]) == float(mass[p, r])
         if float(scales[p]) == float(scales[-1]):
             assert torch.equal(cache[-1, row], cache[p, r])
+
+
+def test_select_on_two_streams_at_once_and_replayed_with_other_lengths():
+    cfg = L.make_config(16, 32, "bf16")
+    rng = np.random.default_rng(4)
+    sets = []
+    for batch, n, budget in ((3, 40000, 500), (40, 3000, 700)):
+        most = (n + 31) // 32
+        table = rng.permutation(batch * most).reshape(batch, most).astype(np.int32)
+        mass = rng.random((batch * most, 32)).astype(np.float32)
+        lens = rng.integers(budget // 2, n + 1, batch)
+        s = dict(mass=dev(mass, torch.float32), table=dev(table, torch.int32), lens=dev(lens, torch.int32),
+                 keep=torch.zeros((batch, budget), dtype=torch.int32, device=DEV),
+                 new=torch.zeros(batch, dtype=torch.int32, device=DEV), stream=torch.cuda.Stream())
+        sets.append((s, mass, table, lens, budget, n))
+
+    def call(s):
+        L.mla_evict_select(cfg, s["mass"], s["table"], s["lens"], 2, 50, s["keep"], s["new"])
+
+    def check(s, mass, table, lens, budget):
+        want, want_n = P.select(mass, table, lens, 2, 50, budget)
+        assert np.array_equal(s["new"].cpu().numpy(), want_n)
+        assert np.array_equal(s["keep"].cpu().numpy(), want)
+
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, *_ in sets:
+            with torch.cuda.stream(s["stream"]):
+                call(s)
+    torch.cuda.synchronize()
+    for s, mass, table, lens, budget, _ in sets:
+        check(s, mass, table, lens, budget)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for s, *_ in sets:
+            call(s)
+    for _ in range(2):
+        new = [rng.integers(0, n + 1, len(lens)) for _, _, _, lens, _, n in sets]
+        for (s, *_), lens in zip(sets, new):
+            s["lens"].copy_(dev(lens, torch.int32))
+            s["keep"].fill_(-5)
+        g.replay()
+        torch.cuda.synchronize()
+        for (s, mass, table, _, budget, _), lens in zip(sets, new):
+            check(s, mass, table, lens, budget)
