@@ -153,6 +153,16 @@ def test_write_in_any_order_with_repeats_and_padding(n):
     assert status_bits(w.status) == 0
 
 
+@pytest.mark.parametrize("nb", [200, 1024, 1025, 1100, 2600])
+def test_prompts_scattered_over_small_and_large_caches(nb):
+    """Either side of where the last tokens go by slot or by page, in any order
+    with slots named twice, twice into the same pages."""
+    w = Writer(nb=nb, bs=16, seed=nb)
+    for _ in range(2):
+        w.write(w.rng.integers(-1, nb * 16, 2051), outliers=0.01)
+    assert status_bits(w.status) == 0
+
+
 @pytest.mark.parametrize("n", [40, 1500])
 def test_write_flags_slots_past_the_cache(n):
     w = Writer(nb=4, bs=16, seed=8)
