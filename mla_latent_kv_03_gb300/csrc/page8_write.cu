@@ -23,8 +23,8 @@
 // neighbours in the page.
 //
 // Bound: HBM, 1,152 bytes read and 640 written per token. 262,144 tokens of 64
-// sequences on one GB300: 79 us for 470 MB, 5.9 TB/s (0.87 of a copy's rate), 92 us
-// with the numbering before it (6.3 and 3.5 us and a memset); a step of 64 tokens
+// sequences on one GB300: 79 us for 470 MB, 5.9 TB/s (0.87 of a copy's rate), 87 us
+// with the listing before it (a kernel and a memset); a step of 64 tokens
 // takes 6.1 us alone with a cold L2, 4.0 us behind another kernel.
 #include <type_traits>
 
@@ -38,9 +38,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-// One launch takes 4.0 / 14.1 / 24.4 us for 64 / 1,024 / 2,048 tokens of a page
-// each, 5.5 / 7.4 / 10.4 us where 64 lie in a page; the numbered form 8.8 / 18.5
-// / 28.6 and 8.6 / 9.8 / 10.0 us. At 4,096: 50.6 and 21.3 against 49.3 and 10.1.
+// One launch takes 14.1 / 24.4 us for 1,024 / 2,048 tokens of a page each, 7.5 /
+// 10.4 us where 64 lie in a page; the listed form 18.0 / 27.4 and 9.7 / 9.8 us, and
+// 4 us more of the host's time. At 4,096: 50.7 and 21.3 against 48.5 and 10.3.
 constexpr int64_t kScanTokens = 2048;
 
 struct P8WriteArgs {
@@ -59,7 +59,7 @@ struct P8WriteArgs {
   uint32_t* status;
 };
 
-// The workspace of the numbered form.
+// The workspace of the listed form.
 struct P8WriteWs {
   size_t count, id_of, list, last, total;
 };
