@@ -1436,7 +1436,7 @@ template <int P>
 __global__ void __launch_bounds__(256) page8_mass_kernel(MassArgs a) {
   // (what the caller gave and the old mass are there, see page8_decode_kernel;
   // the scores and sums have to be waited for)
-  const int b = blockIdx.y, t = (blockIdx.x * 256 + threadIdx.x) / P, part = threadIdx.x % P;
+  const int b = blockIdx.y, t = blockIdx.x * (256 / P) + threadIdx.x / P, part = threadIdx.x % P;
   const int len = a.seq_lens[b], q0 = a.query_start_loc[b], q1 = a.query_start_loc[b + 1];
   const int ql = q1 - q0;
   const int64_t max_tokens = (int64_t)a.max_blocks * a.block_size;
