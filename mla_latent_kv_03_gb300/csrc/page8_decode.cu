@@ -19,9 +19,10 @@
 //     a bf16 exactly down to 2^-15 of the head's largest, and the rest within
 //     2^-23 of that largest;
 //   output  O[512, 3 NH] = codes[128, 512]^T . (p_1 | p_2 | p_3)
-//     p = p_1 + p_2 + 2^-5 p_3 in e5m2: 9 significant bits (error 2^-10), in
-//     steps of 2^-25 of the running reference at the least, so a long tail of
-//     small weights behind a large one is not lost.
+//     p = p_1 + p_2 + 2^-5 p_3 in e5m2, each term the nearest to what is left:
+//     the f16 nearest to p, 11 significant bits (error 2^-11), in steps of
+//     2^-25 of the running reference at the least, so a long tail of small
+//     weights behind a large one is not lost.
 // The page's scale enters a score as a factor of its token (a row), and the
 // output as part of the weight: the columns hold 2^(s_t - ref) S_p, and the
 // softmax sum adds the same number divided by S_p again. The running reference
@@ -981,16 +982,19 @@ __global__ void __launch_bounds__(Sm<NH>::threads, 1)
           const __half2 hh = __floats2half2_rn(p.x, p.y);
           hp[k] = *reinterpret_cast<const uint32_t*>(&hh);
         }
-        // as three e5m2 terms. e5m2 is the upper byte of f16: cut the first two
-        // off, round the rest, which is below 2^-5 of the weight, times 2^5
+        // as three e5m2 terms. e5m2 is the upper byte of f16: the first two are
+        // rounded to the nearest (half a step added, the lower byte dropped), so
+        // each leaves at most 2^-3 of what it was given, of either sign, and the
+        // third, times 2^5, holds all that is left of the f16
         uint32_t tm[3][HT / 4];
 #pragma unroll
         for (int k = 0; k < HT / 2; k += 2) {
           uint32_t a0 = hp[k], a1 = hp[k + 1];
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
-            tm[s][k / 2] = __byte_perm(a0, a1, 0x7531);
-            const uint32_t c0 = a0 & 0xff00ff00u, c1 = a1 & 0xff00ff00u;
+            // (0x7fff, the NaN, is 0 here and NaN in the last term)
+            const uint32_t c0 = (a0 + 0x00800080u) & 0xff00ff00u, c1 = (a1 + 0x00800080u) & 0xff00ff00u;
+            tm[s][k / 2] = __byte_perm(c0, c1, 0x7531);
             const __half2 r0 = __hsub2(*reinterpret_cast<const __half2*>(&a0), *reinterpret_cast<const __half2*>(&c0));
             const __half2 r1 = __hsub2(*reinterpret_cast<const __half2*>(&a1), *reinterpret_cast<const __half2*>(&c1));
             a0 = *reinterpret_cast<const uint32_t*>(&r0);
