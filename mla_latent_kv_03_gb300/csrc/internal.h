@@ -102,9 +102,10 @@ cudaError_t launch_absorb_tc(const CUtensorMap& q_map, const CUtensorMap& w_map,
                              void* q_abs, int64_t num_q, cudaStream_t stream);
 
 // Output projection on tcgen05 for bf16 and many rows; w_map views W_uv as
-// [H * 512 rows, 128 columns] with 64 x 64 boxes and the 128-byte swizzle.
+// [H * 512 rows, 128 columns] with 64 x 64 boxes and the 128-byte swizzle. The
+// latents are rounded to bf16, or (two_terms) held as two bf16 terms.
 cudaError_t launch_out_proj_tc(const CUtensorMap& w_map, const float* o_lat, void* out,
-                               int64_t num_q, int H, cudaStream_t stream);
+                               int64_t num_q, int H, bool two_terms, cudaStream_t stream);
 
 cudaError_t launch_combine_out_proj(const mla_config& cfg, const void* workspace, int32_t groups,
                                    int32_t num_ctas, int64_t num_q, int32_t batch, const void* W_uv,

@@ -658,7 +658,7 @@ mla_status mla_out_proj(const mla_config* cfg, const float* o_lat, const void* W
   if (cfg->dtype == MLA_BF16 && num_q >= kTcProjRows) {
     CUtensorMap w_map;
     if (!make_map_2d(&w_map, W_uv, kDv, (uint64_t)cfg->num_heads * kDc, 64, 64)) return MLA_ERR_CUDA;
-    return from_cuda(launch_out_proj_tc(w_map, o_lat, out, num_q, cfg->num_heads, as_stream(stream)));
+    return from_cuda(launch_out_proj_tc(w_map, o_lat, out, num_q, cfg->num_heads, false, as_stream(stream)));
   }
   return from_cuda(launch_out_proj(*cfg, o_lat, W_uv, out, num_q, as_stream(stream)));
 }

@@ -10,7 +10,8 @@ from _helpers import to_f64
 from mla_latent_kv_03_gb300 import libmla as L
 from mla_latent_kv_03_gb300 import workloads as W
 from mla_latent_kv_03_gb300.step import MlaDecodeStep
-from test_gpu_page8 import DEV
+from oracle import mla_oracle as O
+from test_gpu_page8 import CASES, DEV, _step, oracle_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +45,29 @@ def test_weights_are_held_to_eleven_bits(heads, rows):
     torch.cuda.synchronize()
     off = to_f64(s.out).mean(-1) / column.mean() - 1
     assert np.abs(off).max() <= 2.0 ** -11 + 2.0 ** -14, np.abs(off).max()
+
+
+@pytest.mark.parametrize("name", sorted(CASES))
+def test_the_output_is_rounded_once_in_every_form(name):
+    """A bf16 output rounded once is off by 2^-7 / m of itself at the most on a
+    mantissa m in [1, 2), half of it either way, uniformly: over mantissas with
+    uniform logarithms a mean square of 2^-14 / 12 * (3/8) / ln 2, its root
+    1.66e-3. Weights of 11 bits (2^-11, a root of 0.28e-3) make it 1.68e-3 at
+    the most, latents of two bf16 terms (2^-16) no more, and 2,048 outputs or more
+    settle the mean to a few percent. A second rounding to bf16 on the way would
+    make it 2.3e-3."""
+    w, s = _step(name)
+    s.page8_decode()
+    torch.cuda.synchronize()
+    rows, q, W_uv, got = oracle_rows(s), to_f64(s.q_abs), to_f64(s.W_uv), to_f64(s.out)
+    num = den = 0.0
+    for b in range(w.batch):
+        qr, n = w.q_range(b), int(w.seq_lens[b])
+        if qr.stop == qr.start:
+            continue
+        kv = O.gather_paged(rows, w.block_table[b], n, w.block_size)
+        o, _ = O.latent_attention(q[qr], kv, np.arange(n - (qr.stop - qr.start), n), w.softmax_scale)
+        want = O.out_proj(o, W_uv)
+        num += float(((got[qr] - want) ** 2).sum())
+        den += float((want ** 2).sum())
+    assert num <= (1.8e-3) ** 2 * den, (num / den) ** 0.5
