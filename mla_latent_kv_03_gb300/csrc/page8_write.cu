@@ -26,6 +26,7 @@
 // sequences on one GB300: 79 us for 470 MB, 5.9 TB/s (0.87 of a copy's rate), 87 us
 // with the listing before it (a kernel and a memset); a step of 64 tokens
 // takes 6.1 us alone with a cold L2, 4.0 us behind another kernel.
+#include <cmath>
 #include <type_traits>
 
 #include "async_copy.cuh"
@@ -92,21 +93,33 @@ struct PageSm {
   static constexpr int bytes = mx + kWarps * 4;
 };
 
-// cos and sin of pos * inv_freq (hi + lo). The angle as in rope_cos_sin, reduced
-// by multiples of pi / 2 to [-pi/4, pi/4] (Cody and Waite, pi / 2 in two
-// floats), then the Taylor series to r^9 and r^8 (remainders below 2e-9 and
-// 3e-8), a third of the instructions of sincosf.
-__device__ __forceinline__ void page_cos_sin(int pos, float hi, float lo, float* c, float* s) {
-  const float p = (float)pos, a = p * hi, tail = fmaf(p, lo, fmaf(p, hi, -a));
-  const float k = rintf(a * 0.636619772367581f);
-  float r = fmaf(-k, 1.57079637050628662f, a);   // pi / 2 rounded to a float
-  r = fmaf(-k, -4.37113900018624283e-08f, r);    // what that rounding took off
-  r += tail;
+// The frequencies in turns: inv_freq_i / (2 pi) modulo 1, in units of 2^-64. A
+// position times that, modulo 2^64, is the angle for every int32 position: whole
+// turns fall away in the integer product, and what the double's 53 bits leave out
+// is below 2^-24 turns at 2^31.
+struct PageFreq {
+  uint64_t turns[32];
+};
+PageFreq make_page_freq(double base) {
+  PageFreq f;
+  for (int i = 0; i < 32; ++i) {
+    const double t = std::pow(base, -2.0 * i / 64.0) * 0.15915494309189533577;  // 1 / (2 pi)
+    f.turns[i] = (uint64_t)std::ldexp(t - std::floor(t), 64);
+  }
+  return f;
+}
+
+// cos and sin of a position's angle: its upper 32 bits in turns, split into the
+// nearest quarter and a rest of [-pi/4, pi/4), then the Taylor series to r^9 and
+// r^8 (remainders below 2e-9 and 3e-8), a third of the instructions of sincosf.
+__device__ __forceinline__ void page_cos_sin(int pos, uint64_t turns, float* c, float* s) {
+  const uint32_t a = (uint32_t)(((uint64_t)(int64_t)pos * turns) >> 32);
+  const uint32_t q = (a + 0x20000000u) >> 30;
+  const float r = (float)(int32_t)(a - (q << 30)) * 1.46291807926716e-9f;  // 2 pi / 2^32
   const float z = r * r;
   const float sp = fmaf(z, fmaf(z, fmaf(z, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f);
   const float cp = fmaf(z, fmaf(z, fmaf(z, 1.f / 40320.f, -1.f / 720.f), 1.f / 24.f), -0.5f);
   const float sn = fmaf(r * z, sp, r), cs = fmaf(z, cp, 1.f);
-  const int q = (int)k;
   const float u = q & 1 ? cs : sn, v = q & 1 ? sn : cs;
   *s = q & 2 ? -u : u;
   *c = (q + 1) & 2 ? -v : v;
@@ -160,7 +173,7 @@ struct PageWriter {
   // to fetch meanwhile, complete at the barrier inside (after publish(), which
   // every thread calls before it), or NULL.
   template <typename F>
-  __device__ __forceinline__ void write(const RopeFreq& freq, int64_t page, const int* nextTok, F publish) {
+  __device__ __forceinline__ void write(const PageFreq& freq, int64_t page, const int* nextTok, F publish) {
     float* sMax = reinterpret_cast<float*>(sm + S::mx);
     const float old = a.scales[page];
     const uint4 w0 = __ldg(reinterpret_cast<const uint4*>(a.w + lane * 8));
@@ -222,7 +235,7 @@ struct PageWriter {
     const float inv = 1.0f / scale;
     const bool grew = old > 0.f && scale > old;
     const float f = grew ? old / scale : 1.f;
-    const float fhi = freq.hi[lane], flo = freq.lo[lane];
+    const uint64_t turns = freq.turns[lane];
     const int i1 = rope_i1(a.interleaved, lane), i2 = rope_i2(a.interleaved, lane);
     uint32_t next = 0;
     // (the page whose every row is written has no branches but the copies')
@@ -261,7 +274,7 @@ struct PageWriter {
         *reinterpret_cast<uint2*>(dst + lane * 8) = make_uint2(q[0], q[1]);
         *reinterpret_cast<uint2*>(dst + kDc / 2 + lane * 8) = make_uint2(q[2], q[3]);
         float cs, sn;
-        page_cos_sin(p, fhi, flo, &cs, &sn);
+        page_cos_sin(p, turns, &cs, &sn);
         __nv_bfloat16* kr = reinterpret_cast<__nv_bfloat16*>(dst + kDc);
         kr[i1] = __float2bfloat16_rn(x1 * cs - x2 * sn);
         kr[i2] = __float2bfloat16_rn(x2 * cs + x1 * sn);
@@ -279,7 +292,7 @@ struct PageWriter {
 
 template <int BS>
 __global__ void __launch_bounds__(kThreads, 3) p8_write_scan_kernel(P8WriteArgs a,
-                                                                    const __grid_constant__ RopeFreq freq) {
+                                                                    const __grid_constant__ PageFreq freq) {
   extern __shared__ __align__(16) uint8_t sm_page[];
   int* sTok = reinterpret_cast<int*>(sm_page + PageSm<BS>::tok);
   pdl_wait();
@@ -348,7 +361,7 @@ __global__ void __launch_bounds__(kThreads) p8_last_token_kernel(P8WriteArgs a, 
 
 template <int BS>
 __global__ void __launch_bounds__(kThreads, 3) p8_write_pages_kernel(P8WriteArgs a,
-                                                                     const __grid_constant__ RopeFreq freq,
+                                                                     const __grid_constant__ PageFreq freq,
                                                                      const int* count, const int* list,
                                                                      const int* last, int slot_last) {
   extern __shared__ __align__(16) uint8_t sm_page[];
@@ -388,7 +401,7 @@ int device_sms() {
 }
 
 template <int BS>
-cudaError_t write_pages(const P8WriteArgs& a, const RopeFreq& freq, uint8_t* ws, cudaStream_t st) {
+cudaError_t write_pages(const P8WriteArgs& a, const PageFreq& freq, uint8_t* ws, cudaStream_t st) {
   const int smem = PageSm<BS>::bytes;
   const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
   if (a.num_tokens <= kScanTokens) {
@@ -463,7 +476,7 @@ mla_status mla_page8_cache_write(const mla_config* cfg, const void* c_kv, const 
   P8WriteArgs a{(const __nv_bfloat16*)c_kv, (const __nv_bfloat16*)k_pe, positions, slot_mapping,
                 (int)num_tokens, (const __nv_bfloat16*)rms_weight, (uint8_t*)cache8, page_scales,
                 num_blocks, mass, cfg->rms_eps, cfg->rope_interleaved, dev_status};
-  const RopeFreq freq = make_rope_freq((double)cfg->rope_base);
+  const PageFreq freq = make_page_freq((double)cfg->rope_base);
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = cfg->block_size == 16   ? write_pages<16>(a, freq, ws, st)

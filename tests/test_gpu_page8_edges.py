@@ -6,12 +6,12 @@ import numpy as np
 import pytest
 import torch
 
-from _helpers import to_f64
+from _helpers import bf16_ulp, to_f64
 from mla_latent_kv_03_gb300 import libmla as L
 from mla_latent_kv_03_gb300 import workloads as W
 from mla_latent_kv_03_gb300.step import MlaDecodeStep
 from oracle import mla_oracle as O
-from test_gpu_page8 import CASES, DEV, _step, oracle_rows
+from test_gpu_page8 import CASES, DEV, _step, dev, oracle_rows, split_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -71,3 +71,34 @@ def test_the_output_is_rounded_once_in_every_form(name):
         num += float(((got[qr] - want) ** 2).sum())
         den += float((want ** 2).sum())
     assert num <= (1.8e-3) ** 2 * den, (num / den) ** 0.5
+
+
+# -------------------------------------------------------------- positions
+@pytest.mark.parametrize("n", [40, 2100])            # either form of the write
+@pytest.mark.parametrize("base", [10000.0, 1e6])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("around", [1 << 15, 1 << 17, 1 << 20, 1 << 22, 1 << 24, 1 << 26, 1 << 28, (1 << 31) - 2500])
+def test_keys_of_far_positions(around, interleaved, base, n):
+    """The angle is off by 2^-21 at 2^31 (53 bits of a frequency, here and in the
+    oracle), its sine and cosine by 2^-23 more, two products and their sum by
+    2^-24 each: in all below 2^-20 (|x1| + |x2|), and the bf16 rounding."""
+    rng = np.random.default_rng(around % 1000 + n)
+    nb = n // 16 + 1
+    cfg = L.make_config(16, 16, "bf16", rope_base=base, rope_interleaved=interleaved)
+    k = W.round_to_dtype(rng.standard_normal((n, 64)), "bf16")
+    pos = around + rng.integers(-2500, 2500, n)
+    cache = torch.zeros((nb, 16, 640), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(L.mla_page8_write_workspace_size(cfg, n, nb), dtype=torch.uint8, device=DEV)
+    L.mla_page8_cache_write(cfg, dev(rng.standard_normal((n, 512)), torch.bfloat16), dev(k, torch.bfloat16),
+                            dev(pos, torch.int32), dev(np.arange(n), torch.int64),
+                            dev(np.ones(512), torch.bfloat16), cache, torch.zeros(nb, device=DEV), ws)
+    torch.cuda.synchronize()
+    got = split_cache(cache)[1].reshape(-1, 64)[:n]
+    want = O.rope(k, pos, base, interleaved)
+    i = np.arange(32)
+    a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + 32)
+    size = np.abs(np.asarray(k, np.float64))
+    pair = np.zeros_like(size)
+    pair[:, a] = pair[:, b] = size[:, a] + size[:, b]
+    off = np.abs(got - want)
+    assert np.all(off <= bf16_ulp(want) + 2.0 ** -20 * pair), float(off.max())
