@@ -208,10 +208,14 @@ class MlaDecodeStep:
         with torch.cuda.stream(stream):  # memory of the stream that writes it
             keep = torch.empty((self.w.batch, budget), dtype=torch.int32, device=self.device)
             lens = torch.empty(self.w.batch, dtype=torch.int32, device=self.device)
-        L.mla_evict_select(self.cfg, self.p8_mass, self.p8_table, self.p8_lens, sinks, recent, keep,
-                           lens, dev_status=self.status, stream=stream)
-        L.mla_page8_compact(self.cfg, self.p8_cache, self.p8_scales, self.p8_mass, self.p8_table,
-                            keep, lens, dst_block_table, dev_status=self.status, stream=stream)
+            L.mla_evict_select(self.cfg, self.p8_mass, self.p8_table, self.p8_lens, sinks, recent,
+                               keep, lens, dev_status=self.status)
+            L.mla_page8_compact(self.cfg, self.p8_cache, self.p8_scales, self.p8_mass, self.p8_table,
+                                keep, lens, dst_block_table, dev_status=self.status)
+            # the calls above read the old table and lengths on this stream, and
+            # their memory may be another's: it is not free before they have
+            for t in (self.p8_table, self.p8_lens):
+                t.record_stream(torch.cuda.current_stream())
         self.p8_table, self.p8_lens = dst_block_table, lens
         return keep, lens
 

@@ -11,7 +11,7 @@ from mla_latent_kv_03_gb300 import libmla as L
 from mla_latent_kv_03_gb300 import workloads as W
 from mla_latent_kv_03_gb300.step import MlaDecodeStep
 from oracle import mla_oracle as O
-from test_gpu_page8 import CASES, DEV, _step, dev, oracle_rows, split_cache
+from test_gpu_page8 import CASES, DEV, _step, _together, dev, oracle_rows, split_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -102,3 +102,33 @@ def test_keys_of_far_positions(around, interleaved, base, n):
     pair[:, a] = pair[:, b] = size[:, a] + size[:, b]
     off = np.abs(got - want)
     assert np.all(off <= bf16_ulp(want) + 2.0 ** -20 * pair), float(off.max())
+
+
+# --------------------------------------------------------------- eviction
+def test_an_eviction_reads_lengths_and_table_of_another_streams_memory():
+    """The lengths and the table of one eviction are of its stream's memory. The
+    next one reads them on a stream that is late; what the first stream allocates
+    meanwhile must not take their place."""
+    def run(first, second):
+        w, s, dst, budget = _together()
+        s.page8_decode(0.9)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(first):
+            dst = dst.clone()
+        first.synchronize()
+        s.page8_evict(budget, 4, 20, dst, stream=first)
+        torch.cuda.synchronize()
+        del dst                                          # the step alone has them now
+        back = dev(w.block_table[:, :2], torch.int32)    # two of each sequence's old pages
+        if second is not first:
+            with torch.cuda.stream(second):
+                torch.cuda._sleep(100_000_000)
+        got = s.page8_evict(60, 4, 20, back, stream=second)
+        with torch.cuda.stream(first):
+            _ = [torch.ones((4, n), dtype=torch.int32, device=DEV) for n in (1, 5) * 8]
+        torch.cuda.synchronize()
+        return [*got, s.p8_cache[back.long()], s.p8_mass[back.long()]]
+
+    one = torch.cuda.Stream()
+    for want, got in zip(run(one, one), run(torch.cuda.Stream(), torch.cuda.Stream())):
+        assert torch.equal(want, got)
