@@ -165,6 +165,16 @@ class MlaDecodeStep:
         self.p8_mass = (torch.zeros((self.p8_blocks, w.block_size), dtype=torch.float32, device=dev)
                         if with_mass else None)
         self.p8_table, self.p8_lens = self.block_table, self.seq_lens
+        if not hasattr(self, "p8_q_positions"):
+            self.p8_q_positions = self.q_positions.clone()
+        self.q_positions.copy_(self.p8_q_positions)  # (evictions before this: they went on)
+        # each new token's sequence, its number among that one's new tokens, and their count
+        seq = w.token_seq[self.new_idx]
+        self.p8_new_seq = _dev(seq, torch.int64, dev)
+        self.p8_new_nth = _dev(w.kv_positions[self.new_idx] - (w.seq_lens - w.q_lens)[seq],
+                               torch.int32, dev)
+        self.p8_new_of = _dev(w.q_lens, torch.int32, dev)
+        self.p8_pos = None  # of the next new tokens, once the sequences have been cut
         need = L.mla_page8_decode_workspace_size(self.cfg, w.num_q, w.batch,
                                                  self.block_table.shape[1], with_mass)
         wneed = L.mla_page8_write_workspace_size(self.cfg, int(self.c_kv.shape[0]), self.p8_blocks)
@@ -175,14 +185,42 @@ class MlaDecodeStep:
         L.mla_workspace_init(self.p8_ws)
 
     def page8_populate(self) -> None:
+        if self.p8_pos is not None:
+            raise ValueError("page8_populate fills the pages that an eviction gave up: page8_setup starts over")
         L.mla_page8_cache_write(self.cfg, self.c_kv, self.k_pe, self.kv_positions, self.slot_mapping,
                                 self.rms_weight, self.p8_cache, self.p8_scales, self.p8_write_ws,
                                 mass=self.p8_mass, dev_status=self.status)
 
     def page8_write_new(self, stream=None) -> None:
-        L.mla_page8_cache_write(self.cfg, self.c_kv_new, self.k_pe_new, self.pos_new, self.slot_new,
-                                self.rms_weight, self.p8_cache, self.p8_scales, self.p8_write_ws,
-                                mass=self.p8_mass, dev_status=self.status, stream=stream)
+        """The step's new tokens. After an eviction each call is a step of its
+        own: they go behind the last tokens of the cut sequences, whose lengths
+        grow, and their positions and the queries' (for absorb) go on from where
+        the sequences were. A sequence without a page for one is flagged
+        MLA_DEV_BAD_SLOT."""
+        with torch.cuda.stream(self._page8_stream(stream)):
+            slots, pos = (self.slot_new, self.pos_new) if self.p8_pos is None else self._page8_next()
+            L.mla_page8_cache_write(self.cfg, self.c_kv_new, self.k_pe_new, pos, slots,
+                                    self.rms_weight, self.p8_cache, self.p8_scales, self.p8_write_ws,
+                                    mass=self.p8_mass, dev_status=self.status)
+
+    def _page8_stream(self, stream):
+        if stream is None or isinstance(stream, torch.cuda.Stream):
+            return stream
+        return torch.cuda.ExternalStream(int(stream), device=self.device)
+
+    def _page8_next(self):
+        """Slots and positions of the next new tokens behind the sequences of
+        p8_table and p8_lens, which grow by them."""
+        bs, most = self.w.block_size, self.p8_table.shape[1]
+        at = self.p8_lens[self.p8_new_seq] + self.p8_new_nth
+        page = self.p8_table[self.p8_new_seq, (at // bs).clamp(max=most - 1)].long()
+        there = (at < most * bs) & (page >= 0)
+        slots = torch.where(there, page * bs + at % bs, self.p8_blocks * bs)  # (past the cache)
+        self.p8_lens += self.p8_new_of
+        step = self.p8_new_of[self.p8_new_seq]
+        self.p8_pos += step
+        self.q_positions += step
+        return slots, self.p8_pos
 
     def page8_decode(self, decay: float = 1.0, stream=None) -> torch.Tensor:
         """The step's attention and output projection; with a mass, the
@@ -199,13 +237,19 @@ class MlaDecodeStep:
 
     def page8_evict(self, budget: int, sinks: int, recent: int, dst_block_table, stream=None):
         """Cut every sequence to `budget` tokens, moved into the pages of
-        dst_block_table, which becomes the sequences' table. Returns (keep,
-        new lengths)."""
+        dst_block_table, which becomes the sequences' table; columns beyond the
+        kept tokens are for what page8_write_new writes next. The old pages stay
+        as they were and are the caller's. Returns (keep, new lengths)."""
         if self.p8_mass is None:
             raise ValueError("page8_evict needs page8_setup(with_mass=True)")
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
-        with torch.cuda.stream(stream):  # memory of the stream that writes it
+        if dst_block_table.dim() != 2 or dst_block_table.shape[1] < 1:
+            raise ValueError("dst_block_table must have a column of pages at least")
+        need = L.mla_page8_decode_workspace_size(self.cfg, self.w.num_q, self.w.batch,
+                                                 dst_block_table.shape[1], True)
+        if not 0 < need <= self.p8_ws.numel():
+            raise ValueError(f"dst_block_table has more columns ({dst_block_table.shape[1]}) than the "
+                             "decode's workspace is for")
+        with torch.cuda.stream(self._page8_stream(stream)):  # memory of the stream that writes it
             keep = torch.empty((self.w.batch, budget), dtype=torch.int32, device=self.device)
             lens = torch.empty(self.w.batch, dtype=torch.int32, device=self.device)
             L.mla_evict_select(self.cfg, self.p8_mass, self.p8_table, self.p8_lens, sinks, recent,
@@ -216,7 +260,9 @@ class MlaDecodeStep:
             # their memory may be another's: it is not free before they have
             for t in (self.p8_table, self.p8_lens):
                 t.record_stream(torch.cuda.current_stream())
-        self.p8_table, self.p8_lens = dst_block_table, lens
+            self.p8_table, self.p8_lens = dst_block_table, lens.clone()  # (they grow)
+            if self.p8_pos is None:
+                self.p8_pos = self.pos_new.clone()
         return keep, lens
 
     # -- the projections either side (the whole attention layer) -----------

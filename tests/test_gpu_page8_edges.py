@@ -11,7 +11,9 @@ from mla_latent_kv_03_gb300 import libmla as L
 from mla_latent_kv_03_gb300 import workloads as W
 from mla_latent_kv_03_gb300.step import MlaDecodeStep
 from oracle import mla_oracle as O
-from test_gpu_page8 import CASES, DEV, _step, _together, dev, oracle_rows, split_cache
+from oracle import page8_oracle as P
+from test_gpu_page8 import (CASES, DEV, Writer, _step, _together, check_out, dev, oracle_rows, split_cache,
+                            status_bits)
 
 pytestmark = pytest.mark.gpu
 
@@ -132,3 +134,82 @@ def test_an_eviction_reads_lengths_and_table_of_another_streams_memory():
     one = torch.cuda.Stream()
     for want, got in zip(run(one, one), run(torch.cuda.Stream(), torch.cuda.Stream())):
         assert torch.equal(want, got)
+
+
+def test_steps_after_an_eviction_go_behind_the_kept_tokens():
+    """Three steps, of one, three and no new tokens a sequence, into pages that the
+    eviction filled in part and beyond them: larger values grow the moved scales."""
+    lens, qs, bs, budget = [400, 130, 64, 900], [1, 3, 0, 3], 16, 125
+    w = W.make("p8_after", lens, qs, 16, bs, "bf16", 33)
+    s = MlaDecodeStep(w, device=DEV)
+    columns = (budget + 9 + bs - 1) // bs + 1
+    s.page8_setup(with_mass=True, spare_blocks=4 * columns)
+    s.page8_populate()
+    s.absorb()
+    s.page8_decode(0.9)
+    table = np.arange(4 * columns).reshape(4, columns)[:, ::-1] + w.num_blocks
+    _, cut = s.page8_evict(budget, 4, 20, dev(table, torch.int32))
+    n = np.minimum(lens, budget)
+    writer = Writer.__new__(Writer)
+    writer.nb, writer.bs, writer.inter, writer.weight = s.p8_blocks, bs, False, w.rms_weight
+    writer.cache, writer.scales, writer.mass = s.p8_cache, s.p8_scales, s.p8_mass
+    seq = w.token_seq[w.is_new]
+    nth = np.concatenate([np.arange(q) for q in qs])
+    grown = 0
+    for step in range(3):
+        s.c_kv_new[:, 5] *= 50
+        x, k = to_f64(s.c_kv_new), to_f64(s.k_pe_new)
+        before = split_cache(s.p8_cache), to_f64(s.p8_scales), s.p8_mass.cpu().clone()
+        s.page8_write_new()
+        at = n[seq] + nth
+        n = n + qs
+        pos = w.kv_positions[w.is_new] + (step + 1) * np.asarray(qs)[seq]
+        torch.cuda.synchronize()
+        assert s.p8_lens.tolist() == n.tolist() and cut.tolist() == np.minimum(lens, budget).tolist()
+        assert s.q_positions.tolist() == pos.tolist()
+        writer.check(before, x, k, pos, table[seq, at // bs] * bs + at % bs, True)
+        old = before[1]
+        grown += int(((old > 0) & (to_f64(s.p8_scales) > old)).sum())
+        m0 = to_f64(s.p8_mass)
+        s.absorb()
+        s.page8_decode(0.9)
+        torch.cuda.synchronize()
+        rows = oracle_rows(s)
+        check_out(w, s, s.out, rows, table, n)
+        _, mass = P.decode(to_f64(s.q_abs), rows, table, n, w.query_start_loc, w.softmax_scale,
+                           to_f64(s.W_uv), m0, 0.9)
+        # (a score is off by 2^-18 of sum |q||k|, exp2 and the sums by 2^-20)
+        size = max(float(np.abs(O.gather_paged(rows, table[b], int(n[b]), bs)).max(0) @
+                         np.abs(to_f64(s.q_abs[w.q_range(b)])).max((0, 1))) for b in (0, 1, 3))
+        tol = 2.0 ** -18 * w.softmax_scale * size + 2.0 ** -20
+        assert np.all(np.abs(to_f64(s.p8_mass) - mass) <= tol * np.abs(mass))
+    assert grown > 0 and status_bits(s.status) == 0 and status_bits(s.p8_ws) == 0
+    with pytest.raises(ValueError, match="page8_setup"):
+        s.page8_populate()
+    s.page8_setup(with_mass=True)
+    s.page8_populate()
+    assert s.q_positions.tolist() == w.q_positions.tolist()
+
+
+def test_a_step_without_a_page_for_it_is_flagged():
+    w, s, dst, budget = _together()
+    s.page8_decode(0.9)
+    table = dst[:, :4].contiguous()                       # 128 tokens
+    table[1, 3] = -1                                      # 96, of which 96 are kept
+    keep, lens = s.page8_evict(96, 4, 20, table)
+    assert lens.tolist() == [96, 96, 64, 96]
+    cache = s.p8_cache.clone()
+    s.page8_write_new()
+    assert status_bits(s.status) == L.DEV_BAD_SLOT
+    assert torch.equal(s.p8_cache[w.block_table[1][w.block_table[1] >= 0]], cache[w.block_table[1][w.block_table[1] >= 0]])
+    changed = (s.p8_cache != cache).any(-1).any(-1).nonzero().view(-1).tolist()
+    assert changed == sorted(int(table[b, i]) for b, i in ((0, 3), (2, 2), (3, 3)))
+
+
+def test_eviction_refuses_tables_it_has_no_workspace_for():
+    w, s, dst, budget = _together()
+    with pytest.raises(ValueError, match="columns"):
+        s.page8_evict(budget, 4, 20, dst.repeat(1, 40))
+    with pytest.raises(ValueError, match="column"):
+        s.page8_evict(budget, 4, 20, dst[:, :0])
+    assert s.p8_table is s.block_table
