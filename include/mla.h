@@ -339,7 +339,8 @@ mla_status mla_page8_cache_write(const mla_config* cfg, const void* c_kv, const 
  *   sequences. Scales below 2^-64 read as 2^-64.
  *   workspace: mla_page8_decode_workspace_size(cfg, num_q, batch,
  *   max_blocks_per_seq, with_mass) bytes, 256-byte aligned, mla_workspace_init
- *   once; its first word is the device status. Calls that share it must not
+ *   once; its first word is the device status. A workspace for a program's most
+ *   rows, sequences and blocks does for any fewer. Calls that share it must not
  *   overlap.
  *
  * mla_page8_decode_mass -- the same, and each visible token's attention weight

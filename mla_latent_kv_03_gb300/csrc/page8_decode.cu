@@ -163,9 +163,11 @@ bool p8_sizes_fit(int64_t num_q, int32_t max_blocks, int bs) {
   const int64_t tokens = (int64_t)max_blocks * bs;
   return num_q <= 48 * 1024 && tokens <= (int64_t)1 << 30 && num_q * ((tokens + kTile - 1) / kTile) <= (int64_t)1 << 30;
 }
-P8Ws p8_ws(int64_t num_q, int H, bool pair, int shares, int64_t max_tokens, bool mass) {
+P8Ws p8_ws(int64_t num_q, int H, int shares, int64_t max_tokens, bool mass) {
   const WsLayout W = ws_layout(num_q, 1, shares);
-  const size_t rest = (size_t)((pair ? 2 : H / kHG) - 1) * W.slots * kHG;
+  // (16 heads: room for pairs whether they are used or not, which goes by the
+  // batch, so that a workspace for many sequences does for fewer)
+  const size_t rest = (size_t)((H == 16 ? 2 : H / kHG) - 1) * W.slots * kHG;
   P8Ws L;
   L.lse_rest = align_up(W.total, 256);
   L.o_rest = align_up(L.lse_rest + rest * 4, 256);
@@ -1501,7 +1503,7 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
   const int shares = p8_shares(H, C);
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const P8Ws L = p8_ws(num_q, H, pair, shares, (int64_t)max_blocks * bs, with_mass);
+  const P8Ws L = p8_ws(num_q, H, shares, (int64_t)max_blocks * bs, with_mass);
   if (ws_bytes < L.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
   const WsLayout W = ws_layout(num_q, 1, shares);
   // With num_blocks == 0 every block id is rejected before any copy; the maps
@@ -1632,9 +1634,7 @@ size_t mla_page8_decode_workspace_size(const mla_config* cfg, int64_t num_q, int
     return 0;
   const int C = split_ctas(cfg), H = cfg->num_heads;
   if (C <= 0) return 0;
-  return p8_ws(num_q, H, use_pairs(H, num_q, batch), p8_shares(H, C), (int64_t)max_blocks_per_seq * cfg->block_size,
-               with_mass != 0)
-      .total;
+  return p8_ws(num_q, H, p8_shares(H, C), (int64_t)max_blocks_per_seq * cfg->block_size, with_mass != 0).total;
 }
 
 mla_status mla_page8_decode(const mla_config* cfg, const void* q_abs, const void* cache8,

@@ -213,3 +213,24 @@ def test_eviction_refuses_tables_it_has_no_workspace_for():
     with pytest.raises(ValueError, match="column"):
         s.page8_evict(budget, 4, 20, dst[:, :0])
     assert s.p8_table is s.block_table
+
+
+# -------------------------------------------------------------- workspaces
+@pytest.mark.parametrize("heads", [16, 32])
+def test_one_workspace_for_the_most_rows_and_sequences(heads):
+    """Sized once, then used by batches that shrink: the same rows over fewer
+    sequences, fewer rows, narrower tables."""
+    cfg = L.make_config(heads, 16, "bf16")
+    ws = torch.empty(L.mla_page8_decode_workspace_size(cfg, 64, 64, 20), dtype=torch.uint8, device=DEV)
+    L.mla_workspace_init(ws)
+    for batch, rows in ((64, 1), (32, 2), (20, 3), (1, 64), (7, 1)):
+        w = W.make("p8_fewer", [200 + b for b in range(batch)], [rows] * batch, heads, 16, "bf16", batch)
+        s = MlaDecodeStep(w, device=DEV)
+        s.page8_setup()
+        s.p8_ws = ws
+        s.page8_populate()
+        s.absorb()
+        s.page8_decode()
+        torch.cuda.synchronize()
+        assert status_bits(ws) == 0
+        check_out(w, s, s.out, oracle_rows(s))

@@ -173,3 +173,31 @@ def test_binding_refuses_shapes_before_any_pointer_is_read():
         L.mla_evict_select(cfg, z(4, 64), z(2, 2), z(2), 0, 0, z(2, 5), z(3))
     with pytest.raises(ValueError, match="keep"):
         L.mla_page8_compact(cfg, z(4, 64, 640), z(4), None, z(2, 2), z(3, 5), z(2), z(2, 1))
+
+
+@pytest.mark.parametrize("heads", [16, 32, 128])
+@pytest.mark.parametrize("with_mass", [0, 1])
+def test_decode_workspaces_of_fewer_rows_sequences_and_blocks_are_no_larger(lib, heads, with_mass):
+    """A program sizes once for its most of each."""
+    c = _cfg(heads=heads)
+    size = lambda n, b, mb: lib.mla_page8_decode_workspace_size(ctypes.byref(c), n, b, mb, with_mass)  # noqa: E731
+    steps = [1, 2, 7, 16, 38, 39, 63, 64, 300, 2048]
+    for n in steps:
+        for b in steps:
+            for mb in (1, 64, 2048):
+                most = size(n, b, mb)
+                assert most > 0
+                assert all(size(n2, b, mb) <= most for n2 in steps if n2 <= n)
+                assert all(size(n, b2, mb) <= most for b2 in steps if b2 <= b)
+                assert mb == 1 or size(n, b, mb // 2) <= most
+
+
+@pytest.mark.parametrize("bs", [16, 64])
+def test_write_workspaces_of_fewer_tokens_are_no_larger(lib, bs):
+    c = _cfg(bs=bs)
+    size = lambda n, nb: lib.mla_page8_write_workspace_size(ctypes.byref(c), n, nb)  # noqa: E731
+    for nb in (1, 100, 4000, 50000):
+        last = 0
+        for n in sorted((0, 1, 2048, 2049, 3000, max(nb * bs // 8 - 1, 0), nb * bs // 8, nb, nb + 1, 1 << 20)):
+            assert size(n, nb) >= max(last, 256)
+            last = size(n, nb)
