@@ -287,11 +287,15 @@ __device__ __forceinline__ float warp_max(float x) {
   return r;
 }
 
-// The log-sum-exp of merged parts from their largest and 1 / the weight sum
-// (0 where the sum is not a positive number).
-__device__ __forceinline__ float merged_lse(float m, float inv) {
-  if (m == -INFINITY) return m;
-  return inv > 0.f ? m - log2f(inv) : __int_as_float(0x7fffffff);
+// The log-sum-exp of merged parts (kHG apart) from the largest that is not NaN and
+// 1 / the weight sum (0 where the sum is not a positive number). Where there is no
+// largest, the parts have no token, or one is NaN.
+__device__ __forceinline__ float merged_lse(float m, float inv, const float* lse, int parts) {
+  const float nan = __int_as_float(0x7fffffff);
+  if (m != -INFINITY) return inv > 0.f ? m - log2f(inv) : nan;
+  for (int s = 0; s < parts; ++s)
+    if (isnan(__ldcg(lse + s * kHG))) return nan;
+  return m;
 }
 
 // The two e4m3 terms of 16 scaled query values (eight bf16 pairs in u):
@@ -1139,7 +1143,9 @@ __global__ void __launch_bounds__(Sm<NH>::threads, 1)
             merge_qtile<256>(lse_part(a, t16), o_part(a, t16), (int64_t)c_first + seg.n, parts, 1,
                              a.o_lat + ((size_t)row * a.num_heads + hb) * kDc, ht, own,
                              [&] { named_bar_sync(kHeadsBar + c16, 256); });
-            if (ht < kHG) a.lse[(size_t)row * a.num_heads + hb + ht] = merged_lse(own[ht], own[kHG + ht]);
+            if (ht < kHG)
+              a.lse[(size_t)row * a.num_heads + hb + ht] =
+                  merged_lse(own[ht], own[kHG + ht], lse_part(a, t16) + ((int64_t)c_first + seg.n) * kHG + ht, parts);
           }
         }
       }
@@ -1178,7 +1184,8 @@ __device__ __forceinline__ HeadParts head_parts(const P8Args& a, const int4* row
   return r;
 }
 // 2^lse sums: the largest log-sum-exp m, and den = sum of 2^(lse - m), by a
-// group of G neighbouring lanes.
+// group of G neighbouring lanes. (fmaxf passes NaN over, the sum does not: den is
+// NaN where a part's is, and 0 only where no part has a token.)
 template <int G>
 __device__ __forceinline__ void merge_weights(const HeadParts& hp, int lane_in_group, float& m, float& den) {
   m = -INFINITY;
@@ -1186,8 +1193,8 @@ __device__ __forceinline__ void merge_weights(const HeadParts& hp, int lane_in_g
 #pragma unroll
   for (int o = G / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   den = 0.f;
-  if (m != -INFINITY)
-    for (int s = lane_in_group; s < hp.count; s += G) den += fast_exp2(hp.lse[s * kHG] - m);
+  const float base = m == -INFINITY ? 0.f : m;
+  for (int s = lane_in_group; s < hp.count; s += G) den += fast_exp2(hp.lse[s * kHG] - base);
 #pragma unroll
   for (int o = G / 2; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
 }

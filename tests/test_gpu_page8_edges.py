@@ -215,6 +215,31 @@ def test_eviction_refuses_tables_it_has_no_workspace_for():
     assert s.p8_table is s.block_table
 
 
+# ---------------------------------------------------- NaN and infinities
+@pytest.mark.parametrize("num_ctas", [0, 1, 7])
+@pytest.mark.parametrize("name", ["tails_bs64", "bs16_h32", "chunks", "speculative", "h128", "merged_pairs", "merged_h128"])
+def test_a_nan_key_makes_the_weights_of_its_sequence_nan(name, num_ctas):
+    """However its rows are cut into parts, and wherever the parts are merged; no
+    other sequence's weights change."""
+    w, s = _step(name, num_ctas, with_mass=True)
+    m0 = s.p8_mass.clone()
+    s.page8_decode(0.5)
+    clean = s.p8_mass.clone()
+    b = int(np.argmax(w.seq_lens))
+    s.p8_mass.copy_(m0)
+    s.p8_cache[int(w.block_table[b, 0]), 0, 30] = 0x7F
+    s.page8_decode(0.5)
+    torch.cuda.synchronize()
+    t = np.arange(int(w.seq_lens[b]))
+    at = torch.from_numpy(w.block_table[b][t // w.block_size].astype(np.int64) * w.block_size + t % w.block_size)
+    its = torch.zeros(clean.numel(), dtype=torch.bool)
+    its[at] = True
+    got = s.p8_mass.cpu().view(-1)
+    assert torch.isnan(got[its]).all()
+    assert torch.equal(got[~its], clean.cpu().view(-1)[~its])
+    assert torch.isnan(s.out[w.q_range(b)].float()).all()
+
+
 # -------------------------------------------------------------- workspaces
 @pytest.mark.parametrize("heads", [16, 32])
 def test_one_workspace_for_the_most_rows_and_sequences(heads):
