@@ -324,6 +324,18 @@ __device__ __forceinline__ void query_terms(const uint32_t* u, float f, uint4& t
   t2 = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
+// Is one of a token's codes NaN? (its row of the first slab; in any order)
+__device__ __forceinline__ bool nan_code(const uint8_t* row) {
+  uint32_t found = 0;
+#pragma unroll 1
+  for (int c = 0; c < 32; ++c) {
+    const uint4 x = *reinterpret_cast<const uint4*>(row + (c >> 3) * kSlab + (c & 7) * 16);
+    found |= __vcmpeq4(x.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(x.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
+             __vcmpeq4(x.z & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(x.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+  }
+  return found != 0;
+}
+
 // Untiled copy of `bytes` (a multiple of 16) to shared memory.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile(
@@ -907,11 +919,14 @@ __global__ void __launch_bounds__(Sm<NH>::threads, 1)
           if constexpr (R == 2) {
             // a token that only the second row sees, with a NaN code: all of
             // that row is NaN by its scores, and the codes must not reach the
-            // first row's columns (0 times NaN)
-            odd = c16 == 1 && live && nrows == 2 && tok == seen - 1;
+            // first row's columns (0 times NaN). NaN scores may also be some
+            // heads' query, so the codes decide. (The row's first heads zero them
+            // for all.)
+            odd = sg == kHG / HT && live && nrows == 2 && tok == seen - 1;
             if (odd) {
 #pragma unroll
               for (int k = 0; k < HT; ++k) odd &= isnan(d1[k]);
+              if (odd) odd = nan_code(sm + S::stage + slot * kStageB + r * 128);
             }
           }
 #pragma unroll

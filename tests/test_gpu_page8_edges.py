@@ -240,6 +240,25 @@ def test_a_nan_key_makes_the_weights_of_its_sequence_nan(name, num_ctas):
     assert torch.isnan(s.out[w.q_range(b)].float()).all()
 
 
+@pytest.mark.parametrize("heads", [range(8), range(8, 16), [0, 15], range(1, 16)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_query_that_is_not_finite_in_some_heads_leaves_the_others(heads, value):
+    """First and second rows of pairs, and single ones: the other heads, and the
+    rows beside them, keep every bit."""
+    w, s = _step("chunks")
+    s.page8_decode()
+    clean = s.out.clone()
+    bad = torch.zeros(w.num_q, 16, dtype=torch.bool)
+    for n in (0, 1, 7, 38, 39, 40, 42, 44, 173):
+        for h in heads:
+            s.q_abs[n, h, 17] = value
+            bad[n, h] = True
+    s.page8_decode()
+    torch.cuda.synchronize()
+    assert torch.isnan(s.out.cpu()[bad].float()).all()
+    assert torch.equal(s.out.cpu()[~bad], clean.cpu()[~bad])
+
+
 # -------------------------------------------------------------- workspaces
 @pytest.mark.parametrize("heads", [16, 32])
 def test_one_workspace_for_the_most_rows_and_sequences(heads):
