@@ -304,7 +304,8 @@ mla_status mla_decode_paged_combine_fp8(const mla_config* cfg, const void* q_abs
  * stale scale costs precision only, never correctness). bf16 only.
  *
  * mla_page8_cache_write -- mla_cache_write into such pages. With amax_p the
- * largest |c_hat| of the call's tokens in page p,
+ * largest |c_hat| of the tokens that the call writes in page p (a token whose
+ * slot a later one takes is not written and does not count),
  *   page_scales[p] = max(page_scales[p], 2^e),
  *   e = the least integer in [-64, 64] with amax_p <= 448 * 2^e;
  * rows already in a page whose scale grows keep their values in the new scale

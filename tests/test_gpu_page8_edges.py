@@ -106,6 +106,29 @@ def test_keys_of_far_positions(around, interleaved, base, n):
     assert np.all(off <= bf16_ulp(want) + 2.0 ** -20 * pair), float(off.max())
 
 
+# ----------------------------------------------------------- page scales
+@pytest.mark.parametrize("nb", [200, 2000])          # last tokens by slot and by page
+@pytest.mark.parametrize("n", [100, 2100])           # either form of the write
+def test_a_token_whose_slot_is_taken_again_leaves_the_scale_alone(n, nb):
+    w = Writer(nb=nb, bs=16, seed=n + nb)
+    x, k = w.tokens(n)
+    slots = np.arange(n) + 3
+    x[:n - 1:7, 11] = 3000.0                             # outliers in every page,
+    late = np.arange(0, n - 1, 7)                        # each followed by another token for its slot
+    x = np.concatenate([x, x[late + 1]])
+    k = np.concatenate([k, k[late + 1]])
+    slots = np.concatenate([slots, slots[late]])
+    pos = np.arange(len(slots)).astype(np.int32)
+    before = split_cache(w.cache), to_f64(w.scales), w.mass.cpu().clone()
+    ws = torch.empty(L.mla_page8_write_workspace_size(w.cfg, len(slots), nb), dtype=torch.uint8, device=DEV)
+    L.mla_page8_cache_write(w.cfg, dev(x, torch.bfloat16), dev(k, torch.bfloat16), dev(pos, torch.int32),
+                            dev(slots, torch.int64), dev(w.weight, torch.bfloat16), w.cache, w.scales, ws,
+                            mass=w.mass, dev_status=w.status)
+    torch.cuda.synchronize()
+    w.check(before, x, k, pos, slots, True)
+    assert to_f64(w.scales).max() <= 2.0 ** -5           # (c_hat of an outlier: 22, a scale of 2^-4)
+
+
 # --------------------------------------------------------------- eviction
 def test_an_eviction_reads_lengths_and_table_of_another_streams_memory():
     """The lengths and the table of one eviction are of its stream's memory. The
