@@ -501,8 +501,8 @@ mla_status mla_page8_compact(const mla_config* cfg, void* cache8, float* page_sc
       max_blocks_per_seq > ((int64_t)1 << 30) / cfg->block_size ||
       dst_max_blocks > ((int64_t)1 << 30) / cfg->block_size || batch > 65535)
     return MLA_ERR_UNSUPPORTED;
-  if (batch == 0 || dst_max_blocks == 0) return MLA_OK;
-  if (!cache8 || !page_scales || !block_table || !keep || !new_lens || !dst_block_table)
+  if (batch == 0) return MLA_OK;
+  if (!cache8 || !page_scales || !block_table || !keep || !new_lens || (!dst_block_table && dst_max_blocks > 0))
     return MLA_ERR_INVALID_ARGUMENT;
   if (!p8_aligned(cache8, 16) || !p8_aligned(page_scales, 4) || !p8_aligned(mass, 4) ||
       !p8_aligned(block_table, 4) || !p8_aligned(keep, 4) || !p8_aligned(new_lens, 4) ||
@@ -512,7 +512,8 @@ mla_status mla_page8_compact(const mla_config* cfg, void* cache8, float* page_sc
                       max_blocks_per_seq, keep, new_lens, budget, dst_block_table, dst_max_blocks,
                       dev_status};
   const int bs = cfg->block_size;
-  const dim3 grid((unsigned)dst_max_blocks, (unsigned)batch);
+  // (without destination pages, to flag the sequences that have tokens)
+  const dim3 grid((unsigned)(dst_max_blocks > 0 ? dst_max_blocks : 1), (unsigned)batch);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e =
       bs == 16   ? launch_pdl(page8_compact_kernel<16>, grid, dim3(kCmpThreads), 0, st, a)

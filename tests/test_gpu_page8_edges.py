@@ -238,6 +238,20 @@ def test_eviction_refuses_tables_it_has_no_workspace_for():
     assert s.p8_table is s.block_table
 
 
+def test_compaction_without_destination_pages_is_flagged():
+    cfg = L.make_config(16, 16, "bf16")
+    cache = torch.full((3, 16, 640), 5, dtype=torch.uint8, device=DEV)
+    scales = torch.ones(3, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    table, none = dev([[0], [1]], torch.int32), torch.empty((2, 0), dtype=torch.int32, device=DEV)
+    keep = dev([[3, 4], [1, -1]], torch.int32)
+    for lens, want in (([0, 0], 0), ([0, 1], L.DEV_BAD_SEQ)):
+        L.mla_page8_compact(cfg, cache, scales, None, table, keep, dev(lens, torch.int32), none, dev_status=status)
+        torch.cuda.synchronize()
+        assert status_bits(status) == want
+    assert torch.all(cache == 5) and torch.all(scales == 1)
+
+
 # ---------------------------------------------------- NaN and infinities
 @pytest.mark.parametrize("num_ctas", [0, 1, 7])
 @pytest.mark.parametrize("name", ["tails_bs64", "bs16_h32", "chunks", "speculative", "h128", "merged_pairs", "merged_h128"])

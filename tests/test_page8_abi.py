@@ -201,3 +201,8 @@ def test_write_workspaces_of_fewer_tokens_are_no_larger(lib, bs):
         for n in sorted((0, 1, 2048, 2049, 3000, max(nb * bs // 8 - 1, 0), nb * bs // 8, nb, nb + 1, 1 << 20)):
             assert size(n, nb) >= max(last, 256)
             last = size(n, nb)
+
+
+def test_compact_refuses_a_missing_table_unless_it_has_no_columns(lib):
+    assert _compact(lib, _cfg(), dst=NONE, dmb=1) == 1
+    assert _compact(lib, _cfg(), dst=NONE, dmb=0, keep=NONE) == 1
