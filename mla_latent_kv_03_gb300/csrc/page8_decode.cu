@@ -1571,9 +1571,9 @@ mla_status p8_decode(const mla_config* cfg, const void* q_abs, const void* cache
   // are so few outputs, each cut into more than a few parts (one per 64 tokens at
   // the most), that the merge has to spread over the device first. Measured on
   // one GB300, us:
-  //   rows x heads       320 x 16  448 x 16  56 x 128  256 x 32  256 x 128
-  //   in the projection    66.7      82.7      59.4      77.2      223.4
-  //   in the decode        68.1      83.0      56.4      74.5      181.1
+  //   rows x heads       320 x 16  448 x 16  56 x 128  256 x 32  256 x 128  (1,024 tokens)
+  //   in the projection    72.3      93.3      61.1      75.1      223.5
+  //   in the decode        73.8      88.4      54.7      73.1      178.1
   //   rows x heads (65,536 tokens)  1 x 16  8 x 16  16 x 16  32 x 16  1 x 128  4 x 128
   //   in the projection              61.1    27.4    24.9     23.2      52.5     45.7
   //   spread                         26.6    23.6    25.2     28.5      46.8     51.2
