@@ -58,8 +58,8 @@
 //    the main loop, at 6.2 TB/s (0.92 of a copy's rate); the rest is the start
 //    (split, block table, first pages: 5 us), the last products, the partials
 //    and a tail of shares that end apart.
-//  - 32 sequences of up to 32,768 tokens, 128 heads: 275 us; 4 chunks of 512 rows
-//    on 2,560 tokens, 16 heads: 293 us. Neither bytes (0.18 and 0.04 of HBM) nor
+//  - 32 sequences of up to 32,768 tokens, 128 heads: 274 us; 4 chunks of 512 rows
+//    on 2,560 tokens, 16 heads: 292 us. Neither bytes (0.18 and 0.04 of HBM) nor
 //    products (tensor pipe busy 0.30 and 0.27) bound these, but the time of one
 //    stage from copy to release: copy 1,700 cycles, scores 1,500, softmax 1,900,
 //    output products 1,600, over two stages 3,400 cycles a tile of which the

@@ -23,9 +23,9 @@
 // neighbours in the page.
 //
 // Bound: HBM, 1,152 bytes read and 640 written per token. 262,144 tokens of 64
-// sequences on one GB300: 79 us for 470 MB, 5.9 TB/s (0.87 of a copy's rate), 87 us
+// sequences on one GB300: 74 us for 470 MB, 6.4 TB/s (0.94 of a copy's rate), 85 us
 // with the listing before it (a kernel and a memset); a step of 64 tokens
-// takes 6.1 us alone with a cold L2, 4.0 us behind another kernel.
+// takes 6.1 us alone with a cold L2, 3.7 us behind another kernel.
 #include <cmath>
 #include <type_traits>
 
@@ -39,9 +39,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-// One launch takes 14.1 / 24.4 us for 1,024 / 2,048 tokens of a page each, 7.5 /
-// 10.4 us where 64 lie in a page; the listed form 18.0 / 27.4 and 9.7 / 9.8 us, and
-// 4 us more of the host's time. At 4,096: 50.7 and 21.3 against 48.5 and 10.3.
+// One launch takes 11.7 / 21.1 us for 1,024 / 2,048 tokens of a page each, 7.1 /
+// 9.9 us where 64 lie in a page; the listed form 17.0 / 25.2 and 10.4 / 10.4 us, and
+// 5 us more of the host's time. At 4,096: 45.6 and 21.1 against 43.7 and 10.6.
 constexpr int64_t kScanTokens = 2048;
 
 struct P8WriteArgs {
@@ -67,12 +67,12 @@ struct P8WriteWs {
 // Last tokens by slot of the cache, not by number of the page: one kernel less,
 // and the workspace is the same where the cache has fewer pages than the call has
 // tokens, as here (num_blocks <= tokens / 2). Where the cache is larger its entries
-// lie far apart. By slot / by page, us: 64 x 4,096 tokens in one slot a token 87.4 /
-// 92.2; 2,051 in 8 slots a token 7.0 / 8.5; 8,192 in 64 10.8 / 11.7; 65,536 in 20
-// 32.9 / 30.6, in 64 35.1 / 33.1.
+// lie far apart. By slot / by page, us: 64 x 4,096 tokens in one slot a token 85.1 /
+// 86.8; 2,051 in 8 slots a token 6.8 / 8.6; 8,192 in 64 10.7 / 11.6; 65,536 in 20
+// 32.9 / 30.6, in 64 35.2 / 33.2.
 bool by_slot(int64_t tokens, int64_t num_blocks, int bs) { return num_blocks * bs <= 8 * tokens; }
 P8WriteWs write_ws(int64_t tokens, int64_t num_blocks, int bs) {
-  const int64_t pages = tokens < num_blocks ? tokens : num_blocks;
+  const int64_t pages = tokens < num_blocks && !by_slot(tokens, num_blocks, bs) ? tokens : num_blocks;
   P8WriteWs L;
   L.count = 0;
   L.id_of = 256;
