@@ -136,6 +136,7 @@ def test_an_eviction_reads_lengths_and_table_of_another_streams_memory():
     meanwhile must not take their place."""
     def run(first, second):
         w, s, dst, budget = _together()
+        s.absorb()
         s.page8_decode(0.9)
         torch.cuda.synchronize()
         with torch.cuda.stream(first):
@@ -167,6 +168,7 @@ def test_steps_after_an_eviction_go_behind_the_kept_tokens():
     s = MlaDecodeStep(w, device=DEV)
     columns = (budget + 9 + bs - 1) // bs + 1
     s.page8_setup(with_mass=True, spare_blocks=4 * columns)
+    s.p8_cache.fill_(0x33)
     s.page8_populate()
     s.absorb()
     s.page8_decode(0.9)
@@ -214,8 +216,57 @@ def test_steps_after_an_eviction_go_behind_the_kept_tokens():
     assert s.q_positions.tolist() == w.q_positions.tolist()
 
 
+def test_steps_after_an_eviction_captured_and_by_a_streams_handle():
+    """The eviction and two steps: on the current stream, on a stream given by its
+    handle, and captured and replayed twice from the same state."""
+    def start():
+        w, s, dst, budget = _together()
+        s.p8_cache.zero_()                               # (compared whole)
+        s.p8_scales.zero_()
+        s.page8_populate()
+        s.absorb()
+        s.page8_decode(0.9)
+        torch.cuda.synchronize()
+        return s, dst
+
+    def calls(s, dst, stream=None):
+        s.page8_evict(140, 4, 20, dst, stream=stream)
+        for _ in range(2):
+            s.page8_write_new(stream=stream)
+            s.absorb(stream=stream)
+            s.page8_decode(0.9, stream=stream)
+
+    def state(s):
+        torch.cuda.synchronize()
+        return [t.clone() for t in (s.out, s.p8_cache, s.p8_scales, s.p8_mass, s.p8_lens, s.q_positions)]
+
+    s, dst = start()
+    calls(s, dst)
+    want = state(s)
+    assert s.p8_lens.tolist() == [142, 132, 66, 142]
+    s, dst = start()
+    side = torch.cuda.Stream()
+    calls(s, dst, side.cuda_stream)
+    assert all(torch.equal(a, b) for a, b in zip(state(s), want))
+    s, dst = start()
+    keep = [s.p8_cache, s.p8_scales, s.p8_mass, s.q_positions]
+    first = [t.clone() for t in keep]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls(s, dst)
+    for _ in range(2):
+        for t, v in zip(keep, first):
+            t.copy_(v)
+        s.out.fill_(float("nan"))
+        g.replay()
+        assert all(torch.equal(a, b) for a, b in zip(state(s), want))
+    assert status_bits(s.status) == 0 and status_bits(s.p8_ws) == 0
+
+
 def test_a_step_without_a_page_for_it_is_flagged():
     w, s, dst, budget = _together()
+    s.p8_cache[w.num_blocks:] = 0x33                      # the free pages
+    s.absorb()
     s.page8_decode(0.9)
     table = dst[:, :4].contiguous()                       # 128 tokens
     table[1, 3] = -1                                      # 96, of which 96 are kept
