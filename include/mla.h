@@ -58,7 +58,9 @@ typedef enum {
   MLA_ERR_BAD_BLOCK = 6,           /* device: block-table entry out of range   */
   MLA_ERR_BAD_SEQ = 7,             /* device: q_len > seq_len, or seq_len
                                       beyond max_blocks_per_seq * block_size   */
-  MLA_ERR_BAD_SLOT = 8             /* device: slot_mapping entry out of range  */
+  MLA_ERR_BAD_SLOT = 8,            /* device: slot_mapping entry out of range  */
+  MLA_ERR_BAD_TOKEN = 9            /* device: token id out of range, or a
+                                      distribution without weight              */
 } mla_status;
 
 /* Bits of the device status word (a uint32_t in device memory). */
@@ -66,6 +68,7 @@ typedef enum {
 #define MLA_DEV_BAD_BLOCK (1u << 1)
 #define MLA_DEV_BAD_SEQ   (1u << 2)
 #define MLA_DEV_BAD_SLOT  (1u << 3)
+#define MLA_DEV_BAD_TOKEN (1u << 4)
 
 typedef enum { MLA_F32 = 0, MLA_BF16 = 1 } mla_dtype;
 
@@ -413,6 +416,131 @@ mla_status mla_page8_compact(const mla_config* cfg, void* cache8, float* page_sc
                              uint32_t* dev_status, void* stream);
 
 /*
+ * A speculative step over a tree of drafted tokens. The pages have none; these
+ * four calls let a program that drafts several continuations of a sequence run
+ * all of them through one step, decide which the target model accepts, and go
+ * on from there. The q_len rows of a sequence are its tree, at most 1,024, in
+ * an order in which a parent comes before its children; row 0 is the last token
+ * that was accepted before (its latent is written by this step), the others are
+ * drafted. parents [num_q] int32 holds the parent's row within the sequence, or
+ * -1 for a root. seq_lens counts the tree's rows, as everywhere; past =
+ * seq_lens[b] - q_len, and row j's latent has the cache place past + j. A step:
+ *   mla_tree_plan -> mla_cache_write (its slots and positions) -> mla_absorb_q
+ *   (its positions) -> mla_tree_decode, per layer; the target's probabilities
+ *   -> mla_tree_verify -> mla_tree_commit (all layers).
+ * Where the trees are the same in every step, their masks can be kept.
+ *
+ * mla_tree_plan -- what the other calls need to know about the trees:
+ *   tree_mask [num_q, mask_words] uint64 (output): bit j of a row's words is set
+ *     for j the row itself and each of its ancestors;
+ *   positions [num_q] int32 (output): past + the row's depth (a root's is 0), the
+ *     position for RoPE;
+ *   slots [num_q] int64 (output): the cache slot of place past + j, for
+ *     mla_cache_write.
+ * 1 <= mask_words <= 16; a sequence of more than 64 * mask_words rows, with a
+ * parent that does not come before its child, longer than its block table or
+ * with more rows than tokens sets MLA_DEV_BAD_SEQ, and its rows get an empty
+ * mask, position 0 and slot -1 (which the cache write skips). A page out of
+ * range sets MLA_DEV_BAD_BLOCK (slot -1). Rows that no sequence has are left as
+ * they were. dev_status may be NULL.
+ */
+mla_status mla_tree_plan(const mla_config* cfg, const int32_t* parents, const int32_t* seq_lens,
+                         const int32_t* query_start_loc, const int32_t* block_table,
+                         int32_t max_blocks_per_seq, int64_t num_blocks, int32_t batch,
+                         int64_t num_q, int32_t mask_words, uint64_t* tree_mask,
+                         int32_t* positions, int64_t* slots, uint32_t* dev_status, void* stream);
+
+/*
+ * mla_tree_decode -- mla_decode_paged, mla_combine and mla_out_proj for rows
+ * that see the whole past and, of the step's own rows, those in their mask:
+ *   out[n,h] = (sum_t softmax(s)_t row_t[0:512]) W_uv[h],
+ *   s_t = softmax_scale * (q_abs[n,h] . row_t) for t < past, and for t = past + j
+ *   with bit j of tree_mask[n] set (j < q_len; later bits are ignored; a row's
+ *   own bit is not implied, and masks need not come from a tree).
+ *   q_abs [num_q, H, 576], cache [num_blocks, block_size, 576], W_uv [H, 512, 128],
+ *   out [num_q, H, 128] bf16 (bf16 only); zeros for a row that sees no token or
+ *   that no sequence has. A token that a row does not see has no part in it,
+ *   whatever its latent holds (NaN, infinities); among the tokens that it does
+ *   see, one that is not finite makes it NaN.
+ * Limits: those of mla_page8_decode, with num_q times a block table's tokens at
+ * most 2^35; a sequence of more than 64 * mask_words rows sets MLA_DEV_BAD_SEQ
+ * and gets zeros, as do all when query_start_loc does not ascend.
+ *   workspace: mla_tree_decode_workspace_size() bytes, 256-byte aligned,
+ *   mla_workspace_init once; its first word is the device status. A workspace
+ *   for a program's most rows and sequences does for any fewer. Calls that share
+ *   it must not overlap. W_uv may be read before the kernel launched just before
+ *   the call has finished.
+ */
+size_t mla_tree_decode_workspace_size(const mla_config* cfg, int64_t num_q, int32_t batch);
+mla_status mla_tree_decode(const mla_config* cfg, const void* q_abs, const void* cache,
+                           int64_t num_blocks, const int32_t* block_table,
+                           int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                           const int32_t* query_start_loc, int32_t batch, int64_t num_q,
+                           const uint64_t* tree_mask, int32_t mask_words, const void* W_uv,
+                           void* workspace, size_t ws_bytes, void* out, void* stream);
+
+/*
+ * mla_tree_verify -- which drafted tokens the target accepts, so that what is
+ * kept is distributed as the target's own samples would be.
+ *   target_probs [num_q, vocab_size] float32: row n is the target's distribution
+ *     behind row n's token; draft_probs, the same for the draft, or NULL;
+ *   tokens, parents [num_q] int32 (row 0's token is not looked at, and its parent
+ *     taken as -1); uniforms [num_q], final_uniforms [batch] float32 in [0, 1).
+ * The walk starts at row 0. At row c the children are asked in order. With w_0 =
+ * target_probs[c] (clamped to [0, 1], NaN 0) and Z_0 = 1, the next child, of row
+ * i and token x, is accepted if
+ *   uniforms[i] * draft_probs[c][x] * Z_r < w_r[x]      (in 64 bits),
+ * and the walk goes on from it; else
+ *   w_{r+1} = max(w_r - Z_r draft_probs[c], 0),  Z_{r+1} = sum of w_{r+1},
+ * which takes drafted tokens to be drawn from draft_probs[c], each on its own.
+ * Without draft_probs they are taken as given, not drawn, and different from one
+ * another: a child is accepted if uniforms[i] * Z_r < w_r[x]; else w_{r+1}[x] = 0 and
+ * Z_{r+1} = Z_r - w_r[x]. When no child is left, or max_path rows are kept, the
+ * next token is drawn from what is left of the last row's distribution: the first
+ * token at which the running sum of floor(2^40 w) passes final_uniforms[b] * its
+ * total. (The sums are of whole numbers: they depend on no order. w is float32, Z
+ * the sum times 2^-40 rounded to float32.) Where nothing is left it is drawn from
+ * target_probs[c] itself.
+ *   path [batch, max_path] int32 (output): the rows kept, row 0 first, -1 behind;
+ *   path_lens [batch] int32 (output): their number; next_tokens [batch] int32
+ *   (output). A sequence without rows: 0 rows, next token -1.
+ * vocab_size <= 2^20. A token out of range is never accepted (MLA_DEV_BAD_TOKEN),
+ * a row whose parent does not come before it never reached (MLA_DEV_BAD_SEQ); a
+ * row with no weight at all gives next token -1 (MLA_DEV_BAD_TOKEN); sequences
+ * with bad query_start_loc entries or more than 1,024 rows are as those without
+ * rows (MLA_DEV_BAD_SEQ). target_probs and draft_probs are 16-byte aligned.
+ * dev_status may be NULL. No workspace.
+ */
+mla_status mla_tree_verify(const float* target_probs, const float* draft_probs, int32_t vocab_size,
+                           const int32_t* tokens, const int32_t* parents,
+                           const int32_t* query_start_loc, int32_t batch, int64_t num_q,
+                           const float* uniforms, const float* final_uniforms, int32_t* path,
+                           int32_t* path_lens, int32_t max_path, int32_t* next_tokens,
+                           uint32_t* dev_status, void* stream);
+
+/*
+ * mla_tree_commit -- the kept rows' latents moved behind the past: place past +
+ * path[b][i] goes to place past + i for i < path_lens[b], in each of num_layers
+ * caches that lie one after another ([num_layers, num_blocks, block_size] rows of
+ * row_bytes: 1,152 for bf16, 2,304 for fp32, or 640 for the FP8 rows of
+ * mla_cache_write_fp8; page-scaled rows do not move between pages this way).
+ * new_lens [batch] int32 (output, not seq_lens itself) = past + path_lens[b]. Keys
+ * keep their rotation: a kept row's position is past + its depth = past + i. Bytes
+ * of places behind the kept rows are left as they were. seq_lens, query_start_loc
+ * and block_table are those of the step. A path that does not ascend or leaves the
+ * sequence's rows sets MLA_DEV_BAD_SLOT: nothing of it moves and new_lens is past.
+ * A sequence longer than its block table or with more rows than tokens sets
+ * MLA_DEV_BAD_SEQ (new_lens 0). Pages out of range set MLA_DEV_BAD_BLOCK and
+ * that row stays. A page belongs to one sequence. dev_status may be NULL.
+ */
+mla_status mla_tree_commit(const mla_config* cfg, void* cache, int32_t num_layers,
+                           int64_t num_blocks, int32_t row_bytes, const int32_t* block_table,
+                           int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                           const int32_t* query_start_loc, int32_t batch, const int32_t* path,
+                           const int32_t* path_lens, int32_t max_path, int32_t* new_lens,
+                           uint32_t* dev_status, void* stream);
+
+/*
  * mla_combine -- merge the split partials of mla_decode_paged.
  * For each (n, h): M = max_s lse_s, o_lat = sum_s 2^(lse_s - M) o_s /
  * sum_s 2^(lse_s - M) (the split-softmax identity; lse is kept in base 2
@@ -619,7 +747,8 @@ mla_status mla_o_proj(const mla_config* cfg, const void* attn_out, const void* W
  * mla_get_device_status -- synchronise `stream`, read the device status word
  * at `status_word` (a workspace's first word, or the dev_status buffer given
  * to mla_cache_write), optionally clear it, and map it to a status: the
- * lowest set bit wins (TIMEOUT, BAD_BLOCK, BAD_SEQ, BAD_SLOT); MLA_OK if none.
+ * lowest set bit wins (TIMEOUT, BAD_BLOCK, BAD_SEQ, BAD_SLOT, BAD_TOKEN); MLA_OK
+ * if none.
  * `mask_out` (host pointer, may be NULL) receives the raw bits.
  */
 mla_status mla_get_device_status(const void* status_word, uint32_t* mask_out, int clear,

@@ -134,6 +134,10 @@ bool encode_fp8_maps(CUtensorMap* codes, CUtensorMap* rope, const void* base, ui
                      uint32_t box_rows);
 bool encode_map_2d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
                    uint32_t box_cols, uint32_t box_rows);
+// 3-D view of 576-value rows as (64 columns, row, column block): one box holds
+// `nslab` column blocks of box_rows rows, slab by slab (make_slab_map in libmla.cu).
+bool encode_slab_map(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows,
+                     uint32_t nslab);
 // 3-D map over (d, head, row) of a [rows, heads, dims] bf16 tensor: box =
 // (box_d, 1, box_rows), 128-byte swizzle.
 bool encode_map_heads(CUtensorMap* map, const void* base, uint64_t dims, uint64_t heads,

@@ -249,6 +249,10 @@ bool encode_map_2d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t r
                    uint32_t box_cols, uint32_t box_rows) {
   return make_map_2d(map, base, cols, rows, box_cols, box_rows);
 }
+bool encode_slab_map(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows,
+                     uint32_t nslab) {
+  return make_slab_map(map, base, rows, box_rows, nslab);
+}
 bool encode_map_heads(CUtensorMap* map, const void* base, uint64_t dims, uint64_t heads,
                       uint64_t rows, uint32_t box_d, uint32_t box_rows) {
   return make_map_heads(map, base, dims, heads, rows, box_d, box_rows);
@@ -274,6 +278,7 @@ const char* mla_status_string(mla_status s) {
     case MLA_ERR_BAD_BLOCK: return "block table entry out of range";
     case MLA_ERR_BAD_SEQ: return "query longer than its sequence, or sequence longer than its block table";
     case MLA_ERR_BAD_SLOT: return "slot_mapping entry out of range";
+    case MLA_ERR_BAD_TOKEN: return "token id out of range, or a distribution without weight";
   }
   return "unknown status";
 }
@@ -678,6 +683,7 @@ mla_status mla_get_device_status(const void* status_word, uint32_t* mask_out, in
   if (v & MLA_DEV_BAD_BLOCK) return MLA_ERR_BAD_BLOCK;
   if (v & MLA_DEV_BAD_SEQ) return MLA_ERR_BAD_SEQ;
   if (v & MLA_DEV_BAD_SLOT) return MLA_ERR_BAD_SLOT;
+  if (v & MLA_DEV_BAD_TOKEN) return MLA_ERR_BAD_TOKEN;
   return MLA_OK;
 }
 

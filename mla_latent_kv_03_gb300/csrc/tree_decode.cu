@@ -1,0 +1,1161 @@
+// mla_tree_decode: split-KV latent attention of the rows of drafted trees over
+// the paged bf16 cache, the merge of the splits and the output projection.
+//
+// Row n of sequence b sees every token t < past = seq_lens[b] - q_len, and of
+// the tree's own tokens past + j those whose bit j its mask has:
+//   s_t = softmax_scale * log2(e) * (q_abs[n,h] . row_t)        (base 2)
+//   out[n,h] = (sum_t 2^(s_t - m) c_t / sum_t 2^(s_t - m)) W_uv[h]
+//
+// The (row, head) pairs of a sequence are cut into q-blocks of 128, which are
+// the M of the tensor-core products; work units are (q-block, 64-token tile).
+// The units are cut into equal contiguous shares, one to a cluster of two CTAs.
+// Where a sequence has several q-blocks its tokens are taken in strips as long
+// as a share, and the q-blocks follow one another within a strip: neighbouring
+// clusters then read the same tokens at the same time, which come from HBM once.
+// CTA h of a pair owns latent columns [256 h, 256 h + 256) of the cache, and CTA
+// 1 the rope columns too:
+//   S_h = Q[:, cols_h] K[:, cols_h]^T    (partial scores, in TMEM, fp32)
+//   S   = S_h + the peer's partial       (sent as f16 into this CTA's shared memory)
+//   O_h += P V[:, cols_h]                (this CTA's half of the output)
+// so every byte of a cache row goes to one shared memory only.
+//
+// Each CTA takes the softmax of its own sums: its own part is fp32 and the
+// peer's rounded to f16 (11 bits, saturating), so the two CTAs' weights differ
+// by that rounding, each half of the output is divided by the sum of its own
+// weights, and the merge weighs each half by its own log-sum-exp. The weights
+// are rounded to bf16 for the product (V is bf16, and the tensor cores take one
+// type); the sum adds the rounded weights, so that a row with one large weight
+// loses nothing.
+//
+// TMEM (512 columns): O [0, 256), two score buffers of 64 columns, whose first
+// half takes the weights (bf16 pairs) once the scores are read, and the
+// query's 256 latent columns (bf16 pairs) [384, 512). CTA 1's rope columns of
+// the query lie in shared memory. Shared memory: four stages of 64 tokens,
+// three buffers of the peer's scores.
+// Per CTA (384 threads):
+//   warp 0      copies the cache stages (TMA, SWIZZLE_128B); block ids are checked
+//   warp 1      issues O += P V of a tile; owns the TMEM
+//   warp 2      issues the scores of a tile
+//   warps 8-11  send a tile's partial scores to the peer
+//   warps 4-7   softmax, a thread a row; at a segment's end they write the
+//               normalised rows and log-sum-exps of it
+// Every wait is bounded; on a timeout the roles leave their loops, the issuers
+// wait for their products and the copies' warp for its copies before TMEM is
+// freed, and the pair meets at a last barrier.
+#include <cuda_fp16.h>
+
+#include "async_copy.cuh"
+#include "cluster.cuh"
+#include "common.cuh"
+#include "internal.h"
+#include "pair_math.cuh"
+#include "tcgen05.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kBlockRows = 128;
+constexpr int kTok = 64;
+constexpr int kSlab = kTok * 128;              // 64 rows of 64 bf16 columns
+constexpr int kMaxSlabs = 5;
+constexpr int kStage = kMaxSlabs * kSlab;      // 40 KB
+constexpr int kStages = 4;
+constexpr int kXBufs = 3;
+constexpr int kXBytes = kBlockRows * kTok * 2; // 16 KB: [8 chunks][128 rows][16 bytes]
+constexpr int kThreads = 384;
+constexpr int kSoftWarp0 = 4, kSendWarp0 = 8;
+constexpr uint32_t kOCol = 0, kSCol = 256, kQCol = 384, kTmemCols = 512;
+constexpr float kRescaleLog2 = 8.f;
+constexpr int kTreeMaxRows = 48 * 1024;
+
+enum {
+  kFull0 = 0,
+  kEmpty0 = kFull0 + kStages,
+  kSFull0 = kEmpty0 + kStages,   // [2] partial scores of tile i in S[i % 2]
+  kSRead0 = kSFull0 + 2,         // [2] S[i % 2] read by the senders (4 arrivals)
+  kPFull0 = kSRead0 + 2,         // [2] weights of tile i in S[i % 2] (128 arrivals)
+  kPVDone0 = kPFull0 + 2,        // [2] O += P V of tile i done
+  kXFull0 = kPVDone0 + 2,        // [kXBufs] the peer's scores of tile i (bytes from the peer)
+  kPeerFree0 = kXFull0 + kXBufs, // [kXBufs] the peer has read its buffer (4 remote arrivals)
+  kQReady = kPeerFree0 + kXBufs, // query columns in place (128 arrivals)
+  kQEmpty,                       // every score product of the segment done
+  kODone,                        // every output product of the segment done
+  kOFree,                        // O read out (128 arrivals)
+  kFinalS,
+  kFinalP,
+  kNumBars
+};
+
+struct Smem {
+  static constexpr int stage = 0;
+  static constexpr int x = stage + kStages * kStage;
+  static constexpr int rope = x + kXBufs * kXBytes;       // [128 rows][64 columns], SWIZZLE_128B
+  static constexpr int info = rope + kBlockRows * 128;    // [kStages] int2
+  static constexpr int bars = info + kStages * 8;
+  static constexpr int misc = bars + kNumBars * 8;        // tmem base, abort flag
+  static constexpr int plan = misc + 16;                  // start of this share: int4; scan scratch
+  static constexpr int bytes = plan + 16 + 2 * (kThreads / 32) * 4;
+  static constexpr int alloc = bytes + 1024;
+};
+static_assert(Smem::alloc <= 227 * 1024, "shared memory budget");
+static_assert(Smem::bars % 8 == 0 && Smem::plan % 16 == 0, "alignment");
+
+struct TreeArgs {
+  const uint16_t* q_abs;
+  int64_t num_blocks, num_q;
+  const int32_t* block_table;
+  int32_t max_blocks, block_size, num_heads, batch, words, shares;
+  const int32_t* seq_lens;
+  const int32_t* query_start_loc;
+  const uint64_t* mask;
+  float scale_log2;
+  uint8_t* ws;
+  uint32_t* status;
+  int4* plan;      // [batch] {first unit, first item, tiles, q-blocks}
+  float* lse;      // [slots][2][128]
+  float* opart;    // [slots][128][512]
+  float* o_lat;    // [num_q, H, 512]
+};
+
+// Workspace: header (status word, share), plan, partials. An item is what one
+// q-block has in one strip; its part in cluster c has slot c + item, which is
+// unique because items and shares are both contiguous and in order.
+struct TreeWs {
+  size_t plan, lse, opart, o_lat, total;
+};
+__host__ __device__ inline TreeWs tree_ws(int64_t num_q, int heads, int shares, int64_t batch) {
+  TreeWs L;
+  // items: a q-block has one, and one more for every share's worth of its units
+  const int64_t slots = 2 * (int64_t)shares + num_q * heads / kBlockRows + batch + 1;
+  size_t off = kLayoutStart;
+  L.plan = off;   off = align_up(off + (size_t)batch * 16, 256);
+  L.lse = off;    off = align_up(off + (size_t)slots * 2 * kBlockRows * 4, 256);
+  L.o_lat = off;  off = align_up(off + (size_t)num_q * heads * kDc * 4, 256);
+  L.opart = off;  off = align_up(off + (size_t)slots * kBlockRows * kDc * 4, 256);
+  L.total = off;
+  return L;
+}
+
+struct TreeSeq {
+  int q0, ql, len, n, m;   // rows [q0, q0 + ql); n tiles, m q-blocks (0: nothing to do)
+  bool broken;             // query_start_loc does not ascend here, or leaves [0, num_q]
+};
+__device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, bool report) {
+  TreeSeq s;
+  s.q0 = a.query_start_loc[b];
+  const int q1 = a.query_start_loc[b + 1];
+  s.ql = q1 - s.q0;
+  s.len = a.seq_lens[b];
+  s.n = s.m = 0;
+  const bool rows_ok = s.q0 >= 0 && q1 <= a.num_q && q1 >= s.q0;
+  s.broken = !rows_ok;
+  const bool ok = rows_ok && s.ql <= s.len && s.ql <= 64 * a.words &&
+                  (int64_t)s.len <= (int64_t)a.max_blocks * a.block_size;
+  if (report && !ok) set_status(a.status, MLA_DEV_BAD_SEQ);
+  if (ok && s.ql > 0) {
+    s.n = (s.len + kTok - 1) / kTok;
+    s.m = (s.ql * a.num_heads + kBlockRows - 1) / kBlockRows;
+  }
+  return s;
+}
+__host__ __device__ __forceinline__ int strips_of(int n, int m, int share) {
+  return m <= 1 ? m : (n + share - 1) / share;
+}
+
+struct TreeSeg {
+  int b, j, k0, k1, item, q0, ql, len;
+};
+
+// Walks the units of one share; every role has its own.
+struct TreeWalk {
+  int u, u_end, share, b, ubase, ibase;
+  TreeSeq s;
+
+  __device__ __forceinline__ bool next(const TreeArgs& a, TreeSeg& g) {
+    if (u >= u_end) return false;
+    while (u >= ubase + s.n * s.m) {
+      ubase += s.n * s.m;
+      ibase += s.m * strips_of(s.n, s.m, share);
+      s = tree_seq(a, ++b, false);
+    }
+    const int off = u - ubase;
+    g.b = b;
+    g.q0 = s.q0;
+    g.ql = s.ql;
+    g.len = s.len;
+    if (s.m == 1) {
+      g.j = 0;
+      g.k0 = off;
+      g.k1 = min(s.n, off + u_end - u);
+      g.item = ibase;
+    } else {
+      const int strip = off / (share * s.m), rem = off - strip * share * s.m;
+      const int L = min(share, s.n - strip * share), k = rem % L;
+      g.j = rem / L;
+      g.k0 = strip * share + k;
+      g.k1 = g.k0 + min(L - k, u_end - u);
+      g.item = ibase + strip * s.m + g.j;
+    }
+    u += g.k1 - g.k0;
+    return true;
+  }
+};
+
+// Exclusive prefix of v over the CTA's threads, and the total.
+__device__ __forceinline__ int block_scan(int v, int* scratch, int tid, int& total) {
+  const int lane = tid & 31, warp = tid >> 5;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) scratch[warp] = incl;
+  __syncthreads();
+  int run = incl - v;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) run += scratch[w];
+    total += scratch[w];
+  }
+  return run;
+}
+
+// The split: where share c begins. Every CTA finds it; the first writes the
+// plan that the merge follows.
+__device__ __forceinline__ bool find_share(const TreeArgs& a, int c, int4* start, int* scratch, int tid, TreeWalk& w) {
+  const bool first = blockIdx.x == 0;
+  const int per = (a.batch + kThreads - 1) / kThreads;
+  const int beg = min(a.batch, tid * per), end = min(a.batch, beg + per);
+  int units = 0, items = 0, total, dummy;
+  bool broken = false;
+  for (int b = beg; b < end; ++b) {
+    const TreeSeq s = tree_seq(a, b, first);
+    units += s.n * s.m;
+    broken |= s.broken;
+  }
+  // (rows that two sequences have would not fit the workspace: nothing is done)
+  if (__syncthreads_or(broken)) {
+    if (first)
+      for (int b = beg; b < end; ++b) a.plan[b] = make_int4(0, 0, 0, 0);
+    return false;
+  }
+  int ubase = block_scan(units, scratch, tid, total);
+  const int share = max(1, (total + a.shares - 1) / a.shares);
+  for (int b = beg; b < end; ++b) {
+    const TreeSeq s = tree_seq(a, b, false);
+    items += s.m * strips_of(s.n, s.m, share);
+  }
+  int ibase = block_scan(items, scratch + kThreads / 32, tid, dummy);
+  const int u0 = (int)min((int64_t)c * share, (int64_t)total);
+  for (int b = beg; b < end; ++b) {
+    const TreeSeq s = tree_seq(a, b, false);
+    if (first) a.plan[b] = make_int4(ubase, ibase, s.n, s.m);
+    if (u0 >= ubase && u0 < ubase + s.n * s.m) *start = make_int4(b, ubase, ibase, 0);
+    ubase += s.n * s.m;
+    ibase += s.m * strips_of(s.n, s.m, share);
+  }
+  if (first && tid == 0) {
+    WsHeader* hdr = reinterpret_cast<WsHeader*>(a.ws);
+    hdr->total_units = total;
+    hdr->share = share;
+  }
+  __syncthreads();
+  w.u = u0;
+  w.u_end = min(u0 + share, total);
+  w.share = share;
+  if (w.u >= w.u_end) return false;
+  const int4 st = *start;
+  w.b = st.x;
+  w.ubase = st.y;
+  w.ibase = st.z;
+  w.s = tree_seq(a, w.b, false);
+  return true;
+}
+
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 15u) == 0) {
+      if (*abort_flag) return false;
+      if (globaltimer_ns() - t0 > kWaitTimeoutNs) return false;
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_f16_sat(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// An infinite score is passed on as NaN: saturated, it would be a large one.
+__device__ __forceinline__ float finite_or_nan(uint32_t x) {
+  return fmaf(__uint_as_float(x), 0.f, __uint_as_float(x));
+}
+// 16 bytes into the peer's shared memory, counted on its barrier.
+__device__ __forceinline__ void send16(uint32_t dst, uint32_t bar, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%2, %3, %4, %5}, [%1];" ::"r"(dst),
+      "r"(bar), "r"(a), "r"(b), "r"(c), "r"(d)
+      : "memory");
+}
+// This CTA's columns of query row `qrow` (of all (row, head)s): 256 latent ones
+// into TMEM lane r, CTA 1's 64 rope ones into shared memory.
+__device__ __forceinline__ void load_query(const TreeArgs& a, int h, int64_t qrow, bool live, uint32_t trow, uint8_t* rope,
+                                           int r) {
+  const uint4* src = reinterpret_cast<const uint4*>(a.q_abs + (size_t)qrow * kRow + 256 * h);
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int hb = 0; hb < 2; ++hb) {
+    uint4 buf[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) buf[i] = live ? __ldg(src + 16 * hb + i) : zero;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t w[16];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        w[4 * k] = buf[4 * c + k].x;
+        w[4 * k + 1] = buf[4 * c + k].y;
+        w[4 * k + 2] = buf[4 * c + k].z;
+        w[4 * k + 3] = buf[4 * c + k].w;
+      }
+      tc::st16(trow + kQCol + 64 * hb + 16 * c, w);
+    }
+  }
+  if (h == 1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<uint4*>(rope + sw128(r, i)) = live ? __ldg(src + 32 + i) : zero;
+    fence_proxy_async_smem();
+  }
+}
+
+// Bit i: row `j0 + i` of the tree is in the mask (words of 64, `words` of them).
+__device__ __forceinline__ uint64_t mask_from(const uint64_t* m, int words, int j0) {
+  const int w = j0 >> 6, sh = j0 & 63;
+  uint64_t x = w < words ? __ldg(m + w) >> sh : 0;
+  if (sh && w + 1 < words) x |= __ldg(m + w + 1) << (64 - sh);
+  return x;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    tree_decode_kernel(const __grid_constant__ CUtensorMap cache_map, const __grid_constant__ CUtensorMap slab4,
+                       const __grid_constant__ CUtensorMap slab5, const __grid_constant__ TreeArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Smem::bars);
+  int2* info = reinterpret_cast<int2*>(sm + Smem::info);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Smem::misc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Smem::misc + 4);
+  uint8_t* sStage = sm + Smem::stage;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = (int)cl::rank();
+  const int share_idx = blockIdx.x >> 1;
+  const int slab0 = 4 * h, nslab = 4 + h;
+  const int bs = a.block_size, bs_shift = bs == 16 ? 4 : bs == 32 ? 5 : 6;
+  const int pages = kTok / bs;                      // of a stage
+  const int full_mask = (1 << pages) - 1;
+
+  if (tid == 0) {
+    for (int i = 0; i < kNumBars; ++i) {
+      const bool all = (i >= kPFull0 && i < kPFull0 + 2) || i == kQReady || i == kOFree;
+      const bool warps = (i >= kSRead0 && i < kSRead0 + 2) || (i >= kPeerFree0 && i < kPeerFree0 + kXBufs);
+      mbar_init(&bars[i], all ? 128 : warps ? 4 : 1);
+    }
+    for (int i = 0; i < kXBufs; ++i) mbar_arrive_expect_tx(&bars[kXFull0 + i], kXBytes);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tc::alloc(tmem_slot, kTmemCols);
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&cache_map);
+    prefetch_tensormap(h ? &slab5 : &slab4);
+  }
+  tc::fence_before_sync();
+  cl::sync();  // both CTAs' barriers exist before either sends
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  TreeWalk sw;
+  int* scratch = reinterpret_cast<int*>(sm + Smem::plan + 16);
+  const bool has_work = find_share(a, share_idx, reinterpret_cast<int4*>(sm + Smem::plan), scratch, tid, sw);
+  TreeSeg seg;
+  auto warp_wait = [&](int bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_or_abort(&bars[bar], parity, abort_flag));
+  };
+  auto fail_out = [&]() {
+    set_status(a.status, MLA_DEV_TIMEOUT);
+    *abort_flag = 1;
+  };
+
+  if (has_work && warp == 0) {
+    // ------------------------------------------------------------ copies
+    const uint64_t policy = l2_evict_first_policy();
+    int i = 0;
+    bool ok = true;
+    while (ok && sw.next(a, seg)) {
+      const int32_t* bt = a.block_table + (size_t)seg.b * a.max_blocks;
+      int cache_base = -(1 << 30), cached = -1;   // lane l holds bt[cache_base + l]
+#pragma unroll 1
+      for (int k = seg.k0; k < seg.k1; ++k, ++i) {
+        const int tstart = k * kTok, v = min(kTok, seg.len - tstart), slot = i % kStages;
+        const int p0 = tstart >> bs_shift;
+        if (p0 < cache_base || p0 + pages > cache_base + 32) {
+          cache_base = p0;
+          cached = p0 + lane < a.max_blocks ? bt[p0 + lane] : -1;
+        }
+        if (i >= kStages && !warp_wait(kEmpty0 + slot, ((i / kStages) - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        // lane l: page l / nslab of the stage, slab l % nslab (64-token pages:
+        // one copy of all slabs)
+        const int pg = bs == kTok ? 0 : lane / nslab, sl = lane % nslab;
+        const int blk = __shfl_sync(0xffffffffu, cached, min(p0 - cache_base + pg, 31));
+        const bool wanted = pg < pages && (pg << bs_shift) < v;
+        const bool there = wanted && blk >= 0 && blk < a.num_blocks;
+        if (wanted && !there && sl == 0) set_status(a.status, MLA_DEV_BAD_BLOCK);
+        const uint32_t loads = __ballot_sync(0xffffffffu, there);
+        uint8_t* dst = sStage + slot * kStage;
+        if (bs == kTok) {
+          if (lane == 0) {
+            info[slot] = make_int2(v, there);
+            mbar_arrive_expect_tx(&bars[kFull0 + slot], there ? nslab * kSlab : 0);
+            if (there)
+              tma_load_3d_hint(dst, h ? &slab5 : &slab4, 0, blk * bs, slab0, &bars[kFull0 + slot], policy);
+          }
+        } else {
+          if (lane == 0) {
+            int okmask = 0;
+            for (int p = 0; p < pages; ++p) okmask |= ((loads >> (p * nslab)) & 1) << p;
+            info[slot] = make_int2(v, okmask);
+            mbar_arrive_expect_tx(&bars[kFull0 + slot], __popc(loads) * bs * 128);
+          }
+          __syncwarp();
+          if (there)
+            tma_load_2d_hint(dst + sl * kSlab + (pg << bs_shift) * 128, &cache_map, 64 * (slab0 + sl), blk * bs,
+                             &bars[kFull0 + slot], policy);
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) {
+      if (!ok) fail_out();
+      for (int slot = 0; slot < kStages; ++slot) {   // never leave with copies in flight
+        const int fills = i > slot ? (i - 1 - slot) / kStages + 1 : 0;
+        if (fills > 0 && !mbar_wait(&bars[kFull0 + slot], (fills - 1) & 1)) set_status(a.status, MLA_DEV_TIMEOUT);
+      }
+    }
+    __syncwarp();
+  } else if (has_work && warp == 1) {
+    // ---------------------------------------------------- output products
+    constexpr uint32_t kIdO = tc::idesc_bf16(128, 256, false, true);
+    const uint64_t vdesc = tc::smem_desc(smem_u32(sStage), kSlab, 1024, tc::kSwizzle128);
+    const bool leader = tc::elect_one();
+    int i = 0, seg_i = 0;
+    bool ok = true;
+    while (ok && sw.next(a, seg)) {
+      const int n = seg.k1 - seg.k0;
+#pragma unroll 1
+      for (int t = 0; t < n; ++t, ++i) {
+        const int slot = i % kStages, b = i & 1;
+        if (!warp_wait(kPFull0 + b, (i >> 1) & 1)) { ok = false; break; }
+        if (t == 0 && seg_i > 0 && !warp_wait(kOFree, (seg_i - 1) & 1)) { ok = false; break; }
+        tc::fence_after_sync();
+        if (leader) {
+#pragma unroll
+          for (int ks = 0; ks < kTok / 16; ++ks)
+            tc::mma_bf16_tmem_a(tmem + kOCol, tmem + kSCol + (uint32_t)(b * kTok + ks * 8),
+                                vdesc + (uint64_t)((slot * kStage + ks * 16 * 128) >> 4), kIdO, t > 0 || ks > 0);
+          tc::commit(&bars[kEmpty0 + slot]);
+          tc::commit(&bars[kPVDone0 + b]);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (leader) tc::commit(&bars[kODone]);
+      __syncwarp();
+      ++seg_i;
+    }
+    if (!ok && leader) fail_out();
+    if (leader) tc::commit(&bars[kFinalP]);
+    __syncwarp();
+    if (!mbar_wait(&bars[kFinalP], 0) && leader) set_status(a.status, MLA_DEV_TIMEOUT);
+    __syncwarp();
+  } else if (has_work && warp == 2) {
+    // ------------------------------------------------------------- scores
+    constexpr uint32_t kIdS = tc::idesc_bf16(128, kTok, false, false);
+    const uint64_t kdesc = tc::smem_desc(smem_u32(sStage), 16, 1024, tc::kSwizzle128);
+    const uint64_t rdesc = tc::smem_desc(smem_u32(sm + Smem::rope), 16, 1024, tc::kSwizzle128);
+    const bool leader = tc::elect_one();
+    int i = 0, seg_i = 0;
+    bool ok = true;
+    while (ok && sw.next(a, seg)) {
+      const int n = seg.k1 - seg.k0;
+      if (!warp_wait(kQReady, seg_i & 1)) { ok = false; break; }
+#pragma unroll 1
+      for (int t = 0; t < n; ++t, ++i) {
+        const int slot = i % kStages, b = i & 1;
+        // the weights of tile i - 2 in this buffer have been used
+        if (i >= 2 && !warp_wait(kPVDone0 + b, ((i - 2) >> 1) & 1)) { ok = false; break; }
+        if (!warp_wait(kFull0 + slot, (i / kStages) & 1)) { ok = false; break; }
+        tc::fence_after_sync();
+        if (leader) {
+          const uint32_t d = tmem + kSCol + (uint32_t)(b * kTok);
+          const uint64_t kd = kdesc + (uint64_t)((slot * kStage) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 16; ++kk)
+            tc::mma_bf16_tmem_a(d, tmem + kQCol + (uint32_t)(kk * 8),
+                                kd + (uint64_t)(((kk >> 2) * kSlab + (kk & 3) * 32) >> 4), kIdS, kk > 0);
+          if (h == 1) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              tc::mma_bf16(d, rdesc + (uint64_t)((c * 32) >> 4), kd + (uint64_t)((4 * kSlab + c * 32) >> 4), kIdS, true);
+          }
+          tc::commit(&bars[kSFull0 + b]);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (leader) tc::commit(&bars[kQEmpty]);
+      __syncwarp();
+      ++seg_i;
+    }
+    if (!ok && leader) fail_out();
+    if (leader) tc::commit(&bars[kFinalS]);
+    __syncwarp();
+    if (!mbar_wait(&bars[kFinalS], 0) && leader) set_status(a.status, MLA_DEV_TIMEOUT);
+    __syncwarp();
+  } else if (has_work && warp >= kSendWarp0) {
+    // ------------------------------------------------------------ senders
+    const int r = tid - kSendWarp0 * 32;
+    const uint32_t trow = tmem + ((uint32_t)((warp - kSendWarp0) * 32) << 16);
+    const uint32_t peer = (uint32_t)(h ^ 1);
+    const uint32_t x_peer = cl::map(smem_u32(sm + Smem::x), peer) + (uint32_t)r * 16;
+    const uint32_t xbar_peer = cl::map(smem_u32(&bars[kXFull0]), peer);
+    int i = 0;
+    bool ok = true;
+    while (ok && sw.next(a, seg)) {
+      const int n = seg.k1 - seg.k0;
+#pragma unroll 1
+      for (int t = 0; t < n; ++t, ++i) {
+        const int b = i & 1, xb = i % kXBufs;
+        if (!warp_wait(kSFull0 + b, (i >> 1) & 1)) { ok = false; break; }
+        tc::fence_after_sync();
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t sv[32];
+          tc::ld32(trow + kSCol + (uint32_t)(b * kTok + 32 * c), sv);
+          tc::wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            pk[16 * c + k] = pack_f16_sat(finite_or_nan(sv[2 * k]), finite_or_nan(sv[2 * k + 1]));
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kSRead0 + b]);
+        // the peer has read tile i - kXBufs from its buffer
+        if (i >= kXBufs && !warp_wait(kPeerFree0 + xb, ((i / kXBufs) - 1) & 1)) { ok = false; break; }
+        const uint32_t dst = x_peer + (uint32_t)(xb * kXBytes), bar = xbar_peer + (uint32_t)xb * 8;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          send16(dst + c * (kBlockRows * 16), bar, pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+      }
+    }
+    if (!ok && lane == 0) fail_out();
+  } else if (has_work && warp >= kSoftWarp0) {
+    // ------------------------------------------------------------ softmax
+    const int r = tid - kSoftWarp0 * 32;
+    const uint32_t trow = tmem + ((uint32_t)((warp - kSoftWarp0) * 32) << 16);
+    const uint32_t pfree_peer = cl::map(smem_u32(&bars[kPeerFree0]), (uint32_t)(h ^ 1));
+    const float scale = a.scale_log2;
+    int i = 0, seg_i = 0;
+    bool fail = false;
+    auto query_in = [&](const TreeSeg& g) {
+      const int qr = g.j * kBlockRows + r;
+      load_query(a, h, (int64_t)g.q0 * a.num_heads + qr, qr < g.ql * a.num_heads, trow, sm + Smem::rope, r);
+      tc::wait_st();
+      tc::fence_before_sync();
+      mbar_arrive(&bars[kQReady]);
+    };
+    bool have = sw.next(a, seg);
+    if (have) query_in(seg);
+    while (have) {
+      const int n = seg.k1 - seg.k0, past = seg.len - seg.ql;
+      const int qr = seg.j * kBlockRows + r, row = qr / a.num_heads;   // of the sequence
+      const bool live_row = row < seg.ql;
+      const uint64_t* mrow = a.mask + (size_t)(seg.q0 + (live_row ? row : 0)) * a.words;
+      float m_used = -INFINITY, l = 0.f;
+#pragma unroll 1
+      for (int t = 0; t < n; ++t, ++i) {
+        const int slot = i % kStages, b = i & 1, xb = i % kXBufs;
+        fail |= !wait_or_abort(&bars[kSFull0 + b], (i >> 1) & 1, abort_flag);
+        if (__any_sync(0xffffffffu, fail)) { fail = true; break; }
+        tc::fence_after_sync();
+        uint32_t sv[2][32];
+        tc::ld32(trow + kSCol + (uint32_t)(b * kTok), sv[0]);
+        tc::ld32(trow + kSCol + (uint32_t)(b * kTok + 32), sv[1]);
+        tc::wait_ld();
+        fail |= !wait_or_abort(&bars[kXFull0 + xb], (i / kXBufs) & 1, abort_flag);
+        fail |= !wait_or_abort(&bars[kFull0 + slot], (i / kStages) & 1, abort_flag);
+        if (__any_sync(0xffffffffu, fail)) { fail = true; break; }
+        if (r == 0) mbar_arrive_expect_tx(&bars[kXFull0 + xb], kXBytes);   // for tile i + kXBufs
+        float x[64];
+        {
+          const uint8_t* xp = sm + Smem::x + xb * kXBytes + r * 16;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint4 pv = *reinterpret_cast<const uint4*>(xp + c * (kBlockRows * 16));
+            const uint32_t w[4] = {pv.x, pv.y, pv.z, pv.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+              const int at = 8 * (c & 3) + 2 * k;
+              x[8 * c + 2 * k] = __uint_as_float(sv[c >> 2][at]) + f.x;
+              x[8 * c + 2 * k + 1] = __uint_as_float(sv[c >> 2][at + 1]) + f.y;
+            }
+          }
+        }
+        const int2 inf = info[slot];
+        const int tstart = (seg.k0 + t) * kTok, v = inf.x, okmask = inf.y;
+        const bool tree_here = tstart + kTok > past;
+        const bool careful = v < kTok || okmask != full_mask || tree_here;   // (the same for all threads)
+        if (careful) {
+          uint64_t live = 0;
+          if (live_row) {
+            const int before = past - tstart;     // tokens of the tile that came before the tree
+            live = before >= kTok ? ~0ull : before > 0 ? (1ull << before) - 1 : 0ull;
+            if (tree_here) {
+              if (before > 0)
+                live |= mask_from(mrow, a.words, 0) << before;
+              else
+                live |= mask_from(mrow, a.words, -before);
+            }
+          }
+          uint64_t there = v < kTok ? (1ull << v) - 1 : ~0ull;
+          for (int p = 0; p < pages; ++p)
+            if (!((okmask >> p) & 1)) there &= ~((bs == 64 ? ~0ull : (1ull << bs) - 1) << (p << bs_shift));
+          live &= there;
+          // A token that is not finite makes a row that sees it NaN, whatever its weight.
+          bool odd = false;
+#pragma unroll
+          for (int j = 0; j < 64; ++j) {
+            const bool seen = (live >> j) & 1;
+            odd |= seen && !(fabsf(x[j]) < INFINITY);
+            if (!seen) x[j] = -INFINITY;
+          }
+          if (odd) l = NAN;
+          // Rows of the stage that are not there may hold anything: zero, so that
+          // a weight of 0 stays 0. So do the tree's tokens that are not finite, for
+          // the rows that do not see them.
+          const int tok = r & 63;
+          uint8_t* stg = sStage + slot * kStage + (r >> 6) * 2 * kSlab;
+          bool zero = !((there >> tok) & 1);
+          if (!zero && tstart + tok >= past) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const uint4 y = *reinterpret_cast<const uint4*>(stg + (c >> 3) * kSlab + sw128(tok, c & 7));
+              const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                zero |= (w[k] & 0x7f80u) == 0x7f80u || (w[k] & 0x7f800000u) == 0x7f800000u;
+            }
+          }
+          if (zero) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              *reinterpret_cast<uint4*>(stg + (c >> 3) * kSlab + sw128(tok, c & 7)) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        float mx[22];
+#pragma unroll
+        for (int j = 0; j < 21; ++j) mx[j] = fmax3(x[3 * j], x[3 * j + 1], x[3 * j + 2]);
+        mx[21] = x[63];
+#pragma unroll
+        for (int j = 0; j < 7; ++j) mx[j] = fmax3(mx[3 * j], mx[3 * j + 1], mx[3 * j + 2]);
+        mx[0] = fmax3(mx[0], mx[1], mx[2]);
+        mx[3] = fmax3(mx[3], mx[4], mx[5]);
+        const float m_cand = fmax3(mx[0], mx[3], fmaxf(mx[6], mx[21])) * scale;
+        float alpha = 1.f;
+        bool rescale = false;
+        if (m_cand > m_used + kRescaleLog2 || (m_used == -INFINITY && m_cand != -INFINITY)) {
+          if (m_used != -INFINITY) {
+            alpha = fast_exp2(m_used - m_cand);
+            rescale = t > 0;
+          }
+          l *= alpha;
+          m_used = m_cand;
+        }
+        const bool any = __any_sync(0xffffffffu, rescale);
+        // (every lane's scores have arrived: their maxima are in the vote)
+        if (lane == 0) cl::arrive_remote_relaxed(pfree_peer + (uint32_t)xb * 8);
+        if (any) {
+          const bool okp = __all_sync(0xffffffffu,
+                                      wait_or_abort(&bars[kPVDone0 + ((i - 1) & 1)], ((i - 1) >> 1) & 1, abort_flag));
+          if (!okp) { fail = true; break; }
+          tc::fence_after_sync();
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[32];
+            tc::ld32(trow + kOCol + 32 * c, o);
+            tc::wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tc::st32(trow + kOCol + 32 * c, o);
+          }
+        }
+        const float mneg = m_used == -INFINITY ? 0.f : -m_used;
+        const float2 sc2 = make_float2(scale, scale), mn2 = make_float2(mneg, mneg);
+        uint32_t pk[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float2 e = fma_f32x2(make_float2(x[2 * j], x[2 * j + 1]), sc2, mn2);
+          pk[j] = pack_bf16(fast_exp2(e.x), fast_exp2(e.y));
+        }
+        // the senders have read this buffer's scores
+        fail |= !wait_or_abort(&bars[kSRead0 + b], (i >> 1) & 1, abort_flag);
+        if (__any_sync(0xffffffffu, fail)) { fail = true; break; }
+        tc::st32(trow + kSCol + (uint32_t)(b * kTok), pk);
+        float2 sum[4] = {};
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          sum[j & 3] = add_f32x2(sum[j & 3], make_float2(__uint_as_float(pk[j] << 16), __uint_as_float(pk[j] & 0xffff0000u)));
+        sum[0] = add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3]));
+        l += sum[0].x + sum[0].y;
+        tc::wait_st();
+        tc::fence_before_sync();
+        mbar_arrive(&bars[kPFull0 + b]);
+      }
+      // (a warp that failed leaves; the others' waits see the abort flag)
+      if (fail) break;
+      TreeSeg nxt;
+      const bool more = sw.next(a, nxt);
+      if (more) {
+        // the next segment's query, while this one's last products finish
+        if (!warp_wait(kQEmpty, seg_i & 1)) { fail = true; break; }
+        tc::fence_after_sync();
+        query_in(nxt);
+      }
+      if (!warp_wait(kODone, seg_i & 1)) { fail = true; break; }
+      tc::fence_after_sync();
+      const int64_t slot = (int64_t)share_idx + seg.item;
+      const float inv = l == 0.f ? 0.f : 1.f / l;      // (NaN stays NaN)
+      float4* dst = reinterpret_cast<float4*>(a.opart + ((size_t)slot * kBlockRows + r) * kDc + 256 * h);
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        uint32_t o[32];
+        tc::ld32(trow + kOCol + 32 * c, o);
+        tc::wait_ld();
+        if (live_row) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            dst[8 * c + k] = make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv,
+                                         __uint_as_float(o[4 * k + 2]) * inv, __uint_as_float(o[4 * k + 3]) * inv);
+        }
+      }
+      a.lse[(slot * 2 + h) * kBlockRows + r] = l == 0.f ? -INFINITY : m_used + log2f(l);
+      tc::fence_before_sync();
+      mbar_arrive(&bars[kOFree]);
+      seg = nxt;
+      have = more;
+      ++seg_i;
+    }
+    if (fail && lane == 0) fail_out();
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 1) tc::dealloc(tmem, kTmemCols);
+  cl::sync();  // the peer no longer sends into this CTA's shared memory
+}
+
+// ------------------------------------------------------- merge and projection
+// The parts of (row n, head h): `count` of them, part i in slot(i), row r of it.
+struct RowParts {
+  int count, r, share, ubase, ibase, m, j, full, per, tail;
+
+  __device__ __forceinline__ int slot(int i) const {
+    if (m == 1) return ubase / share + i + ibase;
+    if (i < full * per) {
+      const int s = i / per;
+      return ubase / share + s * m + j + i % per + ibase + s * m + j;
+    }
+    const int start = ubase + full * share * m + j * tail;
+    return start / share + (i - full * per) + ibase + full * m + j;
+  }
+};
+__device__ __forceinline__ RowParts row_parts(const TreeArgs& a, int64_t n, int h) {
+  RowParts p{};
+  if (n >= a.num_q) return p;
+  int lo = 0, hi = a.batch;   // the last sequence that begins at or before row n
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.query_start_loc[mid] <= n) lo = mid; else hi = mid;
+  }
+  const int q0 = a.query_start_loc[lo];
+  if (q0 < 0 || n < q0 || n >= a.query_start_loc[lo + 1]) return p;
+  const int4 pl = a.plan[lo];
+  if (pl.w <= 0) return p;
+  p.share = reinterpret_cast<const WsHeader*>(a.ws)->share;
+  p.ubase = pl.x;
+  p.ibase = pl.y;
+  p.m = pl.w;
+  const int rr = ((int)n - q0) * a.num_heads + h;
+  p.j = rr / kBlockRows;
+  p.r = rr % kBlockRows;
+  const int tiles = pl.z;
+  if (p.m == 1) {
+    p.count = (p.ubase + tiles - 1) / p.share - p.ubase / p.share + 1;
+  } else {
+    p.full = tiles / p.share;
+    p.per = p.ubase % p.share ? 2 : 1;
+    p.tail = tiles % p.share;
+    p.count = p.full * p.per;
+    if (p.tail) {
+      const int start = p.ubase + p.full * p.share * p.m + p.j * p.tail;
+      p.count += (start + p.tail - 1) / p.share - start / p.share + 1;
+    }
+  }
+  return p;
+}
+
+// The merge of many parts of few (row, head)s, two CTAs each, of 256 columns:
+// thread (p, c) sums 4 columns over every fourth part.
+__global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
+  __shared__ float4 sAcc[3][64];
+  const int n = blockIdx.x / a.num_heads, h = blockIdx.x % a.num_heads, half = blockIdx.y, tid = threadIdx.x;
+  const int p = tid >> 6, c = half * 64 + (tid & 63), lane = tid & 31;
+  pdl_wait();
+  pdl_launch_dependents();
+  const RowParts rp = row_parts(a, n, h);
+  auto lse_at = [&](int i) { return a.lse[((int64_t)rp.slot(i) * 2 + half) * kBlockRows + rp.r]; };
+  auto o_at = [&](int i) {
+    return *reinterpret_cast<const float4*>(a.opart + ((int64_t)rp.slot(i) * kBlockRows + rp.r) * kDc + 4 * c);
+  };
+  float4 v[8];
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (s0 + 4 * u < rp.count) v[u] = o_at(s0 + 4 * u);
+  };
+  load(p);
+  float m = -INFINITY, den = 0.f;
+  for (int s = lane; s < rp.count; s += 32) m = fmaxf(m, lse_at(s));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float base = m == -INFINITY ? 0.f : m;
+  for (int s = lane; s < rp.count; s += 32) den += fast_exp2(lse_at(s) - base);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int s0 = p; s0 < rp.count; s0 += 32) {
+    if (s0 != p) load(s0);
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (s0 + 4 * u < rp.count) {
+        const float w = fast_exp2(lse_at(s0 + 4 * u) - base) * inv;
+        acc.x = fmaf(w, v[u].x, acc.x);
+        acc.y = fmaf(w, v[u].y, acc.y);
+        acc.z = fmaf(w, v[u].z, acc.z);
+        acc.w = fmaf(w, v[u].w, acc.w);
+      }
+  }
+  if (p > 0) sAcc[p - 1][tid & 63] = acc;
+  __syncthreads();
+  if (p == 0) {
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+      const float4 x = sAcc[u][tid];
+      acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+    }
+    *reinterpret_cast<float4*>(a.o_lat + ((size_t)n * a.num_heads + h) * kDc + 4 * c) = acc;
+  }
+}
+
+// The merge of a few parts and the output projection in one: CTA = (ROWS rows,
+// head h). W_uv[h] (128 KB) comes by cp.async while 256 / ROWS threads a row
+// merge its 512 latents to two bf16 terms each, so that the output is rounded
+// once; then 8 warps, each a quarter of K and half of the columns (m16n8k16).
+template <int ROWS>
+struct Pj {
+  static constexpr int stride = kDc * 2 + 16;     // bytes of a merged row, padded against bank conflicts
+  static constexpr int w = 0;                     // two halves of 64 columns, 128-byte rows
+  static constexpr int a = w + kDc * 256;
+  static constexpr int red = a + 2 * ROWS * stride;  // [4][ROWS][128]
+  static constexpr int bytes = red + 4 * ROWS * kDv * 4;
+};
+template <int ROWS, bool MERGED>
+__global__ void __launch_bounds__(256) tree_proj_kernel(const __grid_constant__ TreeArgs a, const __nv_bfloat16* W_uv,
+                                                        __nv_bfloat16* out) {
+  using M = Pj<ROWS>;
+  constexpr int kTr = 256 / ROWS, kVec = kDc / 4 / kTr;     // threads a row, float4s a thread
+  constexpr int kBatch = 16 / kVec;                         // parts at a time
+  extern __shared__ __align__(1024) uint8_t smem_pj[];
+  float* sRed = reinterpret_cast<float*>(smem_pj + M::red);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.y, row0 = blockIdx.x * ROWS, H = a.num_heads;
+  const __nv_bfloat16* src = W_uv + (size_t)h * kDc * kDv;
+#pragma unroll 4
+  for (int i = tid; i < kDc * 16; i += 256) {
+    const int k = i >> 4, c = i & 15;
+    cp_async16(smem_pj + M::w + (c >> 3) * (kDc * 128) + sw128(k, c & 7), src + (size_t)k * kDv + c * 8);
+  }
+  cp_async_commit();
+  pdl_wait();
+  pdl_launch_dependents();
+  {
+    const int r = tid / kTr, j = tid % kTr, n = row0 + r;
+    float4 acc[kVec];
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (MERGED) {
+      if (n < a.num_q) {
+        const float4* o = reinterpret_cast<const float4*>(a.o_lat + ((size_t)n * H + h) * kDc);
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) acc[k] = o[j + kTr * k];
+      }
+    } else {
+      const RowParts rp = row_parts(a, n, h);
+      auto lse_at = [&](int i, int half) { return a.lse[((int64_t)rp.slot(i) * 2 + half) * kBlockRows + rp.r]; };
+      float4 v[kBatch][kVec];
+      auto load = [&](int s0) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+          if (s0 + u < rp.count) {
+            const float4* o =
+                reinterpret_cast<const float4*>(a.opart + ((int64_t)rp.slot(s0 + u) * kBlockRows + rp.r) * kDc);
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) v[u][k] = o[j + kTr * k];
+          }
+      };
+      load(0);
+      float base[2], inv[2];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float m = -INFINITY, den = 0.f;
+        for (int s = j; s < rp.count; s += kTr) m = fmaxf(m, lse_at(s, hf));
+#pragma unroll
+        for (int o = kTr / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        base[hf] = m == -INFINITY ? 0.f : m;
+        for (int s = j; s < rp.count; s += kTr) den += fast_exp2(lse_at(s, hf) - base[hf]);
+#pragma unroll
+        for (int o = kTr / 2; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+        inv[hf] = den == 0.f ? 0.f : 1.f / den;
+      }
+#pragma unroll 1
+      for (int s0 = 0; s0 < rp.count; s0 += kBatch) {
+        if (s0 > 0) load(s0);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+          if (s0 + u < rp.count) {
+            const float w0 = fast_exp2(lse_at(s0 + u, 0) - base[0]) * inv[0];
+            const float w1 = fast_exp2(lse_at(s0 + u, 1) - base[1]) * inv[1];
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) {
+              const float w = k < kVec / 2 ? w0 : w1;       // (columns 4 (j + kTr k))
+              acc[k].x = fmaf(w, v[u][k].x, acc[k].x);
+              acc[k].y = fmaf(w, v[u][k].y, acc[k].y);
+              acc[k].z = fmaf(w, v[u][k].z, acc[k].z);
+              acc[k].w = fmaf(w, v[u][k].w, acc[k].w);
+            }
+          }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+      const uint32_t t0 = pack_bf16(acc[k].x, acc[k].y), t1 = pack_bf16(acc[k].z, acc[k].w);
+      auto low = [](uint32_t t) { return __uint_as_float(t << 16); };
+      auto high = [](uint32_t t) { return __uint_as_float(t & 0xffff0000u); };
+      uint8_t* at = smem_pj + M::a + r * M::stride + (j + kTr * k) * 8;
+      *reinterpret_cast<uint2*>(at) = make_uint2(t0, t1);
+      *reinterpret_cast<uint2*>(at + ROWS * M::stride) =
+          make_uint2(pack_bf16(acc[k].x - low(t0), acc[k].y - high(t0)),
+                     pack_bf16(acc[k].z - low(t1), acc[k].w - high(t1)));
+    }
+  }
+  cp_async_wait_all();
+  __syncthreads();
+  const int g = lane >> 2, q = lane & 3, kq = warp >> 1, nh = warp & 1;
+  const uint8_t* sW = smem_pj + M::w + nh * (kDc * 128);
+  float acc[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+#pragma unroll
+  for (int ks = 0; ks < 8; ++ks) {
+    const int k = kq * 128 + ks * 16;
+    // row g + 8: of the second terms, or a row of its own
+    const uint8_t* lo = smem_pj + M::a + g * M::stride + (k + 2 * q) * 2;
+    auto frag = [&](int row, int at) { return *reinterpret_cast<const uint32_t*>(lo + row * M::stride + at); };
+    const uint32_t a0 = frag(0, 0), a1 = frag(8, 0), a2 = frag(0, 16), a3 = frag(8, 16);
+    uint32_t c0 = 0, c1 = 0, c2 = 0, c3 = 0;
+    if (ROWS == 16) c0 = frag(16, 0), c1 = frag(24, 0), c2 = frag(16, 16), c3 = frag(24, 16);
+    const int kr = k + (lane & 7) + (((lane >> 3) & 1) << 3);
+#pragma unroll
+    for (int np = 0; np < 4; ++np) {
+      uint32_t b0, b1, b2, b3;
+      ldsm_x4_t(smem_u32(sW + sw128(kr, np * 2 + (lane >> 4))), b0, b1, b2, b3);
+      mma_16816(acc[2 * np], a0, a1, a2, a3, b0, b1);
+      mma_16816(acc[2 * np + 1], a0, a1, a2, a3, b2, b3);
+      if (ROWS == 16) {
+        mma_16816(acc[2 * np], c0, c1, c2, c3, b0, b1);
+        mma_16816(acc[2 * np + 1], c0, c1, c2, c3, b2, b3);
+      }
+    }
+  }
+#pragma unroll
+  for (int nt = 0; nt < 8; ++nt) {
+    float* d = sRed + (kq * ROWS + g) * kDv + nh * 64 + nt * 8 + 2 * q;
+    if (ROWS == 16) {
+      *reinterpret_cast<float2*>(d) = make_float2(acc[nt][0], acc[nt][1]);
+      *reinterpret_cast<float2*>(d + 8 * kDv) = make_float2(acc[nt][2], acc[nt][3]);
+    } else {
+      *reinterpret_cast<float2*>(d) = make_float2(acc[nt][0] + acc[nt][2], acc[nt][1] + acc[nt][3]);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = tid; i < ROWS * kDv / 4; i += 256) {
+    const int r = i / (kDv / 4), c = (i % (kDv / 4)) * 4, row = row0 + r;
+    if (row >= a.num_q) continue;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 x = *reinterpret_cast<const float4*>(sRed + (k * ROWS + r) * kDv + c);
+      v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+    }
+    *reinterpret_cast<uint2*>(out + ((size_t)row * H + h) * kDv + c) =
+        make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+  }
+}
+
+bool al(const void* p, uintptr_t x) { return (reinterpret_cast<uintptr_t>(p) & (x - 1)) == 0; }
+
+// Clusters of the decode that run at once on the current device (0: unknown).
+int tree_clusters() {
+  static int cached[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (cached[dev] > 0) return cached[dev];
+  if (cudaFuncSetAttribute(tree_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::alloc) != cudaSuccess)
+    return 0;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(2);
+  lc.blockDim = dim3(kThreads);
+  lc.dynamicSmemBytes = Smem::alloc;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, tree_decode_kernel, &lc) != cudaSuccess) return 0;
+  cached[dev] = n;
+  return n;
+}
+int tree_shares(const mla_config* cfg) {
+  const int c = split_ctas(cfg) / 2;
+  if (cfg->num_ctas > 0) return c > 0 ? c : 1;
+  if (c <= 0) return c;
+  const int most = tree_clusters();
+  return most > 0 && most < c ? most : c;
+}
+bool tree_sizes_fit(int64_t num_q, int64_t max_blocks, int bs) {
+  const int64_t tokens = max_blocks * bs;
+  return num_q <= kTreeMaxRows && tokens <= ((int64_t)1 << 30) && (num_q == 0 || tokens <= ((int64_t)1 << 35) / num_q);
+}
+
+}  // namespace
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" {
+
+size_t mla_tree_decode_workspace_size(const mla_config* cfg, int64_t num_q, int32_t batch) {
+  if (validate_config(cfg) != MLA_OK || cfg->dtype != MLA_BF16 || num_q < 0 || num_q > kTreeMaxRows || batch < 0)
+    return 0;
+  const int C = tree_shares(cfg);
+  if (C <= 0) return 0;
+  return tree_ws(num_q, cfg->num_heads, C, batch).total;
+}
+
+mla_status mla_tree_decode(const mla_config* cfg, const void* q_abs, const void* cache, int64_t num_blocks,
+                           const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                           const int32_t* query_start_loc, int32_t batch, int64_t num_q, const uint64_t* tree_mask,
+                           int32_t mask_words, const void* W_uv, void* workspace, size_t ws_bytes, void* out,
+                           void* stream) {
+  if (validate_config(cfg) == MLA_OK && cfg->dtype != MLA_BF16) return MLA_ERR_UNSUPPORTED;
+  mla_status s = decode_paged_checks(cfg, q_abs, cache, num_blocks, block_table, max_blocks_per_seq, seq_lens,
+                                     query_start_loc, batch, num_q);
+  if (s != MLA_OK) return s;
+  if (mask_words < 1) return MLA_ERR_INVALID_ARGUMENT;
+  if (mask_words > 16) return MLA_ERR_UNSUPPORTED;
+  if (!workspace || !al(workspace, 256)) return MLA_ERR_INVALID_ARGUMENT;
+  if (num_q == 0) return MLA_OK;
+  if (!tree_mask || !W_uv || !out || !al(tree_mask, 8) || !al(W_uv, 16) || !al(out, 16)) return MLA_ERR_INVALID_ARGUMENT;
+  const int H = cfg->num_heads, bs = cfg->block_size;
+  if (!tree_sizes_fit(num_q, max_blocks_per_seq, bs)) return MLA_ERR_UNSUPPORTED;
+  const int C = tree_shares(cfg);
+  if (C <= 0) return MLA_ERR_CUDA;
+  const TreeWs L = tree_ws(num_q, H, C, batch);
+  if (ws_bytes < L.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  TreeArgs a{};
+  a.q_abs = (const uint16_t*)q_abs;
+  a.num_blocks = num_blocks;
+  a.num_q = num_q;
+  a.block_table = block_table;
+  a.max_blocks = max_blocks_per_seq;
+  a.block_size = bs;
+  a.num_heads = H;
+  a.batch = batch;
+  a.words = mask_words;
+  a.shares = C;
+  a.seq_lens = seq_lens;
+  a.query_start_loc = query_start_loc;
+  a.mask = tree_mask;
+  a.scale_log2 = (float)(cfg->softmax_scale * 1.4426950408889634);
+  a.ws = ws;
+  a.status = &reinterpret_cast<WsHeader*>(ws)->status;
+  a.plan = reinterpret_cast<int4*>(ws + L.plan);
+  a.lse = reinterpret_cast<float*>(ws + L.lse);
+  a.opart = reinterpret_cast<float*>(ws + L.opart);
+  a.o_lat = reinterpret_cast<float*>(ws + L.o_lat);
+  // With num_blocks == 0 every block id is rejected before any copy; the maps
+  // still need an extent.
+  const uint64_t rows = (uint64_t)(num_blocks > 0 ? num_blocks : 1) * bs;
+  CUtensorMap cache_map, slab4, slab5;
+  if (!encode_row_map(&cache_map, cache, rows, (uint32_t)bs)) return MLA_ERR_CUDA;
+  slab4 = slab5 = cache_map;
+  if (bs == kTok && (!encode_slab_map(&slab4, cache, rows, kTok, 4) || !encode_slab_map(&slab5, cache, rows, kTok, 5)))
+    return MLA_ERR_CUDA;
+  cudaError_t e = cudaFuncSetAttribute(tree_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::alloc);
+  if (e == cudaSuccess)
+    e = launch_pdl(tree_decode_kernel, dim3(2 * C), dim3(kThreads), Smem::alloc, st, cache_map, slab4, slab5, a);
+  if (e != cudaSuccess) return MLA_ERR_CUDA;
+  auto project = [&](auto kernel, int per, int smem) {
+    const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return r != cudaSuccess ? r
+                            : launch_pdl(kernel, dim3((unsigned)((num_q + per - 1) / per), H), dim3(256), smem, st, a,
+                                         (const __nv_bfloat16*)W_uv, (__nv_bfloat16*)out);
+  };
+  const bool many_parts = num_q * H < 512 && (int64_t)max_blocks_per_seq * bs > 512;
+  if (many_parts) {
+    e = launch_pdl(tree_merge_kernel, dim3((unsigned)(num_q * H), 2), dim3(256), 0, st, a);
+    if (e == cudaSuccess) e = project(tree_proj_kernel<8, true>, 8, Pj<8>::bytes);
+  } else {
+    e = (num_q + 7) / 8 * H <= 2 * C ? project(tree_proj_kernel<8, false>, 8, Pj<8>::bytes)
+                                     : project(tree_proj_kernel<16, false>, 16, Pj<16>::bytes);
+  }
+  return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -23,8 +23,9 @@ STATUS_NAMES = {
     0: "MLA_OK", 1: "MLA_ERR_INVALID_ARGUMENT", 2: "MLA_ERR_UNSUPPORTED",
     3: "MLA_ERR_WORKSPACE_TOO_SMALL", 4: "MLA_ERR_CUDA", 5: "MLA_ERR_TIMEOUT",
     6: "MLA_ERR_BAD_BLOCK", 7: "MLA_ERR_BAD_SEQ", 8: "MLA_ERR_BAD_SLOT",
+    9: "MLA_ERR_BAD_TOKEN",
 }
-DEV_TIMEOUT, DEV_BAD_BLOCK, DEV_BAD_SEQ, DEV_BAD_SLOT = 1, 2, 4, 8
+DEV_TIMEOUT, DEV_BAD_BLOCK, DEV_BAD_SEQ, DEV_BAD_SLOT, DEV_BAD_TOKEN = 1, 2, 4, 8, 16
 
 EXPORTS = (
     "mla_default_config", "mla_cache_write", "mla_absorb_q", "mla_decode_workspace_size",
@@ -34,6 +35,8 @@ EXPORTS = (
     "mla_decode_paged_combine_fp8",
     "mla_page8_write_workspace_size", "mla_page8_cache_write", "mla_page8_decode_workspace_size",
     "mla_page8_decode", "mla_page8_decode_mass", "mla_evict_select", "mla_page8_compact",
+    "mla_tree_plan", "mla_tree_decode_workspace_size", "mla_tree_decode", "mla_tree_verify",
+    "mla_tree_commit",
     "mla_proj_workspace_size", "mla_q_proj", "mla_kv_a_proj", "mla_o_proj",
     "mla_naive_workspace_size", "mla_naive_cache_write",
     "mla_latent_expand", "mla_latent_expand_prepare", "mla_latent_expand_prepared",
@@ -100,6 +103,15 @@ _SIGS = {
                                 _vp, _vp]),
     "mla_page8_compact": (_i32, [_cfgp, _vp, _vp, _vp, _i64, _vp, _i32, _vp, _vp, _i32, _i32, _vp,
                                  _i32, _vp, _vp]),
+    "mla_tree_plan": (_i32, [_cfgp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i64, _i32, _vp, _vp, _vp,
+                             _vp, _vp]),
+    "mla_tree_decode_workspace_size": (_sz, [_cfgp, _i64, _i32]),
+    "mla_tree_decode": (_i32, [_cfgp, _vp, _vp, _i64, _vp, _i32, _vp, _vp, _i32, _i64, _vp, _i32, _vp,
+                               _vp, _sz, _vp, _vp]),
+    "mla_tree_verify": (_i32, [_vp, _vp, _i32, _vp, _vp, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _i32,
+                               _vp, _vp, _vp]),
+    "mla_tree_commit": (_i32, [_cfgp, _vp, _i32, _i64, _i32, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _i32,
+                               _vp, _vp, _vp]),
     "mla_naive_workspace_size": (_sz, [_cfgp, _i64, _i32, _i64]),
     "mla_naive_cache_write": (_i32, [_cfgp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _i64,
                                      _vp, _sz, _vp]),
@@ -438,6 +450,76 @@ def mla_page8_compact(cfg: MlaConfig, cache8, page_scales, mass, block_table, ke
     _check(load().mla_page8_compact(
         ctypes.byref(cfg), p_cache, p_scales, p_mass, nb, p_bt, mb, p_keep, p_new, b, budget, p_dst,
         dmb, _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)), "mla_page8_compact")
+
+
+def mla_tree_plan(cfg: MlaConfig, parents, seq_lens, query_start_loc, block_table, num_blocks: int,
+                  tree_mask, positions, slots, dev_status=None, stream=None) -> None:
+    """tree_mask [num_q, words] holds its 64-bit words as int64."""
+    n, b, mb, words, i32 = parents.shape[0], seq_lens.shape[0], block_table.shape[1], tree_mask.shape[1], torch.int32
+    p_par, p_lens, p_qsl, p_bt, p_mask, p_pos, p_slots = _ptrs(
+        (parents, i32, (n,), "parents"), (seq_lens, i32, (b,), "seq_lens"),
+        (query_start_loc, i32, (b + 1,), "query_start_loc"), (block_table, i32, (b, mb), "block_table"),
+        (tree_mask, torch.int64, (n, words), "tree_mask"), (positions, i32, (n,), "positions"),
+        (slots, torch.int64, (n,), "slots"))
+    _check(load().mla_tree_plan(
+        ctypes.byref(cfg), p_par, p_lens, p_qsl, p_bt, mb, num_blocks, b, n, words, p_mask, p_pos,
+        p_slots, _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)), "mla_tree_plan")
+
+
+def mla_tree_decode_workspace_size(cfg: MlaConfig, num_q: int, batch: int) -> int:
+    return int(load().mla_tree_decode_workspace_size(ctypes.byref(cfg), num_q, batch))
+
+
+def mla_tree_decode(cfg: MlaConfig, q_abs, cache, block_table, seq_lens, query_start_loc, tree_mask,
+                    W_uv, workspace, out, stream=None) -> None:
+    nb, n, b, H = cache.shape[0], q_abs.shape[0], seq_lens.shape[0], cfg.num_heads
+    mb, words, bf, i32 = block_table.shape[1], tree_mask.shape[1], torch.bfloat16, torch.int32
+    p_cache, p_q, p_bt, p_lens, p_qsl, p_mask, p_w, p_out = _ptrs(
+        (cache, bf, (nb, cfg.block_size, 576), "cache"), (q_abs, bf, (n, H, 576), "q_abs"),
+        (block_table, i32, (b, mb), "block_table"), (seq_lens, i32, (b,), "seq_lens"),
+        (query_start_loc, i32, (b + 1,), "query_start_loc"),
+        (tree_mask, torch.int64, (n, words), "tree_mask"), (W_uv, bf, (H, 512, 128), "W_uv"),
+        (out, bf, (n, H, 128), "out"))
+    _check(load().mla_tree_decode(
+        ctypes.byref(cfg), p_q, p_cache, nb, p_bt, mb, p_lens, p_qsl, b, n, p_mask, words, p_w,
+        _ptr(workspace, None, "workspace"), _nbytes(workspace), p_out, _stream(stream)),
+        "mla_tree_decode")
+
+
+def mla_tree_verify(target_probs, draft_probs, tokens, parents, query_start_loc, uniforms,
+                    final_uniforms, path, path_lens, next_tokens, dev_status=None, stream=None) -> None:
+    """draft_probs may be None (tokens that were chosen, not drawn)."""
+    (n, v), b, mp = target_probs.shape, final_uniforms.shape[0], path.shape[1]
+    f32, i32 = torch.float32, torch.int32
+    p_p, p_q, p_tok, p_par, p_qsl, p_u, p_f, p_path, p_lens, p_next = _ptrs(
+        (target_probs, f32, (n, v), "target_probs"), (draft_probs, f32, (n, v), "draft_probs"),
+        (tokens, i32, (n,), "tokens"), (parents, i32, (n,), "parents"),
+        (query_start_loc, i32, (b + 1,), "query_start_loc"), (uniforms, f32, (n,), "uniforms"),
+        (final_uniforms, f32, (b,), "final_uniforms"), (path, i32, (b, mp), "path"),
+        (path_lens, i32, (b,), "path_lens"), (next_tokens, i32, (b,), "next_tokens"))
+    _check(load().mla_tree_verify(
+        p_p, p_q, v, p_tok, p_par, p_qsl, b, n, p_u, p_f, p_path, p_lens, mp, p_next,
+        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)), "mla_tree_verify")
+
+
+def mla_tree_commit(cfg: MlaConfig, cache, block_table, seq_lens, query_start_loc, path, path_lens,
+                    new_lens, dev_status=None, stream=None) -> None:
+    """cache [num_layers, num_blocks, block_size, columns], or one layer's: rows of
+    576 values in the configuration's dtype, or 640 bytes (uint8)."""
+    layers = cache.shape[0] if cache.dim() == 4 else 1
+    nb, bs, cols = cache.shape[-3:]
+    b, mb, mp, i32 = seq_lens.shape[0], block_table.shape[1], path.shape[1], torch.int32
+    dt = torch.uint8 if cache.dtype == torch.uint8 else _torch_dtype(cfg)
+    want = (cfg.block_size, 640 if dt == torch.uint8 else 576)
+    p_cache, p_bt, p_lens, p_qsl, p_path, p_n, p_new = _ptrs(
+        (cache, dt, ((layers, nb) if cache.dim() == 4 else (nb,)) + want, "cache"),
+        (block_table, i32, (b, mb), "block_table"), (seq_lens, i32, (b,), "seq_lens"),
+        (query_start_loc, i32, (b + 1,), "query_start_loc"), (path, i32, (b, mp), "path"),
+        (path_lens, i32, (b,), "path_lens"), (new_lens, i32, (b,), "new_lens"))
+    _check(load().mla_tree_commit(
+        ctypes.byref(cfg), p_cache, layers, nb, cols * cache.element_size(), p_bt, mb, p_lens, p_qsl, b,
+        p_path, p_n, mp, p_new, _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)),
+        "mla_tree_commit")
 
 
 def mla_naive_cache_write(cfg: MlaConfig, c_kv, k_pe, positions, slot_mapping, rms_weight, W_uk,

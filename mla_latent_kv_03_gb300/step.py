@@ -265,6 +265,66 @@ class MlaDecodeStep:
                 self.p8_pos = self.pos_new.clone()
         return keep, lens
 
+    # -- a speculative step over trees of drafted tokens ----------------------
+    def tree_setup(self, parents, mask_words: Optional[int] = None) -> None:
+        """The workload's new rows as trees: parents [num_q] (within a sequence,
+        -1 for a root). seq_lens already counts them."""
+        w, dev = self.w, self.device
+        most = int(w.q_lens.max()) if len(w.q_lens) else 0
+        words = max(1, -(-most // 64)) if mask_words is None else mask_words
+        self.tr_parents = _dev(np.asarray(parents), torch.int32, dev)
+        self.tr_mask = torch.zeros((w.num_q, words), dtype=torch.int64, device=dev)
+        self.tr_positions = torch.zeros(w.num_q, dtype=torch.int32, device=dev)
+        self.tr_slots = torch.zeros(w.num_q, dtype=torch.int64, device=dev)
+        self.tr_lens = self.seq_lens.clone()   # with the step's trees
+        self.tr_new_lens = torch.zeros_like(self.tr_lens)
+        self.tr_q_lens = _dev(w.q_lens, torch.int32, dev)
+        need = L.mla_tree_decode_workspace_size(self.cfg, w.num_q, w.batch)
+        if need == 0:
+            raise L.MlaError(L.MLA_OK + 2, "mla_tree_decode_workspace_size")
+        self.tr_ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        L.mla_workspace_init(self.tr_ws)
+
+    def tree_plan(self, stream=None) -> None:
+        """Masks, positions and slots of the step's trees."""
+        L.mla_tree_plan(self.cfg, self.tr_parents, self.tr_lens, self.query_start_loc, self.block_table,
+                        self.cache.shape[0], self.tr_mask, self.tr_positions, self.tr_slots,
+                        dev_status=self.status, stream=stream)
+
+    def tree_step(self, stream=None) -> torch.Tensor:
+        """One layer of the step: plan, the rows' latents written, their queries
+        absorbed, attention and output projection."""
+        self.tree_plan(stream)
+        L.mla_cache_write(self.cfg, self.c_kv_new, self.k_pe_new, self.tr_positions, self.tr_slots,
+                          self.rms_weight, self.cache, self.status, stream=stream)
+        L.mla_absorb_q(self.cfg, self.q_nope, self.q_pe, self.tr_positions, self.W_uk, self.q_abs,
+                       stream=stream)
+        return self.tree_decode(stream)
+
+    def tree_decode(self, stream=None) -> torch.Tensor:
+        L.mla_tree_decode(self.cfg, self.q_abs, self.cache, self.block_table, self.tr_lens,
+                          self.query_start_loc, self.tr_mask, self.W_uv, self.tr_ws, self.out,
+                          stream=stream)
+        return self.out
+
+    def tree_accept(self, target_probs, draft_probs, tokens, uniforms, final_uniforms, max_path: int,
+                    caches=None, stream=None):
+        """Verify the step's trees and move the kept rows behind the past, in this
+        layer's cache or in `caches` [layers, blocks, block_size, 576]. The lengths
+        go on to the next step's, whose trees are as large. Returns (path, its
+        lengths, the next tokens)."""
+        with torch.cuda.stream(self._page8_stream(stream)):  # memory of the stream that writes it
+            path = torch.empty((self.w.batch, max_path), dtype=torch.int32, device=self.device)
+            lens = torch.empty(self.w.batch, dtype=torch.int32, device=self.device)
+            nxt = torch.empty(self.w.batch, dtype=torch.int32, device=self.device)
+            L.mla_tree_verify(target_probs, draft_probs, tokens, self.tr_parents, self.query_start_loc,
+                              uniforms, final_uniforms, path, lens, nxt, dev_status=self.status)
+            L.mla_tree_commit(self.cfg, self.cache if caches is None else caches, self.block_table,
+                              self.tr_lens, self.query_start_loc, path, lens, self.tr_new_lens,
+                              dev_status=self.status)
+            torch.add(self.tr_new_lens, self.tr_q_lens, out=self.tr_lens)
+        return path, lens, nxt
+
     # -- the projections either side (the whole attention layer) -----------
     def layer_setup(self, hidden_size: int = 2048, seed: int = 7) -> None:
         """Hidden states of every token and the q_proj / kv_a_proj / o_proj
