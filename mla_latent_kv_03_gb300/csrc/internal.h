@@ -138,6 +138,9 @@ bool encode_map_2d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t r
 // `nslab` column blocks of box_rows rows, slab by slab (make_slab_map in libmla.cu).
 bool encode_slab_map(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows,
                      uint32_t nslab);
+// 2-D map over 576-value rows whose boxes hold 32 columns (64 bytes) of box_rows
+// rows with the 64-byte swizzle.
+bool encode_rope_half_map(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows);
 // 3-D map over (d, head, row) of a [rows, heads, dims] bf16 tensor: box =
 // (box_d, 1, box_rows), 128-byte swizzle.
 bool encode_map_heads(CUtensorMap* map, const void* base, uint64_t dims, uint64_t heads,

@@ -249,6 +249,17 @@ bool encode_map_2d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t r
                    uint32_t box_cols, uint32_t box_rows) {
   return make_map_2d(map, base, cols, rows, box_cols, box_rows);
 }
+bool encode_rope_half_map(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)kRow, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)kRow * 2};
+  const cuuint32_t box[2] = {32, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 bool encode_slab_map(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows,
                      uint32_t nslab) {
   return make_slab_map(map, base, rows, box_rows, nslab);

@@ -10,8 +10,8 @@ namespace tc {
 
 // Shared-memory matrix descriptor: start address, leading / stride byte
 // offsets (16-byte units), descriptor version 1, swizzle layout
-// (2 = 128-byte swizzle).
-constexpr uint32_t kSwizzle128 = 2;
+// (2 = 128-byte swizzle, 4 = 64-byte swizzle).
+constexpr uint32_t kSwizzle128 = 2, kSwizzle64 = 4;
 
 __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo,
                                               uint32_t layout) {

@@ -12,8 +12,8 @@
 // Where a sequence has several q-blocks its tokens are taken in strips as long
 // as a share, and the q-blocks follow one another within a strip: neighbouring
 // clusters then read the same tokens at the same time, which come from HBM once.
-// CTA h of a pair owns latent columns [256 h, 256 h + 256) of the cache, and CTA
-// 1 the rope columns too:
+// CTA h of a pair owns latent columns [256 h, 256 h + 256) of the cache, and half
+// of the rope columns, [512 + 32 h, 512 + 32 h + 32):
 //   S_h = Q[:, cols_h] K[:, cols_h]^T    (partial scores, in TMEM, fp32)
 //   S   = S_h + the peer's partial       (sent as f16 into this CTA's shared memory)
 //   O_h += P V[:, cols_h]                (this CTA's half of the output)
@@ -27,23 +27,26 @@
 // type); the sum adds the rounded weights, so that a row with one large weight
 // loses nothing.
 //
-// TMEM (512 columns): O [0, 256), two score buffers of 64 columns, whose first
-// half takes the weights (bf16 pairs) once the scores are read, and the
-// query's 256 latent columns (bf16 pairs) [384, 512). CTA 1's rope columns of
-// the query lie in shared memory. Shared memory: four stages of 64 tokens,
-// three buffers of the peer's scores.
+// TMEM (512 columns): O [0, 256), two score buffers of 64 columns, and the
+// query's 256 latent columns (bf16 pairs) [384, 512). Its 32 rope columns lie in
+// shared memory, with four stages of 64 tokens, two buffers of the peer's scores
+// and two of weights.
 // Per CTA (384 threads):
-//   warp 0      copies the cache stages (TMA, SWIZZLE_128B); block ids are checked
+//   warp 0      copies the cache stages (TMA, SWIZZLE_128B; rope SWIZZLE_64B);
+//               block ids are checked
 //   warp 1      issues O += P V of a tile; owns the TMEM
-//   warp 2      issues the scores of a tile
-//   warps 8-11  send a tile's partial scores to the peer
-//   warps 4-7   softmax, a thread a row; at a segment's end they write the
-//               normalised rows and log-sum-exps of it
+//   warp 2      issues the scores of a tile, up to two tiles ahead of its weights
+//   warp 3      waits for all that a tile's softmax needs and says so in one word
+//               (a poll of an mbarrier takes some 125 cycles, ready or not; the
+//               softmax would spend a fifth of its time on four of them a tile)
+//   warps 4-7   softmax, a thread a row
+//   warps 8-11  send the partial scores to the peer, and load the next segment's
+//               query once the last scores are there
+//   At a segment's end warps 4-11 write its normalised rows, half of the columns
+//   each, and its log-sum-exps.
 // Every wait is bounded; on a timeout the roles leave their loops, the issuers
 // wait for their products and the copies' warp for its copies before TMEM is
 // freed, and the pair meets at a last barrier.
-#include <cuda_fp16.h>
-
 #include "async_copy.cuh"
 #include "cluster.cuh"
 #include "common.cuh"
@@ -57,13 +60,14 @@ namespace {
 constexpr int kBlockRows = 128;
 constexpr int kTok = 64;
 constexpr int kSlab = kTok * 128;              // 64 rows of 64 bf16 columns
-constexpr int kMaxSlabs = 5;
-constexpr int kStage = kMaxSlabs * kSlab;      // 40 KB
+constexpr int kRope = kTok * 64;               // 64 rows of 32 rope columns
+constexpr int kStage = 4 * kSlab + kRope;      // 36 KB
 constexpr int kStages = 4;
-constexpr int kXBufs = 3;
 constexpr int kXBytes = kBlockRows * kTok * 2; // 16 KB: [8 chunks][128 rows][16 bytes]
+constexpr int kPBytes = kBlockRows * 128;      // 16 KB: weights, SWIZZLE_128B
 constexpr int kThreads = 384;
 constexpr int kSoftWarp0 = 4, kSendWarp0 = 8;
+constexpr int kQStage = 2048;                  // a sender warp's staging of query columns: 32 rows of 64 bytes
 constexpr uint32_t kOCol = 0, kSCol = 256, kQCol = 384, kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.f;
 constexpr int kTreeMaxRows = 48 * 1024;
@@ -72,15 +76,15 @@ enum {
   kFull0 = 0,
   kEmpty0 = kFull0 + kStages,
   kSFull0 = kEmpty0 + kStages,   // [2] partial scores of tile i in S[i % 2]
-  kSRead0 = kSFull0 + 2,         // [2] S[i % 2] read by the senders (4 arrivals)
-  kPFull0 = kSRead0 + 2,         // [2] weights of tile i in S[i % 2] (128 arrivals)
+  kSRead0 = kSFull0 + 2,         // [2] S[i % 2] read (8 warps)
+  kPFull0 = kSRead0 + 2,         // [2] weights of tile i in P[i % 2] (4 warps)
   kPVDone0 = kPFull0 + 2,        // [2] O += P V of tile i done
-  kXFull0 = kPVDone0 + 2,        // [kXBufs] the peer's scores of tile i (bytes from the peer)
-  kPeerFree0 = kXFull0 + kXBufs, // [kXBufs] the peer has read its buffer (4 remote arrivals)
-  kQReady = kPeerFree0 + kXBufs, // query columns in place (128 arrivals)
-  kQEmpty,                       // every score product of the segment done
+  kXFull0 = kPVDone0 + 2,        // [2] the peer's scores of tile i (bytes from the peer)
+  kPeerFree0 = kXFull0 + 2,      // [2] the peer has read its buffer (4 warps of the peer)
+  kQReady = kPeerFree0 + 2,      // query columns in place (4 warps)
+  kSums,                         // the segment's weight sums in shared memory (4 warps)
   kODone,                        // every output product of the segment done
-  kOFree,                        // O read out (128 arrivals)
+  kOFree,                        // O read out, staging free (8 warps)
   kFinalS,
   kFinalP,
   kNumBars
@@ -89,16 +93,21 @@ enum {
 struct Smem {
   static constexpr int stage = 0;
   static constexpr int x = stage + kStages * kStage;
-  static constexpr int rope = x + kXBufs * kXBytes;       // [128 rows][64 columns], SWIZZLE_128B
-  static constexpr int info = rope + kBlockRows * 128;    // [kStages] int2
+  static constexpr int p = x + 2 * kXBytes;
+  static constexpr int rope = p + 2 * kPBytes;            // [128 rows][32 columns], SWIZZLE_64B
+  static constexpr int qstage = rope + kBlockRows * 64;   // [4 warps]
+  static constexpr int sum = qstage + 4 * kQStage;        // [128] 1 / weight sum
+  static constexpr int info = sum + kBlockRows * 4;   // [kStages] int2
   static constexpr int bars = info + kStages * 8;
-  static constexpr int misc = bars + kNumBars * 8;        // tmem base, abort flag
-  static constexpr int plan = misc + 16;                  // start of this share: int4; scan scratch
+  static constexpr int misc = bars + kNumBars * 8;        // tmem base, abort flag, tiles ready
+  static constexpr int plan = (misc + 12 + 15) / 16 * 16;  // start of this share: int4; scan scratch
   static constexpr int bytes = plan + 16 + 2 * (kThreads / 32) * 4;
   static constexpr int alloc = bytes + 1024;
 };
 static_assert(Smem::alloc <= 227 * 1024, "shared memory budget");
-static_assert(Smem::bars % 8 == 0 && Smem::plan % 16 == 0, "alignment");
+static_assert(Smem::bars % 8 == 0 && Smem::stage % 1024 == 0 && kStage % 1024 == 0 && Smem::p % 1024 == 0 &&
+                  Smem::rope % 1024 == 0,
+              "alignment");
 
 struct TreeArgs {
   const uint16_t* q_abs;
@@ -140,7 +149,7 @@ struct TreeSeq {
   int q0, ql, len, n, m;   // rows [q0, q0 + ql); n tiles, m q-blocks (0: nothing to do)
   bool broken;             // query_start_loc does not ascend here, or leaves [0, num_q]
 };
-__device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, bool report) {
+__device__ __noinline__ TreeSeq tree_seq(const TreeArgs& a, int b, bool report) {
   TreeSeq s;
   s.q0 = a.query_start_loc[b];
   const int q1 = a.query_start_loc[b + 1];
@@ -166,12 +175,15 @@ struct TreeSeg {
   int b, j, k0, k1, item, q0, ql, len;
 };
 
-// Walks the units of one share; every role has its own.
+// Walks the units of one share; every role has its own. (What is done once a
+// segment, and what is done when a wait takes long, is out of line throughout:
+// with its roles' code one behind another the kernel is bound by fetching
+// instructions. Inlined, it was 109 KB and a tile took 3,900 cycles.)
 struct TreeWalk {
   int u, u_end, share, b, ubase, ibase;
   TreeSeq s;
 
-  __device__ __forceinline__ bool next(const TreeArgs& a, TreeSeg& g) {
+  __device__ __noinline__ bool next(const TreeArgs& a, TreeSeg& g) {
     if (u >= u_end) return false;
     while (u >= ubase + s.n * s.m) {
       ubase += s.n * s.m;
@@ -274,8 +286,7 @@ __device__ __forceinline__ bool find_share(const TreeArgs& a, int c, int4* start
   return true;
 }
 
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  if (mbar_try_wait(bar, parity)) return true;
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -285,15 +296,54 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, vo
     }
   }
 }
+// By whole warps: try_wait suspends a converged warp until the phase completes and
+// wakes it within 82 cycles; with one lane polling for the others it took 190.
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return mbar_try_wait(bar, parity) || mbar_try_wait(bar, parity) || mbar_try_wait(bar, parity) ||
+         wait_long(bar, parity, abort_flag);
+}
 
-__device__ __forceinline__ uint32_t pack_f16_sat(float lo, float hi) {
+// Waits until *word > i; false on a timeout or another role's.
+__device__ __forceinline__ bool word_passed(const int* word, int i) {
+  int x;
+  asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(x) : "r"(smem_u32(word)) : "memory");
+  return x > i;
+}
+__device__ __noinline__ bool word_long(const int* word, int i, volatile int* abort_flag) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t n = 1;; ++n) {
+    if (word_passed(word, i)) return true;
+    if ((n & 63u) == 0) {
+      if (*abort_flag) return false;
+      if (globaltimer_ns() - t0 > kWaitTimeoutNs) return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait_word(const int* word, int i, volatile int* abort_flag) {
+  return word_passed(word, i) || word_long(word, i, abort_flag);
+}
+
+// Two scores as an f16 pair, saturating; an infinite one is passed on as NaN
+// (saturated, it would be a large one).
+__device__ __forceinline__ uint32_t pack_score(uint32_t lo, uint32_t hi) {
+  const float2 x = make_float2(__uint_as_float(lo), __uint_as_float(hi));
+  const float2 y = fma_f32x2(x, make_float2(0.f, 0.f), x);
   uint32_t r;
-  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y.y), "f"(y.x));
   return r;
 }
-// An infinite score is passed on as NaN: saturated, it would be a large one.
-__device__ __forceinline__ float finite_or_nan(uint32_t x) {
-  return fmaf(__uint_as_float(x), 0.f, __uint_as_float(x));
+// lo += the pair's low f16, hi += its high one, in fp32.
+__device__ __forceinline__ void add_f16x2(uint32_t pair, float& lo, float& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "add.rn.f32.f16 %0, l, %0;\n\tadd.rn.f32.f16 %1, h, %1;\n\t}"
+      : "+f"(lo), "+f"(hi)
+      : "r"(pair));
+}
+__device__ __forceinline__ void add_bf16x2(uint32_t pair, float& lo, float& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "add.rn.f32.bf16 %0, l, %0;\n\tadd.rn.f32.bf16 %1, h, %1;\n\t}"
+      : "+f"(lo), "+f"(hi)
+      : "r"(pair));
 }
 // 16 bytes into the peer's shared memory, counted on its barrier.
 __device__ __forceinline__ void send16(uint32_t dst, uint32_t bar, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -302,40 +352,118 @@ __device__ __forceinline__ void send16(uint32_t dst, uint32_t bar, uint32_t a, u
       "r"(bar), "r"(a), "r"(b), "r"(c), "r"(d)
       : "memory");
 }
-// This CTA's columns of query row `qrow` (of all (row, head)s): 256 latent ones
-// into TMEM lane r, CTA 1's 64 rope ones into shared memory.
-__device__ __forceinline__ void load_query(const TreeArgs& a, int h, int64_t qrow, bool live, uint32_t trow, uint8_t* rope,
-                                           int r) {
-  const uint4* src = reinterpret_cast<const uint4*>(a.q_abs + (size_t)qrow * kRow + 256 * h);
+// Byte offset of 16-byte chunk `chunk` of row `row` in a tile of 64-byte rows with
+// the 64-byte swizzle (chunk XOR (row / 2) mod 4).
+__device__ __forceinline__ uint32_t sw64(int row, int chunk) {
+  return static_cast<uint32_t>(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
+}
+
+// Uses of loaded registers stay behind the wait for the loads.
+__device__ __forceinline__ void loaded(uint32_t (&r)[32]) {
+#pragma unroll
+  for (int k = 0; k < 32; k += 16)
+    asm volatile("" : "+r"(r[k]), "+r"(r[k + 1]), "+r"(r[k + 2]), "+r"(r[k + 3]), "+r"(r[k + 4]), "+r"(r[k + 5]),
+                 "+r"(r[k + 6]), "+r"(r[k + 7]), "+r"(r[k + 8]), "+r"(r[k + 9]), "+r"(r[k + 10]), "+r"(r[k + 11]),
+                 "+r"(r[k + 12]), "+r"(r[k + 13]), "+r"(r[k + 14]), "+r"(r[k + 15]));
+}
+
+// A sender warp's part of a q-block's query, 32 rows: this CTA's 256 latent columns
+// into TMEM, its 32 rope columns into shared memory. Fetched by 64 bytes of a row
+// to 4 lanes, and handed to the lanes of their rows through `stage`.
+__device__ __noinline__ void load_query(const TreeArgs& a, const TreeSeg& g, int h, int row0, int lane, uint32_t trow,
+                                           uint8_t* stage, uint8_t* rope_rows) {
+  const int rows = g.ql * a.num_heads, first = g.j * kBlockRows + row0;
+  const uint4* q = reinterpret_cast<const uint4*>(a.q_abs) + ((int64_t)g.q0 * a.num_heads + first) * (kRow / 8);
   const uint4 zero = make_uint4(0, 0, 0, 0);
+  auto fetch = [&](uint4 (&v)[4], int c) {   // columns [32 c, 32 c + 32) of the row's 256; c = 8: rope
 #pragma unroll
-  for (int hb = 0; hb < 2; ++hb) {
-    uint4 buf[16];
+    for (int u = 0; u < 4; ++u) {
+      const int r = 8 * u + (lane >> 2);
+      v[u] = first + r < rows ? __ldg(q + r * (kRow / 8) + (c < 8 ? 32 * h + 4 * c : 64 + 4 * h) + (lane & 3)) : zero;
+    }
+  };
+#pragma unroll 1
+  for (int c0 = 0; c0 < 9; c0 += 3) {
+    uint4 v[3][4];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) buf[i] = live ? __ldg(src + 16 * hb + i) : zero;
+    for (int c = 0; c < 3; ++c) fetch(v[c], c0 + c);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < 3; ++c) {
+      if (c0 + c == 8) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          *reinterpret_cast<uint4*>(rope_rows + sw64(row0 + 8 * u + (lane >> 2), lane & 3)) = v[c][u];
+        break;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int u = 0; u < 4; ++u) *reinterpret_cast<uint4*>(stage + sw64(8 * u + (lane >> 2), lane & 3)) = v[c][u];
+      __syncwarp();
       uint32_t w[16];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        w[4 * k] = buf[4 * c + k].x;
-        w[4 * k + 1] = buf[4 * c + k].y;
-        w[4 * k + 2] = buf[4 * c + k].z;
-        w[4 * k + 3] = buf[4 * c + k].w;
+      for (int u = 0; u < 4; ++u) {
+        const uint4 y = *reinterpret_cast<const uint4*>(stage + sw64(lane, u));
+        w[4 * u] = y.x;
+        w[4 * u + 1] = y.y;
+        w[4 * u + 2] = y.z;
+        w[4 * u + 3] = y.w;
       }
-      tc::st16(trow + kQCol + 64 * hb + 16 * c, w);
+      tc::st16(trow + kQCol + 16 * (c0 + c), w);
     }
   }
-  if (h == 1) {
+  fence_proxy_async_smem();
+  tc::wait_st();
+}
+
+// The normalised columns [128 part, 128 part + 128) of this CTA's half of a
+// segment's O, 32 rows, to `dst`, by whole 128-byte lines through `stage` (4 KB).
+__device__ __noinline__ void store_rows(uint32_t trow, int part, float inv, int rows, float* dst, uint8_t* stage, int lane) {
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t o[32];
+    tc::ld32(trow + kOCol + 128 * part + 32 * c, o);
+    tc::wait_ld();
+    loaded(o);
+    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      *reinterpret_cast<uint4*>(rope + sw128(r, i)) = live ? __ldg(src + 32 + i) : zero;
-    fence_proxy_async_smem();
+    for (int k = 0; k < 8; ++k)
+      *reinterpret_cast<float4*>(stage + sw128(lane, k)) =
+          make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv,
+                      __uint_as_float(o[4 * k + 2]) * inv, __uint_as_float(o[4 * k + 3]) * inv);
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int r = 4 * u + (lane >> 3);
+      const float4 y = *reinterpret_cast<const float4*>(stage + sw128(r, lane & 7));
+      if (r < rows) *reinterpret_cast<float4*>(dst + (size_t)r * kDc + 128 * part + 32 * c + 4 * (lane & 7)) = y;
+    }
+  }
+  tc::fence_before_sync();
+}
+
+// Rows of a stage that are not there may hold anything: zero, so that a weight of
+// 0 stays 0. So do the tree's tokens that are not finite, for the rows that do
+// not see them. Two slabs (128 columns) of row `tok`.
+__device__ __noinline__ void clean_stage(uint8_t* stg, int tok, bool there, bool of_tree) {
+  bool zero = !there;
+  if (there && of_tree) {
+    uint32_t most = 0;   // the largest exponent and fraction of the low and of the high values
+#pragma unroll 4
+    for (int c = 0; c < 16; ++c) {
+      const uint4 y = *reinterpret_cast<const uint4*>(stg + (c >> 3) * kSlab + sw128(tok, c & 7));
+      most = __vmaxu2(__vmaxu2(most, y.x & 0x7fff7fffu), __vmaxu2(y.y & 0x7fff7fffu, __vmaxu2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu)));
+    }
+    zero = (most & 0xffffu) >= 0x7f80u || (most >> 16) >= 0x7f80u;
+  }
+  if (zero) {
+#pragma unroll 4
+    for (int c = 0; c < 16; ++c)
+      *reinterpret_cast<uint4*>(stg + (c >> 3) * kSlab + sw128(tok, c & 7)) = make_uint4(0, 0, 0, 0);
   }
 }
 
 // Bit i: row `j0 + i` of the tree is in the mask (words of 64, `words` of them).
-__device__ __forceinline__ uint64_t mask_from(const uint64_t* m, int words, int j0) {
+__device__ __noinline__ uint64_t mask_from(const uint64_t* m, int words, int j0) {
   const int w = j0 >> 6, sh = j0 & 63;
   uint64_t x = w < words ? __ldg(m + w) >> sh : 0;
   if (sh && w + 1 < words) x |= __ldg(m + w + 1) << (64 - sh);
@@ -344,7 +472,7 @@ __device__ __forceinline__ uint64_t mask_from(const uint64_t* m, int words, int 
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tree_decode_kernel(const __grid_constant__ CUtensorMap cache_map, const __grid_constant__ CUtensorMap slab4,
-                       const __grid_constant__ CUtensorMap slab5, const __grid_constant__ TreeArgs a) {
+                       const __grid_constant__ CUtensorMap rope_map, const __grid_constant__ TreeArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
@@ -352,29 +480,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   int2* info = reinterpret_cast<int2*>(sm + Smem::info);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Smem::misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Smem::misc + 4);
+  int* ready = reinterpret_cast<int*>(sm + Smem::misc + 8);   // tiles whose softmax may begin
   uint8_t* sStage = sm + Smem::stage;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = (int)cl::rank();
   const int share_idx = blockIdx.x >> 1;
-  const int slab0 = 4 * h, nslab = 4 + h;
   const int bs = a.block_size, bs_shift = bs == 16 ? 4 : bs == 32 ? 5 : 6;
   const int pages = kTok / bs;                      // of a stage
   const int full_mask = (1 << pages) - 1;
 
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
-      const bool all = (i >= kPFull0 && i < kPFull0 + 2) || i == kQReady || i == kOFree;
-      const bool warps = (i >= kSRead0 && i < kSRead0 + 2) || (i >= kPeerFree0 && i < kPeerFree0 + kXBufs);
-      mbar_init(&bars[i], all ? 128 : warps ? 4 : 1);
+      const bool eight = i == kSRead0 || i == kSRead0 + 1 || i == kOFree;
+      const bool four = (i >= kPFull0 && i < kPVDone0) || (i >= kPeerFree0 && i <= kSums);
+      mbar_init(&bars[i], eight ? 8 : four ? 4 : 1);
     }
-    for (int i = 0; i < kXBufs; ++i) mbar_arrive_expect_tx(&bars[kXFull0 + i], kXBytes);
+    for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&bars[kXFull0 + i], kXBytes);
     *abort_flag = 0;
+    *ready = 0;
     fence_mbar_init();
   }
   if (warp == 1) tc::alloc(tmem_slot, kTmemCols);
   if (warp == 0 && lane == 0) {
-    prefetch_tensormap(&cache_map);
-    prefetch_tensormap(h ? &slab5 : &slab4);
+    prefetch_tensormap(bs == kTok ? &slab4 : &cache_map);
+    prefetch_tensormap(&rope_map);
   }
   tc::fence_before_sync();
   cl::sync();  // both CTAs' barriers exist before either sends
@@ -388,7 +517,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const bool has_work = find_share(a, share_idx, reinterpret_cast<int4*>(sm + Smem::plan), scratch, tid, sw);
   TreeSeg seg;
   auto warp_wait = [&](int bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait_or_abort(&bars[bar], parity, abort_flag));
+    const bool ok = wait_or_abort(&bars[bar], parity, abort_flag);   // (the same for all lanes)
+    __syncwarp();
+    return ok;
   };
   auto fail_out = [&]() {
     set_status(a.status, MLA_DEV_TIMEOUT);
@@ -415,33 +546,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        // lane l: page l / nslab of the stage, slab l % nslab (64-token pages:
-        // one copy of all slabs)
-        const int pg = bs == kTok ? 0 : lane / nslab, sl = lane % nslab;
+        // lane l: of page l / 5 of the stage, slab l % 5 (4: the rope columns);
+        // of a 64-token page one copy of all four slabs
+        const int pg = lane / 5, sl = lane % 5;
         const int blk = __shfl_sync(0xffffffffu, cached, min(p0 - cache_base + pg, 31));
         const bool wanted = pg < pages && (pg << bs_shift) < v;
         const bool there = wanted && blk >= 0 && blk < a.num_blocks;
         if (wanted && !there && sl == 0) set_status(a.status, MLA_DEV_BAD_BLOCK);
         const uint32_t loads = __ballot_sync(0xffffffffu, there);
+        uint64_t* full = &bars[kFull0 + slot];
         uint8_t* dst = sStage + slot * kStage;
-        if (bs == kTok) {
-          if (lane == 0) {
-            info[slot] = make_int2(v, there);
-            mbar_arrive_expect_tx(&bars[kFull0 + slot], there ? nslab * kSlab : 0);
-            if (there)
-              tma_load_3d_hint(dst, h ? &slab5 : &slab4, 0, blk * bs, slab0, &bars[kFull0 + slot], policy);
-          }
-        } else {
-          if (lane == 0) {
-            int okmask = 0;
-            for (int p = 0; p < pages; ++p) okmask |= ((loads >> (p * nslab)) & 1) << p;
-            info[slot] = make_int2(v, okmask);
-            mbar_arrive_expect_tx(&bars[kFull0 + slot], __popc(loads) * bs * 128);
-          }
-          __syncwarp();
-          if (there)
-            tma_load_2d_hint(dst + sl * kSlab + (pg << bs_shift) * 128, &cache_map, 64 * (slab0 + sl), blk * bs,
-                             &bars[kFull0 + slot], policy);
+        if (lane == 0) {
+          int okmask = 0;
+          for (int p = 0; p < pages; ++p) okmask |= ((loads >> (p * 5)) & 1) << p;
+          info[slot] = make_int2(v, okmask);
+          mbar_arrive_expect_tx(full, __popc(okmask) * bs * (4 * 128 + 64));
+        }
+        __syncwarp();
+        if (there) {
+          if (sl == 4)
+            tma_load_2d_hint(dst + 4 * kSlab + (pg << bs_shift) * 64, &rope_map, kDc + 32 * h, blk * bs, full, policy);
+          else if (bs != kTok)
+            tma_load_2d_hint(dst + sl * kSlab + (pg << bs_shift) * 128, &cache_map, 256 * h + 64 * sl, blk * bs, full,
+                             policy);
+          else if (sl == 0)
+            tma_load_3d_hint(dst, &slab4, 0, blk * bs, 4 * h, full, policy);
         }
         __syncwarp();
       }
@@ -458,6 +587,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------- output products
     constexpr uint32_t kIdO = tc::idesc_bf16(128, 256, false, true);
     const uint64_t vdesc = tc::smem_desc(smem_u32(sStage), kSlab, 1024, tc::kSwizzle128);
+    const uint64_t pdesc = tc::smem_desc(smem_u32(sm + Smem::p), 16, 1024, tc::kSwizzle128);
     const bool leader = tc::elect_one();
     int i = 0, seg_i = 0;
     bool ok = true;
@@ -472,8 +602,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (leader) {
 #pragma unroll
           for (int ks = 0; ks < kTok / 16; ++ks)
-            tc::mma_bf16_tmem_a(tmem + kOCol, tmem + kSCol + (uint32_t)(b * kTok + ks * 8),
-                                vdesc + (uint64_t)((slot * kStage + ks * 16 * 128) >> 4), kIdO, t > 0 || ks > 0);
+            tc::mma_bf16(tmem + kOCol, pdesc + (uint64_t)((b * kPBytes + ks * 32) >> 4),
+                         vdesc + (uint64_t)((slot * kStage + ks * 16 * 128) >> 4), kIdO, t > 0 || ks > 0);
           tc::commit(&bars[kEmpty0 + slot]);
           tc::commit(&bars[kPVDone0 + b]);
         }
@@ -493,7 +623,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------- scores
     constexpr uint32_t kIdS = tc::idesc_bf16(128, kTok, false, false);
     const uint64_t kdesc = tc::smem_desc(smem_u32(sStage), 16, 1024, tc::kSwizzle128);
-    const uint64_t rdesc = tc::smem_desc(smem_u32(sm + Smem::rope), 16, 1024, tc::kSwizzle128);
+    const uint64_t krdesc = tc::smem_desc(smem_u32(sStage + 4 * kSlab), 16, 512, tc::kSwizzle64);
+    const uint64_t qrdesc = tc::smem_desc(smem_u32(sm + Smem::rope), 16, 512, tc::kSwizzle64);
     const bool leader = tc::elect_one();
     int i = 0, seg_i = 0;
     bool ok = true;
@@ -503,29 +634,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int t = 0; t < n; ++t, ++i) {
         const int slot = i % kStages, b = i & 1;
-        // the weights of tile i - 2 in this buffer have been used
-        if (i >= 2 && !warp_wait(kPVDone0 + b, ((i - 2) >> 1) & 1)) { ok = false; break; }
+        if (i >= 2 && !warp_wait(kSRead0 + b, ((i - 2) >> 1) & 1)) { ok = false; break; }
         if (!warp_wait(kFull0 + slot, (i / kStages) & 1)) { ok = false; break; }
         tc::fence_after_sync();
         if (leader) {
           const uint32_t d = tmem + kSCol + (uint32_t)(b * kTok);
-          const uint64_t kd = kdesc + (uint64_t)((slot * kStage) >> 4);
+          const uint64_t at = (uint64_t)((slot * kStage) >> 4);
 #pragma unroll
           for (int kk = 0; kk < 16; ++kk)
             tc::mma_bf16_tmem_a(d, tmem + kQCol + (uint32_t)(kk * 8),
-                                kd + (uint64_t)(((kk >> 2) * kSlab + (kk & 3) * 32) >> 4), kIdS, kk > 0);
-          if (h == 1) {
+                                kdesc + at + (uint64_t)(((kk >> 2) * kSlab + (kk & 3) * 32) >> 4), kIdS, kk > 0);
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              tc::mma_bf16(d, rdesc + (uint64_t)((c * 32) >> 4), kd + (uint64_t)((4 * kSlab + c * 32) >> 4), kIdS, true);
-          }
+          for (int c = 0; c < 2; ++c)
+            tc::mma_bf16(d, qrdesc + (uint64_t)((c * 32) >> 4), krdesc + at + (uint64_t)((c * 32) >> 4), kIdS, true);
           tc::commit(&bars[kSFull0 + b]);
         }
         __syncwarp();
       }
       if (!ok) break;
-      if (leader) tc::commit(&bars[kQEmpty]);
-      __syncwarp();
       ++seg_i;
     }
     if (!ok && leader) fail_out();
@@ -533,107 +659,141 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (!mbar_wait(&bars[kFinalS], 0) && leader) set_status(a.status, MLA_DEV_TIMEOUT);
     __syncwarp();
-  } else if (has_work && warp >= kSendWarp0) {
-    // ------------------------------------------------------------ senders
-    const int r = tid - kSendWarp0 * 32;
-    const uint32_t trow = tmem + ((uint32_t)((warp - kSendWarp0) * 32) << 16);
-    const uint32_t peer = (uint32_t)(h ^ 1);
-    const uint32_t x_peer = cl::map(smem_u32(sm + Smem::x), peer) + (uint32_t)r * 16;
-    const uint32_t xbar_peer = cl::map(smem_u32(&bars[kXFull0]), peer);
+  } else if (has_work && warp == 3) {
+    // ---------------------------------------------------- what a tile needs
     int i = 0;
     bool ok = true;
     while (ok && sw.next(a, seg)) {
-      const int n = seg.k1 - seg.k0;
 #pragma unroll 1
-      for (int t = 0; t < n; ++t, ++i) {
-        const int b = i & 1, xb = i % kXBufs;
-        if (!warp_wait(kSFull0 + b, (i >> 1) & 1)) { ok = false; break; }
-        tc::fence_after_sync();
-        uint32_t pk[32];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t sv[32];
-          tc::ld32(trow + kSCol + (uint32_t)(b * kTok + 32 * c), sv);
-          tc::wait_ld();
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            pk[16 * c + k] = pack_f16_sat(finite_or_nan(sv[2 * k]), finite_or_nan(sv[2 * k + 1]));
+      for (int k = seg.k0; k < seg.k1; ++k, ++i) {
+        const int b = i & 1, slot = i % kStages;
+        ok = (i < 2 || warp_wait(kPVDone0 + b, ((i >> 1) - 1) & 1)) &&   // its weights' buffer
+             warp_wait(kFull0 + slot, (i / kStages) & 1) &&              // what is in the stage
+             warp_wait(kSFull0 + b, (i >> 1) & 1) && warp_wait(kXFull0 + b, (i >> 1) & 1);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars[kXFull0 + b], kXBytes);   // for tile i + 2
+          asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(smem_u32(ready)), "r"(i + 1) : "memory");
         }
-        tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kSRead0 + b]);
-        // the peer has read tile i - kXBufs from its buffer
-        if (i >= kXBufs && !warp_wait(kPeerFree0 + xb, ((i / kXBufs) - 1) & 1)) { ok = false; break; }
-        const uint32_t dst = x_peer + (uint32_t)(xb * kXBytes), bar = xbar_peer + (uint32_t)xb * 8;
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          send16(dst + c * (kBlockRows * 16), bar, pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
       }
     }
     if (!ok && lane == 0) fail_out();
-  } else if (has_work && warp >= kSoftWarp0) {
-    // ------------------------------------------------------------ softmax
-    const int r = tid - kSoftWarp0 * 32;
-    const uint32_t trow = tmem + ((uint32_t)((warp - kSoftWarp0) * 32) << 16);
-    const uint32_t pfree_peer = cl::map(smem_u32(&bars[kPeerFree0]), (uint32_t)(h ^ 1));
-    const float scale = a.scale_log2;
+  } else if (has_work && warp >= kSendWarp0) {
+    // ------------------------------------------------------------ senders
+    const int quad = warp - kSendWarp0, r = quad * 32 + lane;
+    const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t peer = (uint32_t)(h ^ 1);
+    const uint32_t x_peer = cl::map(smem_u32(sm + Smem::x), peer) + (uint32_t)r * 16;
+    const uint32_t xbar_peer = cl::map(smem_u32(&bars[kXFull0]), peer);
+    uint8_t* rope = sm + Smem::rope;
+    const float* sSum = reinterpret_cast<const float*>(sm + Smem::sum);
     int i = 0, seg_i = 0;
-    bool fail = false;
+    bool ok = true;
     auto query_in = [&](const TreeSeg& g) {
-      const int qr = g.j * kBlockRows + r;
-      load_query(a, h, (int64_t)g.q0 * a.num_heads + qr, qr < g.ql * a.num_heads, trow, sm + Smem::rope, r);
-      tc::wait_st();
+      load_query(a, g, h, quad * 32, lane, trow, sm + Smem::qstage + quad * kQStage, rope);
       tc::fence_before_sync();
-      mbar_arrive(&bars[kQReady]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kQReady]);
     };
     bool have = sw.next(a, seg);
     if (have) query_in(seg);
-    while (have) {
-      const int n = seg.k1 - seg.k0, past = seg.len - seg.ql;
-      const int qr = seg.j * kBlockRows + r, row = qr / a.num_heads;   // of the sequence
-      const bool live_row = row < seg.ql;
-      const uint64_t* mrow = a.mask + (size_t)(seg.q0 + (live_row ? row : 0)) * a.words;
-      float m_used = -INFINITY, l = 0.f;
+    while (have && ok) {
+      const int n = seg.k1 - seg.k0;
 #pragma unroll 1
       for (int t = 0; t < n; ++t, ++i) {
-        const int slot = i % kStages, b = i & 1, xb = i % kXBufs;
-        fail |= !wait_or_abort(&bars[kSFull0 + b], (i >> 1) & 1, abort_flag);
-        if (__any_sync(0xffffffffu, fail)) { fail = true; break; }
+        const int b = i & 1;
+        // the peer has read tile i - 2 from the buffer
+        if (i >= 2 && !warp_wait(kPeerFree0 + b, ((i >> 1) - 1) & 1)) { ok = false; break; }
+        if (!warp_wait(kSFull0 + b, (i >> 1) & 1)) { ok = false; break; }
         tc::fence_after_sync();
         uint32_t sv[2][32];
         tc::ld32(trow + kSCol + (uint32_t)(b * kTok), sv[0]);
         tc::ld32(trow + kSCol + (uint32_t)(b * kTok + 32), sv[1]);
         tc::wait_ld();
-        fail |= !wait_or_abort(&bars[kXFull0 + xb], (i / kXBufs) & 1, abort_flag);
-        fail |= !wait_or_abort(&bars[kFull0 + slot], (i / kStages) & 1, abort_flag);
-        if (__any_sync(0xffffffffu, fail)) { fail = true; break; }
-        if (r == 0) mbar_arrive_expect_tx(&bars[kXFull0 + xb], kXBytes);   // for tile i + kXBufs
-        float x[64];
-        {
-          const uint8_t* xp = sm + Smem::x + xb * kXBytes + r * 16;
+        loaded(sv[0]);
+        loaded(sv[1]);
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kSRead0 + b]);
+        const uint32_t dst = x_peer + (uint32_t)(b * kXBytes), bar = xbar_peer + (uint32_t)b * 8;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const uint4 pv = *reinterpret_cast<const uint4*>(xp + c * (kBlockRows * 16));
-            const uint32_t w[4] = {pv.x, pv.y, pv.z, pv.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-              const int at = 8 * (c & 3) + 2 * k;
-              x[8 * c + 2 * k] = __uint_as_float(sv[c >> 2][at]) + f.x;
-              x[8 * c + 2 * k + 1] = __uint_as_float(sv[c >> 2][at + 1]) + f.y;
-            }
-          }
+        for (int c = 0; c < 8; ++c) {
+          const uint32_t* v = sv[c >> 2] + 8 * (c & 3);
+          send16(dst + c * (kBlockRows * 16), bar, pack_score(v[0], v[1]), pack_score(v[2], v[3]),
+                 pack_score(v[4], v[5]), pack_score(v[6], v[7]));
         }
+      }
+      if (!ok) break;
+      // every score product of the segment is done: the next query's columns, then
+      // half of this segment's output
+      TreeSeg nxt;
+      const bool more = sw.next(a, nxt);
+      if (more) query_in(nxt);
+      if (!warp_wait(kODone, seg_i & 1) || !warp_wait(kSums, seg_i & 1)) { ok = false; break; }
+      tc::fence_after_sync();
+      store_rows(trow, 1, sSum[r], seg.ql * a.num_heads - seg.j * kBlockRows - quad * 32,
+                 a.opart + (((size_t)share_idx + seg.item) * kBlockRows + quad * 32) * kDc + 256 * h,
+                 sm + Smem::p + (4 + quad) * 4096, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kOFree]);
+      seg = nxt;
+      have = more;
+      ++seg_i;
+    }
+    if (!ok && lane == 0) fail_out();
+  } else if (has_work) {
+    // ------------------------------------------------------------ softmax
+    const int quad = warp - kSoftWarp0, r = quad * 32 + lane;
+    const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t pfree_peer = cl::map(smem_u32(&bars[kPeerFree0]), (uint32_t)(h ^ 1));
+    float* sSum = reinterpret_cast<float*>(sm + Smem::sum);
+    const float scale = a.scale_log2;
+    int i = 0, seg_i = 0;
+    bool ok = true;
+    while (ok && sw.next(a, seg)) {
+      const int n = seg.k1 - seg.k0, past = seg.len - seg.ql;
+      const int row = (seg.j * kBlockRows + r) / a.num_heads;   // of the sequence
+      const bool live_row = row < seg.ql;
+      const uint64_t* mrow = a.mask + (size_t)(seg.q0 + (live_row ? row : 0)) * a.words;
+      float m_used = -INFINITY, l = 0.f;
+#pragma unroll 1
+      for (int t = 0; t < n; ++t, ++i) {
+        const int slot = i % kStages, b = i & 1;
+        if (!wait_word(ready, i, abort_flag)) ok = false;
+        if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
+        tc::fence_after_sync();
+        uint32_t sv[2][32];
+        tc::ld32(trow + kSCol + (uint32_t)(b * kTok), sv[0]);
+        tc::ld32(trow + kSCol + (uint32_t)(b * kTok + 32), sv[1]);
+        const uint8_t* xp = sm + Smem::x + b * kXBytes + r * 16;
+        uint4 pv[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) pv[c] = *reinterpret_cast<const uint4*>(xp + c * (kBlockRows * 16));
         const int2 inf = info[slot];
+        tc::wait_ld();
+        loaded(sv[0]);
+        loaded(sv[1]);
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kSRead0 + b]);
+        float x[64];
+#pragma unroll
+        for (int j = 0; j < 64; ++j) x[j] = __uint_as_float(sv[j >> 5][j & 31]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          add_f16x2(pv[c].x, x[8 * c], x[8 * c + 1]);
+          add_f16x2(pv[c].y, x[8 * c + 2], x[8 * c + 3]);
+          add_f16x2(pv[c].z, x[8 * c + 4], x[8 * c + 5]);
+          add_f16x2(pv[c].w, x[8 * c + 6], x[8 * c + 7]);
+        }
         const int tstart = (seg.k0 + t) * kTok, v = inf.x, okmask = inf.y;
-        const bool tree_here = tstart + kTok > past;
-        const bool careful = v < kTok || okmask != full_mask || tree_here;   // (the same for all threads)
-        if (careful) {
+        if (v < kTok || okmask != full_mask || tstart + kTok > past) {   // (the same for all threads)
           uint64_t live = 0;
           if (live_row) {
             const int before = past - tstart;     // tokens of the tile that came before the tree
             live = before >= kTok ? ~0ull : before > 0 ? (1ull << before) - 1 : 0ull;
-            if (tree_here) {
+            if (before < kTok) {
               if (before > 0)
                 live |= mask_from(mrow, a.words, 0) << before;
               else
@@ -648,33 +808,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           bool odd = false;
 #pragma unroll
           for (int j = 0; j < 64; ++j) {
-            const bool seen = (live >> j) & 1;
+            const bool seen = ((j < 32 ? (uint32_t)live : (uint32_t)(live >> 32)) >> (j & 31)) & 1;
             odd |= seen && !(fabsf(x[j]) < INFINITY);
-            if (!seen) x[j] = -INFINITY;
+            x[j] = seen ? x[j] : -INFINITY;
           }
           if (odd) l = NAN;
-          // Rows of the stage that are not there may hold anything: zero, so that
-          // a weight of 0 stays 0. So do the tree's tokens that are not finite, for
-          // the rows that do not see them.
-          const int tok = r & 63;
-          uint8_t* stg = sStage + slot * kStage + (r >> 6) * 2 * kSlab;
-          bool zero = !((there >> tok) & 1);
-          if (!zero && tstart + tok >= past) {
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              const uint4 y = *reinterpret_cast<const uint4*>(stg + (c >> 3) * kSlab + sw128(tok, c & 7));
-              const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                zero |= (w[k] & 0x7f80u) == 0x7f80u || (w[k] & 0x7f800000u) == 0x7f800000u;
-            }
-          }
-          if (zero) {
-#pragma unroll
-            for (int c = 0; c < 16; ++c)
-              *reinterpret_cast<uint4*>(stg + (c >> 3) * kSlab + sw128(tok, c & 7)) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
+          clean_stage(sStage + slot * kStage + (r >> 6) * 2 * kSlab, r & 63, (there >> (r & 63)) & 1,
+                      tstart + (r & 63) >= past);
         }
         float mx[22];
 #pragma unroll
@@ -696,80 +836,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           m_used = m_cand;
         }
         const bool any = __any_sync(0xffffffffu, rescale);
-        // (every lane's scores have arrived: their maxima are in the vote)
-        if (lane == 0) cl::arrive_remote_relaxed(pfree_peer + (uint32_t)xb * 8);
+        // (every lane has the peer's scores: they are in the vote's maxima)
+        if (lane == 0) cl::arrive_remote_relaxed(pfree_peer + (uint32_t)b * 8);
         if (any) {
-          const bool okp = __all_sync(0xffffffffu,
-                                      wait_or_abort(&bars[kPVDone0 + ((i - 1) & 1)], ((i - 1) >> 1) & 1, abort_flag));
-          if (!okp) { fail = true; break; }
+          if (!warp_wait(kPVDone0 + (b ^ 1), ((i - 1) >> 1) & 1)) { ok = false; break; }
           tc::fence_after_sync();
 #pragma unroll 1
           for (int c = 0; c < 8; ++c) {
             uint32_t o[32];
             tc::ld32(trow + kOCol + 32 * c, o);
             tc::wait_ld();
+            loaded(o);
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
             tc::st32(trow + kOCol + 32 * c, o);
           }
+          tc::wait_st();
+          tc::fence_before_sync();
         }
         const float mneg = m_used == -INFINITY ? 0.f : -m_used;
         const float2 sc2 = make_float2(scale, scale), mn2 = make_float2(mneg, mneg);
-        uint32_t pk[32];
+        // the senders' staging is in the weights' buffers
+        if (t == 0 && seg_i > 0 && !warp_wait(kOFree, (seg_i - 1) & 1)) { ok = false; break; }
+        uint8_t* pp = sm + Smem::p + b * kPBytes;
+        float sum[4] = {};
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float2 e = fma_f32x2(make_float2(x[2 * j], x[2 * j + 1]), sc2, mn2);
-          pk[j] = pack_bf16(fast_exp2(e.x), fast_exp2(e.y));
+        for (int c = 0; c < 8; ++c) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 e = fma_f32x2(make_float2(x[8 * c + 2 * k], x[8 * c + 2 * k + 1]), sc2, mn2);
+            pk[k] = pack_bf16(fast_exp2(e.x), fast_exp2(e.y));
+            add_bf16x2(pk[k], sum[2 * (k & 1)], sum[2 * (k & 1) + 1]);
+          }
+          *reinterpret_cast<uint4*>(pp + sw128(r, c)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
-        // the senders have read this buffer's scores
-        fail |= !wait_or_abort(&bars[kSRead0 + b], (i >> 1) & 1, abort_flag);
-        if (__any_sync(0xffffffffu, fail)) { fail = true; break; }
-        tc::st32(trow + kSCol + (uint32_t)(b * kTok), pk);
-        float2 sum[4] = {};
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          sum[j & 3] = add_f32x2(sum[j & 3], make_float2(__uint_as_float(pk[j] << 16), __uint_as_float(pk[j] & 0xffff0000u)));
-        sum[0] = add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3]));
-        l += sum[0].x + sum[0].y;
-        tc::wait_st();
-        tc::fence_before_sync();
-        mbar_arrive(&bars[kPFull0 + b]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kPFull0 + b]);
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       }
-      // (a warp that failed leaves; the others' waits see the abort flag)
-      if (fail) break;
-      TreeSeg nxt;
-      const bool more = sw.next(a, nxt);
-      if (more) {
-        // the next segment's query, while this one's last products finish
-        if (!warp_wait(kQEmpty, seg_i & 1)) { fail = true; break; }
-        tc::fence_after_sync();
-        query_in(nxt);
-      }
-      if (!warp_wait(kODone, seg_i & 1)) { fail = true; break; }
-      tc::fence_after_sync();
-      const int64_t slot = (int64_t)share_idx + seg.item;
+      if (!ok) break;
+      // ---- the segment's sums, then its output rows
       const float inv = l == 0.f ? 0.f : 1.f / l;      // (NaN stays NaN)
-      float4* dst = reinterpret_cast<float4*>(a.opart + ((size_t)slot * kBlockRows + r) * kDc + 256 * h);
-#pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
-        uint32_t o[32];
-        tc::ld32(trow + kOCol + 32 * c, o);
-        tc::wait_ld();
-        if (live_row) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            dst[8 * c + k] = make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv,
-                                         __uint_as_float(o[4 * k + 2]) * inv, __uint_as_float(o[4 * k + 3]) * inv);
-        }
-      }
+      sSum[r] = inv;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kSums]);
+      const int64_t slot = (int64_t)share_idx + seg.item;
       a.lse[(slot * 2 + h) * kBlockRows + r] = l == 0.f ? -INFINITY : m_used + log2f(l);
-      tc::fence_before_sync();
-      mbar_arrive(&bars[kOFree]);
-      seg = nxt;
-      have = more;
+      if (!warp_wait(kODone, seg_i & 1)) { ok = false; break; }
+      tc::fence_after_sync();
+      store_rows(trow, 0, inv, seg.ql * a.num_heads - seg.j * kBlockRows - quad * 32,
+                 a.opart + ((size_t)slot * kBlockRows + quad * 32) * kDc + 256 * h, sm + Smem::p + quad * 4096, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kOFree]);
       ++seg_i;
     }
-    if (fail && lane == 0) fail_out();
+    if (!ok && lane == 0) fail_out();
   }
 
   tc::fence_before_sync();
@@ -1132,14 +1255,15 @@ mla_status mla_tree_decode(const mla_config* cfg, const void* q_abs, const void*
   // With num_blocks == 0 every block id is rejected before any copy; the maps
   // still need an extent.
   const uint64_t rows = (uint64_t)(num_blocks > 0 ? num_blocks : 1) * bs;
-  CUtensorMap cache_map, slab4, slab5;
-  if (!encode_row_map(&cache_map, cache, rows, (uint32_t)bs)) return MLA_ERR_CUDA;
-  slab4 = slab5 = cache_map;
-  if (bs == kTok && (!encode_slab_map(&slab4, cache, rows, kTok, 4) || !encode_slab_map(&slab5, cache, rows, kTok, 5)))
+  CUtensorMap cache_map, slab4, rope_map;
+  if (!encode_row_map(&cache_map, cache, rows, (uint32_t)bs) ||
+      !encode_rope_half_map(&rope_map, cache, rows, (uint32_t)bs))
     return MLA_ERR_CUDA;
+  slab4 = cache_map;
+  if (bs == kTok && !encode_slab_map(&slab4, cache, rows, kTok, 4)) return MLA_ERR_CUDA;
   cudaError_t e = cudaFuncSetAttribute(tree_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::alloc);
   if (e == cudaSuccess)
-    e = launch_pdl(tree_decode_kernel, dim3(2 * C), dim3(kThreads), Smem::alloc, st, cache_map, slab4, slab5, a);
+    e = launch_pdl(tree_decode_kernel, dim3(2 * C), dim3(kThreads), Smem::alloc, st, cache_map, slab4, rope_map, a);
   if (e != cudaSuccess) return MLA_ERR_CUDA;
   auto project = [&](auto kernel, int per, int smem) {
     const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
