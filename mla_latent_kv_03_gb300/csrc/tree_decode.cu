@@ -32,7 +32,7 @@
 // shared memory, with four stages of 64 tokens, two buffers of the peer's scores
 // and two of weights.
 // Per CTA (384 threads):
-//   warp 0      copies the cache stages (TMA, SWIZZLE_128B; rope SWIZZLE_64B);
+//   warp 0      copies a segment's query and its cache stages into the ring (TMA, SWIZZLE_128B; rope SWIZZLE_64B);
 //               block ids are checked
 //   warp 1      issues O += P V of a tile; owns the TMEM
 //   warp 2      issues the scores of a tile, up to two tiles ahead of its weights
@@ -40,8 +40,8 @@
 //               (a poll of an mbarrier takes some 125 cycles, ready or not; the
 //               softmax would spend a fifth of its time on four of them a tile)
 //   warps 4-7   softmax, a thread a row
-//   warps 8-11  send the partial scores to the peer, and load the next segment's
-//               query once the last scores are there
+//   warps 8-11  send the partial scores to the peer, and move the next segment's
+//               query from the ring to TMEM once the last scores are there
 //   At a segment's end warps 4-11 write its normalised rows, half of the columns
 //   each, and its log-sum-exps.
 // Every wait is bounded; on a timeout the roles leave their loops, the issuers
@@ -67,7 +67,6 @@ constexpr int kXBytes = kBlockRows * kTok * 2; // 16 KB: [8 chunks][128 rows][16
 constexpr int kPBytes = kBlockRows * 128;      // 16 KB: weights, SWIZZLE_128B
 constexpr int kThreads = 384;
 constexpr int kSoftWarp0 = 4, kSendWarp0 = 8;
-constexpr int kQStage = 2048;                  // a sender warp's staging of query columns: 32 rows of 64 bytes
 constexpr uint32_t kOCol = 0, kSCol = 256, kQCol = 384, kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.f;
 constexpr int kTreeMaxRows = 48 * 1024;
@@ -81,7 +80,8 @@ enum {
   kPVDone0 = kPFull0 + 2,        // [2] O += P V of tile i done
   kXFull0 = kPVDone0 + 2,        // [2] the peer's scores of tile i (bytes from the peer)
   kPeerFree0 = kXFull0 + 2,      // [2] the peer has read its buffer (4 warps of the peer)
-  kQReady = kPeerFree0 + 2,      // query columns in place (4 warps)
+  kQRead0 = kPeerFree0 + 2,      // [2] the stage with half of a query read (4 warps)
+  kQReady = kQRead0 + 2,         // query columns in place (4 warps)
   kSums,                         // the segment's weight sums in shared memory (4 warps)
   kODone,                        // every output product of the segment done
   kOFree,                        // O read out, staging free (8 warps)
@@ -95,8 +95,7 @@ struct Smem {
   static constexpr int x = stage + kStages * kStage;
   static constexpr int p = x + 2 * kXBytes;
   static constexpr int rope = p + 2 * kPBytes;            // [128 rows][32 columns], SWIZZLE_64B
-  static constexpr int qstage = rope + kBlockRows * 64;   // [4 warps]
-  static constexpr int sum = qstage + 4 * kQStage;        // [128] 1 / weight sum
+  static constexpr int sum = rope + kBlockRows * 64;      // [128] 1 / weight sum
   static constexpr int info = sum + kBlockRows * 4;   // [kStages] int2
   static constexpr int bars = info + kStages * 8;
   static constexpr int misc = bars + kNumBars * 8;        // tmem base, abort flag, tiles ready
@@ -149,7 +148,7 @@ struct TreeSeq {
   int q0, ql, len, n, m;   // rows [q0, q0 + ql); n tiles, m q-blocks (0: nothing to do)
   bool broken;             // query_start_loc does not ascend here, or leaves [0, num_q]
 };
-__device__ __noinline__ TreeSeq tree_seq(const TreeArgs& a, int b, bool report) {
+__device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, bool report) {
   TreeSeq s;
   s.q0 = a.query_start_loc[b];
   const int q1 = a.query_start_loc[b + 1];
@@ -214,23 +213,24 @@ struct TreeWalk {
 };
 
 // Exclusive prefix of v over the CTA's threads, and the total.
-__device__ __forceinline__ int block_scan(int v, int* scratch, int tid, int& total) {
+__device__ __noinline__ int block_scan(int v, int* scratch, int tid, int* total) {
   const int lane = tid & 31, warp = tid >> 5;
   int incl = v;
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const int x = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += x;
   }
   if (lane == 31) scratch[warp] = incl;
   __syncthreads();
-  int run = incl - v;
-  total = 0;
-#pragma unroll
+  int run = incl - v, all = 0;
+#pragma unroll 1
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) run += scratch[w];
-    total += scratch[w];
+    const int x = scratch[w];
+    if (w < warp) run += x;
+    all += x;
   }
+  *total = all;
   return run;
 }
 
@@ -240,33 +240,42 @@ __device__ __forceinline__ bool find_share(const TreeArgs& a, int c, int4* start
   const bool first = blockIdx.x == 0;
   const int per = (a.batch + kThreads - 1) / kThreads;
   const int beg = min(a.batch, tid * per), end = min(a.batch, beg + per);
-  int units = 0, items = 0, total, dummy;
-  bool broken = false;
-  for (int b = beg; b < end; ++b) {
-    const TreeSeq s = tree_seq(a, b, first);
-    units += s.n * s.m;
-    broken |= s.broken;
-  }
-  // (rows that two sequences have would not fit the workspace: nothing is done)
-  if (__syncthreads_or(broken)) {
-    if (first)
-      for (int b = beg; b < end; ++b) a.plan[b] = make_int4(0, 0, 0, 0);
-    return false;
-  }
-  int ubase = block_scan(units, scratch, tid, total);
-  const int share = max(1, (total + a.shares - 1) / a.shares);
-  for (int b = beg; b < end; ++b) {
-    const TreeSeq s = tree_seq(a, b, false);
-    items += s.m * strips_of(s.n, s.m, share);
-  }
-  int ibase = block_scan(items, scratch + kThreads / 32, tid, dummy);
-  const int u0 = (int)min((int64_t)c * share, (int64_t)total);
-  for (int b = beg; b < end; ++b) {
-    const TreeSeq s = tree_seq(a, b, false);
-    if (first) a.plan[b] = make_int4(ubase, ibase, s.n, s.m);
-    if (u0 >= ubase && u0 < ubase + s.n * s.m) *start = make_int4(b, ubase, ibase, 0);
-    ubase += s.n * s.m;
-    ibase += s.m * strips_of(s.n, s.m, share);
+  int ubase = 0, ibase = 0, total = 0, share = 1, u0 = 0;
+  // three passes over a thread's sequences: their units, their items, where they begin
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    int sum = 0;
+    bool broken = false;
+#pragma unroll 1
+    for (int b = beg; b < end; ++b) {
+      const TreeSeq s = tree_seq(a, b, first && pass == 0);
+      const int units = s.n * s.m, items = pass == 0 ? 0 : s.m * strips_of(s.n, s.m, share);
+      if (pass == 0) {
+        sum += units;
+        broken |= s.broken;
+      } else if (pass == 1) {
+        sum += items;
+      } else {
+        if (first) a.plan[b] = make_int4(ubase, ibase, s.n, s.m);
+        if (u0 >= ubase && u0 < ubase + units) *start = make_int4(b, ubase, ibase, 0);
+        ubase += units;
+        ibase += items;
+      }
+    }
+    if (pass == 0) {
+      // (rows that two sequences have would not fit the workspace: nothing is done)
+      if (__syncthreads_or(broken)) {
+        if (first)
+          for (int b = beg; b < end; ++b) a.plan[b] = make_int4(0, 0, 0, 0);
+        return false;
+      }
+      ubase = block_scan(sum, scratch, tid, &total);
+      share = max(1, (total + a.shares - 1) / a.shares);
+      u0 = (int)min((int64_t)c * share, (int64_t)total);
+    } else if (pass == 1) {
+      int items;
+      ibase = block_scan(sum, scratch + kThreads / 32, tid, &items);
+    }
   }
   if (first && tid == 0) {
     WsHeader* hdr = reinterpret_cast<WsHeader*>(a.ws);
@@ -367,52 +376,33 @@ __device__ __forceinline__ void loaded(uint32_t (&r)[32]) {
                  "+r"(r[k + 12]), "+r"(r[k + 13]), "+r"(r[k + 14]), "+r"(r[k + 15]));
 }
 
-// A sender warp's part of a q-block's query, 32 rows: this CTA's 256 latent columns
-// into TMEM, its 32 rope columns into shared memory. Fetched by 64 bytes of a row
-// to 4 lanes, and handed to the lanes of their rows through `stage`.
-__device__ __noinline__ void load_query(const TreeArgs& a, const TreeSeg& g, int h, int row0, int lane, uint32_t trow,
-                                           uint8_t* stage, uint8_t* rope_rows) {
-  const int rows = g.ql * a.num_heads, first = g.j * kBlockRows + row0;
-  const uint4* q = reinterpret_cast<const uint4*>(a.q_abs) + ((int64_t)g.q0 * a.num_heads + first) * (kRow / 8);
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  auto fetch = [&](uint4 (&v)[4], int c) {   // columns [32 c, 32 c + 32) of the row's 256; c = 8: rope
+// A warp's 32 rows of two of the query's column slabs (128 columns) from a stage
+// that holds them, [2 slabs][128 rows][128 bytes], into TMEM, and of 64 rows' rope
+// columns into their place.
+__device__ __noinline__ void take_query(const uint8_t* stage, int part, int r, uint32_t tcols, uint8_t* rope_rows) {
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t w[16];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int r = 8 * u + (lane >> 2);
-      v[u] = first + r < rows ? __ldg(q + r * (kRow / 8) + (c < 8 ? 32 * h + 4 * c : 64 + 4 * h) + (lane & 3)) : zero;
+      const uint4 y = *reinterpret_cast<const uint4*>(stage + (c >> 1) * (kBlockRows * 128) + sw128(r, 4 * (c & 1) + u));
+      w[4 * u] = y.x;
+      w[4 * u + 1] = y.y;
+      w[4 * u + 2] = y.z;
+      w[4 * u + 3] = y.w;
     }
-  };
-#pragma unroll 1
-  for (int c0 = 0; c0 < 9; c0 += 3) {
-    uint4 v[3][4];
+    tc::st16(tcols + 64 * part + 16 * c, w);
+  }
+  if (r >> 6 == part) {
 #pragma unroll
-    for (int c = 0; c < 3; ++c) fetch(v[c], c0 + c);
-#pragma unroll
-    for (int c = 0; c < 3; ++c) {
-      if (c0 + c == 8) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          *reinterpret_cast<uint4*>(rope_rows + sw64(row0 + 8 * u + (lane >> 2), lane & 3)) = v[c][u];
-        break;
-      }
-      __syncwarp();
-#pragma unroll
-      for (int u = 0; u < 4; ++u) *reinterpret_cast<uint4*>(stage + sw64(8 * u + (lane >> 2), lane & 3)) = v[c][u];
-      __syncwarp();
-      uint32_t w[16];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const uint4 y = *reinterpret_cast<const uint4*>(stage + sw64(lane, u));
-        w[4 * u] = y.x;
-        w[4 * u + 1] = y.y;
-        w[4 * u + 2] = y.z;
-        w[4 * u + 3] = y.w;
-      }
-      tc::st16(trow + kQCol + 16 * (c0 + c), w);
-    }
+    for (int u = 0; u < 4; ++u)
+      *reinterpret_cast<uint4*>(rope_rows + r * 64 + 16 * u) =
+          *reinterpret_cast<const uint4*>(stage + 4 * kSlab + (r & 63) * 64 + 16 * u);
   }
   fence_proxy_async_smem();
   tc::wait_st();
+  tc::fence_before_sync();
+  __syncwarp();
 }
 
 // The normalised columns [128 part, 128 part + 128) of this CTA's half of a
@@ -472,7 +462,8 @@ __device__ __noinline__ uint64_t mask_from(const uint64_t* m, int words, int j0)
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tree_decode_kernel(const __grid_constant__ CUtensorMap cache_map, const __grid_constant__ CUtensorMap slab4,
-                       const __grid_constant__ CUtensorMap rope_map, const __grid_constant__ TreeArgs a) {
+                       const __grid_constant__ CUtensorMap rope_map, const __grid_constant__ CUtensorMap q_map,
+                       const __grid_constant__ CUtensorMap qrope_map, const __grid_constant__ TreeArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
@@ -504,6 +495,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(bs == kTok ? &slab4 : &cache_map);
     prefetch_tensormap(&rope_map);
+    prefetch_tensormap(&q_map);
+    prefetch_tensormap(&qrope_map);
   }
   tc::fence_before_sync();
   cl::sync();  // both CTAs' barriers exist before either sends
@@ -528,24 +521,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (has_work && warp == 0) {
     // ------------------------------------------------------------ copies
+    // The ring takes a segment's query in two stages (128 latent columns each, and
+    // 64 rows' rope columns), then its tiles.
     const uint64_t policy = l2_evict_first_policy();
-    int i = 0;
+    int ri = 0;                                   // stages filled so far
+    uint32_t holds_q = 0, phase = 0;              // per slot: what it holds; the parity of its next Empty
+    int seg_i = 0;
     bool ok = true;
+    auto room = [&](int slot) {
+      if (ri < kStages) return true;
+      if ((holds_q >> slot) & 1) return warp_wait(kQRead0 + ((holds_q >> (8 + slot)) & 1), (holds_q >> (16 + slot)) & 1);
+      const bool free = warp_wait(kEmpty0 + slot, (phase >> slot) & 1);
+      phase ^= 1u << slot;
+      return free;
+    };
     while (ok && sw.next(a, seg)) {
       const int32_t* bt = a.block_table + (size_t)seg.b * a.max_blocks;
+      for (int part = 0; part < 2 && ok; ++part, ++ri) {
+        const int slot = ri % kStages;
+        if (!room(slot)) { ok = false; break; }
+        holds_q = (holds_q & ~(0x10101u << slot)) | (0x1u | (uint32_t)part << 8 | (uint32_t)(seg_i & 1) << 16) << slot;
+        if (lane == 0) {
+          uint64_t* full = &bars[kFull0 + slot];
+          uint8_t* dst = sStage + slot * kStage;
+          const int row = seg.q0 * a.num_heads + seg.j * kBlockRows;
+          mbar_arrive_expect_tx(full, kStage);
+          tma_load_2d(dst, &q_map, 256 * h + 128 * part, row, full);
+          tma_load_2d(dst + kBlockRows * 128, &q_map, 256 * h + 128 * part + 64, row, full);
+          tma_load_2d(dst + 4 * kSlab, &qrope_map, kDc + 32 * h, row + 64 * part, full);
+        }
+        __syncwarp();
+      }
+      ++seg_i;
       int cache_base = -(1 << 30), cached = -1;   // lane l holds bt[cache_base + l]
 #pragma unroll 1
-      for (int k = seg.k0; k < seg.k1; ++k, ++i) {
-        const int tstart = k * kTok, v = min(kTok, seg.len - tstart), slot = i % kStages;
+      for (int k = seg.k0; k < seg.k1 && ok; ++k, ++ri) {
+        const int tstart = k * kTok, v = min(kTok, seg.len - tstart), slot = ri % kStages;
         const int p0 = tstart >> bs_shift;
         if (p0 < cache_base || p0 + pages > cache_base + 32) {
           cache_base = p0;
           cached = p0 + lane < a.max_blocks ? bt[p0 + lane] : -1;
         }
-        if (i >= kStages && !warp_wait(kEmpty0 + slot, ((i / kStages) - 1) & 1)) {
-          ok = false;
-          break;
-        }
+        if (!room(slot)) { ok = false; break; }
+        holds_q &= ~(1u << slot);
         // lane l: of page l / 5 of the stage, slab l % 5 (4: the rope columns);
         // of a 64-token page one copy of all four slabs
         const int pg = lane / 5, sl = lane % 5;
@@ -578,7 +596,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       if (!ok) fail_out();
       for (int slot = 0; slot < kStages; ++slot) {   // never leave with copies in flight
-        const int fills = i > slot ? (i - 1 - slot) / kStages + 1 : 0;
+        const int fills = ri > slot ? (ri - 1 - slot) / kStages + 1 : 0;
         if (fills > 0 && !mbar_wait(&bars[kFull0 + slot], (fills - 1) & 1)) set_status(a.status, MLA_DEV_TIMEOUT);
       }
     }
@@ -589,13 +607,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint64_t vdesc = tc::smem_desc(smem_u32(sStage), kSlab, 1024, tc::kSwizzle128);
     const uint64_t pdesc = tc::smem_desc(smem_u32(sm + Smem::p), 16, 1024, tc::kSwizzle128);
     const bool leader = tc::elect_one();
-    int i = 0, seg_i = 0;
+    int i = 0, ri = 0, seg_i = 0;
     bool ok = true;
     while (ok && sw.next(a, seg)) {
       const int n = seg.k1 - seg.k0;
+      ri += 2;
 #pragma unroll 1
-      for (int t = 0; t < n; ++t, ++i) {
-        const int slot = i % kStages, b = i & 1;
+      for (int t = 0; t < n; ++t, ++i, ++ri) {
+        const int slot = ri % kStages, b = i & 1;
         if (!warp_wait(kPFull0 + b, (i >> 1) & 1)) { ok = false; break; }
         if (t == 0 && seg_i > 0 && !warp_wait(kOFree, (seg_i - 1) & 1)) { ok = false; break; }
         tc::fence_after_sync();
@@ -626,16 +645,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint64_t krdesc = tc::smem_desc(smem_u32(sStage + 4 * kSlab), 16, 512, tc::kSwizzle64);
     const uint64_t qrdesc = tc::smem_desc(smem_u32(sm + Smem::rope), 16, 512, tc::kSwizzle64);
     const bool leader = tc::elect_one();
-    int i = 0, seg_i = 0;
+    int i = 0, ri = 0, seg_i = 0;
     bool ok = true;
     while (ok && sw.next(a, seg)) {
       const int n = seg.k1 - seg.k0;
+      ri += 2;
       if (!warp_wait(kQReady, seg_i & 1)) { ok = false; break; }
 #pragma unroll 1
-      for (int t = 0; t < n; ++t, ++i) {
-        const int slot = i % kStages, b = i & 1;
+      for (int t = 0; t < n; ++t, ++i, ++ri) {
+        const int slot = ri % kStages, b = i & 1;
         if (i >= 2 && !warp_wait(kSRead0 + b, ((i - 2) >> 1) & 1)) { ok = false; break; }
-        if (!warp_wait(kFull0 + slot, (i / kStages) & 1)) { ok = false; break; }
+        if (!warp_wait(kFull0 + slot, (ri / kStages) & 1)) { ok = false; break; }
         tc::fence_after_sync();
         if (leader) {
           const uint32_t d = tmem + kSCol + (uint32_t)(b * kTok);
@@ -661,14 +681,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (has_work && warp == 3) {
     // ---------------------------------------------------- what a tile needs
-    int i = 0;
+    int i = 0, ri = 0;
     bool ok = true;
     while (ok && sw.next(a, seg)) {
+      ri += 2;
 #pragma unroll 1
-      for (int k = seg.k0; k < seg.k1; ++k, ++i) {
-        const int b = i & 1, slot = i % kStages;
+      for (int k = seg.k0; k < seg.k1; ++k, ++i, ++ri) {
+        const int b = i & 1, slot = ri % kStages;
         ok = (i < 2 || warp_wait(kPVDone0 + b, ((i >> 1) - 1) & 1)) &&   // its weights' buffer
-             warp_wait(kFull0 + slot, (i / kStages) & 1) &&              // what is in the stage
+             warp_wait(kFull0 + slot, (ri / kStages) & 1) &&             // what is in the stage
              warp_wait(kSFull0 + b, (i >> 1) & 1) && warp_wait(kXFull0 + b, (i >> 1) & 1);
         if (!ok) break;
         if (lane == 0) {
@@ -688,18 +709,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t xbar_peer = cl::map(smem_u32(&bars[kXFull0]), peer);
     uint8_t* rope = sm + Smem::rope;
     const float* sSum = reinterpret_cast<const float*>(sm + Smem::sum);
-    int i = 0, seg_i = 0;
+    int i = 0, ri = 0, seg_i = 0;
     bool ok = true;
-    auto query_in = [&](const TreeSeg& g) {
-      load_query(a, g, h, quad * 32, lane, trow, sm + Smem::qstage + quad * kQStage, rope);
-      tc::fence_before_sync();
-      __syncwarp();
+    auto query_in = [&]() {
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part, ++ri) {
+        const int slot = ri % kStages;
+        if (!warp_wait(kFull0 + slot, (ri / kStages) & 1)) return false;
+        take_query(sStage + slot * kStage, part, r, trow + kQCol, rope);
+        if (lane == 0) mbar_arrive(&bars[kQRead0 + part]);
+      }
       if (lane == 0) mbar_arrive(&bars[kQReady]);
+      return true;
     };
     bool have = sw.next(a, seg);
-    if (have) query_in(seg);
+    if (have) ok = query_in();
     while (have && ok) {
       const int n = seg.k1 - seg.k0;
+      ri += n;
 #pragma unroll 1
       for (int t = 0; t < n; ++t, ++i) {
         const int b = i & 1;
@@ -729,7 +756,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // half of this segment's output
       TreeSeg nxt;
       const bool more = sw.next(a, nxt);
-      if (more) query_in(nxt);
+      if (more && !query_in()) { ok = false; break; }
       if (!warp_wait(kODone, seg_i & 1) || !warp_wait(kSums, seg_i & 1)) { ok = false; break; }
       tc::fence_after_sync();
       store_rows(trow, 1, sSum[r], seg.ql * a.num_heads - seg.j * kBlockRows - quad * 32,
@@ -749,17 +776,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t pfree_peer = cl::map(smem_u32(&bars[kPeerFree0]), (uint32_t)(h ^ 1));
     float* sSum = reinterpret_cast<float*>(sm + Smem::sum);
     const float scale = a.scale_log2;
-    int i = 0, seg_i = 0;
+    int i = 0, ri = 0, seg_i = 0;
     bool ok = true;
     while (ok && sw.next(a, seg)) {
+      ri += 2;
       const int n = seg.k1 - seg.k0, past = seg.len - seg.ql;
       const int row = (seg.j * kBlockRows + r) / a.num_heads;   // of the sequence
       const bool live_row = row < seg.ql;
       const uint64_t* mrow = a.mask + (size_t)(seg.q0 + (live_row ? row : 0)) * a.words;
       float m_used = -INFINITY, l = 0.f;
 #pragma unroll 1
-      for (int t = 0; t < n; ++t, ++i) {
-        const int slot = i % kStages, b = i & 1;
+      for (int t = 0; t < n; ++t, ++i, ++ri) {
+        const int slot = ri % kStages, b = i & 1;
         if (!wait_word(ready, i, abort_flag)) ok = false;
         if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
         tc::fence_after_sync();
@@ -1255,7 +1283,10 @@ mla_status mla_tree_decode(const mla_config* cfg, const void* q_abs, const void*
   // With num_blocks == 0 every block id is rejected before any copy; the maps
   // still need an extent.
   const uint64_t rows = (uint64_t)(num_blocks > 0 ? num_blocks : 1) * bs;
-  CUtensorMap cache_map, slab4, rope_map;
+  CUtensorMap cache_map, slab4, rope_map, q_map, qrope_map;
+  if (!encode_row_map(&q_map, q_abs, (uint64_t)num_q * H, kBlockRows) ||
+      !encode_rope_half_map(&qrope_map, q_abs, (uint64_t)num_q * H, kBlockRows / 2))
+    return MLA_ERR_CUDA;
   if (!encode_row_map(&cache_map, cache, rows, (uint32_t)bs) ||
       !encode_rope_half_map(&rope_map, cache, rows, (uint32_t)bs))
     return MLA_ERR_CUDA;
@@ -1263,7 +1294,7 @@ mla_status mla_tree_decode(const mla_config* cfg, const void* q_abs, const void*
   if (bs == kTok && !encode_slab_map(&slab4, cache, rows, kTok, 4)) return MLA_ERR_CUDA;
   cudaError_t e = cudaFuncSetAttribute(tree_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::alloc);
   if (e == cudaSuccess)
-    e = launch_pdl(tree_decode_kernel, dim3(2 * C), dim3(kThreads), Smem::alloc, st, cache_map, slab4, rope_map, a);
+    e = launch_pdl(tree_decode_kernel, dim3(2 * C), dim3(kThreads), Smem::alloc, st, cache_map, slab4, rope_map, q_map, qrope_map, a);
   if (e != cudaSuccess) return MLA_ERR_CUDA;
   auto project = [&](auto kernel, int per, int smem) {
     const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
