@@ -90,6 +90,13 @@ enum {
   kNumBars
 };
 
+// A stage: per page its 4 column slabs of block_size rows (128 bytes of a row, 64
+// columns), then the rope columns of the 64 rows. Byte offset of token t's row in
+// its page's first slab, without the swizzle:
+__device__ __forceinline__ int token_at(int t, int bs_shift) {
+  return ((t >> bs_shift) << (bs_shift + 9)) + (t & ((1 << bs_shift) - 1)) * 128;
+}
+
 struct Smem {
   static constexpr int stage = 0;
   static constexpr int x = stage + kStages * kStage;
@@ -433,14 +440,14 @@ __device__ __noinline__ void store_rows(uint32_t trow, int part, float inv, int 
 
 // Rows of a stage that are not there may hold anything: zero, so that a weight of
 // 0 stays 0. So do the tree's tokens that are not finite, for the rows that do
-// not see them. Two slabs (128 columns) of row `tok`.
-__device__ __noinline__ void clean_stage(uint8_t* stg, int tok, bool there, bool of_tree) {
+// not see them. Two slabs (128 columns) of row `row`.
+__device__ __noinline__ void clean_stage(uint8_t* stg, int slab_bytes, int row, bool there, bool of_tree) {
   bool zero = !there;
   if (there && of_tree) {
     uint32_t most = 0;   // the largest exponent and fraction of the low and of the high values
 #pragma unroll 4
     for (int c = 0; c < 16; ++c) {
-      const uint4 y = *reinterpret_cast<const uint4*>(stg + (c >> 3) * kSlab + sw128(tok, c & 7));
+      const uint4 y = *reinterpret_cast<const uint4*>(stg + (c >> 3) * slab_bytes + sw128(row, c & 7));
       most = __vmaxu2(__vmaxu2(most, y.x & 0x7fff7fffu), __vmaxu2(y.y & 0x7fff7fffu, __vmaxu2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu)));
     }
     zero = (most & 0xffffu) >= 0x7f80u || (most >> 16) >= 0x7f80u;
@@ -448,7 +455,7 @@ __device__ __noinline__ void clean_stage(uint8_t* stg, int tok, bool there, bool
   if (zero) {
 #pragma unroll 4
     for (int c = 0; c < 16; ++c)
-      *reinterpret_cast<uint4*>(stg + (c >> 3) * kSlab + sw128(tok, c & 7)) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(stg + (c >> 3) * slab_bytes + sw128(row, c & 7)) = make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -461,8 +468,7 @@ __device__ __noinline__ uint64_t mask_from(const uint64_t* m, int words, int j0)
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    tree_decode_kernel(const __grid_constant__ CUtensorMap cache_map, const __grid_constant__ CUtensorMap slab4,
-                       const __grid_constant__ CUtensorMap rope_map, const __grid_constant__ CUtensorMap q_map,
+    tree_decode_kernel(const __grid_constant__ CUtensorMap slab4, const __grid_constant__ CUtensorMap rope_map, const __grid_constant__ CUtensorMap q_map,
                        const __grid_constant__ CUtensorMap qrope_map, const __grid_constant__ TreeArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -493,7 +499,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   if (warp == 1) tc::alloc(tmem_slot, kTmemCols);
   if (warp == 0 && lane == 0) {
-    prefetch_tensormap(bs == kTok ? &slab4 : &cache_map);
+    prefetch_tensormap(&slab4);
     prefetch_tensormap(&rope_map);
     prefetch_tensormap(&q_map);
     prefetch_tensormap(&qrope_map);
@@ -524,6 +530,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // The ring takes a segment's query in two stages (128 latent columns each, and
     // 64 rows' rope columns), then its tiles.
     const uint64_t policy = l2_evict_first_policy();
+    const bool leader = tc::elect_one();
     int ri = 0;                                   // stages filled so far
     uint32_t holds_q = 0, phase = 0;              // per slot: what it holds; the parity of its next Empty
     int seg_i = 0;
@@ -541,7 +548,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int slot = ri % kStages;
         if (!room(slot)) { ok = false; break; }
         holds_q = (holds_q & ~(0x10101u << slot)) | (0x1u | (uint32_t)part << 8 | (uint32_t)(seg_i & 1) << 16) << slot;
-        if (lane == 0) {
+        if (leader) {
           uint64_t* full = &bars[kFull0 + slot];
           uint8_t* dst = sStage + slot * kStage;
           const int row = seg.q0 * a.num_heads + seg.j * kBlockRows;
@@ -562,33 +569,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           cache_base = p0;
           cached = p0 + lane < a.max_blocks ? bt[p0 + lane] : -1;
         }
+        const bool wanted = lane < pages && (lane << bs_shift) < v;     // lane l: page l of the stage
+        const int blk = __shfl_sync(0xffffffffu, cached, min(p0 - cache_base + lane, 31));
+        const bool there = wanted && blk >= 0 && blk < a.num_blocks;
+        if (wanted && !there) set_status(a.status, MLA_DEV_BAD_BLOCK);
+        const uint32_t okmask = __ballot_sync(0xffffffffu, there);
         if (!room(slot)) { ok = false; break; }
         holds_q &= ~(1u << slot);
-        // lane l: of page l / 5 of the stage, slab l % 5 (4: the rope columns);
-        // of a 64-token page one copy of all four slabs
-        const int pg = lane / 5, sl = lane % 5;
-        const int blk = __shfl_sync(0xffffffffu, cached, min(p0 - cache_base + pg, 31));
-        const bool wanted = pg < pages && (pg << bs_shift) < v;
-        const bool there = wanted && blk >= 0 && blk < a.num_blocks;
-        if (wanted && !there && sl == 0) set_status(a.status, MLA_DEV_BAD_BLOCK);
-        const uint32_t loads = __ballot_sync(0xffffffffu, there);
-        uint64_t* full = &bars[kFull0 + slot];
         uint8_t* dst = sStage + slot * kStage;
-        if (lane == 0) {
-          int okmask = 0;
-          for (int p = 0; p < pages; ++p) okmask |= ((loads >> (p * 5)) & 1) << p;
-          info[slot] = make_int2(v, okmask);
-          mbar_arrive_expect_tx(full, __popc(okmask) * bs * (4 * 128 + 64));
+        if (leader) {
+          info[slot] = make_int2(v, (int)okmask);
+          mbar_arrive_expect_tx(&bars[kFull0 + slot], __popc(okmask) * bs * (4 * 128 + 64));
         }
         __syncwarp();
-        if (there) {
-          if (sl == 4)
-            tma_load_2d_hint(dst + 4 * kSlab + (pg << bs_shift) * 64, &rope_map, kDc + 32 * h, blk * bs, full, policy);
-          else if (bs != kTok)
-            tma_load_2d_hint(dst + sl * kSlab + (pg << bs_shift) * 128, &cache_map, 256 * h + 64 * sl, blk * bs, full,
+#pragma unroll 1
+        for (int p = 0; p < pages; ++p) {
+          const int y = __shfl_sync(0xffffffffu, blk, p) << bs_shift;
+          if (leader && ((okmask >> p) & 1)) {
+            tma_load_3d_hint(dst + (p << bs_shift) * 512, &slab4, 0, y, 4 * h, &bars[kFull0 + slot], policy);
+            tma_load_2d_hint(dst + 4 * kSlab + (p << bs_shift) * 64, &rope_map, kDc + 32 * h, y, &bars[kFull0 + slot],
                              policy);
-          else if (sl == 0)
-            tma_load_3d_hint(dst, &slab4, 0, blk * bs, 4 * h, full, policy);
+          }
         }
         __syncwarp();
       }
@@ -604,7 +605,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (has_work && warp == 1) {
     // ---------------------------------------------------- output products
     constexpr uint32_t kIdO = tc::idesc_bf16(128, 256, false, true);
-    const uint64_t vdesc = tc::smem_desc(smem_u32(sStage), kSlab, 1024, tc::kSwizzle128);
+    const uint64_t vdesc = tc::smem_desc(smem_u32(sStage), (uint32_t)bs * 128, 1024, tc::kSwizzle128);
     const uint64_t pdesc = tc::smem_desc(smem_u32(sm + Smem::p), 16, 1024, tc::kSwizzle128);
     const bool leader = tc::elect_one();
     int i = 0, ri = 0, seg_i = 0;
@@ -622,7 +623,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int ks = 0; ks < kTok / 16; ++ks)
             tc::mma_bf16(tmem + kOCol, pdesc + (uint64_t)((b * kPBytes + ks * 32) >> 4),
-                         vdesc + (uint64_t)((slot * kStage + ks * 16 * 128) >> 4), kIdO, t > 0 || ks > 0);
+                         vdesc + (uint64_t)((slot * kStage + token_at(ks * 16, bs_shift)) >> 4), kIdO, t > 0 || ks > 0);
           tc::commit(&bars[kEmpty0 + slot]);
           tc::commit(&bars[kPVDone0 + b]);
         }
@@ -641,6 +642,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (has_work && warp == 2) {
     // ------------------------------------------------------------- scores
     constexpr uint32_t kIdS = tc::idesc_bf16(128, kTok, false, false);
+    const uint32_t id_page = tc::idesc_bf16(128, bs, false, false);
     const uint64_t kdesc = tc::smem_desc(smem_u32(sStage), 16, 1024, tc::kSwizzle128);
     const uint64_t krdesc = tc::smem_desc(smem_u32(sStage + 4 * kSlab), 16, 512, tc::kSwizzle64);
     const uint64_t qrdesc = tc::smem_desc(smem_u32(sm + Smem::rope), 16, 512, tc::kSwizzle64);
@@ -660,10 +662,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (leader) {
           const uint32_t d = tmem + kSCol + (uint32_t)(b * kTok);
           const uint64_t at = (uint64_t)((slot * kStage) >> 4);
+// (rolled: this code is fetched anew for every tile)
+#pragma unroll 1
+          for (int pj = 0; pj < 4 * pages; ++pj) {     // page by page, slab by slab
 #pragma unroll
-          for (int kk = 0; kk < 16; ++kk)
-            tc::mma_bf16_tmem_a(d, tmem + kQCol + (uint32_t)(kk * 8),
-                                kdesc + at + (uint64_t)(((kk >> 2) * kSlab + (kk & 3) * 32) >> 4), kIdS, kk > 0);
+            for (int c = 0; c < 4; ++c)
+              tc::mma_bf16_tmem_a(d + ((pj >> 2) << bs_shift), tmem + kQCol + (uint32_t)((pj & 3) * 32 + c * 8),
+                                  kdesc + at + (uint64_t)(((pj << (bs_shift + 7)) + c * 32) >> 4), id_page,
+                                  (pj & 3) > 0 || c > 0);
+          }
 #pragma unroll
           for (int c = 0; c < 2; ++c)
             tc::mma_bf16(d, qrdesc + (uint64_t)((c * 32) >> 4), krdesc + at + (uint64_t)((c * 32) >> 4), kIdS, true);
@@ -841,8 +848,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             x[j] = seen ? x[j] : -INFINITY;
           }
           if (odd) l = NAN;
-          clean_stage(sStage + slot * kStage + (r >> 6) * 2 * kSlab, r & 63, (there >> (r & 63)) & 1,
-                      tstart + (r & 63) >= past);
+          const int tok = r & 63;    // each thread one token's half of the columns
+          clean_stage(sStage + slot * kStage + ((tok >> bs_shift) << (bs_shift + 9)) + (r >> 6) * 2 * (bs * 128), bs * 128,
+                      tok & (bs - 1), (there >> tok) & 1, tstart + tok >= past);
         }
         float mx[22];
 #pragma unroll
@@ -1283,18 +1291,16 @@ mla_status mla_tree_decode(const mla_config* cfg, const void* q_abs, const void*
   // With num_blocks == 0 every block id is rejected before any copy; the maps
   // still need an extent.
   const uint64_t rows = (uint64_t)(num_blocks > 0 ? num_blocks : 1) * bs;
-  CUtensorMap cache_map, slab4, rope_map, q_map, qrope_map;
+  CUtensorMap slab4, rope_map, q_map, qrope_map;
   if (!encode_row_map(&q_map, q_abs, (uint64_t)num_q * H, kBlockRows) ||
       !encode_rope_half_map(&qrope_map, q_abs, (uint64_t)num_q * H, kBlockRows / 2))
     return MLA_ERR_CUDA;
-  if (!encode_row_map(&cache_map, cache, rows, (uint32_t)bs) ||
+  if (!encode_slab_map(&slab4, cache, rows, (uint32_t)bs, 4) ||
       !encode_rope_half_map(&rope_map, cache, rows, (uint32_t)bs))
     return MLA_ERR_CUDA;
-  slab4 = cache_map;
-  if (bs == kTok && !encode_slab_map(&slab4, cache, rows, kTok, 4)) return MLA_ERR_CUDA;
   cudaError_t e = cudaFuncSetAttribute(tree_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::alloc);
   if (e == cudaSuccess)
-    e = launch_pdl(tree_decode_kernel, dim3(2 * C), dim3(kThreads), Smem::alloc, st, cache_map, slab4, rope_map, q_map, qrope_map, a);
+    e = launch_pdl(tree_decode_kernel, dim3(2 * C), dim3(kThreads), Smem::alloc, st, slab4, rope_map, q_map, qrope_map, a);
   if (e != cudaSuccess) return MLA_ERR_CUDA;
   auto project = [&](auto kernel, int per, int smem) {
     const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
