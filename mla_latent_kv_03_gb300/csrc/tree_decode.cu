@@ -53,12 +53,12 @@
 #include "internal.h"
 #include "pair_math.cuh"
 #include "tcgen05.cuh"
+#include "tree_parts.cuh"
 
 namespace mla {
 namespace {
 
-constexpr int kBlockRows = 128;
-constexpr int kTok = 64;
+constexpr int kBlockRows = kTreeBlockRows, kTok = kTreeTok;
 constexpr int kSlab = kTok * 128;              // 64 rows of 64 bf16 columns
 constexpr int kRope = kTok * 64;               // 64 rows of 32 rope columns
 constexpr int kStage = 4 * kSlab + kRope;      // 36 KB
@@ -115,42 +115,6 @@ static_assert(Smem::bars % 8 == 0 && Smem::stage % 1024 == 0 && kStage % 1024 ==
                   Smem::rope % 1024 == 0,
               "alignment");
 
-struct TreeArgs {
-  const uint16_t* q_abs;
-  int64_t num_blocks, num_q;
-  const int32_t* block_table;
-  int32_t max_blocks, block_size, num_heads, batch, words, shares;
-  const int32_t* seq_lens;
-  const int32_t* query_start_loc;
-  const uint64_t* mask;
-  float scale_log2;
-  uint8_t* ws;
-  uint32_t* status;
-  int4* plan;      // [batch] {first unit, first item, tiles, q-blocks}
-  float* lse;      // [slots][2][128]
-  float* opart;    // [slots][128][512]
-  float* o_lat;    // [num_q, H, 512]
-};
-
-// Workspace: header (status word, share), plan, partials. An item is what one
-// q-block has in one strip; its part in cluster c has slot c + item, which is
-// unique because items and shares are both contiguous and in order.
-struct TreeWs {
-  size_t plan, lse, opart, o_lat, total;
-};
-__host__ __device__ inline TreeWs tree_ws(int64_t num_q, int heads, int shares, int64_t batch) {
-  TreeWs L;
-  // items: a q-block has one, and one more for every share's worth of its units
-  const int64_t slots = 2 * (int64_t)shares + num_q * heads / kBlockRows + batch + 1;
-  size_t off = kLayoutStart;
-  L.plan = off;   off = align_up(off + (size_t)batch * 16, 256);
-  L.lse = off;    off = align_up(off + (size_t)slots * 2 * kBlockRows * 4, 256);
-  L.o_lat = off;  off = align_up(off + (size_t)num_q * heads * kDc * 4, 256);
-  L.opart = off;  off = align_up(off + (size_t)slots * kBlockRows * kDc * 4, 256);
-  L.total = off;
-  return L;
-}
-
 struct TreeSeq {
   int q0, ql, len, n, m;   // rows [q0, q0 + ql); n tiles, m q-blocks (0: nothing to do)
   bool broken;             // query_start_loc does not ascend here, or leaves [0, num_q]
@@ -173,10 +137,6 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, bool repor
   }
   return s;
 }
-__host__ __device__ __forceinline__ int strips_of(int n, int m, int share) {
-  return m <= 1 ? m : (n + share - 1) / share;
-}
-
 struct TreeSeg {
   int b, j, k0, k1, item, q0, ql, len;
 };
@@ -193,7 +153,7 @@ struct TreeWalk {
     if (u >= u_end) return false;
     while (u >= ubase + s.n * s.m) {
       ubase += s.n * s.m;
-      ibase += s.m * strips_of(s.n, s.m, share);
+      ibase += s.m * tree_strips(s.n, s.m, share);
       s = tree_seq(a, ++b, false);
     }
     const int off = u - ubase;
@@ -256,7 +216,7 @@ __device__ __forceinline__ bool find_share(const TreeArgs& a, int c, int4* start
 #pragma unroll 1
     for (int b = beg; b < end; ++b) {
       const TreeSeq s = tree_seq(a, b, first && pass == 0);
-      const int units = s.n * s.m, items = pass == 0 ? 0 : s.m * strips_of(s.n, s.m, share);
+      const int units = s.n * s.m, items = pass == 0 ? 0 : s.m * tree_strips(s.n, s.m, share);
       if (pass == 0) {
         sum += units;
         broken |= s.broken;
@@ -368,12 +328,6 @@ __device__ __forceinline__ void send16(uint32_t dst, uint32_t bar, uint32_t a, u
       "r"(bar), "r"(a), "r"(b), "r"(c), "r"(d)
       : "memory");
 }
-// Byte offset of 16-byte chunk `chunk` of row `row` in a tile of 64-byte rows with
-// the 64-byte swizzle (chunk XOR (row / 2) mod 4).
-__device__ __forceinline__ uint32_t sw64(int row, int chunk) {
-  return static_cast<uint32_t>(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
-}
-
 // Uses of loaded registers stay behind the wait for the loads.
 __device__ __forceinline__ void loaded(uint32_t (&r)[32]) {
 #pragma unroll
@@ -410,6 +364,14 @@ __device__ __noinline__ void take_query(const uint8_t* stage, int part, int r, u
   tc::wait_st();
   tc::fence_before_sync();
   __syncwarp();
+}
+
+// Where a segment's rows go: to the merged latents if it has all tokens of its
+// q-block (the merge passes such rows over), to its part's slot if not.
+__device__ __forceinline__ float* part_rows(const TreeArgs& a, const TreeSeg& g, int share_idx) {
+  return g.k0 == 0 && g.k1 * kTok >= g.len
+             ? a.o_lat + ((size_t)g.q0 * a.num_heads + (size_t)g.j * kBlockRows) * kDc
+             : a.opart + ((size_t)share_idx + g.item) * kBlockRows * kDc;
 }
 
 // The normalised columns [128 part, 128 part + 128) of this CTA's half of a
@@ -767,7 +729,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!warp_wait(kODone, seg_i & 1) || !warp_wait(kSums, seg_i & 1)) { ok = false; break; }
       tc::fence_after_sync();
       store_rows(trow, 1, sSum[r], seg.ql * a.num_heads - seg.j * kBlockRows - quad * 32,
-                 a.opart + (((size_t)share_idx + seg.item) * kBlockRows + quad * 32) * kDc + 256 * h,
+                 part_rows(a, seg, share_idx) + (size_t)(quad * 32) * kDc + 256 * h,
                  sm + Smem::p + (4 + quad) * 4096, lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kOFree]);
@@ -923,7 +885,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!warp_wait(kODone, seg_i & 1)) { ok = false; break; }
       tc::fence_after_sync();
       store_rows(trow, 0, inv, seg.ql * a.num_heads - seg.j * kBlockRows - quad * 32,
-                 a.opart + ((size_t)slot * kBlockRows + quad * 32) * kDc + 256 * h, sm + Smem::p + quad * 4096, lane);
+                 part_rows(a, seg, share_idx) + (size_t)(quad * 32) * kDc + 256 * h, sm + Smem::p + quad * 4096, lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kOFree]);
       ++seg_i;
@@ -936,267 +898,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc::fence_after_sync();
   if (warp == 1) tc::dealloc(tmem, kTmemCols);
   cl::sync();  // the peer no longer sends into this CTA's shared memory
-}
-
-// ------------------------------------------------------- merge and projection
-// The parts of (row n, head h): `count` of them, part i in slot(i), row r of it.
-struct RowParts {
-  int count, r, share, ubase, ibase, m, j, full, per, tail;
-
-  __device__ __forceinline__ int slot(int i) const {
-    if (m == 1) return ubase / share + i + ibase;
-    if (i < full * per) {
-      const int s = i / per;
-      return ubase / share + s * m + j + i % per + ibase + s * m + j;
-    }
-    const int start = ubase + full * share * m + j * tail;
-    return start / share + (i - full * per) + ibase + full * m + j;
-  }
-};
-__device__ __forceinline__ RowParts row_parts(const TreeArgs& a, int64_t n, int h) {
-  RowParts p{};
-  if (n >= a.num_q) return p;
-  int lo = 0, hi = a.batch;   // the last sequence that begins at or before row n
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.query_start_loc[mid] <= n) lo = mid; else hi = mid;
-  }
-  const int q0 = a.query_start_loc[lo];
-  if (q0 < 0 || n < q0 || n >= a.query_start_loc[lo + 1]) return p;
-  const int4 pl = a.plan[lo];
-  if (pl.w <= 0) return p;
-  p.share = reinterpret_cast<const WsHeader*>(a.ws)->share;
-  p.ubase = pl.x;
-  p.ibase = pl.y;
-  p.m = pl.w;
-  const int rr = ((int)n - q0) * a.num_heads + h;
-  p.j = rr / kBlockRows;
-  p.r = rr % kBlockRows;
-  const int tiles = pl.z;
-  if (p.m == 1) {
-    p.count = (p.ubase + tiles - 1) / p.share - p.ubase / p.share + 1;
-  } else {
-    p.full = tiles / p.share;
-    p.per = p.ubase % p.share ? 2 : 1;
-    p.tail = tiles % p.share;
-    p.count = p.full * p.per;
-    if (p.tail) {
-      const int start = p.ubase + p.full * p.share * p.m + p.j * p.tail;
-      p.count += (start + p.tail - 1) / p.share - start / p.share + 1;
-    }
-  }
-  return p;
-}
-
-// The merge of many parts of few (row, head)s, two CTAs each, of 256 columns:
-// thread (p, c) sums 4 columns over every fourth part.
-__global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
-  __shared__ float4 sAcc[3][64];
-  const int n = blockIdx.x / a.num_heads, h = blockIdx.x % a.num_heads, half = blockIdx.y, tid = threadIdx.x;
-  const int p = tid >> 6, c = half * 64 + (tid & 63), lane = tid & 31;
-  pdl_wait();
-  pdl_launch_dependents();
-  const RowParts rp = row_parts(a, n, h);
-  auto lse_at = [&](int i) { return a.lse[((int64_t)rp.slot(i) * 2 + half) * kBlockRows + rp.r]; };
-  auto o_at = [&](int i) {
-    return *reinterpret_cast<const float4*>(a.opart + ((int64_t)rp.slot(i) * kBlockRows + rp.r) * kDc + 4 * c);
-  };
-  float4 v[8];
-  auto load = [&](int s0) {
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-      if (s0 + 4 * u < rp.count) v[u] = o_at(s0 + 4 * u);
-  };
-  load(p);
-  float m = -INFINITY, den = 0.f;
-  for (int s = lane; s < rp.count; s += 32) m = fmaxf(m, lse_at(s));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float base = m == -INFINITY ? 0.f : m;
-  for (int s = lane; s < rp.count; s += 32) den += fast_exp2(lse_at(s) - base);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-  const float inv = den == 0.f ? 0.f : 1.f / den;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-  for (int s0 = p; s0 < rp.count; s0 += 32) {
-    if (s0 != p) load(s0);
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-      if (s0 + 4 * u < rp.count) {
-        const float w = fast_exp2(lse_at(s0 + 4 * u) - base) * inv;
-        acc.x = fmaf(w, v[u].x, acc.x);
-        acc.y = fmaf(w, v[u].y, acc.y);
-        acc.z = fmaf(w, v[u].z, acc.z);
-        acc.w = fmaf(w, v[u].w, acc.w);
-      }
-  }
-  if (p > 0) sAcc[p - 1][tid & 63] = acc;
-  __syncthreads();
-  if (p == 0) {
-#pragma unroll
-    for (int u = 0; u < 3; ++u) {
-      const float4 x = sAcc[u][tid];
-      acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
-    }
-    *reinterpret_cast<float4*>(a.o_lat + ((size_t)n * a.num_heads + h) * kDc + 4 * c) = acc;
-  }
-}
-
-// The merge of a few parts and the output projection in one: CTA = (ROWS rows,
-// head h). W_uv[h] (128 KB) comes by cp.async while 256 / ROWS threads a row
-// merge its 512 latents to two bf16 terms each, so that the output is rounded
-// once; then 8 warps, each a quarter of K and half of the columns (m16n8k16).
-template <int ROWS>
-struct Pj {
-  static constexpr int stride = kDc * 2 + 16;     // bytes of a merged row, padded against bank conflicts
-  static constexpr int w = 0;                     // two halves of 64 columns, 128-byte rows
-  static constexpr int a = w + kDc * 256;
-  static constexpr int red = a + 2 * ROWS * stride;  // [4][ROWS][128]
-  static constexpr int bytes = red + 4 * ROWS * kDv * 4;
-};
-template <int ROWS, bool MERGED>
-__global__ void __launch_bounds__(256) tree_proj_kernel(const __grid_constant__ TreeArgs a, const __nv_bfloat16* W_uv,
-                                                        __nv_bfloat16* out) {
-  using M = Pj<ROWS>;
-  constexpr int kTr = 256 / ROWS, kVec = kDc / 4 / kTr;     // threads a row, float4s a thread
-  constexpr int kBatch = 16 / kVec;                         // parts at a time
-  extern __shared__ __align__(1024) uint8_t smem_pj[];
-  float* sRed = reinterpret_cast<float*>(smem_pj + M::red);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.y, row0 = blockIdx.x * ROWS, H = a.num_heads;
-  const __nv_bfloat16* src = W_uv + (size_t)h * kDc * kDv;
-#pragma unroll 4
-  for (int i = tid; i < kDc * 16; i += 256) {
-    const int k = i >> 4, c = i & 15;
-    cp_async16(smem_pj + M::w + (c >> 3) * (kDc * 128) + sw128(k, c & 7), src + (size_t)k * kDv + c * 8);
-  }
-  cp_async_commit();
-  pdl_wait();
-  pdl_launch_dependents();
-  {
-    const int r = tid / kTr, j = tid % kTr, n = row0 + r;
-    float4 acc[kVec];
-#pragma unroll
-    for (int k = 0; k < kVec; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (MERGED) {
-      if (n < a.num_q) {
-        const float4* o = reinterpret_cast<const float4*>(a.o_lat + ((size_t)n * H + h) * kDc);
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) acc[k] = o[j + kTr * k];
-      }
-    } else {
-      const RowParts rp = row_parts(a, n, h);
-      auto lse_at = [&](int i, int half) { return a.lse[((int64_t)rp.slot(i) * 2 + half) * kBlockRows + rp.r]; };
-      float4 v[kBatch][kVec];
-      auto load = [&](int s0) {
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-          if (s0 + u < rp.count) {
-            const float4* o =
-                reinterpret_cast<const float4*>(a.opart + ((int64_t)rp.slot(s0 + u) * kBlockRows + rp.r) * kDc);
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) v[u][k] = o[j + kTr * k];
-          }
-      };
-      load(0);
-      float base[2], inv[2];
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        float m = -INFINITY, den = 0.f;
-        for (int s = j; s < rp.count; s += kTr) m = fmaxf(m, lse_at(s, hf));
-#pragma unroll
-        for (int o = kTr / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        base[hf] = m == -INFINITY ? 0.f : m;
-        for (int s = j; s < rp.count; s += kTr) den += fast_exp2(lse_at(s, hf) - base[hf]);
-#pragma unroll
-        for (int o = kTr / 2; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-        inv[hf] = den == 0.f ? 0.f : 1.f / den;
-      }
-#pragma unroll 1
-      for (int s0 = 0; s0 < rp.count; s0 += kBatch) {
-        if (s0 > 0) load(s0);
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-          if (s0 + u < rp.count) {
-            const float w0 = fast_exp2(lse_at(s0 + u, 0) - base[0]) * inv[0];
-            const float w1 = fast_exp2(lse_at(s0 + u, 1) - base[1]) * inv[1];
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) {
-              const float w = k < kVec / 2 ? w0 : w1;       // (columns 4 (j + kTr k))
-              acc[k].x = fmaf(w, v[u][k].x, acc[k].x);
-              acc[k].y = fmaf(w, v[u][k].y, acc[k].y);
-              acc[k].z = fmaf(w, v[u][k].z, acc[k].z);
-              acc[k].w = fmaf(w, v[u][k].w, acc[k].w);
-            }
-          }
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kVec; ++k) {
-      const uint32_t t0 = pack_bf16(acc[k].x, acc[k].y), t1 = pack_bf16(acc[k].z, acc[k].w);
-      auto low = [](uint32_t t) { return __uint_as_float(t << 16); };
-      auto high = [](uint32_t t) { return __uint_as_float(t & 0xffff0000u); };
-      uint8_t* at = smem_pj + M::a + r * M::stride + (j + kTr * k) * 8;
-      *reinterpret_cast<uint2*>(at) = make_uint2(t0, t1);
-      *reinterpret_cast<uint2*>(at + ROWS * M::stride) =
-          make_uint2(pack_bf16(acc[k].x - low(t0), acc[k].y - high(t0)),
-                     pack_bf16(acc[k].z - low(t1), acc[k].w - high(t1)));
-    }
-  }
-  cp_async_wait_all();
-  __syncthreads();
-  const int g = lane >> 2, q = lane & 3, kq = warp >> 1, nh = warp & 1;
-  const uint8_t* sW = smem_pj + M::w + nh * (kDc * 128);
-  float acc[8][4];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-#pragma unroll
-  for (int ks = 0; ks < 8; ++ks) {
-    const int k = kq * 128 + ks * 16;
-    // row g + 8: of the second terms, or a row of its own
-    const uint8_t* lo = smem_pj + M::a + g * M::stride + (k + 2 * q) * 2;
-    auto frag = [&](int row, int at) { return *reinterpret_cast<const uint32_t*>(lo + row * M::stride + at); };
-    const uint32_t a0 = frag(0, 0), a1 = frag(8, 0), a2 = frag(0, 16), a3 = frag(8, 16);
-    uint32_t c0 = 0, c1 = 0, c2 = 0, c3 = 0;
-    if (ROWS == 16) c0 = frag(16, 0), c1 = frag(24, 0), c2 = frag(16, 16), c3 = frag(24, 16);
-    const int kr = k + (lane & 7) + (((lane >> 3) & 1) << 3);
-#pragma unroll
-    for (int np = 0; np < 4; ++np) {
-      uint32_t b0, b1, b2, b3;
-      ldsm_x4_t(smem_u32(sW + sw128(kr, np * 2 + (lane >> 4))), b0, b1, b2, b3);
-      mma_16816(acc[2 * np], a0, a1, a2, a3, b0, b1);
-      mma_16816(acc[2 * np + 1], a0, a1, a2, a3, b2, b3);
-      if (ROWS == 16) {
-        mma_16816(acc[2 * np], c0, c1, c2, c3, b0, b1);
-        mma_16816(acc[2 * np + 1], c0, c1, c2, c3, b2, b3);
-      }
-    }
-  }
-#pragma unroll
-  for (int nt = 0; nt < 8; ++nt) {
-    float* d = sRed + (kq * ROWS + g) * kDv + nh * 64 + nt * 8 + 2 * q;
-    if (ROWS == 16) {
-      *reinterpret_cast<float2*>(d) = make_float2(acc[nt][0], acc[nt][1]);
-      *reinterpret_cast<float2*>(d + 8 * kDv) = make_float2(acc[nt][2], acc[nt][3]);
-    } else {
-      *reinterpret_cast<float2*>(d) = make_float2(acc[nt][0] + acc[nt][2], acc[nt][1] + acc[nt][3]);
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = tid; i < ROWS * kDv / 4; i += 256) {
-    const int r = i / (kDv / 4), c = (i % (kDv / 4)) * 4, row = row0 + r;
-    if (row >= a.num_q) continue;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float4 x = *reinterpret_cast<const float4*>(sRed + (k * ROWS + r) * kDv + c);
-      v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
-    }
-    *reinterpret_cast<uint2*>(out + ((size_t)row * H + h) * kDv + c) =
-        make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-  }
 }
 
 bool al(const void* p, uintptr_t x) { return (reinterpret_cast<uintptr_t>(p) & (x - 1)) == 0; }
@@ -1302,20 +1003,7 @@ mla_status mla_tree_decode(const mla_config* cfg, const void* q_abs, const void*
   if (e == cudaSuccess)
     e = launch_pdl(tree_decode_kernel, dim3(2 * C), dim3(kThreads), Smem::alloc, st, slab4, rope_map, q_map, qrope_map, a);
   if (e != cudaSuccess) return MLA_ERR_CUDA;
-  auto project = [&](auto kernel, int per, int smem) {
-    const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    return r != cudaSuccess ? r
-                            : launch_pdl(kernel, dim3((unsigned)((num_q + per - 1) / per), H), dim3(256), smem, st, a,
-                                         (const __nv_bfloat16*)W_uv, (__nv_bfloat16*)out);
-  };
-  const bool many_parts = num_q * H < 512 && (int64_t)max_blocks_per_seq * bs > 512;
-  if (many_parts) {
-    e = launch_pdl(tree_merge_kernel, dim3((unsigned)(num_q * H), 2), dim3(256), 0, st, a);
-    if (e == cudaSuccess) e = project(tree_proj_kernel<8, true>, 8, Pj<8>::bytes);
-  } else {
-    e = (num_q + 7) / 8 * H <= 2 * C ? project(tree_proj_kernel<8, false>, 8, Pj<8>::bytes)
-                                     : project(tree_proj_kernel<16, false>, 16, Pj<16>::bytes);
-  }
+  e = launch_tree_out(a, W_uv, out, st);
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 

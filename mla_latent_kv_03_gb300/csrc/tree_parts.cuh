@@ -1,0 +1,55 @@
+// What the kernels of mla_tree_decode share: their arguments, their workspace, and
+// where the parts of a (row, head) lie in it.
+#pragma once
+#include "common.cuh"
+#include "internal.h"
+
+namespace mla {
+
+constexpr int kTreeBlockRows = 128;    // (row, head) pairs of a q-block
+constexpr int kTreeTok = 64;           // tokens of a tile
+
+struct TreeArgs {
+  const uint16_t* q_abs;
+  int64_t num_blocks, num_q;
+  const int32_t* block_table;
+  int32_t max_blocks, block_size, num_heads, batch, words, shares;
+  const int32_t* seq_lens;
+  const int32_t* query_start_loc;
+  const uint64_t* mask;
+  float scale_log2;
+  uint8_t* ws;
+  uint32_t* status;
+  int4* plan;      // [batch] {first unit, first item, tiles, q-blocks}
+  float* lse;      // [slots][2][128]
+  float* opart;    // [slots][128][512]
+  float* o_lat;    // [num_q, H, 512]
+};
+
+// Workspace: header (status word, share), plan, partials. An item is what one
+// q-block has in one strip; its part in cluster c has slot c + item, which is
+// unique because items and shares are both contiguous and in order.
+struct TreeWs {
+  size_t plan, lse, opart, o_lat, total;
+};
+__host__ __device__ inline TreeWs tree_ws(int64_t num_q, int heads, int shares, int64_t batch) {
+  TreeWs L;
+  // items: a q-block has one, and one more for every share's worth of its units
+  const int64_t slots = 2 * (int64_t)shares + num_q * heads / kTreeBlockRows + batch + 1;
+  size_t off = kLayoutStart;
+  L.plan = off;   off = align_up(off + (size_t)batch * 16, 256);
+  L.lse = off;    off = align_up(off + (size_t)slots * 2 * kTreeBlockRows * 4, 256);
+  L.o_lat = off;  off = align_up(off + (size_t)num_q * heads * kDc * 4, 256);
+  L.opart = off;  off = align_up(off + (size_t)slots * kTreeBlockRows * kDc * 4, 256);
+  L.total = off;
+  return L;
+}
+
+__host__ __device__ __forceinline__ int tree_strips(int n, int m, int share) {
+  return m <= 1 ? m : (n + share - 1) / share;
+}
+
+// The merge of a call's parts and the projection, after the attention on `st`.
+cudaError_t launch_tree_out(const TreeArgs& a, const void* W_uv, void* out, cudaStream_t st);
+
+}  // namespace mla
