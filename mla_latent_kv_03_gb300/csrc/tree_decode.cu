@@ -106,8 +106,8 @@ struct Smem {
   static constexpr int info = sum + kBlockRows * 4;   // [kStages] int2
   static constexpr int bars = info + kStages * 8;
   static constexpr int misc = bars + kNumBars * 8;        // tmem base, abort flag, tiles ready
-  static constexpr int plan = (misc + 12 + 15) / 16 * 16;  // start of this share: int4; scan scratch
-  static constexpr int bytes = plan + 16 + 2 * (kThreads / 32) * 4;
+  static constexpr int plan = (misc + 12 + 15) / 16 * 16;  // ShareStart
+  static constexpr int bytes = plan + 32 + 12 * (kThreads / 32);
   static constexpr int alloc = bytes + 1024;
 };
 static_assert(Smem::alloc <= 227 * 1024, "shared memory budget");
@@ -179,70 +179,87 @@ struct TreeWalk {
   }
 };
 
-// Exclusive prefix of v over the CTA's threads, and the total.
-__device__ __noinline__ int block_scan(int v, int* scratch, int tid, int* total) {
+// Of the CTA's threads before this one, the sum of v; and of all.
+__device__ __noinline__ int2 block_scan(int2 v, int2* scratch, int tid, int2& all) {
   const int lane = tid & 31, warp = tid >> 5;
-  int incl = v;
-#pragma unroll 1
+  int2 sum = v;
+#pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
+    const int x = __shfl_up_sync(0xffffffffu, sum.x, o), y = __shfl_up_sync(0xffffffffu, sum.y, o);
+    if (lane >= o) sum.x += x, sum.y += y;
   }
-  if (lane == 31) scratch[warp] = incl;
+  if (lane == 31) scratch[warp] = sum;
   __syncthreads();
-  int run = incl - v, all = 0;
-#pragma unroll 1
+  sum.x -= v.x;
+  sum.y -= v.y;
+  all = make_int2(0, 0);
+#pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    const int x = scratch[w];
-    if (w < warp) run += x;
-    all += x;
+    const int2 x = scratch[w];
+    if (w < warp) sum.x += x.x, sum.y += x.y;
+    all.x += x.x;
+    all.y += x.y;
   }
-  *total = all;
-  return run;
+  return sum;
 }
 
-// The split: where share c begins. Every CTA finds it; the first writes the
-// plan that the merge follows.
-__device__ __forceinline__ bool find_share(const TreeArgs& a, int c, int4* start, int* scratch, int tid, TreeWalk& w) {
+// The split: where share c begins. Every CTA finds it, a thread a sequence (of more
+// than the threads, in rounds); the first writes the plan that the merge follows.
+struct ShareStart {
+  int b, ubase, ibase, q0, ql, len, n, m;
+  int sums[kThreads / 32];
+  int2 scan[kThreads / 32];
+};
+__device__ __forceinline__ bool find_share(const TreeArgs& a, int c, ShareStart* st, int tid, TreeWalk& w) {
   const bool first = blockIdx.x == 0;
-  const int per = (a.batch + kThreads - 1) / kThreads;
-  const int beg = min(a.batch, tid * per), end = min(a.batch, beg + per);
-  int ubase = 0, ibase = 0, total = 0, share = 1, u0 = 0;
-  // three passes over a thread's sequences: their units, their items, where they begin
+  TreeSeq s{};
+  int sum = 0;
+  bool broken = false;
 #pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    int sum = 0;
-    bool broken = false;
+  for (int b = tid; b < a.batch; b += kThreads) {
+    s = tree_seq(a, b, first);
+    sum += s.n * s.m;
+    broken |= s.broken;
+  }
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  if ((tid & 31) == 0) st->sums[tid >> 5] = sum;
+  // (rows that two sequences have would not fit the workspace: nothing is done)
+  if (__syncthreads_or(broken)) {
+    if (first)
+      for (int b = tid; b < a.batch; b += kThreads) a.plan[b] = make_int4(0, 0, 0, 0);
+    return false;
+  }
+  int total = 0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) total += st->sums[i];
+  const int share = max(1, (total + a.shares - 1) / a.shares);
+  const int u0 = (int)min((int64_t)c * share, (int64_t)total);
+  int2 base = make_int2(0, 0);
 #pragma unroll 1
-    for (int b = beg; b < end; ++b) {
-      const TreeSeq s = tree_seq(a, b, first && pass == 0);
-      const int units = s.n * s.m, items = pass == 0 ? 0 : s.m * tree_strips(s.n, s.m, share);
-      if (pass == 0) {
-        sum += units;
-        broken |= s.broken;
-      } else if (pass == 1) {
-        sum += items;
-      } else {
-        if (first) a.plan[b] = make_int4(ubase, ibase, s.n, s.m);
-        if (u0 >= ubase && u0 < ubase + units) *start = make_int4(b, ubase, ibase, 0);
-        ubase += units;
-        ibase += items;
-      }
+  for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+    const int b = b0 + tid;
+    if (a.batch > kThreads) {
+      s.n = s.m = 0;
+      if (b < a.batch) s = tree_seq(a, b, false);
+      __syncthreads();         // (the last round's scan is read)
     }
-    if (pass == 0) {
-      // (rows that two sequences have would not fit the workspace: nothing is done)
-      if (__syncthreads_or(broken)) {
-        if (first)
-          for (int b = beg; b < end; ++b) a.plan[b] = make_int4(0, 0, 0, 0);
-        return false;
-      }
-      ubase = block_scan(sum, scratch, tid, &total);
-      share = max(1, (total + a.shares - 1) / a.shares);
-      u0 = (int)min((int64_t)c * share, (int64_t)total);
-    } else if (pass == 1) {
-      int items;
-      ibase = block_scan(sum, scratch + kThreads / 32, tid, &items);
+    const int units = s.n * s.m;
+    int2 all;
+    const int2 at = block_scan(make_int2(units, s.m * tree_strips(s.n, s.m, share)), st->scan, tid, all);
+    const int ubase = base.x + at.x, ibase = base.y + at.y;
+    if (first && b < a.batch) a.plan[b] = make_int4(ubase, ibase, s.n, s.m);
+    if (u0 >= ubase && u0 < ubase + units) {
+      st->b = b;
+      st->ubase = ubase;
+      st->ibase = ibase;
+      st->q0 = s.q0;
+      st->ql = s.ql;
+      st->len = s.len;
+      st->n = s.n;
+      st->m = s.m;
     }
+    base.x += all.x;
+    base.y += all.y;
   }
   if (first && tid == 0) {
     WsHeader* hdr = reinterpret_cast<WsHeader*>(a.ws);
@@ -254,11 +271,14 @@ __device__ __forceinline__ bool find_share(const TreeArgs& a, int c, int4* start
   w.u_end = min(u0 + share, total);
   w.share = share;
   if (w.u >= w.u_end) return false;
-  const int4 st = *start;
-  w.b = st.x;
-  w.ubase = st.y;
-  w.ibase = st.z;
-  w.s = tree_seq(a, w.b, false);
+  w.b = st->b;
+  w.ubase = st->ubase;
+  w.ibase = st->ibase;
+  w.s.q0 = st->q0;
+  w.s.ql = st->ql;
+  w.s.len = st->len;
+  w.s.n = st->n;
+  w.s.m = st->m;
   return true;
 }
 
@@ -474,8 +494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
 
   TreeWalk sw;
-  int* scratch = reinterpret_cast<int*>(sm + Smem::plan + 16);
-  const bool has_work = find_share(a, share_idx, reinterpret_cast<int4*>(sm + Smem::plan), scratch, tid, sw);
+  const bool has_work = find_share(a, share_idx, reinterpret_cast<ShareStart*>(sm + Smem::plan), tid, sw);
   TreeSeg seg;
   auto warp_wait = [&](int bar, uint32_t parity) {
     const bool ok = wait_or_abort(&bars[bar], parity, abort_flag);   // (the same for all lanes)
@@ -624,14 +643,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (leader) {
           const uint32_t d = tmem + kSCol + (uint32_t)(b * kTok);
           const uint64_t at = (uint64_t)((slot * kStage) >> 4);
-// (rolled: this code is fetched anew for every tile)
-#pragma unroll 1
-          for (int pj = 0; pj < 4 * pages; ++pj) {     // page by page, slab by slab
+          if (pages == 1) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              tc::mma_bf16_tmem_a(d + ((pj >> 2) << bs_shift), tmem + kQCol + (uint32_t)((pj & 3) * 32 + c * 8),
-                                  kdesc + at + (uint64_t)(((pj << (bs_shift + 7)) + c * 32) >> 4), id_page,
-                                  (pj & 3) > 0 || c > 0);
+            for (int c = 0; c < 16; ++c)
+              tc::mma_bf16_tmem_a(d, tmem + kQCol + (uint32_t)(c * 8),
+                                  kdesc + at + (uint64_t)(((c >> 2) * kSlab + (c & 3) * 32) >> 4), kIdS, c > 0);
+          } else {
+#pragma unroll 1
+            for (int pj = 0; pj < 4 * pages; ++pj) {     // page by page, slab by slab
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                tc::mma_bf16_tmem_a(d + ((pj >> 2) << bs_shift), tmem + kQCol + (uint32_t)((pj & 3) * 32 + c * 8),
+                                    kdesc + at + (uint64_t)(((pj << (bs_shift + 7)) + c * 32) >> 4), id_page,
+                                    (pj & 3) > 0 || c > 0);
+            }
           }
 #pragma unroll
           for (int c = 0; c < 2; ++c)
@@ -691,51 +716,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&bars[kQReady]);
       return true;
     };
-    bool have = sw.next(a, seg);
-    if (have) ok = query_in();
-    while (have && ok) {
-      const int n = seg.k1 - seg.k0;
-      ri += n;
+    // Once the last tile of a segment is sent, the next one's query comes in and its
+    // first two tiles are sent; the output of the last segment is written after them,
+    // when they are on their way.
+    TreeSeg last;
+    int t = 0, n = 0, store_at = -1;     // -1: nothing waits to be written
+    bool more = sw.next(a, seg);
+    if (more) {
+      n = seg.k1 - seg.k0;
+      ok = query_in();
+    }
 #pragma unroll 1
-      for (int t = 0; t < n; ++t, ++i) {
-        const int b = i & 1;
-        // the peer has read tile i - 2 from the buffer
-        if (i >= 2 && !warp_wait(kPeerFree0 + b, ((i >> 1) - 1) & 1)) { ok = false; break; }
-        if (!warp_wait(kSFull0 + b, (i >> 1) & 1)) { ok = false; break; }
+    while (ok) {
+      if (t == store_at) {
+        if (!warp_wait(kODone, seg_i & 1) || !warp_wait(kSums, seg_i & 1)) { ok = false; break; }
         tc::fence_after_sync();
-        uint32_t sv[2][32];
-        tc::ld32(trow + kSCol + (uint32_t)(b * kTok), sv[0]);
-        tc::ld32(trow + kSCol + (uint32_t)(b * kTok + 32), sv[1]);
-        tc::wait_ld();
-        loaded(sv[0]);
-        loaded(sv[1]);
-        tc::fence_before_sync();
+        store_rows(trow, 1, sSum[r], last.ql * a.num_heads - last.j * kBlockRows - quad * 32,
+                   part_rows(a, last, share_idx) + (size_t)(quad * 32) * kDc + 256 * h,
+                   sm + Smem::p + (4 + quad) * 4096, lane);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kSRead0 + b]);
-        const uint32_t dst = x_peer + (uint32_t)(b * kXBytes), bar = xbar_peer + (uint32_t)b * 8;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint32_t* v = sv[c >> 2] + 8 * (c & 3);
-          send16(dst + c * (kBlockRows * 16), bar, pack_score(v[0], v[1]), pack_score(v[2], v[3]),
-                 pack_score(v[4], v[5]), pack_score(v[6], v[7]));
-        }
+        if (lane == 0) mbar_arrive(&bars[kOFree]);
+        ++seg_i;
+        store_at = -1;
       }
-      if (!ok) break;
-      // every score product of the segment is done: the next query's columns, then
-      // half of this segment's output
-      TreeSeg nxt;
-      const bool more = sw.next(a, nxt);
-      if (more && !query_in()) { ok = false; break; }
-      if (!warp_wait(kODone, seg_i & 1) || !warp_wait(kSums, seg_i & 1)) { ok = false; break; }
+      if (!more) break;
+      if (t == n) {
+        ri += n;
+        last = seg;
+        more = sw.next(a, seg);
+        if (more) {
+          n = seg.k1 - seg.k0;
+          ok = query_in();
+        }
+        t = 0;
+        store_at = more ? min(2, n) : 0;
+        continue;
+      }
+      const int b = i & 1;
+      // the peer has read tile i - 2 from the buffer
+      if (i >= 2 && !warp_wait(kPeerFree0 + b, ((i >> 1) - 1) & 1)) { ok = false; break; }
+      if (!warp_wait(kSFull0 + b, (i >> 1) & 1)) { ok = false; break; }
       tc::fence_after_sync();
-      store_rows(trow, 1, sSum[r], seg.ql * a.num_heads - seg.j * kBlockRows - quad * 32,
-                 part_rows(a, seg, share_idx) + (size_t)(quad * 32) * kDc + 256 * h,
-                 sm + Smem::p + (4 + quad) * 4096, lane);
+      uint32_t sv[2][32];
+      tc::ld32(trow + kSCol + (uint32_t)(b * kTok), sv[0]);
+      tc::ld32(trow + kSCol + (uint32_t)(b * kTok + 32), sv[1]);
+      tc::wait_ld();
+      loaded(sv[0]);
+      loaded(sv[1]);
+      tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kOFree]);
-      seg = nxt;
-      have = more;
-      ++seg_i;
+      if (lane == 0) mbar_arrive(&bars[kSRead0 + b]);
+      const uint32_t dst = x_peer + (uint32_t)(b * kXBytes), bar = xbar_peer + (uint32_t)b * 8;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const uint32_t* v = sv[c >> 2] + 8 * (c & 3);
+        send16(dst + c * (kBlockRows * 16), bar, pack_score(v[0], v[1]), pack_score(v[2], v[3]),
+               pack_score(v[4], v[5]), pack_score(v[6], v[7]));
+      }
+      ++t;
+      ++i;
     }
     if (!ok && lane == 0) fail_out();
   } else if (has_work) {
