@@ -105,9 +105,10 @@ struct Smem {
   static constexpr int sum = rope + kBlockRows * 64;      // [128] 1 / weight sum
   static constexpr int info = sum + kBlockRows * 4;   // [kStages] int2
   static constexpr int bars = info + kStages * 8;
-  static constexpr int misc = bars + kNumBars * 8;        // tmem base, abort flag, tiles ready
-  static constexpr int plan = (misc + 12 + 15) / 16 * 16;  // ShareStart
-  static constexpr int bytes = plan + 32 + 12 * (kThreads / 32);
+  static constexpr int misc = bars + kNumBars * 8;        // tmem base, abort flag, tiles ready, segments laid out
+  static constexpr int plan = (misc + 16 + 15) / 16 * 16;  // ShareStart
+  static constexpr int segs = (plan + 32 + 12 * (kThreads / 32) + 15) / 16 * 16;   // [4] TreeSeg
+  static constexpr int bytes = segs + 4 * 48;
   static constexpr int alloc = bytes + 1024;
 };
 static_assert(Smem::alloc <= 227 * 1024, "shared memory budget");
@@ -137,20 +138,18 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, bool repor
   }
   return s;
 }
-struct TreeSeg {
-  int b, j, k0, k1, item, q0, ql, len;
+struct alignas(16) TreeSeg {
+  int b, j, k0, k1, item, q0, ql, len, more;   // more: another one follows
 };
 
-// Walks the units of one share; every role has its own. (What is done once a
-// segment, and what is done when a wait takes long, is out of line throughout:
-// with its roles' code one behind another the kernel is bound by fetching
-// instructions. Inlined, it was 109 KB and a tile took 3,900 cycles.)
+// Walks the units of one share.
 struct TreeWalk {
   int u, u_end, share, b, ubase, ibase;
   TreeSeq s;
 
-  __device__ __noinline__ bool next(const TreeArgs& a, TreeSeg& g) {
+  __device__ __forceinline__ bool next(const TreeArgs& a, TreeSeg& g) {
     if (u >= u_end) return false;
+#pragma unroll 1
     while (u >= ubase + s.n * s.m) {
       ubase += s.n * s.m;
       ibase += s.m * tree_strips(s.n, s.m, share);
@@ -175,6 +174,7 @@ struct TreeWalk {
       g.item = ibase + strip * s.m + g.j;
     }
     u += g.k1 - g.k0;
+    g.more = u < u_end;
     return true;
   }
 };
@@ -460,6 +460,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Smem::misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Smem::misc + 4);
   int* ready = reinterpret_cast<int*>(sm + Smem::misc + 8);   // tiles whose softmax may begin
+  int* segments = ready + 1;                                  // segments laid out in `list`
+  TreeSeg* list = reinterpret_cast<TreeSeg*>(sm + Smem::segs);
   uint8_t* sStage = sm + Smem::stage;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = (int)cl::rank();
@@ -477,6 +479,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&bars[kXFull0 + i], kXBytes);
     *abort_flag = 0;
     *ready = 0;
+    *segments = 0;
     fence_mbar_init();
   }
   if (warp == 1) tc::alloc(tmem_slot, kTmemCols);
@@ -501,6 +504,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
     return ok;
   };
+  // The copies' warp walks the share and lays its segments out for the others, some 50
+  // cycles a read; each walking by itself, with its state in local memory behind the
+  // stores of the last segment's rows, took 6,000 cycles a segment. A list of four does:
+  // a segment has three stages of the ring or more, so when the copies have come to
+  // segment s + 3, a tile of s + 1 has been through every role.
+  auto segment = [&](int i) {
+    if (!wait_word(segments, i, abort_flag)) return false;
+    seg = list[i & 3];
+    return true;
+  };
   auto fail_out = [&]() {
     set_status(a.status, MLA_DEV_TIMEOUT);
     *abort_flag = 1;
@@ -524,6 +537,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       return free;
     };
     while (ok && sw.next(a, seg)) {
+      if (leader) {
+        list[seg_i & 3] = seg;
+        asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(smem_u32(segments)), "r"(seg_i + 1) : "memory");
+      }
+      __syncwarp();
       const int32_t* bt = a.block_table + (size_t)seg.b * a.max_blocks;
       for (int part = 0; part < 2 && ok; ++part, ++ri) {
         const int slot = ri % kStages;
@@ -590,8 +608,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint64_t pdesc = tc::smem_desc(smem_u32(sm + Smem::p), 16, 1024, tc::kSwizzle128);
     const bool leader = tc::elect_one();
     int i = 0, ri = 0, seg_i = 0;
-    bool ok = true;
-    while (ok && sw.next(a, seg)) {
+    bool ok = true, more = true;
+    while (more) {
+      if (!(ok = segment(seg_i))) break;
+      more = seg.more;
       const int n = seg.k1 - seg.k0;
       ri += 2;
 #pragma unroll 1
@@ -629,8 +649,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint64_t qrdesc = tc::smem_desc(smem_u32(sm + Smem::rope), 16, 512, tc::kSwizzle64);
     const bool leader = tc::elect_one();
     int i = 0, ri = 0, seg_i = 0;
-    bool ok = true;
-    while (ok && sw.next(a, seg)) {
+    bool ok = true, more = true;
+    while (more) {
+      if (!(ok = segment(seg_i))) break;
+      more = seg.more;
       const int n = seg.k1 - seg.k0;
       ri += 2;
       if (!warp_wait(kQReady, seg_i & 1)) { ok = false; break; }
@@ -675,9 +697,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (has_work && warp == 3) {
     // ---------------------------------------------------- what a tile needs
-    int i = 0, ri = 0;
-    bool ok = true;
-    while (ok && sw.next(a, seg)) {
+    int i = 0, ri = 0, seg_i = 0;
+    bool ok = true, more = true;
+    while (ok && more) {
+      if (!(ok = segment(seg_i++))) break;
+      more = seg.more;
       ri += 2;
 #pragma unroll 1
       for (int k = seg.k0; k < seg.k1; ++k, ++i, ++ri) {
@@ -721,11 +745,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // when they are on their way.
     TreeSeg last;
     int t = 0, n = 0, store_at = -1;     // -1: nothing waits to be written
-    bool more = sw.next(a, seg);
-    if (more) {
-      n = seg.k1 - seg.k0;
-      ok = query_in();
-    }
+    int read = 0;                        // segments read
+    bool more = true;
+    ok = segment(read++) && query_in();
+    if (ok) n = seg.k1 - seg.k0;
 #pragma unroll 1
     while (ok) {
       if (t == store_at) {
@@ -743,10 +766,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (t == n) {
         ri += n;
         last = seg;
-        more = sw.next(a, seg);
+        more = seg.more;
         if (more) {
+          ok = segment(read++) && query_in();
           n = seg.k1 - seg.k0;
-          ok = query_in();
         }
         t = 0;
         store_at = more ? min(2, n) : 0;
@@ -785,8 +808,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     float* sSum = reinterpret_cast<float*>(sm + Smem::sum);
     const float scale = a.scale_log2;
     int i = 0, ri = 0, seg_i = 0;
-    bool ok = true;
-    while (ok && sw.next(a, seg)) {
+    bool ok = true, more = true;
+    while (more) {
+      if (!(ok = __all_sync(0xffffffffu, segment(seg_i)))) break;
+      more = seg.more;
       ri += 2;
       const int n = seg.k1 - seg.k0, past = seg.len - seg.ql;
       const int row = (seg.j * kBlockRows + r) / a.num_heads;   // of the sequence
@@ -796,6 +821,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int t = 0; t < n; ++t, ++i, ++ri) {
         const int slot = ri % kStages, b = i & 1;
+        const int tstart = (seg.k0 + t) * kTok, before = past - tstart;   // tokens from here on that precede the tree
+        uint64_t live = ~0ull;
+        if (before < kTok) {
+          live = 0;
+          if (live_row) {
+            live = mask_from(mrow, a.words, max(-before, 0));
+            if (before > 0) live = live << before | ((1ull << before) - 1);
+          }
+        }
         if (!wait_word(ready, i, abort_flag)) ok = false;
         if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
         tc::fence_after_sync();
@@ -823,35 +857,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           add_f16x2(pv[c].z, x[8 * c + 4], x[8 * c + 5]);
           add_f16x2(pv[c].w, x[8 * c + 6], x[8 * c + 7]);
         }
-        const int tstart = (seg.k0 + t) * kTok, v = inf.x, okmask = inf.y;
-        if (v < kTok || okmask != full_mask || tstart + kTok > past) {   // (the same for all threads)
-          uint64_t live = 0;
-          if (live_row) {
-            const int before = past - tstart;     // tokens of the tile that came before the tree
-            live = before >= kTok ? ~0ull : before > 0 ? (1ull << before) - 1 : 0ull;
-            if (before < kTok) {
-              if (before > 0)
-                live |= mask_from(mrow, a.words, 0) << before;
-              else
-                live |= mask_from(mrow, a.words, -before);
-            }
-          }
-          uint64_t there = v < kTok ? (1ull << v) - 1 : ~0ull;
+        if (before < kTok || inf.x < kTok || inf.y != full_mask) {      // (the same for all threads)
+          uint64_t there = inf.x < kTok ? (1ull << inf.x) - 1 : ~0ull;
           for (int p = 0; p < pages; ++p)
-            if (!((okmask >> p) & 1)) there &= ~((bs == 64 ? ~0ull : (1ull << bs) - 1) << (p << bs_shift));
+            if (!((inf.y >> p) & 1)) there &= ~((bs == 64 ? ~0ull : (1ull << bs) - 1) << (p << bs_shift));
           live &= there;
           // A token that is not finite makes a row that sees it NaN, whatever its weight.
-          bool odd = false;
+          bool odd = false, some = there != ~0ull;
 #pragma unroll
           for (int j = 0; j < 64; ++j) {
             const bool seen = ((j < 32 ? (uint32_t)live : (uint32_t)(live >> 32)) >> (j & 31)) & 1;
-            odd |= seen && !(fabsf(x[j]) < INFINITY);
+            const bool wild = !(fabsf(x[j]) < INFINITY);
+            odd |= seen && wild;
+            some |= wild;
             x[j] = seen ? x[j] : -INFINITY;
           }
           if (odd) l = NAN;
-          const int tok = r & 63;    // each thread one token's half of the columns
-          clean_stage(sStage + slot * kStage + ((tok >> bs_shift) << (bs_shift + 9)) + (r >> 6) * 2 * (bs * 128), bs * 128,
-                      tok & (bs - 1), (there >> tok) & 1, tstart + tok >= past);
+          // Each thread one token's half of the columns. (A token that is not finite has
+          // no row with a finite score.)
+          const int tok = r & 63;
+          if (some)
+            clean_stage(sStage + slot * kStage + ((tok >> bs_shift) << (bs_shift + 9)) + (r >> 6) * 2 * (bs * 128), bs * 128,
+                        tok & (bs - 1), (there >> tok) & 1, tstart + tok >= past);
         }
         float mx[22];
 #pragma unroll
