@@ -862,21 +862,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int p = 0; p < pages; ++p)
             if (!((inf.y >> p) & 1)) there &= ~((bs == 64 ? ~0ull : (1ull << bs) - 1) << (p << bs_shift));
           live &= there;
-          // A token that is not finite makes a row that sees it NaN, whatever its weight.
-          bool odd = false, some = there != ~0ull;
+          float2 wild2 = make_float2(0.f, 0.f);      // stays 0 if every score is finite
 #pragma unroll
-          for (int j = 0; j < 64; ++j) {
-            const bool seen = ((j < 32 ? (uint32_t)live : (uint32_t)(live >> 32)) >> (j & 31)) & 1;
-            const bool wild = !(fabsf(x[j]) < INFINITY);
-            odd |= seen && wild;
-            some |= wild;
-            x[j] = seen ? x[j] : -INFINITY;
+          for (int j = 0; j < 64; j += 2)
+            wild2 = fma_f32x2(make_float2(x[j], x[j + 1]), make_float2(0.f, 0.f), wild2);
+          const bool wild = !(wild2.x + wild2.y == 0.f);
+          if (__builtin_expect(wild, 0)) {
+            // A token that is not finite makes a row that sees it NaN, whatever its weight.
+#pragma unroll
+            for (int j = 0; j < 64; ++j)
+              if ((((j < 32 ? (uint32_t)live : (uint32_t)(live >> 32)) >> (j & 31)) & 1) && !(fabsf(x[j]) < INFINITY)) l = NAN;
           }
-          if (odd) l = NAN;
+#pragma unroll
+          for (int j = 0; j < 64; ++j)
+            x[j] = ((j < 32 ? (uint32_t)live : (uint32_t)(live >> 32)) >> (j & 31)) & 1 ? x[j] : -INFINITY;
           // Each thread one token's half of the columns. (A token that is not finite has
           // no row with a finite score.)
           const int tok = r & 63;
-          if (some)
+          if (wild || there != ~0ull)
             clean_stage(sStage + slot * kStage + ((tok >> bs_shift) << (bs_shift + 9)) + (r >> 6) * 2 * (bs * 128), bs * 128,
                         tok & (bs - 1), (there >> tok) & 1, tstart + tok >= past);
         }
