@@ -741,8 +741,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       return true;
     };
     // Once the last tile of a segment is sent, the next one's query comes in and its
-    // first two tiles are sent; the output of the last segment is written after them,
-    // when they are on their way.
+    // first tile is sent; the output of the last segment is written after it, when its
+    // scores are on their way. (After two tiles it is written 3,000 cycles later.)
     TreeSeg last;
     int t = 0, n = 0, store_at = -1;     // -1: nothing waits to be written
     int read = 0;                        // segments read
@@ -772,7 +772,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           n = seg.k1 - seg.k0;
         }
         t = 0;
-        store_at = more ? min(2, n) : 0;
+        store_at = more;
         continue;
       }
       const int b = i & 1;
