@@ -145,6 +145,27 @@ __device__ __forceinline__ uint64_t fixed40(float w) {
 }
 
 // What is left of p after the rejections so far: w <- max(w - Z q, 0) for each.
+template <int N>
+__device__ __forceinline__ void rest_of(float4 (&w)[N], const float4 (&q)[N], const float* z, int r) {
+#pragma unroll
+  for (int u = 0; u < N; ++u) w[u] = make_float4(clamp01(w[u].x), clamp01(w[u].y), clamp01(w[u].z), clamp01(w[u].w));
+#pragma unroll 1
+  for (int k = 0; k < r; ++k) {
+    const float m = -z[k];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      w[u].x = fmaxf(fmaf(m, q[u].x, w[u].x), 0.f);
+      w[u].y = fmaxf(fmaf(m, q[u].y, w[u].y), 0.f);
+      w[u].z = fmaxf(fmaf(m, q[u].z, w[u].z), 0.f);
+      w[u].w = fmaxf(fmaf(m, q[u].w, w[u].w), 0.f);
+    }
+  }
+  if (r > 0) {
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+      w[u] = make_float4(fminf(w[u].x, 1.f), fminf(w[u].y, 1.f), fminf(w[u].z, 1.f), fminf(w[u].w, 1.f));
+  }
+}
 __device__ __forceinline__ float rest_of(float p, float q, const float* z, int r) {
   float w = clamp01(p);
   for (int k = 0; k < r; ++k) w = fmaxf(fmaf(-z[k], q, w), 0.f);
@@ -156,6 +177,8 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const __grid_c
   __shared__ int sUp[kTreeRows], sTok[kTreeRows], sOut[DRAFT ? 1 : kTreeRows];
   __shared__ float sU[kTreeRows], sP[kTreeRows], sQ[DRAFT ? kTreeRows : 1], sZ[DRAFT ? kTreeRows : 1];
   __shared__ uint64_t sWarp[kVerWarps], sCta[2][kVerMaxCl];
+  __shared__ uint64_t sDraw[2][kVerWarps];
+  __shared__ bool sYes[kTreeRows];      // the row is accepted if none of its siblings was rejected
   __shared__ int sCur, sRej, sDone;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int CL = (int)gridDim.y, rank = (int)cl::rank(), b = blockIdx.x;
@@ -192,8 +215,14 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const __grid_c
     sU[i] = a.u[q0 + i];
     if (up >= 0) {
       const size_t at = (size_t)(q0 + up) * V + x;
-      sP[i] = clamp01(a.p[at]);
-      if constexpr (DRAFT) sQ[i] = a.q[at];
+      const float w = clamp01(a.p[at]);
+      double bar = (double)sU[i];
+      if constexpr (DRAFT) {
+        sQ[i] = a.q[at];
+        bar *= (double)sQ[i];
+      }
+      sP[i] = w;
+      sYes[i] = bar < (double)w;
     }
   }
   __syncthreads();
@@ -215,13 +244,14 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const __grid_c
       }
       if (nxt == ql) return true;
       i = nxt;
-      float w;
+      float w = sP[i];
       bool yes;
-      if constexpr (DRAFT) {
+      if (rej == 0) {
+        yes = sYes[i];
+      } else if constexpr (DRAFT) {
         w = rest_of(sP[i], sQ[i], sZ, rej);
         yes = (double)sU[i] * (double)sQ[i] * z < (double)w;
       } else {
-        w = sP[i];
         bool gone = false;   // the token was rejected before
         for (int k = lane; k < rej; k += 32) gone |= sOut[k] == sTok[i];
         if (__any_sync(0xffffffffu, gone)) w = 0.f;
@@ -267,26 +297,25 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const __grid_c
     const float *pr = a.p + first, *qr = DRAFT ? a.q + first : nullptr;
     uint32_t hi = 0, lo = 0;
     for (int v0 = base + 4 * lane; v0 < end; v0 += 128 * kVerUnroll) {
-      float4 pv[kVerUnroll], qv[kVerUnroll];
+      float4 w[kVerUnroll], qv[kVerUnroll];
 #pragma unroll
-      for (int u = 0; u < kVerUnroll; ++u)
-        if (v0 + 128 * u < end) {
-          pv[u] = load4(pr, v0 + 128 * u, off);
-          if (DRAFT && r > 0) qv[u] = load4(qr, v0 + 128 * u, off);
+      for (int u = 0; u < kVerUnroll; ++u) {
+        const int v = v0 + 128 * u;
+        w[u] = v < end ? load4(pr, v, off) : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (DRAFT) qv[u] = v < end && r > 0 ? load4(qr, v, off) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      rest_of(w, qv, sZ, DRAFT ? r : 0);
+#pragma unroll
+      for (int u = 0; u < kVerUnroll; ++u) {
+        const float x[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t h1, l1;
+          fixed40(x[k], h1, l1);
+          hi += h1;
+          lo += l1;
         }
-#pragma unroll
-      for (int u = 0; u < kVerUnroll; ++u)
-        if (v0 + 128 * u < end) {
-          float w[4] = {pv[u].x, pv[u].y, pv[u].z, pv[u].w};
-          const float d[4] = {qv[u].x, qv[u].y, qv[u].z, qv[u].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t h1, l1;
-            fixed40(DRAFT ? rest_of(w[k], d[k], sZ, r) : clamp01(w[k]), h1, l1);
-            hi += h1;
-            lo += l1;
-          }
-        }
+      }
     }
     uint64_t s = ((uint64_t)hi << 20) + lo;
     if constexpr (!DRAFT) {   // the rejected tokens of this piece weigh nothing
@@ -355,41 +384,52 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const __grid_c
     goal -= sCta[par][c];
   }
   if (goal >= sCta[par][rank]) return;
-  for (int w = 0; w < warp; ++w) {
-    if (goal < sWarp[w]) return;
-    goal -= sWarp[w];
-  }
-  if (goal >= sWarp[warp]) return;
+  int piece = 0;
+  for (; goal >= sWarp[piece]; ++piece) goal -= sWarp[piece];
+  // all of the CTA looks through that warp's piece
   const size_t first = (size_t)(q0 + row) * V;
-  const int off = (int)(first & 3), end = min(base + a.warp_tokens, V + off);
+  const int off = (int)(first & 3), from = (rank * kVerWarps + piece) * a.warp_tokens;
+  const int end = min(from + a.warp_tokens, V + off);
   const float *pr = a.p + first, *qr = DRAFT ? a.q + first : nullptr;
-  for (int v0 = base; v0 < end; v0 += 128) {
-    const int v = v0 + 4 * lane;
-    float4 pv = make_float4(0.f, 0.f, 0.f, 0.f), qv = pv;
+  for (int v0 = from, flip = 0; v0 < end; v0 += 4 * kVerThreads, flip ^= 1) {
+    const int v = v0 + 4 * tid;
+    float4 w[1], qv[1];
+    w[0] = qv[0] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (v < end) {
-      pv = load4(pr, v, off);
-      if (DRAFT && r > 0) qv = load4(qr, v, off);
+      w[0] = load4(pr, v, off);
+      if (DRAFT && r > 0) qv[0] = load4(qr, v, off);
     }
-    const float w[4] = {pv.x, pv.y, pv.z, pv.w}, d[4] = {qv.x, qv.y, qv.z, qv.w};
+    rest_of(w, qv, sZ, DRAFT ? r : 0);
+    const float x[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
     uint64_t f[4], own = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      f[k] = fixed40(DRAFT ? rest_of(w[k], d[k], sZ, r) : clamp01(w[k]));
-      if constexpr (!DRAFT) {
-        for (int m = 0; m < r; ++m)
-          if (sOut[m] == v + k - off) f[k] = 0;
+    for (int k = 0; k < 4; ++k) f[k] = fixed40(x[k]);
+    if constexpr (!DRAFT) {
+      for (int m = 0; m < r; ++m) {
+        const int k = sOut[m] + off - v;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (k == u) f[u] = 0;
       }
-      own += f[k];
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) own += f[k];
     uint64_t upto = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
+      const uint64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
     }
-    const uint32_t hit = __ballot_sync(0xffffffffu, upto > goal);
-    if (hit) {
-      if (lane == __ffs(hit) - 1) {
+    if (lane == 31) sDraw[flip][warp] = upto;
+    __syncthreads();
+    uint64_t all = 0;
+#pragma unroll
+    for (int k = 0; k < kVerWarps; ++k) {
+      if (k == warp) upto += all;
+      all += sDraw[flip][k];
+    }
+    if (goal < all) {
+      if (goal < upto && goal >= upto - own) {
         uint64_t run = upto - own;
         int k = 0;
         while (k < 3 && (run += f[k]) <= goal) ++k;
@@ -397,7 +437,7 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const __grid_c
       }
       return;
     }
-    goal -= __shfl_sync(0xffffffffu, upto, 31);
+    goal -= all;
   }
 }
 
