@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const __grid_c
   __shared__ int sUp[kTreeRows], sTok[kTreeRows], sOut[DRAFT ? 1 : kTreeRows];
   __shared__ float sU[kTreeRows], sP[kTreeRows], sQ[DRAFT ? kTreeRows : 1], sZ[DRAFT ? kTreeRows : 1];
   __shared__ uint64_t sWarp[kVerWarps], sCta[2][kVerMaxCl];
-  __shared__ uint64_t sDraw[2][kVerWarps];
+  __shared__ uint64_t sDraw[2][kVerWarps], sGoal;
   __shared__ bool sYes[kTreeRows];      // the row is accepted if none of its siblings was rejected
   __shared__ int sCur, sRej, sDone;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const __grid_c
   pdl_wait();
   pdl_launch_dependents();
   const int q0 = a.query_start_loc[b], q1 = a.query_start_loc[b + 1];
+  const float last_u = tid == 0 ? a.u_last[b] : 0.f;
   const int ql = q1 - q0;
   const bool bad = q0 < 0 || q1 > a.num_q || ql < 0 || ql > kTreeRows;
   if (bad || ql == 0) {   // (the whole cluster)
@@ -355,7 +356,7 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const __grid_c
     done = sDone;
     // (a rejection's sums are the last draw's too, where no row follows it)
     if (!done || !DRAFT || sRej == 0) sum_all(sCur, sRej);
-    if (DRAFT && !done) z = (double)(float)((double)total * 0x1p-40);
+    if (DRAFT && !done && warp == 0) z = (double)(__ull2float_rn(total) * 0x1p-40f);
   }
   int row = sCur, r = sRej;
   if (total == 0 && r > 0) {   // nothing is left: the target's own distribution
@@ -376,8 +377,10 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const __grid_c
   }
   if (total == 0) return;
   // the first token whose running sum passes u * total: its CTA, its warp, it
-  const double ud = fmax((double)a.u_last[b], 0.0);
-  uint64_t goal = min((uint64_t)__double2ull_rd(ud * (double)total), total - 1);
+  // (64-bit products by one thread: of all 512 they take 1,000 cycles)
+  if (tid == 0) sGoal = min((uint64_t)__double2ull_rd(fmax((double)last_u, 0.0) * (double)total), total - 1);
+  __syncthreads();
+  uint64_t goal = sGoal;
   const int par = (passes - 1) & 1;
   for (int c = 0; c < rank; ++c) {
     if (goal < sCta[par][c]) return;
