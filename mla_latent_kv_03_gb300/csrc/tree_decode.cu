@@ -507,10 +507,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // The copies' warp walks the share and lays its segments out for the others, some 50
   // cycles a read; each walking by itself, with its state in local memory behind the
   // stores of the last segment's rows, took 6,000 cycles a segment. A list of four does:
-  // a segment has three stages of the ring or more, so when the copies have come to
-  // segment s + 3, a tile of s + 1 has been through every role.
+  // a segment has three stages of the ring or more, so when the copies come to segment
+  // s + 3, the last tile of s has been through every role, and s - 1 is not read again.
   auto segment = [&](int i) {
-    if (!wait_word(segments, i, abort_flag)) return false;
+    if (!__all_sync(0xffffffffu, wait_word(segments, i, abort_flag))) return false;
     seg = list[i & 3];
     return true;
   };
@@ -810,7 +810,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int i = 0, ri = 0, seg_i = 0;
     bool ok = true, more = true;
     while (more) {
-      if (!(ok = __all_sync(0xffffffffu, segment(seg_i)))) break;
+      if (!(ok = segment(seg_i))) break;
       more = seg.more;
       ri += 2;
       const int n = seg.k1 - seg.k0, past = seg.len - seg.ql;

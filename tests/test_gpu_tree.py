@@ -320,6 +320,85 @@ def test_decode_workspace_of_more_rows_streams_and_replay():
     b.check()
 
 
+@pytest.mark.parametrize("heads,seqs,num_ctas", [
+    (16, [(5, 64)] * 5 + [(900, 40)], 0),                # many rows: some with all their tokens in one share
+    (128, [(30, 9)] * 3 + [(700, 4)], 0),
+    (16, [(3, 1), (200, 2), (0, 1), (64, 1)] * 120, 0),  # more sequences than a CTA's threads
+    (16, [(7, 1024), (0, 900)], 0),                      # the widest masks
+    (16, [(5200, 8)], 0),                                # more than 32 parts a row: few rows
+    (16, [(0, 1)] * 15 + [(5200, 2)] + [(1, 1)] * 16, 0),  # and many
+    (16, [(2500, 3), (0, 1), (90, 40)], 300),            # shares of a tile
+])
+def test_decode_of_many_rows_sequences_and_parts(heads, seqs, num_ctas):
+    b = Batch(seqs, heads=heads, seed=len(seqs), num_ctas=num_ctas).fill()
+    b.decode()
+    assert bits(b.ws) == 0
+    # (of the largest, the heads at the ends)
+    b.check(heads=None if b.nq * heads * max(b.lens) < 2e7 else [0, heads - 1])
+
+
+def test_decode_rows_behind_the_last_sequence():
+    b = Batch([(100, 5), (37, 6)], seed=31).fill()
+    b.decode()
+    q = torch.full((b.nq + 21, 16, 576), float("nan"), dtype=torch.bfloat16, device=DEV)
+    q[:b.nq] = b.t_q
+    mask = torch.full((b.nq + 21, 1), -1, dtype=torch.int64, device=DEV)
+    mask[:b.nq] = b.t_mask
+    out = torch.full((b.nq + 21, 16, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    ws = torch.full((L.mla_tree_decode_workspace_size(b.cfg, b.nq + 21, 2),), 255, dtype=torch.uint8, device=DEV)
+    L.mla_workspace_init(ws)
+    L.mla_tree_decode(b.cfg, q, b.cache, b.t_table, b.t_lens, b.t_qsl, mask, b.t_W, ws, out)
+    # (Not bit for bit what 11 rows alone give: with 512 (row, head)s or more the parts
+    # are added one behind another, with fewer in four groups. Both are within the bound,
+    # whose fp32 term counts any order.)
+    b.check(out[:b.nq])
+    assert not out[b.nq:].any() and bits(ws) == 0
+
+
+def test_decode_of_pages_that_sequences_share():
+    """Two sequences over the same pages, with trees of their own."""
+    b = Batch([(150, 7), (150, 7)], seed=17, trees=[[-1, 0, 0, 1, 2, 2, 5], [-1, 0, 1, 2, 3, 4, 5]]).fill()
+    b.rows[1] = b.rows[0]
+    b.t_table[1] = b.t_table[0]
+    b.decode()
+    b.check()
+
+
+def test_decode_on_two_streams_at_once():
+    bs = [Batch([(1200, 8)] * 6, seed=41).fill(), Batch([(40, 60), (2000, 3)], heads=32, bs=16, seed=42).fill()]
+    want = [b.decode().clone() for b in bs]
+    streams = [torch.cuda.Stream() for _ in bs]
+    for b in bs:
+        b.out.fill_(7.0)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for b, s in zip(bs, streams):
+            L.mla_tree_decode(b.cfg, b.t_q, b.cache, b.t_table, b.t_lens, b.t_qsl, b.t_mask, b.t_W, b.ws, b.out, stream=s)
+    torch.cuda.synchronize()
+    for b, w in zip(bs, want):
+        assert torch.equal(b.out, w) and bits(b.ws) == 0
+
+
+def test_decode_and_commit_behind_four_gigabytes():
+    b = Batch([(130, 8), (3, 5)], seed=19).fill()
+    far = (1 << 32) // (64 * 1152) + 5                   # pages whose bytes begin past 2^32
+    cache = torch.zeros((far + b.nb, 64, 576), dtype=torch.bfloat16, device=DEV)
+    cache[far:] = b.cache
+    want = b.decode().clone()
+    table = torch.where(b.t_table >= 0, b.t_table + far, b.t_table)
+    b.out.fill_(7.0)
+    L.mla_tree_decode(b.cfg, b.t_q, cache, table, b.t_lens, b.t_qsl, b.t_mask, b.t_W, b.ws, b.out)
+    assert torch.equal(b.out, want) and bits(b.ws) == 0
+    path, n = dev([[0, 3, 5, 7], [1, 4, -1, -1]], torch.int32), dev([4, 2], torch.int32)
+    new = torch.zeros(2, dtype=torch.int32, device=DEV)
+    b.cache.nan_to_num_(0.0)
+    cache.nan_to_num_(0.0)
+    L.mla_tree_commit(b.cfg, b.cache[None], b.t_table, b.t_lens, b.t_qsl, path, n, new, dev_status=b.status)
+    L.mla_tree_commit(b.cfg, cache[None], table, b.t_lens, b.t_qsl, path, n, new, dev_status=b.status)
+    assert torch.equal(cache[far:], b.cache) and not cache[:far].any()
+    assert new.tolist() == [134, 5] and bits(b.status) == 0
+
+
 # ---------------------------------------------------------------------- verify
 class Verify:
     def __init__(self, trees, V, drawn, seed=0, near=0.4, temp=1.5):
@@ -436,6 +515,62 @@ def test_verify_flags_bad_rows():
     v.trees[1][2], v.qsl = 1, np.array([0, 3, 6, 9])     # past the rows
     v.run()
     assert bits(v.status) == L.DEV_BAD_SEQ and int(v.lens[2]) == 0 and int(v.nxt[2]) == -1
+
+
+@pytest.mark.parametrize("drawn", [True, False])
+def test_verify_pieces_of_several_rounds(drawn):
+    """One CTA a sequence, whose warps' pieces the draw looks through in rounds."""
+    v = Verify([[-1, 0]] * 160, 40000, drawn, seed=12).run()
+    v.check()
+    assert bits(v.status) == 0
+
+
+def test_plan_verify_and_commit_captured_and_replayed():
+    trees = [[-1, 0, 0, 1, 2, 2, 4], [-1, 0, 1, 2, 3, 4, 5], [-1, 0, 0, 0, 0, 0, 0]]
+    past = [70, 0, 33]
+    b = Batch([(p, 7) for p in past], trees=trees, seed=23)
+    rng = np.random.default_rng(23)
+    V = 777
+    first = Verify(trees, V, True, seed=1, near=0.2)
+    i32, f32 = torch.int32, torch.float32
+    par = dev(sum(trees, []), i32)
+    p, q, tok, u, f = dev(first.p, f32), dev(first.q, f32), dev(first.tok, i32), dev(first.u, f32), dev(first.f, f32)
+    mask = torch.zeros((21, 1), dtype=torch.int64, device=DEV)
+    pos = torch.zeros(21, dtype=i32, device=DEV)
+    slots = torch.zeros(21, dtype=torch.int64, device=DEV)
+    path = torch.zeros((3, 7), dtype=i32, device=DEV)
+    n, nxt, new = (torch.zeros(3, dtype=i32, device=DEV) for _ in range(3))
+    cache = torch.zeros((2, b.nb, 64, 576), dtype=torch.bfloat16, device=DEV)
+
+    def calls():
+        L.mla_tree_plan(b.cfg, par, b.t_lens, b.t_qsl, b.t_table, b.nb, mask, pos, slots, dev_status=b.status)
+        L.mla_tree_verify(p, q, tok, par, b.t_qsl, u, f, path, n, nxt, dev_status=b.status)
+        L.mla_tree_commit(b.cfg, cache, b.t_table, b.t_lens, b.t_qsl, path, n, new, dev_status=b.status)
+
+    calls()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls()
+    for seed in (2, 3, 4):
+        v = Verify(trees, V, True, seed=seed, near=0.2)
+        for t, x in ((p, v.p), (q, v.q), (tok, v.tok), (u, v.u), (f, v.f)):
+            t.copy_(dev(x, t.dtype))
+        rows = rng.standard_normal((2, b.nb, 64, 576)).astype(np.float32)
+        cache.copy_(dev(rows, torch.bfloat16))
+        want = to_f64(cache).reshape(2, -1, 576)
+        g.replay()
+        torch.cuda.synchronize()
+        assert bits(b.status) == 0 and np.array_equal(mask.cpu().numpy(), b.mask_words())
+        for i, t in enumerate(trees):
+            r = slice(7 * i, 7 * i + 7)
+            kept, after = T.verify(v.p[r], v.q[r], v.tok[r], t, v.u[r], v.f[i])
+            assert path[i].tolist() == kept + [-1] * (7 - len(kept)) and int(nxt[i]) == after
+            assert int(n[i]) == len(kept) and int(new[i]) == past[i] + len(kept)
+            at = np.array([b.table[i, j // 64] * 64 + j % 64 for j in range(past[i] + 7)])
+            for layer in range(2):
+                want[layer, at] = T.commit(want[layer, at], past[i], kept)
+        assert np.array_equal(to_f64(cache).reshape(2, -1, 576), want)
 
 
 # ---------------------------------------------------------------------- commit
