@@ -120,8 +120,12 @@ __global__ void __launch_bounds__(512) tree_merge_few_kernel(const __grid_consta
       make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
 }
 
-// Of many: 16 (row, head)s to a CTA, whose parts 16 threads find; then a warp for
-// each of two, as above but for all of its parts and columns.
+// Of 512 (row, head)s or more: 16 to a CTA, whose parts 16 threads find; then a warp for
+// each of two, as above but for all of its parts and columns. Bound by latency: a few
+// dependent loads a row. With a warp or with eight rows to each step of its own, or
+// more CTAs an SM and fewer parts ahead, a call of 64 x 4,096 tokens took 1 to 8 us
+// longer (of 100); a CTA a row, as few rows have it, 7 us longer, and 31 us longer
+// for 49,280 (row, head)s of short sequences.
 __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
   constexpr int kAhead = 4;
   __shared__ RowParts sParts[16];
