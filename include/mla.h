@@ -462,6 +462,9 @@ mla_status mla_tree_plan(const mla_config* cfg, const int32_t* parents, const in
  *   that no sequence has. A token that a row does not see has no part in it,
  *   whatever its latent holds (NaN, infinities); among the tokens that it does
  *   see, one that is not finite makes it NaN.
+ * A weight is rounded to bf16 before the product (the sum adds the rounded ones),
+ * and one of the two halves that q_abs . row_t is summed in (256 latent and 32 rope
+ * columns each) to f16: 2^-11 of that half, which ends at 65,504.
  * Limits: those of mla_page8_decode, with num_q times a block table's tokens at
  * most 2^35; a sequence of more than 64 * mask_words rows sets MLA_DEV_BAD_SEQ
  * and gets zeros, as do all when query_start_loc does not ascend.
