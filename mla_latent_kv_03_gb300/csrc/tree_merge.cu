@@ -3,6 +3,7 @@
 //   out[n,h] = o_lat[n,h] W_uv[h]        ([512] . [512, 128]).
 #include "async_copy.cuh"
 #include "pair_math.cuh"
+#include "tcgen05.cuh"
 #include "tree_parts.cuh"
 
 namespace mla {
@@ -120,108 +121,274 @@ __global__ void __launch_bounds__(512) tree_merge_few_kernel(const __grid_consta
       make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
 }
 
-// Of 512 (row, head)s or more: 16 to a CTA, whose parts 16 threads find; then a warp for
-// each of two, as above but for all of its parts and columns. Bound by latency: a few
-// dependent loads a row. With a warp or with eight rows to each step of its own, or
-// more CTAs an SM and fewer parts ahead, a call of 64 x 4,096 tokens took 1 to 8 us
-// longer (of 100); a CTA a row, as few rows have it, 7 us longer, and 31 us longer
-// for 49,280 (row, head)s of short sequences.
-__global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
+// The merge and the projection in one, for many (row, head)s: CTA = (R rows, head
+// h). A warp finds the parts of every eighth row, loads and weighs them, and
+// splits each to two bf16 terms, so that the output is rounded once. The products have
+// the output's columns as the 128 rows of the accumulator and the terms as its 2 R
+// columns: W_uv[h], 64 k-rows a stage by TMA, is the first operand as it lies in memory.
+// Bound by the parts' bytes from the L2 and by latency: behind the attention it adds
+// 13 us to a call of 64 x 4,096 tokens and 8 rows; a merge that wrote the latents, and a
+// projection that read them, added 26.
+template <int R>
+struct Pt {
+  static constexpr int stages = 3;
+  static constexpr int chunk = 2 * R * 128;       // 64 latents of the rows' first, then of their second terms
+  static constexpr int wstage = 64 * 256;         // two slabs of 64 columns
+  static constexpr int w = 0;
+  static constexpr int terms = w + stages * wstage;
+  static constexpr int bars = terms + 8 * chunk;  // full[stages], free[stages], done
+  static constexpr int misc = bars + (2 * stages + 1) * 8;
+  static constexpr int bytes = misc + 16;
+  static constexpr uint32_t cols = 2 * R < 32 ? 32 : 2 * R;
+};
+template <int R>
+__global__ void __launch_bounds__(256, 2)
+    tree_merge_proj_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ TreeArgs a, __nv_bfloat16* out) {
+  using M = Pt<R>;
   constexpr int kAhead = 4;
-  __shared__ RowParts sParts[16];
+  extern __shared__ __align__(1024) uint8_t smem_pt[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem_pt + M::bars);
+  uint64_t* free_ = full + M::stages;
+  uint64_t* done = free_ + M::stages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_pt + M::misc);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int first = blockIdx.x * 16, all = (int)(a.num_q * a.num_heads);
+  const int h = blockIdx.y, row0 = blockIdx.x * R, H = a.num_heads;
+  auto load_w = [&](int c) {
+    uint64_t* bar = full + c % M::stages;
+    uint8_t* dst = smem_pt + M::w + c % M::stages * M::wstage;
+    mbar_arrive_expect_tx(bar, M::wstage);
+    tma_load_2d(dst, &w_map, 0, h * kDc + 64 * c, bar);
+    tma_load_2d(dst + M::wstage / 2, &w_map, 64, h * kDc + 64 * c, bar);
+  };
+  if (tid == 0) {
+    for (int i = 0; i < 2 * M::stages + 1; ++i) mbar_init(full + i, 1);
+    fence_mbar_init();
+    for (int c = 0; c < M::stages; ++c) load_w(c);     // (W_uv does not depend on earlier kernels)
+  }
+  if (warp == 0) tc::alloc(tmem_slot, M::cols);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
   pdl_wait();
   pdl_launch_dependents();
-  bool work = false;
-  if (tid < 16) {
-    RowParts rp{};
-    rp.count = 1;
-    if (first + tid < all) rp = row_parts(a, (first + tid) / a.num_heads, (first + tid) % a.num_heads);
-    sParts[tid] = rp;
-    work = rp.count != 1;
+  // A row's two terms: latents 4 lane + 128 k and on, in chunk 2 k + lane / 16.
+  auto put = [&](int r, const float4 (&x)[4]) {
+    auto low = [](uint32_t t) { return __uint_as_float(t << 16); };
+    auto high = [](uint32_t t) { return __uint_as_float(t & 0xffff0000u); };
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t t0 = pack_bf16(x[k].x, x[k].y), t1 = pack_bf16(x[k].z, x[k].w);
+      uint8_t* at = smem_pt + M::terms + (2 * k + (lane >> 4)) * M::chunk + sw128(r, (lane & 15) >> 1) + (lane & 1) * 8;
+      *reinterpret_cast<uint2*>(at) = make_uint2(t0, t1);
+      *reinterpret_cast<uint2*>(at + R * 128) =
+          make_uint2(pack_bf16(x[k].x - low(t0), x[k].y - high(t0)), pack_bf16(x[k].z - low(t1), x[k].w - high(t1)));
+    }
+  };
+  auto add = [](float4 (&acc)[4], const float4 (&v)[4], float x0, float x1) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float x = k < 2 ? x0 : x1;
+      acc[k].x = fmaf(x, v[k].x, acc[k].x);
+      acc[k].y = fmaf(x, v[k].y, acc[k].y);
+      acc[k].z = fmaf(x, v[k].z, acc[k].z);
+      acc[k].w = fmaf(x, v[k].w, acc[k].w);
+    }
+  };
+  // This warp's rows are row0 + warp + 8 j; kLanes lanes find the parts of each.
+  constexpr int kLanes = 32 / (R / 8);
+  const RowParts mine = row_parts(a, row0 + warp + 8 * (lane / kLanes), h);
+  const int i = lane % kLanes;
+  const bool few = mine.count <= kLanes, have = few && i < mine.count;
+  const float4* src = reinterpret_cast<const float4*>(a.o_lat);
+  float l0 = -INFINITY, l1 = -INFINITY;
+  if (have && mine.count == 1) {
+    src += ((size_t)(row0 + warp + 8 * (lane / kLanes)) * H + h) * (kDc / 4);
+    l0 = l1 = 0.f;
+  } else if (have) {
+    const int64_t slot = mine.slot(i);
+    src = reinterpret_cast<const float4*>(a.opart) + (slot * kTreeBlockRows + mine.r) * (kDc / 4);
+    l0 = a.lse[slot * 2 * kTreeBlockRows + mine.r];
+    l1 = a.lse[(slot * 2 + 1) * kTreeBlockRows + mine.r];
   }
-  if (!__syncthreads_or(work)) return;
+  float m0 = l0, m1 = l1;
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) {
+    m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+    m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+  }
+  float w0 = fast_exp2(l0 - (m0 == -INFINITY ? 0.f : m0)), w1 = fast_exp2(l1 - (m1 == -INFINITY ? 0.f : m1));
+  float d0 = w0, d1 = w1;
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) {
+    d0 += __shfl_xor_sync(0xffffffffu, d0, o);
+    d1 += __shfl_xor_sync(0xffffffffu, d1, o);
+  }
+  w0 = d0 == 0.f ? 0.f : w0 / d0;         // (a row that sees nothing: weights of 0)
+  w1 = d1 == 0.f ? 0.f : w1 / d1;
+  // all parts of all rows one behind another, kAhead on their way at a time
+  float4 acc[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  uint32_t todo = __ballot_sync(0xffffffffu, have);
+  const uint32_t none = __ballot_sync(0xffffffffu, mine.count == 0 && i == 0), many = __ballot_sync(0xffffffffu, !few && i == 0);
 #pragma unroll 1
-  for (int at = warp; at < 16; at += 8) {
-    const RowParts rp = sParts[at];
-    if (rp.count == 1) continue;
-    auto part = [&](int i, int& slot, float& l0, float& l1) {
+  for (uint32_t rows = none; rows; rows &= rows - 1) put(warp + 8 * ((__ffs(rows) - 1) / kLanes), acc);
+#pragma unroll 1
+  while (todo) {
+    float4 v[kAhead][4];
+    uint32_t left = todo;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int from = left ? __ffs(left) - 1 : 0;
+      const float4* p = reinterpret_cast<const float4*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), from));
+      if (left) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[u][k] = __ldcs(p + lane + 32 * k);
+      }
+      left &= left - 1;
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (!todo) break;
+      const int from = __ffs(todo) - 1;
+      todo &= todo - 1;
+      add(acc, v[u], __shfl_sync(0xffffffffu, w0, from), __shfl_sync(0xffffffffu, w1, from));
+      if (!todo || (__ffs(todo) - 1) / kLanes != from / kLanes) {     // the row's last part
+        put(warp + 8 * (from / kLanes), acc);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+  }
+  // rows of more parts: 32 at a time
+#pragma unroll 1
+  for (uint32_t rows = many; rows; rows &= rows - 1) {
+    const int owner = __ffs(rows) - 1, r = warp + 8 * (owner / kLanes);
+    const RowParts rp = row_parts(a, row0 + r, h);
+    auto part = [&](int n, int& slot, float& x0, float& x1) {
       slot = 0;
-      l0 = l1 = -INFINITY;
-      if (i < rp.count) {
-        slot = rp.slot(i);
-        l0 = a.lse[(int64_t)slot * 2 * kTreeBlockRows + rp.r];
-        l1 = a.lse[((int64_t)slot * 2 + 1) * kTreeBlockRows + rp.r];
+      x0 = x1 = -INFINITY;
+      if (n < rp.count) {
+        slot = rp.slot(n);
+        x0 = a.lse[(int64_t)slot * 2 * kTreeBlockRows + rp.r];
+        x1 = a.lse[((int64_t)slot * 2 + 1) * kTreeBlockRows + rp.r];
       }
     };
-    int slot;
-    float l0, l1, m0 = -INFINITY, m1 = -INFINITY, d0 = 0.f, d1 = 0.f;
+    int slot = 0;
+    float x0, x1, n0 = -INFINITY, n1 = -INFINITY, e0 = 0.f, e1 = 0.f;
 #pragma unroll 1
     for (int s0 = 0; s0 < rp.count; s0 += 32) {
-      part(s0 + lane, slot, l0, l1);
-      m0 = fmaxf(m0, l0);
-      m1 = fmaxf(m1, l1);
+      part(s0 + lane, slot, x0, x1);
+      n0 = fmaxf(n0, x0);
+      n1 = fmaxf(n1, x1);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-      m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+      n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, o));
+      n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, o));
     }
-    if (m0 == -INFINITY) m0 = 0.f;
-    if (m1 == -INFINITY) m1 = 0.f;
-    float4 acc[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (n0 == -INFINITY) n0 = 0.f;
+    if (n1 == -INFINITY) n1 = 0.f;
 #pragma unroll 1
     for (int s0 = 0; s0 < rp.count; s0 += 32) {
-      if (rp.count > 32) part(s0 + lane, slot, l0, l1);
-      const float w0 = fast_exp2(l0 - m0), w1 = fast_exp2(l1 - m1);
-      d0 += w0;
-      d1 += w1;
+      part(s0 + lane, slot, x0, x1);
+      x0 = fast_exp2(x0 - n0);
+      x1 = fast_exp2(x1 - n1);
+      e0 += x0;
+      e1 += x1;
       const int live = min(32, rp.count - s0);
 #pragma unroll 1
       for (int u0 = 0; u0 < live; u0 += kAhead) {
         float4 v[kAhead][4];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-          const int at1 = __shfl_sync(0xffffffffu, slot, (u0 + u) & 31);
-          const float4* src = reinterpret_cast<const float4*>(a.opart + ((int64_t)at1 * kTreeBlockRows + rp.r) * kDc) + lane;
+          const int from = __shfl_sync(0xffffffffu, slot, (u0 + u) & 31);
+          const float4* p = reinterpret_cast<const float4*>(a.opart + ((int64_t)from * kTreeBlockRows + rp.r) * kDc) + lane;
           if (u0 + u < live) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[u][k] = __ldcs(src + 32 * k);
+            for (int k = 0; k < 4; ++k) v[u][k] = __ldcs(p + 32 * k);
           }
         }
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          const float x0 = __shfl_sync(0xffffffffu, w0, (u0 + u) & 31), x1 = __shfl_sync(0xffffffffu, w1, (u0 + u) & 31);
-          if (u0 + u < live) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float x = k < 2 ? x0 : x1;
-              acc[k].x = fmaf(x, v[u][k].x, acc[k].x);
-              acc[k].y = fmaf(x, v[u][k].y, acc[k].y);
-              acc[k].z = fmaf(x, v[u][k].z, acc[k].z);
-              acc[k].w = fmaf(x, v[u][k].w, acc[k].w);
-            }
-          }
-        }
+        for (int u = 0; u < kAhead; ++u)
+          if (u0 + u < live)
+            add(acc, v[u], __shfl_sync(0xffffffffu, x0, (u0 + u) & 31), __shfl_sync(0xffffffffu, x1, (u0 + u) & 31));
       }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      d0 += __shfl_xor_sync(0xffffffffu, d0, o);
-      d1 += __shfl_xor_sync(0xffffffffu, d1, o);
+      e0 += __shfl_xor_sync(0xffffffffu, e0, o);
+      e1 += __shfl_xor_sync(0xffffffffu, e1, o);
     }
-    d0 = d0 == 0.f ? 0.f : 1.f / d0;
-    d1 = d1 == 0.f ? 0.f : 1.f / d1;
-    float4* dst = reinterpret_cast<float4*>(a.o_lat + (size_t)(first + at) * kDc) + lane;
+    e0 = e0 == 0.f ? 0.f : 1.f / e0;
+    e1 = e1 == 0.f ? 0.f : 1.f / e1;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float d = k < 2 ? d0 : d1;
-      dst[32 * k] = make_float4(acc[k].x * d, acc[k].y * d, acc[k].z * d, acc[k].w * d);
+      const float d = k < 2 ? e0 : e1;
+      acc[k] = make_float4(acc[k].x * d, acc[k].y * d, acc[k].z * d, acc[k].w * d);
     }
+    put(r, acc);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  fence_proxy_async_smem();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  bool ok = true;
+  if (warp == 0) {
+    constexpr uint32_t kId = tc::idesc_bf16(128, 2 * R, true, false);
+    const uint64_t wdesc = tc::smem_desc(smem_u32(smem_pt + M::w), M::wstage / 2, 1024, tc::kSwizzle128);
+    const uint64_t tdesc = tc::smem_desc(smem_u32(smem_pt + M::terms), 16, 1024, tc::kSwizzle128);
+    const bool leader = tc::elect_one();
+    int loaded = M::stages, c = 0;
+#pragma unroll 1
+    for (; c < 8; ++c) {
+      const int at = c % M::stages;
+      if (c > 0 && loaded < 8) {      // the stage of the chunk before takes the next
+        if (!(ok = mbar_wait(free_ + (c - 1) % M::stages, ((c - 1) / M::stages) & 1))) break;
+        if (lane == 0) load_w(loaded);
+        ++loaded;
+      }
+      if (!(ok = mbar_wait(full + at, (c / M::stages) & 1))) break;
+      tc::fence_after_sync();
+      if (leader) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc::mma_bf16(tmem, wdesc + (uint64_t)((at * M::wstage + k * 16 * 128) >> 4),
+                       tdesc + (uint64_t)((c * M::chunk + k * 32) >> 4), kId, c > 0 || k > 0);
+        tc::commit(free_ + at);
+      }
+      __syncwarp();
+    }
+    if (leader) tc::commit(done);
+    __syncwarp();
+    if (!ok)       // never leave with copies in flight
+      for (; c < loaded; ++c) mbar_wait(full + c % M::stages, (c / M::stages) & 1);
+  }
+  ok = __syncthreads_and(mbar_wait(done, 0) && ok);
+  tc::fence_after_sync();
+  // thread = output column, the rows behind one another
+  if (warp < 4) {
+    __nv_bfloat16* dst = out + ((size_t)row0 * H + h) * kDv + warp * 32 + lane;
+    const uint32_t at = tmem + ((uint32_t)(warp * 32) << 16);
+    uint32_t v[32], y[32];
+    tc::ld32(at, v);
+    if (R == 32) tc::ld32(at + 32, y);
+    tc::wait_ld();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float second = __uint_as_float(R == 32 ? y[r] : v[(R + r) & 31]);
+      const float x = ok ? __uint_as_float(v[r]) + second : NAN;     // (no result: not passed for one)
+      if (row0 + r < a.num_q) dst[(size_t)r * H * kDv] = __float2bfloat16_rn(x);
+    }
+    tc::fence_before_sync();
+  }
+  if (!ok && tid == 0) set_status(a.status, MLA_DEV_TIMEOUT);
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 0) tc::dealloc(tmem, M::cols);
 }
 
 // The projection of few rows: CTA = (8 rows, head h). W_uv[h] (128 KB) comes by
@@ -310,20 +477,32 @@ __global__ void __launch_bounds__(256) tree_proj_kernel(const __grid_constant__ 
 
 }  // namespace
 
-// tree_proj_kernel reads all of W_uv[h] for 8 rows, out_proj_tc for 128. With at most
-// three CTAs of the former an SM it is the faster: 24.5 against 32.1 us for a call of 64
-// rows of 16 heads, 31.8 against 37.5 for 128; it takes 51.2 against 52.2 for 256, and
-// 68.9 against 67.2 for 32 rows of 128 heads.
+// Few (row, head)s with many parts want a CTA each for the merge; more of them are merged
+// where they are projected. In graphs, us, a merge of its own / in one: 1 x 8 rows of 16
+// heads over 4,096 tokens 23.0 / 43.6, over 30,000 31.2 / 53.2; 512 (row, head)s (4 x 8
+// rows) 25.8 / 29.5; 1,024 (8 x 8 rows) 39.1 / 35.1, (2 x 4 of 128 heads) 47.3 / 43.4;
+// 4,096 96.1 / 56.6. Rows of a CTA: the most that leave a CTA an SM (W_uv[h] is read for
+// each). 32 / 16 / 8: 64 x 8 rows of 16 heads 87.6 / 93.9 / 106; 8 x 4 of 128 heads
+// 174.8 / 162.9 / 169.5; 12 x 2 of 32 heads 22.5 / 21.3 / 20.5. (64 rows with 512
+// threads: 88.5 for the first, 127 against 121 for 11 x 70 rows of 64 heads.)
 cudaError_t launch_tree_out(const TreeArgs& a, const void* W_uv, void* out, cudaStream_t st) {
   const int64_t rows = a.num_q * a.num_heads;
-  cudaError_t e = rows < 512 ? launch_pdl(tree_merge_few_kernel, dim3((unsigned)rows), dim3(512), 0, st, a)
-                             : launch_pdl(tree_merge_kernel, dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, st, a);
-  if (e != cudaSuccess) return e;
-  if ((a.num_q + Pj::rows - 1) / Pj::rows * a.num_heads > 6 * a.shares) {
+  if (rows >= 768) {
     CUtensorMap w_map;
     if (!encode_map_2d(&w_map, W_uv, kDv, (uint64_t)a.num_heads * kDc, 64, 64)) return cudaErrorInvalidValue;
-    return launch_out_proj_tc(w_map, a.o_lat, out, a.num_q, a.num_heads, true, st);
+    auto both = [&](auto kernel, int per, int smem) {
+      const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      return r != cudaSuccess ? r
+                              : launch_pdl(kernel, dim3((unsigned)((a.num_q + per - 1) / per), a.num_heads),
+                                           dim3(256), smem, st, w_map, a, (__nv_bfloat16*)out);
+    };
+    auto ctas = [&](int per) { return (a.num_q + per - 1) / per * a.num_heads; };
+    return ctas(32) >= 2 * a.shares   ? both(tree_merge_proj_kernel<32>, 32, Pt<32>::bytes)
+           : ctas(16) >= 2 * a.shares ? both(tree_merge_proj_kernel<16>, 16, Pt<16>::bytes)
+                                      : both(tree_merge_proj_kernel<8>, 8, Pt<8>::bytes);
   }
+  cudaError_t e = launch_pdl(tree_merge_few_kernel, dim3((unsigned)rows), dim3(512), 0, st, a);
+  if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(tree_proj_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Pj::bytes);
   if (e != cudaSuccess) return e;
   return launch_pdl(tree_proj_kernel, dim3((unsigned)((a.num_q + Pj::rows - 1) / Pj::rows), a.num_heads), dim3(256),

@@ -337,6 +337,21 @@ def test_decode_of_many_rows_sequences_and_parts(heads, seqs, num_ctas):
     b.check(heads=None if b.nq * heads * max(b.lens) < 2e7 else [0, heads - 1])
 
 
+@pytest.mark.parametrize("heads,seqs", [
+    (16, [(100, 8)] * 8), (16, [(5200, 2)] + [(0, 1)] * 50),          # 8 rows a CTA; more parts than lanes
+    (128, [(90, 7)] * 3 + [(5, 1)]), (128, [(5200, 1)] + [(0, 1)] * 20),   # 16 rows
+    (16, [(5200, 2)] + [(0, 1)] * 400), (16, [(70, 3), (0, 0), (3, 12)] * 40),   # 32 rows
+    (64, [(200, 5), (0, 2)] * 9),
+])
+def test_decode_merged_where_it_is_projected(heads, seqs):
+    b = Batch(seqs, heads=heads, seed=heads + len(seqs)).fill()
+    b.masks = [m.copy() for m in b.masks]
+    b.masks[-1][:] = False                     # rows that see nothing but the past
+    b.decode()
+    assert bits(b.ws) == 0
+    b.check()
+
+
 def test_decode_rows_behind_the_last_sequence():
     b = Batch([(100, 5), (37, 6)], seed=31).fill()
     b.decode()
