@@ -93,8 +93,8 @@ enum {
   kPVDone0 = kPFull0 + 2,        // [2] O += P V of tile i done
   kXFull0 = kPVDone0 + 2,        // [2] the peer's scores of tile i (bytes from the peer)
   kPeerFree0 = kXFull0 + 2,      // [2] the peer has read its buffer (4 warps of the peer)
-  kQRead0 = kPeerFree0 + 2,      // [2] the stage with half of a query read (4 warps)
-  kQReady = kQRead0 + 2,         // query columns in place (4 warps)
+  kQRead0 = kPeerFree0 + 2,      // [QuerySlots::kBars] the stage with half of a query read (4 warps)
+  kQReady = kQRead0 + QuerySlots::kBars,         // query columns in place (4 warps)
   kSums,                         // the segment's weight sums in shared memory (4 warps)
   kODone,                        // every output product of the segment done
   kOFree,                        // O read out, staging free (8 warps)
@@ -539,12 +539,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint64_t policy = l2_evict_first_policy();
     const bool leader = tc::elect_one();
     int ri = 0;                                   // stages filled so far
-    uint32_t holds_q = 0, phase = 0;              // per slot: what it holds; the parity of its next Empty
+    QuerySlots queries;
+    uint32_t phase = 0;                           // per slot: the parity of its next Empty
     int seg_i = 0;
     bool ok = true;
     auto room = [&](int slot) {
       if (ri < kStages) return true;
-      if ((holds_q >> slot) & 1) return warp_wait(kQRead0 + ((holds_q >> (8 + slot)) & 1), (holds_q >> (16 + slot)) & 1);
+      if (queries.held(slot)) return warp_wait(kQRead0 + queries.bar(slot), queries.parity(slot));
       const bool free = warp_wait(kEmpty0 + slot, (phase >> slot) & 1);
       phase ^= 1u << slot;
       return free;
@@ -559,7 +560,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int part = 0; part < 2 && ok; ++part, ++ri) {
         const int slot = ri % kStages;
         if (!room(slot)) { ok = false; break; }
-        holds_q = (holds_q & ~(0x10101u << slot)) | (0x1u | (uint32_t)part << 8 | (uint32_t)(seg_i & 1) << 16) << slot;
+        queries.put(slot, seg_i, part);
         if (leader) {
           uint64_t* full = &bars[kFull0 + slot];
           uint8_t* dst = sStage + slot * kStage;
@@ -587,7 +588,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (wanted && !there) set_status(a.status, MLA_DEV_BAD_BLOCK);
         const uint32_t okmask = __ballot_sync(0xffffffffu, there);
         if (!room(slot)) { ok = false; break; }
-        holds_q &= ~(1u << slot);
+        queries.clear(slot);
         uint8_t* dst = sStage + slot * kStage;
         if (leader) {
           info[slot] = make_int2(v, (int)okmask);
@@ -741,6 +742,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint8_t* rope = sm + Smem::rope;
     const float* sSum = reinterpret_cast<const float*>(sm + Smem::sum);
     int i = 0, ri = 0, seg_i = 0;
+    int read = 0;                        // segments read
     bool ok = true;
     auto query_in = [&]() {
 #pragma unroll 1
@@ -748,7 +750,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int slot = ri % kStages;
         if (!warp_wait(kFull0 + slot, (ri / kStages) & 1)) return false;
         take_query(sStage + slot * kStage, part, r, trow + kQCol, rope);
-        if (lane == 0) mbar_arrive(&bars[kQRead0 + part]);
+        if (lane == 0) mbar_arrive(&bars[kQRead0 + QuerySlots::bar_of(read - 1, part)]);
       }
       if (lane == 0) mbar_arrive(&bars[kQReady]);
       return true;
@@ -758,7 +760,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // scores are on their way. (After two tiles it is written 3,000 cycles later.)
     TreeSeg last;
     int t = 0, n = 0, store_at = -1;     // -1: nothing waits to be written
-    int read = 0;                        // segments read
     bool more = true;
     ok = segment(read++) && query_in();
     if (ok) n = seg.k1 - seg.k0;

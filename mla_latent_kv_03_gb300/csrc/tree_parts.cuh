@@ -49,6 +49,27 @@ __host__ __device__ __forceinline__ int tree_strips(int n, int m, int share) {
   return m <= 1 ? m : (n + share - 1) / share;
 }
 
+// Which slots of the decode's ring (four) hold half of a segment's query, and the barrier
+// and the phase that say that it is read. A slot is taken again four stages on, while a
+// segment may have only three (its query's two and a tile): by then the same half of the
+// next segment's query may be read too, and a barrier for both would be a phase ahead of
+// the wait. That of the segment after it (six stages on) is not on its way yet, so there
+// is a barrier for each half and each parity of the segment.
+struct QuerySlots {
+  static constexpr int kBars = 4;
+  uint32_t bits = 0;   // per slot: held [0, 4), barrier [8, 16), parity [16, 20)
+
+  __host__ __device__ __forceinline__ static int bar_of(int seg, int part) { return 2 * (seg & 1) + part; }
+  __host__ __device__ __forceinline__ void put(int slot, int seg, int part) {
+    bits = (bits & ~(0x10001u << slot | 3u << (8 + 2 * slot))) | 1u << slot |
+           (uint32_t)bar_of(seg, part) << (8 + 2 * slot) | (uint32_t)((seg >> 1) & 1) << (16 + slot);
+  }
+  __host__ __device__ __forceinline__ void clear(int slot) { bits &= ~(1u << slot); }
+  __host__ __device__ __forceinline__ bool held(int slot) const { return (bits >> slot) & 1; }
+  __host__ __device__ __forceinline__ int bar(int slot) const { return (bits >> (8 + 2 * slot)) & 3; }
+  __host__ __device__ __forceinline__ uint32_t parity(int slot) const { return (bits >> (16 + slot)) & 1; }
+};
+
 // The merge of a call's parts and the projection, after the attention on `st`.
 cudaError_t launch_tree_out(const TreeArgs& a, const void* W_uv, void* out, cudaStream_t st);
 
