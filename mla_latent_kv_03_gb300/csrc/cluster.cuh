@@ -59,5 +59,10 @@ __device__ __forceinline__ void sync() {
           : "memory");
 }
 
+// The two halves of a barrier that orders no memory: that a CTA of the cluster has
+// started, before anything is written to its shared memory.
+__device__ __forceinline__ void started() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_started() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
 }  // namespace cl
 }  // namespace mla

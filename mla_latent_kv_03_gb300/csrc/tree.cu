@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const __grid_c
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int CL = (int)gridDim.y, rank = (int)cl::rank(), b = blockIdx.x;
   const int V = a.vocab;
+  cl::started();       // (waited for behind the gathering of the rows)
   pdl_wait();
   pdl_launch_dependents();
   const int q0 = a.query_start_loc[b], q1 = a.query_start_loc[b + 1];
@@ -207,6 +208,8 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const __grid_c
         if (bad) set_status(a.status, MLA_DEV_BAD_SEQ);
       }
     }
+    __syncwarp();
+    cl::wait_started();
     return;
   }
   for (int i = tid; i < ql; i += kVerThreads) {
@@ -235,6 +238,8 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const __grid_c
       sYes[i] = bar < (double)w;
     }
   }
+  __syncwarp();
+  cl::wait_started();  // (sums go to the others' shared memory from here on)
   __syncthreads();
 
   // the walk's state, of warp 0

@@ -1,7 +1,9 @@
 """What the tree attention's kernels count with, run on the host: the functions of
 csrc/tree_parts.cuh, compiled into a program of its own (no GPU needed)."""
 
+import glob
 import os
+import re
 import subprocess
 
 import pytest
@@ -61,3 +63,16 @@ def test_the_wait_for_a_query_is_never_lapped(tmp_path):
     """Also with a tile a segment, where a slot is taken again after the same half of
     the next segment's query was copied."""
     assert run(tmp_path, RING) == "1 0 0"
+
+
+@pytest.mark.parametrize("path", [p for p in sorted(glob.glob(os.path.join(B.CSRC, "*.cu"))) if "cl::map(" in open(p).read()],
+                         ids=os.path.basename)
+def test_a_cluster_meets_before_its_shared_memory_is_written(path):
+    """A CTA of the cluster may not have started when another has. Each kernel that uses an
+    address in a peer's shared memory waits at a barrier of the cluster before that. (By
+    the order in the source: a late CTA can not be made to happen.)"""
+    for kernel in re.split(r"__global__", open(path).read())[1:]:
+        use = kernel.find("cl::map(")
+        if use >= 0:
+            met = re.search(r"cl::sync\(\);|cl::wait_started\(\);  //|barrier\.cluster\.wait", kernel[:use])
+            assert met, (os.path.basename(path), kernel[:120])
