@@ -179,12 +179,11 @@ struct TreeWalk {
       g.k1 = min(s.n, off + u_end - u);
       g.item = ibase;
     } else {
-      const int strip = off / (share * s.m), rem = off - strip * share * s.m;
-      const int L = min(share, s.n - strip * share), k = rem % L;
-      g.j = rem / L;
-      g.k0 = strip * share + k;
-      g.k1 = g.k0 + min(L - k, u_end - u);
-      g.item = ibase + strip * s.m + g.j;
+      const TreeUnit at = tree_unit(off, s.n, s.m, share);
+      g.j = at.j;
+      g.k0 = at.strip * share + at.k;
+      g.k1 = g.k0 + min(at.tiles - at.k, u_end - u);
+      g.item = ibase + at.strip * s.m + at.j;
     }
     u += g.k1 - g.k0;
     g.more = u < u_end;

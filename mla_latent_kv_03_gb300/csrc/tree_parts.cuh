@@ -49,6 +49,22 @@ __host__ __device__ __forceinline__ int tree_strips(int n, int m, int share) {
   return m <= 1 ? m : (n + share - 1) / share;
 }
 
+// Unit `off` of a sequence of n tiles and m > 1 q-blocks: tile k of q-block j in the
+// strip of `tiles` tiles from strip * share on. (share * m passes 32 bits where few
+// clusters have long sequences of many q-blocks; n * m does not.)
+struct TreeUnit {
+  int strip, tiles, j, k;
+};
+__host__ __device__ __forceinline__ TreeUnit tree_unit(int off, int n, int m, int share) {
+  TreeUnit x;
+  x.strip = off / m / share;
+  const int first = x.strip * share, rem = off - first * m;
+  x.tiles = share < n - first ? share : n - first;
+  x.j = rem / x.tiles;
+  x.k = rem - x.j * x.tiles;
+  return x;
+}
+
 // Which slots of the decode's ring (four) hold half of a segment's query, and the barrier
 // and the phase that say that it is read. A slot is taken again four stages on, while a
 // segment may have only three (its query's two and a tile): by then the same half of the

@@ -6,7 +6,8 @@ import pytest
 import torch
 
 from mla_latent_kv_03_gb300 import libmla as L
-from test_gpu_tree import Batch, Verify, bits, random_tree
+from oracle import tree_oracle as T
+from test_gpu_tree import DEV, SCALE, Batch, Verify, bits, dev, random_tree
 
 pytestmark = pytest.mark.gpu
 
@@ -31,6 +32,36 @@ def test_decode_of_segments_of_one_tile(heads, seqs, num_ctas):
     b.decode()
     assert bits(b.ws) == 0
     b.check()
+
+
+def test_decode_of_a_share_whose_q_blocks_pass_32_bits():
+    """One cluster for 1,024 rows of 128 heads over 131,200 tokens (of 70 pages, again and
+    again): a share of 2,099,200 units, times 1,024 q-blocks."""
+    H, T_, n, bs = 128, 1024, 131200, 64
+    cfg = L.make_config(H, bs, "bf16", num_ctas=2)
+    g = torch.Generator(DEV).manual_seed(5)
+    cache = torch.randn(70, bs, 576, device=DEV, generator=g).bfloat16()
+    q = (torch.randn(T_, H, 576, device=DEV, generator=g) * 0.4).bfloat16()
+    W_uv = (torch.randn(H, 512, 128, device=DEV, generator=g) * 512 ** -0.5).bfloat16()
+    table = (torch.arange(n // bs, device=DEV, dtype=torch.int32) * 3 % 70)[None]
+    mask = dev(T.words(np.tril(np.ones((T_, T_), bool)), 16), torch.int64)
+    ws = torch.empty(L.mla_tree_decode_workspace_size(cfg, T_, 1), dtype=torch.uint8, device=DEV)
+    L.mla_workspace_init(ws)
+    out = torch.full((T_, H, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    L.mla_tree_decode(cfg, q, cache, table, dev([n], torch.int32), dev([0, T_], torch.int32), mask, W_uv, ws, out)
+    assert bits(ws) == 0 and bool(out.isfinite().all())
+    kv = cache[table[0].long()].reshape(n, 576).double()
+    for r, h in ((0, 0), (1, 127), (500, 64), (1022, 3), (1023, 127)):
+        rows = kv[:n - T_ + r + 1]
+        s, part = (SCALE * (x @ q[r, h].double()[:c]) for x, c in ((rows, 576), (rows[:, :256], 256)))
+        half = float(torch.maximum(part.abs(), (s - part).abs()).max())
+        p = torch.softmax(s, 0)
+        w = W_uv[h].double()
+        want, size = p @ rows[:, :512] @ w, p @ rows[:, :512].abs() @ w.abs()
+        bound = 2.0 ** -8 * want.abs() + (2 * 2.0 ** -8 + 2 * 2.0 ** -11 * half + 2.0 ** -11) * size
+        assert bool(((out[r, h].double() - want).abs() <= bound).all()), (r, h)
+        # (the output is far below that bound, which takes every rounding one way)
+        assert float((out[r, h].double() - want).norm() / want.norm()) <= 5e-3
 
 
 # ---------------------------------------------------------------------- verify

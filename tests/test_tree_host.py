@@ -65,6 +65,31 @@ def test_the_wait_for_a_query_is_never_lapped(tmp_path):
     assert run(tmp_path, RING) == "1 0 0"
 
 
+UNITS = """
+int main() {
+  const int sizes[][3] = {{1, 2, 1}, {7, 3, 2}, {100, 5, 9}, {33, 4, 33}, {33, 4, 500},      // n, m, share
+                          {2048, 1024, 2048 * 1024}, {2050, 1024, 1 << 21}, {16384, 1024, 16384 * 1024 / 7},
+                          {1 << 19, 1024, 1 << 21}, {1 << 19, 1024, 1 << 29}, {1 << 19, 1023, 6900000}};
+  long long wrong = 0, seen = 0;
+  for (auto& z : sizes) {
+    const long long n = z[0], m = z[1], share = z[2], step = n * m > 4000 ? n * m / 4001 : 1;
+    for (long long off = 0; off < n * m; off += step, ++seen) {
+      const TreeUnit x = tree_unit((int)off, (int)n, (int)m, (int)share);
+      const long long strip = off / (share * m), rem = off - strip * share * m;
+      const long long tiles = share < n - strip * share ? share : n - strip * share;
+      wrong += x.strip != strip || x.tiles != tiles || x.j != rem / tiles || x.k != rem % tiles || x.j >= m;
+    }
+  }
+  printf("%d %lld", seen > 20000, wrong);
+}
+"""
+
+
+def test_units_of_many_q_blocks(tmp_path):
+    """Also where a share times the q-blocks passes 32 bits."""
+    assert run(tmp_path, UNITS) == "1 0"
+
+
 @pytest.mark.parametrize("path", [p for p in sorted(glob.glob(os.path.join(B.CSRC, "*.cu"))) if "cl::map(" in open(p).read()],
                          ids=os.path.basename)
 def test_a_cluster_meets_before_its_shared_memory_is_written(path):
