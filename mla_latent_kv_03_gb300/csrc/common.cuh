@@ -368,6 +368,17 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// Kernels that mask a score with -inf and then scale it want a scale above 0 (-inf times
+// 0 is NaN, times less +inf). They scale by this, and the sign, or a factor of 0, is the
+// query's (two bf16 values): exact, and what is not finite stays so.
+__device__ __forceinline__ float score_scale(float scale) { return scale == 0.f ? 1.f : fabsf(scale); }
+__device__ __forceinline__ uint32_t signed_query(uint32_t q, float scale) {
+  if (scale > 0.f) return q;
+  const __nv_bfloat162 f = __float2bfloat162_rn(scale < 0.f ? -1.f : 0.f);
+  const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&q), f);
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+
 // Byte offset of 16-byte chunk `chunk` of row `row` in a 128-byte-swizzled
 // tile whose rows are 128 bytes (the TMA SWIZZLE_128B pattern: chunk index
 // XOR row mod 8; the tile base must be 1024-byte aligned).

@@ -371,26 +371,29 @@ __device__ __forceinline__ void loaded(uint32_t (&r)[32]) {
 
 // A warp's 32 rows of two of the query's column slabs (128 columns) from a stage
 // that holds them, [2 slabs][128 rows][128 bytes], into TMEM, and of 64 rows' rope
-// columns into their place.
-__device__ __noinline__ void take_query(const uint8_t* stage, int part, int r, uint32_t tcols, uint8_t* rope_rows) {
+// columns into their place; the sign of a scale that is not positive goes with them.
+__device__ __noinline__ void take_query(const uint8_t* stage, int part, int r, uint32_t tcols, uint8_t* rope_rows,
+                                        float scale) {
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     uint32_t w[16];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const uint4 y = *reinterpret_cast<const uint4*>(stage + (c >> 1) * (kBlockRows * 128) + sw128(r, 4 * (c & 1) + u));
-      w[4 * u] = y.x;
-      w[4 * u + 1] = y.y;
-      w[4 * u + 2] = y.z;
-      w[4 * u + 3] = y.w;
+      w[4 * u] = signed_query(y.x, scale);
+      w[4 * u + 1] = signed_query(y.y, scale);
+      w[4 * u + 2] = signed_query(y.z, scale);
+      w[4 * u + 3] = signed_query(y.w, scale);
     }
     tc::st16(tcols + 64 * part + 16 * c, w);
   }
   if (r >> 6 == part) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < 4; ++u) {
+      const uint4 y = *reinterpret_cast<const uint4*>(stage + 4 * kSlab + (r & 63) * 64 + 16 * u);
       *reinterpret_cast<uint4*>(rope_rows + r * 64 + 16 * u) =
-          *reinterpret_cast<const uint4*>(stage + 4 * kSlab + (r & 63) * 64 + 16 * u);
+          make_uint4(signed_query(y.x, scale), signed_query(y.y, scale), signed_query(y.z, scale), signed_query(y.w, scale));
+    }
   }
   fence_proxy_async_smem();
   tc::wait_st();
@@ -748,7 +751,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int part = 0; part < 2; ++part, ++ri) {
         const int slot = ri % kStages;
         if (!warp_wait(kFull0 + slot, (ri / kStages) & 1)) return false;
-        take_query(sStage + slot * kStage, part, r, trow + kQCol, rope);
+        take_query(sStage + slot * kStage, part, r, trow + kQCol, rope, a.scale_log2);
         if (lane == 0) mbar_arrive(&bars[kQRead0 + QuerySlots::bar_of(read - 1, part)]);
       }
       if (lane == 0) mbar_arrive(&bars[kQReady]);
@@ -819,7 +822,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t pfree_peer = cl::map(smem_u32(&bars[kPeerFree0]), (uint32_t)(h ^ 1));
     float* sSum = reinterpret_cast<float*>(sm + Smem::sum);
-    const float scale = a.scale_log2;
+    const float scale = score_scale(a.scale_log2);
     int i = 0, ri = 0, seg_i = 0;
     bool ok = true, more = true;
     while (more) {

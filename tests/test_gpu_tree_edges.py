@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+import test_gpu_tree
 from mla_latent_kv_03_gb300 import libmla as L
 from oracle import tree_oracle as T
 from test_gpu_tree import DEV, SCALE, Batch, Verify, bits, dev, random_tree
@@ -62,6 +63,22 @@ def test_decode_of_a_share_whose_q_blocks_pass_32_bits():
         assert bool(((out[r, h].double() - want).abs() <= bound).all()), (r, h)
         # (the output is far below that bound, which takes every rounding one way)
         assert float((out[r, h].double() - want).norm() / want.norm()) <= 5e-3
+
+
+@pytest.mark.parametrize("scale", [-0.072, -0.5, 0.0, 1e-38, 0.9])
+def test_decode_of_any_scale(scale, monkeypatch):
+    """Tokens that are masked, not there or in a page out of range weigh nothing whatever
+    the scale; a row that sees nothing is zero."""
+    monkeypatch.setattr(test_gpu_tree, "SCALE", scale)
+    b = Batch([(70, 9), (0, 3), (300, 65), (0, 12), (1, 1)], bs=32, seed=51)
+    rng = np.random.default_rng(3)
+    b.masks = [rng.random(m.shape) < 0.4 for m in b.masks]
+    b.masks[1][1] = b.masks[3][:, 4:] = False
+    b.cfg.softmax_scale = scale
+    b.fill().decode()
+    assert bits(b.ws) == 0
+    b.check()
+    assert not b.out[b.qsl[1] + 1].any()
 
 
 # ---------------------------------------------------------------------- verify
