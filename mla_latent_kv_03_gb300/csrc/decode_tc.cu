@@ -250,10 +250,11 @@ __device__ __forceinline__ int seg_stages(const TcSeg& s) {
 }
 
 // This CTA's query columns [col0, col0 + 8 * nvec) of q-block row `qrow` into
-// its TMEM lane (rows past the last query row are zero). Warp-collective.
+// its TMEM lane (rows past the last query row are zero), with the sign of a scale that is
+// not positive. Warp-collective.
 template <int NVEC>
 __device__ __forceinline__ void load_q_tmem(const uint16_t* q_abs, int64_t qrow, int64_t qrows,
-                                            int col0, uint32_t taddr) {
+                                            int col0, uint32_t taddr, float scale) {
   static_assert(NVEC % 8 == 0, "whole x16 stores per batch");
   const uint4* src = reinterpret_cast<const uint4*>(q_abs + (size_t)qrow * kRow + col0);
   const bool live = qrow < qrows;
@@ -278,17 +279,21 @@ __device__ __forceinline__ void load_q_tmem(const uint16_t* q_abs, int64_t qrow,
         w[4 * k + 2] = buf[4 * c + k].z;
         w[4 * k + 3] = buf[4 * c + k].w;
       }
+      if (!(scale > 0.f)) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) w[k] = signed_query(w[k], scale);
+      }
       tc::st16(taddr + kQCol + 4 * kHalf * hb + 16 * c, w);
     }
   }
 }
 
 __device__ __forceinline__ void load_q_cta(int h, const uint16_t* q_abs, int64_t qrow,
-                                           int64_t qrows, uint32_t trow) {
+                                           int64_t qrows, uint32_t trow, float scale) {
   if (h == 0)
-    load_q_tmem<32>(q_abs, qrow, qrows, 0, trow);      // columns [0, 256)
+    load_q_tmem<32>(q_abs, qrow, qrows, 0, trow, scale);      // columns [0, 256)
   else
-    load_q_tmem<40>(q_abs, qrow, qrows, 256, trow);    // columns [256, 576)
+    load_q_tmem<40>(q_abs, qrow, qrows, 256, trow, scale);    // columns [256, 576)
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -609,7 +614,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int* arrive = reinterpret_cast<int*>(ws + L.arrive);
     const uint16_t* q_abs = reinterpret_cast<const uint16_t*>(a.q_abs);
     const int64_t qrows = a.num_q * a.num_heads;
-    const float scale = a.scale_log2;
+    const float scale = score_scale(a.scale_log2);
     const uint32_t peer = (uint32_t)(h ^ 1);
     const uint32_t pfree_peer0 = cl::map(smem_u32(&bars[kPeerFree0]), peer);
     float* wsm = reinterpret_cast<float*>(sm + Smem::w);
@@ -630,7 +635,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     bool have = sw.next(seg);
     if (have) {
-      load_q_cta(h, q_abs, (int64_t)kHG * seg.t_first + r, qrows, trow);
+      load_q_cta(h, q_abs, (int64_t)kHG * seg.t_first + r, qrows, trow, a.scale_log2);
       tc::wait_st();
       tc::fence_before_sync();
       mbar_arrive(&bars[kQtReady]);
@@ -697,7 +702,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         m12[11] = x[31];
         const float mxr = fmaxf(fmax3(fmax3(m12[0], m12[1], m12[2]), fmax3(m12[3], m12[4], m12[5]), m12[6]),
                                 fmax3(fmax3(m12[7], m12[8], m12[9]), m12[10], m12[11]));
-        const float m_cand = mxr * scale;   // scale > 0
+        const float m_cand = mxr * scale;
         float alpha = 1.f;
         bool rescale_o = false;
         if (m_cand > m_used + kRescaleLog2 || (m_used == -INFINITY && m_cand != -INFINITY)) {
@@ -771,7 +776,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool okq = wait_or_abort(&bars[kQEmpty], seg_i & 1, abort_flag);
         if (soft_red_or(!okq || fail)) { aborted = true; break; }
         tc::fence_after_sync();
-        load_q_cta(h, q_abs, (int64_t)kHG * nxt.t_first + r, qrows, trow);
+        load_q_cta(h, q_abs, (int64_t)kHG * nxt.t_first + r, qrows, trow, a.scale_log2);
         tc::wait_st();
         tc::fence_before_sync();
         mbar_arrive(&bars[kQtReady]);
