@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const bool live_row = r < rows;
     const int n = q0 + r;                              // query row index (when live)
     const int lim = pos0 + r;                          // last token this row sees
-    const float scale = a.scale_log2;
+    const float scale = score_scale(a.scale_log2);
     float* lx = reinterpret_cast<float*>(sm + PtSmem::lx);
     bool aborted = false, fail = false;
     // ---- the query tile into TMEM: q_nope by warpgroup 0, RoPE(q_pe) by 1
@@ -408,6 +408,18 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       }
     }
     tc::wait_st();
+    if (!(a.scale_log2 > 0.f)) {       // (out of the way of the stores above: rare)
+#pragma unroll 1
+      for (int c = 0; c < 2 - wg; ++c) {
+        uint32_t w32[32];
+        tc::ld32(trow + kTQ + 64 * wg + 32 * c, w32);
+        tc::wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) w32[k] = signed_query(w32[k], a.scale_log2);
+        tc::st32(trow + kTQ + 64 * wg + 32 * c, w32);
+      }
+      tc::wait_st();
+    }
     tc::fence_before_sync();
     mbar_arrive(&bars[kPtQReady]);
 
@@ -467,7 +479,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       for (int c = 0; c < 7; ++c) m8[c] = fmax3(m22[3 * c], m22[3 * c + 1], m22[3 * c + 2]);
       m8[7] = m22[21];
       const float mxr = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
-      const float m_cand = mxr * scale;               // scale > 0
+      const float m_cand = mxr * scale;
       const float m_prev = j > 0 ? wait_m(j - 1) : -INFINITY;
       if (m_prev != m_prev) fail = true;               // NaN: the wait gave up
       float m_new = m_prev, alpha = 1.f;

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from _helpers import assert_close, ref_o_lat_from, to_f64
+from test_gpu_naive import _expanded_ref
 from mla_latent_kv_03_gb300 import libmla as L
 from mla_latent_kv_03_gb300 import workloads as W
 from mla_latent_kv_03_gb300.step import MlaDecodeStep
@@ -48,3 +49,19 @@ def test_decode(name, scale):
     s.decode_paged_combine()
     assert s.device_status()[0][0] == 0
     assert_close(to_f64(s.o_lat), ref, w.dtype, f"o_lat, merged in the decode, {name}")
+
+
+@pytest.mark.parametrize("scale", SCALES)
+@pytest.mark.parametrize("name", ["rows", "chunks", "h64"])
+def test_expanded_prefill_and_decode(name, scale):
+    w = CASES[name]()
+    w.softmax_scale = scale
+    s = MlaDecodeStep(w, device=DEV)
+    s.naive_setup()
+    s.naive_populate()
+    ref = _expanded_ref(w, s)
+    for call in (s.naive_prefill, s.naive_decode):
+        s.out_naive.fill_(float("nan"))
+        call()
+        assert L.mla_get_device_status(s.naive_ws)[0] == 0
+        assert_close(to_f64(s.out_naive), ref, "bf16", f"{call.__name__} {name}")
