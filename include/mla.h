@@ -441,8 +441,10 @@ mla_status mla_page8_compact(const mla_config* cfg, void* cache8, float* page_sc
  * parent that does not come before its child, longer than its block table or
  * with more rows than tokens sets MLA_DEV_BAD_SEQ, and its rows get an empty
  * mask, position 0 and slot -1 (which the cache write skips). A page out of
- * range sets MLA_DEV_BAD_BLOCK (slot -1). Rows that no sequence has are left as
- * they were. dev_status may be NULL.
+ * range sets MLA_DEV_BAD_BLOCK (slot -1). Rows that no sequence has, and those of
+ * a sequence whose query_start_loc entries do not ascend or leave [0, num_q]
+ * (MLA_DEV_BAD_SEQ), are left as they were: a program that may have such rows sets
+ * their slots to -1 before the call. dev_status may be NULL.
  */
 mla_status mla_tree_plan(const mla_config* cfg, const int32_t* parents, const int32_t* seq_lens,
                          const int32_t* query_start_loc, const int32_t* block_table,

@@ -286,7 +286,10 @@ class MlaDecodeStep:
         L.mla_workspace_init(self.tr_ws)
 
     def tree_plan(self, stream=None) -> None:
-        """Masks, positions and slots of the step's trees."""
+        """Masks, positions and slots of the step's trees. Rows that no sequence has (a
+        step of fixed size with fewer) get slot -1, which the cache write skips."""
+        with torch.cuda.stream(self._page8_stream(stream)):
+            self.tr_slots.fill_(-1)
         L.mla_tree_plan(self.cfg, self.tr_parents, self.tr_lens, self.query_start_loc, self.block_table,
                         self.cache.shape[0], self.tr_mask, self.tr_positions, self.tr_slots,
                         dev_status=self.status, stream=stream)

@@ -7,6 +7,8 @@ import torch
 
 import test_gpu_tree
 from mla_latent_kv_03_gb300 import libmla as L
+from mla_latent_kv_03_gb300 import workloads as W
+from mla_latent_kv_03_gb300.step import MlaDecodeStep
 from oracle import tree_oracle as T
 from test_gpu_tree import DEV, SCALE, Batch, Verify, bits, dev, random_tree
 
@@ -107,3 +109,39 @@ def test_verify_clusters_of_uneven_sequences(drawn, V, sizes):
     assert v.lens[1:3].tolist() == [0, 0] and v.nxt[1:3].tolist() == [-1, -1]
     assert all(torch.equal(a[3:], b[3:]) for a, b in zip((v.path, v.lens, v.nxt), first))
     v.qsl = keep
+
+
+# --------------------------------------------------------- the step as a whole
+def tree_driver(seqs, t, seed):
+    """A step driver whose sequences have `past` tokens and trees of t rows."""
+    w = W.make("trees", [p + t for p in seqs], [t] * len(seqs), 16, 16, "bf16", seed)
+    s = MlaDecodeStep(w, cache_fill=3.0)
+    rng = np.random.default_rng(seed)
+    trees = [random_tree(rng, t, 3) for _ in seqs]
+    s.tree_setup(sum(trees, []))
+    return w, s, trees
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_step_of_fewer_rows_than_it_has_room_for(side):
+    """Rows behind the last sequence write nothing, neither in a first step nor behind one
+    in which they belonged to a sequence."""
+    past, t = [40, 7, 20], 8
+    for first in (True, False):
+        w, s, trees = tree_driver(past, t, 61)
+        stream = torch.cuda.Stream() if side else None
+        if not first:
+            s.tree_step(stream)
+            torch.cuda.synchronize()
+        s.cache.fill_(3.0)
+        # (trees of 8 and 5 rows; the last sequence has none, and 11 rows are nobody's)
+        s.query_start_loc.copy_(dev([0, 8, 13, 13], torch.int32))
+        s.tr_lens.copy_(dev([48, 12, 20], torch.int32))
+        torch.cuda.synchronize()
+        s.tree_step(stream)
+        torch.cuda.synchronize()
+        assert s.device_status() == ((0, 0), (0, 0)) and bits(s.tr_ws) == 0
+        written = (s.cache != 3.0).any(-1).view(-1).nonzero()[:, 0].tolist()
+        want = [int(w.block_table[b][j // 16]) * 16 + j % 16 for b, k in ((0, 8), (1, 5)) for j in range(past[b], past[b] + k)]
+        assert written == sorted(want)
+        assert not s.out[13:].any()
