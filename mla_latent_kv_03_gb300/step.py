@@ -278,7 +278,6 @@ class MlaDecodeStep:
         self.tr_slots = torch.zeros(w.num_q, dtype=torch.int64, device=dev)
         self.tr_lens = self.seq_lens.clone()   # with the step's trees
         self.tr_new_lens = torch.zeros_like(self.tr_lens)
-        self.tr_q_lens = _dev(w.q_lens, torch.int32, dev)
         need = L.mla_tree_decode_workspace_size(self.cfg, w.num_q, w.batch)
         if need == 0:
             raise L.MlaError(L.MLA_OK + 2, "mla_tree_decode_workspace_size")
@@ -314,8 +313,8 @@ class MlaDecodeStep:
                     caches=None, stream=None):
         """Verify the step's trees and move the kept rows behind the past, in this
         layer's cache or in `caches` [layers, blocks, block_size, 576]. The lengths
-        go on to the next step's, whose trees are as large. Returns (path, its
-        lengths, the next tokens)."""
+        go on to the next step's, whose trees are as large as this one's. Returns
+        (path, its lengths, the next tokens)."""
         with torch.cuda.stream(self._page8_stream(stream)):  # memory of the stream that writes it
             path = torch.empty((self.w.batch, max_path), dtype=torch.int32, device=self.device)
             lens = torch.empty(self.w.batch, dtype=torch.int32, device=self.device)
@@ -325,7 +324,8 @@ class MlaDecodeStep:
             L.mla_tree_commit(self.cfg, self.cache if caches is None else caches, self.block_table,
                               self.tr_lens, self.query_start_loc, path, lens, self.tr_new_lens,
                               dev_status=self.status)
-            torch.add(self.tr_new_lens, self.tr_q_lens, out=self.tr_lens)
+            q_lens = self.query_start_loc[1:] - self.query_start_loc[:-1]
+            torch.add(self.tr_new_lens, q_lens, out=self.tr_lens)
         return path, lens, nxt
 
     # -- the projections either side (the whole attention layer) -----------

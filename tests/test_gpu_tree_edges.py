@@ -113,12 +113,14 @@ def test_verify_clusters_of_uneven_sequences(drawn, V, sizes):
 
 # --------------------------------------------------------- the step as a whole
 def tree_driver(seqs, t, seed):
-    """A step driver whose sequences have `past` tokens and trees of t rows."""
-    w = W.make("trees", [p + t for p in seqs], [t] * len(seqs), 16, 16, "bf16", seed)
+    """A step driver whose sequences have `past` tokens and trees of t rows, with pages for
+    three steps."""
+    w = W.make("trees", [p + 3 * t for p in seqs], [t] * len(seqs), 16, 16, "bf16", seed)
     s = MlaDecodeStep(w, cache_fill=3.0)
     rng = np.random.default_rng(seed)
     trees = [random_tree(rng, t, 3) for _ in seqs]
     s.tree_setup(sum(trees, []))
+    s.tr_lens.copy_(dev([p + t for p in seqs], torch.int32))
     return w, s, trees
 
 
@@ -145,3 +147,21 @@ def test_step_of_fewer_rows_than_it_has_room_for(side):
         want = [int(w.block_table[b][j // 16]) * 16 + j % 16 for b, k in ((0, 8), (1, 5)) for j in range(past[b], past[b] + k)]
         assert written == sorted(want)
         assert not s.out[13:].any()
+
+
+def test_step_with_trees_of_other_sizes_than_the_first():
+    """The lengths follow the rows that the sequences have now."""
+    past, t = [40, 7, 20], 8
+    w, s, trees = tree_driver(past, t, 63)
+    s.query_start_loc.copy_(dev([0, 8, 13, 13], torch.int32))
+    s.tr_lens.copy_(dev([48, 12, 20], torch.int32))
+    v = Verify([trees[0], trees[1][:5], []], 50, True, seed=2, near=0.1)
+    pad = lambda x: np.concatenate([x, np.zeros((w.num_q - 13,) + x.shape[1:], x.dtype)])  # noqa: E731
+    f32, i32 = torch.float32, torch.int32
+    s.tree_step()
+    path, n, nxt = s.tree_accept(dev(pad(v.p), f32), dev(pad(v.q), f32), dev(pad(v.tok), i32), dev(pad(v.u), f32),
+                                 dev(v.f, f32), t)
+    assert s.device_status() == ((0, 0), (0, 0))
+    want = [T.verify(v.p[r], v.q[r], v.tok[r], v.trees[b], v.u[r], v.f[b]) for b, r in ((0, slice(0, 8)), (1, slice(8, 13)))]
+    assert n.tolist() == [len(want[0][0]), len(want[1][0]), 0] and nxt.tolist() == [want[0][1], want[1][1], -1]
+    assert s.tr_lens.tolist() == [40 + int(n[0]) + 8, 7 + int(n[1]) + 5, 20]
