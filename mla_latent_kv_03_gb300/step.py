@@ -313,7 +313,8 @@ class MlaDecodeStep:
                     caches=None, stream=None):
         """Verify the step's trees and move the kept rows behind the past, in this
         layer's cache or in `caches` [layers, blocks, block_size, 576]. The lengths
-        go on to the next step's, whose trees are as large as this one's. Returns
+        go on to the next step's, whose trees are as large as this one's; a sequence that
+        the commit flags (one that outgrew its block table) keeps its length. Returns
         (path, its lengths, the next tokens)."""
         with torch.cuda.stream(self._page8_stream(stream)):  # memory of the stream that writes it
             path = torch.empty((self.w.batch, max_path), dtype=torch.int32, device=self.device)
@@ -324,8 +325,9 @@ class MlaDecodeStep:
             L.mla_tree_commit(self.cfg, self.cache if caches is None else caches, self.block_table,
                               self.tr_lens, self.query_start_loc, path, lens, self.tr_new_lens,
                               dev_status=self.status)
+            # (0: flagged, or nothing before the tree and nothing kept)
             q_lens = self.query_start_loc[1:] - self.query_start_loc[:-1]
-            torch.add(self.tr_new_lens, q_lens, out=self.tr_lens)
+            self.tr_lens.copy_(torch.where(self.tr_new_lens > 0, self.tr_new_lens + q_lens, self.tr_lens))
         return path, lens, nxt
 
     # -- the projections either side (the whole attention layer) -----------

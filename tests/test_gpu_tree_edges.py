@@ -149,6 +149,31 @@ def test_step_of_fewer_rows_than_it_has_room_for(side):
         assert not s.out[13:].any()
 
 
+def test_step_of_a_sequence_that_outgrew_its_table():
+    """It is flagged, and neither its cache nor its length is lost; the others go on."""
+    past, t = [40, 7, 20], 8
+    w, s, trees = tree_driver(past, t, 62)
+    room = w.block_table.shape[1] * 16
+    full = room - 3                       # (sequence 0's table is full, of the longest)
+    s.tr_lens.copy_(dev([full + t, 7 + t, 20 + t], torch.int32))
+    before = s.cache.clone()
+    V = 50
+    v = Verify(trees, V, True, seed=1, near=0.1)
+    args = [dev(x, k) for x, k in ((v.p, torch.float32), (v.q, torch.float32), (v.tok, torch.int32),
+                                   (v.u, torch.float32), (v.f, torch.float32))]
+    at = np.array([7, 20])
+    for step in range(2):
+        s.tree_step()
+        s.tree_accept(*args, t)
+        assert bits(s.status) == L.DEV_BAD_SEQ and bits(s.tr_ws) == L.DEV_BAD_SEQ
+        kept = np.array([len(T.verify(v.p[r], v.q[r], v.tok[r], trees[b], v.u[r], v.f[b])[0])
+                         for b, r in ((1, slice(8, 16)), (2, slice(16, 24)))])
+        at = at + kept
+        assert s.tr_lens.tolist() == [full + t, at[0] + t, at[1] + t]
+    own = torch.from_numpy(w.block_table[0][w.block_table[0] >= 0].astype(np.int64)).to(DEV)
+    assert torch.equal(s.cache[own], before[own])
+
+
 def test_step_with_trees_of_other_sizes_than_the_first():
     """The lengths follow the rows that the sequences have now."""
     past, t = [40, 7, 20], 8
