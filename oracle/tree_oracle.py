@@ -101,7 +101,7 @@ def verify(target, draft, tokens, parents, u, u_last, max_path=None):
         elif draft is not None:
             # one rounding, as a fused multiply-add has
             less = w.astype(np.float64) - z * draft[cur].astype(np.float64)
-            w = np.maximum(less.astype(np.float32), np.float32(0))
+            w = np.fmax(less.astype(np.float32), np.float32(0))   # (of a NaN: 0)
             z = float(np.float32(math.ldexp(float(sum(_whole(w))), -40)))
         else:
             z = max(z - float(w[x]), 0.0)

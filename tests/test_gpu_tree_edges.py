@@ -83,6 +83,56 @@ def test_decode_of_any_scale(scale, monkeypatch):
     assert not b.out[b.qsl[1] + 1].any()
 
 
+# Columns of the latents and of the rope key, in either CTA's half.
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("col", [3, 300, 515, 560])
+@pytest.mark.parametrize("place", [2, 64 * 5 + 7, 64 * 7 - 2, 64 * 7 + 4])
+def test_decode_makes_rows_that_see_a_token_that_is_not_finite_nan(value, col, place):
+    """In the first tile, in one that every row sees whole, and in the tree's own tiles:
+    every output of a row that sees the token is NaN, the others are what they were. With
+    one part a row and with several, merged in a kernel of their own and in the projection."""
+    past, trees = 64 * 7 - 1, [[-1, 0, 0, 1, 2, 4, 3, 5]]
+    for more, num_ctas in ((0, 2), (0, 0), (5, 6), (60, 0)):
+        b = Batch([(past, 8)] + [(90, 1)] * more, trees=trees + [[-1]] * more, seed=71, num_ctas=num_ctas).fill()
+        want = b.decode().clone()
+        b.cache[int(b.table[0, place // 64]), place % 64, col] = value
+        got = b.decode()
+        seen = b.masks[0][:, place - past] if place >= past else np.ones(8, bool)
+        for r in range(b.nq):
+            if r < 8 and seen[r]:
+                assert got[r].isnan().all(), r
+            else:
+                assert torch.equal(got[r], want[r]), r
+
+
+@pytest.mark.parametrize("heads,seqs,behind", [
+    (16, [(100, 5), (37, 6)], 21),                       # 512 (row, head)s: merged by themselves
+    (16, [(100, 5), (37, 6)], 37),                       # where they are projected: 8 rows a CTA
+    (128, [(700, 2), (5, 1), (0, 2)], 15),               # 16
+    (16, [(300, 7)] * 40, 11), (16, [(1500, 3), (70, 30)], 380), (128, [(700, 2), (0, 3)], 35),   # 32
+])
+def test_decode_of_rows_behind_the_last_sequence(heads, seqs, behind):
+    """Queries and masks of rows that no sequence has may hold anything: zeros there, and
+    the others are what they are without them (bit by bit below 768 (row, head)s, from
+    where on the parts are added in another order)."""
+    b = Batch(seqs, heads=heads, seed=73).fill()
+    want = b.decode().clone()
+    b.check()
+    n = b.nq + behind
+    q = torch.full((n, heads, 576), float("nan"), dtype=torch.bfloat16, device=DEV)
+    q[:b.nq] = b.t_q
+    mask = torch.full((n, 1), -1, dtype=torch.int64, device=DEV)
+    mask[:b.nq] = b.t_mask
+    out = torch.full((n, heads, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    ws = torch.full((L.mla_tree_decode_workspace_size(b.cfg, n, len(seqs)),), 255, dtype=torch.uint8, device=DEV)
+    L.mla_workspace_init(ws)
+    L.mla_tree_decode(b.cfg, q, b.cache, b.t_table, b.t_lens, b.t_qsl, mask, b.t_W, ws, out)
+    assert bits(ws) == 0 and not out[b.nq:].any()
+    b.check(out[:b.nq])
+    if n * heads < 768:
+        assert torch.equal(out[:b.nq], want)
+
+
 # ---------------------------------------------------------------------- verify
 @pytest.mark.parametrize("drawn", [True, False])
 @pytest.mark.parametrize("V,sizes", [
@@ -109,6 +159,28 @@ def test_verify_clusters_of_uneven_sequences(drawn, V, sizes):
     assert v.lens[1:3].tolist() == [0, 0] and v.nxt[1:3].tolist() == [-1, -1]
     assert all(torch.equal(a[3:], b[3:]) for a, b in zip((v.path, v.lens, v.nxt), first))
     v.qsl = keep
+
+
+@pytest.mark.parametrize("drawn", [True, False])
+@pytest.mark.parametrize("V", [600, 9001])
+def test_verify_of_values_that_are_no_probabilities(drawn, V):
+    """NaN and what lies outside of [0, 1] in the target's rows, NaN and infinities in the
+    draft's: the walk and the next token of every sequence are the definition's."""
+    v = Verify([[-1, 0, 0, 0, 1, 1]] * 8, V, drawn, seed=9, near=1.0)
+    v.u[:] = np.linspace(0.05, 0.999, len(v.u), dtype=np.float32)[::-1]
+    n, rng = len(v.u), np.random.default_rng(3)
+    for value in (np.nan, -1.0, np.inf, -np.inf):
+        v.p[rng.integers(0, n, 60), rng.integers(0, V, 60)] = value if value != np.inf else 0.5
+    for value in (np.nan, np.inf):
+        v.q[rng.integers(0, n, 200), rng.integers(0, V, 200)] = value
+    v.p[6:12, ::2] = np.nan
+    v.q[12:18, 1::3] = np.nan
+    v.p[18:24], v.p[18:24, 77] = 0, 2.0    # one token has all, which is more than 1
+    v.q[24:30] = np.inf                    # a first rejection leaves nothing
+    v.u[[31, 37]] = 0                      # accepted, if the target has any weight there
+    lens = v.run().check()
+    assert (lens > 1).any() and (lens == 1).any()
+    assert bits(v.status) == 0
 
 
 # --------------------------------------------------------- the step as a whole
