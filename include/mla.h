@@ -466,7 +466,8 @@ mla_status mla_tree_plan(const mla_config* cfg, const int32_t* parents, const in
  *   see, one that is not finite makes it NaN.
  * A weight is rounded to bf16 before the product (the sum adds the rounded ones),
  * and one of the two halves that q_abs . row_t is summed in (256 latent and 32 rope
- * columns each) to f16: 2^-11 of that half, which ends at 65,504.
+ * columns each) to f16: 2^-11 of that half, which ends at 65,504. Where softmax_scale
+ * times such a half passes 8, that moves a weight by more than its own rounding.
  * Limits: those of mla_page8_decode, with num_q times a block table's tokens at
  * most 2^35; a sequence of more than 64 * mask_words rows sets MLA_DEV_BAD_SEQ
  * and gets zeros, as do all when query_start_loc does not ascend.
@@ -528,7 +529,8 @@ mla_status mla_tree_verify(const float* target_probs, const float* draft_probs, 
  * path[b][i] goes to place past + i for i < path_lens[b], in each of num_layers
  * caches that lie one after another ([num_layers, num_blocks, block_size] rows of
  * row_bytes: 1,152 for bf16, 2,304 for fp32, or 640 for the FP8 rows of
- * mla_cache_write_fp8; page-scaled rows do not move between pages this way).
+ * mla_cache_write_fp8; page-scaled rows do not move between pages this way). Of
+ * these, mla_tree_decode attends over the bf16 cache only.
  * new_lens [batch] int32 (output, not seq_lens itself) = past + path_lens[b]. Keys
  * keep their rotation: a kept row's position is past + its depth = past + i. Bytes
  * of places behind the kept rows are left as they were. seq_lens, query_start_loc

@@ -21,8 +21,8 @@ bool t_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>
 // after k rounds it holds 2^k rows on the way up and `jump` is the row above
 // them, so a chain of 1,024 takes 10 rounds. The words lie word by word, so that a
 // warp's rows are in different banks, and a row has none behind its own. Bound by
-// latency: 8.3 us for 256 trees of 333 rows (11.4 with the words row by row), and for
-// masks of one word, in a kernel of their own, 3.2 us for 64 of 8 (5.2 in the wide one).
+// latency: 8 us for 256 trees of 333 rows (11.4 with the words row by row), and for
+// masks of one word, in a kernel of their own, 3 us for 64 of 8 (5.2 in the wide one).
 struct PlanTreeArgs {
   const int32_t* parents;
   const int32_t* seq_lens;
@@ -113,8 +113,8 @@ __global__ void __launch_bounds__(64 * MAXW) tree_plan_kernel(const __grid_const
 // the vocabulary is wanted: behind a rejection when there are draft
 // probabilities, and for the last draw. Weights enter the sums as whole numbers
 // of 2^-40, so a sum does not depend on how the vocabulary is cut, and neither
-// does the drawn token. 64 chains over 102,400 tokens take 16.0 us, of which the 52 MB
-// that the rejections' sums read from HBM are 7.8; 32 trees over 50,001 tokens 17.2:
+// does the drawn token. 64 chains over 102,400 tokens take 16 us, of which the 49 MB
+// that the rejections' sums read from HBM are 7.4; 32 trees over 50,001 tokens 16:
 // up to four passes one behind another, each of some 5,000 cycles (its loads and sums
 // 2,400, meeting the other CTAs 1,500, the next step of the walk 1,000 to 2,000).
 constexpr int kVerWarps = 16, kVerThreads = 32 * kVerWarps, kVerMaxCl = 16;

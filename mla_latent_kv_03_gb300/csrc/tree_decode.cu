@@ -25,7 +25,10 @@
 // weights, and the merge weighs each half by its own log-sum-exp. The weights
 // are rounded to bf16 for the product (V is bf16, and the tensor cores take one
 // type); the sum adds the rounded weights, so that a row with one large weight
-// loses nothing.
+// loses nothing. The f16 half moves a weight by 2^-11 of that half (in units of the
+// exponent), the bf16 rounding by 2^-8: beyond halves of 8 the exchange is what
+// costs accuracy. fp32 would be twice the exchange, which takes 1,000 cycles of a
+// tile's 1,900 for 16 KB, and 32 KB more of shared memory, of which 9 are free.
 //
 // TMEM (512 columns): O [0, 256), two score buffers of 64 columns, and the
 // query's 256 latent columns (bf16 pairs) [384, 512). Its 32 rope columns lie in
@@ -47,9 +50,9 @@
 //   each, and its log-sum-exps: rows whose tokens are all in the segment to their
 //   place among the latents, others to a part's slot.
 //
-// What bounds it: not a rate. 64 sequences of 4,096 tokens take 78 us alone (4.0 TB/s
-// of HBM, tensor pipe busy 0.40), 16 sequences of 61 rows over up to 8,000 tokens 161
-// (0.47). A tile takes 1,900 cycles on the average, of which its products need 1,140:
+// What bounds it: not a rate. 64 sequences of 4,096 tokens take 75 us alone (in graphs;
+// 4.0 TB/s of HBM, tensor pipe busy 0.40), 16 sequences of 61 rows over up to 8,000
+// tokens 165 (0.46). A tile takes 1,900 cycles on the average, of which its products need 1,140:
 // from the copy of a stage to its release are 7,400 cycles (copy 2,700, scores 800,
 // exchange 1,300, softmax 1,400, output 850) over four stages, which with the peer's
 // scores and the weights fill the shared memory. 32-token tiles in ten stages took 6 to

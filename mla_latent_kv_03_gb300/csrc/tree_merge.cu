@@ -481,7 +481,9 @@ __global__ void __launch_bounds__(256) tree_proj_kernel(const __grid_constant__ 
 // where they are projected. In graphs, us, a merge of its own / in one: 1 x 8 rows of 16
 // heads over 4,096 tokens 23.0 / 43.6, over 30,000 31.2 / 53.2; 512 (row, head)s (4 x 8
 // rows) 25.8 / 29.5; 1,024 (8 x 8 rows) 39.1 / 35.1, (2 x 4 of 128 heads) 47.3 / 43.4;
-// 4,096 96.1 / 56.6. Rows of a CTA: the most that leave a CTA an SM (W_uv[h] is read for
+// 4,096 96.1 / 56.6. Of few parts a row: 1 x 6 rows of 16 heads over 64 tokens 14.9 / 17.1,
+// over 333 17.8 / 19.4, over 1,024 17.3 / 20.5; 512 (row, head)s (4 x 8 rows) over 64 17.0 /
+// 18.7, over 333 21.2 / 21.2, over 1,024 21.9 / 26.0. Rows of a CTA: the most that leave a CTA an SM (W_uv[h] is read for
 // each). 32 / 16 / 8: 64 x 8 rows of 16 heads 87.6 / 93.9 / 106; 8 x 4 of 128 heads
 // 174.8 / 162.9 / 169.5; 12 x 2 of 32 heads 22.5 / 21.3 / 20.5. (64 rows with 512
 // threads: 88.5 for the first, 127 against 121 for 11 x 70 rows of 64 heads.)
