@@ -184,8 +184,8 @@ def test_verify_of_values_that_are_no_probabilities(drawn, V):
 
 
 # --------------------------------------------------------- the step as a whole
-def tree_driver(seqs, t, seed):
-    """A step driver whose sequences have `past` tokens and trees of t rows, with pages for
+def tree_step_of(seqs, t, seed):
+    """A MlaDecodeStep whose sequences have `past` tokens and trees of t rows, with pages for
     three steps."""
     w = W.make("trees", [p + 3 * t for p in seqs], [t] * len(seqs), 16, 16, "bf16", seed)
     s = MlaDecodeStep(w, cache_fill=3.0)
@@ -202,7 +202,7 @@ def test_step_of_fewer_rows_than_it_has_room_for(side):
     in which they belonged to a sequence."""
     past, t = [40, 7, 20], 8
     for first in (True, False):
-        w, s, trees = tree_driver(past, t, 61)
+        w, s, trees = tree_step_of(past, t, 61)
         stream = torch.cuda.Stream() if side else None
         if not first:
             s.tree_step(stream)
@@ -224,7 +224,7 @@ def test_step_of_fewer_rows_than_it_has_room_for(side):
 def test_step_of_a_sequence_that_outgrew_its_table():
     """It is flagged, and neither its cache nor its length is lost; the others go on."""
     past, t = [40, 7, 20], 8
-    w, s, trees = tree_driver(past, t, 62)
+    w, s, trees = tree_step_of(past, t, 62)
     room = w.block_table.shape[1] * 16
     full = room - 3                       # (sequence 0's table is full, of the longest)
     s.tr_lens.copy_(dev([full + t, 7 + t, 20 + t], torch.int32))
@@ -249,7 +249,7 @@ def test_step_of_a_sequence_that_outgrew_its_table():
 def test_step_with_trees_of_other_sizes_than_the_first():
     """The lengths follow the rows that the sequences have now."""
     past, t = [40, 7, 20], 8
-    w, s, trees = tree_driver(past, t, 63)
+    w, s, trees = tree_step_of(past, t, 63)
     s.query_start_loc.copy_(dev([0, 8, 13, 13], torch.int32))
     s.tr_lens.copy_(dev([48, 12, 20], torch.int32))
     v = Verify([trees[0], trees[1][:5], []], 50, True, seed=2, near=0.1)
